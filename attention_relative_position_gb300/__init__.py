@@ -19,8 +19,10 @@ __all__ = [
     "fat_attn_debug_buckets", "fat_attn_debug_set_watchdog", "fat_attn_bwd_stages",
     "fat_attn_bwd_noalloc", "fat_xattn_fwd", "fat_xattn_bwd", "fat_xattn_bwd_workspace_size",
     "fat_xattn_splitkv_num_splits", "fat_rope_apply", "fat_rmsnorm_fwd", "fat_rmsnorm_bwd",
-    "fat_cross_entropy", "FAT_DEVERR_TIMEOUT_FWD", "FAT_DEVERR_TIMEOUT_BWD", "FAT_DEVERR_INDEX",
-    "FAT_DEVERR_SEQLENS", "LIB_PATH",
+    "fat_cross_entropy", "fat_paged_plan", "fat_rope_init", "fat_rope_embed", "fat_paged_append",
+    "fat_paged_attn", "fat_paged_attn_workspace_size", "FAT_DEVERR_TIMEOUT_FWD",
+    "FAT_DEVERR_TIMEOUT_BWD", "FAT_DEVERR_INDEX", "FAT_DEVERR_SEQLENS", "FAT_DEVERR_PAGES",
+    "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfatattn.so")
@@ -29,6 +31,7 @@ FAT_DEVERR_TIMEOUT_FWD = 1
 FAT_DEVERR_TIMEOUT_BWD = 2
 FAT_DEVERR_SEQLENS = 4
 FAT_DEVERR_INDEX = 8
+FAT_DEVERR_PAGES = 16
 
 
 class FatAttnError(RuntimeError):
@@ -51,6 +54,48 @@ class _XShape(ctypes.Structure):
                 ("num_seqs", ctypes.c_int32), ("max_seqlen_q", ctypes.c_int32),
                 ("max_seqlen_k", ctypes.c_int32), ("num_heads_q", ctypes.c_int32),
                 ("num_heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("stream", ctypes.c_void_p)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("stride_page", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class _PlanShape(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("num_free", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("stream", ctypes.c_void_p)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("rate", ctypes.c_uint64 * 128)]
+
+
+class _RopeShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("x_stride_token", ctypes.c_int64),
+                ("x_stride_head", ctypes.c_int64), ("y_stride_token", ctypes.c_int64),
+                ("y_stride_head", ctypes.c_int64), ("stream", ctypes.c_void_p)]
+
+
+class _AppendShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("num_heads_q", ctypes.c_int32),
+                ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+                ("k_stride_token", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+                ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
+                ("stream", ctypes.c_void_p)]
+
+
+class _PagedShape(ctypes.Structure):
+    _fields_ = [("total_q", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("max_seqlen_q", ctypes.c_int32), ("max_seqlen_k", ctypes.c_int32),
+                ("num_heads_q", ctypes.c_int32), ("table_width", ctypes.c_int32),
                 ("stream", ctypes.c_void_p)]
 
 
@@ -116,6 +161,21 @@ def load(path: Optional[str] = None):
     lib.fat_cross_entropy.restype = i32
     lib.fat_rope_apply.argtypes = [S, vp, vp, vp, ctypes.c_double, i32]
     lib.fat_rope_apply.restype = i32
+    P = ctypes.POINTER
+    lib.fat_paged_plan.argtypes = [P(_PlanShape)] + [vp] * 9
+    lib.fat_paged_plan.restype = i32
+    f64 = ctypes.c_double
+    lib.fat_rope_init.argtypes = [P(_Rope), i32, i32, f64, f64, f64, f64, f64, f64]
+    lib.fat_rope_init.restype = i32
+    lib.fat_rope_embed.argtypes = [P(_RopeShape), P(_Rope), vp, vp, vp, i32]
+    lib.fat_rope_embed.restype = i32
+    lib.fat_paged_append.argtypes = [P(_AppendShape), P(_Cache), P(_Rope)] + [vp] * 6
+    lib.fat_paged_append.restype = i32
+    lib.fat_paged_attn.argtypes = [P(_PagedShape), P(_Cache), vp, vp, vp, vp, vp, i32, i32, i32,
+                                   vp, i32, f32, vp, ctypes.c_size_t, vp, vp]
+    lib.fat_paged_attn.restype = i32
+    lib.fat_paged_attn_workspace_size.argtypes = [P(_PagedShape), P(_Cache)]
+    lib.fat_paged_attn_workspace_size.restype = ctypes.c_size_t
     lib.fat_attn_get_device_error.argtypes = [vp, ctypes.POINTER(i32)]
     lib.fat_attn_get_device_error.restype = i32
     lib.fat_attn_strerror.argtypes = [i32]
@@ -510,6 +570,249 @@ def fat_cross_entropy(logits, target, z_loss: float = 0.0, grad_scale: float = 1
     if rc != 0:
         raise FatAttnError(rc, "fat_cross_entropy")
     return loss, lse, (dlogits if want_grad else None)
+
+
+# ---- paged key/value cache ---------------------------------------------------------------------
+# These calls serve single decode steps, where the host's time counts: their checks read each
+# attribute once, and the device is switched only when it is not the current one.
+
+def _ints(name, t, numel, dev):
+    """An int32 array argument: contiguous, on device index dev, numel entries (None: any)."""
+    import torch
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} entries, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, dev):
+    """A bf16 array of rows whose last dimension is contiguous (views of packed rows are fine)."""
+    import torch
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return st
+
+
+def _paged_cache(k_cache, v_cache, dev) -> _Cache:
+    st = _rows("k_cache", k_cache, (None,) * 4, dev)
+    shape = k_cache.shape
+    if _rows("v_cache", v_cache, shape, dev) != st:
+        raise ValueError("v_cache must have the strides of k_cache")
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], shape[2], shape[3],
+                  st[0], st[1], st[2])
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _call_on(dev: int, fn, *args) -> int:
+    """fn(*args) with device index dev current."""
+    import torch
+    if torch.cuda.current_device() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def fat_paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size: int, num_pages: int,
+                   max_tokens: int, cu_seqlens_q=None, seqlens_k=None, positions=None, slots=None,
+                   counts=None, stream=None):
+    """The maps of a step in which request i (ctx_lens[i] cached tokens) brings new_lens[i] tokens:
+    pages it lacks are taken from free_pages in request order and written to block_table (int32
+    [n, width], in place). Returns (cu_seqlens_q [n + 1], seqlens_k [n], positions [max_tokens],
+    slots [max_tokens], counts [2] = pages taken, tokens), all int32; tokens behind the last
+    request get position 0 and slot -1."""
+    import torch
+    lib = load()
+    dev = ctx_lens.get_device()
+    n = ctx_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError(f"block_table must have shape [{n}, width]")
+    max_tokens = int(max_tokens)
+    pc = _ints("ctx_lens", ctx_lens, n, dev)
+    pn = _ints("new_lens", new_lens, n, dev)
+    pf = _ints("free_pages", free_pages, None, dev)
+    pt = _ints("block_table", block_table, None, dev)
+
+    def buf(t, size):
+        return torch.empty(size, dtype=torch.int32, device=ctx_lens.device) if t is None else t
+    cu_seqlens_q, seqlens_k = buf(cu_seqlens_q, n + 1), buf(seqlens_k, n)
+    positions, slots = buf(positions, max_tokens), buf(slots, max_tokens)
+    counts = buf(counts, 2)
+    sh = _PlanShape(n, page_size, num_pages, block_table.shape[1], free_pages.numel(), max_tokens,
+                    _raw_stream(stream, dev))
+    rc = _call_on(dev, lib.fat_paged_plan, sh, pc, pn, pf, pt,
+                  _ints("cu_seqlens_q", cu_seqlens_q, n + 1, dev),
+                  _ints("seqlens_k", seqlens_k, n, dev),
+                  _ints("positions", positions, max_tokens, dev),
+                  _ints("slots", slots, max_tokens, dev), _ints("counts", counts, 2, dev))
+    if rc != 0:
+        raise FatAttnError(rc, "fat_paged_plan")
+    return cu_seqlens_q, seqlens_k, positions, slots, counts
+
+
+def fat_rope_init(rotary_dim: int, base: float = 10000.0, interleaved: bool = True,
+                  factor: float = 1.0, ramp=None, amplitude: float = 1.0) -> _Rope:
+    """The rotation fat_rope_embed and fat_paged_append apply (made once, kept by the caller): the
+    first rotary_dim channels of a head turn in pairs (2i, 2i + 1), or (i, i + rotary_dim / 2) when
+    not interleaved. factor divides the frequencies; ramp = (low_turns, high_turns,
+    original_length) keeps those that turn at least high_turns times over original_length and
+    blends down to low_turns. amplitude multiplies the turned channels."""
+    low, high, original = ramp if ramp is not None else (0.0, 0.0, 0.0)
+    r = _Rope()
+    rc = load().fat_rope_init(ctypes.byref(r), int(rotary_dim), int(bool(interleaved)),
+                              float(base), float(factor), float(low), float(high),
+                              float(original), float(amplitude))
+    if rc != 0:
+        raise FatAttnError(rc, "fat_rope_init")
+    return r
+
+
+def fat_rope_embed(x, positions, rope: _Rope, inverse: bool = False, out=None, stream=None):
+    """Rotary embedding of bf16 rows x [T, H, d] (strided views are fine) at positions int32 [T];
+    inverse=True applies the transpose, which takes the gradient of the result to the gradient of
+    x. out may be x itself (in place). Returns out."""
+    import torch
+    lib = load()
+    dev = x.get_device()
+    xs = _rows("x", x, (None, None, None), dev)
+    T, H, d = x.shape
+    if out is None:
+        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=x.device)
+    ys = _rows("out", out, (T, H, d), dev)
+    sh = _RopeShape(T, H, d, xs[0], xs[1], ys[0], ys[1], _raw_stream(stream, dev))
+    rc = _call_on(dev, lib.fat_rope_embed, sh, rope, x.data_ptr(), out.data_ptr(),
+                  _ints("positions", positions, T, dev), 1 if inverse else 0)
+    if rc != 0:
+        raise FatAttnError(rc, "fat_rope_embed")
+    return out
+
+
+def fat_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, rope=None, q_out=None,
+                     stream=None):
+    """Write the rows k, v (bf16 [T, Hkv, d], strided views are fine) to their slots (int32 [T],
+    page * page_size + offset; negative: dropped) of the caches (bf16 [pages, page_size, Hkv, d],
+    any strides with a contiguous row, the same for both). With rope, k is turned at positions
+    (int32 [T]) on the way, and q (bf16 [T, Hq, d]) too. Returns q_out (contiguous) or None."""
+    import torch
+    lib = load()
+    dev = k.get_device()
+    cache = _paged_cache(k_cache, v_cache, dev)
+    T = k.shape[0]
+    rows = (T, cache.num_heads, cache.head_dim)
+    ks, vs = _rows("k", k, rows, dev), _rows("v", v, rows, dev)
+    Hq, qs, pq, po = 0, (0, 0), None, None
+    if q is not None:
+        qs = _rows("q", q, (T, None, cache.head_dim), dev)
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, Hq, cache.head_dim), dtype=torch.bfloat16, device=q.device)
+        _rows("q_out", q_out, (T, Hq, cache.head_dim), dev)
+        if not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous")
+        pq, po = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    sh = _AppendShape(T, Hq, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], _raw_stream(stream, dev))
+    rc = _call_on(dev, lib.fat_paged_append, sh, cache, rope, pq, k.data_ptr(), v.data_ptr(),
+                  None if positions is None else _ints("positions", positions, T, dev),
+                  _ints("slots", slots, T, dev), po)
+    if rc != 0:
+        raise FatAttnError(rc, "fat_paged_append")
+    return q_out
+
+
+def fat_paged_attn_workspace_size(q, k_cache, cu_seqlens_q, max_seqlen_q: int,
+                                  max_seqlen_k: int) -> int:
+    """Workspace bytes of fat_paged_attn for these arguments on q's device."""
+    dev = q.get_device()
+    sh = _PagedShape(q.shape[0], cu_seqlens_q.numel() - 1, int(max_seqlen_q), int(max_seqlen_k),
+                     q.shape[1], 0, None)
+    P, ps, H, d = k_cache.shape
+    cache = _Cache(None, None, P, ps, H, d, 0, 0, 0)
+    return int(_call_on(dev, load().fat_paged_attn_workspace_size, sh, cache))
+
+
+def fat_paged_attn(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q: int,
+                   max_seqlen_k: int, bias_table=None, num_buckets: int = 0,
+                   max_distance: int = 0, bidirectional: bool = True, alibi_slopes=None,
+                   causal: bool = False, softmax_scale: float = 1.0, out=None, lse=None,
+                   workspace=None, stream=None):
+    """Attention of new tokens over a paged cache: q bf16 [Tq, Hq, d] packed by cu_seqlens_q (int32
+    [n + 1]); request i's seqlens_k[i] keys and values lie in the pages block_table[i] (int32
+    [n, width]) of the caches (bf16 [pages, page_size, Hkv, d], any strides with a contiguous row);
+    its last query lines up with its last key. Bias, mask and scale as fat_xattn_fwd. workspace:
+    fat_paged_attn_workspace_size bytes (None: allocated here), for one call at a time. Returns
+    (out bf16 [Tq, Hq, d], lse fp32 [Hq, Tq])."""
+    import torch
+    lib = load()
+    dev = q.get_device()
+    _rows("q", q, (None, None, None), dev)
+    Tq, Hq, d = q.shape
+    n = seqlens_k.numel()
+    cache = _paged_cache(k_cache, v_cache, dev)
+    if cache.head_dim != d:
+        raise ValueError(f"q has head_dim {d}, the cache {cache.head_dim}")
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError(f"block_table must have shape [{n}, width]")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    pb = ps = None
+    if bias_table is not None:
+        _check_tensor("bias_table", bias_table, torch.float32, 2)
+        if bias_table.shape != (num_buckets, Hq) or bias_table.get_device() != dev:
+            raise ValueError(f"bias_table must have shape [{num_buckets}, {Hq}], on q's device")
+        pb = bias_table.data_ptr()
+    if alibi_slopes is not None:
+        _check_tensor("alibi_slopes", alibi_slopes, torch.float32, 1)
+        if alibi_slopes.numel() != Hq or alibi_slopes.get_device() != dev:
+            raise ValueError(f"alibi_slopes must have {Hq} entries, on q's device")
+        ps = alibi_slopes.data_ptr()
+    if out is None:
+        out = torch.empty_like(q)
+    elif not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    else:
+        _rows("out", out, (Tq, Hq, d), dev)
+    if lse is None:
+        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+    else:
+        _check_tensor("lse", lse, torch.float32, 2)
+        if lse.shape != (Hq, Tq) or lse.get_device() != dev:
+            raise ValueError(f"lse must have shape [{Hq}, {Tq}], on q's device")
+    sh = _PagedShape(Tq, n, max_seqlen_q, max_seqlen_k, Hq, block_table.shape[1],
+                     _raw_stream(stream, dev))
+    if workspace is None:
+        need = int(_call_on(dev, lib.fat_paged_attn_workspace_size, sh, cache))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+    rc = _call_on(dev, lib.fat_paged_attn, sh, cache, q.data_ptr(),
+                  _ints("block_table", block_table, None, dev),
+                  _ints("cu_seqlens_q", cu_seqlens_q, n + 1, dev),
+                  _ints("seqlens_k", seqlens_k, n, dev), pb, num_buckets, max_distance,
+                  1 if bidirectional else 0, ps, 1 if causal else 0, softmax_scale,
+                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                  out.data_ptr(), lse.data_ptr())
+    if rc != 0:
+        raise FatAttnError(rc, "fat_paged_attn")
+    return out, lse
 
 
 def fat_attn_get_device_error(stream=None, device=None) -> int:

@@ -178,6 +178,17 @@ int cuda_rc(int e) { return e == 0 ? FAT_OK : FAT_ECUDA; }
 
 int device_error_address(int **out) { return device_error_ptr(out); }
 
+int make_bias_params(BiasParams *b, const float *table, int nb, int md, int bidir,
+                     const float *slopes) {
+  return fill_bias(b, table, nb, md, bidir, slopes);
+}
+
+void runtime_knobs(long long *timeout_ns, int *debug_flags) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  *timeout_ns = g_timeout_ns;
+  *debug_flags = g_debug_flags;
+}
+
 // Per (kernel, device): the largest dynamic shared-memory size already allowed, and whether the
 // compiled register count times the block size holds the kernel's register re-balancing.
 // Launchers call this before every launch; only the first call per size does any CUDA work.
@@ -672,12 +683,6 @@ int launch_rc(const char *what) {
   return FAT_ECUDA;
 }
 
-void fill_runtime_knobs(long long *timeout_ns, int *debug_flags) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  *timeout_ns = g_timeout_ns;
-  *debug_flags = g_debug_flags;
-}
-
 // Split-key forward workspace: normalised partial outputs fp32 [splits, Tq, Hq, d], then
 // partial lse fp32 [splits, Hq, Tq], each 256-byte aligned.
 size_t splitkv_bytes(const XShape &x, int splits) {
@@ -772,7 +777,7 @@ int fwd_impl(const XShape &x, const void *q, const void *k, const void *v,
   p.scale_log2 = softmax_scale * kLog2e;
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
-  fill_runtime_knobs(&p.timeout_ns, &p.debug_flags);
+  runtime_knobs(&p.timeout_ns, &p.debug_flags);
   p.kv_splits = splits;
   const int nkt = (x.maxk + 127) / 128;
   p.split_tiles = splits == 1 ? (1 << 30) : (nkt + splits - 1) / splits;
@@ -907,7 +912,7 @@ int bwd_main_impl(const XShape &x, const void *q, const void *k, const void *v,
   p.dk_acc = ws.dk_acc;
   p.dv_acc = ws.dv_acc;
   p.dbias = dbias_table;
-  fill_runtime_knobs(&p.timeout_ns, &p.debug_flags);
+  runtime_knobs(&p.timeout_ns, &p.debug_flags);
   if (split_tail && !causal && (ws.tail_acc || ws.dk_acc)) {
     const TailPlan t = bwd_tail_plan(x);
     p.tail_first = t.first;

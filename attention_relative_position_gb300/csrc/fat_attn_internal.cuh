@@ -356,6 +356,16 @@ int check_bwd_args(const fat_shape_t *sh, const void *q, const void *k, const vo
                    const float *lse, const void *dout, const void *dq, const void *dk,
                    const void *dv, const float *dbias_table);
 
+// The bias arguments of a call as kernel parameters (FAT_OK or FAT_EINVAL_BUCKETS), and the debug
+// knobs that launches carry.
+int make_bias_params(BiasParams *b, const float *table, int nb, int md, int bidir,
+                     const float *slopes);
+void runtime_knobs(long long *timeout_ns, int *debug_flags);
+
+// Host checks of a paged cache (FAT_OK or the FAT_E* code); *c receives it with the strides over
+// single entries filled in, *log2_page its page size.
+int check_paged_cache(const fat_paged_cache_t *in, fat_paged_cache_t *c, int *log2_page);
+
 // Address of the current device's error word (FAT_OK, or FAT_ECUDA with the reason recorded).
 int device_error_address(int **out);
 

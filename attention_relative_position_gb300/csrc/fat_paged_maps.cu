@@ -1,0 +1,549 @@
+// fat_paged_maps.cu -- what a serving step does around attention over a paged key/value cache: the
+// step's maps (block tables, slots, positions) from the requests' lengths, rotary positions at
+// explicit positions, and the new key/value rows written into their slots.
+//
+//   plan: request i holds ctx_i cached tokens and brings new_i; with page size s it has
+//         ceil(ctx_i / s) pages and needs ceil((ctx_i + new_i) / s) of them. The missing ones come
+//         from a list of free pages in request order (exclusive prefix sums of the needs), and
+//         token j of request i goes to slot table[i][(ctx_i + j) / s] * s + (ctx_i + j) % s.
+//   rows: y = a (x cos p - x' sin p, x sin p + x' cos p) for the channel pairs of the rotated part
+//         of each head, p = position * rate of the pair; the other channels are copied.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "fat_attn_internal.cuh"
+
+namespace fat {
+namespace {
+
+// ---- plan ---------------------------------------------------------------------------------------
+// A few hundred kilobytes at most: bound by the latency of one launch and of the scan. Every block
+// scans all lengths by itself (they are read from L2; a separate scan launch would cost more than
+// the repeated reads) and then takes its share of the tokens and pages, finding each one's request
+// by binary search over the prefix sums in shared memory. Requests are taken kPlanTile at a time.
+constexpr int kPlanThreads = 256;
+constexpr int kPlanPer = 4;  // consecutive requests per thread
+constexpr int kPlanTile = kPlanThreads * kPlanPer;
+
+struct PlanParams {
+  int n, log2_page, num_pages, width, num_free, max_tokens;
+  const int32_t *ctx, *add, *free_pages;
+  int32_t *table, *cu, *lk, *pos, *slots, *counts;
+  int *err;
+};
+
+struct PlanPair {
+  long long tok, page;
+};
+__device__ __forceinline__ PlanPair plan_add(PlanPair a, PlanPair b) {
+  return PlanPair{a.tok + b.tok, a.page + b.page};
+}
+
+// The last index i in [0, m) with start[i] <= x (start[0] <= x): among requests without tokens the
+// last one, which is the one that holds x.
+__device__ __forceinline__ int plan_find(const int *start, int m, int x) {
+  int lo = 0, hi = m - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fat_paged_plan_kernel(const PlanParams p) {
+  __shared__ int tok_s[kPlanTile];   // first token of each request of the tile
+  __shared__ int page_s[kPlanTile];  // first free-list index of each request
+  __shared__ int ctx_s[kPlanTile];   // cached tokens; -1 - ctx: a request that takes no pages
+  __shared__ PlanPair warp_s[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gtid = blockIdx.x * kPlanThreads + tid, gthreads = gridDim.x * kPlanThreads;
+  const int page_mask = (1 << p.log2_page) - 1;
+  const long long row_tokens = (long long)p.width << p.log2_page;
+  PlanPair base{0, 0};
+  for (int i0 = 0; i0 < p.n; i0 += kPlanTile) {
+    const int m = min(kPlanTile, p.n - i0);
+    int c[kPlanPer], a[kPlanPer], need[kPlanPer];
+    PlanPair sum{0, 0};
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      const int i = tid * kPlanPer + k;
+      c[k] = i < m ? __ldg(p.ctx + i0 + i) : 0;
+      a[k] = i < m ? __ldg(p.add + i0 + i) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      if (c[k] < 0 || a[k] < 0) {
+        if (blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
+        c[k] = a[k] = 0;
+      }
+      const long long all = (long long)c[k] + a[k];
+      const bool fits = all <= row_tokens;
+      if (!fits && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_PAGES);
+      need[k] = fits ? (int)(((all + page_mask) >> p.log2_page) -
+                             (((long long)c[k] + page_mask) >> p.log2_page))
+                     : 0;
+      if (!fits) c[k] = -1 - c[k];
+      sum.tok += a[k];
+      sum.page += need[k];
+    }
+    PlanPair inc = sum;  // inclusive over the warp, then over the block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc.tok, o);
+      const long long g = __shfl_up_sync(0xffffffffu, inc.page, o);
+      if (lane >= o) inc = plan_add(inc, PlanPair{t, g});
+    }
+    __syncthreads();  // the previous tile's shared arrays are no longer read
+    if (lane == 31) warp_s[warp] = inc;
+    __syncthreads();
+    PlanPair at = base, total = base;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) at = plan_add(at, warp_s[w]);
+      total = plan_add(total, warp_s[w]);
+    }
+    at.tok += inc.tok - sum.tok;
+    at.page += inc.page - sum.page;
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      const int i = tid * kPlanPer + k;
+      if (i < m) {
+        tok_s[i] = (int)min(at.tok, (long long)p.max_tokens);
+        page_s[i] = (int)min(at.page, 0x7fffffffLL);
+        ctx_s[i] = c[k];
+        if (blockIdx.x == 0) {
+          const long long ctx = c[k] < 0 ? -1 - (long long)c[k] : c[k];
+          p.cu[i0 + i] = (int)min(at.tok, (long long)p.max_tokens);
+          p.lk[i0 + i] = (int)min(ctx + a[k], 0x7fffffffLL);
+        }
+      }
+      at.tok += a[k];
+      at.page += need[k];
+    }
+    __syncthreads();
+    // the tile's tokens
+    const int t_end = (int)min(total.tok, (long long)p.max_tokens);
+    for (long long t = min(base.tok, (long long)p.max_tokens) + gtid; t < t_end; t += gthreads) {
+      const int i = plan_find(tok_s, m, (int)t);
+      const bool fits = ctx_s[i] >= 0;
+      const int ctx = fits ? ctx_s[i] : -1 - ctx_s[i];
+      const int pos = (int)min((long long)ctx + ((int)t - tok_s[i]), 0x7fffffffLL);
+      int slot = -1;
+      if (fits) {
+        const int col = pos >> p.log2_page, have = (int)(((long long)ctx + page_mask) >> p.log2_page);
+        int page;
+        if (col < have) {  // the last page it already holds
+          page = p.table[(size_t)(i0 + i) * p.width + col];
+        } else {
+          const long long f = (long long)page_s[i] + (col - have);
+          page = f < p.num_free ? __ldg(p.free_pages + f) : -1;
+        }
+        if ((unsigned)page < (unsigned)p.num_pages)
+          slot = (page << p.log2_page) + (pos & page_mask);
+        else
+          atomicOr(p.err, FAT_DEVERR_PAGES);
+      }
+      p.pos[t] = pos;
+      p.slots[t] = slot;
+    }
+    // the tile's new pages
+    const long long f_end = min(total.page, 0x7fffffffLL);
+    for (long long f = base.page + gtid; f < f_end; f += gthreads) {
+      const int i = plan_find(page_s, m, (int)f);
+      const int have = (int)(((long long)ctx_s[i] + page_mask) >> p.log2_page);
+      int page = f < p.num_free ? __ldg(p.free_pages + f) : -1;
+      if ((unsigned)page >= (unsigned)p.num_pages) {
+        page = -1;
+        atomicOr(p.err, FAT_DEVERR_PAGES);
+      }
+      p.table[(size_t)(i0 + i) * p.width + have + (f - page_s[i])] = page;
+    }
+    base = total;
+  }
+  const int tokens = (int)min(base.tok, (long long)p.max_tokens);
+  if (gtid == 0) {
+    if (base.tok > p.max_tokens) atomicOr(p.err, FAT_DEVERR_SEQLENS);
+    p.cu[p.n] = tokens;
+    p.counts[0] = (int)min(base.page, 0x7fffffffLL);
+    p.counts[1] = (int)min(base.tok, 0x7fffffffLL);
+  }
+  for (long long t = (long long)tokens + gtid; t < p.max_tokens; t += gthreads) {  // padding
+    p.pos[t] = 0;
+    p.slots[t] = -1;
+  }
+}
+
+// ---- rows ---------------------------------------------------------------------------------------
+// Memory bound: every row is read and written once. A block takes `tok_per_block` tokens: their
+// cosines and sines are computed once into shared memory (all heads of a token share them), then
+// its threads walk (token, head, unit) with 16-byte accesses, kRowBatch units in flight per thread.
+// A unit is one 16-byte chunk (pairs 2i, 2i + 1 lie inside it), or with the halves layout two
+// chunks, i and i + rotary_dim / 2, that turn together; what is not rotated goes chunk by chunk.
+// Angles as in fat_rope_apply: position * rate mod one turn in 64-bit integers, exact at any
+// position, its top 24 bits through sincospif.
+constexpr int kRowThreads = 256;
+constexpr int kRowBatch = 4;
+
+struct RowSeg {
+  const uint16_t *src;
+  uint16_t *dst;
+  long long src_tok, src_head, dst_tok, dst_head;  // element strides
+  int heads;
+  int rotate;
+  int to_slots;  // dst is a cache: the token's slot gives its row
+};
+struct RowParams {
+  RowSeg seg[3];
+  int nseg, tokens, units, pair_units, half_chunks, tok_per_block, all_heads;
+  int log2_page;
+  long long page_stride, num_slots;
+  float sign;
+  const int32_t *positions, *slots;
+  int *err;
+  fat_rope_t rope;
+};
+
+__device__ __forceinline__ uint4 rotate_pairs(uint4 v, const float2 *cs) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 a = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&w[k]));
+    w[k] = pack_bf16x2(a.x * cs[k].x - a.y * cs[k].y, a.x * cs[k].y + a.y * cs[k].x);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void rotate_halves(uint4 &u, uint4 &v, const float2 *cs) {
+  uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&a[k]));
+    const float2 y = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&b[k]));
+    const float2 c0 = cs[2 * k], c1 = cs[2 * k + 1];
+    a[k] = pack_bf16x2(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
+    b[k] = pack_bf16x2(x.x * c0.y + y.x * c0.x, x.y * c1.y + y.y * c1.x);
+  }
+  u = make_uint4(a[0], a[1], a[2], a[3]);
+  v = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+template <bool PAIRS>
+__global__ void __launch_bounds__(kRowThreads) fat_rows_kernel(const __grid_constant__ RowParams p) {
+  extern __shared__ float2 cs_s[];  // [tok_per_block][pairs] (amplitude cos, amplitude sin)
+  const int tid = threadIdx.x;
+  const int npairs = p.rope.rotary_dim >> 1;
+  const int t0 = blockIdx.x * p.tok_per_block;
+  const int nt = min(p.tok_per_block, p.tokens - t0);
+  for (int i = tid; i < nt * npairs; i += kRowThreads) {
+    const int t = i / npairs, k = i - t * npairs;
+    // negative positions wrap in two's complement: still exact modulo one turn
+    const unsigned long long pos = (unsigned long long)(long long)__ldg(p.positions + t0 + t);
+    const unsigned long long turns = pos * p.rope.rate[k];
+    const float frac = (float)(uint32_t)(turns >> 40) * (1.0f / 16777216.0f);
+    float sn, cn;
+    sincospif(2.0f * frac, &sn, &cn);
+    cs_s[i] = make_float2(cn * p.rope.amplitude, sn * p.sign * p.rope.amplitude);
+  }
+  __syncthreads();
+  const int per_tok = p.all_heads * p.units;
+  const int n = nt * per_tok;
+  for (int i0 = tid; i0 < n; i0 += kRowThreads * kRowBatch) {
+    uint4 lo[kRowBatch], hi[kRowBatch];
+    uint16_t *dst[kRowBatch];
+    const float2 *cs[kRowBatch];  // null: copied as it is
+    bool two[kRowBatch];
+#pragma unroll
+    for (int b = 0; b < kRowBatch; ++b) {
+      const int i = i0 + b * kRowThreads;
+      dst[b] = nullptr;
+      if (i >= n) continue;
+      const int t = i / per_tok, rest = i - t * per_tok;
+      int h = rest / p.units;
+      const int u = rest - h * p.units;
+      int sg = 0;
+      while (h >= p.seg[sg].heads) h -= p.seg[sg++].heads;
+      const RowSeg &s = p.seg[sg];
+      long long row = (long long)(t0 + t) * s.dst_tok;
+      if (s.to_slots) {
+        const int slot = __ldg(p.slots + t0 + t);
+        if (slot < 0) continue;
+        if (slot >= p.num_slots) {
+          atomicOr(p.err, FAT_DEVERR_INDEX);
+          continue;
+        }
+        const int page = slot >> p.log2_page;
+        row = (long long)page * p.page_stride +
+              (long long)(slot - (page << p.log2_page)) * s.dst_tok;
+      }
+      // channels of the unit: the first chunk, and (halves) the one rotary_dim / 2 further
+      two[b] = !PAIRS && u < p.pair_units;
+      const int chunk = (PAIRS || u < p.pair_units) ? u : u + p.pair_units;
+      const uint16_t *src =
+          s.src + (long long)(t0 + t) * s.src_tok + (long long)h * s.src_head + chunk * 8;
+      dst[b] = s.dst + row + (long long)h * s.dst_head + chunk * 8;
+      const bool turned = s.rotate && u < p.pair_units;
+      cs[b] = turned ? cs_s + t * npairs + u * (PAIRS ? 4 : 8) : nullptr;
+      lo[b] = *reinterpret_cast<const uint4 *>(src);
+      if (two[b]) hi[b] = *reinterpret_cast<const uint4 *>(src + p.half_chunks * 8);
+    }
+#pragma unroll
+    for (int b = 0; b < kRowBatch; ++b) {
+      if (dst[b] == nullptr) continue;
+      if (cs[b] != nullptr) {
+        if constexpr (PAIRS)
+          lo[b] = rotate_pairs(lo[b], cs[b]);
+        else
+          rotate_halves(lo[b], hi[b], cs[b]);
+      }
+      *reinterpret_cast<uint4 *>(dst[b]) = lo[b];
+      if (two[b]) *reinterpret_cast<uint4 *>(dst[b] + p.half_chunks * 8) = hi[b];
+    }
+  }
+}
+
+bool odd16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool odd4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+// A stride of rows that are accessed 16 bytes at a time
+bool bad_stride(long long s) { return s < 0 || (s & 7) != 0; }
+
+int check_rope(const fat_rope_t *r, int head_dim) {
+  if (r->rotary_dim < 16 || r->rotary_dim % 16 || r->rotary_dim > 2 * FAT_ROPE_MAX_PAIRS ||
+      r->rotary_dim > head_dim)
+    return FAT_EINVAL_SHAPE;
+  return FAT_OK;
+}
+
+// head_dim, the rotation (null: rows are copied) and the segments are set: fill in the rest and
+// launch. Tokens per block: enough units for every thread's batch, as long as that leaves two
+// blocks for every SM.
+int launch_rows(RowParams &p, const fat_rope_t *rope, int head_dim, cudaStream_t stream) {
+  if (rope) {
+    p.rope = *rope;
+  } else {
+    p.rope.rotary_dim = 0;
+    p.rope.interleaved = 1;
+    p.rope.amplitude = 1.f;
+  }
+  const bool pairs = p.rope.interleaved != 0;
+  const int chunks = head_dim / 8;
+  p.half_chunks = p.rope.rotary_dim / 16;
+  p.pair_units = pairs ? p.rope.rotary_dim / 8 : p.half_chunks;
+  p.units = pairs ? chunks : chunks - p.half_chunks;
+  p.all_heads = 0;
+  for (int i = 0; i < p.nseg; ++i) p.all_heads += p.seg[i].heads;
+  const int sms = sm_count() > 0 ? sm_count() : 152;
+  const long long per_tok = (long long)p.all_heads * p.units;
+  if (per_tok > (1 << 24)) return FAT_EUNSUPPORTED;
+  long long tb = std::max<long long>(1, (2LL * kRowThreads * kRowBatch) / per_tok);
+  tb = std::min<long long>(tb, std::max(1, p.tokens / (2 * sms)));
+  tb = std::min<long long>(tb, 16);
+  p.tok_per_block = (int)tb;
+  const int blocks = (int)((p.tokens + tb - 1) / tb);
+  const size_t smem = (size_t)tb * (p.rope.rotary_dim / 2) * sizeof(float2);
+  if (pairs)
+    fat_rows_kernel<true><<<blocks, kRowThreads, smem, stream>>>(p);
+  else
+    fat_rows_kernel<false><<<blocks, kRowThreads, smem, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return FAT_OK;
+  set_last_error("rotary / append rows launch", (int)e, cudaGetErrorString(e));
+  return FAT_ECUDA;
+}
+
+}  // namespace
+
+int check_paged_cache(const fat_paged_cache_t *in, fat_paged_cache_t *c, int *log2_page) {
+  if (!in || !in->k || !in->v) return FAT_EINVAL_NULL;
+  *c = *in;
+  if (c->num_pages <= 0 || c->num_heads <= 0 || c->head_dim <= 0 || c->head_dim % 8)
+    return FAT_EINVAL_SHAPE;
+  int lg = 0;
+  while (lg < 16 && (1 << lg) < c->page_size) ++lg;
+  if (c->page_size < 16 || c->page_size != (1 << lg)) return FAT_EINVAL_SHAPE;
+  if ((long long)c->num_pages * c->page_size > 0x7fffffffLL) return FAT_EINVAL_SHAPE;
+  // a stride over one entry says nothing
+  if (c->num_heads == 1) c->stride_head = c->head_dim;
+  if (c->num_pages == 1) c->stride_page = c->stride_token * c->page_size;
+  if (odd16(c->k) || odd16(c->v) || bad_stride(c->stride_page) || bad_stride(c->stride_token) ||
+      bad_stride(c->stride_head))
+    return FAT_EINVAL_SHAPE;
+  // rows of different heads, tokens and pages lie apart
+  if (c->stride_token < c->head_dim || c->stride_head < c->head_dim ||
+      c->stride_page < c->head_dim)
+    return FAT_EINVAL_SHAPE;
+  *log2_page = lg;
+  return FAT_OK;
+}
+
+}  // namespace fat
+
+using namespace fat;
+
+extern "C" {
+
+int fat_paged_plan(const fat_plan_shape_t *sh, const int32_t *ctx_lens, const int32_t *new_lens,
+                   const int32_t *free_pages, int32_t *block_table, int32_t *cu_seqlens_q,
+                   int32_t *seqlens_k, int32_t *positions, int32_t *slots, int32_t *counts) {
+  if (!sh || !cu_seqlens_q || !counts) return FAT_EINVAL_NULL;
+  if (sh->num_seqs < 0 || sh->num_pages <= 0 || sh->table_width < 0 || sh->num_free < 0 ||
+      sh->max_tokens < 0)
+    return FAT_EINVAL_SHAPE;
+  if (sh->num_seqs > 0 && (!ctx_lens || !new_lens || !seqlens_k)) return FAT_EINVAL_NULL;
+  if (sh->num_seqs > 0 && sh->table_width > 0 && !block_table) return FAT_EINVAL_NULL;
+  if (sh->max_tokens > 0 && (!positions || !slots)) return FAT_EINVAL_NULL;
+  if (sh->num_free > 0 && !free_pages) return FAT_EINVAL_NULL;
+  int lg = 0;
+  while (lg < 16 && (1 << lg) < sh->page_size) ++lg;
+  if (sh->page_size < 16 || sh->page_size != (1 << lg)) return FAT_EINVAL_SHAPE;
+  if ((long long)sh->num_pages * sh->page_size > 0x7fffffffLL) return FAT_EINVAL_SHAPE;
+  if (odd4(ctx_lens) || odd4(new_lens) || odd4(free_pages) || odd4(block_table) ||
+      odd4(cu_seqlens_q) || odd4(seqlens_k) || odd4(positions) || odd4(slots) || odd4(counts))
+    return FAT_EINVAL_SHAPE;
+  PlanParams p{};
+  int rc = device_error_address(&p.err);
+  if (rc) return rc;
+  p.n = sh->num_seqs;
+  p.log2_page = lg;
+  p.num_pages = sh->num_pages;
+  p.width = sh->table_width;
+  p.num_free = sh->num_free;
+  p.max_tokens = sh->max_tokens;
+  p.ctx = ctx_lens;
+  p.add = new_lens;
+  p.free_pages = free_pages;
+  p.table = block_table;
+  p.cu = cu_seqlens_q;
+  p.lk = seqlens_k;
+  p.pos = positions;
+  p.slots = slots;
+  p.counts = counts;
+  const int sms = sm_count() > 0 ? sm_count() : 152;
+  // a block for every 1024 tokens or requests, one per SM at most
+  const int units = std::max(sh->max_tokens, sh->num_seqs);
+  const int blocks = std::max(1, std::min(sms, (units + 1023) / 1024));
+  fat_paged_plan_kernel<<<blocks, kPlanThreads, 0, static_cast<cudaStream_t>(sh->stream)>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return FAT_OK;
+  set_last_error("paged plan launch", (int)e, cudaGetErrorString(e));
+  return FAT_ECUDA;
+}
+
+int fat_rope_init(fat_rope_t *r, int rotary_dim, int interleaved, double base, double factor,
+                  double low_turns, double high_turns, double original_length, double amplitude) {
+  if (!r) return FAT_EINVAL_NULL;
+  if (rotary_dim < 16 || rotary_dim % 16 || rotary_dim > 2 * FAT_ROPE_MAX_PAIRS)
+    return FAT_EINVAL_SHAPE;
+  if (!(base > 1.0) || !std::isfinite(base) || !(factor > 0.0) || !std::isfinite(factor) ||
+      !(amplitude > 0.0) || !std::isfinite((float)amplitude) || !(original_length >= 0.0) ||
+      !std::isfinite(original_length))
+    return FAT_EINVAL_SHAPE;
+  if (original_length > 0.0 &&
+      (!(low_turns >= 0.0) || !(high_turns > low_turns) || !std::isfinite(high_turns)))
+    return FAT_EINVAL_SHAPE;
+  *r = fat_rope_t{};
+  r->rotary_dim = rotary_dim;
+  r->interleaved = interleaved ? 1 : 0;
+  r->amplitude = (float)amplitude;
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double turns = std::pow(base, -2.0 * i / rotary_dim) / two_pi;  // per position
+    double keep = 0.0;
+    if (original_length > 0.0)
+      keep = std::min(1.0, std::max(0.0, (original_length * turns - low_turns) /
+                                             (high_turns - low_turns)));
+    turns = turns * keep + turns * (1.0 - keep) / factor;
+    const double scaled = std::ldexp(turns - std::floor(turns), 64);
+    r->rate[i] = scaled >= 18446744073709551615.0 ? ~0ull : (unsigned long long)scaled;
+  }
+  return FAT_OK;
+}
+
+int fat_rope_embed(const fat_rope_shape_t *sh, const fat_rope_t *rope, const void *x, void *y,
+                   const int32_t *positions, int inverse) {
+  if (!sh || !rope) return FAT_EINVAL_NULL;
+  if (sh->tokens < 0 || sh->num_heads <= 0 || sh->head_dim <= 0 || sh->head_dim % 8)
+    return FAT_EINVAL_SHAPE;
+  int rc = check_rope(rope, sh->head_dim);
+  if (rc) return rc;
+  if (sh->tokens == 0) return FAT_OK;
+  if (!x || !y || !positions) return FAT_EINVAL_NULL;
+  if (odd16(x) || odd16(y) || odd4(positions) || bad_stride(sh->x_stride_token) ||
+      bad_stride(sh->x_stride_head) || bad_stride(sh->y_stride_token) ||
+      bad_stride(sh->y_stride_head))
+    return FAT_EINVAL_SHAPE;
+  // rows of y lie apart; in place, every row stays where it is
+  if ((sh->num_heads > 1 && sh->y_stride_head < sh->head_dim) ||
+      (sh->tokens > 1 && sh->y_stride_token < sh->head_dim))
+    return FAT_EINVAL_SHAPE;
+  if (x == y && ((sh->tokens > 1 && sh->x_stride_token != sh->y_stride_token) ||
+                 (sh->num_heads > 1 && sh->x_stride_head != sh->y_stride_head)))
+    return FAT_EINVAL_SHAPE;
+  RowParams p{};
+  p.seg[0] = RowSeg{static_cast<const uint16_t *>(x), static_cast<uint16_t *>(y),
+                    sh->x_stride_token, sh->x_stride_head, sh->y_stride_token, sh->y_stride_head,
+                    sh->num_heads, 1, 0};
+  p.nseg = 1;
+  p.tokens = sh->tokens;
+  p.sign = inverse ? -1.f : 1.f;
+  p.positions = positions;
+  return launch_rows(p, rope, sh->head_dim, static_cast<cudaStream_t>(sh->stream));
+}
+
+int fat_paged_append(const fat_append_shape_t *sh, const fat_paged_cache_t *cache,
+                     const fat_rope_t *rope, const void *q, const void *k, const void *v,
+                     const int32_t *positions, const int32_t *slots, void *q_out) {
+  if (!sh || !cache) return FAT_EINVAL_NULL;
+  int lg = 0;
+  fat_paged_cache_t cc;
+  int rc = check_paged_cache(cache, &cc, &lg);
+  if (rc) return rc;
+  cache = &cc;
+  if (sh->tokens < 0 || (q && sh->num_heads_q <= 0)) return FAT_EINVAL_SHAPE;
+  if (rope) {
+    rc = check_rope(rope, cache->head_dim);
+    if (rc) return rc;
+  }
+  if ((q == nullptr) != (q_out == nullptr)) return FAT_EINVAL_NULL;
+  if (sh->tokens == 0) return FAT_OK;
+  if (!k || !v || !slots || (rope && !positions)) return FAT_EINVAL_NULL;
+  const int d = cache->head_dim, H = cache->num_heads;
+  if (odd16(q) || odd16(k) || odd16(v) || odd16(q_out) || odd4(positions) || odd4(slots) ||
+      bad_stride(sh->k_stride_token) || bad_stride(sh->k_stride_head) ||
+      bad_stride(sh->v_stride_token) || bad_stride(sh->v_stride_head))
+    return FAT_EINVAL_SHAPE;
+  if (q && (bad_stride(sh->q_stride_token) || bad_stride(sh->q_stride_head)))
+    return FAT_EINVAL_SHAPE;
+  const long long qd = (long long)sh->num_heads_q * d;
+  if (q && q == q_out && ((sh->tokens > 1 && sh->q_stride_token != qd) ||
+                          (sh->num_heads_q > 1 && sh->q_stride_head != d)))
+    return FAT_EINVAL_SHAPE;
+  RowParams p{};
+  rc = device_error_address(&p.err);
+  if (rc) return rc;
+  const int turn = rope ? 1 : 0;
+  p.seg[0] = RowSeg{static_cast<const uint16_t *>(k), static_cast<uint16_t *>(cache->k),
+                    sh->k_stride_token, sh->k_stride_head, cache->stride_token,
+                    cache->stride_head, H, turn, 1};
+  p.seg[1] = RowSeg{static_cast<const uint16_t *>(v), static_cast<uint16_t *>(cache->v),
+                    sh->v_stride_token, sh->v_stride_head, cache->stride_token,
+                    cache->stride_head, H, 0, 1};
+  p.nseg = 2;
+  if (q) {
+    p.seg[2] = RowSeg{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(q_out),
+                      sh->q_stride_token, sh->q_stride_head, qd, d, sh->num_heads_q, turn, 0};
+    p.nseg = 3;
+  }
+  p.tokens = sh->tokens;
+  p.sign = 1.f;
+  p.positions = positions;
+  p.slots = slots;
+  p.log2_page = lg;
+  p.page_stride = cache->stride_page;
+  p.num_slots = (long long)cache->num_pages << lg;
+  return launch_rows(p, rope, d, static_cast<cudaStream_t>(sh->stream));
+}
+
+}  // extern "C"

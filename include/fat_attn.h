@@ -69,6 +69,8 @@ extern "C" {
 #define FAT_DEVERR_SEQLENS 4     /* cu_seqlens had an entry outside [0, total_tokens] or out of
                                     order, or a document longer than max_seqlen (its rows beyond
                                     the grid were not computed) */
+#define FAT_DEVERR_PAGES 16      /* paged cache: the free pages or a table row do not hold a request,
+                                    or a page index lies outside the cache */
 
 typedef struct {
   int32_t total_tokens; /* T: sum of document lengths (rows of q, k, v) */
@@ -327,6 +329,154 @@ int fat_rmsnorm_bwd(long long rows, int dim, const void *x, const float *weight,
 int fat_cross_entropy(long long rows, int vocab, const void *logits, const int32_t *target,
                       float z_loss, float grad_scale, float *loss, float *lse, void *dlogits,
                       void *stream);
+
+/*
+ * Paged key/value cache: the operators of a serving step. (No counterpart in the FAT5 report beyond
+ * its plans for inference, "La suite" section; an addition of this library.) A decoder that serves
+ * many requests keeps their keys and values in pages of page_size tokens; a block table lists each
+ * request's pages in order. One step brings some new tokens of some requests:
+ *   fat_paged_plan    the step's maps on the GPU: pages taken from a free list, slots, positions;
+ *   fat_paged_append  the new keys and values into their slots (rotary embedding on the way);
+ *   fat_paged_attn    attention of the new tokens over their requests' pages.
+ * Nothing here reads a length on the host, so a step can be captured in a CUDA graph and replayed
+ * with other lengths. Index arrays (int32) need 4-byte alignment, everything else 16 bytes.
+ */
+typedef struct {
+  void *k, *v;        /* bf16, read by fat_paged_attn, written by fat_paged_append */
+  int32_t num_pages;
+  int32_t page_size;  /* tokens per page: a power of two, 16 .. 65536; num_pages * page_size < 2^31 */
+  int32_t num_heads;  /* key/value heads */
+  int32_t head_dim;   /* a multiple of 8 (fat_paged_attn: 64 or 128) */
+  /* strides of k and of v in elements, multiples of 8; a row of head_dim elements is contiguous.
+     [num_pages, page_size, num_heads, head_dim] in memory order gives (page_size * num_heads *
+     head_dim, num_heads * head_dim, head_dim); pages with the heads outside, or the pages of
+     several layers in one block, give others. */
+  int64_t stride_page, stride_token, stride_head;
+} fat_paged_cache_t;
+
+/*
+ * The step's maps. Request i holds ctx_lens[i] cached tokens in the first ceil(ctx / page_size)
+ * entries of its table row and brings new_lens[i] tokens. The pages it lacks are the next ones of
+ * free_pages, request by request:
+ *   block_table  [num_seqs, table_width]: the new pages' entries are written, the others stay;
+ *   cu_seqlens_q [num_seqs + 1]: running sums of new_lens;  seqlens_k [num_seqs]: ctx + new;
+ *   positions, slots [max_tokens]: of token cu_seqlens_q[i] + j, ctx_lens[i] + j and
+ *     page * page_size + offset; tokens behind the last request get position 0 and slot -1 (a
+ *     padded batch);
+ *   counts [2]: pages needed (the caller drops that many entries of free_pages), tokens.
+ * FAT_DEVERR_PAGES: the free list is too short (missing pages are written as -1), a request longer
+ * than table_width pages (it takes none), or a page index outside [0, num_pages); the tokens
+ * concerned get slot -1. FAT_DEVERR_SEQLENS: a negative length (taken as 0 and 0), or more tokens
+ * than max_tokens (cu_seqlens_q stops there). table_width = 0 is a table without entries.
+ */
+typedef struct {
+  int32_t num_seqs, page_size, num_pages;
+  int32_t table_width; /* entries of a block_table row */
+  int32_t num_free;    /* entries of free_pages */
+  int32_t max_tokens;  /* entries of positions and of slots */
+  void *stream;
+} fat_plan_shape_t;
+int fat_paged_plan(const fat_plan_shape_t *shape, const int32_t *ctx_lens, const int32_t *new_lens,
+                   const int32_t *free_pages, int32_t *block_table, int32_t *cu_seqlens_q,
+                   int32_t *seqlens_k, int32_t *positions, int32_t *slots, int32_t *counts);
+
+/*
+ * Rotary embedding at explicit positions. The first rotary_dim channels of a head turn, the others
+ * are copied: pair i by the angle position * theta'_i, theta_i = base^(-2 i / rotary_dim). Pairs
+ * are the channels (2i, 2i + 1) when interleaved, else (i, i + rotary_dim / 2). For contexts longer
+ * than a model was trained on:
+ *   original_length = 0: theta'_i = theta_i / factor (factor = 1: as it is);
+ *   original_length > 0: with t_i = original_length * theta_i / (2 pi) turns over that length and
+ *     keep_i = clamp((t_i - low_turns) / (high_turns - low_turns), 0, 1):
+ *     theta'_i = theta_i * (keep_i + (1 - keep_i) / factor);
+ *   amplitude multiplies the turned channels.
+ * fat_rope_init (host only) fills the record, which a program keeps for all its calls; its fields
+ * are the library's own. rotary_dim: a multiple of 16, 16 .. 256; base > 1; factor, amplitude > 0.
+ */
+#define FAT_ROPE_MAX_PAIRS 128
+typedef struct {
+  int32_t rotary_dim, interleaved;
+  float amplitude;
+  int32_t reserved;
+  uint64_t rate[FAT_ROPE_MAX_PAIRS]; /* turns per position of each pair, 2^-64 units */
+} fat_rope_t;
+int fat_rope_init(fat_rope_t *rope, int rotary_dim, int interleaved, double base, double factor,
+                  double low_turns, double high_turns, double original_length, double amplitude);
+
+/*
+ * y = the rotation of x (bf16 rows of head_dim channels) at positions[token] (int32, any value);
+ * inverse = 1: its transpose, which turns the gradient of y into the gradient of x. y may be x
+ * itself (equal strides) but not otherwise overlap it. Strides in elements, multiples of 8; rows of
+ * x may repeat (stride 0). head_dim a multiple of 8, at least rotary_dim. Angles are exact modulo
+ * one turn at any position, as in fat_rope_apply.
+ */
+typedef struct {
+  int32_t tokens, num_heads, head_dim;
+  int64_t x_stride_token, x_stride_head, y_stride_token, y_stride_head;
+  void *stream;
+} fat_rope_shape_t;
+int fat_rope_embed(const fat_rope_shape_t *shape, const fat_rope_t *rope, const void *x, void *y,
+                   const int32_t *positions, int inverse);
+
+/*
+ * New rows into the cache: token t's key and value rows [num_heads, head_dim] go to slot
+ * slots[t] = page * page_size + offset; a negative slot drops them (padding), one at or beyond
+ * num_pages * page_size drops them and sets FAT_DEVERR_INDEX. Slots of one call are distinct (if
+ * one is named twice, each 16 bytes there come from either row). With `rope` the keys are turned at
+ * positions[t] on the way (NULL: copied), and with q the queries are too, into q_out (bf16
+ * [tokens, num_heads_q, head_dim] contiguous, of every token, padding included; q itself is
+ * allowed when it is contiguous). q, k and v may be views of one packed projection: strides in
+ * elements, multiples of 8. q and q_out are both given or both NULL; positions may be NULL without
+ * rope.
+ */
+typedef struct {
+  int32_t tokens, num_heads_q;
+  int64_t q_stride_token, q_stride_head, k_stride_token, k_stride_head, v_stride_token,
+      v_stride_head;
+  void *stream;
+} fat_append_shape_t;
+int fat_paged_append(const fat_append_shape_t *shape, const fat_paged_cache_t *cache,
+                     const fat_rope_t *rope, const void *q, const void *k, const void *v,
+                     const int32_t *positions, const int32_t *slots, void *q_out);
+
+/*
+ * Attention of new tokens over a paged cache: fat_xattn_fwd with request i's seqlens_k[i] keys in
+ * the pages block_table[i][0 .. ceil(seqlens_k[i] / page_size)) instead of a packed array. Queries
+ * q [total_q, num_heads_q, head_dim] are packed by cu_seqlens_q; the last query lines up with the
+ * last key (append first); bias, causal mask, grouped heads, out and lse as there. Rows behind
+ * cu_seqlens_q[num_seqs] are left as they were.
+ *   - What lies in a page behind a request's last key is never used, whatever it holds (NaN and
+ *     infinities included). Keys and values below seqlens_k are finite: a value that the causal
+ *     mask hides from an earlier query of the same step still enters that query's product with
+ *     weight 0.
+ *   - A page index outside [0, num_pages) sets FAT_DEVERR_PAGES; its keys and values count as 0.
+ *   - A request whose query count exceeds max_seqlen_q or whose seqlens_k is negative, exceeds
+ *     max_seqlen_k or its table row (table_width pages) sets FAT_DEVERR_SEQLENS, as does a corrupt
+ *     cu_seqlens_q; its rows are left as they were.
+ *   - workspace: fat_paged_attn_workspace_size bytes (256-byte aligned, contents need not be
+ *     initialised), for this call alone until it has finished: calls that may overlap, and captured
+ *     graphs that do, take one each.
+ * head_dim 64 or 128, num_heads_q / num_heads at most 128. FAT_EUNSUPPORTED: more query heads per
+ * key/value head, or bias tables that shared memory does not hold (saturation distances of more
+ * than 8192 keys in all, or num_buckets * num_heads_q / num_heads beyond 4096 entries).
+ */
+typedef struct {
+  int32_t total_q;      /* rows of q and out */
+  int32_t num_seqs;
+  int32_t max_seqlen_q; /* bounds on the requests' query and key counts */
+  int32_t max_seqlen_k;
+  int32_t num_heads_q;
+  int32_t table_width;  /* entries of a block_table row */
+  void *stream;
+} fat_paged_shape_t;
+size_t fat_paged_attn_workspace_size(const fat_paged_shape_t *shape,
+                                     const fat_paged_cache_t *cache);
+int fat_paged_attn(const fat_paged_shape_t *shape, const fat_paged_cache_t *cache, const void *q,
+                   const int32_t *block_table, const int32_t *cu_seqlens_q,
+                   const int32_t *seqlens_k, const float *bias_table, int num_buckets,
+                   int max_distance, int bidirectional, const float *alibi_slopes, int causal,
+                   float softmax_scale, void *workspace, size_t workspace_bytes, void *out,
+                   float *lse);
 
 /* Synchronises `stream`, reads the current GPU's device error word, clears it, and returns
    FAT_OK if it was zero, else FAT_EDEVICE with the word's bits stored in *bits (if not NULL). */

@@ -1,0 +1,173 @@
+"""Argument checks of the paged-cache calls: what is refused on the host, before anything is
+enqueued, through the C ABI (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import attention_relative_position_gb300 as fa
+from attention_relative_position_gb300 import _build
+
+FAKE = 1 << 20  # aligned non-null host value; never dereferenced on these paths
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return fa.load()
+
+
+def test_exports(lib):
+    for name in ("fat_paged_plan", "fat_rope_init", "fat_rope_embed", "fat_paged_append",
+                 "fat_paged_attn", "fat_paged_attn_workspace_size"):
+        assert hasattr(lib, name) and hasattr(fa, name), name
+
+
+def _plan(lib, ptrs=None, **kw):
+    s = dict(num_seqs=2, page_size=16, num_pages=8, table_width=4, num_free=3, max_tokens=5)
+    s.update(kw)
+    p = [FAKE] * 9
+    for i, v in (ptrs or {}).items():
+        p[i] = v
+    return lib.fat_paged_plan(fa._PlanShape(*s.values(), None), *p)
+
+
+def test_plan_refusals(lib):
+    assert lib.fat_paged_plan(None, *[FAKE] * 9) == -1
+    for i in range(9):  # every array of this problem is needed, and 4-byte aligned
+        assert _plan(lib, {i: None}) == -1, i
+        assert _plan(lib, {i: FAKE + 2}) == -2, i
+    for bad in (dict(num_seqs=-1), dict(page_size=0), dict(page_size=8), dict(page_size=48),
+                dict(page_size=1 << 17), dict(num_pages=0), dict(table_width=-1),
+                dict(num_free=-1), dict(max_tokens=-1), dict(num_pages=1 << 27, page_size=16)):
+        assert _plan(lib, **bad) == -2, bad
+
+
+def test_rope_init_refusals_and_rates():
+    for kw in (dict(rotary_dim=0), dict(rotary_dim=8), dict(rotary_dim=24), dict(rotary_dim=272),
+               dict(rotary_dim=64, base=1.0), dict(rotary_dim=64, base=float("inf")),
+               dict(rotary_dim=64, base=float("nan")), dict(rotary_dim=64, factor=0.0),
+               dict(rotary_dim=64, factor=-2.0), dict(rotary_dim=64, amplitude=0.0),
+               dict(rotary_dim=64, amplitude=1e300), dict(rotary_dim=64, ramp=(4.0, 1.0, 4096.0)),
+               dict(rotary_dim=64, ramp=(1.0, 1.0, 4096.0)),
+               dict(rotary_dim=64, ramp=(-1.0, 4.0, 4096.0)),
+               dict(rotary_dim=64, ramp=(1.0, 4.0, -1.0))):
+        with pytest.raises(fa.FatAttnError) as e:
+            fa.fat_rope_init(**kw)
+        assert e.value.code == -2, kw
+    import math
+    from oracle import paged
+    for kw in (dict(), dict(factor=4.0), dict(base=500000.0, factor=8.0, ramp=(1.0, 4.0, 8192.0)),
+               dict(factor=0.25)):
+        r = fa.fat_rope_init(96, **kw)
+        want = paged.rope_angles([1.0], 96, **kw)[0] / (2 * math.pi)
+        for i in range(48):
+            # doubles on both sides: a few roundings of 2^-53 relative, 2^-53 of the fraction
+            assert abs(r.rate[i] / 2.0 ** 64 - (want[i] - math.floor(want[i]))) \
+                <= 16 * 2.0 ** -53 * max(1.0, want[i])
+
+
+def _embed(lib, rope, x=FAKE, y=FAKE + 4096, pos=FAKE, tokens=4, heads=2, d=64, xs=(128, 64),
+           ys=(128, 64)):
+    sh = fa._RopeShape(tokens, heads, d, *xs, *ys, None)
+    return lib.fat_rope_embed(sh, rope, x, y, pos, 0)
+
+
+def test_rope_embed_refusals(lib):
+    r = fa.fat_rope_init(64)
+    assert lib.fat_rope_embed(None, r, FAKE, FAKE, FAKE, 0) == -1
+    assert _embed(lib, None) == -1
+    assert _embed(lib, r, x=None) == -1 and _embed(lib, r, y=None) == -1
+    assert _embed(lib, r, pos=None) == -1
+    assert _embed(lib, r, x=FAKE + 8) == -2 and _embed(lib, r, y=FAKE + 2) == -2
+    assert _embed(lib, r, pos=FAKE + 2) == -2
+    assert _embed(lib, r, tokens=-1) == -2 and _embed(lib, r, heads=0) == -2
+    assert _embed(lib, r, d=60) == -2
+    assert _embed(lib, r, d=32) == -2  # fewer channels than the rotation
+    assert _embed(lib, r, xs=(132, 64)) == -2 and _embed(lib, r, xs=(-128, 64)) == -2
+    assert _embed(lib, r, ys=(128, 32)) == -2  # rows of y that overlap
+    assert _embed(lib, r, ys=(0, 64)) == -2
+    assert _embed(lib, r, x=FAKE, y=FAKE, xs=(256, 64)) == -2  # in place with other strides
+    assert _embed(lib, fa._Rope()) == -2  # a record that fat_rope_init has not filled
+    assert _embed(lib, r, tokens=0) == 0
+
+
+def _cache(**kw):
+    c = dict(k=FAKE, v=FAKE, num_pages=8, page_size=16, num_heads=2, head_dim=64,
+             stride_page=2048, stride_token=128, stride_head=64)
+    c.update(kw)
+    return fa._Cache(*c.values())
+
+
+BAD_CACHES = [(dict(k=None), -1), (dict(v=None), -1), (dict(num_pages=0), -2),
+              (dict(page_size=8), -2), (dict(page_size=24), -2), (dict(page_size=1 << 17), -2),
+              (dict(num_heads=0), -2), (dict(head_dim=0), -2), (dict(head_dim=60), -2),
+              (dict(k=FAKE + 8), -2), (dict(stride_page=2049), -2), (dict(stride_token=-128), -2),
+              (dict(stride_head=32), -2), (dict(stride_token=0), -2), (dict(stride_page=0), -2),
+              (dict(num_pages=1 << 28), -2)]
+
+
+def _append(lib, cache, rope=None, q=None, k=FAKE, v=FAKE, pos=None, slots=FAKE, qo=None, tokens=3,
+            hq=4, qs=(256, 64), ks=(128, 64), vs=(128, 64)):
+    sh = fa._AppendShape(tokens, hq, *qs, *ks, *vs, None)
+    return lib.fat_paged_append(sh, cache, rope, q, k, v, pos, slots, qo)
+
+
+def test_append_refusals(lib):
+    r = fa.fat_rope_init(64)
+    for kw, code in BAD_CACHES:
+        assert _append(lib, _cache(**kw)) == code, kw
+    c = _cache()
+    assert lib.fat_paged_append(None, c, None, None, FAKE, FAKE, None, FAKE, None) == -1
+    assert _append(lib, None) == -1
+    assert _append(lib, c, k=None) == -1 and _append(lib, c, v=None) == -1
+    assert _append(lib, c, slots=None) == -1
+    assert _append(lib, c, rope=r) == -1  # a rotation without positions
+    assert _append(lib, c, q=FAKE) == -1 and _append(lib, c, qo=FAKE) == -1
+    assert _append(lib, c, tokens=-1) == -2
+    assert _append(lib, c, q=FAKE, qo=FAKE, hq=0) == -2
+    assert _append(lib, c, q=FAKE, qo=FAKE, qs=(512, 64)) == -2  # in place, not contiguous
+    assert _append(lib, c, q=FAKE, qo=FAKE + 4096, qs=(257, 64)) == -2
+    assert _append(lib, c, ks=(129, 64)) == -2 and _append(lib, c, vs=(128, 63)) == -2
+    assert _append(lib, c, k=FAKE + 8) == -2 and _append(lib, c, slots=FAKE + 2) == -2
+    assert _append(lib, c, rope=fa.fat_rope_init(128), pos=FAKE) == -2
+    assert _append(lib, c, rope=r, pos=FAKE + 1) == -2
+    assert _append(lib, c, tokens=0) == 0
+
+
+def _attn(lib, cache, ptrs=None, bias=None, nb=0, md=0, bidir=1, slopes=None, ws=FAKE,
+          ws_bytes=1 << 40, **kw):
+    s = dict(total_q=6, num_seqs=2, max_seqlen_q=3, max_seqlen_k=64, num_heads_q=4, table_width=4)
+    s.update(kw)
+    p = dict(q=FAKE, table=FAKE, cu=FAKE, lk=FAKE, out=FAKE, lse=FAKE)
+    p.update(ptrs or {})
+    return lib.fat_paged_attn(fa._PagedShape(*s.values(), None), cache, p["q"], p["table"],
+                              p["cu"], p["lk"], bias, nb, md, bidir, slopes, 1, 0.125, ws,
+                              ws_bytes, p["out"], p["lse"])
+
+
+def test_attn_refusals(lib):
+    for kw, code in BAD_CACHES:
+        assert _attn(lib, _cache(**kw)) == code, kw
+    c = _cache()
+    assert _attn(lib, None) == -1
+    for name in ("q", "table", "cu", "lk", "out"):
+        assert _attn(lib, c, {name: None}) == -1, name
+    for name, off in (("q", 8), ("table", 2), ("cu", 2), ("lk", 1), ("out", 8), ("lse", 4)):
+        assert _attn(lib, c, {name: FAKE + off}) == -2, name
+    for bad in (dict(total_q=-1), dict(num_seqs=-1), dict(max_seqlen_q=-1), dict(max_seqlen_k=-1),
+                dict(num_heads_q=0), dict(num_heads_q=5), dict(table_width=-1)):
+        assert _attn(lib, c, **bad) == -2, bad
+    assert _attn(lib, _cache(head_dim=96, stride_head=96, stride_token=192, stride_page=4096)) == -2
+    assert _attn(lib, c, num_heads_q=258) == -5  # 129 query heads per key/value head
+    assert _attn(lib, c, num_seqs=70000) == -5
+    assert _attn(lib, c, bias=FAKE, nb=31, md=128, bidir=1) == -3
+    assert _attn(lib, c, bias=FAKE, nb=32, md=8, bidir=1) == -3
+    assert _attn(lib, c, bias=FAKE, nb=32, md=40000, bidir=1) == -5  # saturates too far out
+    assert _attn(lib, _cache(num_heads=1), bias=FAKE, nb=128, md=512, num_heads_q=64) == -5
+    assert _attn(lib, c, bias=FAKE + 4, nb=32, md=128) == -2
+    assert _attn(lib, c, slopes=FAKE + 4) == -2
+    assert _attn(lib, c, ws=FAKE + 16) == -2
+    # nothing to do: returns before touching the device
+    for empty in (dict(total_q=0), dict(num_seqs=0), dict(max_seqlen_q=0)):
+        assert _attn(lib, c, **empty) == 0, empty
+    assert lib.fat_paged_attn_workspace_size(None, ctypes.byref(c)) == 0
