@@ -322,9 +322,13 @@ namespace {
 struct TmapKey {
   const void *ptr;
   int T, H, d, box_c, box_rows, fp32;
+  // maps over pages: tokens per page and element strides (0 in the others)
+  int page = 0;
+  long long s_page = 0, s_token = 0, s_head = 0;
   bool operator==(const TmapKey &o) const {
     return ptr == o.ptr && T == o.T && H == o.H && d == o.d && box_c == o.box_c &&
-           box_rows == o.box_rows && fp32 == o.fp32;
+           box_rows == o.box_rows && fp32 == o.fp32 && page == o.page && s_page == o.s_page &&
+           s_token == o.s_token && s_head == o.s_head;
   }
 };
 constexpr int kTmapCache = 128;
@@ -368,6 +372,37 @@ int make_tmap_thd(CUtensorMap *map, const void *ptr, int T, int H, int d, int bo
   }
   tmap_store(key, *map);
   return 0;
+}
+
+int make_tmap_pages(CUtensorMap *map, const void *ptr, const fat_paged_cache_t &c, int box_rows,
+                    int *head_outer) {
+  const bool outer = c.stride_head > c.stride_token;
+  *head_outer = outer ? 1 : 0;
+  const long long inner = outer ? c.stride_token : c.stride_head;
+  const long long mid = outer ? c.stride_head : c.stride_token;
+  if (mid % inner || c.stride_page % mid || c.stride_page >= (1LL << 39)) return FAT_EUNSUPPORTED;
+  const TmapKey key{ptr,  c.num_pages, c.num_heads, c.head_dim,     64, box_rows,
+                    0,    c.page_size, c.stride_page, c.stride_token, c.stride_head};
+  if (tmap_lookup(key, map)) return FAT_OK;
+  if (!resolve_encode()) return FAT_ECUDA;
+  const cuuint64_t H = (cuuint64_t)c.num_heads, S = (cuuint64_t)c.page_size;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, outer ? S : H, outer ? H : S,
+                              (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)inner * 2, (cuuint64_t)mid * 2,
+                                 (cuuint64_t)c.stride_page * 2};
+  const cuuint32_t rows = (cuuint32_t)box_rows;
+  const cuuint32_t box[4] = {64, outer ? rows : 1, outer ? 1 : rows, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_last_error("cuTensorMapEncodeTiled(pages)", (int)r, "");
+    return FAT_ECUDA;
+  }
+  tmap_store(key, *map);
+  return FAT_OK;
 }
 
 int make_tmap_thd_f32(CUtensorMap *map, const void *ptr, int T, int H, int d, int box_c,

@@ -388,6 +388,13 @@ void set_last_error(const char *what, int code, const char *text);
 // Tensor map over a [T, H, d] bf16 tensor, box = 64 channels x 1 head x box_rows tokens,
 // 128-byte swizzle (the shared-memory layout the tcgen05 descriptors expect).
 int make_tmap_thd(CUtensorMap *map, const void *ptr, int T, int H, int d, int box_rows);
+// Tensor map over the pages of a cache (checked by check_paged_cache): coordinates (channel, head,
+// token, page), or (channel, token, head, page) when the heads lie outside the tokens of a page
+// (*head_outer = 1): the map's dimensions go by rising stride, each a multiple of the one before.
+// Box: 64 channels x 1 head x box_rows tokens of one page, 128-byte swizzle. Returns FAT_*
+// (FAT_EUNSUPPORTED: strides that are no such multiples).
+int make_tmap_pages(CUtensorMap *map, const void *ptr, const fat_paged_cache_t &c, int box_rows,
+                    int *head_outer);
 // Tensor map over a [T, H, d] fp32 tensor, box = box_c channels x 1 head x box_rows tokens (for
 // bulk reductions from a shared-memory tile): 64-byte swizzle when a box row is 64 bytes (16-byte
 // chunk c of row r at c ^ ((r / 2) % 4)), else row-major without swizzle.

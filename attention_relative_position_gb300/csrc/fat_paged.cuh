@@ -1,0 +1,202 @@
+// fat_paged.cuh -- what the kernels of paged attention share: their parameters, the division of a
+// ragged batch into equal shares of work, and the layout of the partial rows that shares leave.
+//
+// Division. The lengths are known on the device only. An item is (request, key/value head) for the
+// few-row kernel and (request, key/value head, block of queries) for the tile kernel; its cost is
+// the number of key stages its rows see (at least 1). All items in order form one line of total
+// cost U, and CTA c of G takes the stretch [c, c + 1) * max(ceil(U / G), min_share): every SM gets
+// the same number of stages whatever the lengths are. An item cut by a boundary leaves, in each
+// CTA that holds a part, unnormalised fp32 rows with their maximum and sum; a CTA has at most two
+// such parts (its first item's end or middle, its last item's beginning), so the workspace depends
+// on the grid alone, and a second grid merges them in the order of the CTAs (no atomics: the result
+// does not depend on timing).
+#pragma once
+#include "fat_attn_internal.cuh"
+
+namespace fat {
+
+constexpr int kMaxBiasSpan = 8192;     // sat_neg + sat_pos of a bias table, at most
+constexpr int kMaxBiasEntries = 4096;  // buckets x group, at most
+
+struct PagedParams {
+  int total_q, n, max_q, max_k, hq, hkv, group, width, log2_page, num_pages, head_outer;
+  const __nv_bfloat16 *q;
+  const int32_t *table, *cu, *lk;
+  BiasParams bias;
+  int causal;
+  float scale_log2;
+  __nv_bfloat16 *out;
+  float *lse;
+  int *err;
+  long long timeout_ns;
+  int debug_flags;
+  int few_rows;   // requests with at most this many rows (queries x group) are the few-row kernel's
+  int split;      // 0: items are not cut (each goes to the CTA in whose share it begins)
+  float *part;    // partial rows of this kernel's grid (see PartLayout)
+};
+
+// A request as the kernels see it.
+struct PagedDoc {
+  int sq, lq, lk;
+  bool ok;
+};
+__device__ __forceinline__ PagedDoc paged_doc(const PagedParams &p, int i) {
+  PagedDoc d;
+  d.sq = __ldg(p.cu + i);
+  const int eq = __ldg(p.cu + i + 1);
+  d.lk = __ldg(p.lk + i);
+  d.ok = d.sq >= 0 && eq >= d.sq && eq <= p.total_q && eq - d.sq <= p.max_q && d.lk >= 0 &&
+         d.lk <= p.max_k && d.lk <= ((long long)p.width << p.log2_page);
+  d.lq = eq - d.sq;
+  return d;
+}
+
+// ---- partial rows -------------------------------------------------------------------------------
+// Per CTA: two records (part 0: its first item, begun by an earlier CTA; part 1: its last item,
+// begun here and continued by the next CTA), then for each record [rows][D] unnormalised rows and
+// [rows][2] (maximum in log2 units, sum).
+struct PartRecord {
+  int valid;   // this part exists
+  int ends;    // the item ends in this CTA
+  int row0;    // first row of q and out of the item's block (token), and its key/value head
+  int hk;
+  int rows;    // packed rows (token-major, the group's heads inside)
+  int pad[3];
+};
+__host__ __device__ inline size_t part_records_floats(int ctas) {
+  return (size_t)ctas * 2 * sizeof(PartRecord) / 4;
+}
+__host__ __device__ inline size_t part_floats(int ctas, int rows, int d) {
+  return part_records_floats(ctas) + (size_t)ctas * 2 * rows * (d + 2);
+}
+__device__ __forceinline__ PartRecord *part_record(float *part, int cta, int which) {
+  return reinterpret_cast<PartRecord *>(part) + cta * 2 + which;
+}
+template <int ROWS, int D>
+__device__ __forceinline__ float *part_rows(float *part, int ctas, int cta, int which) {
+  return part + part_records_floats(ctas) + (size_t)(cta * 2 + which) * ROWS * D;
+}
+template <int ROWS, int D>
+__device__ __forceinline__ float *part_stats(float *part, int ctas, int cta, int which) {
+  return part + part_records_floats(ctas) + (size_t)ctas * 2 * ROWS * D +
+         (size_t)(cta * 2 + which) * ROWS * 2;
+}
+
+// ---- this CTA's stretch -------------------------------------------------------------------------
+constexpr int kShareDocs = 256;  // requests staged in shared memory from the stretch's first on
+
+struct Share {
+  long long total;   // U
+  long long lo, hi;  // this CTA's stretch; lo >= hi: none
+  int doc;           // the request in which it begins
+  long long off;     // cost of that request before lo
+};
+
+// Scratch of share_find, and the staged requests.
+template <int NT>
+struct ShareSmem {
+  long long wsum[NT / 32 + 1];
+  long long off;
+  int doc;
+  int sq[kShareDocs], lq[kShareDocs], lk[kShareDocs];
+};
+
+template <int NT>
+__device__ __forceinline__ long long share_scan(long long v, ShareSmem<NT> &s, long long *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  __syncthreads();
+  if (lane == 31) s.wsum[warp] = inc;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += s.wsum[w];
+    all += s.wsum[w];
+  }
+  *total = all;
+  return before + inc - v;
+}
+
+// Find this CTA's stretch (all NT threads of the block; cost(doc) is the request's cost in this
+// kernel, 0 for the others'), report corrupt requests once, stage the requests it may hold.
+template <int NT, typename CostFn>
+__device__ __forceinline__ Share share_find(const PagedParams &p, int min_share, CostFn cost,
+                                            ShareSmem<NT> &s) {
+  const int tid = threadIdx.x;
+  Share r;
+  // the requests' costs; those of the first NT requests stay in a register for the second pass
+  long long first = 0, mine = 0;
+  for (int i = tid; i < p.n; i += NT) {
+    const PagedDoc d = paged_doc(p, i);
+    if (!d.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
+    const long long c = d.ok && d.lq > 0 ? cost(d) : 0;
+    if (i < NT) first = c;
+    mine += c;
+  }
+  long long total, before = share_scan<NT>(p.n <= NT ? first : mine, s, &total);
+  r.total = total;
+  const long long G = gridDim.x;
+  const long long share = max((total + G - 1) / G, (long long)min_share);
+  r.lo = blockIdx.x * share;
+  r.hi = min(total, r.lo + share);
+  r.doc = 0;
+  r.off = 0;
+  if (r.lo >= r.hi) return r;
+  long long base = 0;
+  for (int i0 = 0;; i0 += NT) {  // the stretch begins in one of the requests: this ends
+    long long c = first, chunk = total;
+    if (p.n > NT) {
+      const int i = i0 + tid;
+      c = 0;
+      if (i < p.n) {
+        const PagedDoc d = paged_doc(p, i);
+        c = d.ok && d.lq > 0 ? cost(d) : 0;
+      }
+      before = share_scan<NT>(c, s, &chunk);
+    }
+    if (r.lo >= base + before && r.lo < base + before + c) {
+      s.doc = i0 + tid;
+      s.off = r.lo - (base + before);
+    }
+    base += chunk;
+    if (r.lo < base || i0 + NT >= p.n) break;  // the same for every thread
+  }
+  __syncthreads();
+  r.doc = s.doc;
+  r.off = s.off;
+  for (int i = tid; i < kShareDocs; i += NT) {
+    PagedDoc d{0, 0, 0, false};
+    if (r.doc + i < p.n) d = paged_doc(p, r.doc + i);
+    s.sq[i] = d.sq;
+    s.lq[i] = d.ok ? d.lq : 0;
+    s.lk[i] = d.lk;
+  }
+  __syncthreads();
+  return r;
+}
+
+template <int NT>
+__device__ __forceinline__ PagedDoc share_doc(const PagedParams &p, const ShareSmem<NT> &s,
+                                              int first_doc, int doc) {
+  const int i = doc - first_doc;
+  if (i < kShareDocs) return PagedDoc{s.sq[i], s.lq[i], s.lk[i], s.lq[i] > 0};
+  PagedDoc d = paged_doc(p, doc);
+  d.ok = d.ok && d.lq > 0;
+  return d;
+}
+
+// ---- launchers ----------------------------------------------------------------------------------
+constexpr int kFewRows = 16;  // rows of the few-row kernel's items
+int paged_few_ctas();
+// Whether items are cut: contexts of at most this many keys are computed by one CTA in a few stages
+// per warp, which costs less than the merge grid.
+constexpr int kWholeKeys = 1024;
+int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
+
+}  // namespace fat

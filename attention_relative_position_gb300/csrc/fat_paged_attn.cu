@@ -7,26 +7,19 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "fat_attn_internal.cuh"
+#include "fat_paged.cuh"
 
 namespace fat {
 namespace {
 
-struct PagedParams {
-  int total_q, n, max_q, max_k, hq, hkv, group, width, log2_page, num_pages;
+struct RowsParams {
+  PagedParams p;
+  const __nv_bfloat16 *k, *v;
   long long page_stride, tok_stride, head_stride;
-  const __nv_bfloat16 *q, *k, *v;
-  const int32_t *table, *cu, *lk;
-  BiasParams bias;
-  int causal;
-  float scale_log2;
-  __nv_bfloat16 *out;
-  float *lse;
-  int *err;
 };
-
 template <int D>
-__global__ void __launch_bounds__(128) fat_paged_rows_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(128) fat_paged_rows_kernel(const RowsParams rp) {
+  const PagedParams &p = rp.p;
   constexpr int CPL = D / 32;
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x;
@@ -41,7 +34,7 @@ __global__ void __launch_bounds__(128) fat_paged_rows_kernel(const PagedParams p
       hi = mid - 1;
   }
   const int sq = __ldg(p.cu + lo), eq = __ldg(p.cu + lo + 1), lk = __ldg(p.lk + lo);
-  if (row < sq || row >= eq) return;
+  if (row < sq || row >= eq || (long long)(eq - sq) * p.group <= p.few_rows) return;
   if (sq < 0 || eq > p.total_q || eq - sq > p.max_q || lk < 0 || lk > p.max_k ||
       lk > ((long long)p.width << p.log2_page)) {
     if (lane == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
@@ -61,10 +54,10 @@ __global__ void __launch_bounds__(128) fat_paged_rows_kernel(const PagedParams p
       const int page = __ldg(p.table + (size_t)lo * p.width + (key >> p.log2_page));
       float dot = 0.f;
       if ((unsigned)page < (unsigned)p.num_pages) {
-        off = page * p.page_stride + (key & ((1 << p.log2_page) - 1)) * p.tok_stride +
-              hk * p.head_stride;
+        off = page * rp.page_stride + (key & ((1 << p.log2_page) - 1)) * rp.tok_stride +
+              hk * rp.head_stride;
         for (int c = 0; c < D; ++c)
-          dot = fmaf(__bfloat162float(q[c]), __bfloat162float(p.k[off + c]), dot);
+          dot = fmaf(__bfloat162float(q[c]), __bfloat162float(rp.k[off + c]), dot);
       } else {
         atomicOr(p.err, FAT_DEVERR_PAGES);
       }
@@ -87,7 +80,7 @@ __global__ void __launch_bounds__(128) fat_paged_rows_kernel(const PagedParams p
       const long long oj = __shfl_sync(0xffffffffu, off, j);
       if (oj >= 0)
         for (int c = 0; c < CPL; ++c)
-          o[c] = fmaf(pj, __bfloat162float(p.v[oj + lane * CPL + c]), o[c]);
+          o[c] = fmaf(pj, __bfloat162float(rp.v[oj + lane * CPL + c]), o[c]);
     }
   }
   for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
@@ -96,6 +89,118 @@ __global__ void __launch_bounds__(128) fat_paged_rows_kernel(const PagedParams p
     p.out[((size_t)row * p.hq + h) * D + lane * CPL + c] = __float2bfloat16(o[c] * inv);
   if (lane == 0 && p.lse)
     p.lse[(size_t)h * p.total_q + row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+}
+
+// ---- merge of cut items -------------------------------------------------------------------------
+// A chain is an item's parts in the order of their CTAs: part 1 of the CTA in which it begins, then
+// part 0 of the following ones up to the one in which it ends. One block per (CTA, kMergeRows rows)
+// whose CTA begins a chain; kMergeWarps warps share each row's parts, every lane owning D / 32
+// channels. Reads chain x (D + 2) x 4 bytes per row from L2, writes a row of out: bound by the
+// latency of the chain (a few parts, or all CTAs' when one long item fills the grid).
+constexpr int kMergeRows = 2, kMergeWarps = 4;
+
+template <int ROWS, int D>
+__global__ void __launch_bounds__(kMergeRows *kMergeWarps * 32)
+    fat_paged_merge_kernel(const __grid_constant__ PagedParams p, const int ctas) {
+  constexpr int CPL = D / 32;
+  __shared__ float acc_s[kMergeRows][kMergeWarps][D];
+  __shared__ float2 st_s[kMergeRows][kMergeWarps];
+  grid_dep_wait();
+  const int c = blockIdx.x;
+  const PartRecord rec = *part_record(p.part, c, 1);
+  const int r = blockIdx.y * kMergeRows + (threadIdx.x >> 5) % kMergeRows;
+  if (!rec.valid || blockIdx.y * kMergeRows >= rec.rows) return;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) / kMergeRows;
+  // parts 1 .. n - 1 lie in CTAs c + 1 .. c + n - 1
+  int n = 1;
+  for (int i0 = 1;; i0 += 32) {
+    const int i = c + i0 + lane;
+    const unsigned end = __ballot_sync(0xffffffffu, i >= ctas || part_record(p.part, i, 0)->ends ||
+                                                        !part_record(p.part, i, 0)->valid);
+    if (end) {
+      n = min(i0 + __ffs(end), ctas - c);
+      break;
+    }
+  }
+  float m = -INFINITY, l = 0.f, o[CPL];
+#pragma unroll
+  for (int k = 0; k < CPL; ++k) o[k] = 0.f;
+  if (r < rec.rows) {
+#pragma unroll 4
+    for (int i = w; i < n; i += kMergeWarps) {
+      const int which = i == 0 ? 1 : 0;
+      const float2 st = *reinterpret_cast<const float2 *>(
+          part_stats<ROWS, D>(p.part, ctas, c + i, which) + r * 2);
+      const float *src = part_rows<ROWS, D>(p.part, ctas, c + i, which) + r * D + lane * CPL;
+      float v[CPL];
+      if constexpr (CPL == 4) {
+        const float4 t = *reinterpret_cast<const float4 *>(src);
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+      } else {
+        const float2 t = *reinterpret_cast<const float2 *>(src);
+        v[0] = t.x, v[1] = t.y;
+      }
+      const float mn = fmaxf(m, st.x);
+      const float fo = m == -INFINITY ? 0.f : ex2(m - mn);
+      const float fn = st.x == -INFINITY ? 0.f : ex2(st.x - mn);
+      l = l * fo + st.y * fn;
+#pragma unroll
+      for (int k = 0; k < CPL; ++k) o[k] = o[k] * fo + v[k] * fn;
+      m = mn;
+    }
+  }
+  const int rs = (threadIdx.x >> 5) % kMergeRows;
+#pragma unroll
+  for (int k = 0; k < CPL; ++k) acc_s[rs][w][lane * CPL + k] = o[k];
+  if (lane == 0) st_s[rs][w] = make_float2(m, l);
+  __syncthreads();
+  if (w != 0 || r >= rec.rows) return;
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMergeWarps; ++i) M = fmaxf(M, st_s[rs][i].x);
+#pragma unroll
+  for (int k = 0; k < CPL; ++k) o[k] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMergeWarps; ++i) {
+    const float2 st = st_s[rs][i];
+    const float f = st.x == -INFINITY ? 0.f : ex2(st.x - M);
+    L += st.y * f;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) o[k] += acc_s[rs][i][lane * CPL + k] * f;
+  }
+  const float inv = L > 0.f ? 1.0f / L : 0.f;
+  const int q = r / p.group, h = rec.hk * p.group + (r - q * p.group);
+  const size_t row = (size_t)rec.row0 + q;
+  __nv_bfloat16 *dst = p.out + (row * p.hq + h) * D + lane * CPL;
+  if constexpr (CPL == 4)
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  else
+    *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[(size_t)h * p.total_q + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int ROWS, int D>
+int launch_merge(const PagedParams &p, int ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas, ROWS / kMergeRows);
+  cfg.blockDim = dim3(kMergeRows * kMergeWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fat_paged_merge_kernel<ROWS, D>, p, ctas);
+  if (e == cudaSuccess) return FAT_OK;
+  set_last_error("paged merge launch", (int)e, cudaGetErrorString(e));
+  return FAT_ECUDA;
+}
+
+size_t few_bytes(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
+  if (sh->max_seqlen_k <= kWholeKeys) return 0;
+  return part_floats(paged_few_ctas(), kFewRows, c->head_dim) * 4;
 }
 
 int check_shape(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
@@ -122,7 +227,7 @@ extern "C" {
 
 size_t fat_paged_attn_workspace_size(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache) {
   if (check_shape(sh, cache)) return 0;
-  return 0;
+  return few_bytes(sh, cache);
 }
 
 int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, const void *q,
@@ -142,7 +247,7 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   rc = make_bias_params(&p.bias, bias_table, num_buckets, max_distance, bidirectional, alibi_slopes);
   if (rc) return rc;
   const int group = sh->num_heads_q / cache->num_heads;
-  if (bias_table && (p.bias.sat_pos + p.bias.sat_neg > 8192 || num_buckets * group > 4096))
+  if (bias_table && (p.bias.sat_pos + p.bias.sat_neg > kMaxBiasSpan || num_buckets * group > kMaxBiasEntries))
     return FAT_EUNSUPPORTED;
   if (sh->total_q == 0 || sh->num_seqs == 0 || sh->max_seqlen_q == 0) return FAT_OK;
   if (!q || !cu_seqlens_q || !seqlens_k || !out || (sh->table_width > 0 && !block_table))
@@ -165,12 +270,7 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   p.width = sh->table_width;
   p.log2_page = lg;
   p.num_pages = cache->num_pages;
-  p.page_stride = cache->stride_page;
-  p.tok_stride = cache->stride_token;
-  p.head_stride = cache->stride_head;
   p.q = static_cast<const __nv_bfloat16 *>(q);
-  p.k = static_cast<const __nv_bfloat16 *>(cache->k);
-  p.v = static_cast<const __nv_bfloat16 *>(cache->v);
   p.table = block_table;
   p.cu = cu_seqlens_q;
   p.lk = seqlens_k;
@@ -178,16 +278,31 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   p.scale_log2 = softmax_scale * kLog2e;
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
-  const dim3 grid(sh->total_q, (sh->num_heads_q + 3) / 4);
+  runtime_knobs(&p.timeout_ns, &p.debug_flags);
+  p.few_rows = kFewRows;
+  const int d = cache->head_dim;
   const cudaStream_t s = static_cast<cudaStream_t>(sh->stream);
-  if (cache->head_dim == 64)
-    fat_paged_rows_kernel<64><<<grid, 128, 0, s>>>(p);
-  else
-    fat_paged_rows_kernel<128><<<grid, 128, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) return FAT_OK;
-  set_last_error("paged attention launch", (int)e, cudaGetErrorString(e));
-  return FAT_ECUDA;
+  if ((long long)sh->max_seqlen_q * group > kFewRows) {
+    const RowsParams rp{p, static_cast<const __nv_bfloat16 *>(cache->k),
+                        static_cast<const __nv_bfloat16 *>(cache->v), cache->stride_page,
+                        cache->stride_token, cache->stride_head};
+    const dim3 grid(sh->total_q, (sh->num_heads_q + 3) / 4);
+    if (d == 64)
+      fat_paged_rows_kernel<64><<<grid, 128, 0, s>>>(rp);
+    else
+      fat_paged_rows_kernel<128><<<grid, 128, 0, s>>>(rp);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) {
+      set_last_error("paged attention launch", (int)e, cudaGetErrorString(e));
+      return FAT_ECUDA;
+    }
+  }
+  p.split = need > 0;
+  p.part = static_cast<float *>(workspace);
+  rc = launch_paged_few(p, *cache, s);
+  if (rc || !p.split) return rc;
+  return d == 64 ? launch_merge<kFewRows, 64>(p, paged_few_ctas(), s)
+                 : launch_merge<kFewRows, 128>(p, paged_few_ctas(), s);
 }
 
 }  // extern "C"

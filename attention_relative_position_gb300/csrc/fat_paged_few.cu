@@ -1,0 +1,579 @@
+// fat_paged_few.cu -- attention over a paged cache for requests with few rows: a decode step, a few
+// drafted tokens, a group's heads over their key/value head (queries x group heads <= 16 rows).
+//
+// The work is one read of the requests' keys and values; the rows ride along. A CTA (one per SM)
+// takes an equal share of all key stages (fat_paged.cuh); a stage is 16 KB of keys and values (32
+// tokens at head_dim 128, 64 at 64). Four warps work on their own, each with a ring of three
+// stages that it fills by TMA itself (pages of 16 tokens and more come as boxes of 16 rows x 64
+// channels, 128-byte swizzle) and waits for: no producer warp and no hand-off between warps, the
+// next stages' copies and their page numbers are always in flight. Per stage and warp: S = Q K^T
+// for 16 rows with warp-level matrix products (Q in registers), bias and mask, a running maximum
+// that moves only when it grows by more than 2^32, P as bf16 in registers, O += P V. Warp-level
+// products suffice here: with 16 of 128 rows of a tcgen05 tile filled, its round trip through
+// tensor memory would cost more than the 64 products of a stage.
+// A short item (two stages at most) is one warp's; the warps of a longer one merge their rows in
+// shared memory once. Items cut by the share boundaries leave partial rows for the merge grid.
+#include <algorithm>
+#include <cstdint>
+
+#include "fat_paged.cuh"
+
+namespace fat {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kRing = 3;           // stages per warp
+constexpr int kShortStages = 2;    // items of at most this many stages are one warp's
+constexpr int kMinShare = 8;       // stages a CTA takes at least
+constexpr int kOStride = 72;       // floats per row of a merge buffer (64 channels at a time)
+
+template <int D>
+struct FewCfg {
+  static constexpr int KT = 64 * 64 / D;         // tokens per stage
+  static constexpr int DB = D / 64;              // 64-channel blocks
+  static constexpr int PIECE = 16 * 128;         // one box: 16 rows x 64 channels
+  static constexpr int PIECES = KT / 16;         // boxes per 64-channel block
+  static constexpr int BLK = KT * 128;           // one 64-channel block of a stage
+  static constexpr int TILE = DB * BLK;          // K or V of a stage
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int OFF_MERGE = kWarps * kRing * STAGE;
+  static constexpr int OFF_STATS = OFF_MERGE + kWarps * kFewRows * kOStride * 4;
+  static constexpr int OFF_BAR = OFF_STATS + (kWarps + 1) * kFewRows * 2 * 4;
+  static constexpr int OFF_THR = OFF_BAR + kWarps * kRing * 8 + 64;
+  static constexpr int OFF_SHARE = OFF_THR + kMaxThresholds * 4;
+  static constexpr int OFF_LUT = OFF_SHARE + (int)sizeof(ShareSmem<kThreads>);
+  // bucket bytes of the deltas -sat_neg .. sat_pos
+  static int bytes(const BiasParams &b) {
+    return OFF_LUT + (b.table ? (b.sat_neg + b.sat_pos + 1 + 15) & ~15 : 0);
+  }
+  static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
+  static_assert(STAGE == 16384, "a stage is 16 KB");
+};
+
+// Cost of a request: the stages of its keys for every key/value head.
+template <int D>
+struct FewCost {
+  const PagedParams &p;
+  __device__ long long operator()(const PagedDoc &d) const {
+    if ((long long)d.lq * p.group > p.few_rows) return 0;
+    constexpr int KT = FewCfg<D>::KT;
+    return (long long)p.hkv * max(1, (d.lk + KT - 1) / KT);
+  }
+};
+
+// The items of a share in order.
+struct FewItem {
+  int doc, hk, sq, lq, lk, nst;  // nst: stages of the item (0: no keys)
+  int s0, s1;                    // the stages taken here
+  bool begins, ends;
+};
+template <int D>
+struct FewWalk {
+  const PagedParams &p;
+  const ShareSmem<kThreads> &sm;
+  int first_doc, doc, hk;
+  long long left;  // cost still to take
+  int off;         // cost of the current item that lies before the stretch
+  __device__ bool next(FewItem &it) {
+    while (left > 0 && doc < p.n) {
+      const PagedDoc d = share_doc(p, sm, first_doc, doc);
+      if (!d.ok || (long long)d.lq * p.group > p.few_rows) {
+        ++doc;
+        hk = 0;
+        continue;
+      }
+      constexpr int KT = FewCfg<D>::KT;
+      it.nst = (d.lk + KT - 1) / KT;
+      const int cost = max(1, it.nst);
+      const int o = off;
+      off = 0;
+      const int take = (int)min(left, (long long)(cost - o));
+      left -= take;
+      it.doc = doc;
+      it.hk = hk;
+      it.sq = d.sq;
+      it.lq = d.lq;
+      it.lk = d.lk;
+      if (++hk == p.hkv) {
+        hk = 0;
+        ++doc;
+      }
+      if (!p.split) {  // whole items: the one that begins earlier is another CTA's
+        if (o > 0) continue;
+        it.s0 = 0;
+        it.s1 = it.nst;
+        it.begins = it.ends = true;
+        return true;
+      }
+      it.s0 = min(o, it.nst);
+      it.s1 = min(o + take, it.nst);
+      it.begins = o == 0;
+      it.ends = o + take == cost;
+      return true;
+    }
+    return false;
+  }
+};
+
+// The stages of one warp, in order: of a short item all (items take turns over the warps), of a
+// longer one every kWarps-th, continuing the turn of the item before.
+template <int D>
+struct FewStages {
+  FewWalk<D> walk;
+  FewItem it;
+  int s, step;   // next stage of `it` and the distance to the one after
+  int turn;      // stages dealt so far, modulo kWarps
+  int shorts;    // short items so far
+  __device__ explicit FewStages(const FewWalk<D> &w) : walk(w), s(0), step(1), turn(0), shorts(0) {}
+  // The next item with its first stage for `warp` (s >= it.s1: none of its stages).
+  __device__ bool item(int warp) {
+    if (!walk.next(it)) return false;
+    if (it.s1 - it.s0 <= kShortStages) {
+      s = (shorts & (kWarps - 1)) == warp ? it.s0 : it.s1;
+      step = 1;
+      ++shorts;
+    } else {
+      s = it.s0 + ((warp - turn) & (kWarps - 1));
+      step = kWarps;
+      turn = (turn + it.s1 - it.s0) & (kWarps - 1);
+    }
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    fat_paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ PagedParams p) {
+  using C = FewCfg<D>;
+  constexpr int KT = C::KT, NT = KT / 8;  // key groups of 8
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto &share_s = *reinterpret_cast<ShareSmem<kThreads> *>(sm + C::OFF_SHARE);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR) + warp * kRing;
+  volatile int *abort_flag =
+      reinterpret_cast<volatile int *>(sm + C::OFF_BAR + kWarps * kRing * 8);
+  int *thr_s = reinterpret_cast<int *>(sm + C::OFF_THR);
+  float *stats = reinterpret_cast<float *>(sm + C::OFF_STATS);  // [warps + 1][16][2]
+  grid_dep_launch();
+  if (tid == 0) *abort_flag = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(full + i, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  for (int i = tid; i < p.bias.n_thr; i += kThreads) thr_s[i] = p.bias.thr[i];
+  if (p.split && tid < 2) {
+    PartRecord *r = part_record(p.part, blockIdx.x, tid);
+    r->valid = 0;
+  }
+  const Share sh = share_find<kThreads>(p, kMinShare, FewCost<D>{p}, share_s);
+  if (sh.lo >= sh.hi) return;
+  const Watchdog wd{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
+  const PagedDoc d0 = share_doc(p, share_s, sh.doc, sh.doc);
+  const int cost0 = max(1, (d0.lk + KT - 1) / KT);
+  const FewWalk<D> start{p, share_s, sh.doc, sh.doc, (int)(sh.off / cost0), sh.hi - sh.lo,
+                         (int)(sh.off % cost0)};
+  uint8_t *ring = sm + warp * kRing * C::STAGE;
+
+  // ---- copies: a cursor ahead of the computation. Lane i < PIECES holds the page of piece i.
+  FewStages<D> ahead(start);
+  bool more = false;
+  int page_next = 0;
+  auto fetch_page = [&]() {  // the page numbers of the stage the cursor stands on
+    if (more && lane < C::PIECES) {
+      const int tok = ahead.s * KT + lane * 16;
+      page_next = tok < ahead.it.lk
+                      ? __ldg(p.table + (size_t)ahead.it.doc * p.width + (tok >> p.log2_page))
+                      : 0;
+    }
+  };
+  auto settle = [&]() {  // on to an item that has a stage for this warp
+    more = true;
+    while (ahead.s >= ahead.it.s1)
+      if (!ahead.item(warp)) {
+        more = false;
+        break;
+      }
+    fetch_page();
+  };
+  auto issue = [&](int slot) {  // the cursor's stage into `slot`; the cursor moves on
+    const int tok = ahead.s * KT + lane * 16;
+    const int pieces = min(C::PIECES, (ahead.it.lk - ahead.s * KT + 15) >> 4);
+    uint8_t *dst = ring + slot * C::STAGE + lane * C::PIECE;
+    if (lane == 0) mbar_arrive_expect_tx(full + slot, pieces * C::DB * 2 * C::PIECE);
+    __syncwarp();
+    if (lane < pieces) {
+      int page = page_next;
+      if ((unsigned)page >= (unsigned)p.num_pages) {
+        atomicOr(p.err, FAT_DEVERR_PAGES);
+        page = p.num_pages;  // just outside: filled with zeros
+      }
+      const int in = tok & ((1 << p.log2_page) - 1), hk = ahead.it.hk;
+      const int c1 = p.head_outer ? in : hk, c2 = p.head_outer ? hk : in;
+#pragma unroll
+      for (int b = 0; b < C::DB; ++b) {
+        tma_load_4d(&tm_k, full + slot, dst + b * C::BLK, 64 * b, c1, c2, page);
+        tma_load_4d(&tm_v, full + slot, dst + C::TILE + b * C::BLK, 64 * b, c1, c2, page);
+      }
+    }
+    ahead.s += ahead.step;
+    settle();
+  };
+  ahead.it.s1 = 0;
+  settle();
+  int issued = 0;  // stages whose copies were started
+  bool live = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
+#pragma unroll
+  for (int i = 0; i < kRing; ++i)
+    if (more && live) {
+      issue(i);
+      ++issued;
+    }
+
+  // ---- computation
+  FewStages<D> cur(start);
+  const int G = p.group;
+  const int r0 = lane >> 2, r1 = r0 + 8;  // this thread's rows, keys 2 (lane % 4) + {0, 1} + 8 t
+  const bool t5 = p.bias.table != nullptr;
+  const bool biased = p.bias.has_bias != 0;
+  // bucket of every near delta, one byte each (the first copies are on their way)
+  uint8_t *lut = sm + C::OFF_LUT;
+  const int span = p.bias.sat_neg + p.bias.sat_pos;
+  if (t5) {
+    for (int i = tid; i <= span; i += kThreads)
+      lut[i] = (uint8_t)t5_bucket_staged(i - p.bias.sat_neg, p.bias, thr_s);
+    __syncthreads();
+  }
+  const int bucket_pos = t5 ? lut[span] : 0, bucket_neg = t5 ? lut[0] : 0;
+  int done = 0;           // stages computed
+  int slot = 0, phase = 0;
+  bool ok = true;
+  while (cur.item(warp)) {
+    const FewItem &it = cur.it;
+    const bool shortened = it.s1 - it.s0 <= kShortStages;  // one warp's
+    const bool mine = !shortened || ((cur.shorts - 1) & (kWarps - 1)) == warp;
+    if (!mine) continue;
+    const int rows = it.lq * G, shift = it.lk - it.lq;
+    // Q as the A operand: rows r0, r1, channels 16 kk + 2 (lane % 4) + {0, 1} and + 8
+    uint32_t qf[D / 16][4];
+    {
+      const __nv_bfloat16 *qb = p.q + ((size_t)it.sq * p.hq + (size_t)it.hk * G) * D;
+      const int q0 = r0 / G, q1 = r1 / G;
+      const uint32_t *a = reinterpret_cast<const uint32_t *>(
+          qb + ((size_t)q0 * p.hq + (r0 - q0 * G)) * D) + (lane & 3);
+      const uint32_t *b = reinterpret_cast<const uint32_t *>(
+          qb + ((size_t)q1 * p.hq + (r1 - q1 * G)) * D) + (lane & 3);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][0] = r0 < rows ? __ldg(a + kk * 8) : 0u;
+        qf[kk][1] = r1 < rows ? __ldg(b + kk * 8) : 0u;
+        qf[kk][2] = r0 < rows ? __ldg(a + kk * 8 + 4) : 0u;
+        qf[kk][3] = r1 < rows ? __ldg(b + kk * 8 + 4) : 0u;
+      }
+    }
+    // per row: query position among the keys, last visible key, bias constants
+    int qpos[2], lim[2], head[2];
+    float slope[2], far_pos[2], far_neg[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i ? r1 : r0, q = r / G;
+      qpos[i] = q + shift;
+      head[i] = it.hk * G + (r - q * G);
+      lim[i] = p.causal ? min(qpos[i], it.lk - 1) : it.lk - 1;
+      slope[i] = p.bias.slopes ? __ldg(p.bias.slopes + head[i]) * kLog2e : 0.f;
+      far_pos[i] = t5 ? __ldg(p.bias.table + (size_t)bucket_pos * p.hq + head[i]) * kLog2e : 0.f;
+      far_neg[i] = t5 ? __ldg(p.bias.table + (size_t)bucket_neg * p.hq + head[i]) * kLog2e : 0.f;
+    }
+    const int lim_all = p.causal ? min(shift, it.lk - 1) : it.lk - 1;  // every row sees up to here
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[D / 8][4];
+#pragma unroll
+    for (int t = 0; t < D / 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+
+    for (int s = cur.s; s < it.s1; s += cur.step) {
+      if (ok) ok = warp_wait(full + slot, phase, wd);
+      if (ok) {
+        const uint8_t *kt = ring + slot * C::STAGE;
+        uint8_t *vt = ring + slot * C::STAGE + C::TILE;
+        const int k0 = s * KT;
+        if (k0 + KT > it.lk) {  // values behind the last key: whatever the page holds, they are 0
+          const int first = it.lk - k0;
+          for (int i = first * 8 * C::DB + lane; i < KT * 8 * C::DB; i += 32) {
+            const int row = i / (8 * C::DB), c = i % (8 * C::DB);
+            *reinterpret_cast<uint4 *>(vt + (c >> 3) * C::BLK + row * 128 + (c & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+        }
+        // S = Q K^T
+        float x[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+        const uint32_t ka = smem_u32(kt) + (lane & 7) * 128 + (lane >> 4) * 1024;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t ch = ((uint32_t)(((2 * kk) & 7) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4;
+#pragma unroll
+          for (int t = 0; t < NT; t += 2) {
+            uint32_t b[4];
+            ldmatrix_x4(ka + (kk >> 2) * C::BLK + t * 1024 + ch, b);
+            mma_16x8x16(x[t], qf[kk], b[0], b[1]);
+            mma_16x8x16(x[t + 1], qf[kk], b[2], b[3]);
+          }
+        }
+        // logits in log2 units
+        const int kb = k0 + 2 * (lane & 3);
+        if (!biased) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[t][e] *= p.scale_log2;
+        } else if (k0 - (shift + it.lq - 1) >= p.bias.sat_pos ||
+                   k0 + KT - 1 - shift <= -p.bias.sat_neg) {  // every delta on one far side
+          const bool pos = k0 - (shift + it.lq - 1) >= p.bias.sat_pos;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = e >> 1;
+              const float dist = fabsf((float)(kb + 8 * t + (e & 1) - qpos[i]));
+              x[t][e] = fmaf(x[t][e], p.scale_log2,
+                             fmaf(-slope[i], dist, pos ? far_pos[i] : far_neg[i]));
+            }
+        } else {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = e >> 1, delta = kb + 8 * t + (e & 1) - qpos[i];
+              float b = -slope[i] * fabsf((float)delta);
+              if (t5) {
+                const int bk = lut[min(max(delta + p.bias.sat_neg, 0), span)];
+                b += __ldg(p.bias.table + bk * p.hq + head[i]) * kLog2e;
+              }
+              x[t][e] = fmaf(x[t][e], p.scale_log2, b);
+            }
+        }
+        if (k0 + KT - 1 > lim_all) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (kb + 8 * t + (e & 1) > lim[e >> 1]) x[t][e] = -INFINITY;
+        }
+        // the running maximum, moved only when it grows by more than 2^32
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mx[0] = fmax3(mx[0], x[t][0], x[t][1]);
+          mx[1] = fmax3(mx[1], x[t][2], x[t][3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+        }
+        const bool up0 = mx[0] > m[0] + 32.f || (m[0] == -INFINITY && mx[0] > m[0]);
+        const bool up1 = mx[1] > m[1] + 32.f || (m[1] == -INFINITY && mx[1] > m[1]);
+        if (__any_sync(0xffffffffu, up0 || up1)) {
+          const float f0 = up0 ? ex2(m[0] - mx[0]) : 1.f, f1 = up1 ? ex2(m[1] - mx[1]) : 1.f;
+          if (up0) m[0] = mx[0];
+          if (up1) m[1] = mx[1];
+          l[0] *= f0;
+          l[1] *= f1;
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t) {
+            o[t][0] *= f0;
+            o[t][1] *= f0;
+            o[t][2] *= f1;
+            o[t][3] *= f1;
+          }
+        }
+        const float s0 = m[0] == -INFINITY ? 0.f : m[0], s1 = m[1] == -INFINITY ? 0.f : m[1];
+        // P (sums from the unrounded weights), O += P V
+        const uint32_t va = smem_u32(vt) + ((lane & 7) + ((lane >> 3) & 1) * 8) * 128;
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk) {
+          uint32_t pf[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float a = ex2(x[2 * kk + h][0] - s0), b = ex2(x[2 * kk + h][1] - s0);
+            const float c = ex2(x[2 * kk + h][2] - s1), d = ex2(x[2 * kk + h][3] - s1);
+            l[0] += a + b;
+            l[1] += c + d;
+            pf[2 * h] = pack_bf16x2(a, b);
+            pf[2 * h + 1] = pack_bf16x2(c, d);
+          }
+#pragma unroll
+          for (int t = 0; t < D / 8; t += 2) {
+            uint32_t b[4];
+            ldmatrix_x4_trans(va + (t >> 3) * C::BLK + kk * 2048 +
+                                  (((uint32_t)((t & 7) + (lane >> 4)) ^ (lane & 7)) << 4), b);
+            mma_16x8x16(o[t], pf, b[0], b[1]);
+            mma_16x8x16(o[t + 1], pf, b[2], b[3]);
+          }
+        }
+        // the stage has been read (and its zeros written): its place is free for the next copy
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (more && live) {
+          issue(slot);
+          ++issued;
+        }
+        ++done;
+      }
+      if (++slot == kRing) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+
+    // ---- the item's rows: whole ones to out, cut ones to the workspace
+    const bool whole = it.begins && it.ends;
+    const int which = it.begins ? 1 : 0;
+    if (!whole && (shortened || warp == 0) && lane == 0) {
+      PartRecord *rec = part_record(p.part, blockIdx.x, which);
+      rec->valid = 1;
+      rec->ends = it.ends;
+      rec->row0 = it.sq;
+      rec->hk = it.hk;
+      rec->rows = rows;
+    }
+    if (shortened) {
+      float *po = whole ? nullptr : part_rows<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which);
+      float *ps = whole ? nullptr : part_stats<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = i ? r1 : r0;
+        if (r >= rows) continue;
+        const int q = r / G, h = it.hk * G + (r - q * G), row = it.sq + q;
+        if (whole) {
+          const float inv = l[i] > 0.f ? 1.0f / l[i] : 0.f;
+          uint32_t *dst =
+              reinterpret_cast<uint32_t *>(p.out + ((size_t)row * p.hq + h) * D) + (lane & 3);
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t)
+            dst[t * 4] = pack_bf16x2(o[t][2 * i] * inv, o[t][2 * i + 1] * inv);
+          if ((lane & 3) == 0 && p.lse != nullptr)
+            p.lse[(size_t)h * p.total_q + row] =
+                l[i] > 0.f ? (m[i] + __log2f(l[i])) * kLn2 : -INFINITY;
+        } else {
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t)
+            *reinterpret_cast<float2 *>(po + r * D + t * 8 + 2 * (lane & 3)) =
+                make_float2(o[t][2 * i], o[t][2 * i + 1]);
+          if ((lane & 3) == 0) *reinterpret_cast<float2 *>(ps + r * 2) = make_float2(m[i], l[i]);
+        }
+      }
+      continue;
+    }
+    // merge of the four warps
+    if ((lane & 3) == 0) {
+      *reinterpret_cast<float2 *>(stats + (warp * kFewRows + r0) * 2) = make_float2(m[0], l[0]);
+      *reinterpret_cast<float2 *>(stats + (warp * kFewRows + r1) * 2) = make_float2(m[1], l[1]);
+    }
+    __syncthreads();
+    float f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i ? r1 : r0;
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stats[(w * kFewRows + r) * 2]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v = *reinterpret_cast<const float2 *>(stats + (w * kFewRows + r) * 2);
+        if (v.x != -INFINITY) L += v.y * ex2(v.x - M);
+      }
+      f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - M);
+      if (warp == 0 && (lane & 3) == 0) {
+        float *fin = stats + (kWarps * kFewRows + r) * 2;
+        fin[0] = M;
+        fin[1] = L;
+      }
+    }
+    float *buf = reinterpret_cast<float *>(sm + C::OFF_MERGE);
+    const float *fin = stats + kWarps * kFewRows * 2;
+#pragma unroll
+    for (int b = 0; b < C::DB; ++b) {  // 64 channels at a time
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        float *dst = buf + warp * kFewRows * kOStride + t * 8 + 2 * (lane & 3);
+        *reinterpret_cast<float2 *>(dst + r0 * kOStride) =
+            make_float2(o[b * 8 + t][0] * f[0], o[b * 8 + t][1] * f[0]);
+        *reinterpret_cast<float2 *>(dst + r1 * kOStride) =
+            make_float2(o[b * 8 + t][2] * f[1], o[b * 8 + t][3] * f[1]);
+      }
+      __syncthreads();
+      for (int i = tid; i < rows * 16; i += kThreads) {
+        const int r = i >> 4, c = (i & 15) * 4;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 v =
+              *reinterpret_cast<const float4 *>(buf + (w * kFewRows + r) * kOStride + c);
+          a.x += v.x;
+          a.y += v.y;
+          a.z += v.z;
+          a.w += v.w;
+        }
+        const float M = fin[r * 2], L = fin[r * 2 + 1];
+        if (whole) {
+          const int q = r / G, h = it.hk * G + (r - q * G), row = it.sq + q;
+          const float inv = L > 0.f ? 1.0f / L : 0.f;
+          *reinterpret_cast<uint2 *>(p.out + ((size_t)row * p.hq + h) * D + b * 64 + c) =
+              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+          if (b == 0 && c == 0 && p.lse != nullptr)
+            p.lse[(size_t)h * p.total_q + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+        } else {
+          *reinterpret_cast<float4 *>(part_rows<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which) +
+                                      r * D + b * 64 + c) = a;
+          if (b == 0 && c == 0)
+            *reinterpret_cast<float2 *>(
+                part_stats<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which) + r * 2) =
+                make_float2(M, L);
+        }
+      }
+      __syncthreads();  // buf (and, after the last block, stats) are written again
+    }
+  }
+  // copies that were started and not waited for (after a timeout) land before the block exits
+  for (; done < issued; ++done) {
+    mbar_wait_teardown(full + done % kRing, (done / kRing) & 1, kTeardownNs);
+  }
+}
+
+template <int D>
+int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
+  PagedParams pp = p;
+  CUtensorMap mk, mv;
+  int rc = make_tmap_pages(&mk, c.k, c, 16, &pp.head_outer);
+  if (!rc) rc = make_tmap_pages(&mv, c.v, c, 16, &pp.head_outer);
+  if (rc) return rc;
+  const size_t smem = FewCfg<D>::bytes(p.bias) + 1024;
+  if (prepare_kernel((const void *)fat_paged_few_kernel<D>, smem, kThreads, 0)) return FAT_ECUDA;
+  fat_paged_few_kernel<D><<<paged_few_ctas(), kThreads, smem, stream>>>(mk, mv, pp);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return FAT_OK;
+  set_last_error("paged few-row kernel launch", (int)e, cudaGetErrorString(e));
+  return FAT_ECUDA;
+}
+
+}  // namespace
+
+int paged_few_ctas() { return sm_count() > 0 ? sm_count() : 152; }
+
+int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
+  return c.head_dim == 64 ? launch_t<64>(p, c, stream) : launch_t<128>(p, c, stream);
+}
+
+}  // namespace fat

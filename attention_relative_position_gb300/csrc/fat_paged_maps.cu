@@ -365,7 +365,7 @@ int check_paged_cache(const fat_paged_cache_t *in, fat_paged_cache_t *c, int *lo
   if (c->page_size < 16 || c->page_size != (1 << lg)) return FAT_EINVAL_SHAPE;
   if ((long long)c->num_pages * c->page_size > 0x7fffffffLL) return FAT_EINVAL_SHAPE;
   // a stride over one entry says nothing
-  if (c->num_heads == 1) c->stride_head = c->head_dim;
+  if (c->num_heads == 1) c->stride_head = c->stride_token;
   if (c->num_pages == 1) c->stride_page = c->stride_token * c->page_size;
   if (odd16(c->k) || odd16(c->v) || bad_stride(c->stride_page) || bad_stride(c->stride_token) ||
       bad_stride(c->stride_head))
