@@ -322,13 +322,14 @@ namespace {
 struct TmapKey {
   const void *ptr;
   int T, H, d, box_c, box_rows, fp32;
-  // maps over pages: tokens per page and element strides (0 in the others)
+  // maps over pages: tokens per page and element strides (0 in the others); heads per box
   int page = 0;
   long long s_page = 0, s_token = 0, s_head = 0;
+  int box_heads = 1;
   bool operator==(const TmapKey &o) const {
     return ptr == o.ptr && T == o.T && H == o.H && d == o.d && box_c == o.box_c &&
            box_rows == o.box_rows && fp32 == o.fp32 && page == o.page && s_page == o.s_page &&
-           s_token == o.s_token && s_head == o.s_head;
+           s_token == o.s_token && s_head == o.s_head && box_heads == o.box_heads;
   }
 };
 constexpr int kTmapCache = 128;
@@ -355,12 +356,18 @@ void tmap_store(const TmapKey &k, const CUtensorMap &map) {
 }  // namespace
 
 int make_tmap_thd(CUtensorMap *map, const void *ptr, int T, int H, int d, int box_rows) {
-  const TmapKey key{ptr, T, H, d, 64, box_rows, 0};
+  return make_tmap_rows(map, ptr, T, H, d, 1, box_rows);
+}
+
+int make_tmap_rows(CUtensorMap *map, const void *ptr, int T, int H, int d, int box_heads,
+                   int box_rows) {
+  TmapKey key{ptr, T, H, d, 64, box_rows, 0};
+  key.box_heads = box_heads;
   if (tmap_lookup(key, map)) return 0;
   if (!resolve_encode()) return -1;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)(T > 0 ? T : 1)};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

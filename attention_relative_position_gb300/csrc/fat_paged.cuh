@@ -194,9 +194,13 @@ __device__ __forceinline__ PagedDoc share_doc(const PagedParams &p, const ShareS
 // ---- launchers ----------------------------------------------------------------------------------
 constexpr int kFewRows = 16;  // rows of the few-row kernel's items
 int paged_few_ctas();
+constexpr int kTileRows = 256;  // packed rows of the tile kernel's items, at most
+int paged_tile_ctas();
 // Whether items are cut: contexts of at most this many keys are computed by one CTA in a few stages
 // per warp, which costs less than the merge grid.
 constexpr int kWholeKeys = 1024;
-int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
+int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream,
+                     bool overlap_previous);
+int launch_paged_tile(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
 
 }  // namespace fat

@@ -1,9 +1,10 @@
 // fat_paged_attn.cu -- attention of new tokens over a paged key/value cache: per row (query, head)
 // softmax(scale * q K^T + bias) V over the row's visible keys, whose pages a block table lists.
+// Argument checks, the choice of kernels, and the merge of items that share boundaries cut.
 //
-// One warp per row walks its keys 32 at a time: lane i takes the dot product with key i (bias and
-// mask applied), the maximum and sum are running ones, and the lanes then own head_dim / 32
-// channels each for P V.
+// A request goes to the kernel that fits its rows (queries x group heads): at most 16 to the few-row
+// kernel, more to the tile kernel. Only the device knows the lengths, so a call whose bounds allow
+// both launches both, the second beside the first, and each skips the other's requests.
 #include <algorithm>
 #include <cstdint>
 
@@ -11,85 +12,6 @@
 
 namespace fat {
 namespace {
-
-struct RowsParams {
-  PagedParams p;
-  const __nv_bfloat16 *k, *v;
-  long long page_stride, tok_stride, head_stride;
-};
-template <int D>
-__global__ void __launch_bounds__(128) fat_paged_rows_kernel(const RowsParams rp) {
-  const PagedParams &p = rp.p;
-  constexpr int CPL = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x;
-  const int h = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (h >= p.hq) return;
-  int lo = 0, hi = p.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.cu + mid) <= row)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const int sq = __ldg(p.cu + lo), eq = __ldg(p.cu + lo + 1), lk = __ldg(p.lk + lo);
-  if (row < sq || row >= eq || (long long)(eq - sq) * p.group <= p.few_rows) return;
-  if (sq < 0 || eq > p.total_q || eq - sq > p.max_q || lk < 0 || lk > p.max_k ||
-      lk > ((long long)p.width << p.log2_page)) {
-    if (lane == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
-    return;
-  }
-  const int qpos = lk - (eq - sq) + (row - sq), hk = h / p.group;
-  const int nk = p.causal ? min(lk, qpos + 1) : lk;
-  const float slope = p.bias.slopes ? __ldg(p.bias.slopes + h) * kLog2e : 0.f;
-  const __nv_bfloat16 *q = p.q + ((size_t)row * p.hq + h) * D;
-  float m = -INFINITY, l = 0.f, o[CPL];
-  for (int c = 0; c < CPL; ++c) o[c] = 0.f;
-  for (int k0 = 0; k0 < nk; k0 += 32) {
-    const int key = k0 + lane;
-    long long off = -1;
-    float x = -INFINITY;
-    if (key < nk) {
-      const int page = __ldg(p.table + (size_t)lo * p.width + (key >> p.log2_page));
-      float dot = 0.f;
-      if ((unsigned)page < (unsigned)p.num_pages) {
-        off = page * rp.page_stride + (key & ((1 << p.log2_page) - 1)) * rp.tok_stride +
-              hk * rp.head_stride;
-        for (int c = 0; c < D; ++c)
-          dot = fmaf(__bfloat162float(q[c]), __bfloat162float(rp.k[off + c]), dot);
-      } else {
-        atomicOr(p.err, FAT_DEVERR_PAGES);
-      }
-      const int delta = key - qpos;
-      x = dot * p.scale_log2;
-      if (p.bias.table)
-        x += __ldg(p.bias.table + (size_t)t5_bucket_dev(delta, p.bias) * p.hq + h) * kLog2e;
-      x -= slope * (float)(delta < 0 ? -delta : delta);
-    }
-    float mx = x;
-    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-    const float mn = fmaxf(m, mx);
-    const float corr = m == -INFINITY ? 0.f : ex2(m - mn);
-    const float pr = x == -INFINITY ? 0.f : ex2(x - mn);
-    m = mn;
-    l = l * corr + pr;
-    for (int c = 0; c < CPL; ++c) o[c] *= corr;
-    for (int j = 0; j < min(32, nk - k0); ++j) {
-      const float pj = __shfl_sync(0xffffffffu, pr, j);
-      const long long oj = __shfl_sync(0xffffffffu, off, j);
-      if (oj >= 0)
-        for (int c = 0; c < CPL; ++c)
-          o[c] = fmaf(pj, __bfloat162float(rp.v[oj + lane * CPL + c]), o[c]);
-    }
-  }
-  for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
-  for (int c = 0; c < CPL; ++c)
-    p.out[((size_t)row * p.hq + h) * D + lane * CPL + c] = __float2bfloat16(o[c] * inv);
-  if (lane == 0 && p.lse)
-    p.lse[(size_t)h * p.total_q + row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-}
 
 // ---- merge of cut items -------------------------------------------------------------------------
 // A chain is an item's parts in the order of their CTAs: part 1 of the CTA in which it begins, then
@@ -108,9 +30,9 @@ __global__ void __launch_bounds__(kMergeRows *kMergeWarps * 32)
   grid_dep_wait();
   const int c = blockIdx.x;
   const PartRecord rec = *part_record(p.part, c, 1);
-  const int r = blockIdx.y * kMergeRows + (threadIdx.x >> 5) % kMergeRows;
   if (!rec.valid || blockIdx.y * kMergeRows >= rec.rows) return;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) / kMergeRows;
+  const int rs = (threadIdx.x >> 5) % kMergeRows;
   // parts 1 .. n - 1 lie in CTAs c + 1 .. c + n - 1
   int n = 1;
   for (int i0 = 1;; i0 += 32) {
@@ -122,69 +44,72 @@ __global__ void __launch_bounds__(kMergeRows *kMergeWarps * 32)
       break;
     }
   }
-  float m = -INFINITY, l = 0.f, o[CPL];
+  for (int r0 = blockIdx.y * kMergeRows; r0 < rec.rows; r0 += gridDim.y * kMergeRows) {
+    const int r = r0 + rs;
+    float m = -INFINITY, l = 0.f, o[CPL];
 #pragma unroll
-  for (int k = 0; k < CPL; ++k) o[k] = 0.f;
-  if (r < rec.rows) {
+    for (int k = 0; k < CPL; ++k) o[k] = 0.f;
+    if (r < rec.rows) {
 #pragma unroll 4
-    for (int i = w; i < n; i += kMergeWarps) {
-      const int which = i == 0 ? 1 : 0;
-      const float2 st = *reinterpret_cast<const float2 *>(
-          part_stats<ROWS, D>(p.part, ctas, c + i, which) + r * 2);
-      const float *src = part_rows<ROWS, D>(p.part, ctas, c + i, which) + r * D + lane * CPL;
-      float v[CPL];
-      if constexpr (CPL == 4) {
-        const float4 t = *reinterpret_cast<const float4 *>(src);
-        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-      } else {
-        const float2 t = *reinterpret_cast<const float2 *>(src);
-        v[0] = t.x, v[1] = t.y;
+      for (int i = w; i < n; i += kMergeWarps) {
+        const int which = i == 0 ? 1 : 0;
+        const float2 st = *reinterpret_cast<const float2 *>(
+            part_stats<ROWS, D>(p.part, ctas, c + i, which) + r * 2);
+        const float *src = part_rows<ROWS, D>(p.part, ctas, c + i, which) + r * D + lane * CPL;
+        float v[CPL];
+        if constexpr (CPL == 4) {
+          const float4 t = *reinterpret_cast<const float4 *>(src);
+          v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+        } else {
+          const float2 t = *reinterpret_cast<const float2 *>(src);
+          v[0] = t.x, v[1] = t.y;
+        }
+        const float mn = fmaxf(m, st.x);
+        const float fo = m == -INFINITY ? 0.f : ex2(m - mn);
+        const float fn = st.x == -INFINITY ? 0.f : ex2(st.x - mn);
+        l = l * fo + st.y * fn;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) o[k] = o[k] * fo + v[k] * fn;
+        m = mn;
       }
-      const float mn = fmaxf(m, st.x);
-      const float fo = m == -INFINITY ? 0.f : ex2(m - mn);
-      const float fn = st.x == -INFINITY ? 0.f : ex2(st.x - mn);
-      l = l * fo + st.y * fn;
-#pragma unroll
-      for (int k = 0; k < CPL; ++k) o[k] = o[k] * fo + v[k] * fn;
-      m = mn;
     }
+    __syncthreads();  // the rows before have been read
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) acc_s[rs][w][lane * CPL + k] = o[k];
+    if (lane == 0) st_s[rs][w] = make_float2(m, l);
+    __syncthreads();
+    if (w != 0 || r >= rec.rows) continue;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMergeWarps; ++i) M = fmaxf(M, st_s[rs][i].x);
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) o[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMergeWarps; ++i) {
+      const float2 st = st_s[rs][i];
+      const float f = st.x == -INFINITY ? 0.f : ex2(st.x - M);
+      L += st.y * f;
+#pragma unroll
+      for (int k = 0; k < CPL; ++k) o[k] += acc_s[rs][i][lane * CPL + k] * f;
+    }
+    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    const int q = r / p.group, h = rec.hk * p.group + (r - q * p.group);
+    const size_t row = (size_t)rec.row0 + q;
+    __nv_bfloat16 *dst = p.out + (row * p.hq + h) * D + lane * CPL;
+    if constexpr (CPL == 4)
+      *reinterpret_cast<uint2 *>(dst) =
+          make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    else
+      *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[(size_t)h * p.total_q + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
   }
-  const int rs = (threadIdx.x >> 5) % kMergeRows;
-#pragma unroll
-  for (int k = 0; k < CPL; ++k) acc_s[rs][w][lane * CPL + k] = o[k];
-  if (lane == 0) st_s[rs][w] = make_float2(m, l);
-  __syncthreads();
-  if (w != 0 || r >= rec.rows) return;
-  float M = -INFINITY, L = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMergeWarps; ++i) M = fmaxf(M, st_s[rs][i].x);
-#pragma unroll
-  for (int k = 0; k < CPL; ++k) o[k] = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMergeWarps; ++i) {
-    const float2 st = st_s[rs][i];
-    const float f = st.x == -INFINITY ? 0.f : ex2(st.x - M);
-    L += st.y * f;
-#pragma unroll
-    for (int k = 0; k < CPL; ++k) o[k] += acc_s[rs][i][lane * CPL + k] * f;
-  }
-  const float inv = L > 0.f ? 1.0f / L : 0.f;
-  const int q = r / p.group, h = rec.hk * p.group + (r - q * p.group);
-  const size_t row = (size_t)rec.row0 + q;
-  __nv_bfloat16 *dst = p.out + (row * p.hq + h) * D + lane * CPL;
-  if constexpr (CPL == 4)
-    *reinterpret_cast<uint2 *>(dst) =
-        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  else
-    *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[(size_t)h * p.total_q + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
 template <int ROWS, int D>
 int launch_merge(const PagedParams &p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas, ROWS / kMergeRows);
+  cfg.gridDim = dim3((unsigned)ctas, std::min(ROWS / kMergeRows, 16));
   cfg.blockDim = dim3(kMergeRows * kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -198,9 +123,22 @@ int launch_merge(const PagedParams &p, int ctas, cudaStream_t stream) {
   return FAT_ECUDA;
 }
 
-size_t few_bytes(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
-  if (sh->max_seqlen_k <= kWholeKeys) return 0;
-  return part_floats(paged_few_ctas(), kFewRows, c->head_dim) * 4;
+// The kernels a call launches and their partial rows' places in the workspace. When every request
+// has exactly max_seqlen_q queries (as the totals say), one kernel takes them all.
+struct Plan {
+  bool few, tile, split;
+  size_t few_off, bytes;
+};
+Plan make_plan(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
+  Plan l{};
+  const long long rows = (long long)sh->max_seqlen_q * (sh->num_heads_q / c->num_heads);
+  l.tile = rows > kFewRows;
+  l.few = !l.tile || (long long)sh->num_seqs * sh->max_seqlen_q != sh->total_q;
+  l.split = sh->max_seqlen_k > kWholeKeys;
+  if (!l.split) return l;
+  if (l.tile) l.few_off = (part_floats(paged_tile_ctas(), kTileRows, c->head_dim) * 4 + 255) & ~(size_t)255;
+  l.bytes = l.few_off + (l.few ? part_floats(paged_few_ctas(), kFewRows, c->head_dim) * 4 : 0);
+  return l;
 }
 
 int check_shape(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
@@ -227,7 +165,7 @@ extern "C" {
 
 size_t fat_paged_attn_workspace_size(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache) {
   if (check_shape(sh, cache)) return 0;
-  return few_bytes(sh, cache);
+  return make_plan(sh, cache).bytes;
 }
 
 int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, const void *q,
@@ -252,7 +190,8 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   if (sh->total_q == 0 || sh->num_seqs == 0 || sh->max_seqlen_q == 0) return FAT_OK;
   if (!q || !cu_seqlens_q || !seqlens_k || !out || (sh->table_width > 0 && !block_table))
     return FAT_EINVAL_NULL;
-  const size_t need = fat_paged_attn_workspace_size(sh, cache);
+  const Plan plan = make_plan(sh, cache);
+  const size_t need = plan.bytes;
   if (need && !workspace) return FAT_EINVAL_NULL;
   if (odd(q, 16) || odd(out, 16) || odd(lse, 16) || odd(bias_table, 16) || odd(alibi_slopes, 16) ||
       odd(block_table, 4) || odd(cu_seqlens_q, 4) || odd(seqlens_k, 4) || odd(workspace, 256) ||
@@ -282,27 +221,28 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   p.few_rows = kFewRows;
   const int d = cache->head_dim;
   const cudaStream_t s = static_cast<cudaStream_t>(sh->stream);
-  if ((long long)sh->max_seqlen_q * group > kFewRows) {
-    const RowsParams rp{p, static_cast<const __nv_bfloat16 *>(cache->k),
-                        static_cast<const __nv_bfloat16 *>(cache->v), cache->stride_page,
-                        cache->stride_token, cache->stride_head};
-    const dim3 grid(sh->total_q, (sh->num_heads_q + 3) / 4);
-    if (d == 64)
-      fat_paged_rows_kernel<64><<<grid, 128, 0, s>>>(rp);
-    else
-      fat_paged_rows_kernel<128><<<grid, 128, 0, s>>>(rp);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) {
-      set_last_error("paged attention launch", (int)e, cudaGetErrorString(e));
-      return FAT_ECUDA;
-    }
-  }
-  p.split = need > 0;
+  p.split = plan.split;
+  PagedParams pf = p;
   p.part = static_cast<float *>(workspace);
-  rc = launch_paged_few(p, *cache, s);
-  if (rc || !p.split) return rc;
-  return d == 64 ? launch_merge<kFewRows, 64>(p, paged_few_ctas(), s)
-                 : launch_merge<kFewRows, 128>(p, paged_few_ctas(), s);
+  pf.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.few_off);
+  if (plan.tile) {
+    rc = launch_paged_tile(p, *cache, s);
+    if (rc) return rc;
+  }
+  if (plan.few) {
+    rc = launch_paged_few(pf, *cache, s, plan.tile);
+    if (rc) return rc;
+  }
+  if (!plan.split) return FAT_OK;
+  if (plan.tile) {
+    rc = d == 64 ? launch_merge<kTileRows, 64>(p, paged_tile_ctas(), s)
+                 : launch_merge<kTileRows, 128>(p, paged_tile_ctas(), s);
+    if (rc) return rc;
+  }
+  if (plan.few)
+    rc = d == 64 ? launch_merge<kFewRows, 64>(pf, paged_few_ctas(), s)
+                 : launch_merge<kFewRows, 128>(pf, paged_few_ctas(), s);
+  return rc;
 }
 
 }  // extern "C"

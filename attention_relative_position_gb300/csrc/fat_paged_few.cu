@@ -171,7 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     r->valid = 0;
   }
   const Share sh = share_find<kThreads>(p, kMinShare, FewCost<D>{p}, share_s);
-  if (sh.lo >= sh.hi) return;
+  if (sh.lo >= sh.hi) {
+    grid_dep_wait();
+    return;
+  }
   const Watchdog wd{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
   const PagedDoc d0 = share_doc(p, share_s, sh.doc, sh.doc);
   const int cost0 = max(1, (d0.lk + KT - 1) / KT);
@@ -550,10 +553,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (; done < issued; ++done) {
     mbar_wait_teardown(full + done % kRing, (done / kRing) & 1, kTeardownNs);
   }
+  // A grid that was started beside the tile kernel's ends after it, so that the merge grids, which
+  // wait for this one, find both complete (returns at once when there is none before).
+  grid_dep_wait();
 }
 
 template <int D>
-int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
+int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream, bool overlap) {
   PagedParams pp = p;
   CUtensorMap mk, mv;
   int rc = make_tmap_pages(&mk, c.k, c, 16, &pp.head_outer);
@@ -561,8 +567,17 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
   if (rc) return rc;
   const size_t smem = FewCfg<D>::bytes(p.bias) + 1024;
   if (prepare_kernel((const void *)fat_paged_few_kernel<D>, smem, kThreads, 0)) return FAT_ECUDA;
-  fat_paged_few_kernel<D><<<paged_few_ctas(), kThreads, smem, stream>>>(mk, mv, pp);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)paged_few_ctas());
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fat_paged_few_kernel<D>, mk, mv, pp);
   if (e == cudaSuccess) return FAT_OK;
   set_last_error("paged few-row kernel launch", (int)e, cudaGetErrorString(e));
   return FAT_ECUDA;
@@ -572,8 +587,10 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
 
 int paged_few_ctas() { return sm_count() > 0 ? sm_count() : 152; }
 
-int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
-  return c.head_dim == 64 ? launch_t<64>(p, c, stream) : launch_t<128>(p, c, stream);
+int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream,
+                     bool overlap_previous) {
+  return c.head_dim == 64 ? launch_t<64>(p, c, stream, overlap_previous)
+                          : launch_t<128>(p, c, stream, overlap_previous);
 }
 
 }  // namespace fat

@@ -1,0 +1,768 @@
+// fat_paged_tile.cu -- attention over a paged cache for requests with more rows than the few-row
+// kernel takes: chunks of a prompt, drafted tokens of large groups.
+//
+// Rows are packed: the group's heads of a query lie side by side (row = token * group + head), so
+// every key/value tile is read once for all heads of its group, and a chunk of a few tokens fills a
+// tile. An item is (request, key/value head, up to two tiles of floor(128 / group) tokens); one
+// persistent CTA per SM takes an equal share of all key tiles (fat_paged.cuh) and walks its items:
+//   warps 0-7   two softmax warpgroups, one row per thread (a TMEM lane): logits, bias, mask, running
+//               maximum (moved only when it grows by more than 2^32), P as bf16 into tensor memory;
+//   warp 8      producer: Q by one TMA box per 64 channels ([tokens][group heads]), K and V tiles of
+//               128 tokens page by page (a lane per page, its number fetched a tile ahead);
+//   warps 9-10  MMA issuers, one per softmax warpgroup: S = Q K^T, O += P V (tcgen05, TMEM);
+//   warp 11     values behind a request's last key are zeroed in its last tile (a page may hold
+//               anything there, and 0 * NaN is NaN).
+// An item of two tiles gives each warpgroup its own rows, both over every key tile (the copies are
+// shared, one warpgroup's softmax overlaps the other's products). An item of one tile gives both the
+// same rows and every other key tile each, and adds the two results at the end through tensor
+// memory: a short chunk over a long context keeps both busy as well.
+// Key tiles go from the last one backwards: the first holds each row's largest linear bias, so the
+// maximum rarely moves afterwards.
+#include <algorithm>
+#include <cstdint>
+#include <cstdio>
+
+#include "fat_paged.cuh"
+
+namespace fat {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kWarpProd = 8, kWarpMma = 9, kWarpTail = 11;
+constexpr int kMinShare = 4;  // cost units (a key tile of one Q tile) a CTA takes at least
+
+template <int D>
+struct TileCfg {
+  static constexpr int DB = D / 64;
+  static constexpr int BLK = 128 * 128;    // 128 rows x 64 bf16
+  static constexpr int TILE = DB * BLK;
+  static constexpr int NS = D == 64 ? 4 : 2;  // K and V stages (a power of two)
+  static constexpr int NS_LOG2 = D == 64 ? 2 : 1;
+  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_V = OFF_K + NS * TILE;
+  static constexpr int OFF_BAR = OFF_V + NS * TILE;
+  static constexpr int OFF_STATS = OFF_BAR + 512;            // float2 [128]
+  static constexpr int OFF_SHARE = OFF_STATS + 1024;
+  static constexpr int OFF_THR = OFF_SHARE + (int)sizeof(ShareSmem<kThreads>);
+  static constexpr int OFF_LUT = OFF_THR + kMaxThresholds * 4;
+  static_assert((2 + 4 * NS + 15) * 8 + 64 <= 512, "barrier block");
+  static_assert(OFF_LUT + kMaxBiasSpan + 512 + 1024 <= kSmemLimit, "shared memory");
+  static constexpr int REG_SM = 216, REG_OTHER = 72;
+  static constexpr int REGS_NEEDED = 256 * REG_SM + 128 * REG_OTHER;
+  static_assert(REGS_NEEDED <= kThreads * ((65536 / kThreads) & ~7), "register split");
+  // TMEM columns: S_t at 128 t, O_t behind them; d 64: P_t has columns of its own, so that the next
+  // S_t is computed while P_t is still read; d 128: P_t overwrites S_t.
+  static constexpr bool SEP_P = D == 64;
+  static constexpr uint32_t COL_O = 256, O_STRIDE = SEP_P ? 64 : 128;
+  static constexpr uint32_t COL_P = COL_O + 2 * O_STRIDE;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static_assert(COL_P + (SEP_P ? 128 : 0) <= TMEM_COLS, "TMEM column budget");
+  static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, 0, 0);
+  static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
+};
+
+// One block of queries of a request: tokens [q0, q0 + ntok), one or two tiles, the key tiles that
+// its rows see, its cost in (Q tile, key tile) pairs.
+struct TileBlock {
+  int q0, ntok, nkv, tiles, cost;
+};
+__device__ __forceinline__ TileBlock tile_block(const PagedDoc &d, int b, int tq, int causal) {
+  TileBlock t;
+  t.q0 = b * 2 * tq;
+  t.ntok = min(d.lq - t.q0, 2 * tq);
+  t.tiles = t.ntok > tq ? 2 : 1;
+  t.nkv = (d.lk + 127) >> 7;
+  if (causal) {
+    const int last = d.lk - d.lq + t.q0 + t.ntok - 1;  // key position of the last row
+    t.nkv = last < 0 ? 0 : min(t.nkv, (last >> 7) + 1);
+  }
+  t.cost = max(1, t.tiles * t.nkv);
+  return t;
+}
+__device__ __forceinline__ long long tile_head_cost(const PagedDoc &d, int tq, int causal) {
+  long long c = 0;
+  for (int b = 0; b * 2 * tq < d.lq; ++b) c += tile_block(d, b, tq, causal).cost;
+  return c;
+}
+struct TileCost {
+  const PagedParams &p;
+  int tq;
+  __device__ long long operator()(const PagedDoc &d) const {
+    return (long long)d.lq * p.group <= p.few_rows ? 0 : p.hkv * tile_head_cost(d, tq, p.causal);
+  }
+};
+
+struct TileItem {
+  int doc, hk, row0;      // row0: token of q and out
+  int q0, ntok, tiles;    // tokens of the request, tiles
+  int lk, shift;          // shift: key position of the request's first query
+  int j0, j1;             // key tiles taken here: key tile nkv - 1 - j for j in [j0, j1)
+  int nkv;
+  bool begins, ends;
+};
+struct TileWalk {
+  const PagedParams &p;
+  const ShareSmem<kThreads> &sm;
+  int tq, first_doc, doc, hk, b;
+  long long left;
+  int off;
+  __device__ TileWalk(const PagedParams &pp, const ShareSmem<kThreads> &s, int tq_, const Share &sh)
+      : p(pp), sm(s), tq(tq_), first_doc(sh.doc), doc(sh.doc), b(0), left(sh.hi - sh.lo) {
+    const PagedDoc d = share_doc(p, sm, doc, doc);
+    const long long per = tile_head_cost(d, tq, p.causal);
+    hk = (int)(sh.off / per);
+    long long rest = sh.off - hk * per;
+    for (int c; rest >= (c = tile_block(d, b, tq, p.causal).cost); rest -= c) ++b;
+    off = (int)rest;
+  }
+  __device__ bool next(TileItem &it) {
+    while (left > 0 && doc < p.n) {
+      const PagedDoc d = share_doc(p, sm, first_doc, doc);
+      if (!d.ok || (long long)d.lq * p.group <= p.few_rows) {
+        ++doc;
+        hk = b = 0;
+        continue;
+      }
+      const TileBlock t = tile_block(d, b, tq, p.causal);
+      const int o = off;
+      off = 0;
+      const int take = (int)min(left, (long long)(t.cost - o));
+      left -= take;
+      it.doc = doc;
+      it.hk = hk;
+      it.row0 = d.sq + t.q0;
+      it.q0 = t.q0;
+      it.ntok = t.ntok;
+      it.tiles = t.tiles;
+      it.lk = d.lk;
+      it.shift = d.lk - d.lq;
+      it.nkv = t.nkv;
+      ++b;
+      if (b * 2 * tq >= d.lq) {
+        b = 0;
+        if (++hk == p.hkv) {
+          hk = 0;
+          ++doc;
+        }
+      }
+      if (!p.split) {  // whole items: the one that begins earlier is another CTA's
+        if (o > 0) continue;
+        it.j0 = 0;
+        it.j1 = t.nkv;
+        it.begins = it.ends = true;
+        return true;
+      }
+      it.j0 = min((o + t.tiles - 1) / t.tiles, t.nkv);
+      it.j1 = min((o + take + t.tiles - 1) / t.tiles, t.nkv);
+      if (t.nkv > 0 && it.j0 == it.j1) continue;  // the boundary lies inside a pair of tiles
+      it.begins = it.j0 == 0;
+      it.ends = it.j1 == t.nkv;
+      return true;
+    }
+    return false;
+  }
+  // key tiles of `it` that Q tile t multiplies: first, step (both tiles every one, or alternating)
+  static __device__ int first(const TileItem &it, int t) { return it.tiles == 2 ? 0 : t; }
+  static __device__ int step(const TileItem &it) { return it.tiles == 2 ? 1 : 2; }
+  static __device__ int count(const TileItem &it, int t) {
+    const int n = it.j1 - it.j0;
+    return it.tiles == 2 ? n : (n + 1 - t) >> 1;
+  }
+};
+
+// The S row from tensor memory as logits x (log2 units, relative to the row's reference maximum when
+// FOLD), masked; returns the row's maximum.
+//   MODE 0: bias = rowc;  1: rowc + kk * j;  2: table[lut[j]] - slope |delta0 + j| - mref
+template <int MODE, bool MASK>
+__device__ __forceinline__ float tile_logits(uint32_t tS, uint32_t (&x)[4][32], float scale_log2,
+                                             float rowc, float kk, const uint8_t *lut,
+                                             const float *tab, int tab_stride, float slope,
+                                             int delta0, int lim) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32_issue(tS + c * 32, x[c]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32_fence(x[c]);
+  const uint64_t sl2 = f2_pack(scale_log2, scale_log2);
+  const uint64_t rc2 = f2_pack(rowc, rowc);
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const int j = c * 32 + i;
+      uint64_t b2;
+      if (MODE == 0) {
+        b2 = rc2;
+      } else if (MODE == 1) {
+        b2 = f2_pack(fmaf(kk, (float)j, rowc), fmaf(kk, (float)(j + 1), rowc));
+      } else {
+        float b[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          b[e] = fmaf(-slope, fabsf((float)(delta0 + j + e)), rowc);
+          if (tab != nullptr) b[e] = fmaf(__ldg(tab + lut[j + e] * tab_stride), kLog2e, b[e]);
+        }
+        b2 = f2_pack(b[0], b[1]);
+      }
+      float v0, v1;
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), sl2, b2),
+                v0, v1);
+      if (MASK) {
+        v0 = (j < lim) ? v0 : -INFINITY;
+        v1 = (j + 1 < lim) ? v1 : -INFINITY;
+      }
+      x[c][i] = __float_as_uint(v0);
+      x[c][i + 1] = __float_as_uint(v1);
+      mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], v0, v1);
+    }
+  }
+  return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    fat_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ PagedParams p) {
+  using C = TileCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.group, tq = 128 / G, RT = tq * G;  // tokens and rows of a tile
+  uint8_t *sQ = sm, *sK = sm + C::OFF_K, *sV = sm + C::OFF_V;
+  auto &share_s = *reinterpret_cast<ShareSmem<kThreads> *>(sm + C::OFF_SHARE);
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
+  uint64_t *q_empty = q_full + 1;
+  uint64_t *k_full = q_empty + 1;
+  uint64_t *v_full = k_full + C::NS;
+  uint64_t *k_empty = v_full + C::NS;
+  uint64_t *v_empty = k_empty + C::NS;
+  uint64_t *s_full = v_empty + C::NS;  // [2] each
+  uint64_t *p_ready = s_full + 2;
+  uint64_t *o_ready = p_ready + 2;
+  uint64_t *s_free = o_ready + 2;
+  uint64_t *o_free = s_free + 2;
+  uint64_t *mma_done = o_free + 2;
+  uint64_t *merge_ready = mma_done + 2;
+  uint64_t *tail = merge_ready + 1;  // a last tile's values have arrived (before they are zeroed)
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  Watchdog *wdp = reinterpret_cast<Watchdog *>(sm + C::OFF_BAR + 448);
+  int *thr_s = reinterpret_cast<int *>(sm + C::OFF_THR);
+  uint8_t *lut = sm + C::OFF_LUT;
+  grid_dep_launch();
+  if (p.split && tid < 2) part_record(p.part, blockIdx.x, tid)->valid = 0;
+  for (int i = tid; i < p.bias.n_thr; i += kThreads) thr_s[i] = p.bias.thr[i];
+  const Share share = share_find<kThreads>(p, kMinShare, TileCost{p, tq}, share_s);
+  if (share.lo >= share.hi) return;
+
+  if (warp == kWarpProd && lane == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(k_full + s, 1);
+      mbar_init(v_full + s, 1);
+      mbar_init(k_empty + s, 2);  // two commits: one per issuer, or both by the one that used it
+      mbar_init(v_empty + s, 2);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full + t, 1);
+      mbar_init(p_ready + t, 128);
+      mbar_init(o_ready + t, 1);
+      mbar_init(s_free + t, 128);
+      mbar_init(o_free + t, 128);
+      mbar_init(mma_done + t, 1);
+    }
+    mbar_init(merge_ready, 128);
+    mbar_init(tail, 1);
+    *abort_flag = 0;
+    *wdp = Watchdog{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  // rows of the Q tiles that no token fills (group does not divide 128): zeros, never overwritten
+  for (int i = tid; i < 2 * C::DB * (128 - RT) * 8; i += kThreads) {
+    const int blk = i / ((128 - RT) * 8), rest = i % ((128 - RT) * 8);
+    *reinterpret_cast<uint4 *>(sQ + blk * C::BLK + RT * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  if (p.bias.table != nullptr)
+    for (int i = tid; i < p.bias.lut_len; i += kThreads)
+      lut[i] = (uint8_t)t5_bucket_staged(p.bias.lut_lo + i, p.bias, thr_s);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Watchdog &wd = *wdp;
+  if (warp >= kWarpProd) regs_dec<C::REG_OTHER>();
+
+  if (warp == kWarpProd) {
+    // ------------------------------------------------------------------ producer
+    const int kbox = min(128, 1 << p.log2_page), pieces = 128 / kbox;
+    TileWalk walk(p, share_s, tq, share);
+    TileItem it;
+    uint32_t J = 0;      // K/V stream position
+    int ni = 0;          // items with keys
+    uint32_t last_tail = 0;
+    bool any_tail = false, ok = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
+    while (ok && walk.next(it)) {
+      const int n = it.j1 - it.j0;
+      if (n == 0) continue;
+      // this lane's page of key tile kt (the next one's is fetched while this one's copies go out)
+      auto fetch = [&](int kt) -> int {
+        const int tok = kt * 128 + lane * kbox;
+        return (lane < pieces && tok < it.lk)
+                   ? __ldg(p.table + (size_t)it.doc * p.width + (tok >> p.log2_page))
+                   : 0;
+      };
+      int kt = it.nkv - 1 - it.j0;
+      int page = fetch(kt);
+      if (ni > 0) ok = warp_wait(q_empty, (ni - 1) & 1, wd);
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)RT * 128 * C::DB * it.tiles;
+        mbar_arrive_expect_tx(q_full, bytes);
+        for (int t = 0; t < it.tiles; ++t)
+          for (int b = 0; b < C::DB; ++b)
+            tma_load_3d(&tm_q, q_full, sQ + t * C::TILE + b * C::BLK, 64 * b, it.hk * G,
+                        it.row0 + t * tq);
+      }
+      ++ni;
+      for (int jj = 0; jj < n; ++jj, --kt, ++J) {
+        const int s = J & (C::NS - 1);
+        const uint32_t u = J >> C::NS_LOG2;
+        const int tok = kt * 128 + lane * kbox;
+        const int nvalid = min(pieces, (it.lk - kt * 128 + kbox - 1) / kbox);
+        const bool issue = lane < nvalid;
+        if (issue && (unsigned)page >= (unsigned)p.num_pages) {
+          atomicOr(p.err, FAT_DEVERR_PAGES);
+          page = p.num_pages;  // just outside: filled with zeros
+        }
+        const int in = tok & ((1 << p.log2_page) - 1);
+        const int c1 = p.head_outer ? in : it.hk, c2 = p.head_outer ? it.hk : in;
+        const int cur = page;
+        if (jj + 1 < n) page = fetch(kt - 1);
+        const uint32_t bytes = (uint32_t)nvalid * kbox * 128 * C::DB;
+        if (u > 0 && !(ok = warp_wait(k_empty + s, (u - 1) & 1, wd))) break;
+        if (lane == 0) mbar_arrive_expect_tx(k_full + s, bytes);
+        __syncwarp();
+        if (issue)
+          for (int b = 0; b < C::DB; ++b)
+            tma_load_4d(&tm_k, k_full + s, sK + s * C::TILE + b * C::BLK + lane * kbox * 128, 64 * b,
+                        c1, c2, cur);
+        if (u > 0 && !(ok = warp_wait(v_empty + s, (u - 1) & 1, wd))) break;
+        // a request's last tile: its values complete on `tail`, and warp 11 arrives on v_full
+        uint64_t *vbar = v_full + s;
+        if (kt * 128 + 128 > it.lk) {
+          if (any_tail && J - last_tail < (uint32_t)C::NS) {  // the one before has been passed on
+            const uint32_t sl = last_tail & (C::NS - 1), ul = last_tail >> C::NS_LOG2;
+            if (!(ok = warp_wait(v_full + sl, ul & 1, wd))) break;
+          }
+          any_tail = true;
+          last_tail = J;
+          vbar = tail;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
+        __syncwarp();
+        if (issue)
+          for (int b = 0; b < C::DB; ++b)
+            tma_load_4d(&tm_v, vbar, sV + s * C::TILE + b * C::BLK + lane * kbox * 128, 64 * b, c1,
+                        c2, cur);
+      }
+      if (!ok) break;
+    }
+    // After a wait ran out, copies may still be on their way: give them time to land before the
+    // block exits (a stage's barrier alone does not tell which of its phases they belong to).
+    if (*abort_flag) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    // ------------------------------------------------------------------ MMA issuers
+    const int t = warp - kWarpMma;
+    if (lane == 0) {
+      const uint32_t dS = tmem + 128 * t, dO = tmem + C::COL_O + C::O_STRIDE * t;
+      const uint32_t aP = C::SEP_P ? tmem + C::COL_P + 64 * t : dS;
+      const uint64_t dKd = sw128_desc(smem_u32(sK), 16, 1024);
+      const uint64_t dVd = sw128_desc(smem_u32(sV), C::BLK, 1024);
+      TileWalk walk(p, share_s, tq, share);
+      TileItem it;
+      uint32_t J = 0, g = 0;  // stream position, this tile's steps
+      int ni = 0, act = 0;    // items with keys, those in which this tile has steps
+      bool ok = true;
+      while (ok && walk.next(it)) {
+        const int n = it.j1 - it.j0;
+        if (n == 0) continue;
+        const int first = TileWalk::first(it, t), step = TileWalk::step(it);
+        if (first >= n) {  // one key tile: the other issuer's
+          J += n;
+          ++ni;
+          continue;
+        }
+        const uint64_t dQd = sw128_desc(smem_u32(sQ) + (it.tiles == 2 ? t * C::TILE : 0), 16, 1024);
+        const bool alone = it.tiles == 1;            // the stages are this tile's alone
+        const bool only = alone && n == 1;           // and so is Q
+        auto issue_S = [&](int jj) {
+          const uint64_t kd = dKd + ((((J + jj) & (C::NS - 1)) * C::TILE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4;
+            mma_bf16_ss(dS, dQd + off, kd + off, C::IDESC_S, kk > 0);
+          }
+          mma_commit(s_full + t);
+          uint64_t *ke = k_empty + ((J + jj) & (C::NS - 1));
+          mma_commit(ke);
+          if (alone) mma_commit(ke);
+          if (jj + step >= n) {  // the item's last S of this tile
+            mma_commit(q_empty);
+            if (only) mma_commit(q_empty);
+          }
+        };
+        auto k_wait = [&](int jj) {
+          return mbar_wait(k_full + ((J + jj) & (C::NS - 1)), ((J + jj) >> C::NS_LOG2) & 1, wd);
+        };
+        ok = mbar_wait(q_full, ni & 1, wd) && k_wait(first);
+        if (!ok) break;
+        tc_fence_after();
+        issue_S(first);
+        for (int jj = first; jj < n; jj += step, ++g) {
+          const uint32_t jp = J + jj;
+          const int s = jp & (C::NS - 1);
+          if (C::SEP_P) {  // the next S as soon as this one has been read
+            if (!(ok = mbar_wait(s_free + t, g & 1, wd))) break;
+            if (jj + step < n) {
+              if (!(ok = k_wait(jj + step))) break;
+              tc_fence_after();
+              issue_S(jj + step);
+            }
+          }
+          if (!(ok = mbar_wait(v_full + s, (jp >> C::NS_LOG2) & 1, wd) &&
+                     mbar_wait(p_ready + t, g & 1, wd)))
+            break;
+          // the first P V overwrites O: the previous item's rows have been read
+          if (jj == first && act > 0 && !(ok = mbar_wait(o_free + t, (act - 1) & 1, wd))) break;
+          tc_fence_after();
+          const uint64_t vd = dVd + ((s * C::TILE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(dO, aP + kk * 8, vd + ((kk * 2048) >> 4), C::IDESC_PV,
+                        (jj > first || kk > 0) ? 1u : 0u);
+          mma_commit(o_ready + t);
+          mma_commit(v_empty + s);
+          if (alone) mma_commit(v_empty + s);
+          if (!C::SEP_P && jj + step < n) {
+            if (!(ok = k_wait(jj + step))) break;
+            tc_fence_after();
+            issue_S(jj + step);
+          }
+        }
+        J += n;
+        ++ni;
+        ++act;
+      }
+      mma_commit(mma_done + t);
+      mbar_wait_teardown(mma_done + t, 0, kTeardownNs);
+    }
+  } else if (warp == kWarpTail) {
+    // ------------------------------------------------------------------ values behind the last key
+    TileWalk walk(p, share_s, tq, share);
+    TileItem it;
+    uint32_t J = 0;
+    int nt = 0;
+    while (walk.next(it)) {
+      const int n = it.j1 - it.j0;
+      if (n == 0) continue;
+      const int kt = it.nkv - 1 - it.j0;
+      if (kt * 128 + 128 > it.lk) {  // only an item's first position can be the last tile
+        if (!warp_wait(tail, nt & 1, wd)) break;
+        ++nt;
+        const int s = J & (C::NS - 1), row = it.lk - kt * 128;
+        for (int b = 0; b < C::DB; ++b)
+          for (int i = row * 8 + lane; i < 128 * 8; i += 32)
+            *reinterpret_cast<uint4 *>(sV + s * C::TILE + b * C::BLK + i * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full + s);
+      }
+      J += n;
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax warpgroups
+    regs_inc<C::REG_SM>();
+    constexpr bool FOLD = !C::SEP_P;
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + 128 * t;
+    const uint32_t tO = tmem + lane_off + C::COL_O + C::O_STRIDE * t;
+    const uint32_t tP = C::SEP_P ? tmem + lane_off + C::COL_P + 64 * t : tS;
+    float2 *stats = reinterpret_cast<float2 *>(sm + C::OFF_STATS);
+    const int rq = r / G, rg = r - rq * G;  // token and head of this row within the tile
+    const bool has_slopes = p.bias.slopes != nullptr, has_table = p.bias.table != nullptr;
+    TileWalk walk(p, share_s, tq, share);
+    TileItem it;
+    uint32_t g = 0, g_other = 0;  // steps of this tile and of the other one
+    int merges = 0;
+    bool ok = true;
+    while (walk.next(it)) {
+      const int t_row = it.tiles == 2 ? t : 0;           // which tile's rows
+      const int ntok = min(it.ntok - t_row * tq, tq);    // its tokens
+      const bool valid = rq < ntok && r < RT;
+      const int h = it.hk * G + rg;
+      const int row = it.row0 + t_row * tq + rq;
+      const bool whole = it.begins && it.ends;
+      const int which = it.begins ? 1 : 0;
+      if (!whole && r == 0 && t == 0) {
+        PartRecord *rec = part_record(p.part, blockIdx.x, which);
+        rec->valid = 1;
+        rec->ends = it.ends;
+        rec->row0 = it.row0;
+        rec->hk = it.hk;
+        rec->rows = it.ntok * G;
+      }
+      const int steps = TileWalk::count(it, t), steps_other = TileWalk::count(it, 1 - t);
+      if (it.nkv == 0) {  // no key for any row
+        if (valid && (it.tiles == 2 || t == 0)) {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)row * p.hq + h) * D);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse != nullptr) p.lse[(size_t)h * p.total_q + row] = -INFINITY;
+        }
+        continue;
+      }
+      // positions: of the tile's first and last row, and of this one (a row without a token: as
+      // the last one's)
+      const int pos_lo = it.shift + it.q0 + t_row * tq, pos_hi = pos_lo + ntok - 1;
+      const int qpos = min(pos_lo + rq, pos_hi);
+      const float slope = has_slopes ? __ldg(p.bias.slopes + h) * kLog2e : 0.f;
+      const float *tab = has_table ? p.bias.table + h : nullptr;
+      float c_pos = 0.f, c_neg = 0.f;
+      if (has_table) {
+        c_pos = __ldg(tab + lut[p.bias.sat_pos - p.bias.lut_lo] * p.hq) * kLog2e;
+        c_neg = __ldg(tab + lut[-p.bias.sat_neg - p.bias.lut_lo] * p.hq) * kLog2e;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < steps; ++i) {
+        const uint32_t gi = g + i;
+        if (ok) ok = warp_wait(s_full + t, gi & 1, wd);
+        if (!ok) break;
+        tc_fence_after();
+        const int jj = TileWalk::first(it, t) + i * TileWalk::step(it);
+        const int ks = 128 * (it.nkv - 1 - it.j0 - jj);
+        const bool need_mask = ks + 128 > it.lk || (p.causal && ks + 127 > pos_lo);
+        const int lim = min(it.lk - ks, p.causal ? qpos - ks + 1 : 128);
+        const float m_ref = (FOLD && m != -INFINITY) ? m : 0.f;
+        int mode = 0;
+        float rowc = 0.f, kk = 0.f;
+        if (p.bias.has_bias) {
+          if (ks - pos_hi >= p.bias.sat_pos) {
+            kk = -slope;
+            rowc = fmaf(kk, (float)(ks - qpos), c_pos);
+            mode = has_slopes ? 1 : 0;
+          } else if (ks + 127 - pos_lo <= -p.bias.sat_neg) {
+            kk = slope;
+            rowc = fmaf(kk, (float)(ks - qpos), c_neg);
+            mode = has_slopes ? 1 : 0;
+          } else {
+            mode = 2;
+          }
+        }
+        rowc -= m_ref;
+        uint32_t x[4][32];
+        float mx;
+#define FAT_TILE_LOGITS(MODE, MASK)                                                             \
+  tile_logits<MODE, MASK>(tS, x, p.scale_log2, rowc, kk, lut + (ks - qpos - p.bias.lut_lo), tab, \
+                          p.hq, slope, ks - qpos, lim)
+        if (mode == 0)
+          mx = need_mask ? FAT_TILE_LOGITS(0, true) : FAT_TILE_LOGITS(0, false);
+        else if (mode == 1)
+          mx = need_mask ? FAT_TILE_LOGITS(1, true) : FAT_TILE_LOGITS(1, false);
+        else
+          mx = FAT_TILE_LOGITS(2, true);
+#undef FAT_TILE_LOGITS
+        if (C::SEP_P) {  // S is in registers: the next one may be computed
+          tc_fence_before();
+          mbar_arrive(s_free + t);
+        }
+        float sub = 0.f;  // what the exponentials still subtract (FOLD)
+        if (i == 0) {
+          m = mx;
+          sub = mx == -INFINITY ? 0.f : mx;
+        } else {
+          const bool fresh = m == -INFINITY;  // no key of this row so far
+          const bool need = fresh ? mx != -INFINITY : mx > (FOLD ? 0.f : m) + 32.0f;
+          if (C::SEP_P) {  // P and O are still read by the previous P V
+            ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (__any_sync(0xffffffffu, need)) {
+            if (!C::SEP_P) {
+              ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const float f = need ? (fresh ? 0.f : ex2(FOLD ? -mx : m - mx)) : 1.0f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32(tO + c * 32, o);
+            }
+            if (need) {
+              l *= f;
+              m = (fresh || !FOLD) ? mx : m + mx;
+              sub = mx;
+            }
+          }
+        }
+        uint64_t sum2[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum2[k] = f2_pack(0.f, 0.f);
+        if (!FOLD) {
+          const float m_use = m == -INFINITY ? 0.f : m;
+          fwd_exp_pass<true>(x, f2_pack(m_use, m_use), tP, sum2);
+        } else if (__any_sync(0xffffffffu, sub != 0.f)) {
+          fwd_exp_pass<true>(x, f2_pack(sub, sub), tP, sum2);
+        } else {
+          fwd_exp_pass<false>(x, 0, tP, sum2);
+        }
+        {
+          float s0, s1, s2, s3;
+          f2_unpack(f2_add(sum2[0], sum2[2]), s0, s1);
+          f2_unpack(f2_add(sum2[1], sum2[3]), s2, s3);
+          l += (s0 + s1) + (s2 + s3);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_ready + t);
+      }
+      // ---- the item's rows
+      g += steps;
+      g_other += steps_other;
+      if (steps == 0) continue;  // one key tile: the other warpgroup's
+      if (ok) ok = warp_wait(o_ready + t, (g - 1) & 1, wd);
+      const bool pair = it.tiles == 1 && it.j1 - it.j0 > 1;  // both warpgroups hold these rows
+      if (pair && t == 1) {
+        if (ok) {
+          stats[r] = make_float2(m, l);
+          mbar_arrive(merge_ready);
+        }
+        continue;
+      }
+      float f0 = 1.f, f1 = 0.f;
+      if (pair) {
+        if (ok) ok = warp_wait(merge_ready, merges & 1, wd) &&
+                     warp_wait(o_ready + 1, (g_other - 1) & 1, wd);
+        ++merges;
+        if (ok) {
+          const float2 st = stats[r];
+          const float M = fmaxf(m, st.x);
+          f0 = m == -INFINITY ? 0.f : ex2(m - M);
+          f1 = st.x == -INFINITY ? 0.f : ex2(st.x - M);
+          l = l * f0 + st.y * f1;
+          m = M;
+        }
+      }
+      if (!ok) continue;  // nothing more is waited for: the walk ends quickly
+      tc_fence_after();
+      const float inv = whole ? (l > 0.f ? 1.0f / l : 0.f) : 1.f;
+      f0 *= inv;
+      f1 *= inv;
+      const int prow = t_row * RT + r;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32(tO + c * 32, o);
+        if (pair) {
+          uint32_t o1[32];
+          tmem_ld32(tO + C::O_STRIDE + c * 32, o1);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f0);
+        }
+        if (valid && whole) {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)row * p.hq + h) * D + c * 32);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * k]),
+                                 __uint_as_float(o[8 * v + 2 * k + 1]));
+            dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (valid) {
+          float4 *dst = reinterpret_cast<float4 *>(
+              part_rows<kTileRows, D>(p.part, gridDim.x, blockIdx.x, which) + prow * D + c * 32);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            dst[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                 __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      mbar_arrive(o_free + t);
+      if (pair) mbar_arrive(o_free + 1);
+      if (valid) {
+        if (!whole)
+          *reinterpret_cast<float2 *>(
+              part_stats<kTileRows, D>(p.part, gridDim.x, blockIdx.x, which) + prow * 2) =
+              make_float2(m, l);
+        else if (p.lse != nullptr)
+          p.lse[(size_t)h * p.total_q + row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int D>
+int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
+  using C = TileCfg<D>;
+  PagedParams pp = p;
+  CUtensorMap mq, mk, mv;
+  const int kbox = std::min(128, 1 << p.log2_page);
+  int rc = make_tmap_pages(&mk, c.k, c, kbox, &pp.head_outer);
+  if (!rc) rc = make_tmap_pages(&mv, c.v, c, kbox, &pp.head_outer);
+  if (rc) return rc;
+  if (make_tmap_rows(&mq, p.q, p.total_q, p.hq, D, p.group, 128 / p.group)) return FAT_ECUDA;
+  const size_t smem = 1024 + C::OFF_LUT + (p.bias.table ? (size_t)((p.bias.lut_len + 15) & ~15) : 0);
+  if (prepare_kernel((const void *)fat_paged_tile_kernel<D>, smem, kThreads, C::REGS_NEEDED))
+    return FAT_ECUDA;
+  fat_paged_tile_kernel<D><<<paged_tile_ctas(), kThreads, smem, stream>>>(mq, mk, mv, pp);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return FAT_OK;
+  set_last_error("paged tile kernel launch", (int)e, cudaGetErrorString(e));
+  return FAT_ECUDA;
+}
+
+}  // namespace
+
+int paged_tile_ctas() { return sm_count() > 0 ? sm_count() : 152; }
+
+int launch_paged_tile(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
+  return c.head_dim == 64 ? launch_t<64>(p, c, stream) : launch_t<128>(p, c, stream);
+}
+
+}  // namespace fat

@@ -515,6 +515,21 @@ def test_attention_on_streams_and_from_graphs():
             x.check(out, lse)
 
 
+@pytest.mark.parametrize("name", ["decode_gqa16", "chunk_group5_d128", "mixed"])
+def test_attention_watchdog(name):
+    """No copies are issued: the waits run out, the status says so, and the next call is right."""
+    p = Problem(seed=33, **CASES[name])
+    try:
+        fa.fat_attn_debug_set_watchdog(50_000_000, 1)
+        p.run()
+        assert _errors() == fa.FAT_DEVERR_TIMEOUT_FWD
+    finally:
+        fa.fat_attn_debug_set_watchdog(0, 0)
+    out, lse = p.run()
+    assert _errors() == 0
+    p.check(out, lse)
+
+
 def test_arguments_are_checked():
     p = Problem(seed=9, **CASES["decode_gqa16"])
     args = [p.q, p.kc, p.vc, _i32(p.table), _i32(p.cu), _i32(p.lk), 1, 4000]
@@ -536,6 +551,8 @@ def test_arguments_are_checked():
     refused(ValueError, 5, _i32(p.lk).cpu())
     with pytest.raises(ValueError):
         p.run(out=torch.empty_like(p.q)[:, :-1])
+    with pytest.raises(fa.FatAttnError):
+        p.run(workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
     k = _bf16(np.random.default_rng(1), 3, 2, 128)
     with pytest.raises(ValueError):
         fa.fat_paged_append(k, k, p.kc, p.vc, _i32([1, 2]))
