@@ -178,11 +178,12 @@ __global__ void __launch_bounds__(kPlanThreads) fat_paged_plan_kernel(const Plan
 }
 
 // ---- rows ---------------------------------------------------------------------------------------
-// Memory bound: every row is read and written once. A block takes `tok_per_block` tokens: their
-// cosines and sines are computed once into shared memory (all heads of a token share them), then
-// its threads walk (token, head, unit) with 16-byte accesses, kRowBatch units in flight per thread.
-// A unit is one 16-byte chunk (pairs 2i, 2i + 1 lie inside it), or with the halves layout two
-// chunks, i and i + rotary_dim / 2, that turn together; what is not rotated goes chunk by chunk.
+// Memory bound: every row is read and written once. A thread takes one (token, unit) position,
+// computes its cosines and sines once and turns that unit of a run of heads (all heads share them),
+// kRowBatch heads' loads in flight together. A unit is one 16-byte chunk (pairs 2i, 2i + 1 lie inside
+// it), or with the halves layout two chunks, i and i + rotary_dim / 2, that turn together; what is
+// not rotated goes chunk by chunk. Few tokens: the heads are split over more threads (kRowThreads
+// and the run length are launch_rows' choice), since a decode step's rows are bound by latency.
 // Angles as in fat_rope_apply: position * rate mod one turn in 64-bit integers, exact at any
 // position, its top 24 bits through sincospif.
 constexpr int kRowThreads = 256;
@@ -198,7 +199,7 @@ struct RowSeg {
 };
 struct RowParams {
   RowSeg seg[3];
-  int nseg, tokens, units, pair_units, half_chunks, tok_per_block, all_heads;
+  int nseg, tokens, units, pair_units, half_chunks, all_heads, run;  // run: heads per thread
   int log2_page;
   long long page_stride, num_slots;
   float sign;
@@ -207,7 +208,7 @@ struct RowParams {
   fat_rope_t rope;
 };
 
-__device__ __forceinline__ uint4 rotate_pairs(uint4 v, const float2 *cs) {
+__device__ __forceinline__ uint4 rotate_pairs(uint4 v, const float2 (&cs)[8]) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -216,7 +217,7 @@ __device__ __forceinline__ uint4 rotate_pairs(uint4 v, const float2 *cs) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void rotate_halves(uint4 &u, uint4 &v, const float2 *cs) {
+__device__ __forceinline__ void rotate_halves(uint4 &u, uint4 &v, const float2 (&cs)[8]) {
   uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -232,75 +233,73 @@ __device__ __forceinline__ void rotate_halves(uint4 &u, uint4 &v, const float2 *
 
 template <bool PAIRS>
 __global__ void __launch_bounds__(kRowThreads) fat_rows_kernel(const __grid_constant__ RowParams p) {
-  extern __shared__ float2 cs_s[];  // [tok_per_block][pairs] (amplitude cos, amplitude sin)
-  const int tid = threadIdx.x;
-  const int npairs = p.rope.rotary_dim >> 1;
-  const int t0 = blockIdx.x * p.tok_per_block;
-  const int nt = min(p.tok_per_block, p.tokens - t0);
-  for (int i = tid; i < nt * npairs; i += kRowThreads) {
-    const int t = i / npairs, k = i - t * npairs;
+  const long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x;
+  const int t = (int)(i / p.units), u = (int)(i - (long long)t * p.units);
+  if (t >= p.tokens) return;
+  const bool turned = u < p.pair_units;
+  const bool two = !PAIRS && turned;
+  const int chunk = (PAIRS || turned) ? u : u + p.pair_units;
+  float2 cs[8];
+  if (turned) {
     // negative positions wrap in two's complement: still exact modulo one turn
-    const unsigned long long pos = (unsigned long long)(long long)__ldg(p.positions + t0 + t);
-    const unsigned long long turns = pos * p.rope.rate[k];
-    const float frac = (float)(uint32_t)(turns >> 40) * (1.0f / 16777216.0f);
-    float sn, cn;
-    sincospif(2.0f * frac, &sn, &cn);
-    cs_s[i] = make_float2(cn * p.rope.amplitude, sn * p.sign * p.rope.amplitude);
+    const unsigned long long pos = (unsigned long long)(long long)__ldg(p.positions + t);
+#pragma unroll
+    for (int k = 0; k < (PAIRS ? 4 : 8); ++k) {
+      const unsigned long long turns = pos * p.rope.rate[u * (PAIRS ? 4 : 8) + k];
+      const float frac = (float)(uint32_t)(turns >> 40) * (1.0f / 16777216.0f);
+      float sn, cn;
+      sincospif(2.0f * frac, &sn, &cn);
+      cs[k] = make_float2(cn * p.rope.amplitude, sn * p.sign * p.rope.amplitude);
+    }
   }
-  __syncthreads();
-  const int per_tok = p.all_heads * p.units;
-  const int n = nt * per_tok;
-  for (int i0 = tid; i0 < n; i0 += kRowThreads * kRowBatch) {
-    uint4 lo[kRowBatch], hi[kRowBatch];
-    uint16_t *dst[kRowBatch];
-    const float2 *cs[kRowBatch];  // null: copied as it is
-    bool two[kRowBatch];
-#pragma unroll
-    for (int b = 0; b < kRowBatch; ++b) {
-      const int i = i0 + b * kRowThreads;
-      dst[b] = nullptr;
-      if (i >= n) continue;
-      const int t = i / per_tok, rest = i - t * per_tok;
-      int h = rest / p.units;
-      const int u = rest - h * p.units;
-      int sg = 0;
-      while (h >= p.seg[sg].heads) h -= p.seg[sg++].heads;
-      const RowSeg &s = p.seg[sg];
-      long long row = (long long)(t0 + t) * s.dst_tok;
-      if (s.to_slots) {
-        const int slot = __ldg(p.slots + t0 + t);
-        if (slot < 0) continue;
-        if (slot >= p.num_slots) {
-          atomicOr(p.err, FAT_DEVERR_INDEX);
-          continue;
-        }
-        const int page = slot >> p.log2_page;
-        row = (long long)page * p.page_stride +
-              (long long)(slot - (page << p.log2_page)) * s.dst_tok;
-      }
-      // channels of the unit: the first chunk, and (halves) the one rotary_dim / 2 further
-      two[b] = !PAIRS && u < p.pair_units;
-      const int chunk = (PAIRS || u < p.pair_units) ? u : u + p.pair_units;
-      const uint16_t *src =
-          s.src + (long long)(t0 + t) * s.src_tok + (long long)h * s.src_head + chunk * 8;
-      dst[b] = s.dst + row + (long long)h * s.dst_head + chunk * 8;
-      const bool turned = s.rotate && u < p.pair_units;
-      cs[b] = turned ? cs_s + t * npairs + u * (PAIRS ? 4 : 8) : nullptr;
-      lo[b] = *reinterpret_cast<const uint4 *>(src);
-      if (two[b]) hi[b] = *reinterpret_cast<const uint4 *>(src + p.half_chunks * 8);
+  int h0 = blockIdx.y * p.run, left = min(p.run, p.all_heads - h0);  // heads of all segments in a row
+  for (int sg = 0; left > 0; ++sg) {
+    const RowSeg &s = p.seg[sg];
+    if (h0 >= s.heads) {
+      h0 -= s.heads;
+      continue;
     }
-#pragma unroll
-    for (int b = 0; b < kRowBatch; ++b) {
-      if (dst[b] == nullptr) continue;
-      if (cs[b] != nullptr) {
-        if constexpr (PAIRS)
-          lo[b] = rotate_pairs(lo[b], cs[b]);
-        else
-          rotate_halves(lo[b], hi[b], cs[b]);
-      }
-      *reinterpret_cast<uint4 *>(dst[b]) = lo[b];
-      if (two[b]) *reinterpret_cast<uint4 *>(dst[b] + p.half_chunks * 8) = hi[b];
+    const int n = min(left, s.heads - h0);
+    const uint16_t *src = s.src + (long long)t * s.src_tok + h0 * s.src_head + chunk * 8;
+    long long row = (long long)t * s.dst_tok;
+    bool keep = true;
+    if (s.to_slots) {
+      const int slot = __ldg(p.slots + t);
+      const int page = slot >> p.log2_page;
+      row = (long long)page * p.page_stride +
+            (long long)(slot - (page << p.log2_page)) * s.dst_tok;
+      keep = slot >= 0 && slot < p.num_slots;
+      if (slot >= p.num_slots) atomicOr(p.err, FAT_DEVERR_INDEX);
     }
+    uint16_t *dst = s.dst + row + h0 * s.dst_head + chunk * 8;
+    if (keep) {
+      const bool turn = turned && s.rotate;
+      for (int h = 0; h < n; h += kRowBatch) {
+        uint4 lo[kRowBatch], hi[kRowBatch];
+#pragma unroll
+        for (int b = 0; b < kRowBatch; ++b)
+          if (h + b < n) {
+            lo[b] = *reinterpret_cast<const uint4 *>(src + b * s.src_head);
+            if (two) hi[b] = *reinterpret_cast<const uint4 *>(src + b * s.src_head + p.half_chunks * 8);
+          }
+#pragma unroll
+        for (int b = 0; b < kRowBatch; ++b)
+          if (h + b < n) {
+            if (turn) {
+              if constexpr (PAIRS)
+                lo[b] = rotate_pairs(lo[b], cs);
+              else
+                rotate_halves(lo[b], hi[b], cs);
+            }
+            *reinterpret_cast<uint4 *>(dst + b * s.dst_head) = lo[b];
+            if (two) *reinterpret_cast<uint4 *>(dst + b * s.dst_head + p.half_chunks * 8) = hi[b];
+          }
+        src += kRowBatch * s.src_head;
+        dst += kRowBatch * s.dst_head;
+      }
+    }
+    left -= n;
+    h0 = 0;
   }
 }
 
@@ -317,8 +316,9 @@ int check_rope(const fat_rope_t *r, int head_dim) {
 }
 
 // head_dim, the rotation (null: rows are copied) and the segments are set: fill in the rest and
-// launch. Tokens per block: enough units for every thread's batch, as long as that leaves two
-// blocks for every SM.
+// launch. A thread takes all heads of its position when the positions alone give every SM
+// kRowThreadsPerSm threads, else a run of at least kRowBatch of them.
+constexpr int kRowThreadsPerSm = 1024;
 int launch_rows(RowParams &p, const fat_rope_t *rope, int head_dim, cudaStream_t stream) {
   if (rope) {
     p.rope = *rope;
@@ -334,19 +334,19 @@ int launch_rows(RowParams &p, const fat_rope_t *rope, int head_dim, cudaStream_t
   p.units = pairs ? chunks : chunks - p.half_chunks;
   p.all_heads = 0;
   for (int i = 0; i < p.nseg; ++i) p.all_heads += p.seg[i].heads;
-  const int sms = sm_count() > 0 ? sm_count() : 152;
-  const long long per_tok = (long long)p.all_heads * p.units;
-  if (per_tok > (1 << 24)) return FAT_EUNSUPPORTED;
-  long long tb = std::max<long long>(1, (2LL * kRowThreads * kRowBatch) / per_tok);
-  tb = std::min<long long>(tb, std::max(1, p.tokens / (2 * sms)));
-  tb = std::min<long long>(tb, 16);
-  p.tok_per_block = (int)tb;
-  const int blocks = (int)((p.tokens + tb - 1) / tb);
-  const size_t smem = (size_t)tb * (p.rope.rotary_dim / 2) * sizeof(float2);
+  const long long sms = sm_count() > 0 ? sm_count() : 152;
+  const long long positions = (long long)p.tokens * p.units;
+  const long long want = std::max<long long>(1, sms * kRowThreadsPerSm / positions);  // runs
+  const long long runs =
+      std::min<long long>(std::min<long long>(want, (p.all_heads + kRowBatch - 1) / kRowBatch), 65535);
+  p.run = (int)(((p.all_heads + runs - 1) / runs + kRowBatch - 1) / kRowBatch * kRowBatch);
+  const long long blocks = (positions + kRowThreads - 1) / kRowThreads;
+  if (blocks > 0x7fffffffLL || (p.all_heads + p.run - 1) / p.run > 65535) return FAT_EUNSUPPORTED;
+  const dim3 grid((unsigned)blocks, (unsigned)((p.all_heads + p.run - 1) / p.run));
   if (pairs)
-    fat_rows_kernel<true><<<blocks, kRowThreads, smem, stream>>>(p);
+    fat_rows_kernel<true><<<grid, kRowThreads, 0, stream>>>(p);
   else
-    fat_rows_kernel<false><<<blocks, kRowThreads, smem, stream>>>(p);
+    fat_rows_kernel<false><<<grid, kRowThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) return FAT_OK;
   set_last_error("rotary / append rows launch", (int)e, cudaGetErrorString(e));
