@@ -576,13 +576,18 @@ def fat_cross_entropy(logits, target, z_loss: float = 0.0, grad_scale: float = 1
 # These calls serve single decode steps, where the host's time counts: their checks read each
 # attribute once, and the device is switched only when it is not the current one.
 
+def _refuse(name, t, dtype, dev):
+    """Why t is no dtype tensor on device index dev."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments")
+
+
 def _ints(name, t, numel, dev):
-    """An int32 array argument: contiguous, on device index dev, numel entries (None: any)."""
-    import torch
-    if t.dtype is not torch.int32:
-        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments")
+    """Address of an int32 array argument: contiguous, on device index dev, numel entries (None:
+    any)."""
+    if t.dtype is not _torch.int32 or t.get_device() != dev:
+        _refuse(name, t, _torch.int32, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if numel is not None and t.numel() != numel:
@@ -591,43 +596,68 @@ def _ints(name, t, numel, dev):
 
 
 def _rows(name, t, shape, dev):
-    """A bf16 array of rows whose last dimension is contiguous (views of packed rows are fine)."""
-    import torch
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments")
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    """Strides of a bf16 array of rows whose last dimension is contiguous (views of packed rows are
+    fine); shape None: any."""
+    if t.dtype is not _torch.bfloat16 or t.get_device() != dev:
+        _refuse(name, t, _torch.bfloat16, dev)
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
     if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return st
 
 
+def _rank(name, t, rank):
+    if t.dim() != rank:
+        raise ValueError(f"{name} must have {rank} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
 def _paged_cache(k_cache, v_cache, dev) -> _Cache:
-    st = _rows("k_cache", k_cache, (None,) * 4, dev)
-    shape = k_cache.shape
+    shape = _rank("k_cache", k_cache, 4)
+    st = _rows("k_cache", k_cache, None, dev)
     if _rows("v_cache", v_cache, shape, dev) != st:
         raise ValueError("v_cache must have the strides of k_cache")
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], shape[2], shape[3],
-                  st[0], st[1], st[2])
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), *shape, *st[:3])
+
+
+def _floats(name, t, shape, dev):
+    """Address of a contiguous fp32 array argument of the given shape."""
+    if t.dtype is not _torch.float32 or t.get_device() != dev:
+        _refuse(name, t, _torch.float32, dev)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _call_on(dev: int, fn, *args) -> int:
     """fn(*args) with device index dev current."""
-    import torch
-    if torch.cuda.current_device() == dev:
+    if _torch.cuda.current_device() == dev:
         return fn(*args)
-    with torch.cuda.device(dev):
+    with _torch.cuda.device(dev):
         return fn(*args)
+
+
+_torch = None
+
+
+def _start(t):
+    """The library, with the first argument's device index (torch is imported by the first call)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the arguments must be CUDA tensors")
+    return (_lib if _lib is not None else load()), dev
 
 
 def fat_paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size: int, num_pages: int,
@@ -638,24 +668,23 @@ def fat_paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size: int, 
     [n, width], in place). Returns (cu_seqlens_q [n + 1], seqlens_k [n], positions [max_tokens],
     slots [max_tokens], counts [2] = pages taken, tokens), all int32; tokens behind the last
     request get position 0 and slot -1."""
-    import torch
-    lib = load()
-    dev = ctx_lens.get_device()
+    lib, dev = _start(ctx_lens)
     n = ctx_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != n:
-        raise ValueError(f"block_table must have shape [{n}, width]")
+    width = _rank("block_table", block_table, 2)[1]
     max_tokens = int(max_tokens)
     pc = _ints("ctx_lens", ctx_lens, n, dev)
     pn = _ints("new_lens", new_lens, n, dev)
     pf = _ints("free_pages", free_pages, None, dev)
-    pt = _ints("block_table", block_table, None, dev)
+    pt = _ints("block_table", block_table, n * width, dev)
+    if block_table.shape[0] != n:
+        raise ValueError(f"block_table must have shape [{n}, width]")
 
     def buf(t, size):
-        return torch.empty(size, dtype=torch.int32, device=ctx_lens.device) if t is None else t
+        return _torch.empty(size, dtype=_torch.int32, device=ctx_lens.device) if t is None else t
     cu_seqlens_q, seqlens_k = buf(cu_seqlens_q, n + 1), buf(seqlens_k, n)
     positions, slots = buf(positions, max_tokens), buf(slots, max_tokens)
     counts = buf(counts, 2)
-    sh = _PlanShape(n, page_size, num_pages, block_table.shape[1], free_pages.numel(), max_tokens,
+    sh = _PlanShape(n, int(page_size), int(num_pages), width, free_pages.numel(), max_tokens,
                     _raw_stream(stream, dev))
     rc = _call_on(dev, lib.fat_paged_plan, sh, pc, pn, pf, pt,
                   _ints("cu_seqlens_q", cu_seqlens_q, n + 1, dev),
@@ -688,14 +717,12 @@ def fat_rope_embed(x, positions, rope: _Rope, inverse: bool = False, out=None, s
     """Rotary embedding of bf16 rows x [T, H, d] (strided views are fine) at positions int32 [T];
     inverse=True applies the transpose, which takes the gradient of the result to the gradient of
     x. out may be x itself (in place). Returns out."""
-    import torch
-    lib = load()
-    dev = x.get_device()
-    xs = _rows("x", x, (None, None, None), dev)
-    T, H, d = x.shape
+    lib, dev = _start(x)
+    T, H, d = shape = _rank("x", x, 3)
+    xs = _rows("x", x, None, dev)
     if out is None:
-        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=x.device)
-    ys = _rows("out", out, (T, H, d), dev)
+        out = _torch.empty(shape, dtype=_torch.bfloat16, device=x.device)
+    ys = _rows("out", out, shape, dev)
     sh = _RopeShape(T, H, d, xs[0], xs[1], ys[0], ys[1], _raw_stream(stream, dev))
     rc = _call_on(dev, lib.fat_rope_embed, sh, rope, x.data_ptr(), out.data_ptr(),
                   _ints("positions", positions, T, dev), 1 if inverse else 0)
@@ -710,20 +737,19 @@ def fat_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, rope
     page * page_size + offset; negative: dropped) of the caches (bf16 [pages, page_size, Hkv, d],
     any strides with a contiguous row, the same for both). With rope, k is turned at positions
     (int32 [T]) on the way, and q (bf16 [T, Hq, d]) too. Returns q_out (contiguous) or None."""
-    import torch
-    lib = load()
-    dev = k.get_device()
+    lib, dev = _start(k)
     cache = _paged_cache(k_cache, v_cache, dev)
-    T = k.shape[0]
-    rows = (T, cache.num_heads, cache.head_dim)
+    T = _rank("k", k, 3)[0]
+    d = cache.head_dim
+    rows = (T, cache.num_heads, d)
     ks, vs = _rows("k", k, rows, dev), _rows("v", v, rows, dev)
     Hq, qs, pq, po = 0, (0, 0), None, None
     if q is not None:
-        qs = _rows("q", q, (T, None, cache.head_dim), dev)
-        Hq = q.shape[1]
+        Hq = _rank("q", q, 3)[1]
+        qs = _rows("q", q, (T, Hq, d), dev)
         if q_out is None:
-            q_out = torch.empty((T, Hq, cache.head_dim), dtype=torch.bfloat16, device=q.device)
-        _rows("q_out", q_out, (T, Hq, cache.head_dim), dev)
+            q_out = _torch.empty((T, Hq, d), dtype=_torch.bfloat16, device=q.device)
+        _rows("q_out", q_out, (T, Hq, d), dev)
         if not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous")
         pq, po = q.data_ptr(), q_out.data_ptr()
@@ -741,12 +767,12 @@ def fat_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, rope
 def fat_paged_attn_workspace_size(q, k_cache, cu_seqlens_q, max_seqlen_q: int,
                                   max_seqlen_k: int) -> int:
     """Workspace bytes of fat_paged_attn for these arguments on q's device."""
-    dev = q.get_device()
+    lib, dev = _start(q)
     sh = _PagedShape(q.shape[0], cu_seqlens_q.numel() - 1, int(max_seqlen_q), int(max_seqlen_k),
                      q.shape[1], 0, None)
     P, ps, H, d = k_cache.shape
     cache = _Cache(None, None, P, ps, H, d, 0, 0, 0)
-    return int(_call_on(dev, load().fat_paged_attn_workspace_size, sh, cache))
+    return int(_call_on(dev, lib.fat_paged_attn_workspace_size, sh, cache))
 
 
 def fat_paged_attn(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q: int,
@@ -760,56 +786,47 @@ def fat_paged_attn(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, ma
     its last query lines up with its last key. Bias, mask and scale as fat_xattn_fwd. workspace:
     fat_paged_attn_workspace_size bytes (None: allocated here), for one call at a time. Returns
     (out bf16 [Tq, Hq, d], lse fp32 [Hq, Tq])."""
-    import torch
-    lib = load()
-    dev = q.get_device()
-    _rows("q", q, (None, None, None), dev)
-    Tq, Hq, d = q.shape
+    lib, dev = _start(q)
+    Tq, Hq, d = shape = _rank("q", q, 3)
+    _rows("q", q, None, dev)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
     n = seqlens_k.numel()
     cache = _paged_cache(k_cache, v_cache, dev)
     if cache.head_dim != d:
         raise ValueError(f"q has head_dim {d}, the cache {cache.head_dim}")
-    if block_table.dim() != 2 or block_table.shape[0] != n:
+    rows, width = _rank("block_table", block_table, 2)
+    if rows != n:
         raise ValueError(f"block_table must have shape [{n}, width]")
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
     pb = ps = None
     if bias_table is not None:
-        _check_tensor("bias_table", bias_table, torch.float32, 2)
-        if bias_table.shape != (num_buckets, Hq) or bias_table.get_device() != dev:
-            raise ValueError(f"bias_table must have shape [{num_buckets}, {Hq}], on q's device")
-        pb = bias_table.data_ptr()
+        pb = _floats("bias_table", bias_table, (num_buckets, Hq), dev)
     if alibi_slopes is not None:
-        _check_tensor("alibi_slopes", alibi_slopes, torch.float32, 1)
-        if alibi_slopes.numel() != Hq or alibi_slopes.get_device() != dev:
-            raise ValueError(f"alibi_slopes must have {Hq} entries, on q's device")
-        ps = alibi_slopes.data_ptr()
+        ps = _floats("alibi_slopes", alibi_slopes, (Hq,), dev)
     if out is None:
-        out = torch.empty_like(q)
-    elif not out.is_contiguous():
-        raise ValueError("out must be contiguous")
+        out = _torch.empty_like(q)
     else:
-        _rows("out", out, (Tq, Hq, d), dev)
+        _rows("out", out, shape, dev)
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
     if lse is None:
-        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+        lse = _torch.empty((Hq, Tq), dtype=_torch.float32, device=q.device)
+        pl = lse.data_ptr()
     else:
-        _check_tensor("lse", lse, torch.float32, 2)
-        if lse.shape != (Hq, Tq) or lse.get_device() != dev:
-            raise ValueError(f"lse must have shape [{Hq}, {Tq}], on q's device")
-    sh = _PagedShape(Tq, n, max_seqlen_q, max_seqlen_k, Hq, block_table.shape[1],
+        pl = _floats("lse", lse, (Hq, Tq), dev)
+    sh = _PagedShape(Tq, n, int(max_seqlen_q), int(max_seqlen_k), Hq, width,
                      _raw_stream(stream, dev))
     if workspace is None:
         need = int(_call_on(dev, lib.fat_paged_attn_workspace_size, sh, cache))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _torch.empty(need, dtype=_torch.uint8, device=q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
     rc = _call_on(dev, lib.fat_paged_attn, sh, cache, q.data_ptr(),
                   _ints("block_table", block_table, None, dev),
                   _ints("cu_seqlens_q", cu_seqlens_q, n + 1, dev),
-                  _ints("seqlens_k", seqlens_k, n, dev), pb, num_buckets, max_distance,
-                  1 if bidirectional else 0, ps, 1 if causal else 0, softmax_scale,
-                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                  out.data_ptr(), lse.data_ptr())
+                  _ints("seqlens_k", seqlens_k, n, dev), pb, int(num_buckets), int(max_distance),
+                  1 if bidirectional else 0, ps, 1 if causal else 0, float(softmax_scale),
+                  workspace.data_ptr(), workspace.nbytes, out.data_ptr(), pl)
     if rc != 0:
         raise FatAttnError(rc, "fat_paged_attn")
     return out, lse
