@@ -53,8 +53,9 @@ __device__ __forceinline__ PagedDoc paged_doc(const PagedParams &p, int i) {
 
 // ---- partial rows -------------------------------------------------------------------------------
 // Per CTA: two records (part 0: its first item, begun by an earlier CTA; part 1: its last item,
-// begun here and continued by the next CTA), then for each record [rows][D] unnormalised rows and
-// [rows][2] (maximum in log2 units, sum).
+// begun here and continued by the next CTA), then for each record [D / 4][rows][4] unnormalised rows
+// (four channels of consecutive rows side by side: the threads that write and merge them hold a row
+// each, and their 16-byte accesses line up) and [rows][2] (maximum in log2 units, sum).
 struct PartRecord {
   int valid;   // this part exists
   int ends;    // the item ends in this CTA
@@ -76,6 +77,11 @@ template <int ROWS, int D>
 __device__ __forceinline__ float *part_rows(float *part, int ctas, int cta, int which) {
   return part + part_records_floats(ctas) + (size_t)(cta * 2 + which) * ROWS * D;
 }
+// channels 4 c4 .. 4 c4 + 3 of a row
+template <int ROWS>
+__device__ __forceinline__ float4 *part_quad(float *rows, int row, int c4) {
+  return reinterpret_cast<float4 *>(rows) + (size_t)c4 * ROWS + row;
+}
 template <int ROWS, int D>
 __device__ __forceinline__ float *part_stats(float *part, int ctas, int cta, int which) {
   return part + part_records_floats(ctas) + (size_t)ctas * 2 * ROWS * D +
@@ -83,7 +89,7 @@ __device__ __forceinline__ float *part_stats(float *part, int ctas, int cta, int
 }
 
 // ---- this CTA's stretch -------------------------------------------------------------------------
-constexpr int kShareDocs = 256;  // requests staged in shared memory from the stretch's first on
+constexpr int kShareDocs = 128;  // requests staged in shared memory from the stretch's first on
 
 struct Share {
   long long total;   // U
@@ -124,22 +130,30 @@ __device__ __forceinline__ long long share_scan(long long v, ShareSmem<NT> &s, l
 }
 
 // Find this CTA's stretch (all NT threads of the block; cost(doc) is the request's cost in this
-// kernel, 0 for the others'), report corrupt requests once, stage the requests it may hold.
-template <int NT, typename CostFn>
-__device__ __forceinline__ Share share_find(const PagedParams &p, int min_share, CostFn cost,
-                                            ShareSmem<NT> &s) {
+// kernel, 0 for the others'; change(total) may change the cost function once and says whether it
+// did), report corrupt requests once, stage the requests the stretch may hold. Up to NT requests,
+// one per thread, are read once; more are read again to find the stretch's first.
+template <int NT, typename CostFn, typename ChangeFn>
+__device__ __forceinline__ Share share_find(const PagedParams &p, int min_share, CostFn &cost,
+                                            ChangeFn change, ShareSmem<NT> &s) {
   const int tid = threadIdx.x;
+  const bool small = p.n <= NT;
   Share r;
-  // the requests' costs; those of the first NT requests stay in a register for the second pass
-  long long first = 0, mine = 0;
-  for (int i = tid; i < p.n; i += NT) {
-    const PagedDoc d = paged_doc(p, i);
-    if (!d.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
-    const long long c = d.ok && d.lq > 0 ? cost(d) : 0;
-    if (i < NT) first = c;
-    mine += c;
+  PagedDoc d{0, 0, 0, false};
+  if (tid < p.n) d = paged_doc(p, tid);
+  long long first, total, before;
+  for (int pass = 0;; ++pass) {
+    first = d.ok && d.lq > 0 ? cost(d) : 0;
+    long long mine = first;
+    for (int i = tid + NT; i < p.n; i += NT) {
+      const PagedDoc e = paged_doc(p, i);
+      if (pass == 0 && !e.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
+      if (e.ok && e.lq > 0) mine += cost(e);
+    }
+    before = share_scan<NT>(small ? first : mine, s, &total);
+    if (pass > 0 || !change(total)) break;
   }
-  long long total, before = share_scan<NT>(p.n <= NT ? first : mine, s, &total);
+  if (tid < p.n && !d.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
   r.total = total;
   const long long G = gridDim.x;
   const long long share = max((total + G - 1) / G, (long long)min_share);
@@ -148,36 +162,46 @@ __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share,
   r.doc = 0;
   r.off = 0;
   if (r.lo >= r.hi) return r;
-  long long base = 0;
-  for (int i0 = 0;; i0 += NT) {  // the stretch begins in one of the requests: this ends
-    long long c = first, chunk = total;
-    if (p.n > NT) {
-      const int i = i0 + tid;
-      c = 0;
-      if (i < p.n) {
-        const PagedDoc d = paged_doc(p, i);
-        c = d.ok && d.lq > 0 ? cost(d) : 0;
+  if (small) {
+    if (r.lo >= before && r.lo < before + first) {
+      s.doc = tid;
+      s.off = r.lo - before;
+    }
+    __syncthreads();
+    const int i = tid - s.doc;
+    if (i >= 0 && i < kShareDocs) {
+      s.sq[i] = d.sq;
+      s.lq[i] = d.ok ? d.lq : 0;
+      s.lk[i] = d.lk;
+    }
+  } else {
+    long long base = 0;
+    for (int i0 = 0;; i0 += NT) {  // the stretch begins in one of the requests: this ends
+      long long c = 0, chunk;
+      if (i0 + tid < p.n) {
+        const PagedDoc e = paged_doc(p, i0 + tid);
+        c = e.ok && e.lq > 0 ? cost(e) : 0;
       }
       before = share_scan<NT>(c, s, &chunk);
+      if (r.lo >= base + before && r.lo < base + before + c) {
+        s.doc = i0 + tid;
+        s.off = r.lo - (base + before);
+      }
+      base += chunk;
+      if (r.lo < base || i0 + NT >= p.n) break;  // the same for every thread
     }
-    if (r.lo >= base + before && r.lo < base + before + c) {
-      s.doc = i0 + tid;
-      s.off = r.lo - (base + before);
+    __syncthreads();
+    for (int i = tid; i < kShareDocs; i += NT) {
+      PagedDoc e{0, 0, 0, false};
+      if (s.doc + i < p.n) e = paged_doc(p, s.doc + i);
+      s.sq[i] = e.sq;
+      s.lq[i] = e.ok ? e.lq : 0;
+      s.lk[i] = e.lk;
     }
-    base += chunk;
-    if (r.lo < base || i0 + NT >= p.n) break;  // the same for every thread
   }
   __syncthreads();
   r.doc = s.doc;
   r.off = s.off;
-  for (int i = tid; i < kShareDocs; i += NT) {
-    PagedDoc d{0, 0, 0, false};
-    if (r.doc + i < p.n) d = paged_doc(p, r.doc + i);
-    s.sq[i] = d.sq;
-    s.lq[i] = d.ok ? d.lq : 0;
-    s.lk[i] = d.lk;
-  }
-  __syncthreads();
   return r;
 }
 

@@ -15,24 +15,29 @@ namespace {
 
 // ---- merge of cut items -------------------------------------------------------------------------
 // A chain is an item's parts in the order of their CTAs: part 1 of the CTA in which it begins, then
-// part 0 of the following ones up to the one in which it ends. One block per (CTA, kMergeRows rows)
-// whose CTA begins a chain; kMergeWarps warps share each row's parts, every lane owning D / 32
-// channels. Reads chain x (D + 2) x 4 bytes per row from L2, writes a row of out: bound by the
-// latency of the chain (a few parts, or all CTAs' when one long item fills the grid).
-constexpr int kMergeRows = 2, kMergeWarps = 4;
+// part 0 of the following ones up to the one in which it ends. One column of blocks per CTA that
+// begins a chain; a task is 32 lanes' rows (16 rows x 2 for the few-row kernel's items) by 16
+// channels, a lane owning one row's 16 channels: every load of a warp is a run of 16-byte quads of
+// consecutive rows, a lane's output one 32-byte sector. Chains of a few parts: a warp per task, the
+// parts' loads in flight together. Long chains (one context over most of the grid): the block's
+// warps share a task's parts and add their sums through shared memory.
+// Reads chain x (D + 2) x 4 bytes per row from L2; bound by the latency of a few dependent loads.
+constexpr int kMergeWarps = 8;
+constexpr int kLongChain = 16;  // parts from which the warps of a block share a task
+constexpr int kMergeBatch = 4;  // parts whose loads a lane has in flight
 
 template <int ROWS, int D>
-__global__ void __launch_bounds__(kMergeRows *kMergeWarps * 32)
+__global__ void __launch_bounds__(kMergeWarps * 32)
     fat_paged_merge_kernel(const __grid_constant__ PagedParams p, const int ctas) {
-  constexpr int CPL = D / 32;
-  __shared__ float acc_s[kMergeRows][kMergeWarps][D];
-  __shared__ float2 st_s[kMergeRows][kMergeWarps];
+  constexpr int RL = ROWS < 32 ? ROWS : 32;        // rows side by side in a warp
+  constexpr int CH = 16;                           // channels per lane
+  constexpr int RG = ROWS / RL, CG = D / CH / (32 / RL);  // tasks: row groups x channel groups
+  __shared__ float sum_s[kMergeWarps][CH + 2][32];
   grid_dep_wait();
   const int c = blockIdx.x;
   const PartRecord rec = *part_record(p.part, c, 1);
-  if (!rec.valid || blockIdx.y * kMergeRows >= rec.rows) return;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) / kMergeRows;
-  const int rs = (threadIdx.x >> 5) % kMergeRows;
+  if (!rec.valid) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   // parts 1 .. n - 1 lie in CTAs c + 1 .. c + n - 1
   int n = 1;
   for (int i0 = 1;; i0 += 32) {
@@ -44,73 +49,90 @@ __global__ void __launch_bounds__(kMergeRows *kMergeWarps * 32)
       break;
     }
   }
-  for (int r0 = blockIdx.y * kMergeRows; r0 < rec.rows; r0 += gridDim.y * kMergeRows) {
-    const int r = r0 + rs;
-    float m = -INFINITY, l = 0.f, o[CPL];
+  const bool shared = n > kLongChain;
+  const int first = shared ? blockIdx.y : blockIdx.y * kMergeWarps + w;
+  const int step = shared ? gridDim.y : gridDim.y * kMergeWarps;
+  for (int task = first; task < RG * CG; task += step) {  // the same count for all warps if shared
+    const int r = (task / CG) * RL + lane % RL;
+    const int q0 = ((task % CG) * (32 / RL) + lane / RL) * (CH / 4);  // first quad of channels
+    float m = -INFINITY, l = 0.f, o[CH];
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) o[k] = 0.f;
+    for (int k = 0; k < CH; ++k) o[k] = 0.f;
     if (r < rec.rows) {
-#pragma unroll 4
-      for (int i = w; i < n; i += kMergeWarps) {
-        const int which = i == 0 ? 1 : 0;
-        const float2 st = *reinterpret_cast<const float2 *>(
-            part_stats<ROWS, D>(p.part, ctas, c + i, which) + r * 2);
-        const float *src = part_rows<ROWS, D>(p.part, ctas, c + i, which) + r * D + lane * CPL;
-        float v[CPL];
-        if constexpr (CPL == 4) {
-          const float4 t = *reinterpret_cast<const float4 *>(src);
-          v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-        } else {
-          const float2 t = *reinterpret_cast<const float2 *>(src);
-          v[0] = t.x, v[1] = t.y;
-        }
-        const float mn = fmaxf(m, st.x);
-        const float fo = m == -INFINITY ? 0.f : ex2(m - mn);
-        const float fn = st.x == -INFINITY ? 0.f : ex2(st.x - mn);
-        l = l * fo + st.y * fn;
+      const int i_step = shared ? kMergeWarps : 1;
+      for (int i0 = shared ? w : 0; i0 < n; i0 += kMergeBatch * i_step) {
+        float2 st[kMergeBatch];  // the loads of several parts first, then their sums
+        float4 v[kMergeBatch][CH / 4];
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) o[k] = o[k] * fo + v[k] * fn;
+        for (int b = 0; b < kMergeBatch; ++b) {
+          const int i = i0 + b * i_step;
+          st[b] = make_float2(-INFINITY, 0.f);
+          if (i < n) {
+            const int which = i == 0 ? 1 : 0;
+            st[b] = *reinterpret_cast<const float2 *>(
+                part_stats<ROWS, D>(p.part, ctas, c + i, which) + r * 2);
+            float *rows = part_rows<ROWS, D>(p.part, ctas, c + i, which);
+#pragma unroll
+            for (int k = 0; k < CH / 4; ++k) v[b][k] = *part_quad<ROWS>(rows, r, q0 + k);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kMergeBatch; ++b) {
+          if (st[b].x == -INFINITY) continue;  // no key in this part
+          const float mn = fmaxf(m, st[b].x);
+          const float fo = m == -INFINITY ? 0.f : ex2(m - mn), fn = ex2(st[b].x - mn);
+          l = l * fo + st[b].y * fn;
+#pragma unroll
+          for (int k = 0; k < CH / 4; ++k) {
+            o[4 * k] = o[4 * k] * fo + v[b][k].x * fn;
+            o[4 * k + 1] = o[4 * k + 1] * fo + v[b][k].y * fn;
+            o[4 * k + 2] = o[4 * k + 2] * fo + v[b][k].z * fn;
+            o[4 * k + 3] = o[4 * k + 3] * fo + v[b][k].w * fn;
+          }
+          m = mn;
+        }
+      }
+    }
+    if (shared) {
+      __syncthreads();  // the task before has been read
+#pragma unroll
+      for (int k = 0; k < CH; ++k) sum_s[w][k][lane] = o[k];
+      sum_s[w][CH][lane] = m;
+      sum_s[w][CH + 1][lane] = l;
+      __syncthreads();
+      if (w != 0) continue;
+#pragma unroll
+      for (int i = 1; i < kMergeWarps; ++i) {
+        const float mi = sum_s[i][CH][lane], mn = fmaxf(m, mi);
+        const float fo = m == -INFINITY ? 0.f : ex2(m - mn);
+        const float fn = mi == -INFINITY ? 0.f : ex2(mi - mn);
+        l = l * fo + sum_s[i][CH + 1][lane] * fn;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) o[k] = o[k] * fo + sum_s[i][k][lane] * fn;
         m = mn;
       }
     }
-    __syncthreads();  // the rows before have been read
-#pragma unroll
-    for (int k = 0; k < CPL; ++k) acc_s[rs][w][lane * CPL + k] = o[k];
-    if (lane == 0) st_s[rs][w] = make_float2(m, l);
-    __syncthreads();
-    if (w != 0 || r >= rec.rows) continue;
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) M = fmaxf(M, st_s[rs][i].x);
-#pragma unroll
-    for (int k = 0; k < CPL; ++k) o[k] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) {
-      const float2 st = st_s[rs][i];
-      const float f = st.x == -INFINITY ? 0.f : ex2(st.x - M);
-      L += st.y * f;
-#pragma unroll
-      for (int k = 0; k < CPL; ++k) o[k] += acc_s[rs][i][lane * CPL + k] * f;
-    }
-    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    if (r >= rec.rows) continue;
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
     const int q = r / p.group, h = rec.hk * p.group + (r - q * p.group);
     const size_t row = (size_t)rec.row0 + q;
-    __nv_bfloat16 *dst = p.out + (row * p.hq + h) * D + lane * CPL;
-    if constexpr (CPL == 4)
-      *reinterpret_cast<uint2 *>(dst) =
-          make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    else
-      *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[(size_t)h * p.total_q + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (row * p.hq + h) * D + q0 * 4);
+#pragma unroll
+    for (int k = 0; k < CH / 8; ++k)
+      dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                          pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                          pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                          pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+    if (q0 == 0 && p.lse != nullptr)
+      p.lse[(size_t)h * p.total_q + row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
   }
 }
 
 template <int ROWS, int D>
 int launch_merge(const PagedParams &p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas, std::min(ROWS / kMergeRows, 16));
-  cfg.blockDim = dim3(kMergeRows * kMergeWarps * 32);
+  cfg.gridDim = dim3((unsigned)ctas, ROWS == kFewRows ? 2 : 8);
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,9 +1,9 @@
 // fat_paged_few.cu -- attention over a paged cache for requests with few rows: a decode step, a few
 // drafted tokens, a group's heads over their key/value head (queries x group heads <= 16 rows).
 //
-// The work is one read of the requests' keys and values; the rows ride along. A CTA (one per SM)
-// takes an equal share of all key stages (fat_paged.cuh); a stage is 16 KB of keys and values (32
-// tokens at head_dim 128, 64 at 64). Four warps work on their own, each with a ring of three
+// The work is one read of the requests' keys and values; the rows ride along. A CTA (two per SM)
+// takes an equal share of all key stages (fat_paged.cuh); a stage is 8 KB of keys and values (16
+// tokens at head_dim 128, 32 at 64). Four warps work on their own, each with a ring of three
 // stages that it fills by TMA itself (pages of 16 tokens and more come as boxes of 16 rows x 64
 // channels, 128-byte swizzle) and waits for: no producer warp and no hand-off between warps, the
 // next stages' copies and their page numbers are always in flight. Per stage and warp: S = Q K^T
@@ -25,11 +25,12 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kRing = 3;           // stages per warp
 constexpr int kShortStages = 2;    // items of at most this many stages are one warp's
 constexpr int kMinShare = 8;       // stages a CTA takes at least
-constexpr int kOStride = 72;       // floats per row of a merge buffer (64 channels at a time)
+constexpr int kMergeCh = 32;        // channels merged at a time
+constexpr int kOStride = kMergeCh + 8;  // floats per row of a merge buffer
 
 template <int D>
 struct FewCfg {
-  static constexpr int KT = 64 * 64 / D;         // tokens per stage
+  static constexpr int KT = 32 * 64 / D;         // tokens per stage
   static constexpr int DB = D / 64;              // 64-channel blocks
   static constexpr int PIECE = 16 * 128;         // one box: 16 rows x 64 channels
   static constexpr int PIECES = KT / 16;         // boxes per 64-channel block
@@ -47,7 +48,7 @@ struct FewCfg {
     return OFF_LUT + (b.table ? (b.sat_neg + b.sat_pos + 1 + 15) & ~15 : 0);
   }
   static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
-  static_assert(STAGE == 16384, "a stage is 16 KB");
+  static_assert(STAGE == 8192, "a stage is 8 KB");
 };
 
 // Cost of a request: the stages of its keys for every key/value head.
@@ -142,7 +143,7 @@ struct FewStages {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     fat_paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ PagedParams p) {
@@ -170,7 +171,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     PartRecord *r = part_record(p.part, blockIdx.x, tid);
     r->valid = 0;
   }
-  const Share sh = share_find<kThreads>(p, kMinShare, FewCost<D>{p}, share_s);
+  FewCost<D> cost{p};
+  const Share sh =
+      share_find<kThreads>(p, kMinShare, cost, [](long long) { return false; }, share_s);
   if (sh.lo >= sh.hi) {
     grid_dep_wait();
     return;
@@ -196,12 +199,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto settle = [&]() {  // on to an item that has a stage for this warp
     more = true;
-    while (ahead.s >= ahead.it.s1)
+    bool fresh = false;
+    while (ahead.s >= ahead.it.s1) {
+      fresh = true;
       if (!ahead.item(warp)) {
         more = false;
         break;
       }
+    }
     fetch_page();
+    if (fresh && more) {  // its queries (a row per two lanes) and bias table rows, towards L1
+      const FewItem &it = ahead.it;
+      const int r = lane >> 1, q = r / p.group;
+      if (q < it.lq && (D == 128 || (lane & 1) == 0))
+        prefetch_l1(p.q + ((size_t)(it.sq + q) * p.hq + it.hk * p.group + (r - q * p.group)) * D +
+                    (lane & 1) * 64);
+      if (p.bias.table != nullptr)
+        for (int b = lane; b < p.bias.nb; b += 32)
+          prefetch_l1(p.bias.table + (size_t)b * p.hq + it.hk * p.group);
+      if (p.bias.slopes != nullptr && lane == 0) prefetch_l1(p.bias.slopes + it.hk * p.group);
+    }
   };
   auto issue = [&](int slot) {  // the cursor's stage into `slot`; the cursor moves on
     const int tok = ahead.s * KT + lane * 16;
@@ -338,15 +355,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (k0 - (shift + it.lq - 1) >= p.bias.sat_pos ||
                    k0 + KT - 1 - shift <= -p.bias.sat_neg) {  // every delta on one far side
           const bool pos = k0 - (shift + it.lq - 1) >= p.bias.sat_pos;
+          const float kk[2] = {pos ? -slope[0] : slope[0], pos ? -slope[1] : slope[1]};
+          const float c0[2] = {fmaf(kk[0], (float)(kb - qpos[0]), pos ? far_pos[0] : far_neg[0]),
+                               fmaf(kk[1], (float)(kb - qpos[1]), pos ? far_pos[1] : far_neg[1])};
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = e >> 1;
-              const float dist = fabsf((float)(kb + 8 * t + (e & 1) - qpos[i]));
+            for (int e = 0; e < 4; ++e)
               x[t][e] = fmaf(x[t][e], p.scale_log2,
-                             fmaf(-slope[i], dist, pos ? far_pos[i] : far_neg[i]));
-            }
+                             fmaf(kk[e >> 1], (float)(8 * t + (e & 1)), c0[e >> 1]));
         } else {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -472,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int t = 0; t < D / 8; ++t)
-            *reinterpret_cast<float2 *>(po + r * D + t * 8 + 2 * (lane & 3)) =
+            reinterpret_cast<float2 *>(
+                part_quad<kFewRows>(po, r, t * 2 + ((lane >> 1) & 1)))[lane & 1] =
                 make_float2(o[t][2 * i], o[t][2 * i + 1]);
           if ((lane & 3) == 0) *reinterpret_cast<float2 *>(ps + r * 2) = make_float2(m[i], l[i]);
         }
@@ -507,18 +525,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *buf = reinterpret_cast<float *>(sm + C::OFF_MERGE);
     const float *fin = stats + kWarps * kFewRows * 2;
 #pragma unroll
-    for (int b = 0; b < C::DB; ++b) {  // 64 channels at a time
+    for (int b = 0; b < D / kMergeCh; ++b) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
+      for (int t = 0; t < kMergeCh / 8; ++t) {
+        const int ot = b * (kMergeCh / 8) + t;
         float *dst = buf + warp * kFewRows * kOStride + t * 8 + 2 * (lane & 3);
         *reinterpret_cast<float2 *>(dst + r0 * kOStride) =
-            make_float2(o[b * 8 + t][0] * f[0], o[b * 8 + t][1] * f[0]);
+            make_float2(o[ot][0] * f[0], o[ot][1] * f[0]);
         *reinterpret_cast<float2 *>(dst + r1 * kOStride) =
-            make_float2(o[b * 8 + t][2] * f[1], o[b * 8 + t][3] * f[1]);
+            make_float2(o[ot][2] * f[1], o[ot][3] * f[1]);
       }
       __syncthreads();
-      for (int i = tid; i < rows * 16; i += kThreads) {
-        const int r = i >> 4, c = (i & 15) * 4;
+      static_assert(kFewRows * kMergeCh / 4 == kThreads, "one quad of channels per thread");
+      const int r = whole ? tid / (kMergeCh / 4) : tid % kFewRows;
+      const int c = 4 * (whole ? tid % (kMergeCh / 4) : tid / kFewRows);
+      if (r < rows) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -530,17 +551,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.w += v.w;
         }
         const float M = fin[r * 2], L = fin[r * 2 + 1];
+        const int ch = b * kMergeCh + c;
         if (whole) {
           const int q = r / G, h = it.hk * G + (r - q * G), row = it.sq + q;
           const float inv = L > 0.f ? 1.0f / L : 0.f;
-          *reinterpret_cast<uint2 *>(p.out + ((size_t)row * p.hq + h) * D + b * 64 + c) =
+          *reinterpret_cast<uint2 *>(p.out + ((size_t)row * p.hq + h) * D + ch) =
               make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-          if (b == 0 && c == 0 && p.lse != nullptr)
+          if (ch == 0 && p.lse != nullptr)
             p.lse[(size_t)h * p.total_q + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
         } else {
-          *reinterpret_cast<float4 *>(part_rows<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which) +
-                                      r * D + b * 64 + c) = a;
-          if (b == 0 && c == 0)
+          *part_quad<kFewRows>(part_rows<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which), r,
+                               ch / 4) = a;
+          if (ch == 0)
             *reinterpret_cast<float2 *>(
                 part_stats<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which) + r * 2) =
                 make_float2(M, L);
@@ -585,7 +607,7 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
 
 }  // namespace
 
-int paged_few_ctas() { return sm_count() > 0 ? sm_count() : 152; }
+int paged_few_ctas() { return 2 * (sm_count() > 0 ? sm_count() : 152); }
 
 int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream,
                      bool overlap_previous) {

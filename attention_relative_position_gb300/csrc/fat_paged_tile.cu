@@ -30,6 +30,9 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kWarpProd = 8, kWarpMma = 9, kWarpTail = 11;
 constexpr int kMinShare = 4;  // cost units (a key tile of one Q tile) a CTA takes at least
+// Blocks of two Q tiles share their key tiles' copies; blocks of one are cut into fewer and smaller
+// partial rows. A CTA with fewer units than this takes blocks of one.
+constexpr int kPairShare = 64;
 
 template <int D>
 struct TileCfg {
@@ -66,10 +69,11 @@ struct TileCfg {
 struct TileBlock {
   int q0, ntok, nkv, tiles, cost;
 };
-__device__ __forceinline__ TileBlock tile_block(const PagedDoc &d, int b, int tq, int causal) {
+__device__ __forceinline__ TileBlock tile_block(const PagedDoc &d, int b, int tq, int blk,
+                                                int causal) {
   TileBlock t;
-  t.q0 = b * 2 * tq;
-  t.ntok = min(d.lq - t.q0, 2 * tq);
+  t.q0 = b * blk;
+  t.ntok = min(d.lq - t.q0, blk);
   t.tiles = t.ntok > tq ? 2 : 1;
   t.nkv = (d.lk + 127) >> 7;
   if (causal) {
@@ -79,16 +83,18 @@ __device__ __forceinline__ TileBlock tile_block(const PagedDoc &d, int b, int tq
   t.cost = max(1, t.tiles * t.nkv);
   return t;
 }
-__device__ __forceinline__ long long tile_head_cost(const PagedDoc &d, int tq, int causal) {
+__device__ __forceinline__ long long tile_head_cost(const PagedDoc &d, int tq, int blk,
+                                                    int causal) {
   long long c = 0;
-  for (int b = 0; b * 2 * tq < d.lq; ++b) c += tile_block(d, b, tq, causal).cost;
+  for (int b = 0; b * blk < d.lq; ++b) c += tile_block(d, b, tq, blk, causal).cost;
   return c;
 }
 struct TileCost {
   const PagedParams &p;
-  int tq;
+  int tq, blk;  // tokens per tile and per block
   __device__ long long operator()(const PagedDoc &d) const {
-    return (long long)d.lq * p.group <= p.few_rows ? 0 : p.hkv * tile_head_cost(d, tq, p.causal);
+    return (long long)d.lq * p.group <= p.few_rows ? 0
+                                                   : p.hkv * tile_head_cost(d, tq, blk, p.causal);
   }
 };
 
@@ -103,16 +109,18 @@ struct TileItem {
 struct TileWalk {
   const PagedParams &p;
   const ShareSmem<kThreads> &sm;
-  int tq, first_doc, doc, hk, b;
+  int tq, blk, first_doc, doc, hk, b;
   long long left;
   int off;
-  __device__ TileWalk(const PagedParams &pp, const ShareSmem<kThreads> &s, int tq_, const Share &sh)
-      : p(pp), sm(s), tq(tq_), first_doc(sh.doc), doc(sh.doc), b(0), left(sh.hi - sh.lo) {
+  __device__ TileWalk(const PagedParams &pp, const ShareSmem<kThreads> &s, const TileCost &c,
+                      const Share &sh)
+      : p(pp), sm(s), tq(c.tq), blk(c.blk), first_doc(sh.doc), doc(sh.doc), b(0),
+        left(sh.hi - sh.lo) {
     const PagedDoc d = share_doc(p, sm, doc, doc);
-    const long long per = tile_head_cost(d, tq, p.causal);
+    const long long per = tile_head_cost(d, tq, blk, p.causal);
     hk = (int)(sh.off / per);
     long long rest = sh.off - hk * per;
-    for (int c; rest >= (c = tile_block(d, b, tq, p.causal).cost); rest -= c) ++b;
+    for (int c; rest >= (c = tile_block(d, b, tq, blk, p.causal).cost); rest -= c) ++b;
     off = (int)rest;
   }
   __device__ bool next(TileItem &it) {
@@ -123,7 +131,7 @@ struct TileWalk {
         hk = b = 0;
         continue;
       }
-      const TileBlock t = tile_block(d, b, tq, p.causal);
+      const TileBlock t = tile_block(d, b, tq, blk, p.causal);
       const int o = off;
       off = 0;
       const int take = (int)min(left, (long long)(t.cost - o));
@@ -138,7 +146,7 @@ struct TileWalk {
       it.shift = d.lk - d.lq;
       it.nkv = t.nkv;
       ++b;
-      if (b * 2 * tq >= d.lq) {
+      if (b * blk >= d.lq) {
         b = 0;
         if (++hk == p.hkv) {
           hk = 0;
@@ -254,12 +262,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();
   if (p.split && tid < 2) part_record(p.part, blockIdx.x, tid)->valid = 0;
   for (int i = tid; i < p.bias.n_thr; i += kThreads) thr_s[i] = p.bias.thr[i];
-  const Share share = share_find<kThreads>(p, kMinShare, TileCost{p, tq}, share_s);
+  TileCost cost{p, tq, 2 * tq};
+  const Share share = share_find<kThreads>(
+      p, kMinShare, cost,
+      [&](long long total) {
+        if (total >= (long long)kPairShare * gridDim.x) return false;
+        cost.blk = tq;
+        return true;
+      },
+      share_s);
   if (share.lo >= share.hi) return;
 
   if (warp == kWarpProd && lane == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 2);
+    mbar_init(q_empty, 2);  // one release per issuer and item
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(k_full + s, 1);
       mbar_init(v_full + s, 1);
@@ -306,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpProd) {
     // ------------------------------------------------------------------ producer
     const int kbox = min(128, 1 << p.log2_page), pieces = 128 / kbox;
-    TileWalk walk(p, share_s, tq, share);
+    TileWalk walk(p, share_s, cost, share);
     TileItem it;
     uint32_t J = 0;      // K/V stream position
     int ni = 0;          // items with keys
@@ -324,7 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int kt = it.nkv - 1 - it.j0;
       int page = fetch(kt);
+      // Q is free once both issuers have released it, which also means that every K tile so far
+      // has been used. The V tiles so far have arrived too before the next Q is loaded: an issuer
+      // that finds Q full then knows every stage's earlier phases to be over, also those of stages
+      // that only the other one used, and tells the phases of its own by their parity.
       if (ni > 0) ok = warp_wait(q_empty, (ni - 1) & 1, wd);
+      for (uint32_t k = 1; ok && k <= min(J, (uint32_t)C::NS); ++k)
+        ok = warp_wait(v_full + ((J - k) & (C::NS - 1)), ((J - k) >> C::NS_LOG2) & 1, wd);
       if (!ok) break;
       if (lane == 0) {
         const uint32_t bytes = (uint32_t)RT * 128 * C::DB * it.tiles;
@@ -392,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t aP = C::SEP_P ? tmem + C::COL_P + 64 * t : dS;
       const uint64_t dKd = sw128_desc(smem_u32(sK), 16, 1024);
       const uint64_t dVd = sw128_desc(smem_u32(sV), C::BLK, 1024);
-      TileWalk walk(p, share_s, tq, share);
+      TileWalk walk(p, share_s, cost, share);
       TileItem it;
       uint32_t J = 0, g = 0;  // stream position, this tile's steps
       int ni = 0, act = 0;    // items with keys, those in which this tile has steps
@@ -401,14 +423,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = it.j1 - it.j0;
         if (n == 0) continue;
         const int first = TileWalk::first(it, t), step = TileWalk::step(it);
-        if (first >= n) {  // one key tile: the other issuer's
+        if (first >= n) {  // one key tile: the other issuer's; Q is released without being used
+          if (!(ok = mbar_wait(q_full, ni & 1, wd))) break;
+          mbar_arrive(q_empty);
           J += n;
           ++ni;
           continue;
         }
         const uint64_t dQd = sw128_desc(smem_u32(sQ) + (it.tiles == 2 ? t * C::TILE : 0), 16, 1024);
-        const bool alone = it.tiles == 1;            // the stages are this tile's alone
-        const bool only = alone && n == 1;           // and so is Q
+        const bool alone = it.tiles == 1;  // each stage is one tile's
         auto issue_S = [&](int jj) {
           const uint64_t kd = dKd + ((((J + jj) & (C::NS - 1)) * C::TILE) >> 4);
 #pragma unroll
@@ -420,10 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t *ke = k_empty + ((J + jj) & (C::NS - 1));
           mma_commit(ke);
           if (alone) mma_commit(ke);
-          if (jj + step >= n) {  // the item's last S of this tile
-            mma_commit(q_empty);
-            if (only) mma_commit(q_empty);
-          }
+          if (jj + step >= n) mma_commit(q_empty);  // the item's last S of this tile
         };
         auto k_wait = [&](int jj) {
           return mbar_wait(k_full + ((J + jj) & (C::NS - 1)), ((J + jj) >> C::NS_LOG2) & 1, wd);
@@ -472,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpTail) {
     // ------------------------------------------------------------------ values behind the last key
-    TileWalk walk(p, share_s, tq, share);
+    TileWalk walk(p, share_s, cost, share);
     TileItem it;
     uint32_t J = 0;
     int nt = 0;
@@ -506,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2 *stats = reinterpret_cast<float2 *>(sm + C::OFF_STATS);
     const int rq = r / G, rg = r - rq * G;  // token and head of this row within the tile
     const bool has_slopes = p.bias.slopes != nullptr, has_table = p.bias.table != nullptr;
-    TileWalk walk(p, share_s, tq, share);
+    TileWalk walk(p, share_s, cost, share);
     TileItem it;
     uint32_t g = 0, g_other = 0;  // steps of this tile and of the other one
     int merges = 0;
@@ -706,11 +726,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (valid) {
-          float4 *dst = reinterpret_cast<float4 *>(
-              part_rows<kTileRows, D>(p.part, gridDim.x, blockIdx.x, which) + prow * D + c * 32);
+          float *part = part_rows<kTileRows, D>(p.part, gridDim.x, blockIdx.x, which);
 #pragma unroll
           for (int v = 0; v < 8; ++v)
-            dst[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+            *part_quad<kTileRows>(part, prow, c * 8 + v) = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
                                  __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
         }
       }
