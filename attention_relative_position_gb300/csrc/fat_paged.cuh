@@ -31,6 +31,8 @@ struct PagedParams {
   long long timeout_ns;
   int debug_flags;
   int few_rows;   // requests with at most this many rows (queries x group) are the few-row kernel's
+  int both;       // the call launches both kernels: they share the SMs (see share_find)
+  int sms;
   int split;      // 0: items are not cut (each goes to the CTA in whose share it begins)
   float *part;    // partial rows of this kernel's grid (see PartLayout)
 };
@@ -49,6 +51,65 @@ __device__ __forceinline__ PagedDoc paged_doc(const PagedParams &p, int i) {
          d.lk <= p.max_k && d.lk <= ((long long)p.width << p.log2_page);
   d.lq = eq - d.sq;
   return d;
+}
+
+// ---- costs --------------------------------------------------------------------------------------
+// Few-row kernel: stages of 8 KB of keys and values for every key/value head.
+__host__ __device__ constexpr int few_stage_tokens(int d) { return 2048 / d; }
+template <int D>
+struct FewCost {
+  const PagedParams &p;
+  __device__ long long operator()(const PagedDoc &d) const {
+    if ((long long)d.lq * p.group > p.few_rows) return 0;
+    constexpr int KT = few_stage_tokens(D);
+    return (long long)p.hkv * max(1, (d.lk + KT - 1) / KT);
+  }
+};
+
+// Tile kernel: one block of queries of a request: tokens [q0, q0 + ntok), one or two tiles, the key
+// tiles that its rows see, its cost in (Q tile, key tile) pairs.
+struct TileBlock {
+  int q0, ntok, nkv, tiles, cost;
+};
+__device__ __forceinline__ TileBlock tile_block(const PagedDoc &d, int b, int tq, int blk,
+                                                int causal) {
+  TileBlock t;
+  t.q0 = b * blk;
+  t.ntok = min(d.lq - t.q0, blk);
+  t.tiles = t.ntok > tq ? 2 : 1;
+  t.nkv = (d.lk + 127) >> 7;
+  if (causal) {
+    const int last = d.lk - d.lq + t.q0 + t.ntok - 1;  // key position of the last row
+    t.nkv = last < 0 ? 0 : min(t.nkv, (last >> 7) + 1);
+  }
+  t.cost = max(1, t.tiles * t.nkv);
+  return t;
+}
+__device__ __forceinline__ long long tile_head_cost(const PagedDoc &d, int tq, int blk,
+                                                    int causal) {
+  long long c = 0;
+  for (int b = 0; b * blk < d.lq; ++b) c += tile_block(d, b, tq, blk, causal).cost;
+  return c;
+}
+struct TileCost {
+  const PagedParams &p;
+  int tq, blk;  // tokens per tile and per block
+  __device__ long long operator()(const PagedDoc &d) const {
+    return (long long)d.lq * p.group <= p.few_rows ? 0
+                                                   : p.hkv * tile_head_cost(d, tq, blk, p.causal);
+  }
+};
+
+// SMs of the tile kernel when a call launches both kernels: in proportion to their times, a pair of
+// tiles weighing as many stages as kPairStages says (1.5 us against 0.18 us of an SM at head_dim
+// 128, measured; half of that at 64), each at least one. The other SMs are the few-row kernel's.
+template <int D>
+__device__ __forceinline__ int tile_sms(const PagedParams &p, long long tile_total,
+                                        long long few_total) {
+  if (!p.both || few_total == 0) return p.sms;
+  if (tile_total == 0) return 0;
+  const float a = (D == 128 ? 8.f : 4.f) * (float)tile_total, b = (float)few_total;
+  return min(max((int)(p.sms * (a / (a + b)) + 0.5f), 1), p.sms - 1);
 }
 
 // ---- partial rows -------------------------------------------------------------------------------
@@ -130,19 +191,30 @@ __device__ __forceinline__ long long share_scan(long long v, ShareSmem<NT> &s, l
 }
 
 // Find this CTA's stretch (all NT threads of the block; cost(doc) is the request's cost in this
-// kernel, 0 for the others'; change(total) may change the cost function once and says whether it
-// did), report corrupt requests once, stage the requests the stretch may hold. Up to NT requests,
+// kernel, other(doc) in the other one, 0 for requests that are not theirs; ctas(total, other total)
+// is the number of CTAs that share the line, and may change the cost function once, of which it
+// tells), report corrupt requests once, stage the requests the stretch may hold. Up to NT requests,
 // one per thread, are read once; more are read again to find the stretch's first.
-template <int NT, typename CostFn, typename ChangeFn>
+template <int NT, typename CostFn, typename OtherFn, typename CtasFn>
 __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share, CostFn &cost,
-                                            ChangeFn change, ShareSmem<NT> &s) {
+                                            const OtherFn &other, CtasFn ctas, ShareSmem<NT> &s) {
   const int tid = threadIdx.x;
   const bool small = p.n <= NT;
   Share r;
   PagedDoc d{0, 0, 0, false};
   if (tid < p.n) d = paged_doc(p, tid);
-  long long first, total, before;
-  for (int pass = 0;; ++pass) {
+  long long first, total, before, other_total = 0;
+  if (p.both) {
+    long long mine = d.ok && d.lq > 0 ? other(d) : 0;
+    for (int i = tid + NT; i < p.n; i += NT) {
+      const PagedDoc e = paged_doc(p, i);
+      if (e.ok && e.lq > 0) mine += other(e);
+    }
+    share_scan<NT>(mine, s, &other_total);
+  }
+  bool again = true;
+  int G = 0;
+  for (int pass = 0; again; ++pass) {
     first = d.ok && d.lq > 0 ? cost(d) : 0;
     long long mine = first;
     for (int i = tid + NT; i < p.n; i += NT) {
@@ -151,16 +223,17 @@ __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share,
       if (e.ok && e.lq > 0) mine += cost(e);
     }
     before = share_scan<NT>(small ? first : mine, s, &total);
-    if (pass > 0 || !change(total)) break;
+    again = false;
+    if (pass == 0) G = ctas(total, other_total, &again);
   }
   if (tid < p.n && !d.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
   r.total = total;
-  const long long G = gridDim.x;
+  r.lo = r.hi = r.off = 0;
+  r.doc = 0;
+  if ((int)blockIdx.x >= G || total == 0) return r;
   const long long share = max((total + G - 1) / G, (long long)min_share);
   r.lo = blockIdx.x * share;
   r.hi = min(total, r.lo + share);
-  r.doc = 0;
-  r.off = 0;
   if (r.lo >= r.hi) return r;
   if (small) {
     if (r.lo >= before && r.lo < before + first) {

@@ -241,6 +241,8 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   p.lse = lse;
   runtime_knobs(&p.timeout_ns, &p.debug_flags);
   p.few_rows = kFewRows;
+  p.both = plan.few && plan.tile;
+  p.sms = paged_tile_ctas();
   const int d = cache->head_dim;
   const cudaStream_t s = static_cast<cudaStream_t>(sh->stream);
   p.split = plan.split;

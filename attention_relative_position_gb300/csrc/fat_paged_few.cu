@@ -30,7 +30,7 @@ constexpr int kOStride = kMergeCh + 8;  // floats per row of a merge buffer
 
 template <int D>
 struct FewCfg {
-  static constexpr int KT = 32 * 64 / D;         // tokens per stage
+  static constexpr int KT = few_stage_tokens(D);  // tokens per stage
   static constexpr int DB = D / 64;              // 64-channel blocks
   static constexpr int PIECE = 16 * 128;         // one box: 16 rows x 64 channels
   static constexpr int PIECES = KT / 16;         // boxes per 64-channel block
@@ -49,17 +49,6 @@ struct FewCfg {
   }
   static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
   static_assert(STAGE == 8192, "a stage is 8 KB");
-};
-
-// Cost of a request: the stages of its keys for every key/value head.
-template <int D>
-struct FewCost {
-  const PagedParams &p;
-  __device__ long long operator()(const PagedDoc &d) const {
-    if ((long long)d.lq * p.group > p.few_rows) return 0;
-    constexpr int KT = FewCfg<D>::KT;
-    return (long long)p.hkv * max(1, (d.lk + KT - 1) / KT);
-  }
 };
 
 // The items of a share in order.
@@ -172,8 +161,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     r->valid = 0;
   }
   FewCost<D> cost{p};
-  const Share sh =
-      share_find<kThreads>(p, kMinShare, cost, [](long long) { return false; }, share_s);
+  const Share sh = share_find<kThreads>(
+      p, kMinShare, cost, TileCost{p, 128 / p.group, 2 * (128 / p.group)},
+      [&](long long mine, long long other, bool *) {
+        return 2 * (p.sms - (p.both ? tile_sms<D>(p, other, mine) : 0));
+      },
+      share_s);
   if (sh.lo >= sh.hi) {
     grid_dep_wait();
     return;
@@ -185,74 +178,70 @@ __global__ void __launch_bounds__(kThreads, 2)
                          (int)(sh.off % cost0)};
   uint8_t *ring = sm + warp * kRing * C::STAGE;
 
-  // ---- copies: a cursor ahead of the computation. Lane i < PIECES holds the page of piece i.
+  // ---- copies: a cursor ahead of the computation. Lane i < PIECES holds the page of piece i. The
+  // code is kept to one place (fill, at the top of a stage's turn): a short call is bound by the
+  // latency of its first instructions too.
   FewStages<D> ahead(start);
-  bool more = false;
-  int page_next = 0;
-  auto fetch_page = [&]() {  // the page numbers of the stage the cursor stands on
-    if (more && lane < C::PIECES) {
-      const int tok = ahead.s * KT + lane * 16;
-      page_next = tok < ahead.it.lk
-                      ? __ldg(p.table + (size_t)ahead.it.doc * p.width + (tok >> p.log2_page))
-                      : 0;
-    }
-  };
-  auto settle = [&]() {  // on to an item that has a stage for this warp
-    more = true;
-    bool fresh = false;
-    while (ahead.s >= ahead.it.s1) {
-      fresh = true;
-      if (!ahead.item(warp)) {
-        more = false;
-        break;
-      }
-    }
-    fetch_page();
-    if (fresh && more) {  // its queries (a row per two lanes) and bias table rows, towards L1
-      const FewItem &it = ahead.it;
-      const int r = lane >> 1, q = r / p.group;
-      if (q < it.lq && (D == 128 || (lane & 1) == 0))
-        prefetch_l1(p.q + ((size_t)(it.sq + q) * p.hq + it.hk * p.group + (r - q * p.group)) * D +
-                    (lane & 1) * 64);
-      if (p.bias.table != nullptr)
-        for (int b = lane; b < p.bias.nb; b += 32)
-          prefetch_l1(p.bias.table + (size_t)b * p.hq + it.hk * p.group);
-      if (p.bias.slopes != nullptr && lane == 0) prefetch_l1(p.bias.slopes + it.hk * p.group);
-    }
-  };
-  auto issue = [&](int slot) {  // the cursor's stage into `slot`; the cursor moves on
-    const int tok = ahead.s * KT + lane * 16;
-    const int pieces = min(C::PIECES, (ahead.it.lk - ahead.s * KT + 15) >> 4);
-    uint8_t *dst = ring + slot * C::STAGE + lane * C::PIECE;
-    if (lane == 0) mbar_arrive_expect_tx(full + slot, pieces * C::DB * 2 * C::PIECE);
-    __syncwarp();
-    if (lane < pieces) {
-      int page = page_next;
-      if ((unsigned)page >= (unsigned)p.num_pages) {
-        atomicOr(p.err, FAT_DEVERR_PAGES);
-        page = p.num_pages;  // just outside: filled with zeros
-      }
-      const int in = tok & ((1 << p.log2_page) - 1), hk = ahead.it.hk;
-      const int c1 = p.head_outer ? in : hk, c2 = p.head_outer ? hk : in;
-#pragma unroll
-      for (int b = 0; b < C::DB; ++b) {
-        tma_load_4d(&tm_k, full + slot, dst + b * C::BLK, 64 * b, c1, c2, page);
-        tma_load_4d(&tm_v, full + slot, dst + C::TILE + b * C::BLK, 64 * b, c1, c2, page);
-      }
-    }
-    ahead.s += ahead.step;
-    settle();
-  };
   ahead.it.s1 = 0;
-  settle();
-  int issued = 0;  // stages whose copies were started
-  bool live = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
+  bool more = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
+  bool primed = false;               // the cursor stands on a stage
+  int page_next = 0, issued = 0, done = 0, slot_in = 0;
+  auto fill = [&]() {
+    while (more && (!primed || issued - done < kRing)) {
+      if (primed) {  // the cursor's stage into the ring
+        const int tok = ahead.s * KT + lane * 16;
+        const int pieces = min(C::PIECES, (ahead.it.lk - ahead.s * KT + 15) >> 4);
+        uint64_t *bar = full + slot_in;
+        uint8_t *dst = ring + slot_in * C::STAGE + lane * C::PIECE;
+        if (lane == 0) mbar_arrive_expect_tx(bar, pieces * C::DB * 2 * C::PIECE);
+        __syncwarp();
+        if (lane < pieces) {
+          int page = page_next;
+          if ((unsigned)page >= (unsigned)p.num_pages) {
+            atomicOr(p.err, FAT_DEVERR_PAGES);
+            page = p.num_pages;  // just outside: filled with zeros
+          }
+          const int in = tok & ((1 << p.log2_page) - 1), hk = ahead.it.hk;
+          const int c1 = p.head_outer ? in : hk, c2 = p.head_outer ? hk : in;
 #pragma unroll
-  for (int i = 0; i < kRing; ++i)
-    if (more && live) {
-      issue(i);
-      ++issued;
+          for (int b = 0; b < C::DB; ++b) {
+            tma_load_4d(&tm_k, bar, dst + b * C::BLK, 64 * b, c1, c2, page);
+            tma_load_4d(&tm_v, bar, dst + C::TILE + b * C::BLK, 64 * b, c1, c2, page);
+          }
+        }
+        ++issued;
+        slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
+        ahead.s += ahead.step;
+      }
+      primed = true;
+      bool fresh = false;
+      while (ahead.s >= ahead.it.s1) {  // on to an item that has a stage for this warp
+        fresh = true;
+        if (!ahead.item(warp)) {
+          more = false;
+          break;
+        }
+      }
+      if (!more) break;
+      const FewItem &it = ahead.it;
+      if (lane < C::PIECES) {  // the page numbers of the stage the cursor stands on
+        const int tok = ahead.s * KT + lane * 16;
+        page_next =
+            tok < it.lk ? __ldg(p.table + (size_t)it.doc * p.width + (tok >> p.log2_page)) : 0;
+      }
+      if (fresh) {  // its queries (a row per two lanes) and bias table rows, towards L1
+        const int r = lane >> 1, q = r / p.group;
+        if (q < it.lq && (D == 128 || (lane & 1) == 0))
+          prefetch_l1(p.q +
+                      ((size_t)(it.sq + q) * p.hq + it.hk * p.group + (r - q * p.group)) * D +
+                      (lane & 1) * 64);
+        if (p.bias.table != nullptr)
+          for (int b = lane; b < p.bias.nb; b += 32)
+            prefetch_l1(p.bias.table + (size_t)b * p.hq + it.hk * p.group);
+        if (p.bias.slopes != nullptr && lane == 0) prefetch_l1(p.bias.slopes + it.hk * p.group);
+      }
     }
+  };
 
   // ---- computation
   FewStages<D> cur(start);
@@ -260,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int r0 = lane >> 2, r1 = r0 + 8;  // this thread's rows, keys 2 (lane % 4) + {0, 1} + 8 t
   const bool t5 = p.bias.table != nullptr;
   const bool biased = p.bias.has_bias != 0;
-  // bucket of every near delta, one byte each (the first copies are on their way)
+  // bucket of every near delta, one byte each
   uint8_t *lut = sm + C::OFF_LUT;
   const int span = p.bias.sat_neg + p.bias.sat_pos;
   if (t5) {
@@ -269,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
   }
   const int bucket_pos = t5 ? lut[span] : 0, bucket_neg = t5 ? lut[0] : 0;
-  int done = 0;           // stages computed
   int slot = 0, phase = 0;
   bool ok = true;
   while (cur.item(warp)) {
@@ -278,43 +266,47 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool mine = !shortened || ((cur.shorts - 1) & (kWarps - 1)) == warp;
     if (!mine) continue;
     const int rows = it.lq * G, shift = it.lk - it.lq;
-    // Q as the A operand: rows r0, r1, channels 16 kk + 2 (lane % 4) + {0, 1} and + 8
     uint32_t qf[D / 16][4];
-    {
-      const __nv_bfloat16 *qb = p.q + ((size_t)it.sq * p.hq + (size_t)it.hk * G) * D;
-      const int q0 = r0 / G, q1 = r1 / G;
-      const uint32_t *a = reinterpret_cast<const uint32_t *>(
-          qb + ((size_t)q0 * p.hq + (r0 - q0 * G)) * D) + (lane & 3);
-      const uint32_t *b = reinterpret_cast<const uint32_t *>(
-          qb + ((size_t)q1 * p.hq + (r1 - q1 * G)) * D) + (lane & 3);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        qf[kk][0] = r0 < rows ? __ldg(a + kk * 8) : 0u;
-        qf[kk][1] = r1 < rows ? __ldg(b + kk * 8) : 0u;
-        qf[kk][2] = r0 < rows ? __ldg(a + kk * 8 + 4) : 0u;
-        qf[kk][3] = r1 < rows ? __ldg(b + kk * 8 + 4) : 0u;
-      }
-    }
-    // per row: query position among the keys, last visible key, bias constants
     int qpos[2], lim[2], head[2];
     float slope[2], far_pos[2], far_neg[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = i ? r1 : r0, q = r / G;
-      qpos[i] = q + shift;
-      head[i] = it.hk * G + (r - q * G);
-      lim[i] = p.causal ? min(qpos[i], it.lk - 1) : it.lk - 1;
-      slope[i] = p.bias.slopes ? __ldg(p.bias.slopes + head[i]) * kLog2e : 0.f;
-      far_pos[i] = t5 ? __ldg(p.bias.table + (size_t)bucket_pos * p.hq + head[i]) * kLog2e : 0.f;
-      far_neg[i] = t5 ? __ldg(p.bias.table + (size_t)bucket_neg * p.hq + head[i]) * kLog2e : 0.f;
-    }
     const int lim_all = p.causal ? min(shift, it.lk - 1) : it.lk - 1;  // every row sees up to here
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[D / 8][4];
 #pragma unroll
     for (int t = 0; t < D / 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 
-    for (int s = cur.s; s < it.s1; s += cur.step) {
+    for (int s = cur.s;; s += cur.step) {
+      fill();
+      if (s >= it.s1) break;
+      if (s == cur.s) {  // the item's first stage here
+        // Q as the A operand: rows r0, r1, channels 16 kk + 2 (lane % 4) + {0, 1} and + 8
+        const __nv_bfloat16 *qb = p.q + ((size_t)it.sq * p.hq + (size_t)it.hk * G) * D;
+        const int q0 = r0 / G, q1 = r1 / G;
+        const uint32_t *a = reinterpret_cast<const uint32_t *>(
+            qb + ((size_t)q0 * p.hq + (r0 - q0 * G)) * D) + (lane & 3);
+        const uint32_t *b = reinterpret_cast<const uint32_t *>(
+            qb + ((size_t)q1 * p.hq + (r1 - q1 * G)) * D) + (lane & 3);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qf[kk][0] = r0 < rows ? __ldg(a + kk * 8) : 0u;
+          qf[kk][1] = r1 < rows ? __ldg(b + kk * 8) : 0u;
+          qf[kk][2] = r0 < rows ? __ldg(a + kk * 8 + 4) : 0u;
+          qf[kk][3] = r1 < rows ? __ldg(b + kk * 8 + 4) : 0u;
+        }
+        // per row: query position among the keys, last visible key, bias constants
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = i ? r1 : r0, q = r / G;
+          qpos[i] = q + shift;
+          head[i] = it.hk * G + (r - q * G);
+          lim[i] = p.causal ? min(qpos[i], it.lk - 1) : it.lk - 1;
+          slope[i] = p.bias.slopes ? __ldg(p.bias.slopes + head[i]) * kLog2e : 0.f;
+          far_pos[i] =
+              t5 ? __ldg(p.bias.table + (size_t)bucket_pos * p.hq + head[i]) * kLog2e : 0.f;
+          far_neg[i] =
+              t5 ? __ldg(p.bias.table + (size_t)bucket_neg * p.hq + head[i]) * kLog2e : 0.f;
+        }
+      }
       if (ok) ok = warp_wait(full + slot, phase, wd);
       if (ok) {
         const uint8_t *kt = ring + slot * C::STAGE;
@@ -440,11 +432,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         // the stage has been read (and its zeros written): its place is free for the next copy
         fence_proxy_async_smem();
         __syncwarp();
-        if (more && live) {
-          issue(slot);
-          ++issued;
-        }
         ++done;
+      } else {
+        more = false;  // a wait ran out: nothing more is copied
       }
       if (++slot == kRing) {
         slot = 0;

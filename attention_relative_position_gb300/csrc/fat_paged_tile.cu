@@ -34,6 +34,16 @@ constexpr int kMinShare = 4;  // cost units (a key tile of one Q tile) a CTA tak
 // partial rows. A CTA with fewer units than this takes blocks of one.
 constexpr int kPairShare = 64;
 
+struct TileItem {
+  int doc, hk, row0;      // row0: token of q and out
+  int q0, ntok, tiles;    // tokens of the request, tiles (0: the end of the list)
+  int lk, shift;          // shift: key position of the request's first query
+  int j0, j1;             // key tiles taken here: key tile nkv - 1 - j for j in [j0, j1)
+  int nkv;
+  int begins, ends;
+};
+// The producer walks the share and hands its items to the other roles through this ring.
+constexpr int kItems = 4;
 template <int D>
 struct TileCfg {
   static constexpr int DB = D / 64;
@@ -45,10 +55,11 @@ struct TileCfg {
   static constexpr int OFF_V = OFF_K + NS * TILE;
   static constexpr int OFF_BAR = OFF_V + NS * TILE;
   static constexpr int OFF_STATS = OFF_BAR + 512;            // float2 [128]
-  static constexpr int OFF_SHARE = OFF_STATS + 1024;
+  static constexpr int OFF_ITEMS = OFF_STATS + 1024;
+  static constexpr int OFF_SHARE = OFF_ITEMS + ((kItems * (int)sizeof(TileItem) + 15) & ~15);
   static constexpr int OFF_THR = OFF_SHARE + (int)sizeof(ShareSmem<kThreads>);
   static constexpr int OFF_LUT = OFF_THR + kMaxThresholds * 4;
-  static_assert((2 + 4 * NS + 15) * 8 + 64 <= 512, "barrier block");
+  static_assert((2 + 4 * NS + 14 + 2 * kItems) * 8 + 8 <= 448, "barrier block");
   static_assert(OFF_LUT + kMaxBiasSpan + 512 + 1024 <= kSmemLimit, "shared memory");
   static constexpr int REG_SM = 216, REG_OTHER = 72;
   static constexpr int REGS_NEEDED = 256 * REG_SM + 128 * REG_OTHER;
@@ -64,48 +75,6 @@ struct TileCfg {
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
 };
 
-// One block of queries of a request: tokens [q0, q0 + ntok), one or two tiles, the key tiles that
-// its rows see, its cost in (Q tile, key tile) pairs.
-struct TileBlock {
-  int q0, ntok, nkv, tiles, cost;
-};
-__device__ __forceinline__ TileBlock tile_block(const PagedDoc &d, int b, int tq, int blk,
-                                                int causal) {
-  TileBlock t;
-  t.q0 = b * blk;
-  t.ntok = min(d.lq - t.q0, blk);
-  t.tiles = t.ntok > tq ? 2 : 1;
-  t.nkv = (d.lk + 127) >> 7;
-  if (causal) {
-    const int last = d.lk - d.lq + t.q0 + t.ntok - 1;  // key position of the last row
-    t.nkv = last < 0 ? 0 : min(t.nkv, (last >> 7) + 1);
-  }
-  t.cost = max(1, t.tiles * t.nkv);
-  return t;
-}
-__device__ __forceinline__ long long tile_head_cost(const PagedDoc &d, int tq, int blk,
-                                                    int causal) {
-  long long c = 0;
-  for (int b = 0; b * blk < d.lq; ++b) c += tile_block(d, b, tq, blk, causal).cost;
-  return c;
-}
-struct TileCost {
-  const PagedParams &p;
-  int tq, blk;  // tokens per tile and per block
-  __device__ long long operator()(const PagedDoc &d) const {
-    return (long long)d.lq * p.group <= p.few_rows ? 0
-                                                   : p.hkv * tile_head_cost(d, tq, blk, p.causal);
-  }
-};
-
-struct TileItem {
-  int doc, hk, row0;      // row0: token of q and out
-  int q0, ntok, tiles;    // tokens of the request, tiles
-  int lk, shift;          // shift: key position of the request's first query
-  int j0, j1;             // key tiles taken here: key tile nkv - 1 - j for j in [j0, j1)
-  int nkv;
-  bool begins, ends;
-};
 struct TileWalk {
   const PagedParams &p;
   const ShareSmem<kThreads> &sm;
@@ -169,14 +138,15 @@ struct TileWalk {
     }
     return false;
   }
-  // key tiles of `it` that Q tile t multiplies: first, step (both tiles every one, or alternating)
-  static __device__ int first(const TileItem &it, int t) { return it.tiles == 2 ? 0 : t; }
-  static __device__ int step(const TileItem &it) { return it.tiles == 2 ? 1 : 2; }
-  static __device__ int count(const TileItem &it, int t) {
-    const int n = it.j1 - it.j0;
-    return it.tiles == 2 ? n : (n + 1 - t) >> 1;
-  }
 };
+// Positions j0 + first, j0 + first + step, ... of an item that Q tile t multiplies: both tiles every
+// one, or (a single tile, shared) alternating.
+__device__ __forceinline__ int item_first(const TileItem &it, int t) { return it.tiles == 2 ? 0 : t; }
+__device__ __forceinline__ int item_step(const TileItem &it) { return it.tiles == 2 ? 1 : 2; }
+__device__ __forceinline__ int item_count(const TileItem &it, int t) {
+  const int n = it.j1 - it.j0;
+  return it.tiles == 2 ? n : (n + 1 - t) >> 1;
+}
 
 // The S row from tensor memory as logits x (log2 units, relative to the row's reference maximum when
 // FOLD), masked; returns the row's maximum.
@@ -254,7 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *mma_done = o_free + 2;
   uint64_t *merge_ready = mma_done + 2;
   uint64_t *tail = merge_ready + 1;  // a last tile's values have arrived (before they are zeroed)
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
+  uint64_t *item_full = tail + 1;    // [kItems] each
+  uint64_t *item_empty = item_full + kItems;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(item_empty + kItems);
+  TileItem *items = reinterpret_cast<TileItem *>(sm + C::OFF_ITEMS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   Watchdog *wdp = reinterpret_cast<Watchdog *>(sm + C::OFF_BAR + 448);
   int *thr_s = reinterpret_cast<int *>(sm + C::OFF_THR);
@@ -264,11 +237,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = tid; i < p.bias.n_thr; i += kThreads) thr_s[i] = p.bias.thr[i];
   TileCost cost{p, tq, 2 * tq};
   const Share share = share_find<kThreads>(
-      p, kMinShare, cost,
-      [&](long long total) {
-        if (total >= (long long)kPairShare * gridDim.x) return false;
-        cost.blk = tq;
-        return true;
+      p, kMinShare, cost, FewCost<D>{p},
+      [&](long long mine, long long other, bool *again) {
+        const int ctas = tile_sms<D>(p, mine, other);
+        if (mine < (long long)kPairShare * ctas) {
+          cost.blk = tq;
+          *again = true;
+        }
+        return ctas;
       },
       share_s);
   if (share.lo >= share.hi) return;
@@ -292,6 +268,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(merge_ready, 128);
     mbar_init(tail, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(item_full + i, 1);
+      mbar_init(item_empty + i, 11);  // eight softmax warps, two issuers, the tail warp
+    }
     *abort_flag = 0;
     *wdp = Watchdog{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
     fence_mbar_init();
@@ -318,6 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const Watchdog &wd = *wdp;
   if (warp >= kWarpProd) regs_dec<C::REG_OTHER>();
+  // item i of the list, for the roles that read it (a whole warp, or the issuers' threads alone)
+  auto item_wait = [&](int i) {
+    return mbar_wait(item_full + (i & (kItems - 1)), (i / kItems) & 1, wd);
+  };
+  auto item_done = [&](int i) { mbar_arrive(item_empty + (i & (kItems - 1))); };
 
   if (warp == kWarpProd) {
     // ------------------------------------------------------------------ producer
@@ -328,7 +313,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ni = 0;          // items with keys
     uint32_t last_tail = 0;
     bool any_tail = false, ok = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
-    while (ok && walk.next(it)) {
+    for (int i = 0; ok; ++i) {
+      const bool last = !walk.next(it);
+      if (i >= kItems) {
+        ok = warp_wait(item_empty + (i & (kItems - 1)), (i / kItems - 1) & 1, wd);
+        if (!ok) break;
+      }
+      if (last) it.tiles = 0;
+      if (lane == 0) {
+        items[i & (kItems - 1)] = it;
+        mbar_arrive(item_full + (i & (kItems - 1)));
+      }
+      if (last) break;
       const int n = it.j1 - it.j0;
       if (n == 0) continue;
       // this lane's page of key tile kt (the next one's is fetched while this one's copies go out)
@@ -414,15 +410,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t aP = C::SEP_P ? tmem + C::COL_P + 64 * t : dS;
       const uint64_t dKd = sw128_desc(smem_u32(sK), 16, 1024);
       const uint64_t dVd = sw128_desc(smem_u32(sV), C::BLK, 1024);
-      TileWalk walk(p, share_s, cost, share);
-      TileItem it;
       uint32_t J = 0, g = 0;  // stream position, this tile's steps
       int ni = 0, act = 0;    // items with keys, those in which this tile has steps
       bool ok = true;
-      while (ok && walk.next(it)) {
+      for (int i = 0; ok; ++i) {
+        if (!(ok = item_wait(i))) break;
+        const TileItem it = items[i & (kItems - 1)];
+        item_done(i);
+        if (it.tiles == 0) break;
         const int n = it.j1 - it.j0;
         if (n == 0) continue;
-        const int first = TileWalk::first(it, t), step = TileWalk::step(it);
+        const int first = item_first(it, t), step = item_step(it);
         if (first >= n) {  // one key tile: the other issuer's; Q is released without being used
           if (!(ok = mbar_wait(q_full, ni & 1, wd))) break;
           mbar_arrive(q_empty);
@@ -492,11 +490,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpTail) {
     // ------------------------------------------------------------------ values behind the last key
-    TileWalk walk(p, share_s, cost, share);
-    TileItem it;
     uint32_t J = 0;
     int nt = 0;
-    while (walk.next(it)) {
+    for (int i = 0;; ++i) {
+      if (!__all_sync(0xffffffffu, item_wait(i))) break;
+      const TileItem it = items[i & (kItems - 1)];
+      __syncwarp();
+      if (lane == 0) item_done(i);
+      if (it.tiles == 0) break;
       const int n = it.j1 - it.j0;
       if (n == 0) continue;
       const int kt = it.nkv - 1 - it.j0;
@@ -505,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nt;
         const int s = J & (C::NS - 1), row = it.lk - kt * 128;
         for (int b = 0; b < C::DB; ++b)
-          for (int i = row * 8 + lane; i < 128 * 8; i += 32)
-            *reinterpret_cast<uint4 *>(sV + s * C::TILE + b * C::BLK + i * 16) =
+          for (int k = row * 8 + lane; k < 128 * 8; k += 32)
+            *reinterpret_cast<uint4 *>(sV + s * C::TILE + b * C::BLK + k * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
         __syncwarp();
@@ -526,12 +527,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2 *stats = reinterpret_cast<float2 *>(sm + C::OFF_STATS);
     const int rq = r / G, rg = r - rq * G;  // token and head of this row within the tile
     const bool has_slopes = p.bias.slopes != nullptr, has_table = p.bias.table != nullptr;
-    TileWalk walk(p, share_s, cost, share);
-    TileItem it;
     uint32_t g = 0, g_other = 0;  // steps of this tile and of the other one
     int merges = 0;
     bool ok = true;
-    while (walk.next(it)) {
+    // The first round is a rehearsal on whatever tensor memory holds, without a barrier and without
+    // a result: it brings the loop's instructions in while the first queries and keys are on their
+    // way (5 us of instruction fetches otherwise). Its P goes where O will be (the first P V
+    // overwrites it, after this warpgroup's first P).
+    for (int n_item = -1;; ++n_item) {
+      const bool live = n_item >= 0;
+      TileItem it{0, 0, 0, 0, tq, 2, 255, 1 << 20, 0, 2, 2, 1, 1};
+      if (live) {
+        if (ok) ok = __all_sync(0xffffffffu, item_wait(n_item));
+        if (!ok) break;
+        it = items[n_item & (kItems - 1)];
+        __syncwarp();
+        if (lane == 0) item_done(n_item);
+        if (it.tiles == 0) break;
+      }
       const int t_row = it.tiles == 2 ? t : 0;           // which tile's rows
       const int ntok = min(it.ntok - t_row * tq, tq);    // its tokens
       const bool valid = rq < ntok && r < RT;
@@ -547,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         rec->hk = it.hk;
         rec->rows = it.ntok * G;
       }
-      const int steps = TileWalk::count(it, t), steps_other = TileWalk::count(it, 1 - t);
+      const int steps = item_count(it, t), steps_other = item_count(it, 1 - t);
       if (it.nkv == 0) {  // no key for any row
         if (valid && (it.tiles == 2 || t == 0)) {
           uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)row * p.hq + h) * D);
@@ -571,10 +584,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < steps; ++i) {
         const uint32_t gi = g + i;
-        if (ok) ok = warp_wait(s_full + t, gi & 1, wd);
-        if (!ok) break;
-        tc_fence_after();
-        const int jj = TileWalk::first(it, t) + i * TileWalk::step(it);
+        if (live) {
+          if (ok) ok = warp_wait(s_full + t, gi & 1, wd);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const int jj = item_first(it, t) + i * item_step(it);
         const int ks = 128 * (it.nkv - 1 - it.j0 - jj);
         const bool need_mask = ks + 128 > it.lk || (p.causal && ks + 127 > pos_lo);
         const int lim = min(it.lk - ks, p.causal ? qpos - ks + 1 : 128);
@@ -607,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mx = FAT_TILE_LOGITS(2, true);
 #undef FAT_TILE_LOGITS
-        if (C::SEP_P) {  // S is in registers: the next one may be computed
+        if (C::SEP_P && live) {  // S is in registers: the next one may be computed
           tc_fence_before();
           mbar_arrive(s_free + t);
         }
@@ -618,13 +633,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const bool fresh = m == -INFINITY;  // no key of this row so far
           const bool need = fresh ? mx != -INFINITY : mx > (FOLD ? 0.f : m) + 32.0f;
-          if (C::SEP_P) {  // P and O are still read by the previous P V
+          if (C::SEP_P && live) {  // P and O are still read by the previous P V
             ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
             if (!ok) break;
             tc_fence_after();
           }
           if (__any_sync(0xffffffffu, need)) {
-            if (!C::SEP_P) {
+            if (!C::SEP_P && live) {
               ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
               if (!ok) break;
               tc_fence_after();
@@ -648,13 +663,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum2[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum2[k] = f2_pack(0.f, 0.f);
+        const uint32_t to = live ? tP : tO;
         if (!FOLD) {
           const float m_use = m == -INFINITY ? 0.f : m;
-          fwd_exp_pass<true>(x, f2_pack(m_use, m_use), tP, sum2);
-        } else if (__any_sync(0xffffffffu, sub != 0.f)) {
-          fwd_exp_pass<true>(x, f2_pack(sub, sub), tP, sum2);
+          fwd_exp_pass<true>(x, f2_pack(m_use, m_use), to, sum2);
+        } else if (live ? __any_sync(0xffffffffu, sub != 0.f) : i == 0) {
+          fwd_exp_pass<true>(x, f2_pack(sub, sub), to, sum2);
         } else {
-          fwd_exp_pass<false>(x, 0, tP, sum2);
+          fwd_exp_pass<false>(x, 0, to, sum2);
         }
         {
           float s0, s1, s2, s3;
@@ -664,8 +680,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(p_ready + t);
+        if (live) mbar_arrive(p_ready + t);
       }
+      if (!live) continue;
       // ---- the item's rows
       g += steps;
       g_other += steps_other;
@@ -693,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = M;
         }
       }
-      if (!ok) continue;  // nothing more is waited for: the walk ends quickly
+      if (!ok) continue;
       tc_fence_after();
       const float inv = whole ? (l > 0.f ? 1.0f / l : 0.f) : 1.f;
       f0 *= inv;
