@@ -3,11 +3,10 @@
 //
 // The work is one read of the requests' keys and values; the rows ride along. A CTA (two per SM)
 // takes an equal share of all key stages (fat_paged.cuh); a stage is 8 KB of keys and values (16
-// tokens at head_dim 128, 32 at 64). Four warps work on their own, each with a ring of three
-// stages that it fills by TMA itself (pages of 16 tokens and more come as boxes of 16 rows x 64
-// channels, 128-byte swizzle) and waits for: no producer warp and no hand-off between warps, the
-// next stages' copies and their page numbers are always in flight. Per stage and warp: S = Q K^T
-// for 16 rows with warp-level matrix products (Q in registers), bias and mask, a running maximum
+// tokens at head_dim 128, 32 at 64). Four warps compute, each on stages of its own from a ring of
+// three; a fifth warp fills the four rings, one lane per ring, by TMA (boxes of 16 rows x 64
+// channels, 128-byte swizzle: pages of 16 tokens and more are made of them), with the next stage's
+// page numbers already on their way. Per stage and warp: S = Q K^T for 16 rows with warp-level matrix products (Q in registers), bias and mask, a running maximum
 // that moves only when it grows by more than 2^32, P as bf16 in registers, O += P V. Warp-level
 // products suffice here: with 16 of 128 rows of a tcgen05 tile filled, its round trip through
 // tensor memory would cost more than the 64 products of a stage.
@@ -21,7 +20,8 @@
 namespace fat {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kWarps = 4;          // computing warps
+constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kRing = 3;           // stages per warp
 constexpr int kShortStages = 2;    // items of at most this many stages are one warp's
 constexpr int kMinShare = 8;       // stages a CTA takes at least
@@ -40,7 +40,7 @@ struct FewCfg {
   static constexpr int OFF_MERGE = kWarps * kRing * STAGE;
   static constexpr int OFF_STATS = OFF_MERGE + kWarps * kFewRows * kOStride * 4;
   static constexpr int OFF_BAR = OFF_STATS + (kWarps + 1) * kFewRows * 2 * 4;
-  static constexpr int OFF_THR = OFF_BAR + kWarps * kRing * 8 + 64;
+  static constexpr int OFF_THR = OFF_BAR + 2 * kWarps * kRing * 8 + 64;
   static constexpr int OFF_SHARE = OFF_THR + kMaxThresholds * 4;
   static constexpr int OFF_LUT = OFF_SHARE + (int)sizeof(ShareSmem<kThreads>);
   // bucket bytes of the deltas -sat_neg .. sat_pos
@@ -142,16 +142,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto &share_s = *reinterpret_cast<ShareSmem<kThreads> *>(sm + C::OFF_SHARE);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR) + warp * kRing;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);  // full, then empty, [warp][ring]
   volatile int *abort_flag =
-      reinterpret_cast<volatile int *>(sm + C::OFF_BAR + kWarps * kRing * 8);
+      reinterpret_cast<volatile int *>(sm + C::OFF_BAR + 2 * kWarps * kRing * 8);
   int *thr_s = reinterpret_cast<int *>(sm + C::OFF_THR);
   float *stats = reinterpret_cast<float *>(sm + C::OFF_STATS);  // [warps + 1][16][2]
   grid_dep_launch();
   if (tid == 0) *abort_flag = 0;
-  if (lane == 0) {
-    for (int i = 0; i < kRing; ++i) mbar_init(full + i, 1);
+  if (tid < 2 * kWarps * kRing) {
+    mbar_init(bars + tid, 1);
     fence_mbar_init();
+  }
+  if (tid == kWarps * 32) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
@@ -176,72 +178,109 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int cost0 = max(1, (d0.lk + KT - 1) / KT);
   const FewWalk<D> start{p, share_s, sh.doc, sh.doc, (int)(sh.off / cost0), sh.hi - sh.lo,
                          (int)(sh.off % cost0)};
-  uint8_t *ring = sm + warp * kRing * C::STAGE;
 
-  // ---- copies: a cursor ahead of the computation. Lane i < PIECES holds the page of piece i. The
-  // code is kept to one place (fill, at the top of a stage's turn): a short call is bound by the
-  // latency of its first instructions too.
-  FewStages<D> ahead(start);
-  ahead.it.s1 = 0;
-  bool more = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
-  bool primed = false;               // the cursor stands on a stage
-  int page_next = 0, issued = 0, done = 0, slot_in = 0;
-  auto fill = [&]() {
-    while (more && (!primed || issued - done < kRing)) {
-      if (primed) {  // the cursor's stage into the ring
-        const int tok = ahead.s * KT + lane * 16;
-        const int pieces = min(C::PIECES, (ahead.it.lk - ahead.s * KT + 15) >> 4);
-        uint64_t *bar = full + slot_in;
-        uint8_t *dst = ring + slot_in * C::STAGE + lane * C::PIECE;
-        if (lane == 0) mbar_arrive_expect_tx(bar, pieces * C::DB * 2 * C::PIECE);
-        __syncwarp();
-        if (lane < pieces) {
-          int page = page_next;
-          if ((unsigned)page >= (unsigned)p.num_pages) {
-            atomicOr(p.err, FAT_DEVERR_PAGES);
-            page = p.num_pages;  // just outside: filled with zeros
-          }
-          const int in = tok & ((1 << p.log2_page) - 1), hk = ahead.it.hk;
-          const int c1 = p.head_outer ? in : hk, c2 = p.head_outer ? hk : in;
-#pragma unroll
-          for (int b = 0; b < C::DB; ++b) {
-            tma_load_4d(&tm_k, bar, dst + b * C::BLK, 64 * b, c1, c2, page);
-            tma_load_4d(&tm_v, bar, dst + C::TILE + b * C::BLK, 64 * b, c1, c2, page);
-          }
-        }
-        ++issued;
-        slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
-        ahead.s += ahead.step;
-      }
-      primed = true;
-      bool fresh = false;
-      while (ahead.s >= ahead.it.s1) {  // on to an item that has a stage for this warp
-        fresh = true;
-        if (!ahead.item(warp)) {
-          more = false;
+  if (warp == kWarps) {
+    // ------------------------------------------------------------------ producer
+    // Lane w < 4 follows warp w's stages. It never blocks on its own ring: a warp that waits for
+    // the others at the end of an item must not hold up their copies.
+    const int w = lane & (kWarps - 1);
+    uint8_t *ring = sm + w * kRing * C::STAGE;
+    uint64_t *full = bars + w * kRing, *empty = bars + (kWarps + w) * kRing;
+    FewStages<D> ahead(start);
+    ahead.it.s1 = 0;
+    bool more = lane < kWarps && !(p.debug_flags & 1);  // test hook: no copies, the waits run out
+    bool primed = false;  // the cursor stands on a stage
+    int page[C::PIECES], slot = 0, issued = 0, phase = 1;
+    uint64_t t0 = 0;      // when this warp last got a stage off
+    while (__any_sync(0xffffffffu, more)) {
+      const bool can = more && (!primed || issued < kRing || mbar_test(empty + slot, phase));
+      if (!__any_sync(0xffffffffu, can)) {
+        __nanosleep(20);
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (*abort_flag || (long long)(now - t0) > p.timeout_ns) {
+          if (!*abort_flag && lane == 0) atomicOr(p.err, FAT_DEVERR_TIMEOUT_FWD);
+          *abort_flag = 1;
           break;
         }
+        continue;
       }
-      if (!more) break;
-      const FewItem &it = ahead.it;
-      if (lane < C::PIECES) {  // the page numbers of the stage the cursor stands on
-        const int tok = ahead.s * KT + lane * 16;
-        page_next =
-            tok < it.lk ? __ldg(p.table + (size_t)it.doc * p.width + (tok >> p.log2_page)) : 0;
+      t0 = 0;
+      bool fresh = false;
+      if (can) {
+        if (primed) {
+          const int tok = ahead.s * KT, hk = ahead.it.hk;
+          const int pieces = min(C::PIECES, (ahead.it.lk - tok + 15) >> 4);
+          uint8_t *dst = ring + slot * C::STAGE;
+          mbar_arrive_expect_tx(full + slot, pieces * C::DB * 2 * C::PIECE);
+#pragma unroll
+          for (int i = 0; i < C::PIECES; ++i) {
+            if (i >= pieces) break;
+            if ((unsigned)page[i] >= (unsigned)p.num_pages) {
+              atomicOr(p.err, FAT_DEVERR_PAGES);
+              page[i] = p.num_pages;  // just outside: filled with zeros
+            }
+            const int in = (tok + i * 16) & ((1 << p.log2_page) - 1);
+            const int c1 = p.head_outer ? in : hk, c2 = p.head_outer ? hk : in;
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b) {
+              uint8_t *d = dst + i * C::PIECE + b * C::BLK;
+              tma_load_4d(&tm_k, full + slot, d, 64 * b, c1, c2, page[i]);
+              tma_load_4d(&tm_v, full + slot, d + C::TILE, 64 * b, c1, c2, page[i]);
+            }
+          }
+          ++issued;
+          if (++slot == kRing) {
+            slot = 0;
+            phase ^= 1;
+          }
+          ahead.s += ahead.step;
+        }
+        primed = true;
+        while (ahead.s >= ahead.it.s1) {  // on to an item that has a stage for this warp
+          fresh = true;
+          if (!ahead.item(w)) {
+            more = false;
+            break;
+          }
+        }
+        fresh = fresh && more;
+        if (more) {  // the page numbers of the stage the cursor stands on
+#pragma unroll
+          for (int i = 0; i < C::PIECES; ++i) {
+            const int tok = ahead.s * KT + i * 16;
+            page[i] = tok < ahead.it.lk ? __ldg(p.table + (size_t)ahead.it.doc * p.width +
+                                                (tok >> p.log2_page))
+                                        : 0;
+          }
+        }
       }
-      if (fresh) {  // its queries (a row per two lanes) and bias table rows, towards L1
+      // an item's queries (a row per two lanes) and bias table rows, towards L1
+      const unsigned who = __ballot_sync(0xffffffffu, fresh);
+      if (who) {
+        const int src = __ffs(who) - 1;
+        const int sq = __shfl_sync(0xffffffffu, ahead.it.sq, src);
+        const int lq = __shfl_sync(0xffffffffu, ahead.it.lq, src);
+        const int h0 = __shfl_sync(0xffffffffu, ahead.it.hk, src) * p.group;
         const int r = lane >> 1, q = r / p.group;
-        if (q < it.lq && (D == 128 || (lane & 1) == 0))
-          prefetch_l1(p.q +
-                      ((size_t)(it.sq + q) * p.hq + it.hk * p.group + (r - q * p.group)) * D +
+        if (q < lq && (D == 128 || (lane & 1) == 0))
+          prefetch_l1(p.q + ((size_t)(sq + q) * p.hq + h0 + (r - q * p.group)) * D +
                       (lane & 1) * 64);
         if (p.bias.table != nullptr)
           for (int b = lane; b < p.bias.nb; b += 32)
-            prefetch_l1(p.bias.table + (size_t)b * p.hq + it.hk * p.group);
-        if (p.bias.slopes != nullptr && lane == 0) prefetch_l1(p.bias.slopes + it.hk * p.group);
+            prefetch_l1(p.bias.table + (size_t)b * p.hq + h0);
+        if (p.bias.slopes != nullptr && lane == 0) prefetch_l1(p.bias.slopes + h0);
       }
     }
-  };
+    if (*abort_flag) {  // copies may still be on their way: give them time to land
+      const uint64_t a = global_timer_ns();
+      while (global_timer_ns() - a < 1000000ull) __nanosleep(1000);
+    }
+    grid_dep_wait();  // as at the end of the other warps
+    return;
+  }
+  uint8_t *ring = sm + warp * kRing * C::STAGE;
+  uint64_t *full = bars + warp * kRing, *empty = bars + (kWarps + warp) * kRing;
 
   // ---- computation
   FewStages<D> cur(start);
@@ -253,9 +292,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t *lut = sm + C::OFF_LUT;
   const int span = p.bias.sat_neg + p.bias.sat_pos;
   if (t5) {
-    for (int i = tid; i <= span; i += kThreads)
+    for (int i = tid; i <= span; i += kWarps * 32)
       lut[i] = (uint8_t)t5_bucket_staged(i - p.bias.sat_neg, p.bias, thr_s);
-    __syncthreads();
+    named_bar_sync(1, kWarps * 32);
   }
   const int bucket_pos = t5 ? lut[span] : 0, bucket_neg = t5 ? lut[0] : 0;
   int slot = 0, phase = 0;
@@ -275,9 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int t = 0; t < D / 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 
-    for (int s = cur.s;; s += cur.step) {
-      fill();
-      if (s >= it.s1) break;
+    for (int s = cur.s; s < it.s1; s += cur.step) {
       if (s == cur.s) {  // the item's first stage here
         // Q as the A operand: rows r0, r1, channels 16 kk + 2 (lane % 4) + {0, 1} and + 8
         const __nv_bfloat16 *qb = p.q + ((size_t)it.sq * p.hq + (size_t)it.hk * G) * D;
@@ -319,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             *reinterpret_cast<uint4 *>(vt + (c >> 3) * C::BLK + row * 128 + (c & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
+          fence_proxy_async_smem();  // before the next copy into this place
           __syncwarp();
         }
         // S = Q K^T
@@ -429,12 +467,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             mma_16x8x16(o[t + 1], pf, b[2], b[3]);
           }
         }
-        // the stage has been read (and its zeros written): its place is free for the next copy
-        fence_proxy_async_smem();
-        __syncwarp();
-        ++done;
-      } else {
-        more = false;  // a wait ran out: nothing more is copied
+        __syncwarp();  // the stage has been read: its place is free for the next copy
+        if (lane == 0) mbar_arrive(empty + slot);
       }
       if (++slot == kRing) {
         slot = 0;
@@ -492,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       *reinterpret_cast<float2 *>(stats + (warp * kFewRows + r0) * 2) = make_float2(m[0], l[0]);
       *reinterpret_cast<float2 *>(stats + (warp * kFewRows + r1) * 2) = make_float2(m[1], l[1]);
     }
-    __syncthreads();
+    named_bar_sync(1, kWarps * 32);
     float f[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -525,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         *reinterpret_cast<float2 *>(dst + r1 * kOStride) =
             make_float2(o[ot][2] * f[1], o[ot][3] * f[1]);
       }
-      __syncthreads();
-      static_assert(kFewRows * kMergeCh / 4 == kThreads, "one quad of channels per thread");
+      named_bar_sync(1, kWarps * 32);
+      static_assert(kFewRows * kMergeCh / 4 == kWarps * 32, "one quad of channels per thread");
       const int r = whole ? tid / (kMergeCh / 4) : tid % kFewRows;
       const int c = 4 * (whole ? tid % (kMergeCh / 4) : tid / kFewRows);
       if (r < rows) {
@@ -558,12 +592,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 make_float2(M, L);
         }
       }
-      __syncthreads();  // buf (and, after the last block, stats) are written again
+      named_bar_sync(1, kWarps * 32);  // buf (and, after the last block, stats) are written again
     }
-  }
-  // copies that were started and not waited for (after a timeout) land before the block exits
-  for (; done < issued; ++done) {
-    mbar_wait_teardown(full + done % kRing, (done / kRing) & 1, kTeardownNs);
   }
   // A grid that was started beside the tile kernel's ends after it, so that the merge grids, which
   // wait for this one, find both complete (returns at once when there is none before).
