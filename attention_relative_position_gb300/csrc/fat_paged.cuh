@@ -54,15 +54,18 @@ __device__ __forceinline__ PagedDoc paged_doc(const PagedParams &p, int i) {
 }
 
 // ---- costs --------------------------------------------------------------------------------------
-// Few-row kernel: stages of 8 KB of keys and values for every key/value head.
+// Few-row kernel: stages of 8 KB of keys and values for every key/value head, and kFewItem for the
+// fixed costs of an item (its first loads, the merge of its warps).
 __host__ __device__ constexpr int few_stage_tokens(int d) { return 2048 / d; }
+constexpr int kFewItem = 10;
+__host__ __device__ inline int few_item_cost(int stages) { return stages + kFewItem; }
 template <int D>
 struct FewCost {
   const PagedParams &p;
   __device__ long long operator()(const PagedDoc &d) const {
     if ((long long)d.lq * p.group > p.few_rows) return 0;
     constexpr int KT = few_stage_tokens(D);
-    return (long long)p.hkv * max(1, (d.lk + KT - 1) / KT);
+    return (long long)p.hkv * few_item_cost((d.lk + KT - 1) / KT);
   }
 };
 
@@ -101,14 +104,15 @@ struct TileCost {
 };
 
 // SMs of the tile kernel when a call launches both kernels: in proportion to their times, a pair of
-// tiles weighing as many stages as kPairStages says (1.5 us against 0.18 us of an SM at head_dim
-// 128, measured; half of that at 64), each at least one. The other SMs are the few-row kernel's.
+// tiles weighing kPairStages stages (1.4 us against 0.12 us of an SM at head_dim 128, and its longer start, measured),
+// each kernel at least one. The other SMs are the few-row kernel's.
+constexpr float kPairStages = 16.f;
 template <int D>
 __device__ __forceinline__ int tile_sms(const PagedParams &p, long long tile_total,
                                         long long few_total) {
   if (!p.both || few_total == 0) return p.sms;
   if (tile_total == 0) return 0;
-  const float a = (D == 128 ? 8.f : 4.f) * (float)tile_total, b = (float)few_total;
+  const float a = (D == 128 ? 1.f : 0.5f) * kPairStages * (float)tile_total, b = (float)few_total;
   return min(max((int)(p.sms * (a / (a + b)) + 0.5f), 1), p.sms - 1);
 }
 
@@ -192,11 +196,11 @@ __device__ __forceinline__ long long share_scan(long long v, ShareSmem<NT> &s, l
 
 // Find this CTA's stretch (all NT threads of the block; cost(doc) is the request's cost in this
 // kernel, other(doc) in the other one, 0 for requests that are not theirs; ctas(total, other total)
-// is the number of CTAs that share the line, and may change the cost function once, of which it
-// tells), report corrupt requests once, stage the requests the stretch may hold. Up to NT requests,
-// one per thread, are read once; more are read again to find the stretch's first.
+// is the number of CTAs that share the line), report corrupt requests once, stage the requests the
+// stretch may hold. Up to NT requests, one per thread, are read once; more are read again to find
+// the stretch's first.
 template <int NT, typename CostFn, typename OtherFn, typename CtasFn>
-__device__ __forceinline__ Share share_find(const PagedParams &p, int min_share, CostFn &cost,
+__device__ __forceinline__ Share share_find(const PagedParams &p, int min_share, const CostFn &cost,
                                             const OtherFn &other, CtasFn ctas, ShareSmem<NT> &s) {
   const int tid = threadIdx.x;
   const bool small = p.n <= NT;
@@ -212,20 +216,17 @@ __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share,
     }
     share_scan<NT>(mine, s, &other_total);
   }
-  bool again = true;
-  int G = 0;
-  for (int pass = 0; again; ++pass) {
-    first = d.ok && d.lq > 0 ? cost(d) : 0;
+  first = d.ok && d.lq > 0 ? cost(d) : 0;
+  {
     long long mine = first;
     for (int i = tid + NT; i < p.n; i += NT) {
       const PagedDoc e = paged_doc(p, i);
-      if (pass == 0 && !e.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
+      if (!e.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
       if (e.ok && e.lq > 0) mine += cost(e);
     }
     before = share_scan<NT>(small ? first : mine, s, &total);
-    again = false;
-    if (pass == 0) G = ctas(total, other_total, &again);
   }
+  const int G = ctas(total, other_total);
   if (tid < p.n && !d.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
   r.total = total;
   r.lo = r.hi = r.off = 0;

@@ -35,15 +35,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   __shared__ float sum_s[kMergeWarps][CH + 2][32];
   grid_dep_wait();
   const int c = blockIdx.x;
-  const PartRecord rec = *part_record(p.part, c, 1);
-  if (!rec.valid) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  // parts 1 .. n - 1 lie in CTAs c + 1 .. c + n - 1
+  const PartRecord rec = *part_record(p.part, c, 1);
+  // parts 1 .. n - 1 lie in CTAs c + 1 .. c + n - 1 (the first records are loaded beside rec)
   int n = 1;
   for (int i0 = 1;; i0 += 32) {
     const int i = c + i0 + lane;
-    const unsigned end = __ballot_sync(0xffffffffu, i >= ctas || part_record(p.part, i, 0)->ends ||
-                                                        !part_record(p.part, i, 0)->valid);
+    int2 next = make_int2(0, 0);  // valid, ends
+    if (i < ctas) next = *reinterpret_cast<const int2 *>(part_record(p.part, i, 0));
+    if (!rec.valid) return;
+    const unsigned end = __ballot_sync(0xffffffffu, !next.x || next.y);
     if (end) {
       n = min(i0 + __ffs(end), ctas - c);
       break;

@@ -74,7 +74,7 @@ struct FewWalk {
       }
       constexpr int KT = FewCfg<D>::KT;
       it.nst = (d.lk + KT - 1) / KT;
-      const int cost = max(1, it.nst);
+      const int cost = few_item_cost(it.nst);
       const int o = off;
       off = 0;
       const int take = (int)min(left, (long long)(cost - o));
@@ -95,10 +95,12 @@ struct FewWalk {
         it.begins = it.ends = true;
         return true;
       }
-      it.s0 = min(o, it.nst);
-      it.s1 = min(o + take, it.nst);
-      it.begins = o == 0;
+      // the fixed part of the cost comes first, before the stages
+      it.s0 = max(o - kFewItem, 0);
+      it.s1 = max(o + take - kFewItem, 0);
+      it.begins = it.s0 == 0;
       it.ends = o + take == cost;
+      if (it.s0 == it.s1 && !(it.nst == 0 && it.ends)) continue;  // a boundary before its stages
       return true;
     }
     return false;
@@ -162,10 +164,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     PartRecord *r = part_record(p.part, blockIdx.x, tid);
     r->valid = 0;
   }
-  FewCost<D> cost{p};
+  const FewCost<D> cost{p};
   const Share sh = share_find<kThreads>(
       p, kMinShare, cost, TileCost{p, 128 / p.group, 2 * (128 / p.group)},
-      [&](long long mine, long long other, bool *) {
+      [&](long long mine, long long other) {
         return 2 * (p.sms - (p.both ? tile_sms<D>(p, other, mine) : 0));
       },
       share_s);
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const Watchdog wd{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
   const PagedDoc d0 = share_doc(p, share_s, sh.doc, sh.doc);
-  const int cost0 = max(1, (d0.lk + KT - 1) / KT);
+  const int cost0 = few_item_cost((d0.lk + KT - 1) / KT);
   const FewWalk<D> start{p, share_s, sh.doc, sh.doc, (int)(sh.off / cost0), sh.hi - sh.lo,
                          (int)(sh.off % cost0)};
 

@@ -30,9 +30,6 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kWarpProd = 8, kWarpMma = 9, kWarpTail = 11;
 constexpr int kMinShare = 4;  // cost units (a key tile of one Q tile) a CTA takes at least
-// Blocks of two Q tiles share their key tiles' copies; blocks of one are cut into fewer and smaller
-// partial rows. A CTA with fewer units than this takes blocks of one.
-constexpr int kPairShare = 64;
 
 struct TileItem {
   int doc, hk, row0;      // row0: token of q and out
@@ -235,18 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();
   if (p.split && tid < 2) part_record(p.part, blockIdx.x, tid)->valid = 0;
   for (int i = tid; i < p.bias.n_thr; i += kThreads) thr_s[i] = p.bias.thr[i];
-  TileCost cost{p, tq, 2 * tq};
+  const TileCost cost{p, tq, 2 * tq};
   const Share share = share_find<kThreads>(
       p, kMinShare, cost, FewCost<D>{p},
-      [&](long long mine, long long other, bool *again) {
-        const int ctas = tile_sms<D>(p, mine, other);
-        if (mine < (long long)kPairShare * ctas) {
-          cost.blk = tq;
-          *again = true;
-        }
-        return ctas;
-      },
-      share_s);
+      [&](long long mine, long long other) { return tile_sms<D>(p, mine, other); }, share_s);
   if (share.lo >= share.hi) return;
 
   if (warp == kWarpProd && lane == 0) {
@@ -530,21 +519,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0, g_other = 0;  // steps of this tile and of the other one
     int merges = 0;
     bool ok = true;
-    // The first round is a rehearsal on whatever tensor memory holds, without a barrier and without
-    // a result: it brings the loop's instructions in while the first queries and keys are on their
-    // way (5 us of instruction fetches otherwise). Its P goes where O will be (the first P V
-    // overwrites it, after this warpgroup's first P).
-    for (int n_item = -1;; ++n_item) {
-      const bool live = n_item >= 0;
-      TileItem it{0, 0, 0, 0, tq, 2, 255, 1 << 20, 0, 2, 2, 1, 1};
-      if (live) {
-        if (ok) ok = __all_sync(0xffffffffu, item_wait(n_item));
-        if (!ok) break;
-        it = items[n_item & (kItems - 1)];
+    for (int n_item = 0;; ++n_item) {
+      if (n_item > 0) {  // the item before is read no more
         __syncwarp();
-        if (lane == 0) item_done(n_item);
-        if (it.tiles == 0) break;
+        if (lane == 0) item_done(n_item - 1);
       }
+      if (ok) ok = __all_sync(0xffffffffu, item_wait(n_item));
+      if (!ok) break;
+      const TileItem &it = items[n_item & (kItems - 1)];  // read where it is: registers are short
+      if (it.tiles == 0) break;
       const int t_row = it.tiles == 2 ? t : 0;           // which tile's rows
       const int ntok = min(it.ntok - t_row * tq, tq);    // its tokens
       const bool valid = rq < ntok && r < RT;
@@ -584,11 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < steps; ++i) {
         const uint32_t gi = g + i;
-        if (live) {
-          if (ok) ok = warp_wait(s_full + t, gi & 1, wd);
-          if (!ok) break;
-          tc_fence_after();
-        }
+        if (ok) ok = warp_wait(s_full + t, gi & 1, wd);
+        if (!ok) break;
+        tc_fence_after();
         const int jj = item_first(it, t) + i * item_step(it);
         const int ks = 128 * (it.nkv - 1 - it.j0 - jj);
         const bool need_mask = ks + 128 > it.lk || (p.causal && ks + 127 > pos_lo);
@@ -622,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mx = FAT_TILE_LOGITS(2, true);
 #undef FAT_TILE_LOGITS
-        if (C::SEP_P && live) {  // S is in registers: the next one may be computed
+        if (C::SEP_P) {  // S is in registers: the next one may be computed
           tc_fence_before();
           mbar_arrive(s_free + t);
         }
@@ -633,13 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const bool fresh = m == -INFINITY;  // no key of this row so far
           const bool need = fresh ? mx != -INFINITY : mx > (FOLD ? 0.f : m) + 32.0f;
-          if (C::SEP_P && live) {  // P and O are still read by the previous P V
+          if (C::SEP_P) {  // P and O are still read by the previous P V
             ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
             if (!ok) break;
             tc_fence_after();
           }
           if (__any_sync(0xffffffffu, need)) {
-            if (!C::SEP_P && live) {
+            if (!C::SEP_P) {
               ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
               if (!ok) break;
               tc_fence_after();
@@ -663,14 +644,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum2[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum2[k] = f2_pack(0.f, 0.f);
-        const uint32_t to = live ? tP : tO;
         if (!FOLD) {
           const float m_use = m == -INFINITY ? 0.f : m;
-          fwd_exp_pass<true>(x, f2_pack(m_use, m_use), to, sum2);
-        } else if (live ? __any_sync(0xffffffffu, sub != 0.f) : i == 0) {
-          fwd_exp_pass<true>(x, f2_pack(sub, sub), to, sum2);
+          fwd_exp_pass<true>(x, f2_pack(m_use, m_use), tP, sum2);
+        } else if (__any_sync(0xffffffffu, sub != 0.f)) {
+          fwd_exp_pass<true>(x, f2_pack(sub, sub), tP, sum2);
         } else {
-          fwd_exp_pass<false>(x, 0, to, sum2);
+          fwd_exp_pass<false>(x, 0, tP, sum2);
         }
         {
           float s0, s1, s2, s3;
@@ -680,9 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        if (live) mbar_arrive(p_ready + t);
+        mbar_arrive(p_ready + t);
       }
-      if (!live) continue;
       // ---- the item's rows
       g += steps;
       g_other += steps_other;
