@@ -15,34 +15,33 @@ namespace {
 
 // ---- merge of cut items -------------------------------------------------------------------------
 // A chain is an item's parts in the order of their CTAs: part 1 of the CTA in which it begins, then
-// part 0 of the following ones up to the one in which it ends. One column of blocks per CTA that
-// begins a chain; a task is 32 lanes' rows (16 rows x 2 for the few-row kernel's items) by 16
-// channels, a lane owning one row's 16 channels: every load of a warp is a run of 16-byte quads of
-// consecutive rows, a lane's output one 32-byte sector. Chains of a few parts: a warp per task, the
-// parts' loads in flight together. Long chains (one context over most of the grid): the block's
-// warps share a task's parts and add their sums through shared memory.
-// Reads chain x (D + 2) x 4 bytes per row from L2; bound by the latency of a few dependent loads.
+// part 0 of the following ones up to the one in which it ends. kTileBlocks or kFewBlocks blocks per
+// CTA that begins a chain; a task is 32 lanes' rows (16 rows x 2 for the few-row kernel's items) by
+// kMergeCh channels, a lane owning one row's: every load of a warp is a run of 16-byte quads of
+// consecutive rows. Chains of a few parts: a warp per task, the parts' loads in flight together.
+// Long chains (one context over most of the grid): the block's warps share a task's parts and add
+// their sums through shared memory. Reads chain x (D + 2) x 4 bytes per row from L2; bound by the
+// latency of three dependent loads, so registers are kept to four blocks per SM.
 constexpr int kMergeWarps = 8;
 constexpr int kLongChain = 16;  // parts from which the warps of a block share a task
 constexpr int kMergeBatch = 4;  // parts whose loads a lane has in flight
+constexpr int kMergeCh = 8;
+constexpr int kTileBlocks = 8, kFewBlocks = 2;
 
 template <int ROWS, int D>
-__global__ void __launch_bounds__(kMergeWarps * 32)
-    fat_paged_merge_kernel(const __grid_constant__ PagedParams p, const int ctas) {
+__device__ __forceinline__ void merge_chain(const PagedParams &p, float *part, int ctas, int c,
+                                            int y, int ny, float (*sum_s)[kMergeCh + 2][32]) {
   constexpr int RL = ROWS < 32 ? ROWS : 32;        // rows side by side in a warp
-  constexpr int CH = 16;                           // channels per lane
+  constexpr int CH = kMergeCh;                     // channels per lane
   constexpr int RG = ROWS / RL, CG = D / CH / (32 / RL);  // tasks: row groups x channel groups
-  __shared__ float sum_s[kMergeWarps][CH + 2][32];
-  grid_dep_wait();
-  const int c = blockIdx.x;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const PartRecord rec = *part_record(p.part, c, 1);
+  const PartRecord rec = *part_record(part, c, 1);
   // parts 1 .. n - 1 lie in CTAs c + 1 .. c + n - 1 (the first records are loaded beside rec)
   int n = 1;
   for (int i0 = 1;; i0 += 32) {
     const int i = c + i0 + lane;
     int2 next = make_int2(0, 0);  // valid, ends
-    if (i < ctas) next = *reinterpret_cast<const int2 *>(part_record(p.part, i, 0));
+    if (i < ctas) next = *reinterpret_cast<const int2 *>(part_record(part, i, 0));
     if (!rec.valid) return;
     const unsigned end = __ballot_sync(0xffffffffu, !next.x || next.y);
     if (end) {
@@ -51,8 +50,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     }
   }
   const bool shared = n > kLongChain;
-  const int first = shared ? blockIdx.y : blockIdx.y * kMergeWarps + w;
-  const int step = shared ? gridDim.y : gridDim.y * kMergeWarps;
+  const int first = shared ? y : y * kMergeWarps + w;
+  const int step = shared ? ny : ny * kMergeWarps;
   for (int task = first; task < RG * CG; task += step) {  // the same count for all warps if shared
     const int r = (task / CG) * RL + lane % RL;
     const int q0 = ((task % CG) * (32 / RL) + lane / RL) * (CH / 4);  // first quad of channels
@@ -71,8 +70,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
           if (i < n) {
             const int which = i == 0 ? 1 : 0;
             st[b] = *reinterpret_cast<const float2 *>(
-                part_stats<ROWS, D>(p.part, ctas, c + i, which) + r * 2);
-            float *rows = part_rows<ROWS, D>(p.part, ctas, c + i, which);
+                part_stats<ROWS, D>(part, ctas, c + i, which) + r * 2);
+            float *rows = part_rows<ROWS, D>(part, ctas, c + i, which);
 #pragma unroll
             for (int k = 0; k < CH / 4; ++k) v[b][k] = *part_quad<ROWS>(rows, r, q0 + k);
           }
@@ -102,7 +101,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
       sum_s[w][CH + 1][lane] = l;
       __syncthreads();
       if (w != 0) continue;
-#pragma unroll
       for (int i = 1; i < kMergeWarps; ++i) {
         const float mi = sum_s[i][CH][lane], mn = fmaxf(m, mi);
         const float fo = m == -INFINITY ? 0.f : ex2(m - mn);
@@ -117,22 +115,37 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const float inv = l > 0.f ? 1.0f / l : 0.f;
     const int q = r / p.group, h = rec.hk * p.group + (r - q * p.group);
     const size_t row = (size_t)rec.row0 + q;
-    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (row * p.hq + h) * D + q0 * 4);
-#pragma unroll
-    for (int k = 0; k < CH / 8; ++k)
-      dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
-                          pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                          pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                          pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+    *reinterpret_cast<uint4 *>(p.out + (row * p.hq + h) * D + q0 * 4) =
+        make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                   pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
     if (q0 == 0 && p.lse != nullptr)
       p.lse[(size_t)h * p.total_q + row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
   }
 }
 
-template <int ROWS, int D>
-int launch_merge(const PagedParams &p, int ctas, cudaStream_t stream) {
+// Blocks [0, tile_ctas * kTileBlocks) merge the tile kernel's items, the others the few-row kernel's.
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32, 4)
+    fat_paged_merge_kernel(const __grid_constant__ PagedParams p, float *tile_part, int tile_ctas,
+                           float *few_part, int few_ctas) {
+  __shared__ float sum_s[kMergeWarps][kMergeCh + 2][32];
+  grid_dep_wait();
+  int b = blockIdx.x;
+  if (b < tile_ctas * kTileBlocks) {
+    merge_chain<kTileRows, D>(p, tile_part, tile_ctas, b / kTileBlocks, b % kTileBlocks,
+                              kTileBlocks, sum_s);
+  } else {
+    b -= tile_ctas * kTileBlocks;
+    merge_chain<kFewRows, D>(p, few_part, few_ctas, b / kFewBlocks, b % kFewBlocks, kFewBlocks,
+                             sum_s);
+  }
+}
+
+template <int D>
+int launch_merge(const PagedParams &p, float *tile_part, int tile_ctas, float *few_part,
+                 int few_ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas, ROWS == kFewRows ? 2 : 8);
+  cfg.gridDim = dim3((unsigned)(tile_ctas * kTileBlocks + few_ctas * kFewBlocks));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -140,7 +153,8 @@ int launch_merge(const PagedParams &p, int ctas, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fat_paged_merge_kernel<ROWS, D>, p, ctas);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fat_paged_merge_kernel<D>, p, tile_part,
+                                           tile_ctas, few_part, few_ctas);
   if (e == cudaSuccess) return FAT_OK;
   set_last_error("paged merge launch", (int)e, cudaGetErrorString(e));
   return FAT_ECUDA;
@@ -259,15 +273,9 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
     if (rc) return rc;
   }
   if (!plan.split) return FAT_OK;
-  if (plan.tile) {
-    rc = d == 64 ? launch_merge<kTileRows, 64>(p, paged_tile_ctas(), s)
-                 : launch_merge<kTileRows, 128>(p, paged_tile_ctas(), s);
-    if (rc) return rc;
-  }
-  if (plan.few)
-    rc = d == 64 ? launch_merge<kFewRows, 64>(pf, paged_few_ctas(), s)
-                 : launch_merge<kFewRows, 128>(pf, paged_few_ctas(), s);
-  return rc;
+  const int tile_ctas = plan.tile ? paged_tile_ctas() : 0, few_ctas = plan.few ? paged_few_ctas() : 0;
+  return d == 64 ? launch_merge<64>(p, p.part, tile_ctas, pf.part, few_ctas, s)
+                 : launch_merge<128>(p, p.part, tile_ctas, pf.part, few_ctas, s);
 }
 
 }  // extern "C"
