@@ -145,14 +145,41 @@ __device__ __forceinline__ int item_count(const TileItem &it, int t) {
   return it.tiles == 2 ? n : (n + 1 - t) >> 1;
 }
 
+// The S row of a tile that the mask cuts or that lies near the diagonal, turned into logits where it
+// stands: scale, bias and mask, chunk by chunk in a rolled loop. Such tiles are few (the ends of a
+// row's keys), so they pay a second pass over tensor memory rather than variants of the whole
+// softmax code: a call's first use of 6 KB of straight instructions costs 3 us of fetches.
+//   NEAR: bias = table[lut[j]] - slope |delta0 + j|;  else rowc + kk * j. Columns from lim on: -inf.
+template <bool NEAR>
+__device__ __forceinline__ void tile_edge(uint32_t tS, float scale_log2, float rowc, float kk,
+                                          const uint8_t *lut, const float *tab, int tab_stride,
+                                          float slope, int delta0, int lim) {
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 32) {
+    uint32_t x[32];
+    tmem_ld32(tS + c, x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float b;
+      if (NEAR) {
+        b = -slope * fabsf((float)(delta0 + c + i));
+        if (tab != nullptr) b = fmaf(__ldg(tab + lut[c + i] * tab_stride), kLog2e, b);
+      } else {
+        b = fmaf(kk, (float)(c + i), rowc);
+      }
+      const float v = fmaf(__uint_as_float(x[i]), scale_log2, b);
+      x[i] = __float_as_uint(c + i < lim ? v : -INFINITY);
+    }
+    tmem_st32(tS + c, x);
+  }
+  tmem_st_wait();
+}
+
 // The S row from tensor memory as logits x (log2 units, relative to the row's reference maximum when
-// FOLD), masked; returns the row's maximum.
-//   MODE 0: bias = rowc;  1: rowc + kk * j;  2: table[lut[j]] - slope |delta0 + j| - mref
-template <int MODE, bool MASK>
+// FOLD): S * scale + rowc, or + rowc + kk * j with LINEAR; returns the row's maximum.
+template <bool LINEAR>
 __device__ __forceinline__ float tile_logits(uint32_t tS, uint32_t (&x)[4][32], float scale_log2,
-                                             float rowc, float kk, const uint8_t *lut,
-                                             const float *tab, int tab_stride, float slope,
-                                             int delta0, int lim) {
+                                             float rowc, float kk) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) tmem_ld32_issue(tS + c * 32, x[c]);
 #pragma unroll
@@ -165,27 +192,11 @@ __device__ __forceinline__ float tile_logits(uint32_t tS, uint32_t (&x)[4][32], 
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const int j = c * 32 + i;
-      uint64_t b2;
-      if (MODE == 0) {
-        b2 = rc2;
-      } else if (MODE == 1) {
-        b2 = f2_pack(fmaf(kk, (float)j, rowc), fmaf(kk, (float)(j + 1), rowc));
-      } else {
-        float b[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          b[e] = fmaf(-slope, fabsf((float)(delta0 + j + e)), rowc);
-          if (tab != nullptr) b[e] = fmaf(__ldg(tab + lut[j + e] * tab_stride), kLog2e, b[e]);
-        }
-        b2 = f2_pack(b[0], b[1]);
-      }
+      const uint64_t b2 =
+          LINEAR ? f2_pack(fmaf(kk, (float)j, rowc), fmaf(kk, (float)(j + 1), rowc)) : rc2;
       float v0, v1;
       f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), sl2, b2),
                 v0, v1);
-      if (MASK) {
-        v0 = (j < lim) ? v0 : -INFINITY;
-        v1 = (j + 1 < lim) ? v1 : -INFINITY;
-      }
       x[c][i] = __float_as_uint(v0);
       x[c][i + 1] = __float_as_uint(v1);
       mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], v0, v1);
@@ -575,34 +586,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool need_mask = ks + 128 > it.lk || (p.causal && ks + 127 > pos_lo);
         const int lim = min(it.lk - ks, p.causal ? qpos - ks + 1 : 128);
         const float m_ref = (FOLD && m != -INFINITY) ? m : 0.f;
-        int mode = 0;
-        float rowc = 0.f, kk = 0.f;
+        float rowc = 0.f, kk = 0.f, scale = p.scale_log2;
+        bool near = false;
         if (p.bias.has_bias) {
-          if (ks - pos_hi >= p.bias.sat_pos) {
-            kk = -slope;
-            rowc = fmaf(kk, (float)(ks - qpos), c_pos);
-            mode = has_slopes ? 1 : 0;
-          } else if (ks + 127 - pos_lo <= -p.bias.sat_neg) {
-            kk = slope;
-            rowc = fmaf(kk, (float)(ks - qpos), c_neg);
-            mode = has_slopes ? 1 : 0;
-          } else {
-            mode = 2;
-          }
+          const bool far_pos = ks - pos_hi >= p.bias.sat_pos;
+          near = !far_pos && ks + 127 - pos_lo > -p.bias.sat_neg;
+          kk = far_pos ? -slope : slope;
+          rowc = fmaf(kk, (float)(ks - qpos), far_pos ? c_pos : c_neg);
         }
-        rowc -= m_ref;
+        const bool edge = near || need_mask;
+        if (edge) {
+          const uint8_t *row_lut = lut + (ks - qpos - p.bias.lut_lo);
+          if (near)
+            tile_edge<true>(tS, scale, 0.f, 0.f, row_lut, tab, p.hq, slope, ks - qpos, lim);
+          else
+            tile_edge<false>(tS, scale, rowc, kk, row_lut, tab, p.hq, slope, ks - qpos, lim);
+          scale = 1.f;
+          rowc = 0.f;
+        }
         uint32_t x[4][32];
-        float mx;
-#define FAT_TILE_LOGITS(MODE, MASK)                                                             \
-  tile_logits<MODE, MASK>(tS, x, p.scale_log2, rowc, kk, lut + (ks - qpos - p.bias.lut_lo), tab, \
-                          p.hq, slope, ks - qpos, lim)
-        if (mode == 0)
-          mx = need_mask ? FAT_TILE_LOGITS(0, true) : FAT_TILE_LOGITS(0, false);
-        else if (mode == 1)
-          mx = need_mask ? FAT_TILE_LOGITS(1, true) : FAT_TILE_LOGITS(1, false);
-        else
-          mx = FAT_TILE_LOGITS(2, true);
-#undef FAT_TILE_LOGITS
+        const float mx = (has_slopes && !edge)
+                             ? tile_logits<true>(tS, x, scale, rowc - m_ref, kk)
+                             : tile_logits<false>(tS, x, scale, rowc - m_ref, 0.f);
         if (C::SEP_P) {  // S is in registers: the next one may be computed
           tc_fence_before();
           mbar_arrive(s_free + t);
