@@ -58,7 +58,7 @@ struct TileCfg {
   static constexpr int OFF_LUT = OFF_THR + kMaxThresholds * 4;
   static_assert((2 + 4 * NS + 14 + 2 * kItems) * 8 + 8 <= 448, "barrier block");
   static_assert(OFF_LUT + kMaxBiasSpan + 512 + 1024 <= kSmemLimit, "shared memory");
-  static constexpr int REG_SM = 216, REG_OTHER = 72;
+  static constexpr int REG_SM = 224, REG_OTHER = 56;
   static constexpr int REGS_NEEDED = 256 * REG_SM + 128 * REG_OTHER;
   static_assert(REGS_NEEDED <= kThreads * ((65536 / kThreads) & ~7), "register split");
   // TMEM columns: S_t at 128 t, O_t behind them; d 64: P_t has columns of its own, so that the next
@@ -336,23 +336,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int kt = it.nkv - 1 - it.j0;
       int page = fetch(kt);
-      // Q is free once both issuers have released it, which also means that every K tile so far
-      // has been used. The V tiles so far have arrived too before the next Q is loaded: an issuer
-      // that finds Q full then knows every stage's earlier phases to be over, also those of stages
-      // that only the other one used, and tells the phases of its own by their parity.
-      if (ni > 0) ok = warp_wait(q_empty, (ni - 1) & 1, wd);
-      for (uint32_t k = 1; ok && k <= min(J, (uint32_t)C::NS); ++k)
-        ok = warp_wait(v_full + ((J - k) & (C::NS - 1)), ((J - k) >> C::NS_LOG2) & 1, wd);
+      // The item's Q. It is free once both issuers have released it, which also means that every K
+      // tile of the items before has been used. Their V tiles have arrived too before Q is loaded:
+      // an issuer that finds Q full then knows every stage's phases of earlier items to be over,
+      // also of stages that only the other one used, and tells the phases of its own by their parity.
+      auto load_q = [&](uint32_t before) {  // before: K/V positions of earlier items
+        if (ni > 0) ok = warp_wait(q_empty, (ni - 1) & 1, wd);
+        for (uint32_t k = 1; ok && k <= min(before, (uint32_t)C::NS); ++k)
+          ok = warp_wait(v_full + ((before - k) & (C::NS - 1)), ((before - k) >> C::NS_LOG2) & 1, wd);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(q_full, (uint32_t)RT * 128 * C::DB * it.tiles);
+          for (int t = 0; t < it.tiles; ++t)
+            for (int b = 0; b < C::DB; ++b)
+              tma_load_3d(&tm_q, q_full, sQ + t * C::TILE + b * C::BLK, 64 * b, it.hk * G,
+                          it.row0 + t * tq);
+        }
+        ++ni;
+      };
+      // With two stages (d 128) the first K would only wait as well; with four it is loaded first.
+      if (C::NS == 2) load_q(J);
       if (!ok) break;
-      if (lane == 0) {
-        const uint32_t bytes = (uint32_t)RT * 128 * C::DB * it.tiles;
-        mbar_arrive_expect_tx(q_full, bytes);
-        for (int t = 0; t < it.tiles; ++t)
-          for (int b = 0; b < C::DB; ++b)
-            tma_load_3d(&tm_q, q_full, sQ + t * C::TILE + b * C::BLK, 64 * b, it.hk * G,
-                        it.row0 + t * tq);
-      }
-      ++ni;
       for (int jj = 0; jj < n; ++jj, --kt, ++J) {
         const int s = J & (C::NS - 1);
         const uint32_t u = J >> C::NS_LOG2;
@@ -375,6 +378,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int b = 0; b < C::DB; ++b)
             tma_load_4d(&tm_k, k_full + s, sK + s * C::TILE + b * C::BLK + lane * kbox * 128, 64 * b,
                         c1, c2, cur);
+        if (C::NS > 2 && jj == 0) {
+          load_q(J);
+          if (!ok) break;
+        }
         if (u > 0 && !(ok = warp_wait(v_empty + s, (u - 1) & 1, wd))) break;
         // a request's last tile: its values complete on `tail`, and warp 11 arrives on v_full
         uint64_t *vbar = v_full + s;
