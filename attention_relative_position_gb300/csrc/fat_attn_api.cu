@@ -381,13 +381,21 @@ int make_tmap_rows(CUtensorMap *map, const void *ptr, int T, int H, int d, int b
   return 0;
 }
 
+int check_page_strides(const fat_paged_cache_t &c) {
+  const long long inner = std::min(c.stride_token, c.stride_head);
+  const long long mid = std::max(c.stride_token, c.stride_head);
+  if (mid % inner || c.stride_page % mid || c.stride_page >= (1LL << 39)) return FAT_EUNSUPPORTED;
+  return FAT_OK;
+}
+
 int make_tmap_pages(CUtensorMap *map, const void *ptr, const fat_paged_cache_t &c, int box_rows,
                     int *head_outer) {
+  const int rc = check_page_strides(c);
+  if (rc) return rc;
   const bool outer = c.stride_head > c.stride_token;
   *head_outer = outer ? 1 : 0;
   const long long inner = outer ? c.stride_token : c.stride_head;
   const long long mid = outer ? c.stride_head : c.stride_token;
-  if (mid % inner || c.stride_page % mid || c.stride_page >= (1LL << 39)) return FAT_EUNSUPPORTED;
   const TmapKey key{ptr,  c.num_pages, c.num_heads, c.head_dim,     64, box_rows,
                     0,    c.page_size, c.stride_page, c.stride_token, c.stride_head};
   if (tmap_lookup(key, map)) return FAT_OK;

@@ -396,6 +396,32 @@ int device_error_address(int **out);
 // (kernel, device, size). Returns a cudaError_t value (the reason recorded on failure).
 int prepare_kernel(const void *fn, size_t smem, int nthreads, int regs_needed);
 
+// Record a description of the last failing CUDA call of this thread (read by the C ABI).
+void set_last_error(const char *what, int code, const char *text);
+
+// Launch a kernel as a programmatic dependent of the work before it in the stream: its blocks may be
+// scheduled while a grid that has called grid_dep_launch still runs (the kernel calls grid_dep_wait
+// before it touches memory), otherwise when that work has completed. Returns FAT_OK or FAT_ECUDA with
+// the reason recorded.
+template <typename... P, typename... A>
+int launch_dependent(const char *what, void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                     cudaStream_t stream, const A &...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e == cudaSuccess) return FAT_OK;
+  set_last_error(what, (int)e, cudaGetErrorString(e));
+  return FAT_ECUDA;
+}
+
 // Number of SMs of the current device (cached per device; 0 if the query fails).
 int sm_count();
 
@@ -404,8 +430,6 @@ int sm_count();
 // co-resident two-CTA clusters, cached per (kernel, device, size); 0 if the query fails.
 int max_pair_ctas(const void *fn, size_t smem, int nthreads);
 
-// Record a description of the last failing CUDA call of this thread (read by the C ABI).
-void set_last_error(const char *what, int code, const char *text);
 
 // Tensor map over a [T, H, d] bf16 tensor, box = 64 channels x 1 head x box_rows tokens,
 // 128-byte swizzle (the shared-memory layout the tcgen05 descriptors expect).
@@ -418,7 +442,8 @@ int make_tmap_rows(CUtensorMap *map, const void *ptr, int T, int H, int d, int b
 // token, page), or (channel, token, head, page) when the heads lie outside the tokens of a page
 // (*head_outer = 1): the map's dimensions go by rising stride, each a multiple of the one before.
 // Box: 64 channels x 1 head x box_rows tokens of one page, 128-byte swizzle. Returns FAT_*
-// (FAT_EUNSUPPORTED: strides that are no such multiples).
+// (FAT_EUNSUPPORTED: strides that are no such multiples, which check_page_strides finds alone).
+int check_page_strides(const fat_paged_cache_t &c);
 int make_tmap_pages(CUtensorMap *map, const void *ptr, const fat_paged_cache_t &c, int box_rows,
                     int *head_outer);
 // Tensor map over a [T, H, d] fp32 tensor, box = box_c channels x 1 head x box_rows tokens (for

@@ -31,6 +31,7 @@ struct PagedParams {
   long long timeout_ns;
   int debug_flags;
   int few_rows;   // requests with at most this many rows (queries x group) are the few-row kernel's
+                  // (0: the tile kernel takes all)
   int both;       // the call launches both kernels: they share the SMs (see share_find)
   int sms;
   int split;      // 0: items are not cut (each goes to the CTA in whose share it begins)
@@ -172,6 +173,11 @@ struct ShareSmem {
   int sq[kShareDocs], lq[kShareDocs], lk[kShareDocs];
 };
 
+// a / b for a >= 0: by a 32-bit division wherever a has 32 bits (the 64-bit one is a long routine).
+__device__ __forceinline__ long long div_small(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 template <int NT>
 __device__ __forceinline__ long long share_scan(long long v, ShareSmem<NT> &s, long long *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -232,7 +238,7 @@ __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share,
   r.lo = r.hi = r.off = 0;
   r.doc = 0;
   if ((int)blockIdx.x >= G || total == 0) return r;
-  const long long share = max((total + G - 1) / G, (long long)min_share);
+  const long long share = max(div_small(total + G - 1, G), (long long)min_share);
   r.lo = blockIdx.x * share;
   r.hi = min(total, r.lo + share);
   if (r.lo >= r.hi) return r;
@@ -297,8 +303,7 @@ int paged_tile_ctas();
 // Whether items are cut: contexts of at most this many keys are computed by one CTA in a few stages
 // per warp, which costs less than the merge grid.
 constexpr int kWholeKeys = 1024;
-int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream,
-                     bool overlap_previous);
+int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
 int launch_paged_tile(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
 
 }  // namespace fat

@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     fat_paged_merge_kernel(const __grid_constant__ PagedParams p, float *tile_part, int tile_ctas,
                            float *few_part, int few_ctas) {
   __shared__ float sum_s[kMergeWarps][kMergeCh + 2][32];
+  grid_dep_launch();
   grid_dep_wait();
   int b = blockIdx.x;
   if (b < tile_ctas * kTileBlocks) {
@@ -144,24 +145,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
 template <int D>
 int launch_merge(const PagedParams &p, float *tile_part, int tile_ctas, float *few_part,
                  int few_ctas, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tile_ctas * kTileBlocks + few_ctas * kFewBlocks));
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fat_paged_merge_kernel<D>, p, tile_part,
-                                           tile_ctas, few_part, few_ctas);
-  if (e == cudaSuccess) return FAT_OK;
-  set_last_error("paged merge launch", (int)e, cudaGetErrorString(e));
-  return FAT_ECUDA;
+  return launch_dependent("paged merge launch", fat_paged_merge_kernel<D>,
+                          dim3((unsigned)(tile_ctas * kTileBlocks + few_ctas * kFewBlocks)),
+                          kMergeWarps * 32, 0, stream, p, tile_part, tile_ctas, few_part, few_ctas);
 }
 
-// The kernels a call launches and their partial rows' places in the workspace. When every request
-// has exactly max_seqlen_q queries (as the totals say), one kernel takes them all.
+// The kernels a call launches and their partial rows' places in the workspace. Bounds that allow
+// few rows only need one kernel. A total of num_seqs * max_seqlen_q rows says that the requests most
+// likely have max_seqlen_q queries each (it may as well be padding): then the tile kernel alone takes
+// every request, whatever its rows, which saves the other one's launch.
 struct Plan {
   bool few, tile, split;
   size_t few_off, bytes;
@@ -186,7 +178,8 @@ int check_shape(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
     return FAT_EINVAL_SHAPE;
   if (c->head_dim != 64 && c->head_dim != 128) return FAT_EINVAL_SHAPE;
   if ((long long)sh->total_q * sh->num_heads_q * c->head_dim > (1LL << 40)) return FAT_EINVAL_SHAPE;
-  if (sh->num_heads_q > 65535 || sh->num_seqs > 65535 || sh->num_heads_q / c->num_heads > 128)
+  if (sh->num_heads_q > 65535 || sh->num_seqs > 65535 || sh->num_heads_q / c->num_heads > 128 ||
+      sh->max_seqlen_k > (1 << 30))
     return FAT_EUNSUPPORTED;
   return FAT_OK;
 }
@@ -216,6 +209,7 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   int lg = 0;
   fat_paged_cache_t cc;
   rc = check_paged_cache(cache, &cc, &lg);
+  if (!rc) rc = check_page_strides(cc);
   if (rc) return rc;
   cache = &cc;
   PagedParams p{};
@@ -255,7 +249,7 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
   runtime_knobs(&p.timeout_ns, &p.debug_flags);
-  p.few_rows = kFewRows;
+  p.few_rows = plan.few ? kFewRows : 0;
   p.both = plan.few && plan.tile;
   p.sms = paged_tile_ctas();
   const int d = cache->head_dim;
@@ -269,7 +263,7 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
     if (rc) return rc;
   }
   if (plan.few) {
-    rc = launch_paged_few(pf, *cache, s, plan.tile);
+    rc = launch_paged_few(pf, *cache, s);
     if (rc) return rc;
   }
   if (!plan.split) return FAT_OK;

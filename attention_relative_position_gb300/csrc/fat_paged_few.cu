@@ -160,6 +160,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tm_v);
   }
   for (int i = tid; i < p.bias.n_thr; i += kThreads) thr_s[i] = p.bias.thr[i];
+  // Beside the tile kernel, which has waited for the work before it, nothing is waited for here.
+  if (!p.both) grid_dep_wait();
   if (p.split && tid < 2) {
     PartRecord *r = part_record(p.part, blockIdx.x, tid);
     r->valid = 0;
@@ -178,8 +180,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const Watchdog wd{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
   const PagedDoc d0 = share_doc(p, share_s, sh.doc, sh.doc);
   const int cost0 = few_item_cost((d0.lk + KT - 1) / KT);
-  const FewWalk<D> start{p, share_s, sh.doc, sh.doc, (int)(sh.off / cost0), sh.hi - sh.lo,
-                         (int)(sh.off % cost0)};
+  const int hk0 = (int)div_small(sh.off, cost0);
+  const FewWalk<D> start{p, share_s, sh.doc, sh.doc, hk0, sh.hi - sh.lo,
+                         (int)(sh.off - (long long)hk0 * cost0)};
 
   if (warp == kWarps) {
     // ------------------------------------------------------------------ producer
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <int D>
-int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream, bool overlap) {
+int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
   PagedParams pp = p;
   CUtensorMap mk, mv;
   int rc = make_tmap_pages(&mk, c.k, c, 16, &pp.head_outer);
@@ -611,30 +614,16 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
   if (rc) return rc;
   const size_t smem = FewCfg<D>::bytes(p.bias) + 1024;
   if (prepare_kernel((const void *)fat_paged_few_kernel<D>, smem, kThreads, 0)) return FAT_ECUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)paged_few_ctas());
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = overlap ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fat_paged_few_kernel<D>, mk, mv, pp);
-  if (e == cudaSuccess) return FAT_OK;
-  set_last_error("paged few-row kernel launch", (int)e, cudaGetErrorString(e));
-  return FAT_ECUDA;
+  return launch_dependent("paged few-row kernel launch", fat_paged_few_kernel<D>,
+                          dim3((unsigned)paged_few_ctas()), kThreads, smem, stream, mk, mv, pp);
 }
 
 }  // namespace
 
 int paged_few_ctas() { return 2 * (sm_count() > 0 ? sm_count() : 152); }
 
-int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream,
-                     bool overlap_previous) {
-  return c.head_dim == 64 ? launch_t<64>(p, c, stream, overlap_previous)
-                          : launch_t<128>(p, c, stream, overlap_previous);
+int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
+  return c.head_dim == 64 ? launch_t<64>(p, c, stream) : launch_t<128>(p, c, stream);
 }
 
 }  // namespace fat

@@ -59,6 +59,8 @@ __global__ void __launch_bounds__(kPlanThreads) fat_paged_plan_kernel(const Plan
   __shared__ int page_s[kPlanTile];  // first free-list index of each request
   __shared__ int ctx_s[kPlanTile];   // cached tokens; -1 - ctx: a request that takes no pages
   __shared__ PlanPair warp_s[kPlanThreads / 32];
+  grid_dep_launch();
+  grid_dep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gtid = blockIdx.x * kPlanThreads + tid, gthreads = gridDim.x * kPlanThreads;
   const int page_mask = (1 << p.log2_page) - 1;
@@ -233,6 +235,7 @@ __device__ __forceinline__ void rotate_halves(uint4 &u, uint4 &v, const float2 (
 
 template <bool PAIRS>
 __global__ void __launch_bounds__(kRowThreads) fat_rows_kernel(const __grid_constant__ RowParams p) {
+  grid_dep_wait();
   const long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x;
   const int t = (int)(i / p.units), u = (int)(i - (long long)t * p.units);
   if (t >= p.tokens) return;
@@ -343,14 +346,9 @@ int launch_rows(RowParams &p, const fat_rope_t *rope, int head_dim, cudaStream_t
   const long long blocks = (positions + kRowThreads - 1) / kRowThreads;
   if (blocks > 0x7fffffffLL || (p.all_heads + p.run - 1) / p.run > 65535) return FAT_EUNSUPPORTED;
   const dim3 grid((unsigned)blocks, (unsigned)((p.all_heads + p.run - 1) / p.run));
-  if (pairs)
-    fat_rows_kernel<true><<<grid, kRowThreads, 0, stream>>>(p);
-  else
-    fat_rows_kernel<false><<<grid, kRowThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) return FAT_OK;
-  set_last_error("rotary / append rows launch", (int)e, cudaGetErrorString(e));
-  return FAT_ECUDA;
+  return launch_dependent("rotary / append rows launch",
+                          pairs ? fat_rows_kernel<true> : fat_rows_kernel<false>, grid, kRowThreads,
+                          0, stream, p);
 }
 
 }  // namespace
@@ -424,11 +422,8 @@ int fat_paged_plan(const fat_plan_shape_t *sh, const int32_t *ctx_lens, const in
   // a block for every 1024 tokens or requests, one per SM at most
   const int units = std::max(sh->max_tokens, sh->num_seqs);
   const int blocks = std::max(1, std::min(sms, (units + 1023) / 1024));
-  fat_paged_plan_kernel<<<blocks, kPlanThreads, 0, static_cast<cudaStream_t>(sh->stream)>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) return FAT_OK;
-  set_last_error("paged plan launch", (int)e, cudaGetErrorString(e));
-  return FAT_ECUDA;
+  return launch_dependent("paged plan launch", fat_paged_plan_kernel, dim3((unsigned)blocks),
+                          kPlanThreads, 0, static_cast<cudaStream_t>(sh->stream), p);
 }
 
 int fat_rope_init(fat_rope_t *r, int rotary_dim, int interleaved, double base, double factor,

@@ -84,7 +84,7 @@ struct TileWalk {
         left(sh.hi - sh.lo) {
     const PagedDoc d = share_doc(p, sm, doc, doc);
     const long long per = tile_head_cost(d, tq, blk, p.causal);
-    hk = (int)(sh.off / per);
+    hk = (int)div_small(sh.off, per);
     long long rest = sh.off - hk * per;
     for (int c; rest >= (c = tile_block(d, b, tq, blk, p.causal).cost); rest -= c) ++b;
     off = (int)rest;
@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Watchdog *wdp = reinterpret_cast<Watchdog *>(sm + C::OFF_BAR + 448);
   int *thr_s = reinterpret_cast<int *>(sm + C::OFF_THR);
   uint8_t *lut = sm + C::OFF_LUT;
-  grid_dep_launch();
+  grid_dep_wait();
+  grid_dep_launch();  // the few-row kernel may start: what this call reads is complete
   if (p.split && tid < 2) part_record(p.part, blockIdx.x, tid)->valid = 0;
   for (int i = tid; i < p.bias.n_thr; i += kThreads) thr_s[i] = p.bias.thr[i];
   const TileCost cost{p, tq, 2 * tq};
@@ -777,11 +778,8 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
   const size_t smem = 1024 + C::OFF_LUT + (p.bias.table ? (size_t)((p.bias.lut_len + 15) & ~15) : 0);
   if (prepare_kernel((const void *)fat_paged_tile_kernel<D>, smem, kThreads, C::REGS_NEEDED))
     return FAT_ECUDA;
-  fat_paged_tile_kernel<D><<<paged_tile_ctas(), kThreads, smem, stream>>>(mq, mk, mv, pp);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) return FAT_OK;
-  set_last_error("paged tile kernel launch", (int)e, cudaGetErrorString(e));
-  return FAT_ECUDA;
+  return launch_dependent("paged tile kernel launch", fat_paged_tile_kernel<D>,
+                          dim3((unsigned)paged_tile_ctas()), kThreads, smem, stream, mq, mk, mv, pp);
 }
 
 }  // namespace

@@ -401,6 +401,19 @@ def test_attention_bounds_padding_and_repeats(name):
     assert torch.equal(a[:p.total], b[:p.total]) and torch.equal(la[:, :p.total], lb[:, :p.total])
 
 
+@pytest.mark.parametrize("lq,pad", [([40, 1, 3, 40], 76), ([9, 9, 9], 0), ([1, 0, 0, 33], 98)])
+def test_attention_rows_that_look_equal(lq, pad):
+    """total_q = num_seqs * max_seqlen_q, with equal requests or with padding: every row is there."""
+    p = Problem(lq=lq, lk=[1500, 64, 2000, 70][:len(lq)], hq=4, hkv=2, d=64, page=16, pad=pad,
+                alibi=True, seed=40)
+    assert p.q.shape[0] == len(lq) * max(lq)
+    out = torch.full_like(p.q, 3.0)
+    _, lse = p.run(out=out)
+    assert _errors() == 0
+    p.check(out, lse)
+    assert (out[p.total:] == 3.0).all()
+
+
 @pytest.mark.parametrize("name", ["decode_gqa16", "chunk_group5_d128", "chunk_group1"])
 @pytest.mark.parametrize("bad", [-1, 1 << 20, -(1 << 31)])
 def test_attention_bad_page_counts_as_zeros(name, bad):

@@ -160,6 +160,9 @@ def test_attn_refusals(lib):
     assert _attn(lib, _cache(head_dim=96, stride_head=96, stride_token=192, stride_page=4096)) == -2
     assert _attn(lib, c, num_heads_q=258) == -5  # 129 query heads per key/value head
     assert _attn(lib, c, num_seqs=70000) == -5
+    assert _attn(lib, c, max_seqlen_k=(1 << 30) + 1) == -5
+    # strides of which one is no multiple of the one before
+    assert _attn(lib, _cache(stride_head=72, stride_token=200, stride_page=4000)) == -5
     assert _attn(lib, c, bias=FAKE, nb=31, md=128, bidir=1) == -3
     assert _attn(lib, c, bias=FAKE, nb=32, md=8, bidir=1) == -3
     assert _attn(lib, c, bias=FAKE, nb=32, md=40000, bidir=1) == -5  # saturates too far out
