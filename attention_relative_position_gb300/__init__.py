@@ -1,8 +1,8 @@
 """GB300-native fused attention with an in-kernel relative-position bias (T5 buckets, ALiBi),
 padding-free varlen packing, forward and backward.
 
-This module is a thin ctypes binding over libfatattn.so (C ABI in include/fat_attn.h): it only
-marshals torch tensors into pointers and sizes. Every step of the computation runs in the CUDA
+This module is a thin binding over libfatattn.so (C ABI in include/fat_attn.h), by ctypes and, for the
+paged-cache calls, a small extension module: it only marshals torch tensors into pointers and sizes. Every step of the computation runs in the CUDA
 kernels of the library; there is no other implementation to fall back to, and a missing or
 unloadable library raises immediately.
 """
@@ -573,91 +573,36 @@ def fat_cross_entropy(logits, target, z_loss: float = 0.0, grad_scale: float = 1
 
 
 # ---- paged key/value cache ---------------------------------------------------------------------
-# These calls serve single decode steps, where the host's time counts: their checks read each
-# attribute once, and the device is switched only when it is not the current one.
+# These calls serve single decode steps, where the host's time counts: their arguments are checked
+# and handed to the library by the extension module of csrc/paged_binding.cpp, in order.
 
-def _refuse(name, t, dtype, dev):
-    """Why t is no dtype tensor on device index dev."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must be a CUDA tensor on the device of the other arguments")
+CALLS_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_paged_calls.so")
+_calls = None
 
 
-def _ints(name, t, numel, dev):
-    """Address of an int32 array argument: contiguous, on device index dev, numel entries (None:
-    any)."""
-    if t.dtype is not _torch.int32 or t.get_device() != dev:
-        _refuse(name, t, _torch.int32, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} entries, got {t.numel()}")
-    return t.data_ptr()
+def _load_calls():
+    """The extension module, bound to the loaded library (built by __graft_entry__.build())."""
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (the module is linked against its libraries)
+        load()
+        if not os.path.exists(CALLS_PATH):
+            raise FileNotFoundError(f"{CALLS_PATH} not found: build the library first (python -c "
+                                    f"'import __graft_entry__ as g; g.build()')")
+        loader = importlib.machinery.ExtensionFileLoader("_paged_calls", CALLS_PATH)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_paged_calls", loader))
+        loader.exec_module(module)
+        module.bind(_lib._name, _Rope)
+        _calls = module
+    return _calls
 
 
-def _rows(name, t, shape, dev):
-    """Strides of a bf16 array of rows whose last dimension is contiguous (views of packed rows are
-    fine); shape None: any."""
-    if t.dtype is not _torch.bfloat16 or t.get_device() != dev:
-        _refuse(name, t, _torch.bfloat16, dev)
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return st
-
-
-def _rank(name, t, rank):
-    if t.dim() != rank:
-        raise ValueError(f"{name} must have {rank} dimensions, got shape {tuple(t.shape)}")
-    return t.shape
-
-
-def _paged_cache(k_cache, v_cache, dev) -> _Cache:
-    shape = _rank("k_cache", k_cache, 4)
-    st = _rows("k_cache", k_cache, None, dev)
-    if _rows("v_cache", v_cache, shape, dev) != st:
-        raise ValueError("v_cache must have the strides of k_cache")
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), *shape, *st[:3])
-
-
-def _floats(name, t, shape, dev):
-    """Address of a contiguous fp32 array argument of the given shape."""
-    if t.dtype is not _torch.float32 or t.get_device() != dev:
-        _refuse(name, t, _torch.float32, dev)
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _raw_stream(stream, dev: int) -> int:
-    if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _call_on(dev: int, fn, *args) -> int:
-    """fn(*args) with device index dev current."""
-    if _torch.cuda.current_device() == dev:
-        return fn(*args)
-    with _torch.cuda.device(dev):
-        return fn(*args)
-
-
-_torch = None
-
-
-def _start(t):
-    """The library, with the first argument's device index (torch is imported by the first call)."""
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("the arguments must be CUDA tensors")
-    return (_lib if _lib is not None else load()), dev
+def _stream_arg(stream):
+    return stream if stream is None else int(getattr(stream, "cuda_stream", stream))
 
 
 def fat_paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size: int, num_pages: int,
@@ -668,32 +613,12 @@ def fat_paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size: int, 
     [n, width], in place). Returns (cu_seqlens_q [n + 1], seqlens_k [n], positions [max_tokens],
     slots [max_tokens], counts [2] = pages taken, tokens), all int32; tokens behind the last
     request get position 0 and slot -1."""
-    lib, dev = _start(ctx_lens)
-    n = ctx_lens.numel()
-    width = _rank("block_table", block_table, 2)[1]
-    max_tokens = int(max_tokens)
-    pc = _ints("ctx_lens", ctx_lens, n, dev)
-    pn = _ints("new_lens", new_lens, n, dev)
-    pf = _ints("free_pages", free_pages, None, dev)
-    pt = _ints("block_table", block_table, n * width, dev)
-    if block_table.shape[0] != n:
-        raise ValueError(f"block_table must have shape [{n}, width]")
-
-    def buf(t, size):
-        return _torch.empty(size, dtype=_torch.int32, device=ctx_lens.device) if t is None else t
-    cu_seqlens_q, seqlens_k = buf(cu_seqlens_q, n + 1), buf(seqlens_k, n)
-    positions, slots = buf(positions, max_tokens), buf(slots, max_tokens)
-    counts = buf(counts, 2)
-    sh = _PlanShape(n, int(page_size), int(num_pages), width, free_pages.numel(), max_tokens,
-                    _raw_stream(stream, dev))
-    rc = _call_on(dev, lib.fat_paged_plan, sh, pc, pn, pf, pt,
-                  _ints("cu_seqlens_q", cu_seqlens_q, n + 1, dev),
-                  _ints("seqlens_k", seqlens_k, n, dev),
-                  _ints("positions", positions, max_tokens, dev),
-                  _ints("slots", slots, max_tokens, dev), _ints("counts", counts, 2, dev))
-    if rc != 0:
-        raise FatAttnError(rc, "fat_paged_plan")
-    return cu_seqlens_q, seqlens_k, positions, slots, counts
+    r = (_calls or _load_calls()).plan(ctx_lens, new_lens, free_pages, block_table, page_size,
+                                       num_pages, max_tokens, cu_seqlens_q, seqlens_k, positions,
+                                       slots, counts, _stream_arg(stream))
+    if type(r) is int:
+        raise FatAttnError(r, "fat_paged_plan")
+    return r
 
 
 def fat_rope_init(rotary_dim: int, base: float = 10000.0, interleaved: bool = True,
@@ -717,18 +642,10 @@ def fat_rope_embed(x, positions, rope: _Rope, inverse: bool = False, out=None, s
     """Rotary embedding of bf16 rows x [T, H, d] (strided views are fine) at positions int32 [T];
     inverse=True applies the transpose, which takes the gradient of the result to the gradient of
     x. out may be x itself (in place). Returns out."""
-    lib, dev = _start(x)
-    T, H, d = shape = _rank("x", x, 3)
-    xs = _rows("x", x, None, dev)
-    if out is None:
-        out = _torch.empty(shape, dtype=_torch.bfloat16, device=x.device)
-    ys = _rows("out", out, shape, dev)
-    sh = _RopeShape(T, H, d, xs[0], xs[1], ys[0], ys[1], _raw_stream(stream, dev))
-    rc = _call_on(dev, lib.fat_rope_embed, sh, rope, x.data_ptr(), out.data_ptr(),
-                  _ints("positions", positions, T, dev), 1 if inverse else 0)
-    if rc != 0:
-        raise FatAttnError(rc, "fat_rope_embed")
-    return out
+    r = (_calls or _load_calls()).rope(x, positions, rope, inverse, out, _stream_arg(stream))
+    if type(r) is int:
+        raise FatAttnError(r, "fat_rope_embed")
+    return r
 
 
 def fat_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, rope=None, q_out=None,
@@ -737,42 +654,18 @@ def fat_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, rope
     page * page_size + offset; negative: dropped) of the caches (bf16 [pages, page_size, Hkv, d],
     any strides with a contiguous row, the same for both). With rope, k is turned at positions
     (int32 [T]) on the way, and q (bf16 [T, Hq, d]) too. Returns q_out (contiguous) or None."""
-    lib, dev = _start(k)
-    cache = _paged_cache(k_cache, v_cache, dev)
-    T = _rank("k", k, 3)[0]
-    d = cache.head_dim
-    rows = (T, cache.num_heads, d)
-    ks, vs = _rows("k", k, rows, dev), _rows("v", v, rows, dev)
-    Hq, qs, pq, po = 0, (0, 0), None, None
-    if q is not None:
-        Hq = _rank("q", q, 3)[1]
-        qs = _rows("q", q, (T, Hq, d), dev)
-        if q_out is None:
-            q_out = _torch.empty((T, Hq, d), dtype=_torch.bfloat16, device=q.device)
-        _rows("q_out", q_out, (T, Hq, d), dev)
-        if not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous")
-        pq, po = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out is given without q")
-    sh = _AppendShape(T, Hq, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], _raw_stream(stream, dev))
-    rc = _call_on(dev, lib.fat_paged_append, sh, cache, rope, pq, k.data_ptr(), v.data_ptr(),
-                  None if positions is None else _ints("positions", positions, T, dev),
-                  _ints("slots", slots, T, dev), po)
-    if rc != 0:
-        raise FatAttnError(rc, "fat_paged_append")
-    return q_out
+    r = (_calls or _load_calls()).append(k, v, k_cache, v_cache, slots, q, positions, rope, q_out,
+                                         _stream_arg(stream))
+    if type(r) is int:
+        raise FatAttnError(r, "fat_paged_append")
+    return r[0]
 
 
 def fat_paged_attn_workspace_size(q, k_cache, cu_seqlens_q, max_seqlen_q: int,
                                   max_seqlen_k: int) -> int:
     """Workspace bytes of fat_paged_attn for these arguments on q's device."""
-    lib, dev = _start(q)
-    sh = _PagedShape(q.shape[0], cu_seqlens_q.numel() - 1, int(max_seqlen_q), int(max_seqlen_k),
-                     q.shape[1], 0, None)
-    P, ps, H, d = k_cache.shape
-    cache = _Cache(None, None, P, ps, H, d, 0, 0, 0)
-    return int(_call_on(dev, lib.fat_paged_attn_workspace_size, sh, cache))
+    return (_calls or _load_calls()).attn_workspace(q, k_cache, cu_seqlens_q, max_seqlen_q,
+                                                    max_seqlen_k)
 
 
 def fat_paged_attn(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q: int,
@@ -786,50 +679,13 @@ def fat_paged_attn(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, ma
     its last query lines up with its last key. Bias, mask and scale as fat_xattn_fwd. workspace:
     fat_paged_attn_workspace_size bytes (None: allocated here), for one call at a time. Returns
     (out bf16 [Tq, Hq, d], lse fp32 [Hq, Tq])."""
-    lib, dev = _start(q)
-    Tq, Hq, d = shape = _rank("q", q, 3)
-    _rows("q", q, None, dev)
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    n = seqlens_k.numel()
-    cache = _paged_cache(k_cache, v_cache, dev)
-    if cache.head_dim != d:
-        raise ValueError(f"q has head_dim {d}, the cache {cache.head_dim}")
-    rows, width = _rank("block_table", block_table, 2)
-    if rows != n:
-        raise ValueError(f"block_table must have shape [{n}, width]")
-    pb = ps = None
-    if bias_table is not None:
-        pb = _floats("bias_table", bias_table, (num_buckets, Hq), dev)
-    if alibi_slopes is not None:
-        ps = _floats("alibi_slopes", alibi_slopes, (Hq,), dev)
-    if out is None:
-        out = _torch.empty_like(q)
-    else:
-        _rows("out", out, shape, dev)
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous")
-    if lse is None:
-        lse = _torch.empty((Hq, Tq), dtype=_torch.float32, device=q.device)
-        pl = lse.data_ptr()
-    else:
-        pl = _floats("lse", lse, (Hq, Tq), dev)
-    sh = _PagedShape(Tq, n, int(max_seqlen_q), int(max_seqlen_k), Hq, width,
-                     _raw_stream(stream, dev))
-    if workspace is None:
-        need = int(_call_on(dev, lib.fat_paged_attn_workspace_size, sh, cache))
-        workspace = _torch.empty(need, dtype=_torch.uint8, device=q.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
-    rc = _call_on(dev, lib.fat_paged_attn, sh, cache, q.data_ptr(),
-                  _ints("block_table", block_table, None, dev),
-                  _ints("cu_seqlens_q", cu_seqlens_q, n + 1, dev),
-                  _ints("seqlens_k", seqlens_k, n, dev), pb, int(num_buckets), int(max_distance),
-                  1 if bidirectional else 0, ps, 1 if causal else 0, float(softmax_scale),
-                  workspace.data_ptr(), workspace.nbytes, out.data_ptr(), pl)
-    if rc != 0:
-        raise FatAttnError(rc, "fat_paged_attn")
-    return out, lse
+    r = (_calls or _load_calls()).attn(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k,
+                                       max_seqlen_q, max_seqlen_k, bias_table, num_buckets,
+                                       max_distance, bidirectional, alibi_slopes, causal,
+                                       softmax_scale, out, lse, workspace, _stream_arg(stream))
+    if type(r) is int:
+        raise FatAttnError(r, "fat_paged_attn")
+    return r
 
 
 def fat_attn_get_device_error(stream=None, device=None) -> int:

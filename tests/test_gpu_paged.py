@@ -575,6 +575,14 @@ def test_arguments_are_checked():
         fa.fat_rope_embed(k, _i32([1, 2]), fa.fat_rope_init(64))
     with pytest.raises(TypeError):
         fa.fat_rope_embed(k, torch.zeros(3, device=DEV), fa.fat_rope_init(64))
+    with pytest.raises(TypeError):  # a rotation that fat_rope_init has not made
+        fa.fat_rope_embed(k, _i32([1, 2, 3]), bytes(1040))
+    with pytest.raises(TypeError):
+        p.run(max_q="1")
+    with pytest.raises(ValueError):
+        p.run(max_k=1 << 40)
+    with pytest.raises(fa.FatAttnError):
+        p.run(max_q=-1)
     with pytest.raises(ValueError):
         fa.fat_paged_plan(_i32([1, 2]), _i32([1]), _i32([0]), _i32([[0], [0]]), 16, 4, 4)
 

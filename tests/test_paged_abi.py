@@ -174,3 +174,28 @@ def test_attn_refusals(lib):
     for empty in (dict(total_q=0), dict(num_seqs=0), dict(max_seqlen_q=0)):
         assert _attn(lib, c, **empty) == 0, empty
     assert lib.fat_paged_attn_workspace_size(None, ctypes.byref(c)) == 0
+
+
+def test_binding_refusals():
+    """What the binding refuses before it reaches the library (which needs no GPU to say so)."""
+    import torch
+    i = torch.zeros(2, dtype=torch.int32)
+    x = torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    cache = torch.zeros(2, 16, 1, 64, dtype=torch.bfloat16)
+    rope = fa.fat_rope_init(64)
+    for err, call in (
+            (TypeError, lambda: fa.fat_paged_plan([1], i, i, i.view(2, 1), 16, 2, 2)),
+            (TypeError, lambda: fa.fat_paged_plan(i.long(), i, i, i.view(2, 1), 16, 2, 2)),
+            (ValueError, lambda: fa.fat_paged_plan(i, i, i, i.view(2, 1), 16, 2, 2)),  # on the CPU
+            (TypeError, lambda: fa.fat_rope_embed(x.float(), i, rope)),
+            (ValueError, lambda: fa.fat_rope_embed(x, i, rope)),
+            (TypeError, lambda: fa.fat_rope_embed(None, i, rope)),
+            (ValueError, lambda: fa.fat_paged_append(x, x, cache, cache, i)),
+            (TypeError, lambda: fa.fat_paged_append(x.half(), x, cache, cache, i)),
+            (ValueError, lambda: fa.fat_paged_attn(x, cache, cache, i.view(2, 1), i, i, 1, 1)),
+            (TypeError, lambda: fa.fat_paged_attn(1, cache, cache, i.view(2, 1), i, i, 1, 1)),
+            (TypeError, lambda: fa.fat_paged_attn_workspace_size("q", cache, i, 1, 1))):
+        with pytest.raises(err):
+            call()
+    with pytest.raises(TypeError):
+        fa._load_calls().plan(1, 2)
