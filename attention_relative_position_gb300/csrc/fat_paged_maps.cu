@@ -419,9 +419,10 @@ int fat_paged_plan(const fat_plan_shape_t *sh, const int32_t *ctx_lens, const in
   p.slots = slots;
   p.counts = counts;
   const int sms = sm_count() > 0 ? sm_count() : 152;
-  // a block for every 1024 tokens or requests, one per SM at most
+  // a block for every 256 tokens or requests, two per SM at most: a thread's tokens are looked up one
+  // after the other (47 K tokens of 1000 requests: 4.7 us, with a quarter of the blocks 6.6 us)
   const int units = std::max(sh->max_tokens, sh->num_seqs);
-  const int blocks = std::max(1, std::min(sms, (units + 1023) / 1024));
+  const int blocks = std::max(1, std::min(2 * sms, (units + 255) / 256));
   return launch_dependent("paged plan launch", fat_paged_plan_kernel, dim3((unsigned)blocks),
                           kPlanThreads, 0, static_cast<cudaStream_t>(sh->stream), p);
 }
