@@ -71,7 +71,9 @@ struct FewCost {
 };
 
 // Tile kernel: one block of queries of a request: tokens [q0, q0 + ntok), one or two tiles, the key
-// tiles that its rows see, its cost in (Q tile, key tile) pairs.
+// tiles that its rows see, its cost in (Q tile, key tile) pairs, kTileItem of them for the fixed costs
+// of an item (its first loads, its rows written).
+constexpr int kTileItem = 5;
 struct TileBlock {
   int q0, ntok, nkv, tiles, cost;
 };
@@ -86,7 +88,7 @@ __device__ __forceinline__ TileBlock tile_block(const PagedDoc &d, int b, int tq
     const int last = d.lk - d.lq + t.q0 + t.ntok - 1;  // key position of the last row
     t.nkv = last < 0 ? 0 : min(t.nkv, (last >> 7) + 1);
   }
-  t.cost = max(1, t.tiles * t.nkv);
+  t.cost = kTileItem + t.tiles * t.nkv;
   return t;
 }
 __device__ __forceinline__ long long tile_head_cost(const PagedDoc &d, int tq, int blk,

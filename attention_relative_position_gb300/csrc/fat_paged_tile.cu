@@ -55,20 +55,28 @@ struct TileCfg {
   static constexpr int OFF_ITEMS = OFF_STATS + 1024;
   static constexpr int OFF_SHARE = OFF_ITEMS + ((kItems * (int)sizeof(TileItem) + 15) & ~15);
   static constexpr int OFF_THR = OFF_SHARE + (int)sizeof(ShareSmem<kThreads>);
-  static constexpr int OFF_LUT = OFF_THR + kMaxThresholds * 4;
-  static_assert((2 + 4 * NS + 14 + 2 * kItems) * 8 + 8 <= 448, "barrier block");
+  static constexpr int OFF_ROWS = (OFF_THR + kMaxThresholds * 4 + 127) & ~127;  // 2 KB per softmax warp
+  static constexpr int OFF_LUT = OFF_ROWS + 8 * 2048;
+  static_assert((2 + 4 * NS + 16 + 2 * kItems) * 8 + 8 <= 448, "barrier block");
   static_assert(OFF_LUT + kMaxBiasSpan + 512 + 1024 <= kSmemLimit, "shared memory");
   static constexpr int REG_SM = 224, REG_OTHER = 56;
   static constexpr int REGS_NEEDED = 256 * REG_SM + 128 * REG_OTHER;
   static_assert(REGS_NEEDED <= kThreads * ((65536 / kThreads) & ~7), "register split");
-  // TMEM columns: S_t at 128 t, O_t behind them; d 64: P_t has columns of its own, so that the next
-  // S_t is computed while P_t is still read; d 128: P_t overwrites S_t.
+  // TMEM columns: S_t at 128 t, O_t behind them.
+  // d 64: P_t has columns of its own, so that the next S_t is computed while P_t is still read.
+  // d 128: there is no room for that. S_t comes in two halves of 64 keys: step g of a tile has its
+  // first 64 keys' S in half g % 2 and the others' in the other half; P of both (bf16 pairs, 64
+  // columns) is written over the first. The second half is free again once it has been read, so the
+  // next step's first S is computed before this step's P V, and the warpgroup finds it when it comes
+  // back (2.07 us a step of two tiles; 2.75 us with S whole). With d 64 the halves' own costs are
+  // higher than what they save (106 us against 91 on 2 x 1024 queries over 8192 keys, 16 heads).
   static constexpr bool SEP_P = D == 64;
-  static constexpr uint32_t COL_O = 256, O_STRIDE = SEP_P ? 64 : 128;
+  static constexpr int SCOLS = SEP_P ? 128 : 64;  // columns of S that are computed and read at once
+  static constexpr uint32_t COL_O = 256, O_STRIDE = D;
   static constexpr uint32_t COL_P = COL_O + 2 * O_STRIDE;
   static constexpr uint32_t TMEM_COLS = 512;
   static_assert(COL_P + (SEP_P ? 128 : 0) <= TMEM_COLS, "TMEM column budget");
-  static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, 0, 0);
+  static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, SCOLS, 0, 0);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
 };
 
@@ -126,10 +134,12 @@ struct TileWalk {
         it.begins = it.ends = true;
         return true;
       }
-      it.j0 = min((o + t.tiles - 1) / t.tiles, t.nkv);
-      it.j1 = min((o + take + t.tiles - 1) / t.tiles, t.nkv);
-      if (t.nkv > 0 && it.j0 == it.j1) continue;  // the boundary lies inside a pair of tiles
+      // the fixed part of the cost comes first, before the key tiles
+      it.j0 = (max(o - kTileItem, 0) + t.tiles - 1) / t.tiles;
+      it.j1 = (max(o + take - kTileItem, 0) + t.tiles - 1) / t.tiles;
       it.begins = it.j0 == 0;
+      it.ends = o + take == t.cost;
+      if (it.j0 == it.j1 && !(t.nkv == 0 && it.ends)) continue;  // no key tile of it lies here
       it.ends = it.j1 == t.nkv;
       return true;
     }
@@ -145,17 +155,17 @@ __device__ __forceinline__ int item_count(const TileItem &it, int t) {
   return it.tiles == 2 ? n : (n + 1 - t) >> 1;
 }
 
-// The S row of a tile that the mask cuts or that lies near the diagonal, turned into logits where it
-// stands: scale, bias and mask, chunk by chunk in a rolled loop. Such tiles are few (the ends of a
-// row's keys), so they pay a second pass over tensor memory rather than variants of the whole
-// softmax code: a call's first use of 6 KB of straight instructions costs 3 us of fetches.
-//   NEAR: bias = table[lut[j]] - slope |delta0 + j|;  else rowc + kk * j. Columns from lim on: -inf.
-template <bool NEAR>
+// COLS columns of the S row turned into logits where they stand: scale, bias and mask (columns from
+// lim on), chunk by chunk in a rolled loop. For the few tiles near the diagonal (and, with d 64, those
+// that the mask cuts): they pay a second pass over tensor memory rather than a variant of the whole
+// softmax code, of which a call's first use of 6 KB costs 3 us of instruction fetches.
+//   NEAR: bias = table[lut[j]] - slope |delta0 + j|;  else rowc + kk * j.
+template <int COLS, bool NEAR>
 __device__ __forceinline__ void tile_edge(uint32_t tS, float scale_log2, float rowc, float kk,
                                           const uint8_t *lut, const float *tab, int tab_stride,
                                           float slope, int delta0, int lim) {
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 32) {
+  for (int c = 0; c < COLS; c += 32) {
     uint32_t x[32];
     tmem_ld32(tS + c, x);
 #pragma unroll
@@ -175,20 +185,20 @@ __device__ __forceinline__ void tile_edge(uint32_t tS, float scale_log2, float r
   tmem_st_wait();
 }
 
-// The S row from tensor memory as logits x (log2 units, relative to the row's reference maximum when
-// FOLD): S * scale + rowc, or + rowc + kk * j with LINEAR; returns the row's maximum.
-template <bool LINEAR>
-__device__ __forceinline__ float tile_logits(uint32_t tS, uint32_t (&x)[4][32], float scale_log2,
-                                             float rowc, float kk) {
+// 32 CHUNKS columns of the S row from tensor memory as logits x (log2 units):
+// S * scale + rowc + kk * j, columns from lim on masked; returns the row's maximum.
+template <int CHUNKS, bool LINEAR, bool MASK>
+__device__ __forceinline__ float tile_logits(uint32_t tS, uint32_t (&x)[CHUNKS][32],
+                                             float scale_log2, float rowc, float kk, int lim) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld32_issue(tS + c * 32, x[c]);
+  for (int c = 0; c < CHUNKS; ++c) tmem_ld32_issue(tS + c * 32, x[c]);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld32_fence(x[c]);
+  for (int c = 0; c < CHUNKS; ++c) tmem_ld32_fence(x[c]);
   const uint64_t sl2 = f2_pack(scale_log2, scale_log2);
   const uint64_t rc2 = f2_pack(rowc, rowc);
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < CHUNKS; ++c) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const int j = c * 32 + i;
@@ -197,12 +207,36 @@ __device__ __forceinline__ float tile_logits(uint32_t tS, uint32_t (&x)[4][32], 
       float v0, v1;
       f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), sl2, b2),
                 v0, v1);
+      if (MASK) {
+        v0 = (j < lim) ? v0 : -INFINITY;
+        v1 = (j + 1 < lim) ? v1 : -INFINITY;
+      }
       x[c][i] = __float_as_uint(v0);
       x[c][i + 1] = __float_as_uint(v1);
       mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], v0, v1);
     }
   }
   return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
+// P = 2^(x - sub) of those columns as bf16 pairs into tensor memory, with their fp32 sum.
+template <int CHUNKS, bool SUB>
+__device__ __forceinline__ void tile_exp(const uint32_t (&x)[CHUNKS][32], uint64_t sub2, uint32_t tP,
+                                         uint64_t (&sum2)[4]) {
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float a = __uint_as_float(x[c][2 * i]), b = __uint_as_float(x[c][2 * i + 1]);
+      if (SUB) f2_unpack(f2_sub(f2_pack(a, b), sub2), a, b);
+      a = ex2(a);
+      b = ex2(b);
+      pk[i] = pack_bf16x2(a, b);
+      sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(a, b));
+    }
+    tmem_st16(tP + c * 16, pk);
+  }
 }
 
 template <int D>
@@ -224,11 +258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *v_full = k_full + C::NS;
   uint64_t *k_empty = v_full + C::NS;
   uint64_t *v_empty = k_empty + C::NS;
-  uint64_t *s_full = v_empty + C::NS;  // [2] each
-  uint64_t *p_ready = s_full + 2;
+  uint64_t *s_full = v_empty + C::NS;  // [tile][half]
+  uint64_t *p_ready = s_full + 4;      // [2] each from here on
   uint64_t *o_ready = p_ready + 2;
-  uint64_t *s_free = o_ready + 2;
-  uint64_t *o_free = s_free + 2;
+  uint64_t *s_read = o_ready + 2;  // S (d 128: the step's second half of it) has been read
+  uint64_t *o_free = s_read + 2;
   uint64_t *mma_done = o_free + 2;
   uint64_t *merge_ready = mma_done + 2;
   uint64_t *tail = merge_ready + 1;  // a last tile's values have arrived (before they are zeroed)
@@ -260,10 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(v_empty + s, 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(s_full + t, 1);
+      mbar_init(s_full + 2 * t, 1);
+      mbar_init(s_full + 2 * t + 1, 1);
       mbar_init(p_ready + t, 128);
       mbar_init(o_ready + t, 1);
-      mbar_init(s_free + t, 128);
+      mbar_init(s_read + t, 128);
       mbar_init(o_free + t, 128);
       mbar_init(mma_done + t, 1);
     }
@@ -415,7 +450,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp - kWarpMma;
     if (lane == 0) {
       const uint32_t dS = tmem + 128 * t, dO = tmem + C::COL_O + C::O_STRIDE * t;
-      const uint32_t aP = C::SEP_P ? tmem + C::COL_P + 64 * t : dS;
       const uint64_t dKd = sw128_desc(smem_u32(sK), 16, 1024);
       const uint64_t dVd = sw128_desc(smem_u32(sV), C::BLK, 1024);
       uint32_t J = 0, g = 0;  // stream position, this tile's steps
@@ -438,18 +472,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint64_t dQd = sw128_desc(smem_u32(sQ) + (it.tiles == 2 ? t * C::TILE : 0), 16, 1024);
         const bool alone = it.tiles == 1;  // each stage is one tile's
-        auto issue_S = [&](int jj) {
-          const uint64_t kd = dKd + ((((J + jj) & (C::NS - 1)) * C::TILE) >> 4);
+        // S of keys SCOLS half .. of position jj, as step gs of this tile
+        auto issue_S = [&](int jj, int half, uint32_t gs) {
+          const int st = (J + jj) & (C::NS - 1);
+          const uint64_t kd = dKd + ((st * C::TILE + half * 64 * 128) >> 4);
+          const uint32_t d = C::SEP_P ? dS : dS + 64 * ((gs & 1) ^ half);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4;
-            mma_bf16_ss(dS, dQd + off, kd + off, C::IDESC_S, kk > 0);
+            mma_bf16_ss(d, dQd + off, kd + off, C::IDESC_S, kk > 0);
           }
-          mma_commit(s_full + t);
-          uint64_t *ke = k_empty + ((J + jj) & (C::NS - 1));
-          mma_commit(ke);
-          if (alone) mma_commit(ke);
-          if (jj + step >= n) mma_commit(q_empty);  // the item's last S of this tile
+          mma_commit(s_full + 2 * t + half);
+          if (C::SEP_P || half == 1) {  // the key tile has been used
+            mma_commit(k_empty + st);
+            if (alone) mma_commit(k_empty + st);
+            if (jj + step >= n) mma_commit(q_empty);  // and so has Q
+          }
         };
         auto k_wait = [&](int jj) {
           return mbar_wait(k_full + ((J + jj) & (C::NS - 1)), ((J + jj) >> C::NS_LOG2) & 1, wd);
@@ -457,17 +495,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait(q_full, ni & 1, wd) && k_wait(first);
         if (!ok) break;
         tc_fence_after();
-        issue_S(first);
+        issue_S(first, 0, g);
+        if (!C::SEP_P) issue_S(first, 1, g);
         for (int jj = first; jj < n; jj += step, ++g) {
           const uint32_t jp = J + jj;
           const int s = jp & (C::NS - 1);
-          if (C::SEP_P) {  // the next S as soon as this one has been read
-            if (!(ok = mbar_wait(s_free + t, g & 1, wd))) break;
-            if (jj + step < n) {
-              if (!(ok = k_wait(jj + step))) break;
-              tc_fence_after();
-              issue_S(jj + step);
-            }
+          const bool more = jj + step < n;
+          // the next step's S (d 128: its first half, where this step's second one has been read)
+          if (!(ok = mbar_wait(s_read + t, g & 1, wd))) break;
+          if (more) {
+            if (!(ok = k_wait(jj + step))) break;
+            tc_fence_after();
+            issue_S(jj + step, 0, g + 1);
           }
           if (!(ok = mbar_wait(v_full + s, (jp >> C::NS_LOG2) & 1, wd) &&
                      mbar_wait(p_ready + t, g & 1, wd)))
@@ -476,6 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (jj == first && act > 0 && !(ok = mbar_wait(o_free + t, (act - 1) & 1, wd))) break;
           tc_fence_after();
           const uint64_t vd = dVd + ((s * C::TILE) >> 4);
+          const uint32_t aP = C::SEP_P ? tmem + C::COL_P + 64 * t : dS + 64 * (g & 1);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_bf16_ts(dO, aP + kk * 8, vd + ((kk * 2048) >> 4), C::IDESC_PV,
@@ -483,11 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(o_ready + t);
           mma_commit(v_empty + s);
           if (alone) mma_commit(v_empty + s);
-          if (!C::SEP_P && jj + step < n) {
-            if (!(ok = k_wait(jj + step))) break;
-            tc_fence_after();
-            issue_S(jj + step);
-          }
+          // the other half over P, which the products above have read
+          if (!C::SEP_P && more) issue_S(jj + step, 1, g + 1);
         }
         J += n;
         ++ni;
@@ -526,13 +563,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------------ softmax warpgroups
     regs_inc<C::REG_SM>();
-    constexpr bool FOLD = !C::SEP_P;
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + 128 * t;
     const uint32_t tO = tmem + lane_off + C::COL_O + C::O_STRIDE * t;
-    const uint32_t tP = C::SEP_P ? tmem + lane_off + C::COL_P + 64 * t : tS;
     float2 *stats = reinterpret_cast<float2 *>(sm + C::OFF_STATS);
+    const uint32_t scratch = smem_u32(sm + C::OFF_ROWS) + warp * 2048;
     const int rq = r / G, rg = r - rq * G;  // token and head of this row within the tile
     const bool has_slopes = p.bias.slopes != nullptr, has_table = p.bias.table != nullptr;
     uint32_t g = 0, g_other = 0;  // steps of this tile and of the other one
@@ -583,18 +619,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         c_pos = __ldg(tab + lut[p.bias.sat_pos - p.bias.lut_lo] * p.hq) * kLog2e;
         c_neg = __ldg(tab + lut[-p.bias.sat_neg - p.bias.lut_lo] * p.hq) * kLog2e;
       }
-      float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < steps; ++i) {
+      // m: the row's reference, which P is relative to. It is raised (and what was summed so far
+      // scaled) only when the row's maximum grows beyond it by more than 2^32, at a step's second half
+      // of S 2^96 (P of the first would have to be scaled as well; pend keeps the growth): every sum
+      // stays far from fp32's and bf16's ends, and the result is exact.
+      float m = -INFINITY, l = 0.f, pend = 0.f;
+      for (int i = 0; i < steps && ok; ++i) {
         const uint32_t gi = g + i;
-        if (ok) ok = warp_wait(s_full + t, gi & 1, wd);
-        if (!ok) break;
-        tc_fence_after();
         const int jj = item_first(it, t) + i * item_step(it);
         const int ks = 128 * (it.nkv - 1 - it.j0 - jj);
         const bool need_mask = ks + 128 > it.lk || (p.causal && ks + 127 > pos_lo);
         const int lim = min(it.lk - ks, p.causal ? qpos - ks + 1 : 128);
-        const float m_ref = (FOLD && m != -INFINITY) ? m : 0.f;
-        float rowc = 0.f, kk = 0.f, scale = p.scale_log2;
+        float rowc = 0.f, kk = 0.f;
         bool near = false;
         if (p.bias.has_bias) {
           const bool far_pos = ks - pos_hi >= p.bias.sat_pos;
@@ -602,68 +638,136 @@ __global__ void __launch_bounds__(kThreads, 1)
           kk = far_pos ? -slope : slope;
           rowc = fmaf(kk, (float)(ks - qpos), far_pos ? c_pos : c_neg);
         }
-        const bool edge = near || need_mask;
-        if (edge) {
-          const uint8_t *row_lut = lut + (ks - qpos - p.bias.lut_lo);
-          if (near)
-            tile_edge<true>(tS, scale, 0.f, 0.f, row_lut, tab, p.hq, slope, ks - qpos, lim);
-          else
-            tile_edge<false>(tS, scale, rowc, kk, row_lut, tab, p.hq, slope, ks - qpos, lim);
-          scale = 1.f;
-          rowc = 0.f;
-        }
-        uint32_t x[4][32];
-        const float mx = (has_slopes && !edge)
-                             ? tile_logits<true>(tS, x, scale, rowc - m_ref, kk)
-                             : tile_logits<false>(tS, x, scale, rowc - m_ref, 0.f);
-        if (C::SEP_P) {  // S is in registers: the next one may be computed
-          tc_fence_before();
-          mbar_arrive(s_free + t);
-        }
-        float sub = 0.f;  // what the exponentials still subtract (FOLD)
-        if (i == 0) {
-          m = mx;
-          sub = mx == -INFINITY ? 0.f : mx;
-        } else {
-          const bool fresh = m == -INFINITY;  // no key of this row so far
-          const bool need = fresh ? mx != -INFINITY : mx > (FOLD ? 0.f : m) + 32.0f;
-          if (C::SEP_P) {  // P and O are still read by the previous P V
-            ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (__any_sync(0xffffffffu, need)) {
-            if (!C::SEP_P) {
-              ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            const float f = need ? (fresh ? 0.f : ex2(FOLD ? -mx : m - mx)) : 1.0f;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO + c * 32, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32(tO + c * 32, o);
-            }
-            if (need) {
-              l *= f;
-              m = (fresh || !FOLD) ? mx : m + mx;
-              sub = mx;
-            }
-          }
-        }
         uint64_t sum2[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum2[k] = f2_pack(0.f, 0.f);
-        if (!FOLD) {
+        if constexpr (C::SEP_P) {
+          const uint32_t tP = tmem + lane_off + C::COL_P + 64 * t;
+          ok = warp_wait(s_full + 2 * t, gi & 1, wd);
+          if (!ok) break;
+          tc_fence_after();
+          float scale = p.scale_log2;
+          const bool edge = near || need_mask;
+          if (edge) {
+            const uint8_t *row_lut = lut + (ks - qpos - p.bias.lut_lo);
+            if (near)
+              tile_edge<128, true>(tS, scale, 0.f, 0.f, row_lut, tab, p.hq, slope, ks - qpos, lim);
+            else
+              tile_edge<128, false>(tS, scale, rowc, kk, row_lut, tab, p.hq, slope, ks - qpos, lim);
+            scale = 1.f;
+            rowc = 0.f;
+          }
+          uint32_t x[4][32];
+          const float mx = (has_slopes && !edge)
+                               ? tile_logits<4, true, false>(tS, x, scale, rowc, kk, 0)
+                               : tile_logits<4, false, false>(tS, x, scale, rowc, 0.f, 0);
+          tc_fence_before();
+          mbar_arrive(s_read + t);  // S is in registers: the next one may be computed
+          if (i == 0) {
+            m = mx;
+          } else {
+            const bool fresh = m == -INFINITY;  // no key of this row so far
+            const bool need = fresh ? mx != -INFINITY : mx > m + 32.0f;
+            // P and O are still read by the previous P V
+            ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
+            if (!ok) break;
+            tc_fence_after();
+            if (__any_sync(0xffffffffu, need)) {
+              const float f = need ? (fresh ? 0.f : ex2(m - mx)) : 1.0f;
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + c * 32, o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st32(tO + c * 32, o);
+              }
+              if (need) {
+                l *= f;
+                m = mx;
+              }
+            }
+          }
           const float m_use = m == -INFINITY ? 0.f : m;
-          fwd_exp_pass<true>(x, f2_pack(m_use, m_use), tP, sum2);
-        } else if (__any_sync(0xffffffffu, sub != 0.f)) {
-          fwd_exp_pass<true>(x, f2_pack(sub, sub), tP, sum2);
+          tile_exp<4, true>(x, f2_pack(m_use, m_use), tP, sum2);
         } else {
-          fwd_exp_pass<false>(x, 0, tP, sum2);
+        const uint32_t tP = tS + 64 * (gi & 1);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          ok = warp_wait(s_full + 2 * t + half, gi & 1, wd);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tH = tS + 64 * ((gi & 1) ^ half);
+          const int c0 = 64 * half;
+          const float m_ref = m == -INFINITY ? 0.f : m;
+          uint32_t x[2][32];
+          float mx;
+          if (near) {
+            tile_edge<64, true>(tH, p.scale_log2, 0.f, 0.f, lut + (ks + c0 - qpos - p.bias.lut_lo), tab,
+                                p.hq, slope, ks + c0 - qpos, lim - c0);
+            mx = tile_logits<2, false, false>(tH, x, 1.f, -m_ref, 0.f, 0);
+          } else {
+            const float rc = fmaf(kk, (float)c0, rowc) - m_ref;
+#define FAT_TILE_LOGITS(LINEAR, MASK) \
+  tile_logits<2, LINEAR, MASK>(tH, x, p.scale_log2, rc, kk, lim - c0)
+            if (has_slopes)
+              mx = need_mask ? FAT_TILE_LOGITS(true, true) : FAT_TILE_LOGITS(true, false);
+            else
+              mx = need_mask ? FAT_TILE_LOGITS(false, true) : FAT_TILE_LOGITS(false, false);
+#undef FAT_TILE_LOGITS
+          }
+          if (half == 1) {  // it is in registers: the next S may be computed there
+            tc_fence_before();
+            mbar_arrive(s_read + t);
+          }
+          float sub = 0.f;  // what the exponentials still subtract
+          bool need = false;
+          if (m == -INFINITY) {  // no key of this row so far: what was summed is zero
+            if (mx != -INFINITY) m = sub = mx;
+          } else {
+            pend = fmaxf(pend, mx);
+            need = pend > (half == 0 ? 32.f : 96.f);
+          }
+          if (__any_sync(0xffffffffu, need)) {
+            const float f = need ? ex2(-pend) : 1.f;
+            if (i > 0) {  // O, once the products so far are complete
+              ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + c, o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st32(tO + c, o);
+              }
+            }
+            if (half == 1) {  // P of the first half
+              tmem_st_wait();
+              uint32_t o[32];
+              tmem_ld32(tP, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                o[k] = pack_bf16x2(__uint_as_float(o[k] << 16) * f,
+                                   __uint_as_float(o[k] & 0xffff0000u) * f);
+              tmem_st32(tP, o);
+            }
+            l *= f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum2[k] = f2_mul(sum2[k], f2_pack(f, f));
+            if (need) {
+              m += pend;
+              sub = pend;
+              pend = 0.f;
+            }
+          }
+          if (__any_sync(0xffffffffu, sub != 0.f))
+            tile_exp<2, true>(x, f2_pack(sub, sub), tP + 32 * half, sum2);
+          else
+            tile_exp<2, false>(x, 0, tP + 32 * half, sum2);
+        }
+        if (!ok) break;
         }
         {
           float s0, s1, s2, s3;
@@ -708,7 +812,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       f0 *= inv;
       f1 *= inv;
       const int prow = t_row * RT + r;
+      // where this lane stores: rows 8 k + lane / 4 of the warp's, relative to the item's first head
+      __nv_bfloat16 *out0 = p.out + ((size_t)(it.row0 + t_row * tq) * p.hq + (size_t)it.hk * G) * D;
+      int to[4];
 #pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rr = (warp & 3) * 32 + 8 * k + (lane >> 2), q = rr / G;
+        to[k] = rr < RT && q < ntok ? (q * p.hq + (rr - q * G)) * D : -1;
+      }
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         __syncwarp();
@@ -723,8 +835,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f0);
         }
-        if (valid && whole) {
-          uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((size_t)row * p.hq + h) * D + c * 32);
+        if (whole) {
+          // through shared memory, so that a store covers 64 bytes of each of eight rows rather than
+          // 16 bytes of 32 (3 us less for an item's 256 rows)
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint32_t w[4];
@@ -732,8 +845,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k)
               w[k] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * k]),
                                  __uint_as_float(o[8 * v + 2 * k + 1]));
-            dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+            st_shared_v4(scratch + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2],
+                         w[3]);
           }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = 8 * k + (lane >> 2);
+            const uint4 w = ld_shared_v4(scratch + rr * 64 +
+                                         (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+            if (to[k] >= 0)
+              *reinterpret_cast<uint4 *>(out0 + (size_t)to[k] + c * 32 + (lane & 3) * 8) = w;
+          }
+          __syncwarp();
         } else if (valid) {
           float *part = part_rows<kTileRows, D>(p.part, gridDim.x, blockIdx.x, which);
 #pragma unroll
