@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // m: the row's reference, which P is relative to. It is raised (and what was summed so far
       // scaled) only when the row's maximum grows beyond it by more than 2^32, at a step's second half
-      // of S 2^96 (P of the first would have to be scaled as well; pend keeps the growth): every sum
+      // of S 2^64 (P of the first would have to be scaled as well; pend keeps the growth): every sum
       // stays far from fp32's and bf16's ends, and the result is exact.
       float m = -INFINITY, l = 0.f, pend = 0.f;
       for (int i = 0; i < steps && ok; ++i) {
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mx != -INFINITY) m = sub = mx;
           } else {
             pend = fmaxf(pend, mx);
-            need = pend > (half == 0 ? 32.f : 96.f);
+            need = pend > (half == 0 ? 32.f : 64.f);
           }
           if (__any_sync(0xffffffffu, need)) {
             const float f = need ? ex2(-pend) : 1.f;

@@ -349,6 +349,12 @@ CASES = {
     "many_chunks": dict(lq=list(np.random.default_rng(2).integers(0, 30, 500)),
                         lk=list(np.random.default_rng(3).integers(30, 90, 500)), hq=4, hkv=2, d=64,
                         page=16),
+    # logits of hundreds: the running reference moves by more than 2^32 and 2^64, in either half of a
+    # key tile, after rows without a key and with grouped heads
+    "large_logits_d128": dict(lq=[150, 40, 300], lk=[900, 500, 250], hq=4, hkv=2, d=128, page=16,
+                              std=3.0, scale=1.0),
+    "large_logits_alibi_d128": dict(lq=[130], lk=[1400], hq=3, hkv=3, d=128, page=64, alibi=True,
+                                    std=4.0, scale=1.0, causal=False),
     "large_logits": dict(lq=[1, 150], lk=[500, 400], hq=2, hkv=2, d=64, page=16, t5=T5D, std=3.0,
                          scale=1.0),
 }
