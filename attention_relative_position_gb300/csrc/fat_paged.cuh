@@ -106,17 +106,20 @@ struct TileCost {
   }
 };
 
-// SMs of the tile kernel when a call launches both kernels: in proportion to their times, a pair of
-// tiles weighing kPairStages stages (1.4 us against 0.12 us of an SM at head_dim 128, and its longer start, measured),
-// each kernel at least one. The other SMs are the few-row kernel's.
-constexpr float kPairStages = 16.f;
+// SMs n of the tile kernel when a call launches both kernels, so that they end together: with its
+// total a and the other's b in stages of the few-row kernel (a pair of tiles weighs kPairStages: 1.05 us
+// against 0.12 us of an SM at head_dim 128, measured) and its start longer by kStartStages,
+// kStartStages + a / n = b / (sms - n). Each kernel has at least one SM.
+constexpr float kPairStages = 9.f, kPairStages64 = 5.f, kStartStages = 80.f;
 template <int D>
 __device__ __forceinline__ int tile_sms(const PagedParams &p, long long tile_total,
                                         long long few_total) {
   if (!p.both || few_total == 0) return p.sms;
   if (tile_total == 0) return 0;
-  const float a = (D == 128 ? 1.f : 0.5f) * kPairStages * (float)tile_total, b = (float)few_total;
-  return min(max((int)(p.sms * (a / (a + b)) + 0.5f), 1), p.sms - 1);
+  const float a = (D == 128 ? kPairStages : kPairStages64) * (float)tile_total;
+  const float N = (float)p.sms, c = kStartStages * N - a - (float)few_total;
+  const float n = 2.f * a * N / (sqrtf(c * c + 4.f * kStartStages * a * N) - c);
+  return min(max((int)(n + 0.5f), 1), p.sms - 1);
 }
 
 // ---- partial rows -------------------------------------------------------------------------------
