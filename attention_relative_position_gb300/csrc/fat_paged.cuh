@@ -160,7 +160,7 @@ __device__ __forceinline__ float *part_stats(float *part, int ctas, int cta, int
 }
 
 // ---- this CTA's stretch -------------------------------------------------------------------------
-constexpr int kShareDocs = 128;  // requests staged in shared memory from the stretch's first on
+constexpr int kShareDocs = 64;  // requests staged in shared memory from the stretch's first on
 
 struct Share {
   long long total;   // U

@@ -4,12 +4,14 @@
 // The work is one read of the requests' keys and values; the rows ride along. A CTA (two per SM)
 // takes an equal share of all key stages (fat_paged.cuh); a stage is 8 KB of keys and values (16
 // tokens at head_dim 128, 32 at 64). Four warps compute, each on stages of its own from a ring of
-// three; a fifth warp fills the four rings, one lane per ring, by TMA (boxes of 16 rows x 64
-// channels, 128-byte swizzle: pages of 16 tokens and more are made of them), with the next stage's
-// page numbers already on their way. Per stage and warp: S = Q K^T for 16 rows with warp-level matrix products (Q in registers), bias and mask, a running maximum
-// that moves only when it grows by more than 2^32, P as bf16 in registers, O += P V. Warp-level
-// products suffice here: with 16 of 128 rows of a tcgen05 tile filled, its round trip through
-// tensor memory would cost more than the 64 products of a stage.
+// three; four more fill the rings, one each, by TMA (boxes of 16 rows x 64 channels, of 32 where
+// stage and page hold as many, 128-byte swizzle), the page numbers of many stages loaded at once.
+// One warp for the four rings, a lane each, put a stage off every 0.9 us, and short contexts waited
+// for it: one token over 500 keys 9.4 us against 7.4.
+// Per stage and warp: S = Q K^T for 16 rows with warp-level matrix products (Q in registers), bias
+// and mask, a running maximum that moves only when it grows by more than 2^32, P as bf16 in
+// registers, O += P V. Warp-level products suffice here: with 16 of 128 rows of a tcgen05 tile
+// filled, its round trip through tensor memory would cost more than the 64 products of a stage.
 // A short item (two stages at most) is one warp's; the warps of a longer one merge their rows in
 // shared memory once. Items cut by the share boundaries leave partial rows for the merge grid.
 #include <algorithm>
@@ -21,25 +23,27 @@ namespace fat {
 namespace {
 
 constexpr int kWarps = 4;          // computing warps
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kThreads = 2 * kWarps * 32;
+// registers of a thread: 128 at launch (two CTAs per SM), then split unevenly
+constexpr int kProdRegs = 56, kCompRegs = 200;
+static_assert(kProdRegs + kCompRegs <= 2 * 128, "what the block was launched with");
 constexpr int kRing = 3;           // stages per warp
 constexpr int kShortStages = 2;    // items of at most this many stages are one warp's
 constexpr int kMinShare = 8;       // stages a CTA takes at least
-constexpr int kMergeCh = 32;        // channels merged at a time
-constexpr int kOStride = kMergeCh + 8;  // floats per row of a merge buffer
 
 template <int D>
 struct FewCfg {
   static constexpr int KT = few_stage_tokens(D);  // tokens per stage
   static constexpr int DB = D / 64;              // 64-channel blocks
-  static constexpr int PIECE = 16 * 128;         // one box: 16 rows x 64 channels
-  static constexpr int PIECES = KT / 16;         // boxes per 64-channel block
+  static constexpr int LOG2_KT = D == 64 ? 5 : 4;
+  static constexpr int PIECE = 16 * 128;         // 16 rows x 64 channels
+  static constexpr int PIECES = KT / 16;         // of these per 64-channel block
   static constexpr int BLK = KT * 128;           // one 64-channel block of a stage
   static constexpr int TILE = DB * BLK;          // K or V of a stage
   static constexpr int STAGE = 2 * TILE;
   static constexpr int OFF_MERGE = kWarps * kRing * STAGE;
-  static constexpr int OFF_STATS = OFF_MERGE + kWarps * kFewRows * kOStride * 4;
-  static constexpr int OFF_BAR = OFF_STATS + (kWarps + 1) * kFewRows * 2 * 4;
+  static constexpr int OFF_STATS = OFF_MERGE + kWarps * (kWarps - 1) * 2 * 32 * 16;
+  static constexpr int OFF_BAR = OFF_STATS + kWarps * kFewRows * 2 * 4;
   static constexpr int OFF_THR = OFF_BAR + 2 * kWarps * kRing * 8 + 64;
   static constexpr int OFF_SHARE = OFF_THR + kMaxThresholds * 4;
   static constexpr int OFF_LUT = OFF_SHARE + (int)sizeof(ShareSmem<kThreads>);
@@ -48,7 +52,7 @@ struct FewCfg {
     return OFF_LUT + (b.table ? (b.sat_neg + b.sat_pos + 1 + 15) & ~15 : 0);
   }
   static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
-  static_assert(STAGE == 8192, "a stage is 8 KB");
+  static_assert(STAGE == 8192 && KT == 1 << LOG2_KT, "a stage is 8 KB");
 };
 
 // The items of a share in order.
@@ -148,14 +152,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int *abort_flag =
       reinterpret_cast<volatile int *>(sm + C::OFF_BAR + 2 * kWarps * kRing * 8);
   int *thr_s = reinterpret_cast<int *>(sm + C::OFF_THR);
-  float *stats = reinterpret_cast<float *>(sm + C::OFF_STATS);  // [warps + 1][16][2]
+  float *stats = reinterpret_cast<float *>(sm + C::OFF_STATS);  // [warps][16][2]
   grid_dep_launch();
   if (tid == 0) *abort_flag = 0;
   if (tid < 2 * kWarps * kRing) {
     mbar_init(bars + tid, 1);
     fence_mbar_init();
   }
-  if (tid == kWarps * 32) {
+  if (tid == kThreads - 32) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
@@ -184,49 +188,65 @@ __global__ void __launch_bounds__(kThreads, 2)
   const FewWalk<D> start{p, share_s, sh.doc, sh.doc, hk0, sh.hi - sh.lo,
                          (int)(sh.off - (long long)hk0 * cost0)};
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------------ producer
-    // Lane w < 4 follows warp w's stages. It never blocks on its own ring: a warp that waits for
-    // the others at the end of an item must not hold up their copies.
-    const int w = lane & (kWarps - 1);
+  if (warp >= kWarps) {
+    // ------------------------------------------------------------------ producers
+    // Warp kWarps + w fills warp w's ring. It waits on that ring alone: a warp that waits for the
+    // others at the end of an item must not hold up their copies.
+    regs_dec<kProdRegs>();
+    const int w = warp - kWarps;
     uint8_t *ring = sm + w * kRing * C::STAGE;
     uint64_t *full = bars + w * kRing, *empty = bars + (kWarps + w) * kRing;
+    const int log2_box = min(p.log2_page, C::LOG2_KT);  // rows of a copy
+    const int in_mask = (1 << p.log2_page) - 1;
     FewStages<D> ahead(start);
-    ahead.it.s1 = 0;
-    bool more = lane < kWarps && !(p.debug_flags & 1);  // test hook: no copies, the waits run out
-    bool primed = false;  // the cursor stands on a stage
-    int page[C::PIECES], slot = 0, issued = 0, phase = 1;
-    uint64_t t0 = 0;      // when this warp last got a stage off
-    while (__any_sync(0xffffffffu, more)) {
-      const bool can = more && (!primed || issued < kRing || mbar_test(empty + slot, phase));
-      if (!__any_sync(0xffffffffu, can)) {
-        __nanosleep(20);
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        if (*abort_flag || (long long)(now - t0) > p.timeout_ns) {
-          if (!*abort_flag && lane == 0) atomicOr(p.err, FAT_DEVERR_TIMEOUT_FWD);
-          *abort_flag = 1;
-          break;
-        }
-        continue;
+    int slot = 0, phase = 1;
+    bool ok = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
+    while (ok && ahead.item(w)) {
+      const FewItem &it = ahead.it;
+      if (ahead.s >= it.s1) continue;
+      // The page numbers of the item's next kBatch stages, lane PIECES j + i those of stage j's
+      // rows 16 i: loaded a batch ahead.
+      constexpr int kBatch = 32 / C::PIECES;
+      const int32_t *row = p.table + (size_t)it.doc * p.width;
+      auto pages = [&](int s) {
+        const int tok =
+            (s + (lane / C::PIECES) * ahead.step) * KT + (lane & (C::PIECES - 1)) * 16;
+        return tok < it.lk ? __ldg(row + (tok >> p.log2_page)) : 0;
+      };
+      int mine = pages(ahead.s), coming = 0;
+      {  // the item's queries (a row per two lanes) and bias table rows, towards L1
+        const int h0 = it.hk * p.group, all = it.s1 - it.s0 >= kWarps ? kWarps : 1;
+        const int r = lane >> 1, q = r / p.group;
+        if (q < it.lq && (D == 128 || (lane & 1) == 0))
+          prefetch_l1(p.q + ((size_t)(it.sq + q) * p.hq + h0 + (r - q * p.group)) * D +
+                      (lane & 1) * 64);
+        if (p.bias.table != nullptr)
+          for (int b = lane + (all > 1 ? w : 0) * 32; b < p.bias.nb; b += 32 * all)
+            prefetch_l1(p.bias.table + (size_t)b * p.hq + h0);
+        if (p.bias.slopes != nullptr && lane == 0) prefetch_l1(p.bias.slopes + h0);
       }
-      t0 = 0;
-      bool fresh = false;
-      if (can) {
-        if (primed) {
-          const int tok = ahead.s * KT, hk = ahead.it.hk;
-          const int pieces = min(C::PIECES, (ahead.it.lk - tok + 15) >> 4);
+      int j = 0;  // the stage's place in the batch
+      for (int s = ahead.s; s < it.s1; s += ahead.step) {
+        if (j == 0) coming = pages(s + kBatch * ahead.step);
+        if (!(ok = warp_wait(empty + slot, phase, wd))) break;
+        const int tok = s * KT, n = min(KT, it.lk - tok);
+        int page[C::PIECES];
+#pragma unroll
+        for (int i = 0; i < C::PIECES; ++i)
+          page[i] = __shfl_sync(0xffffffffu, mine, j * C::PIECES + i);
+        if (lane == 0) {
+          const int copies = (n + (1 << log2_box) - 1) >> log2_box;
           uint8_t *dst = ring + slot * C::STAGE;
-          mbar_arrive_expect_tx(full + slot, pieces * C::DB * 2 * C::PIECE);
+          mbar_arrive_expect_tx(full + slot, (copies << log2_box) * 2 * D * 2);
 #pragma unroll
           for (int i = 0; i < C::PIECES; ++i) {
-            if (i >= pieces) break;
+            if (i >= copies) break;
             if ((unsigned)page[i] >= (unsigned)p.num_pages) {
               atomicOr(p.err, FAT_DEVERR_PAGES);
               page[i] = p.num_pages;  // just outside: filled with zeros
             }
-            const int in = (tok + i * 16) & ((1 << p.log2_page) - 1);
-            const int c1 = p.head_outer ? in : hk, c2 = p.head_outer ? hk : in;
+            const int in = (tok + (i << log2_box)) & in_mask;
+            const int c1 = p.head_outer ? in : it.hk, c2 = p.head_outer ? it.hk : in;
 #pragma unroll
             for (int b = 0; b < C::DB; ++b) {
               uint8_t *d = dst + i * C::PIECE + b * C::BLK;
@@ -234,47 +254,16 @@ __global__ void __launch_bounds__(kThreads, 2)
               tma_load_4d(&tm_v, full + slot, d + C::TILE, 64 * b, c1, c2, page[i]);
             }
           }
-          ++issued;
-          if (++slot == kRing) {
-            slot = 0;
-            phase ^= 1;
-          }
-          ahead.s += ahead.step;
         }
-        primed = true;
-        while (ahead.s >= ahead.it.s1) {  // on to an item that has a stage for this warp
-          fresh = true;
-          if (!ahead.item(w)) {
-            more = false;
-            break;
-          }
+        __syncwarp();
+        if (++slot == kRing) {
+          slot = 0;
+          phase ^= 1;
         }
-        fresh = fresh && more;
-        if (more) {  // the page numbers of the stage the cursor stands on
-#pragma unroll
-          for (int i = 0; i < C::PIECES; ++i) {
-            const int tok = ahead.s * KT + i * 16;
-            page[i] = tok < ahead.it.lk ? __ldg(p.table + (size_t)ahead.it.doc * p.width +
-                                                (tok >> p.log2_page))
-                                        : 0;
-          }
+        if (++j == kBatch) {
+          j = 0;
+          mine = coming;
         }
-      }
-      // an item's queries (a row per two lanes) and bias table rows, towards L1
-      const unsigned who = __ballot_sync(0xffffffffu, fresh);
-      if (who) {
-        const int src = __ffs(who) - 1;
-        const int sq = __shfl_sync(0xffffffffu, ahead.it.sq, src);
-        const int lq = __shfl_sync(0xffffffffu, ahead.it.lq, src);
-        const int h0 = __shfl_sync(0xffffffffu, ahead.it.hk, src) * p.group;
-        const int r = lane >> 1, q = r / p.group;
-        if (q < lq && (D == 128 || (lane & 1) == 0))
-          prefetch_l1(p.q + ((size_t)(sq + q) * p.hq + h0 + (r - q * p.group)) * D +
-                      (lane & 1) * 64);
-        if (p.bias.table != nullptr)
-          for (int b = lane; b < p.bias.nb; b += 32)
-            prefetch_l1(p.bias.table + (size_t)b * p.hq + h0);
-        if (p.bias.slopes != nullptr && lane == 0) prefetch_l1(p.bias.slopes + h0);
       }
     }
     if (*abort_flag) {  // copies may still be on their way: give them time to land
@@ -284,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     grid_dep_wait();  // as at the end of the other warps
     return;
   }
+  regs_inc<kCompRegs>();
   uint8_t *ring = sm + warp * kRing * C::STAGE;
   uint64_t *full = bars + warp * kRing, *empty = bars + (kWarps + warp) * kRing;
 
@@ -526,79 +516,87 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       continue;
     }
-    // merge of the four warps
+    // Merge of the four warps: each takes a quarter of every 64 channels (16: two of its fragments'
+    // blocks of 8) from the other three, which leave theirs, scaled to the common maximum, as they
+    // hold them (a thread's rows and columns are the same in every warp: no transposition).
     if ((lane & 3) == 0) {
       *reinterpret_cast<float2 *>(stats + (warp * kFewRows + r0) * 2) = make_float2(m[0], l[0]);
       *reinterpret_cast<float2 *>(stats + (warp * kFewRows + r1) * 2) = make_float2(m[1], l[1]);
     }
     named_bar_sync(1, kWarps * 32);
-    float f[2];
+    float f[2], M[2], L[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = i ? r1 : r0;
-      float M = -INFINITY, L = 0.f;
+      M[i] = -INFINITY;
+      L[i] = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stats[(w * kFewRows + r) * 2]);
+      for (int w = 0; w < kWarps; ++w) M[i] = fmaxf(M[i], stats[(w * kFewRows + r) * 2]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 v = *reinterpret_cast<const float2 *>(stats + (w * kFewRows + r) * 2);
-        if (v.x != -INFINITY) L += v.y * ex2(v.x - M);
+        if (v.x != -INFINITY) L[i] += v.y * ex2(v.x - M[i]);
       }
-      f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - M);
-      if (warp == 0 && (lane & 3) == 0) {
-        float *fin = stats + (kWarps * kFewRows + r) * 2;
-        fin[0] = M;
-        fin[1] = L;
-      }
+      f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - M[i]);
     }
-    float *buf = reinterpret_cast<float *>(sm + C::OFF_MERGE);
-    const float *fin = stats + kWarps * kFewRows * 2;
+    float4 *buf = reinterpret_cast<float4 *>(sm + C::OFF_MERGE);  // [to][from][2][32]
 #pragma unroll
-    for (int b = 0; b < D / kMergeCh; ++b) {
+    for (int b = 0; b < C::DB; ++b) {
+      if (b > 0) named_bar_sync(1, kWarps * 32);  // the block before has been read
+      float4 own[2];
 #pragma unroll
-      for (int t = 0; t < kMergeCh / 8; ++t) {
-        const int ot = b * (kMergeCh / 8) + t;
-        float *dst = buf + warp * kFewRows * kOStride + t * 8 + 2 * (lane & 3);
-        *reinterpret_cast<float2 *>(dst + r0 * kOStride) =
-            make_float2(o[ot][0] * f[0], o[ot][1] * f[0]);
-        *reinterpret_cast<float2 *>(dst + r1 * kOStride) =
-            make_float2(o[ot][2] * f[1], o[ot][3] * f[1]);
+      for (int t = 0; t < 8; ++t) {
+        const int w = t >> 1, ot = 8 * b + t;
+        const float4 v =
+            make_float4(o[ot][0] * f[0], o[ot][1] * f[0], o[ot][2] * f[1], o[ot][3] * f[1]);
+        if (w == warp)
+          own[t & 1] = v;
+        else
+          buf[((w * (kWarps - 1) + ((warp - w - 1) & (kWarps - 1))) * 2 + (t & 1)) * 32 + lane] = v;
       }
       named_bar_sync(1, kWarps * 32);
-      static_assert(kFewRows * kMergeCh / 4 == kWarps * 32, "one quad of channels per thread");
-      const int r = whole ? tid / (kMergeCh / 4) : tid % kFewRows;
-      const int c = 4 * (whole ? tid % (kMergeCh / 4) : tid / kFewRows);
-      if (r < rows) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        // in the order of the warps, whichever of them adds
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float4 v =
-              *reinterpret_cast<const float4 *>(buf + (w * kFewRows + r) * kOStride + c);
+              w == warp ? own[t]
+                        : buf[((warp * (kWarps - 1) + ((w - warp - 1) & (kWarps - 1))) * 2 + t) *
+                                  32 + lane];
           a.x += v.x;
           a.y += v.y;
           a.z += v.z;
           a.w += v.w;
         }
-        const float M = fin[r * 2], L = fin[r * 2 + 1];
-        const int ch = b * kMergeCh + c;
-        if (whole) {
-          const int q = r / G, h = it.hk * G + (r - q * G), row = it.sq + q;
-          const float inv = L > 0.f ? 1.0f / L : 0.f;
-          *reinterpret_cast<uint2 *>(p.out + ((size_t)row * p.hq + h) * D + ch) =
-              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-          if (ch == 0 && p.lse != nullptr)
-            p.lse[(size_t)h * p.total_q + row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
-        } else {
-          *part_quad<kFewRows>(part_rows<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which), r,
-                               ch / 4) = a;
-          if (ch == 0)
-            *reinterpret_cast<float2 *>(
-                part_stats<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which) + r * 2) =
-                make_float2(M, L);
+        const int ch = 64 * b + 16 * warp + 8 * t + 2 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = i ? r1 : r0;
+          const float x = i ? a.z : a.x, y = i ? a.w : a.y;
+          if (r >= rows) continue;
+          if (whole) {
+            const int q = r / G, h = it.hk * G + (r - q * G), row = it.sq + q;
+            const float inv = L[i] > 0.f ? 1.0f / L[i] : 0.f;
+            *reinterpret_cast<uint32_t *>(p.out + ((size_t)row * p.hq + h) * D + ch) =
+                pack_bf16x2(x * inv, y * inv);
+            if (ch == 0 && p.lse != nullptr)
+              p.lse[(size_t)h * p.total_q + row] =
+                  L[i] > 0.f ? (M[i] + __log2f(L[i])) * kLn2 : -INFINITY;
+          } else {
+            reinterpret_cast<float2 *>(
+                part_quad<kFewRows>(part_rows<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which),
+                                    r, ch >> 2))[lane & 1] = make_float2(x, y);
+            if (ch == 0)
+              *reinterpret_cast<float2 *>(
+                  part_stats<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which) + r * 2) =
+                  make_float2(M[i], L[i]);
+          }
         }
       }
-      named_bar_sync(1, kWarps * 32);  // buf (and, after the last block, stats) are written again
     }
+    // (the next merge writes buf only after its first barrier, stats only after this one's last)
   }
   // A grid that was started beside the tile kernel's ends after it, so that the merge grids, which
   // wait for this one, find both complete (returns at once when there is none before).
@@ -609,8 +607,9 @@ template <int D>
 int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
   PagedParams pp = p;
   CUtensorMap mk, mv;
-  int rc = make_tmap_pages(&mk, c.k, c, 16, &pp.head_outer);
-  if (!rc) rc = make_tmap_pages(&mv, c.v, c, 16, &pp.head_outer);
+  const int rows = std::min(1 << pp.log2_page, FewCfg<D>::KT);
+  int rc = make_tmap_pages(&mk, c.k, c, rows, &pp.head_outer);
+  if (!rc) rc = make_tmap_pages(&mv, c.v, c, rows, &pp.head_outer);
   if (rc) return rc;
   const size_t smem = FewCfg<D>::bytes(p.bias) + 1024;
   if (prepare_kernel((const void *)fat_paged_few_kernel<D>, smem, kThreads, 0)) return FAT_ECUDA;
