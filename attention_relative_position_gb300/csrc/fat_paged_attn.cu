@@ -78,7 +78,7 @@ __device__ __forceinline__ void merge_chain(const PagedParams &p, float *part, i
         }
 #pragma unroll
         for (int b = 0; b < kMergeBatch; ++b) {
-          if (st[b].x == -INFINITY) continue;  // no key in this part
+          if (st[b].x == -INFINITY && st[b].y == 0.f) continue;  // no key here (a NaN's sum is NaN)
           const float mn = fmaxf(m, st[b].x);
           const float fo = m == -INFINITY ? 0.f : ex2(m - mn), fn = ex2(st[b].x - mn);
           l = l * fo + st[b].y * fn;
@@ -112,14 +112,14 @@ __device__ __forceinline__ void merge_chain(const PagedParams &p, float *part, i
       }
     }
     if (r >= rec.rows) continue;
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
     const int q = r / p.group, h = rec.hk * p.group + (r - q * p.group);
     const size_t row = (size_t)rec.row0 + q;
     *reinterpret_cast<uint4 *>(p.out + (row * p.hq + h) * D + q0 * 4) =
         make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
                    pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
     if (q0 == 0 && p.lse != nullptr)
-      p.lse[(size_t)h * p.total_q + row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      p.lse[(size_t)h * p.total_q + row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
   }
 }
 

@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (r >= rows) continue;
         const int q = r / G, h = it.hk * G + (r - q * G), row = it.sq + q;
         if (whole) {
-          const float inv = l[i] > 0.f ? 1.0f / l[i] : 0.f;
+          const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
           uint32_t *dst =
               reinterpret_cast<uint32_t *>(p.out + ((size_t)row * p.hq + h) * D) + (lane & 3);
 #pragma unroll
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             dst[t * 4] = pack_bf16x2(o[t][2 * i] * inv, o[t][2 * i + 1] * inv);
           if ((lane & 3) == 0 && p.lse != nullptr)
             p.lse[(size_t)h * p.total_q + row] =
-                l[i] > 0.f ? (m[i] + __log2f(l[i])) * kLn2 : -INFINITY;
+                l[i] == 0.f ? -INFINITY : (m[i] + __log2f(l[i])) * kLn2;
         } else {
 #pragma unroll
           for (int t = 0; t < D / 8; ++t)
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 v = *reinterpret_cast<const float2 *>(stats + (w * kFewRows + r) * 2);
-        if (v.x != -INFINITY) L[i] += v.y * ex2(v.x - M[i]);
+        L[i] += v.y * (v.x == -INFINITY ? 0.f : ex2(v.x - M[i]));  // (0 * NaN stays NaN)
       }
       f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - M[i]);
     }
@@ -578,12 +578,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (r >= rows) continue;
           if (whole) {
             const int q = r / G, h = it.hk * G + (r - q * G), row = it.sq + q;
-            const float inv = L[i] > 0.f ? 1.0f / L[i] : 0.f;
+            const float inv = L[i] == 0.f ? 0.f : 1.0f / L[i];
             *reinterpret_cast<uint32_t *>(p.out + ((size_t)row * p.hq + h) * D + ch) =
                 pack_bf16x2(x * inv, y * inv);
             if (ch == 0 && p.lse != nullptr)
               p.lse[(size_t)h * p.total_q + row] =
-                  L[i] > 0.f ? (M[i] + __log2f(L[i])) * kLn2 : -INFINITY;
+                  L[i] == 0.f ? -INFINITY : (M[i] + __log2f(L[i])) * kLn2;
           } else {
             reinterpret_cast<float2 *>(
                 part_quad<kFewRows>(part_rows<kFewRows, D>(p.part, gridDim.x, blockIdx.x, which),

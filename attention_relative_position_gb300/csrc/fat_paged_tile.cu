@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) continue;
       tc_fence_after();
-      const float inv = whole ? (l > 0.f ? 1.0f / l : 0.f) : 1.f;
+      const float inv = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
       f0 *= inv;
       f1 *= inv;
       const int prow = t_row * RT + r;
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               part_stats<kTileRows, D>(p.part, gridDim.x, blockIdx.x, which) + prow * 2) =
               make_float2(m, l);
         else if (p.lse != nullptr)
-          p.lse[(size_t)h * p.total_q + row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+          p.lse[(size_t)h * p.total_q + row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
       }
     }
   }

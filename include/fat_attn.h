@@ -448,7 +448,9 @@ int fat_paged_append(const fat_append_shape_t *shape, const fat_paged_cache_t *c
  *   - What lies in a page behind a request's last key is never used, whatever it holds (NaN and
  *     infinities included). Keys and values below seqlens_k are finite: a value that the causal
  *     mask hides from an earlier query of the same step still enters that query's product with
- *     weight 0.
+ *     weight 0. A NaN in a query, or in a key it sees, makes its output and lse NaN.
+ *   - A bias of -infinity (or below -2e38: logits are formed times log2 e) masks its keys; a row
+ *     that is left with none gets 0 and lse -infinity.
  *   - A page index outside [0, num_pages) sets FAT_DEVERR_PAGES; its keys and values count as 0.
  *   - A request whose query count exceeds max_seqlen_q or whose seqlens_k is negative, exceeds
  *     max_seqlen_k or its table row (table_width pages) sets FAT_DEVERR_SEQLENS, as does a corrupt
@@ -457,9 +459,10 @@ int fat_paged_append(const fat_append_shape_t *shape, const fat_paged_cache_t *c
  *     initialised), for this call alone until it has finished: calls that may overlap, and captured
  *     graphs that do, take one each.
  * head_dim 64 or 128, num_heads_q / num_heads at most 128, max_seqlen_k at most 2^30.
- * FAT_EUNSUPPORTED: more query heads per key/value head, longer bounds, bias tables that shared memory does not hold (saturation distances of more
- * than 8192 keys in all, or num_buckets * num_heads_q / num_heads beyond 4096 entries), or cache
- * strides of which, in rising order, one is no multiple of the one before.
+ * FAT_EUNSUPPORTED: more query heads per key/value head, longer bounds, bias tables that shared
+ * memory does not hold (saturation distances of more than 8192 keys in all, or num_buckets *
+ * num_heads_q / num_heads beyond 4096 entries), or cache strides of which, in rising order, one is
+ * no multiple of the one before.
  */
 typedef struct {
   int32_t total_q;      /* rows of q and out */

@@ -430,6 +430,72 @@ def test_attention_bad_page_counts_as_zeros(name, bad):
     p.check(out, lse)
 
 
+NAN_CASES = {
+    "decode_whole": dict(lq=[1, 1, 1], lk=[40, 700, 64], hq=4, hkv=2, d=64, page=16),
+    "decode_cut_d128": dict(lq=[1, 4], lk=[30000, 9000], hq=8, hkv=2, d=128, page=64, alibi=True),
+    "chunk_d64": dict(lq=[200, 40], lk=[5000, 41], hq=4, hkv=4, d=64, page=32),
+    "chunk_cut_d128": dict(lq=[150, 60], lk=[6000, 700], hq=4, hkv=2, d=128, page=16),
+}
+
+
+@pytest.mark.parametrize("name", NAN_CASES)
+def test_attention_nan_queries_and_keys_show(name):
+    """A NaN query leaves its own row NaN, a NaN key every row that sees it; no other row changes."""
+    p = Problem(seed=51, **NAN_CASES[name])
+    want, wl = p.run()
+    row, h = p.total - 1, 1
+    p.q[row, h, 5] = float("nan")
+    out, lse = p.run()
+    assert out[row, h].isnan().all() and lse[h, row].isnan()
+    keep = torch.ones(p.total, p.hq, dtype=torch.bool, device=DEV)
+    keep[row, h] = False
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse.t()[keep], wl.t()[keep])
+    p = Problem(seed=51, **NAN_CASES[name])
+    key = int(p.lk[0]) - int(p.lq[0])  # the first query's own position: every query sees it
+    p.kc[int(p.table[0, key // p.page]), key % p.page, 0, 9] = float("nan")
+    out, lse = p.run()
+    group, n = p.hq // p.hkv, int(p.lq[0])
+    assert out[:n, :group].isnan().all() and lse[:group, :n].isnan().all()
+    keep = torch.ones(p.total, p.hq, dtype=torch.bool, device=DEV)
+    keep[:n, :group] = False
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse.t()[keep], wl.t()[keep])
+    assert _errors() == 0
+
+
+@pytest.mark.parametrize("low", [-float("inf"), float(np.finfo(np.float32).min)])
+@pytest.mark.parametrize("case", [
+    dict(lq=[1, 1, 3], lk=[900, 5, 3000], hq=4, hkv=2, d=64, page=16, t5=T5D, alibi=True),
+    dict(lq=[1] * 3, lk=[2000, 10, 90], hq=8, hkv=2, d=128, page=16, t5=T5D),
+    dict(lq=[130, 300], lk=[2500, 300], hq=4, hkv=2, d=64, page=16, t5=T5D),
+    dict(lq=[130, 300], lk=[2500, 300], hq=4, hkv=2, d=128, page=16, t5=T5B, causal=False),
+], ids=["few_d64", "few_d128", "tile_d64", "tile_d128"])
+def test_attention_bias_that_masks(case, low):
+    """Table entries of -infinity (or the type's lowest value): their keys are masked; a head with
+    nothing else has no keys at all. The oracle gets -1e6 instead, whose weights are exactly 0
+    beside any other key; rows of such keys alone are told by their lse. Tolerances as in check."""
+    p = Problem(seed=52, **case)
+    p.bias[3] = -1e6          # near keys
+    p.bias[-1, 1] = -1e6      # the far side, one head
+    p.bias[:, 2] = -1e6       # a head without a key
+    ro, rl, a, s, _ = p.oracle()
+    b = float(p.bias[p.bias > -1e5].abs().max())
+    if p.slopes is not None:
+        b += float(p.slopes.max()) * 3100
+    p.bias[p.bias == -1e6] = low
+    out, lse = p.run()
+    assert _errors() == 0
+    got, gl = _wide(out), lse.cpu().numpy().astype(np.float64)
+    none = rl < -1e5
+    assert none[2].all() and not none[0].any()
+    assert (gl[none] == -np.inf).all() and (got.transpose(1, 0, 2)[none] == 0).all()
+    ex = (p.d * s + 4 * (s + b)) * 2.0 ** -24
+    keep = ~none.T
+    tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2 * ex + 2.0 ** -18) * a * 1.01 + 1e-30
+    assert (np.abs(got - ro)[keep] <= tol[keep]).all()
+    ltol = ex + 2.0 ** -18 + 2.0 ** -22 * np.abs(rl[~none])
+    assert (np.abs(gl[~none] - rl[~none]) <= ltol).all()
+
+
 def test_attention_corrupt_lengths_leave_their_rows():
     for name in ("decode_t5_ragged", "mixed", "chunk_group5_d128"):
         for what in ("long", "negative", "bound", "queries"):
