@@ -95,12 +95,22 @@ bool truth(PyObject *o) {
   if (v < 0) throw Refused{};
   return v != 0;
 }
-void *stream_of(PyObject *o, int dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-  void *s = PyLong_AsVoidPtr(o);
-  if (!s && PyErr_Occurred()) throw Refused{};
-  return s;
-}
+// The call's stream. A given one is the current one while this lives: results and workspaces are
+// allocated on it, so that their memory is taken and given back in its order.
+struct OnStream {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  void *stream;
+  OnStream(PyObject *o, int dev) {
+    if (o == Py_None) {
+      stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+      return;
+    }
+    stream = PyLong_AsVoidPtr(o);
+    if (!stream && PyErr_Occurred()) throw Refused{};
+    guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream),
+                                                        (c10::DeviceIndex)dev));
+  }
+};
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)dev));
 }
@@ -191,7 +201,8 @@ ENTRY(plan, 13)
   sh.num_free = small(tensor(a[2], "free_pages").numel(), "free_pages");
   sh.max_tokens = max_tokens;
   int32_t *pt = ints(a[3], "block_table", -1, dev);
-  sh.stream = stream_of(a[12], dev);
+  const OnStream on(a[12], dev);
+  sh.stream = on.stream;
   static const char *const names[5] = {"cu_seqlens_q", "seqlens_k", "positions", "slots", "counts"};
   const int64_t sizes[5] = {num + 1, num, max_tokens < 0 ? 0 : max_tokens,
                             max_tokens < 0 ? 0 : max_tokens, 2};
@@ -223,6 +234,7 @@ ENTRY(rope, 6)
   check_rows(x, "x", 3, -1);
   const int dev = x.get_device();
   const Rope rope(a[2]);
+  const OnStream on(a[5], dev);
   at::Tensor made;
   if (a[4] == Py_None) made = make(x.sizes(), at::kBFloat16, dev);
   const at::Tensor &y = made.defined() ? made : tensor(a[4], "out");
@@ -236,7 +248,7 @@ ENTRY(rope, 6)
   sh.x_stride_head = x.stride(1);
   sh.y_stride_token = y.stride(0);
   sh.y_stride_head = y.stride(1);
-  sh.stream = stream_of(a[5], dev);
+  sh.stream = on.stream;
   const int32_t *pos = ints(a[1], "positions", x.size(0), dev);
   const int inverse = truth(a[3]) ? 1 : 0;
   const int rc = call_on(
@@ -262,7 +274,8 @@ ENTRY(append, 10)
   sh.k_stride_head = k.stride(1);
   sh.v_stride_token = v.stride(0);
   sh.v_stride_head = v.stride(1);
-  sh.stream = stream_of(a[9], dev);
+  const OnStream on(a[9], dev);
+  sh.stream = on.stream;
   const void *pq = nullptr;
   void *po = nullptr;
   at::Tensor made;
@@ -344,8 +357,8 @@ ENTRY(attn, 19)
   const float *slopes = a[12] == Py_None ? nullptr : floats(a[12], "alibi_slopes", {Hq}, dev);
   const int bidir = truth(a[11]) ? 1 : 0, causal = truth(a[13]) ? 1 : 0;
   const float scale = (float)number(a[14]);
-  const fat_paged_shape_t sh =
-      attn_shape(q, num, table.size(1), a[6], a[7], stream_of(a[18], dev));
+  const OnStream on(a[18], dev);
+  const fat_paged_shape_t sh = attn_shape(q, num, table.size(1), a[6], a[7], on.stream);
   at::Tensor out, lse, ws;
   void *po;
   float *pl;

@@ -537,6 +537,31 @@ def test_attention_corrupt_lengths_leave_their_rows():
         assert _errors() == fa.FAT_DEVERR_SEQLENS
 
 
+def test_results_and_workspace_belong_to_the_given_stream():
+    """A call on another stream than the current one: what it allocates is not handed out again
+    before it has run."""
+    p = Problem(seed=61, **CASES["chunk_group8_long"])
+    want, wl = p.run()
+    rope = fa.fat_rope_init(128)
+    pos = torch.arange(p.total, dtype=torch.int32, device=DEV)
+    turned = fa.fat_rope_embed(p.q, pos, rope)
+    arrays = p.arrays()
+    size = fa.fat_paged_attn_workspace_size(p.q, p.kc, arrays[1], int(max(p.lq)), int(max(p.lk)))
+    assert size > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(5_000_000)
+        out, lse = p.run(arrays=arrays, stream=side)
+        y = fa.fat_rope_embed(p.q, pos, rope, stream=side)
+        held = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all((h == 7).all() for h in held)
+        assert torch.equal(out, want) and torch.equal(lse, wl) and torch.equal(y, turned)
+        del held, out, lse, y
+
+
 def test_attention_on_streams_and_from_graphs():
     """Two calls at once on their own streams and workspaces; a captured call replayed with other
     lengths, tables and queries."""
