@@ -349,6 +349,8 @@ CASES = {
     "many_chunks": dict(lq=list(np.random.default_rng(2).integers(0, 30, 500)),
                         lk=list(np.random.default_rng(3).integers(30, 90, 500)), hq=4, hkv=2, d=64,
                         page=16),
+    "million_keys": dict(lq=[1, 1], lk=[1 << 20, 900001], hq=2, hkv=1, d=64, page=256, t5=T5D),
+    "chunk_long_context": dict(lq=[20], lk=[300007], hq=2, hkv=2, d=128, page=4096, alibi=True),
     # logits of hundreds: the running reference moves by more than 2^32 and 2^64, in either half of a
     # key tile, after rows without a key and with grouped heads
     "large_logits_d128": dict(lq=[150, 40, 300], lk=[900, 500, 250], hq=4, hkv=2, d=128, page=16,
@@ -535,6 +537,43 @@ def test_attention_corrupt_lengths_leave_their_rows():
         fa.fat_paged_attn(p.q, p.kc, p.vc, _i32(p.table), _i32(cu), _i32(p.lk), 250, 2000,
                           **p.kwargs())
         assert _errors() == fa.FAT_DEVERR_SEQLENS
+
+
+def test_caches_and_rows_beyond_32_bits():
+    """Caches of more than 2^32 elements and rows of more than 2^31: bit for bit the results of
+    the same requests in a small cache, and of the same rows alone."""
+    pages, page, hkv, d = (1 << 18) + 64, 64, 2, 128
+    kc, vc = (torch.empty((pages, page, hkv, d), dtype=torch.bfloat16, device=DEV)
+              for _ in range(2))
+    assert kc.numel() > 1 << 32
+    for name, lq, lk in (("few", [1, 2, 1], [3000, 200, 65]), ("tile", [90, 40], [1500, 41])):
+        p = Problem(lq=lq, lk=lk, hq=8, hkv=hkv, d=d, page=page, seed=63)
+        want, wl = p.run()
+        # the small cache's pages spread over the large one, the last page among them
+        to = np.linspace(pages - 1, 0, p.pages).astype(np.int64)
+        kc[torch.as_tensor(to)] = p.kc
+        vc[torch.as_tensor(to)] = p.vc
+        table = np.where(p.table < p.pages, to[np.minimum(p.table, p.pages - 1)], 0)
+        _, cu, lens = p.arrays()
+        out, lse = fa.fat_paged_attn(p.q, kc, vc, _i32(table), cu, lens, int(max(lq)),
+                                     int(max(lk)), **p.kwargs())
+        assert torch.equal(out, want) and torch.equal(lse, wl), name
+    rng = np.random.default_rng(64)
+    k = _bf16(rng, 5, hkv, d)
+    slots = _i32([pages * page - 1, (1 << 24) + 3, 17, pages * page - 64, 1 << 23])
+    fa.fat_paged_append(k, k, kc, vc, slots)
+    assert torch.equal(kc.view(-1, hkv, d)[slots.long()], k)
+    assert torch.equal(vc.view(-1, hkv, d)[slots.long()], k)
+    assert _errors() == 0
+    del kc, vc
+    x = torch.zeros((1 << 18) + 100, 64, 128, dtype=torch.bfloat16, device=DEV)
+    assert x.numel() > 1 << 31
+    x[-3:] = _bf16(rng, 3, 64, 128)
+    pos = torch.arange(x.shape[0], dtype=torch.int32, device=DEV)
+    rope = fa.fat_rope_init(128, interleaved=False)
+    want = fa.fat_rope_embed(x[-3:].clone(), pos[-3:].clone(), rope)
+    fa.fat_rope_embed(x, pos, rope, out=x)
+    assert torch.equal(x[-3:], want) and (x[:-3] == 0).all()
 
 
 def test_results_and_workspace_belong_to_the_given_stream():
