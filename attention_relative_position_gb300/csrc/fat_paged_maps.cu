@@ -242,6 +242,24 @@ __global__ void __launch_bounds__(kRowThreads) fat_rows_kernel(const __grid_cons
   const bool turned = u < p.pair_units;
   const bool two = !PAIRS && turned;
   const int chunk = (PAIRS || turned) ? u : u + p.pair_units;
+  // this thread's heads: `left` of them, of all segments in a row, from head h0 of segment sg on
+  int sg = 0, h0 = blockIdx.y * p.run, left = min(p.run, p.all_heads - h0);
+  while (h0 >= p.seg[sg].heads) h0 -= p.seg[sg++].heads;
+  int n = min(left, p.seg[sg].heads - h0);  // of them in this segment
+  const uint16_t *src =
+      p.seg[sg].src + (long long)t * p.seg[sg].src_tok + h0 * p.seg[sg].src_head + chunk * 8;
+  uint4 lo[kRowBatch], hi[kRowBatch];
+  auto load = [&]() {
+    const long long step = p.seg[sg].src_head;
+#pragma unroll
+    for (int b = 0; b < kRowBatch; ++b)
+      if (b < n) {
+        lo[b] = *reinterpret_cast<const uint4 *>(src + b * step);
+        if (two) hi[b] = *reinterpret_cast<const uint4 *>(src + b * step + p.half_chunks * 8);
+      }
+  };
+  // The first heads' rows are on their way while the angles are computed.
+  load();
   float2 cs[8];
   if (turned) {
     // negative positions wrap in two's complement: still exact modulo one turn
@@ -255,15 +273,8 @@ __global__ void __launch_bounds__(kRowThreads) fat_rows_kernel(const __grid_cons
       cs[k] = make_float2(cn * p.rope.amplitude, sn * p.sign * p.rope.amplitude);
     }
   }
-  int h0 = blockIdx.y * p.run, left = min(p.run, p.all_heads - h0);  // heads of all segments in a row
-  for (int sg = 0; left > 0; ++sg) {
+  while (true) {
     const RowSeg &s = p.seg[sg];
-    if (h0 >= s.heads) {
-      h0 -= s.heads;
-      continue;
-    }
-    const int n = min(left, s.heads - h0);
-    const uint16_t *src = s.src + (long long)t * s.src_tok + h0 * s.src_head + chunk * 8;
     long long row = (long long)t * s.dst_tok;
     bool keep = true;
     if (s.to_slots) {
@@ -275,34 +286,32 @@ __global__ void __launch_bounds__(kRowThreads) fat_rows_kernel(const __grid_cons
       if (slot >= p.num_slots) atomicOr(p.err, FAT_DEVERR_INDEX);
     }
     uint16_t *dst = s.dst + row + h0 * s.dst_head + chunk * 8;
-    if (keep) {
-      const bool turn = turned && s.rotate;
-      for (int h = 0; h < n; h += kRowBatch) {
-        uint4 lo[kRowBatch], hi[kRowBatch];
-#pragma unroll
-        for (int b = 0; b < kRowBatch; ++b)
-          if (h + b < n) {
-            lo[b] = *reinterpret_cast<const uint4 *>(src + b * s.src_head);
-            if (two) hi[b] = *reinterpret_cast<const uint4 *>(src + b * s.src_head + p.half_chunks * 8);
-          }
-#pragma unroll
-        for (int b = 0; b < kRowBatch; ++b)
-          if (h + b < n) {
-            if (turn) {
-              if constexpr (PAIRS)
-                lo[b] = rotate_pairs(lo[b], cs);
-              else
-                rotate_halves(lo[b], hi[b], cs);
-            }
-            *reinterpret_cast<uint4 *>(dst + b * s.dst_head) = lo[b];
-            if (two) *reinterpret_cast<uint4 *>(dst + b * s.dst_head + p.half_chunks * 8) = hi[b];
-          }
-        src += kRowBatch * s.src_head;
-        dst += kRowBatch * s.dst_head;
-      }
-    }
+    const bool turn = turned && s.rotate;
     left -= n;
+    while (keep) {
+#pragma unroll
+      for (int b = 0; b < kRowBatch; ++b)
+        if (b < n) {
+          if (turn) {
+            if constexpr (PAIRS)
+              lo[b] = rotate_pairs(lo[b], cs);
+            else
+              rotate_halves(lo[b], hi[b], cs);
+          }
+          *reinterpret_cast<uint4 *>(dst + b * s.dst_head) = lo[b];
+          if (two) *reinterpret_cast<uint4 *>(dst + b * s.dst_head + p.half_chunks * 8) = hi[b];
+        }
+      if ((n -= kRowBatch) <= 0) break;
+      src += kRowBatch * s.src_head;
+      dst += kRowBatch * s.dst_head;
+      load();
+    }
+    if (left <= 0) break;
+    ++sg;
     h0 = 0;
+    n = min(left, p.seg[sg].heads);
+    src = p.seg[sg].src + (long long)t * p.seg[sg].src_tok + chunk * 8;
+    load();
   }
 }
 
