@@ -181,14 +181,17 @@ __global__ void __launch_bounds__(kPlanThreads) fat_paged_plan_kernel(const Plan
 
 // ---- rows ---------------------------------------------------------------------------------------
 // Memory bound: every row is read and written once. A thread takes one (token, unit) position,
-// computes its cosines and sines once and turns that unit of a run of heads (all heads share them),
-// kRowBatch heads' loads in flight together. A unit is one 16-byte chunk (pairs 2i, 2i + 1 lie inside
-// it), or with the halves layout two chunks, i and i + rotary_dim / 2, that turn together; what is
-// not rotated goes chunk by chunk. Few tokens: the heads are split over more threads (kRowThreads
-// and the run length are launch_rows' choice), since a decode step's rows are bound by latency.
+// computes its cosines and sines once (while its first rows are on their way) and turns that unit of
+// a run of heads (all heads share them), kRowBatch heads' loads in flight together. A unit is one
+// 16-byte chunk (pairs 2i, 2i + 1 lie inside it), or with the halves layout two chunks, i and
+// i + rotary_dim / 2, that turn together; what is not rotated goes chunk by chunk. Few tokens: the
+// heads are split over more threads (the run length is launch_rows' choice), since a decode step's
+// rows are bound by latency. Small blocks end more evenly: 16383 x 16 x 128 in 22.9 us (5.9 TB/s)
+// against 25.1 with 256 threads and half as many of them; 131072 x 12 x 64 in 59.3 us (6.8 TB/s, the
+// measured copy rate); 37 x 32 x 128 in 2.4 us, the latency of a launch and three dependent loads.
 // Angles as in fat_rope_apply: position * rate mod one turn in 64-bit integers, exact at any
 // position, its top 24 bits through sincospif.
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 constexpr int kRowBatch = 4;
 
 struct RowSeg {
@@ -330,7 +333,7 @@ int check_rope(const fat_rope_t *r, int head_dim) {
 // head_dim, the rotation (null: rows are copied) and the segments are set: fill in the rest and
 // launch. A thread takes all heads of its position when the positions alone give every SM
 // kRowThreadsPerSm threads, else a run of at least kRowBatch of them.
-constexpr int kRowThreadsPerSm = 1024;
+constexpr int kRowThreadsPerSm = 2048;
 int launch_rows(RowParams &p, const fat_rope_t *rope, int head_dim, cudaStream_t stream) {
   if (rope) {
     p.rope = *rope;
