@@ -408,9 +408,12 @@ int make_tmap_pages(CUtensorMap *map, const void *ptr, const fat_paged_cache_t &
   const cuuint32_t rows = (cuuint32_t)box_rows;
   const cuuint32_t box[4] = {64, outer ? rows : 1, outer ? 1 : rows, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
+  // what L2 fetches at a time: a head's row, no more (the next head's may be far away)
+  const CUtensorMapL2promotion l2 =
+      c.head_dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_SWIZZLE_128B, l2,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     set_last_error("cuTensorMapEncodeTiled(pages)", (int)r, "");
