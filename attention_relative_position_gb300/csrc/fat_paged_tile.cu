@@ -57,7 +57,7 @@ struct TileCfg {
   static constexpr int OFF_THR = OFF_SHARE + (int)sizeof(ShareSmem<kThreads>);
   static constexpr int OFF_ROWS = (OFF_THR + kMaxThresholds * 4 + 127) & ~127;  // 2 KB per softmax warp
   static constexpr int OFF_LUT = OFF_ROWS + 8 * 2048;
-  static_assert((2 + 4 * NS + 16 + 2 * kItems) * 8 + 8 <= 448, "barrier block");
+  static_assert((2 + 4 * NS + 20 + 2 * kItems) * 8 + 8 <= 448, "barrier block");
   static_assert(OFF_LUT + kMaxBiasSpan + 512 + 1024 <= kSmemLimit, "shared memory");
   static constexpr int REG_SM = 224, REG_OTHER = 56;
   static constexpr int REGS_NEEDED = 256 * REG_SM + 128 * REG_OTHER;
@@ -259,8 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *k_empty = v_full + C::NS;
   uint64_t *v_empty = k_empty + C::NS;
   uint64_t *s_full = v_empty + C::NS;  // [tile][half]
-  uint64_t *p_ready = s_full + 4;      // [2] each from here on
-  uint64_t *o_ready = p_ready + 2;
+  uint64_t *p_ready = s_full + 4;      // [tile][half]
+  uint64_t *o_half = p_ready + 4;      // [2] each from here on; d 128: the first half's P V is complete
+  uint64_t *o_ready = o_half + 2;
   uint64_t *s_read = o_ready + 2;  // S (d 128: the step's second half of it) has been read
   uint64_t *o_free = s_read + 2;
   uint64_t *mma_done = o_free + 2;
@@ -296,7 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full + 2 * t, 1);
       mbar_init(s_full + 2 * t + 1, 1);
-      mbar_init(p_ready + t, 128);
+      mbar_init(p_ready + 2 * t, 128);
+      mbar_init(p_ready + 2 * t + 1, 128);
+      mbar_init(o_half + t, 1);
       mbar_init(o_ready + t, 1);
       mbar_init(s_read + t, 128);
       mbar_init(o_free + t, 128);
@@ -501,6 +504,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t jp = J + jj;
           const int s = jp & (C::NS - 1);
           const bool more = jj + step < n;
+          const uint64_t vd = dVd + ((s * C::TILE) >> 4);
+          const uint32_t aP = C::SEP_P ? tmem + C::COL_P + 64 * t : dS + 64 * (g & 1);
+          // O += P V of keys 16 k0 .. 16 k1 - 1
+          auto issue_PV = [&](int k0, int k1) {
+#pragma unroll
+            for (int kk = k0; kk < k1; ++kk)
+              mma_bf16_ts(dO, aP + kk * 8, vd + ((kk * 2048) >> 4), C::IDESC_PV,
+                          (jj > first || kk > 0) ? 1u : 0u);
+          };
+          // the first P V overwrites O: the previous item's rows have been read
+          auto o_wait = [&]() {
+            return jj > first || act == 0 || mbar_wait(o_free + t, (act - 1) & 1, wd);
+          };
+          auto v_wait = [&]() { return mbar_wait(v_full + s, (jp >> C::NS_LOG2) & 1, wd); };
+          if constexpr (!C::SEP_P) {  // the first half's P V
+            if (!(ok = v_wait() && mbar_wait(p_ready + 2 * t, g & 1, wd) && o_wait())) break;
+            tc_fence_after();
+            issue_PV(0, 4);
+            mma_commit(o_half + t);
+          }
           // the next step's S (d 128: its first half, where this step's second one has been read)
           if (!(ok = mbar_wait(s_read + t, g & 1, wd))) break;
           if (more) {
@@ -508,18 +531,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             issue_S(jj + step, 0, g + 1);
           }
-          if (!(ok = mbar_wait(v_full + s, (jp >> C::NS_LOG2) & 1, wd) &&
-                     mbar_wait(p_ready + t, g & 1, wd)))
-            break;
-          // the first P V overwrites O: the previous item's rows have been read
-          if (jj == first && act > 0 && !(ok = mbar_wait(o_free + t, (act - 1) & 1, wd))) break;
-          tc_fence_after();
-          const uint64_t vd = dVd + ((s * C::TILE) >> 4);
-          const uint32_t aP = C::SEP_P ? tmem + C::COL_P + 64 * t : dS + 64 * (g & 1);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(dO, aP + kk * 8, vd + ((kk * 2048) >> 4), C::IDESC_PV,
-                        (jj > first || kk > 0) ? 1u : 0u);
+          if constexpr (C::SEP_P) {
+            if (!(ok = v_wait() && mbar_wait(p_ready + 2 * t, g & 1, wd) && o_wait())) break;
+            tc_fence_after();
+            issue_PV(0, 8);
+          } else {
+            if (!(ok = mbar_wait(p_ready + 2 * t + 1, g & 1, wd))) break;
+            tc_fence_after();
+            issue_PV(4, 8);
+          }
           mma_commit(o_ready + t);
           mma_commit(v_empty + s);
           if (alone) mma_commit(v_empty + s);
@@ -620,10 +640,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         c_neg = __ldg(tab + lut[-p.bias.sat_neg - p.bias.lut_lo] * p.hq) * kLog2e;
       }
       // m: the row's reference, which P is relative to. It is raised (and what was summed so far
-      // scaled) only when the row's maximum grows beyond it by more than 2^32, at a step's second half
-      // of S 2^64 (P of the first would have to be scaled as well; pend keeps the growth): every sum
-      // stays far from fp32's and bf16's ends, and the result is exact.
-      float m = -INFINITY, l = 0.f, pend = 0.f;
+      // scaled) only when the row's maximum grows beyond it by more than 2^32: every sum stays far
+      // from fp32's and bf16's ends, and the result is exact.
+      float m = -INFINITY, l = 0.f;
       for (int i = 0; i < steps && ok; ++i) {
         const uint32_t gi = g + i;
         const int jj = item_first(it, t) + i * item_step(it);
@@ -691,83 +710,78 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m_use = m == -INFINITY ? 0.f : m;
           tile_exp<4, true>(x, f2_pack(m_use, m_use), tP, sum2);
         } else {
-        const uint32_t tP = tS + 64 * (gi & 1);
+          const uint32_t tP = tS + 64 * (gi & 1);
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          ok = warp_wait(s_full + 2 * t + half, gi & 1, wd);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t tH = tS + 64 * ((gi & 1) ^ half);
-          const int c0 = 64 * half;
-          const float m_ref = m == -INFINITY ? 0.f : m;
-          uint32_t x[2][32];
-          float mx;
-          if (near) {
-            tile_edge<64, true>(tH, p.scale_log2, 0.f, 0.f, lut + (ks + c0 - qpos - p.bias.lut_lo), tab,
-                                p.hq, slope, ks + c0 - qpos, lim - c0);
-            mx = tile_logits<2, false, false>(tH, x, 1.f, -m_ref, 0.f, 0);
-          } else {
-            const float rc = fmaf(kk, (float)c0, rowc) - m_ref;
+          for (int half = 0; half < 2; ++half) {
+            ok = warp_wait(s_full + 2 * t + half, gi & 1, wd);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tH = tS + 64 * ((gi & 1) ^ half);
+            const int c0 = 64 * half;
+            const float m_ref = m == -INFINITY ? 0.f : m;
+            uint32_t x[2][32];
+            float mx;
+            if (near) {
+              tile_edge<64, true>(tH, p.scale_log2, 0.f, 0.f,
+                                  lut + (ks + c0 - qpos - p.bias.lut_lo), tab, p.hq, slope,
+                                  ks + c0 - qpos, lim - c0);
+              mx = tile_logits<2, false, false>(tH, x, 1.f, -m_ref, 0.f, 0);
+            } else {
+              const float rc = fmaf(kk, (float)c0, rowc) - m_ref;
 #define FAT_TILE_LOGITS(LINEAR, MASK) \
   tile_logits<2, LINEAR, MASK>(tH, x, p.scale_log2, rc, kk, lim - c0)
-            if (has_slopes)
-              mx = need_mask ? FAT_TILE_LOGITS(true, true) : FAT_TILE_LOGITS(true, false);
-            else
-              mx = need_mask ? FAT_TILE_LOGITS(false, true) : FAT_TILE_LOGITS(false, false);
+              if (has_slopes)
+                mx = need_mask ? FAT_TILE_LOGITS(true, true) : FAT_TILE_LOGITS(true, false);
+              else
+                mx = need_mask ? FAT_TILE_LOGITS(false, true) : FAT_TILE_LOGITS(false, false);
 #undef FAT_TILE_LOGITS
-          }
-          if (half == 1) {  // it is in registers: the next S may be computed there
-            tc_fence_before();
-            mbar_arrive(s_read + t);
-          }
-          float sub = 0.f;  // what the exponentials still subtract
-          bool need = false;
-          if (m == -INFINITY) {  // no key of this row so far: what was summed is zero
-            if (mx != -INFINITY) m = sub = mx;
-          } else {
-            pend = fmaxf(pend, mx);
-            need = pend > (half == 0 ? 32.f : 64.f);
-          }
-          if (__any_sync(0xffffffffu, need)) {
-            const float f = need ? ex2(-pend) : 1.f;
-            if (i > 0) {  // O, once the products so far are complete
-              ok = warp_wait(o_ready + t, (gi - 1) & 1, wd);
-              if (!ok) break;
-              tc_fence_after();
+            }
+            if (half == 1) {  // it is in registers: the next S may be computed there
+              tc_fence_before();
+              mbar_arrive(s_read + t);
+            }
+            float sub = 0.f;  // what the exponentials still subtract
+            bool need = false;
+            if (m == -INFINITY) {  // no key of this row so far: what was summed is zero
+              if (mx != -INFINITY) m = sub = mx;
+            } else {
+              need = mx > 32.f;
+            }
+            if (__any_sync(0xffffffffu, need)) {
+              const float f = need ? ex2(-mx) : 1.f;
+              if (i + half > 0) {  // O, once the products so far are complete
+                ok = half == 0 ? warp_wait(o_ready + t, (gi - 1) & 1, wd)
+                               : warp_wait(o_half + t, gi & 1, wd);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(tO + c, o);
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(tO + c, o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tmem_st32(tO + c, o);
+                  for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                  tmem_st32(tO + c, o);
+                }
+              }
+              l *= f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) sum2[k] = f2_mul(sum2[k], f2_pack(f, f));
+              if (need) {
+                m += mx;
+                sub = mx;
               }
             }
-            if (half == 1) {  // P of the first half
+            if (__any_sync(0xffffffffu, sub != 0.f))
+              tile_exp<2, true>(x, f2_pack(sub, sub), tP + 32 * half, sum2);
+            else
+              tile_exp<2, false>(x, 0, tP + 32 * half, sum2);
+            if (half == 0) {  // (the second half's is passed on below)
               tmem_st_wait();
-              uint32_t o[32];
-              tmem_ld32(tP, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                o[k] = pack_bf16x2(__uint_as_float(o[k] << 16) * f,
-                                   __uint_as_float(o[k] & 0xffff0000u) * f);
-              tmem_st32(tP, o);
-            }
-            l *= f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sum2[k] = f2_mul(sum2[k], f2_pack(f, f));
-            if (need) {
-              m += pend;
-              sub = pend;
-              pend = 0.f;
+              tc_fence_before();
+              mbar_arrive(p_ready + 2 * t);
             }
           }
-          if (__any_sync(0xffffffffu, sub != 0.f))
-            tile_exp<2, true>(x, f2_pack(sub, sub), tP + 32 * half, sum2);
-          else
-            tile_exp<2, false>(x, 0, tP + 32 * half, sum2);
-        }
-        if (!ok) break;
+          if (!ok) break;
         }
         {
           float s0, s1, s2, s3;
@@ -777,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(p_ready + t);
+        mbar_arrive(p_ready + 2 * t + (C::SEP_P ? 0 : 1));
       }
       // ---- the item's rows
       g += steps;
