@@ -129,6 +129,28 @@ __device__ __forceinline__ float fwd_logits(uint32_t tS, uint32_t (&x)[4][32], f
   return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
 }
 
+// P = 2^(x - sub) for one row of 128 columns (x already relative to the row's reference max;
+// sub is nonzero only when that reference has just moved), packed to bf16 pairs into TMEM,
+// with the fp32 sum of the row accumulated in four short dependency chains.
+template <bool SUB>
+__device__ __forceinline__ void fwd_exp_pass(const uint32_t (&x)[4][32], uint64_t sub2,
+                                             uint32_t tP, uint64_t (&sum2)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float a = __uint_as_float(x[c][2 * i]), b = __uint_as_float(x[c][2 * i + 1]);
+      if (SUB) f2_unpack(f2_sub(f2_pack(a, b), sub2), a, b);
+      a = ex2(a);
+      b = ex2(b);
+      pk[i] = pack_bf16x2(a, b);
+      sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(a, b));
+    }
+    tmem_st16(tP + c * 16, pk);  // P (bf16 pairs): own columns (d 64) or over S (d 128)
+  }
+}
+
 // Rows that see no key (in this block's key range): out = 0 and lse = -inf, or, for a key range
 // of a split forward, a zero partial output with partial lse -inf. Threads thr, thr + nthr, ...
 // take rows row0 .. row0 + nrows - 1 (document-local) of query head h.

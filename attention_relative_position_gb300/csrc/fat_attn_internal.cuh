@@ -252,28 +252,6 @@ __device__ __forceinline__ FarBias far_bias_staged(const BiasParams &b, const in
   return f;
 }
 
-// P = 2^(x - sub) for one row of 128 columns (x already relative to the row's reference max;
-// sub is nonzero only when that reference has just moved), packed to bf16 pairs into TMEM,
-// with the fp32 sum of the row accumulated in four short dependency chains.
-template <bool SUB>
-__device__ __forceinline__ void fwd_exp_pass(const uint32_t (&x)[4][32], uint64_t sub2,
-                                             uint32_t tP, uint64_t (&sum2)[4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float a = __uint_as_float(x[c][2 * i]), b = __uint_as_float(x[c][2 * i + 1]);
-      if (SUB) f2_unpack(f2_sub(f2_pack(a, b), sub2), a, b);
-      a = ex2(a);
-      b = ex2(b);
-      pk[i] = pack_bf16x2(a, b);
-      sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(a, b));
-    }
-    tmem_st16(tP + c * 16, pk);  // P (bf16 pairs): own columns (d 64) or over S (d 128)
-  }
-}
-
 // ---------------------------------------------------------------------------------------------
 // host-side launch descriptors (filled by the API layer)
 // ---------------------------------------------------------------------------------------------
@@ -429,7 +407,6 @@ int sm_count();
 // prepare_kernel) can be resident at once when launched as clusters of two: twice the number of
 // co-resident two-CTA clusters, cached per (kernel, device, size); 0 if the query fails.
 int max_pair_ctas(const void *fn, size_t smem, int nthreads);
-
 
 // Tensor map over a [T, H, d] bf16 tensor, box = 64 channels x 1 head x box_rows tokens,
 // 128-byte swizzle (the shared-memory layout the tcgen05 descriptors expect).

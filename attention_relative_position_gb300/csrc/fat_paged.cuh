@@ -107,9 +107,10 @@ struct TileCost {
 };
 
 // SMs n of the tile kernel when a call launches both kernels, so that they end together: with its
-// total a and the other's b in stages of the few-row kernel (a pair of tiles weighs kPairStages: 1.05 us
-// against 0.12 us of an SM at head_dim 128, measured) and its start longer by kStartStages,
-// kStartStages + a / n = b / (sms - n). Each kernel has at least one SM.
+// total a and the other's b in stages of the few-row kernel (a pair of tiles weighs kPairStages: 0.96 us
+// against 0.11 us of an SM at head_dim 128, measured) and its start longer by kStartStages,
+// kStartStages + a / n = b / (sms - n). Each kernel has at least one SM. (24 decode steps beside a chunk
+// of 384 tokens, 300 .. 6000 keys: 54 us; shares in proportion to the totals alone gave 62.)
 constexpr float kPairStages = 9.f, kPairStages64 = 5.f, kStartStages = 80.f;
 template <int D>
 __device__ __forceinline__ int tile_sms(const PagedParams &p, long long tile_total,
@@ -305,9 +306,13 @@ constexpr int kFewRows = 16;  // rows of the few-row kernel's items
 int paged_few_ctas();
 constexpr int kTileRows = 256;  // packed rows of the tile kernel's items, at most
 int paged_tile_ctas();
-// Whether items are cut: contexts of at most this many keys are computed by one CTA in a few stages
-// per warp, which costs less than the merge grid.
-constexpr int kWholeKeys = 1024;
+// Whether items are cut: contexts of at most so many keys (the few-row kernel's: stages) are computed by
+// one CTA each, which costs less than the merge grid. Whole against cut, in us:
+//   few rows, head_dim 64, 12 heads: 500 keys 7.4 / 8.2 (16 requests 8.2 / 11.0), 1000 keys 10.3 / 8.9;
+//   head_dim 128, 8 requests, 32 heads over 8: 250 keys 9.3 / 10.4, 500 keys 12.2 / 11.5;
+//   chunks of 64 tokens, 32 heads over 8: 1000 keys 23.3 / 24.5 (32 chunks, head_dim 64: 38 / 43), 2000
+//   keys 37.2 / 28.2.
+constexpr int kWholeStages = 24, kWholeKeys = 1024;
 int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
 int launch_paged_tile(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
 

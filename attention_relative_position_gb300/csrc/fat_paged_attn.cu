@@ -21,7 +21,8 @@ namespace {
 // consecutive rows. Chains of a few parts: a warp per task, the parts' loads in flight together.
 // Long chains (one context over most of the grid): the block's warps share a task's parts and add
 // their sums through shared memory. Reads chain x (D + 2) x 4 bytes per row from L2; bound by the
-// latency of three dependent loads, so registers are kept to four blocks per SM.
+// latency of three dependent loads, so registers are kept to four blocks per SM (2 to 3 us at the end
+// of a call).
 constexpr int kMergeWarps = 8;
 constexpr int kLongChain = 16;  // parts from which the warps of a block share a task
 constexpr int kMergeBatch = 4;  // parts whose loads a lane has in flight
@@ -163,7 +164,8 @@ Plan make_plan(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
   const long long rows = (long long)sh->max_seqlen_q * (sh->num_heads_q / c->num_heads);
   l.tile = rows > kFewRows;
   l.few = !l.tile || (long long)sh->num_seqs * sh->max_seqlen_q != sh->total_q;
-  l.split = sh->max_seqlen_k > kWholeKeys;
+  l.split = sh->max_seqlen_k >
+            (l.tile ? kWholeKeys : kWholeStages * few_stage_tokens(c->head_dim));
   if (!l.split) return l;
   if (l.tile) l.few_off = (part_floats(paged_tile_ctas(), kTileRows, c->head_dim) * 4 + 255) & ~(size_t)255;
   l.bytes = l.few_off + (l.few ? part_floats(paged_few_ctas(), kFewRows, c->head_dim) * 4 : 0);

@@ -15,6 +15,10 @@
 // filled, its round trip through tensor memory would cost more than the 64 products of a stage.
 // A short item (two stages at most) is one warp's; the warps of a longer one merge their rows in
 // shared memory once. Items cut by the share boundaries leave partial rows for the merge grid.
+// Bound by HBM: one token for each of 32 requests over 1024 .. 4096 keys, 64 heads over 16 of 128
+// channels, 602 MB in 102 us with the merge (5.9 TB/s, 0.87 of a copy's rate). Short calls are bound by
+// their start: 1.2 us to the shares, 0.9 to the first copy, 0.7 to its arrival, 0.6 a stage, 1.0 for
+// the merge of the warps (one token over 500 keys, 7.4 us).
 #include <algorithm>
 #include <cstdint>
 
