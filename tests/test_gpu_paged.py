@@ -349,6 +349,8 @@ CASES = {
     "many_chunks": dict(lq=list(np.random.default_rng(2).integers(0, 30, 500)),
                         lk=list(np.random.default_rng(3).integers(30, 90, 500)), hq=4, hkv=2, d=64,
                         page=16),
+    "decode_many": dict(lq=[1] * 700, lk=list(np.random.default_rng(4).integers(0, 90, 700)), hq=4,
+                        hkv=4, d=64, page=16, t5=T5D),
     "million_keys": dict(lq=[1, 1], lk=[1 << 20, 900001], hq=2, hkv=1, d=64, page=256, t5=T5D),
     "chunk_long_context": dict(lq=[20], lk=[300007], hq=2, hkv=2, d=128, page=4096, alibi=True),
     # logits of hundreds: the running reference moves by more than 2^32 and 2^64, in either half of a
@@ -430,6 +432,19 @@ def test_attention_bad_page_counts_as_zeros(name, bad):
     out, lse = p.run()
     assert _errors() == fa.FAT_DEVERR_PAGES
     p.check(out, lse)
+
+
+@pytest.mark.parametrize("lq", [[1, 1, 2], [40, 3]])
+def test_attention_without_any_key(lq):
+    """No request has a key yet: an empty block table, bounds of 0; rows of zeros."""
+    p = Problem(lq=lq, lk=[0] * len(lq), hq=4, hkv=2, d=64, page=16, causal=False, pad=2)
+    out = torch.full_like(p.q, 3.0)
+    _, lse = fa.fat_paged_attn(
+        p.q, p.kc, p.vc, torch.empty((p.n, 0), dtype=torch.int32, device=DEV), _i32(p.cu),
+        _i32(p.lk), max(lq), 0, out=out, **p.kwargs())
+    assert _errors() == 0
+    assert (out[:p.total] == 0).all() and (out[p.total:] == 3.0).all()
+    assert (lse[:, :p.total] == -float("inf")).all()
 
 
 NAN_CASES = {
