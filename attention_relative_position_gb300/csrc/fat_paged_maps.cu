@@ -9,6 +9,7 @@
 //   rows: y = a (x cos p - x' sin p, x sin p + x' cos p) for the channel pairs of the rotated part
 //         of each head, p = position * rate of the pair; the other channels are copied.
 #include <algorithm>
+#include <array>
 #include <cmath>
 #include <cstdint>
 
@@ -324,6 +325,22 @@ bool odd4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 // A stride of rows that are accessed 16 bytes at a time
 bool bad_stride(long long s) { return s < 0 || (s & 7) != 0; }
 
+// Whether rows of d elements at every combination of three indexes lie apart: from the smallest stride
+// on, each one is at least what the indexes before it span (an index of one value spans nothing).
+struct Extent {
+  long long stride, count;
+};
+bool rows_apart(int d, std::array<Extent, 3> e) {
+  std::sort(e.begin(), e.end(), [](const Extent &a, const Extent &b) { return a.stride < b.stride; });
+  double span = d;
+  for (const Extent &x : e) {
+    if (x.count <= 1) continue;
+    if ((double)x.stride < span) return false;
+    span += (double)x.stride * (double)(x.count - 1);
+  }
+  return true;
+}
+
 int check_rope(const fat_rope_t *r, int head_dim) {
   if (r->rotary_dim < 16 || r->rotary_dim % 16 || r->rotary_dim > 2 * FAT_ROPE_MAX_PAIRS ||
       r->rotary_dim > head_dim)
@@ -377,13 +394,17 @@ int check_paged_cache(const fat_paged_cache_t *in, fat_paged_cache_t *c, int *lo
   if ((long long)c->num_pages * c->page_size > 0x7fffffffLL) return FAT_EINVAL_SHAPE;
   // a stride over one entry says nothing
   if (c->num_heads == 1) c->stride_head = c->stride_token;
-  if (c->num_pages == 1) c->stride_page = c->stride_token * c->page_size;
+  if (c->num_pages == 1)
+    c->stride_page = std::max(c->stride_token * c->page_size, c->stride_head * c->num_heads);
   if (odd16(c->k) || odd16(c->v) || bad_stride(c->stride_page) || bad_stride(c->stride_token) ||
       bad_stride(c->stride_head))
     return FAT_EINVAL_SHAPE;
   // rows of different heads, tokens and pages lie apart
   if (c->stride_token < c->head_dim || c->stride_head < c->head_dim ||
-      c->stride_page < c->head_dim)
+      c->stride_page < c->head_dim ||
+      !rows_apart(c->head_dim, {{{c->stride_token, c->page_size},
+                                 {c->stride_head, c->num_heads},
+                                 {c->stride_page, c->num_pages}}}))
     return FAT_EINVAL_SHAPE;
   *log2_page = lg;
   return FAT_OK;
@@ -484,8 +505,9 @@ int fat_rope_embed(const fat_rope_shape_t *sh, const fat_rope_t *rope, const voi
       bad_stride(sh->y_stride_head))
     return FAT_EINVAL_SHAPE;
   // rows of y lie apart; in place, every row stays where it is
-  if ((sh->num_heads > 1 && sh->y_stride_head < sh->head_dim) ||
-      (sh->tokens > 1 && sh->y_stride_token < sh->head_dim))
+  if (!rows_apart(sh->head_dim, {{{sh->y_stride_head, sh->num_heads},
+                                  {sh->y_stride_token, sh->tokens},
+                                  {0, 1}}}))
     return FAT_EINVAL_SHAPE;
   if (x == y && ((sh->tokens > 1 && sh->x_stride_token != sh->y_stride_token) ||
                  (sh->num_heads > 1 && sh->x_stride_head != sh->y_stride_head)))

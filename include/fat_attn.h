@@ -350,7 +350,7 @@ typedef struct {
   /* strides of k and of v in elements, multiples of 8; a row of head_dim elements is contiguous.
      [num_pages, page_size, num_heads, head_dim] in memory order gives (page_size * num_heads *
      head_dim, num_heads * head_dim, head_dim); pages with the heads outside, or the pages of
-     several layers in one block, give others. */
+     several layers in one block, give others. No two rows overlap. */
   int64_t stride_page, stride_token, stride_head;
 } fat_paged_cache_t;
 
@@ -407,7 +407,7 @@ int fat_rope_init(fat_rope_t *rope, int rotary_dim, int interleaved, double base
  * y = the rotation of x (bf16 rows of head_dim channels) at positions[token] (int32, any value);
  * inverse = 1: its transpose, which turns the gradient of y into the gradient of x. y may be x
  * itself (equal strides) but not otherwise overlap it. Strides in elements, multiples of 8; rows of
- * x may repeat (stride 0). head_dim a multiple of 8, at least rotary_dim. Angles are exact modulo
+ * x may repeat (stride 0), those of y lie apart. head_dim a multiple of 8, at least rotary_dim. Angles are exact modulo
  * one turn at any position, as in fat_rope_apply.
  */
 typedef struct {

@@ -384,6 +384,26 @@ def test_attention_cache_layouts(layout, name):
     assert torch.equal(oa, ob) and torch.equal(la, lb)
 
 
+def test_cache_of_one_page_inside_a_block_of_layers():
+    """A single page whose heads lie outside its tokens, two layers apart: appended and attended to as
+    the same page on its own."""
+    rng = np.random.default_rng(12)
+    S, H, d = 32, 2, 64
+    k, v, q = _bf16(rng, 20, H, d), _bf16(rng, 20, H, d), _bf16(rng, 3, H, d)
+    block = torch.full((2, H, 2, S, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    alone = torch.full((2, 1, S, H, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    got = []
+    for kc, vc in ((block[0, :, 1].transpose(0, 1)[None], block[1, :, 1].transpose(0, 1)[None]),
+                   (alone[0], alone[1])):
+        fa.fat_paged_append(k, v, kc, vc, _i32(range(20)))
+        got.append(fa.fat_paged_attn(q, kc, vc, _i32([[0]]), _i32([0, 3]), _i32([20]), 3, 20,
+                                     causal=True, softmax_scale=0.125))
+    assert _errors() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert got[0][0].isfinite().all()
+    assert block[:, :, 0].isnan().all() and block[:, :, 1, 20:].isnan().all()
+
+
 @pytest.mark.parametrize("stale", [float("inf"), -float("inf"), 3e38])
 @pytest.mark.parametrize("name", ["decode_t5_ragged", "chunk_group1", "mixed_d128"])
 def test_attention_ignores_stale_slots(stale, name):

@@ -199,3 +199,36 @@ def test_binding_refusals():
             call()
     with pytest.raises(TypeError):
         fa._load_calls().plan(1, 2)
+
+
+OVERLAPPING = [dict(stride_token=64, stride_head=64),     # a token's second head, the next one's first
+               dict(stride_head=256, stride_token=128),   # heads inside each other's tokens
+               dict(stride_page=1024), dict(stride_page=64, stride_head=512)]
+APART = [dict(), dict(num_heads=1, stride_head=0, stride_token=64, stride_page=1024),
+         dict(stride_head=1024, stride_token=64),         # heads outside the tokens of a page
+         dict(stride_page=64 * 6, stride_head=128, stride_token=64 * 6 * 8),  # pages inside tokens
+         # one page of a block of several layers: its own stride says nothing
+         dict(num_pages=1, stride_page=0, stride_head=4096, stride_token=64)]
+
+
+@pytest.mark.parametrize("kw", OVERLAPPING)
+def test_caches_whose_rows_overlap_are_refused(lib, kw):
+    assert _append(lib, _cache(**kw)) == -2
+    assert _attn(lib, _cache(**kw)) == -2
+
+
+@pytest.mark.parametrize("kw", APART)
+def test_caches_whose_rows_lie_apart_pass(lib, kw):
+    assert _append(lib, _cache(**kw), tokens=0) == 0
+    if "stride_page" not in kw or kw["stride_page"] in (0, 1024):
+        assert _attn(lib, _cache(**kw), total_q=0) == 0
+    else:  # attention wants the pages outermost
+        assert _attn(lib, _cache(**kw), total_q=0) == -5
+
+
+def test_rope_rows_of_the_result_lie_apart(lib):
+    r = fa.fat_rope_init(64)
+    assert _embed(lib, r, ys=(64, 64)) == -2
+    assert _embed(lib, r, ys=(128, 128)) == -2
+    assert _embed(lib, r, ys=(64, 192)) == -2
+    assert _embed(lib, r, tokens=0, ys=(64, 256)) == 0
