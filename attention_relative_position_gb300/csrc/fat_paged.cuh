@@ -107,10 +107,10 @@ struct TileCost {
 };
 
 // SMs n of the tile kernel when a call launches both kernels, so that they end together: with its
-// total a and the other's b in stages of the few-row kernel (a pair of tiles weighs kPairStages: 0.96 us
-// against 0.11 us of an SM at head_dim 128, measured) and its start longer by kStartStages,
-// kStartStages + a / n = b / (sms - n). Each kernel has at least one SM. (24 decode steps beside a chunk
-// of 384 tokens, 300 .. 6000 keys: 54 us; shares in proportion to the totals alone gave 62.)
+// total a and the other's b in stages of the few-row kernel (a pair of tiles weighs kPairStages:
+// 0.96 us against 0.11 us of an SM at head_dim 128, measured) and its start longer by kStartStages,
+// kStartStages + a / n = b / (sms - n). Each kernel has at least one SM. (24 decode steps beside a
+// chunk of 384 tokens, 300 .. 6000 keys: 54 us; shares in proportion to the totals alone gave 62.)
 constexpr float kPairStages = 9.f, kPairStages64 = 5.f, kStartStages = 80.f;
 template <int D>
 __device__ __forceinline__ int tile_sms(const PagedParams &p, long long tile_total,
@@ -164,7 +164,6 @@ __device__ __forceinline__ float *part_stats(float *part, int ctas, int cta, int
 constexpr int kShareDocs = 64;  // requests staged in shared memory from the stretch's first on
 
 struct Share {
-  long long total;   // U
   long long lo, hi;  // this CTA's stretch; lo >= hi: none
   int doc;           // the request in which it begins
   long long off;     // cost of that request before lo
@@ -240,7 +239,6 @@ __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share,
   }
   const int G = ctas(total, other_total);
   if (tid < p.n && !d.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
-  r.total = total;
   r.lo = r.hi = r.off = 0;
   r.doc = 0;
   if ((int)blockIdx.x >= G || total == 0) return r;

@@ -167,7 +167,9 @@ Plan make_plan(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
   l.split = sh->max_seqlen_k >
             (l.tile ? kWholeKeys : kWholeStages * few_stage_tokens(c->head_dim));
   if (!l.split) return l;
-  if (l.tile) l.few_off = (part_floats(paged_tile_ctas(), kTileRows, c->head_dim) * 4 + 255) & ~(size_t)255;
+  if (l.tile)
+    l.few_off =
+        (part_floats(paged_tile_ctas(), kTileRows, c->head_dim) * 4 + 255) & ~(size_t)255;
   l.bytes = l.few_off + (l.few ? part_floats(paged_few_ctas(), kFewRows, c->head_dim) * 4 : 0);
   return l;
 }
@@ -218,7 +220,8 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   rc = make_bias_params(&p.bias, bias_table, num_buckets, max_distance, bidirectional, alibi_slopes);
   if (rc) return rc;
   const int group = sh->num_heads_q / cache->num_heads;
-  if (bias_table && (p.bias.sat_pos + p.bias.sat_neg > kMaxBiasSpan || num_buckets * group > kMaxBiasEntries))
+  if (bias_table && (p.bias.sat_pos + p.bias.sat_neg > kMaxBiasSpan ||
+                     num_buckets * group > kMaxBiasEntries))
     return FAT_EUNSUPPORTED;
   if (sh->total_q == 0 || sh->num_seqs == 0 || sh->max_seqlen_q == 0) return FAT_OK;
   if (!q || !cu_seqlens_q || !seqlens_k || !out || (sh->table_width > 0 && !block_table))

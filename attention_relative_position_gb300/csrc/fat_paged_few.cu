@@ -52,7 +52,8 @@ struct FewCfg {
   static constexpr int OFF_THR = OFF_BAR + 2 * kWarps * kRing * 8 + 64;
   static constexpr int OFF_SHARE = OFF_THR + kMaxThresholds * 4;
   static constexpr int OFF_LUT = OFF_SHARE + (int)sizeof(ShareSmem<kThreads>);
-  // bucket bytes of the deltas -sat_neg .. sat_pos
+  // bucket bytes of the deltas -sat_neg .. sat_pos (up to 2.2 KB two CTAs fit on an SM, beyond that
+  // one: saturation distances of a thousand keys each way still fit)
   static int bytes(const BiasParams &b) {
     return OFF_LUT + (b.table ? (b.sat_neg + b.sat_pos + 1 + 15) & ~15 : 0);
   }

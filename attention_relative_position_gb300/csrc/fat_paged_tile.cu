@@ -25,7 +25,6 @@
 // A call's first steps cost about 10 us more: their instructions come from L2 a line at a time.
 #include <algorithm>
 #include <cstdint>
-#include <cstdio>
 
 #include "fat_paged.cuh"
 
@@ -882,8 +881,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float *part = part_rows<kTileRows, D>(p.part, gridDim.x, blockIdx.x, which);
 #pragma unroll
           for (int v = 0; v < 8; ++v)
-            *part_quad<kTileRows>(part, prow, c * 8 + v) = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                 __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+            *part_quad<kTileRows>(part, prow, c * 8 + v) =
+                make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                            __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
         }
       }
       __syncwarp();

@@ -407,8 +407,8 @@ int fat_rope_init(fat_rope_t *rope, int rotary_dim, int interleaved, double base
  * y = the rotation of x (bf16 rows of head_dim channels) at positions[token] (int32, any value);
  * inverse = 1: its transpose, which turns the gradient of y into the gradient of x. y may be x
  * itself (equal strides) but not otherwise overlap it. Strides in elements, multiples of 8; rows of
- * x may repeat (stride 0), those of y lie apart. head_dim a multiple of 8, at least rotary_dim. Angles are exact modulo
- * one turn at any position, as in fat_rope_apply.
+ * x may repeat (stride 0), those of y lie apart. head_dim a multiple of 8, at least rotary_dim.
+ * Angles are exact modulo one turn at any position, as in fat_rope_apply.
  */
 typedef struct {
   int32_t tokens, num_heads, head_dim;
