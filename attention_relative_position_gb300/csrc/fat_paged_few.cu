@@ -10,9 +10,14 @@
 // for it: one token over 500 keys 9.4 us against 7.4. What is copied is marked to leave L2 first:
 // it is not read again (24 x 5 drafted tokens over 127 MB 33.2 us without, 30.5 with).
 // Per stage and warp: S = Q K^T for 16 rows with warp-level matrix products (Q in registers), bias
-// and mask, a running maximum that moves only when it grows by more than 2^32, P as bf16 in
-// registers, O += P V. Warp-level products suffice here: with 16 of 128 rows of a tcgen05 tile
-// filled, its round trip through tensor memory would cost more than the 64 products of a stage.
+// and mask, a running maximum that moves only when it grows by more than 2^32, P in registers as a sum
+// of two bf16 numbers, O += P V. (With one, the error against 64 bits is 0.0022 where the output's own
+// rounding, and the decode kernel over packed keys with its fp32 weights, leave 0.0016.) Up to 8 rows
+// the second parts take the fragment's other 8 rows and cost no products; with more, every P V is done
+// twice. One part against two, in us: one token over 500 keys 7.5 / 7.7, decode of 32 requests 102.0 /
+// 102.5, drafted tokens (15 rows) 30.6 / 31.8, mixed step 56 / 59.
+// Warp-level products suffice here: with 16 of 128 rows of a tcgen05 tile filled, its round trip
+// through tensor memory would cost more than the 32 or 48 products of a stage.
 // A short item (two stages at most) is one warp's; the warps of a longer one merge their rows in
 // shared memory once. Items cut by the share boundaries leave partial rows for the merge grid.
 // Bound by HBM: one token for each of 32 requests over 1024 .. 4096 keys, 64 heads over 16 of 128
@@ -30,7 +35,7 @@ namespace {
 constexpr int kWarps = 4;          // computing warps
 constexpr int kThreads = 2 * kWarps * 32;
 // registers of a thread: 128 at launch (two CTAs per SM), then split unevenly
-constexpr int kProdRegs = 56, kCompRegs = 200;
+constexpr int kProdRegs = 64, kCompRegs = 192;
 static_assert(kProdRegs + kCompRegs <= 2 * 128, "what the block was launched with");
 constexpr int kRing = 3;           // stages per warp
 constexpr int kShortStages = 2;    // items of at most this many stages are one warp's
@@ -60,6 +65,13 @@ struct FewCfg {
   static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
   static_assert(STAGE == 8192 && KT == 1 << LOG2_KT, "a stage is 8 KB");
 };
+
+// Two weights (at most 2^32) as bf16 pairs hi + lo: what is left is below 2^-16 of them.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  hi = pack_bf16x2(a, b);
+  const float2 r = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&hi));
+  lo = pack_bf16x2(a - r.x, b - r.y);
+}
 
 // The items of a share in order.
 struct FewItem {
@@ -307,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool mine = !shortened || ((cur.shorts - 1) & (kWarps - 1)) == warp;
     if (!mine) continue;
     const int rows = it.lq * G, shift = it.lk - it.lq;
+    const bool half = rows <= 8;  // rows 8 .. 15 of O take the second parts of rows 0 .. 7
     uint32_t qf[D / 16][4];
     int qpos[2], lim[2], head[2];
     float slope[2], far_pos[2], far_neg[2];
@@ -430,9 +443,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
         }
         const bool up0 = mx[0] > m[0] + 32.f || (m[0] == -INFINITY && mx[0] > m[0]);
-        const bool up1 = mx[1] > m[1] + 32.f || (m[1] == -INFINITY && mx[1] > m[1]);
+        const bool up1 = !half && (mx[1] > m[1] + 32.f || (m[1] == -INFINITY && mx[1] > m[1]));
         if (__any_sync(0xffffffffu, up0 || up1)) {
-          const float f0 = up0 ? ex2(m[0] - mx[0]) : 1.f, f1 = up1 ? ex2(m[1] - mx[1]) : 1.f;
+          const float f0 = up0 ? ex2(m[0] - mx[0]) : 1.f;
+          const float f1 = half ? f0 : up1 ? ex2(m[1] - mx[1]) : 1.f;
           if (up0) m[0] = mx[0];
           if (up1) m[1] = mx[1];
           l[0] *= f0;
@@ -446,27 +460,54 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         const float s0 = m[0] == -INFINITY ? 0.f : m[0], s1 = m[1] == -INFINITY ? 0.f : m[1];
-        // P (sums from the unrounded weights), O += P V
+        // P as two bf16 parts, the weight rounded and what that left (16 bits in all; the sums are of
+        // the unrounded weights), O += P V. Up to 8 rows: the second parts are rows 8 .. 15 of the
+        // same products. More: products of their own.
         const uint32_t va = smem_u32(vt) + ((lane & 7) + ((lane >> 3) & 1) * 8) * 128;
+        auto values = [&](int kk, int t, uint32_t (&b)[4]) {  // of 16 keys, channels 8 t .. 8 t + 15
+          ldmatrix_x4_trans(va + (t >> 3) * C::BLK + kk * 2048 +
+                                (((uint32_t)((t & 7) + (lane >> 4)) ^ (lane & 7)) << 4), b);
+        };
+        if (half) {
 #pragma unroll
-        for (int kk = 0; kk < KT / 16; ++kk) {
-          uint32_t pf[4];
+          for (int kk = 0; kk < KT / 16; ++kk) {
+            uint32_t pf[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float a = ex2(x[2 * kk + h][0] - s0), b = ex2(x[2 * kk + h][1] - s0);
-            const float c = ex2(x[2 * kk + h][2] - s1), d = ex2(x[2 * kk + h][3] - s1);
-            l[0] += a + b;
-            l[1] += c + d;
-            pf[2 * h] = pack_bf16x2(a, b);
-            pf[2 * h + 1] = pack_bf16x2(c, d);
+            for (int h = 0; h < 2; ++h) {
+              const float a = ex2(x[2 * kk + h][0] - s0), b = ex2(x[2 * kk + h][1] - s0);
+              l[0] += a + b;
+              split_bf16x2(a, b, pf[2 * h], pf[2 * h + 1]);
+            }
+#pragma unroll
+            for (int t = 0; t < D / 8; t += 2) {
+              uint32_t b[4];
+              values(kk, t, b);
+              mma_16x8x16(o[t], pf, b[0], b[1]);
+              mma_16x8x16(o[t + 1], pf, b[2], b[3]);
+            }
           }
+        } else {
 #pragma unroll
-          for (int t = 0; t < D / 8; t += 2) {
-            uint32_t b[4];
-            ldmatrix_x4_trans(va + (t >> 3) * C::BLK + kk * 2048 +
-                                  (((uint32_t)((t & 7) + (lane >> 4)) ^ (lane & 7)) << 4), b);
-            mma_16x8x16(o[t], pf, b[0], b[1]);
-            mma_16x8x16(o[t + 1], pf, b[2], b[3]);
+          for (int kk = 0; kk < KT / 16; ++kk) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float a = ex2(x[2 * kk + h][0] - s0), b = ex2(x[2 * kk + h][1] - s0);
+              const float c = ex2(x[2 * kk + h][2] - s1), d = ex2(x[2 * kk + h][3] - s1);
+              l[0] += a + b;
+              l[1] += c + d;
+              split_bf16x2(a, b, hi[2 * h], lo[2 * h]);
+              split_bf16x2(c, d, hi[2 * h + 1], lo[2 * h + 1]);
+            }
+#pragma unroll
+            for (int t = 0; t < D / 8; t += 2) {
+              uint32_t b[4];
+              values(kk, t, b);
+              mma_16x8x16(o[t], hi, b[0], b[1]);
+              mma_16x8x16(o[t + 1], hi, b[2], b[3]);
+              mma_16x8x16(o[t], lo, b[0], b[1]);
+              mma_16x8x16(o[t + 1], lo, b[2], b[3]);
+            }
           }
         }
         __syncwarp();  // the stage has been read: its place is free for the next copy
@@ -481,6 +522,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    if (half) {
+#pragma unroll
+      for (int t = 0; t < D / 8; ++t) {
+        o[t][0] += o[t][2];
+        o[t][1] += o[t][3];
+      }
     }
 
     // ---- the item's rows: whole ones to out, cut ones to the workspace

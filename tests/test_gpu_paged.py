@@ -372,6 +372,39 @@ def test_attention(name):
     p.check(out, lse)
 
 
+FINE_CASES = {
+    "whole_d64": dict(lq=[1] * 4, lk=[2, 7, 40, 500], hq=12, hkv=12, d=64, page=16, t5=T5D),
+    "whole_d128": dict(lq=[1] * 5, lk=[3, 16, 17, 200, 380], hq=16, hkv=2, d=128, page=16),
+    "cut_d64": dict(lq=[1, 5, 2], lk=[3000, 1500, 9], hq=6, hkv=2, d=64, page=32, alibi=True),
+    "cut_d128": dict(lq=[1, 4, 2], lk=[4000, 33, 700], hq=8, hkv=2, d=128, page=64, causal=False),
+    "beside_chunk": dict(lq=[1, 1, 60], lk=[600, 12, 90], hq=8, hkv=2, d=64, page=16),
+    "beside_chunk_d128": dict(lq=[1, 3, 70], lk=[2000, 5, 90], hq=4, hkv=2, d=128, page=16),
+}
+
+
+@pytest.mark.parametrize("name", FINE_CASES)
+def test_attention_of_few_rows_keeps_its_weights(name):
+    """At most 16 rows: the weights enter P V with 16 bits, as those of the decode kernel over packed
+    keys do with 24, so only the output's own rounding is of bf16 size. Tolerance: 2^-8 of the value;
+    per |weight x value| twice the logits' ex (as in check), 2^-20 of the exponential, 2^-17 of the
+    weight's two parts, and the fp32 accumulation, a key block of 16 at a time and twice (for both
+    parts): lk / 8 additions that each lose 2^-22 of the sum so far at most."""
+    p = Problem(seed=70, **FINE_CASES[name])
+    out, _ = p.run()
+    assert _errors() == 0
+    ro, _, a, s, b = p.oracle()
+    group = p.hq // p.hkv
+    for i in range(p.n):
+        if p.lq[i] * group > 16:
+            continue
+        rows = slice(int(p.cu[i]), int(p.cu[i + 1]))
+        ex = (p.d * s + 4 * (s + b)) * 2.0 ** -24
+        fine = 2 * ex + 2.0 ** -20 + 2.0 ** -17 + (p.lk[i] / 8 + 2) * 2.0 ** -22
+        tol = 2.0 ** -8 * np.abs(ro[rows]) + fine * a[rows] + 1e-30
+        err = np.abs(_wide(out[rows]) - ro[rows])
+        assert (err <= tol).all(), (i, (err / tol).max())
+
+
 @pytest.mark.parametrize("layout", ["head", "block"])
 @pytest.mark.parametrize("name", ["decode_gqa16", "chunk_group5_d128", "mixed"])
 def test_attention_cache_layouts(layout, name):
