@@ -36,7 +36,8 @@ constexpr int kWarps = 4;          // computing warps
 constexpr int kThreads = 2 * kWarps * 32;
 // registers of a thread: 128 at launch (two CTAs per SM), then split unevenly
 constexpr int kProdRegs = 64, kCompRegs = 192;
-static_assert(kProdRegs + kCompRegs <= 2 * 128, "what the block was launched with");
+constexpr int kRegsNeeded = kThreads / 2 * (kProdRegs + kCompRegs);  // a build with fewer is refused
+static_assert(kRegsNeeded <= kThreads * 128, "what the block is launched with");
 constexpr int kRing = 3;           // stages per warp
 constexpr int kShortStages = 2;    // items of at most this many stages are one warp's
 constexpr int kMinShare = 8;       // stages a CTA takes at least
@@ -667,7 +668,8 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
   if (!rc) rc = make_tmap_pages(&mv, c.v, c, rows, &pp.head_outer);
   if (rc) return rc;
   const size_t smem = FewCfg<D>::bytes(p.bias) + 1024;
-  if (prepare_kernel((const void *)fat_paged_few_kernel<D>, smem, kThreads, 0)) return FAT_ECUDA;
+  if (prepare_kernel((const void *)fat_paged_few_kernel<D>, smem, kThreads, kRegsNeeded))
+    return FAT_ECUDA;
   return launch_dependent("paged few-row kernel launch", fat_paged_few_kernel<D>,
                           dim3((unsigned)paged_few_ctas()), kThreads, smem, stream, mk, mv, pp);
 }

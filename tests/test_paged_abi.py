@@ -232,3 +232,23 @@ def test_rope_rows_of_the_result_lie_apart(lib):
     assert _embed(lib, r, ys=(128, 128)) == -2
     assert _embed(lib, r, ys=(64, 192)) == -2
     assert _embed(lib, r, tokens=0, ys=(64, 256)) == 0
+
+
+def test_register_splits_are_checked_before_a_launch():
+    """A kernel whose warps raise their register share waits for registers that a build with fewer of
+    them never frees: its launcher has to hand the split's need to prepare_kernel, which refuses such
+    a build."""
+    import glob
+    import os
+    import re
+    found = {}
+    for path in glob.glob(os.path.join(_build.CSRC, "*.cu")):
+        text = open(path).read()
+        if not re.search(r"\bregs_inc<", text):
+            continue
+        calls = re.findall(r"\bprepare_kernel\(((?:[^()]|\([^()]*\))*)\)", text)
+        found[os.path.basename(path)] = [c.rsplit(",", 1)[1].strip() for c in calls]
+    assert {"fat_attn_fwd.cu", "fat_paged_few.cu", "fat_paged_tile.cu"} <= set(found)
+    for name, needs in found.items():
+        assert needs and all(re.fullmatch(r"\w*(::)?(REGS_NEEDED|kRegsNeeded)", n) for n in needs), \
+            (name, needs)
