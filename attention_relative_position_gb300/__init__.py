@@ -663,7 +663,8 @@ def fat_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, rope
 
 def fat_paged_attn_workspace_size(q, k_cache, cu_seqlens_q, max_seqlen_q: int,
                                   max_seqlen_k: int) -> int:
-    """Workspace bytes of fat_paged_attn for these arguments on q's device."""
+    """Workspace bytes of fat_paged_attn for these arguments on q's device, and for every call of
+    fewer rows, requests, queries or keys: a buffer for the largest bounds serves all steps."""
     return (_calls or _load_calls()).attn_workspace(q, k_cache, cu_seqlens_q, max_seqlen_q,
                                                     max_seqlen_k)
 

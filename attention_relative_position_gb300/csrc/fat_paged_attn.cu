@@ -159,6 +159,10 @@ struct Plan {
   bool few, tile, split;
   size_t few_off, bytes;
 };
+size_t tile_part_bytes(int d) {
+  return (part_floats(paged_tile_ctas(), kTileRows, d) * 4 + 255) & ~(size_t)255;
+}
+size_t few_part_bytes(int d) { return part_floats(paged_few_ctas(), kFewRows, d) * 4; }
 Plan make_plan(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
   Plan l{};
   const long long rows = (long long)sh->max_seqlen_q * (sh->num_heads_q / c->num_heads);
@@ -167,11 +171,21 @@ Plan make_plan(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
   l.split = sh->max_seqlen_k >
             (l.tile ? kWholeKeys : kWholeStages * few_stage_tokens(c->head_dim));
   if (!l.split) return l;
-  if (l.tile)
-    l.few_off =
-        (part_floats(paged_tile_ctas(), kTileRows, c->head_dim) * 4 + 255) & ~(size_t)255;
-  l.bytes = l.few_off + (l.few ? part_floats(paged_few_ctas(), kFewRows, c->head_dim) * 4 : 0);
+  if (l.tile) l.few_off = tile_part_bytes(c->head_dim);
+  l.bytes = l.few_off + (l.few ? few_part_bytes(c->head_dim) : 0);
   return l;
+}
+
+// What every call within the bounds can do with: of two plans' partial rows a smaller call may need
+// those that the larger one does not (single tokens cut contexts that a chunk leaves whole, and a call
+// of padded rows launches both kernels), so each kernel's are counted wherever some call needs them.
+size_t workspace_bound(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
+  const long long rows = (long long)sh->max_seqlen_q * (sh->num_heads_q / c->num_heads);
+  size_t bytes = 0;
+  if (rows > kFewRows && sh->max_seqlen_k > kWholeKeys) bytes += tile_part_bytes(c->head_dim);
+  if (sh->max_seqlen_k > kWholeStages * few_stage_tokens(c->head_dim))
+    bytes += few_part_bytes(c->head_dim);
+  return bytes;
 }
 
 int check_shape(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
@@ -199,7 +213,7 @@ extern "C" {
 
 size_t fat_paged_attn_workspace_size(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache) {
   if (check_shape(sh, cache)) return 0;
-  return make_plan(sh, cache).bytes;
+  return workspace_bound(sh, cache);
 }
 
 int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, const void *q,

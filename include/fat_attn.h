@@ -457,7 +457,8 @@ int fat_paged_append(const fat_append_shape_t *shape, const fat_paged_cache_t *c
  *     cu_seqlens_q; its rows are left as they were.
  *   - workspace: fat_paged_attn_workspace_size bytes (256-byte aligned, contents need not be
  *     initialised), for this call alone until it has finished: calls that may overlap, and captured
- *     graphs that do, take one each.
+ *     graphs that do, take one each. The size never falls as total_q, num_seqs, max_seqlen_q or
+ *     max_seqlen_k grows: one buffer for the largest bounds serves every smaller step too.
  * head_dim 64 or 128, num_heads_q / num_heads at most 128, max_seqlen_k at most 2^30.
  * FAT_EUNSUPPORTED: more query heads per key/value head, longer bounds, bias tables that shared
  * memory does not hold (saturation distances of more than 8192 keys in all, or num_buckets *

@@ -464,6 +464,27 @@ def test_attention_bounds_padding_and_repeats(name):
     assert torch.equal(a[:p.total], b[:p.total]) and torch.equal(la[:, :p.total], lb[:, :p.total])
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(16, 4, 128), (6, 2, 64)])
+def test_one_workspace_serves_every_smaller_step(hq, hkv, d):
+    """A buffer for the largest bounds: a chunk, a full batch of equal chunks, the same with padding and
+    single tokens run in it."""
+    small = dict(hq=hq, hkv=hkv, d=d, page=16, alibi=True)
+    for lk in (1000, 3000):
+        steps = [Problem(lq=[200, 30, 1, 1], lk=[lk, 700, 900, 40], seed=80, **small),
+                 Problem(lq=[50] * 4, lk=[lk, 700, 900, 50], seed=81, **small),
+                 Problem(lq=[50, 50, 50, 49], lk=[lk, 700, 900, 50], seed=82, **small),
+                 Problem(lq=[1] * 4, lk=[lk, 700, 900, 40], seed=83, **small),
+                 Problem(lq=[2, 1], lk=[lk, 600], seed=84, **small)]
+        big = steps[0]
+        size = fa.fat_paged_attn_workspace_size(big.q, big.kc, _i32(big.cu), 200, lk)
+        ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+        for p in steps:
+            assert p.total <= big.total and p.n <= big.n
+            out, lse = p.run(workspace=ws, max_q=int(max(p.lq)))
+            assert _errors() == 0
+            p.check(out, lse)
+
+
 @pytest.mark.parametrize("lq,pad", [([40, 1, 3, 40], 76), ([9, 9, 9], 0), ([1, 0, 0, 33], 98)])
 def test_attention_rows_that_look_equal(lq, pad):
     """total_q = num_seqs * max_seqlen_q, with equal requests or with padding: every row is there."""

@@ -252,3 +252,32 @@ def test_register_splits_are_checked_before_a_launch():
     for name, needs in found.items():
         assert needs and all(re.fullmatch(r"\w*(::)?(REGS_NEEDED|kRegsNeeded)", n) for n in needs), \
             (name, needs)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 12, 12), (128, 16, 4), (64, 32, 1), (128, 8, 8)])
+def test_workspace_size_never_falls_with_the_bounds(lib, d, hq, hkv):
+    """A buffer for the largest step serves every smaller one: the size for a call is at most what any
+    call of larger bounds is told."""
+    c = _cache(num_heads=hkv, head_dim=d, stride_head=d, stride_token=hkv * d,
+               stride_page=16 * hkv * d)
+
+    def size(total_q, n, max_q, max_k):
+        return lib.fat_paged_attn_workspace_size(
+            fa._PagedShape(total_q, n, max_q, max_k, hq, 1 << 20, None), ctypes.byref(c))
+
+    keys = (1, 380, 400, 760, 770, 1000, 1024, 1025, 4096, 100000)
+    queries = (1, 2, 4, 5, 16, 17, 512)
+    for n in (1, 4, 40):
+        for i, k in enumerate(keys):
+            for j, q in enumerate(queries):
+                for total in (1, n * q - 1, n * q, n * q + 7):
+                    if total < 1:
+                        continue
+                    s = size(total, n, q, k)
+                    for t2, n2, q2, k2 in ((total + 1, n, q, k), (n * q, n, q, k),
+                                           (total, n + 1, q, k),
+                                           (total, n, queries[min(j + 1, len(queries) - 1)], k),
+                                           (total, n, q, keys[min(i + 1, len(keys) - 1)]),
+                                           (n * 512, n, 512, k), (n * 512, n, 512, 100000)):
+                        if t2 >= total and q2 >= q and k2 >= k:
+                            assert size(t2, n2, q2, k2) >= s, (total, n, q, k, t2, n2, q2, k2)
