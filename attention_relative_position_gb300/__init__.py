@@ -612,7 +612,7 @@ def fat_paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size: int, 
     pages it lacks are taken from free_pages in request order and written to block_table (int32
     [n, width], in place). Returns (cu_seqlens_q [n + 1], seqlens_k [n], positions [max_tokens],
     slots [max_tokens], counts [2] = pages taken, tokens), all int32; tokens behind the last
-    request get position 0 and slot -1."""
+    request get position 0 and slot -1. Given results must not lie over other arguments."""
     r = (_calls or _load_calls()).plan(ctx_lens, new_lens, free_pages, block_table, page_size,
                                        num_pages, max_tokens, cu_seqlens_q, seqlens_k, positions,
                                        slots, counts, _stream_arg(stream))

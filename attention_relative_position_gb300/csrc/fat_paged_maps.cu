@@ -325,6 +325,16 @@ bool odd4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 // A stride of rows that are accessed 16 bytes at a time
 bool bad_stride(long long s) { return s < 0 || (s & 7) != 0; }
 
+struct Ints {
+  const int32_t *p;
+  long long count;
+};
+bool share_memory(const Ints &a, const Ints &b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.count > 0 && b.count > 0 && x < y + 4 * (uintptr_t)b.count &&
+         y < x + 4 * (uintptr_t)a.count;
+}
+
 // Whether rows of d elements at every combination of three indexes lie apart: from the smallest stride
 // on, each one is at least what the indexes before it span (an index of one value spans nothing).
 struct Extent {
@@ -434,6 +444,14 @@ int fat_paged_plan(const fat_plan_shape_t *sh, const int32_t *ctx_lens, const in
   if (odd4(ctx_lens) || odd4(new_lens) || odd4(free_pages) || odd4(block_table) ||
       odd4(cu_seqlens_q) || odd4(seqlens_k) || odd4(positions) || odd4(slots) || odd4(counts))
     return FAT_EINVAL_SHAPE;
+  // every block reads the lengths and the free list while others write: no result lies over them
+  const long long n = sh->num_seqs, T = sh->max_tokens;
+  const Ints arrays[9] = {{block_table, n * sh->table_width}, {cu_seqlens_q, n + 1}, {seqlens_k, n},
+                          {positions, T}, {slots, T}, {counts, 2}, {ctx_lens, n}, {new_lens, n},
+                          {free_pages, sh->num_free}};
+  for (int i = 0; i < 6; ++i)
+    for (int j = i + 1; j < 9; ++j)
+      if (share_memory(arrays[i], arrays[j])) return FAT_EINVAL_SHAPE;
   PlanParams p{};
   int rc = device_error_address(&p.err);
   if (rc) return rc;

@@ -368,6 +368,9 @@ typedef struct {
  * than table_width pages (it takes none), or a page index outside [0, num_pages); the tokens
  * concerned get slot -1. FAT_DEVERR_SEQLENS: a negative length (taken as 0 and 0), or more tokens
  * than max_tokens (cu_seqlens_q stops there). table_width = 0 is a table without entries.
+ * No result may lie over another array of the call (FAT_EINVAL_SHAPE): the lengths and the free list
+ * are read until the end. A program that keeps its lengths in place copies seqlens_k over ctx_lens
+ * behind the call.
  */
 typedef struct {
   int32_t num_seqs, page_size, num_pages;

@@ -281,3 +281,25 @@ def test_workspace_size_never_falls_with_the_bounds(lib, d, hq, hkv):
                                            (n * 512, n, 512, k), (n * 512, n, 512, 100000)):
                         if t2 >= total and q2 >= q and k2 >= k:
                             assert size(t2, n2, q2, k2) >= s, (total, n, q, k, t2, n2, q2, k2)
+
+
+def _plan_places():
+    """Places (from FAKE on, in entries) of the nine arrays of _plan, in its order, side by side."""
+    sizes = [2, 2, 3, 8, 3, 2, 5, 5, 2]  # ctx, new, free, table, cu, lens, positions, slots, counts
+    places = [sum(sizes[:i]) for i in range(9)]
+    return sizes, places
+
+
+@pytest.mark.parametrize("out", [3, 4, 5, 6, 7, 8])
+def test_plan_results_over_other_arrays_are_refused(lib, out):
+    """Lengths updated in place (seqlens_k over ctx_lens), say: other blocks still read them."""
+    sizes, places = _plan_places()
+    for other in range(9):
+        if other == out:
+            continue
+        for at in (places[other], places[other] + sizes[other] - 1, places[other] + 1 - sizes[out]):
+            p = [FAKE + 4 * (x + 64) for x in places]
+            # the other arrays lie far away, so that these two alone overlap
+            p = [x + (1 << 16) * i if i not in (out, other) else x for i, x in enumerate(p)]
+            p[out] = FAKE + 4 * (at + 64)
+            assert _plan(lib, dict(enumerate(p)), num_seqs=2) == -2, (out, other, at)
