@@ -437,6 +437,32 @@ def test_cache_of_one_page_inside_a_block_of_layers():
     assert block[:, :, 0].isnan().all() and block[:, :, 1, 20:].isnan().all()
 
 
+@pytest.mark.parametrize("pages,H", [(1, 2), (3, 1), (1, 1)])
+def test_caches_whose_single_entries_have_other_strides(pages, H):
+    """Keys cut out of a larger block, values on their own: strides over a single page or head differ
+    and say nothing."""
+    rng = np.random.default_rng(13)
+    S, d, n = 16, 64, 16 * pages
+    k, v, q = _bf16(rng, n, H, d), _bf16(rng, n, H, d), _bf16(rng, 2, H, d)
+    if pages == 1:
+        kc = torch.full((4, 2, S, H, d), float("nan"), dtype=torch.bfloat16, device=DEV)[2:3, 1]
+    else:  # one head, as a view that has a stride of its own for it
+        kc = torch.full((pages, S, H, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+        kc = kc.as_strided(kc.shape, (S * d, d, 8, 1))
+    vc = torch.full((pages, S, H, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    assert kc.stride() != vc.stride()
+    k2, v2 = kc.clone(memory_format=torch.contiguous_format), vc.clone()
+    got = []
+    for a, b in ((kc, vc), (k2, v2)):
+        fa.fat_paged_append(k, v, a, b, _i32(range(n)))
+        got.append(fa.fat_paged_attn(q, a, b, _i32([list(range(pages))]), _i32([0, 2]), _i32([n]), 2, n,
+                                     causal=True, softmax_scale=0.125))
+    assert _errors() == 0
+    assert torch.equal(kc, k2) and torch.equal(vc, v2)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert got[0][0].isfinite().all()
+
+
 @pytest.mark.parametrize("stale", [float("inf"), -float("inf"), 3e38])
 @pytest.mark.parametrize("name", ["decode_t5_ragged", "chunk_group1", "mixed_d128"])
 def test_attention_ignores_stale_slots(stale, name):
