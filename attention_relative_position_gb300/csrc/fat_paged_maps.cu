@@ -485,16 +485,16 @@ int fat_rope_init(fat_rope_t *r, int rotary_dim, int interleaved, double base, d
   if (rotary_dim < 16 || rotary_dim % 16 || rotary_dim > 2 * FAT_ROPE_MAX_PAIRS)
     return FAT_EINVAL_SHAPE;
   if (!(base > 1.0) || !std::isfinite(base) || !(factor > 0.0) || !std::isfinite(factor) ||
-      !(amplitude > 0.0) || !std::isfinite((float)amplitude) || !(original_length >= 0.0) ||
+      !((float)amplitude > 0.f) || !std::isfinite((float)amplitude) || !(original_length >= 0.0) ||
       !std::isfinite(original_length))
     return FAT_EINVAL_SHAPE;
   if (original_length > 0.0 &&
       (!(low_turns >= 0.0) || !(high_turns > low_turns) || !std::isfinite(high_turns)))
     return FAT_EINVAL_SHAPE;
-  *r = fat_rope_t{};
-  r->rotary_dim = rotary_dim;
-  r->interleaved = interleaved ? 1 : 0;
-  r->amplitude = (float)amplitude;
+  fat_rope_t made{};
+  made.rotary_dim = rotary_dim;
+  made.interleaved = interleaved ? 1 : 0;
+  made.amplitude = (float)amplitude;
   const double two_pi = 6.283185307179586476925286766559;
   for (int i = 0; i < rotary_dim / 2; ++i) {
     double turns = std::pow(base, -2.0 * i / rotary_dim) / two_pi;  // per position
@@ -503,9 +503,11 @@ int fat_rope_init(fat_rope_t *r, int rotary_dim, int interleaved, double base, d
       keep = std::min(1.0, std::max(0.0, (original_length * turns - low_turns) /
                                              (high_turns - low_turns)));
     turns = turns * keep + turns * (1.0 - keep) / factor;
+    if (!std::isfinite(turns)) return FAT_EINVAL_SHAPE;  // a factor next to zero
     const double scaled = std::ldexp(turns - std::floor(turns), 64);
-    r->rate[i] = scaled >= 18446744073709551615.0 ? ~0ull : (unsigned long long)scaled;
+    made.rate[i] = scaled >= 18446744073709551615.0 ? ~0ull : (unsigned long long)scaled;
   }
+  *r = made;
   return FAT_OK;
 }
 

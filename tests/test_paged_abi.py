@@ -303,3 +303,14 @@ def test_plan_results_over_other_arrays_are_refused(lib, out):
             p = [x + (1 << 16) * i if i not in (out, other) else x for i, x in enumerate(p)]
             p[out] = FAKE + 4 * (at + 64)
             assert _plan(lib, dict(enumerate(p)), num_seqs=2) == -2, (out, other, at)
+
+
+@pytest.mark.parametrize("kw", [dict(factor=1e-320), dict(factor=5e-324, base=2.0),
+                                dict(factor=5e-324, ramp=(1.0, 4.0, 64.0)),
+                                dict(amplitude=1e-60), dict(amplitude=1e-46)])
+def test_rope_init_values_that_vanish_are_refused(kw):
+    """A frequency that overflows, an amplitude that is 0 in the record's fp32."""
+    with pytest.raises(fa.FatAttnError) as e:
+        fa.fat_rope_init(64, **kw)
+    assert e.value.code == -2
+    fa.fat_rope_init(64, factor=1e-3, amplitude=1e-44)  # small, but a rotation
