@@ -7,8 +7,10 @@
 // three; four more fill the rings, one each, by TMA (boxes of 16 rows x 64 channels, of 32 where
 // stage and page hold as many, 128-byte swizzle), the page numbers of many stages loaded at once.
 // One warp for the four rings, a lane each, put a stage off every 0.9 us, and short contexts waited
-// for it: one token over 500 keys 9.4 us against 7.4. What is copied is marked to leave L2 first:
-// it is not read again (24 x 5 drafted tokens over 127 MB 33.2 us without, 30.5 with).
+// for it: one token over 500 keys 9.4 us against 7.4. What is copied is marked to leave L2 first: a
+// request reads it once (24 x 5 drafted tokens over 127 MB 33.2 us without, 30.5 with). Pages that
+// requests share (a common prefix) are found in L2 all the same: 32 tokens over one prefix of 4000 keys,
+// 32 heads over 8 of 128 channels, 49 us, over 32 contexts of their own 89.
 // Per stage and warp: S = Q K^T for 16 rows with warp-level matrix products (Q in registers), bias
 // and mask, a running maximum that moves only when it grows by more than 2^32, P in registers as a sum
 // of two bf16 numbers, O += P V. (With one, the error against 64 bits is 0.0022 where the output's own
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint8_t *ring = sm + w * kRing * C::STAGE;
     uint64_t *full = bars + w * kRing, *empty = bars + (kWarps + w) * kRing;
     const int log2_box = min(p.log2_page, C::LOG2_KT);  // rows of a copy
-    const uint64_t once = l2_evict_first();  // every key and value is read by one CTA, once
+    const uint64_t once = l2_evict_first();  // a request's keys and values are read once
     const int in_mask = (1 << p.log2_page) - 1;
     FewStages<D> ahead(start);
     int slot = 0, phase = 1;

@@ -511,6 +511,28 @@ def test_one_workspace_serves_every_smaller_step(hq, hkv, d):
             p.check(out, lse)
 
 
+@pytest.mark.parametrize("d,lq", [(64, [1] * 6), (128, [2] * 6), (64, [40, 1, 90, 3, 1, 33]),
+                                  (128, [70] * 6)])
+def test_requests_share_pages(d, lq):
+    """A common prefix of whole pages, named by every request: bit for bit the results over copies."""
+    page, prefix = 16, 1600
+    lk = [prefix + n + 7 * i for i, n in enumerate(lq)]
+    p = Problem(lq=lq, lk=lk, hq=8, hkv=2, d=d, page=page, alibi=True, seed=90)
+    m = prefix // page
+    for i in range(1, p.n):  # the first request's prefix, copied into the others' pages
+        for c in (p.kc, p.vc):
+            c[torch.as_tensor(p.table[i, :m])] = c[torch.as_tensor(p.table[0, :m])]
+    want, wl = p.run()
+    for i in range(1, p.n):
+        for c in (p.kc, p.vc):
+            c[torch.as_tensor(p.table[i, :m])] = float("nan")  # read no more
+        p.table[i, :m] = p.table[0, :m]
+    out, lse = p.run()
+    assert _errors() == 0
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    p.check(out, lse)
+
+
 @pytest.mark.parametrize("lq,pad", [([40, 1, 3, 40], 76), ([9, 9, 9], 0), ([1, 0, 0, 33], 98)])
 def test_attention_rows_that_look_equal(lq, pad):
     """total_q = num_seqs * max_seqlen_q, with equal requests or with padding: every row is there."""
