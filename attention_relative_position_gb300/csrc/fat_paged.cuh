@@ -16,7 +16,7 @@
 namespace fat {
 
 constexpr int kMaxBiasSpan = 8192;     // sat_neg + sat_pos of a bias table, at most
-constexpr int kMaxBiasEntries = 4096;  // buckets x group, at most
+constexpr int kMaxBiasEntries = 4096;  // buckets x group, at most: larger tables are not tested
 
 struct PagedParams {
   int total_q, n, max_q, max_k, hq, hkv, group, width, log2_page, num_pages, head_outer;
@@ -56,7 +56,10 @@ __device__ __forceinline__ PagedDoc paged_doc(const PagedParams &p, int i) {
 
 // ---- costs --------------------------------------------------------------------------------------
 // Few-row kernel: stages of 8 KB of keys and values for every key/value head, and kFewItem for the
-// fixed costs of an item (its first loads, the merge of its warps).
+// fixed costs of an item (its first loads, the merge of its warps). From a graph, in us, for a cost of
+// 1 / 5 / 10 / 20: drafted tokens 30.1 / 26.5 / 25.0 / 24.8, mixed step 59.4 / 56.8 / 53.8 / 50.8, 64
+// requests of 1 to 1024 tokens over 500 to 8000 keys (32 heads over 8 of 128 channels) 219 / 217 / 212 /
+// 217, decode 100.9 / 100.2 / 98.8 / 99.2.
 __host__ __device__ constexpr int few_stage_tokens(int d) { return 2048 / d; }
 constexpr int kFewItem = 10;
 __host__ __device__ inline int few_item_cost(int stages) { return stages + kFewItem; }
@@ -72,7 +75,9 @@ struct FewCost {
 
 // Tile kernel: one block of queries of a request: tokens [q0, q0 + ntok), one or two tiles, the key
 // tiles that its rows see, its cost in (Q tile, key tile) pairs, kTileItem of them for the fixed costs
-// of an item (its first loads, its rows written).
+// of an item (its first loads, its rows written). From a graph, in us, for a cost of 1 / 2 / 5 / 10: 2 x
+// 1500 first tokens 88.9 / 84.6 / 79.8 / 80.0, 8 chunks of 32 to 64 tokens over 500 to 2000 keys 33.0 /
+// 32.7 / 30.9 / 32.0, 4 T5 chunks of 512 over 2048 to 4096 at head_dim 64 70.2 / 67.7 / 66.6 / 67.5.
 constexpr int kTileItem = 5;
 struct TileBlock {
   int q0, ntok, nkv, tiles, cost;
@@ -109,8 +114,10 @@ struct TileCost {
 // SMs n of the tile kernel when a call launches both kernels, so that they end together: with its
 // total a and the other's b in stages of the few-row kernel (a pair of tiles weighs kPairStages:
 // 0.96 us against 0.11 us of an SM at head_dim 128, measured) and its start longer by kStartStages,
-// kStartStages + a / n = b / (sms - n). Each kernel has at least one SM. (24 decode steps beside a
-// chunk of 384 tokens, 300 .. 6000 keys: 54 us; shares in proportion to the totals alone gave 62.)
+// kStartStages + a / n = b / (sms - n). Each kernel has at least one SM. From a graph, in us: 24 decode
+// steps beside a chunk of 384 tokens, 300 .. 6000 keys, 57 where shares in proportion to the totals alone
+// gave 62. At head_dim 64, for a pair's weight of 3 / 5 / 8: 40 requests of 1 to 256 tokens with T5 bias
+// 39.7 / 38.6 / 39.6, 48 of 1 to 768 tokens over 500 to 8000 keys 136 / 125 / 117.
 constexpr float kPairStages = 9.f, kPairStages64 = 5.f, kStartStages = 80.f;
 template <int D>
 __device__ __forceinline__ int tile_sms(const PagedParams &p, long long tile_total,
@@ -310,6 +317,7 @@ int paged_tile_ctas();
 //   head_dim 128, 8 requests, 32 heads over 8: 250 keys 9.3 / 10.4, 500 keys 12.2 / 11.5;
 //   chunks of 64 tokens, 32 heads over 8: 1000 keys 23.3 / 24.5 (32 chunks, head_dim 64: 38 / 43), 2000
 //   keys 37.2 / 28.2.
+// A call that launches both kernels goes by the tile kernel's figure for both of them.
 constexpr int kWholeStages = 24, kWholeKeys = 1024;
 int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
 int launch_paged_tile(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);

@@ -25,7 +25,7 @@
 // Bound by HBM: one token for each of 32 requests over 1024 .. 4096 keys, 64 heads over 16 of 128
 // channels, 602 MB in 102 us with the merge (5.9 TB/s, 0.87 of a copy's rate). Short calls are bound by
 // their start: 1.2 us to the shares, 0.9 to the first copy, 0.7 to its arrival, 0.6 a stage, 1.0 for
-// the merge of the warps (one token over 500 keys, 7.4 us).
+// the merge of the warps (one token over 500 keys, 7.6 us from a graph).
 #include <algorithm>
 #include <cstdint>
 

@@ -23,7 +23,7 @@ namespace {
 // scans all lengths by itself (they are read from L2; a separate scan launch would cost more than
 // the repeated reads) and then takes its share of the tokens and pages, finding each one's request
 // by binary search over the prefix sums in shared memory. Requests are taken kPlanTile at a time.
-// 64 requests with a token each: 3.4 us; 1000 requests with 47 K tokens: 4.7 us.
+// 64 requests with a token each: 3.7 us (3.4 from a graph); 1000 requests with 47 K tokens: 5.0 (4.7).
 constexpr int kPlanThreads = 256;
 constexpr int kPlanPer = 4;  // consecutive requests per thread
 constexpr int kPlanTile = kPlanThreads * kPlanPer;
@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kPlanThreads) fat_paged_plan_kernel(const Plan
 // heads are split over more threads (the run length is launch_rows' choice), since a decode step's
 // rows are bound by latency. Small blocks end more evenly: 16383 x 16 x 128 in 22.9 us (5.9 TB/s)
 // against 25.1 with 256 threads and half as many of them; 131072 x 12 x 64 in 59.3 us (6.8 TB/s, the
-// measured copy rate); 37 x 32 x 128 in 2.4 us, the latency of a launch and three dependent loads.
+// measured copy rate); 37 x 32 x 128 in 2.9 us (2.4 from a graph), the latency of a launch and three
+// dependent loads.
 // Angles as in fat_rope_apply: position * rate mod one turn in 64-bit integers, exact at any
 // position, its top 24 bits through sincospif.
 constexpr int kRowThreads = 128;
@@ -472,7 +473,7 @@ int fat_paged_plan(const fat_plan_shape_t *sh, const int32_t *ctx_lens, const in
   p.counts = counts;
   const int sms = sm_count() > 0 ? sm_count() : 152;
   // a block for every 256 tokens or requests, two per SM at most: a thread's tokens are looked up one
-  // after the other (47 K tokens of 1000 requests: 4.7 us, with a quarter of the blocks 6.6 us)
+  // after the other (47 K tokens of 1000 requests from a graph: 4.7 us, with a quarter of the blocks 6.6)
   const int units = std::max(sh->max_tokens, sh->num_seqs);
   const int blocks = std::max(1, std::min(2 * sms, (units + 255) / 256));
   return launch_dependent("paged plan launch", fat_paged_plan_kernel, dim3((unsigned)blocks),

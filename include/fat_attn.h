@@ -394,7 +394,8 @@ int fat_paged_plan(const fat_plan_shape_t *shape, const int32_t *ctx_lens, const
  *     theta'_i = theta_i * (keep_i + (1 - keep_i) / factor);
  *   amplitude multiplies the turned channels.
  * fat_rope_init (host only) fills the record, which a program keeps for all its calls; its fields
- * are the library's own. rotary_dim: a multiple of 16, 16 .. 256; base > 1; factor, amplitude > 0.
+ * are the library's own. rotary_dim: a multiple of 16, 16 .. 256; base > 1; factor, amplitude > 0
+ * (amplitude as fp32, and no factor so small that a frequency overflows).
  */
 #define FAT_ROPE_MAX_PAIRS 128
 typedef struct {
@@ -464,10 +465,13 @@ int fat_paged_append(const fat_append_shape_t *shape, const fat_paged_cache_t *c
  *     graphs that do, take one each. The size never falls as total_q, num_seqs, max_seqlen_q or
  *     max_seqlen_k grows: one buffer for the largest bounds serves every smaller step too.
  * head_dim 64 or 128, num_heads_q / num_heads at most 128, max_seqlen_k at most 2^30.
- * FAT_EUNSUPPORTED: more query heads per key/value head, longer bounds, bias tables that shared
- * memory does not hold (saturation distances of more than 8192 keys in all, or num_buckets *
- * num_heads_q / num_heads beyond 4096 entries), or cache strides of which, in rising order, one is
- * no multiple of the one before.
+ * A call whose total_q is exactly num_seqs * max_seqlen_q (beyond 16 rows a request, queries x
+ * group) is taken as a batch of equal chunks; a step whose rows are padded to that total runs faster
+ * with a row more.
+ * FAT_EUNSUPPORTED: more query heads per key/value head, longer bounds, saturation distances of more
+ * than 8192 keys in all (their buckets are looked up in shared memory), bias tables of more than 4096
+ * entries a key/value head (num_buckets * num_heads_q / num_heads: a limit of what is tested), or cache
+ * strides of which, in rising order, one is no multiple of the one before.
  */
 typedef struct {
   int32_t total_q;      /* rows of q and out */
