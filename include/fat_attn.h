@@ -431,7 +431,7 @@ int fat_rope_embed(const fat_rope_shape_t *shape, const fat_rope_t *rope, const 
  * [tokens, num_heads_q, head_dim] contiguous, of every token, padding included; q itself is
  * allowed when it is contiguous). q, k and v may be views of one packed projection: strides in
  * elements, multiples of 8. q and q_out are both given or both NULL; positions may be NULL without
- * rope.
+ * rope. Neither the caches nor q_out (q aside) lie over the call's other arrays, nor over one another.
  */
 typedef struct {
   int32_t tokens, num_heads_q;
@@ -452,7 +452,8 @@ int fat_paged_append(const fat_append_shape_t *shape, const fat_paged_cache_t *c
  *   - What lies in a page behind a request's last key is never used, whatever it holds (NaN and
  *     infinities included). Keys and values below seqlens_k are finite: a value that the causal
  *     mask hides from an earlier query of the same step still enters that query's product with
- *     weight 0. A NaN in a query, or in a key it sees, makes its output and lse NaN.
+ *     weight 0, and an infinite one makes the output NaN. A NaN in a query, or in a key it sees, makes
+ *     its output and lse NaN.
  *   - A bias of -infinity (or below -2e38: logits are formed times log2 e) masks its keys; a row
  *     that is left with none gets 0 and lse -infinity.
  *   - Requests may name the same pages (a common prefix).
