@@ -2,7 +2,7 @@
 padding-free varlen packing, forward and backward.
 
 This module is a thin binding over libfatattn.so (C ABI in include/fat_attn.h), by ctypes and, for the
-paged-cache calls, a small extension module: it only marshals torch tensors into pointers and sizes. Every step of the computation runs in the CUDA
+paged-cache and output-layer calls, a small extension module: it only marshals torch tensors into pointers and sizes. Every step of the computation runs in the CUDA
 kernels of the library; there is no other implementation to fall back to, and a missing or
 unloadable library raises immediately.
 """
@@ -19,7 +19,8 @@ __all__ = [
     "fat_attn_debug_buckets", "fat_attn_debug_set_watchdog", "fat_attn_bwd_stages",
     "fat_attn_bwd_noalloc", "fat_xattn_fwd", "fat_xattn_bwd", "fat_xattn_bwd_workspace_size",
     "fat_xattn_splitkv_num_splits", "fat_rope_apply", "fat_rmsnorm_fwd", "fat_rmsnorm_bwd",
-    "fat_cross_entropy", "fat_paged_plan", "fat_rope_init", "fat_rope_embed", "fat_paged_append",
+    "fat_cross_entropy", "fat_linear_cross_entropy_fwd", "fat_linear_cross_entropy_bwd",
+    "fat_linear_cross_entropy_workspace_size", "fat_paged_plan", "fat_rope_init", "fat_rope_embed", "fat_paged_append",
     "fat_paged_attn", "fat_paged_attn_workspace_size", "FAT_DEVERR_TIMEOUT_FWD",
     "FAT_DEVERR_TIMEOUT_BWD", "FAT_DEVERR_INDEX", "FAT_DEVERR_SEQLENS", "FAT_DEVERR_PAGES",
     "LIB_PATH",
@@ -89,6 +90,13 @@ class _AppendShape(ctypes.Structure):
                 ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
                 ("k_stride_token", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
                 ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
+                ("stream", ctypes.c_void_p)]
+
+
+class _LinearCeShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("hidden_stride", ctypes.c_int64), ("weight_stride", ctypes.c_int64),
+                ("logit_scale", ctypes.c_float), ("z_loss", ctypes.c_float),
                 ("stream", ctypes.c_void_p)]
 
 
@@ -162,6 +170,14 @@ def load(path: Optional[str] = None):
     lib.fat_rope_apply.argtypes = [S, vp, vp, vp, ctypes.c_double, i32]
     lib.fat_rope_apply.restype = i32
     P = ctypes.POINTER
+    H = P(_LinearCeShape)
+    lib.fat_linear_cross_entropy_workspace_size.argtypes = [H, i32]
+    lib.fat_linear_cross_entropy_workspace_size.restype = ctypes.c_size_t
+    lib.fat_linear_cross_entropy_fwd.argtypes = [H, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
+    lib.fat_linear_cross_entropy_fwd.restype = i32
+    lib.fat_linear_cross_entropy_bwd.argtypes = [H, vp, vp, vp, vp, vp, f32, vp, ctypes.c_size_t, vp,
+                                                 vp]
+    lib.fat_linear_cross_entropy_bwd.restype = i32
     lib.fat_paged_plan.argtypes = [P(_PlanShape)] + [vp] * 9
     lib.fat_paged_plan.restype = i32
     f64 = ctypes.c_double
@@ -572,7 +588,7 @@ def fat_cross_entropy(logits, target, z_loss: float = 0.0, grad_scale: float = 1
     return loss, lse, (dlogits if want_grad else None)
 
 
-# ---- paged key/value cache ---------------------------------------------------------------------
+# ---- paged key/value cache, output layer ---------------------------------------------------------
 # These calls serve single decode steps, where the host's time counts: their arguments are checked
 # and handed to the library by the extension module of csrc/paged_binding.cpp, in order.
 
@@ -603,6 +619,44 @@ def _load_calls():
 
 def _stream_arg(stream):
     return stream if stream is None else int(getattr(stream, "cuda_stream", stream))
+
+
+def fat_linear_cross_entropy_workspace_size(rows: int, vocab: int, dim: int,
+                                            backward: bool = False) -> int:
+    """Workspace bytes of fat_linear_cross_entropy_fwd (or _bwd) on the current device."""
+    return (_calls or _load_calls()).lce_workspace(rows, vocab, dim, backward)
+
+
+def fat_linear_cross_entropy_fwd(hidden, weight, target, z_loss: float = 0.0,
+                                 logit_scale: float = 1.0, loss=None, lse=None, workspace=None,
+                                 stream=None):
+    """Cross-entropy (with a z-loss term) of the logits logit_scale * hidden @ weight.T, which are not
+    kept: hidden bf16 [rows, dim] and weight bf16 [vocab, dim] (rows may be strided), target int32
+    [rows] (negative: ignored). With few rows minus the loss is the score (log-probability) of drafted
+    tokens. workspace: fat_linear_cross_entropy_workspace_size bytes (None: allocated here), for one
+    call at a time. Returns (loss fp32 [rows], lse fp32 [rows])."""
+    r = (_calls or _load_calls()).lce_fwd(hidden, weight, target, z_loss, logit_scale, loss, lse,
+                                          workspace, _stream_arg(stream))
+    if type(r) is int:
+        raise FatAttnError(r, "fat_linear_cross_entropy_fwd")
+    return r
+
+
+def fat_linear_cross_entropy_bwd(hidden, weight, target, lse, dloss=None, z_loss: float = 0.0,
+                                 logit_scale: float = 1.0, grad_scale: float = 1.0,
+                                 want_dhidden: bool = True, want_dweight: bool = True, dhidden=None,
+                                 dweight=None, workspace=None, stream=None):
+    """Gradients of grad_scale * sum(dloss * loss) for fat_linear_cross_entropy_fwd (dloss fp32 [rows];
+    None: ones), from its lse; the logits are computed again, a piece of the vocabulary at a time.
+    workspace: fat_linear_cross_entropy_workspace_size(..., backward=True) bytes (None: allocated here),
+    for one call at a time. Returns (dhidden bf16 [rows, dim] or None, dweight bf16 [vocab, dim] or
+    None)."""
+    r = (_calls or _load_calls()).lce_bwd(hidden, weight, target, lse, dloss, z_loss, logit_scale,
+                                          grad_scale, want_dhidden, want_dweight, dhidden, dweight,
+                                          workspace, _stream_arg(stream))
+    if type(r) is int:
+        raise FatAttnError(r, "fat_linear_cross_entropy_bwd")
+    return r
 
 
 def fat_paged_plan(ctx_lens, new_lens, free_pages, block_table, page_size: int, num_pages: int,

@@ -1,6 +1,6 @@
 """Builds libfatattn.so (the CUDA library behind include/fat_attn.h) in-tree with nvcc for
 sm_103a. Translation units compile in parallel; the link uses nvcc with the static CUDA runtime. The
-extension module of the paged-cache calls is compiled beside them with g++ against torch's headers."""
+extension module of the paged-cache and output-layer calls is compiled beside them with g++ against torch's headers."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -15,7 +15,7 @@ OBJ_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libfatattn.so")
 SOURCES = ["fat_attn_api.cu", "fat_attn_fwd.cu", "fat_attn_bwd.cu", "fat_attn_decode.cu",
            "fat_attn_noalloc.cu", "fat_rope.cu", "fat_norm_ce.cu", "fat_paged_maps.cu",
-           "fat_paged_attn.cu", "fat_paged_few.cu", "fat_paged_tile.cu"]
+           "fat_paged_attn.cu", "fat_paged_few.cu", "fat_paged_tile.cu", "fat_linear_ce.cu"]
 HEADERS = ["sm103_ptx.cuh", "fat_attn_internal.cuh", "fat_paged.cuh"]
 PUBLIC_HEADERS = [os.path.join(ROOT, "include", h) for h in ("fat_attn.h", "fat_attn_debug.h")]
 BINDING = "paged_binding.cpp"

@@ -423,6 +423,29 @@ int make_tmap_pages(CUtensorMap *map, const void *ptr, const fat_paged_cache_t &
   return FAT_OK;
 }
 
+int make_tmap_matrix(CUtensorMap *map, const void *ptr, long long rows, int cols, long long stride,
+                     int box_rows, bool fp32) {
+  TmapKey key{ptr, (int)rows, 0, cols, fp32 ? 32 : 64, box_rows, fp32 ? 1 : 0};
+  key.s_token = stride;
+  if (tmap_lookup(key, map)) return 0;
+  if (!resolve_encode()) return -1;
+  const int size = fp32 ? 4 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride * size};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        2, const_cast<void *>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_last_error("cuTensorMapEncodeTiled(matrix)", (int)r, "");
+    return -1;
+  }
+  tmap_store(key, *map);
+  return 0;
+}
+
 int make_tmap_thd_f32(CUtensorMap *map, const void *ptr, int T, int H, int d, int box_c,
                       int box_rows) {
   const TmapKey key{ptr, T, H, d, box_c, box_rows, 1};

@@ -423,6 +423,10 @@ int make_tmap_rows(CUtensorMap *map, const void *ptr, int T, int H, int d, int b
 int check_page_strides(const fat_paged_cache_t &c);
 int make_tmap_pages(CUtensorMap *map, const void *ptr, const fat_paged_cache_t &c, int box_rows,
                     int *head_outer);
+// Tensor map over a matrix of rows of `cols` bf16 or fp32 elements, `stride` elements apart: boxes of
+// 128 bytes x box_rows rows, 128-byte swizzle.
+int make_tmap_matrix(CUtensorMap *map, const void *ptr, long long rows, int cols, long long stride,
+                     int box_rows, bool fp32);
 // Tensor map over a [T, H, d] fp32 tensor, box = box_c channels x 1 head x box_rows tokens (for
 // bulk reductions from a shared-memory tile): 64-byte swizzle when a box row is 64 bytes (16-byte
 // chunk c of row r at c ^ ((r / 2) % 4)), else row-major without swizzle.

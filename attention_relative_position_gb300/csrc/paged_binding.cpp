@@ -1,4 +1,4 @@
-// paged_binding.cpp -- Python side of the paged-cache calls (module _paged_calls): checks the
+// paged_binding.cpp -- Python side of the paged-cache and output-layer calls (module _paged_calls): checks the
 // tensors, allocates the results and calls the C ABI of libfatattn.so. A decode step is bound by the
 // host's time per call, and the same checks in Python cost 10 to 20 us a call on the host cores (25 us
 // against 10 for a one-token attention step). The public functions, with their documentation, are
@@ -12,6 +12,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 
+#include <optional>
+
 #include "../../include/fat_attn.h"
 
 namespace {
@@ -21,6 +23,9 @@ decltype(&fat_rope_embed) p_rope;
 decltype(&fat_paged_append) p_append;
 decltype(&fat_paged_attn) p_attn;
 decltype(&fat_paged_attn_workspace_size) p_attn_ws;
+decltype(&fat_linear_cross_entropy_fwd) p_lce_fwd;
+decltype(&fat_linear_cross_entropy_bwd) p_lce_bwd;
+decltype(&fat_linear_cross_entropy_workspace_size) p_lce_ws;
 PyObject *g_rope_type;  // the Python class of fat_rope_t records
 
 struct Refused {};  // a Python exception is set
@@ -407,6 +412,130 @@ ENTRY(attn, 19)
   return res;
 ENTRY_END
 
+// ---- output layer and loss
+fat_linear_ce_shape_t head_shape(const at::Tensor &h, const at::Tensor &w, PyObject *z_loss,
+                                 PyObject *logit_scale) {
+  check_rows(h, "hidden", 2, -1);
+  check_rows(w, "weight", 2, h.get_device());
+  if (w.size(1) != h.size(1))
+    refuse(PyExc_ValueError, "%s and hidden have different row lengths", "weight");
+  fat_linear_ce_shape_t sh{};
+  sh.rows = small(h.size(0), "hidden");
+  sh.vocab = small(w.size(0), "weight");
+  sh.dim = small(h.size(1), "hidden");
+  // a stride over one row says nothing
+  sh.hidden_stride = h.size(0) > 1 ? h.stride(0) : h.size(1);
+  sh.weight_stride = w.size(0) > 1 ? w.stride(0) : w.size(1);
+  sh.z_loss = (float)number(z_loss);
+  sh.logit_scale = (float)number(logit_scale);
+  return sh;
+}
+// A given workspace, or one of the size that the call needs, made here.
+struct Workspace {
+  at::Tensor made;
+  void *ptr;
+  size_t bytes;
+  template <typename F>
+  Workspace(PyObject *o, int dev, F size) {
+    if (o == Py_None) {
+      const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+      bytes = size();
+      made = make({(int64_t)bytes}, at::kByte, dev);
+      ptr = made.data_ptr();
+      return;
+    }
+    const at::Tensor &t = tensor(o, "workspace");
+    if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
+      refuse(PyExc_ValueError, "%s must be a contiguous CUDA tensor on the device of the call",
+             "workspace");
+    ptr = t.data_ptr();
+    bytes = t.nbytes();
+  }
+};
+// A result: the given tensor, or one made here.
+struct Result {
+  at::Tensor made;
+  PyObject *given;
+  void *ptr;
+  Result(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType type, int dev) : given(o) {
+    if (o == Py_None) {
+      made = make(shape, type, dev);
+      ptr = made.data_ptr();
+      return;
+    }
+    const at::Tensor &t = tensor(o, name);
+    check(t, name, type, dev);
+    check_shape(t, name, shape);
+    check_contiguous(t, name);
+    ptr = t.data_ptr();
+  }
+  PyObject *object() const { return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(given); }
+};
+PyObject *two(PyObject *a, PyObject *b) {
+  PyObject *res = PyTuple_New(2);
+  if (!res) return nullptr;
+  PyTuple_SET_ITEM(res, 0, a);
+  PyTuple_SET_ITEM(res, 1, b);
+  return res;
+}
+
+// rows, vocab, dim, backward
+ENTRY(lce_workspace, 4)
+  fat_linear_ce_shape_t sh{};
+  sh.rows = integer(a[0], "rows");
+  sh.vocab = integer(a[1], "vocab");
+  sh.dim = integer(a[2], "dim");
+  sh.hidden_stride = sh.weight_stride = sh.dim;
+  sh.logit_scale = 1.f;
+  return PyLong_FromSize_t(p_lce_ws(&sh, truth(a[3]) ? 1 : 0));
+ENTRY_END
+
+// hidden, weight, target, z_loss, logit_scale, loss, lse, workspace, stream
+ENTRY(lce_fwd, 9)
+  const at::Tensor &h = tensor(a[0], "hidden"), &w = tensor(a[1], "weight");
+  fat_linear_ce_shape_t sh = head_shape(h, w, a[3], a[4]);
+  const int dev = h.get_device();
+  const int32_t *target = ints(a[2], "target", sh.rows, dev);
+  const OnStream on(a[8], dev);
+  sh.stream = on.stream;
+  const Result loss(a[5], "loss", {sh.rows}, at::kFloat, dev);
+  const Result lse(a[6], "lse", {sh.rows}, at::kFloat, dev);
+  const Workspace ws(a[7], dev, [&] { return p_lce_ws(&sh, 0); });
+  const int rc = call_on(dev, [&] {
+    return p_lce_fwd(&sh, h.data_ptr(), w.data_ptr(), target, ws.ptr, ws.bytes,
+                     static_cast<float *>(loss.ptr), static_cast<float *>(lse.ptr));
+  });
+  if (rc) return PyLong_FromLong(rc);
+  return two(loss.object(), lse.object());
+ENTRY_END
+
+// hidden, weight, target, lse, dloss, z_loss, logit_scale, grad_scale, want_dhidden, want_dweight, dhidden,
+// dweight, workspace, stream
+ENTRY(lce_bwd, 14)
+  const at::Tensor &h = tensor(a[0], "hidden"), &w = tensor(a[1], "weight");
+  fat_linear_ce_shape_t sh = head_shape(h, w, a[5], a[6]);
+  const int dev = h.get_device();
+  const int32_t *target = ints(a[2], "target", sh.rows, dev);
+  const float *lse = floats(a[3], "lse", {sh.rows}, dev);
+  const float *dloss = a[4] == Py_None ? nullptr : floats(a[4], "dloss", {sh.rows}, dev);
+  const float grad_scale = (float)number(a[7]);
+  const bool want_h = truth(a[8]), want_w = truth(a[9]);
+  if ((!want_h && a[10] != Py_None) || (!want_w && a[11] != Py_None))
+    refuse(PyExc_ValueError, "%s is given but not wanted", want_h ? "dweight" : "dhidden");
+  const OnStream on(a[13], dev);
+  sh.stream = on.stream;
+  std::optional<Result> dh, dw;
+  if (want_h) dh.emplace(a[10], "dhidden", h.sizes(), at::kBFloat16, dev);
+  if (want_w) dw.emplace(a[11], "dweight", w.sizes(), at::kBFloat16, dev);
+  const Workspace ws(a[12], dev, [&] { return p_lce_ws(&sh, 1); });
+  const int rc = call_on(dev, [&] {
+    return p_lce_bwd(&sh, h.data_ptr(), w.data_ptr(), target, lse, dloss, grad_scale, ws.ptr, ws.bytes,
+                     dh ? dh->ptr : nullptr, dw ? dw->ptr : nullptr);
+  });
+  if (rc) return PyLong_FromLong(rc);
+  return two(dh ? dh->object() : Py_NewRef(Py_None), dw ? dw->object() : Py_NewRef(Py_None));
+ENTRY_END
+
 // path of libfatattn.so, class of the rotary records
 ENTRY(bind, 2)
   const char *path = PyUnicode_AsUTF8(a[0]);
@@ -421,6 +550,9 @@ ENTRY(bind, 2)
   BIND(p_append, "fat_paged_append");
   BIND(p_attn, "fat_paged_attn");
   BIND(p_attn_ws, "fat_paged_attn_workspace_size");
+  BIND(p_lce_fwd, "fat_linear_cross_entropy_fwd");
+  BIND(p_lce_bwd, "fat_linear_cross_entropy_bwd");
+  BIND(p_lce_ws, "fat_linear_cross_entropy_workspace_size");
 #undef BIND
   Py_XSETREF(g_rope_type, Py_NewRef(a[1]));
   Py_RETURN_NONE;
@@ -428,7 +560,8 @@ ENTRY_END
 
 #define METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(plan),           METHOD(rope), METHOD(append),
-                         METHOD(attn_workspace), METHOD(attn), METHOD(bind),
+                         METHOD(attn_workspace), METHOD(attn), METHOD(lce_workspace),
+                         METHOD(lce_fwd),        METHOD(lce_bwd), METHOD(bind),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

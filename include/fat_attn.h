@@ -65,7 +65,7 @@ extern "C" {
 /* bits of the device error word */
 #define FAT_DEVERR_TIMEOUT_FWD 1 /* a forward pipeline wait exceeded its time limit */
 #define FAT_DEVERR_TIMEOUT_BWD 2 /* a backward pipeline wait exceeded its time limit */
-#define FAT_DEVERR_INDEX 8       /* fat_cross_entropy: a target at or beyond the vocabulary */
+#define FAT_DEVERR_INDEX 8       /* a target at or beyond the vocabulary, a slot beyond the cache */
 #define FAT_DEVERR_SEQLENS 4     /* cu_seqlens had an entry outside [0, total_tokens] or out of
                                     order, or a document longer than max_seqlen (its rows beyond
                                     the grid were not computed) */
@@ -329,6 +329,46 @@ int fat_rmsnorm_bwd(long long rows, int dim, const void *x, const float *weight,
 int fat_cross_entropy(long long rows, int vocab, const void *logits, const int32_t *target,
                       float z_loss, float grad_scale, float *loss, float *lse, void *dlogits,
                       void *stream);
+
+/*
+ * Cross-entropy of hidden rows over a vocabulary, the output layer's product and fat_cross_entropy's
+ * loss in one, without the logits in memory (an addition of this library):
+ *   z_rv = logit_scale * (hidden_r . weight_v),  lse_r = log sum_v exp(z_rv),
+ *   loss_r = lse_r - z_r,target + z_loss * lse_r^2;
+ *   rows with a negative target are ignored (loss 0, gradient 0; lse is theirs all the same).
+ * With few rows: minus the loss is the log-probability of a drafted token.
+ *   hidden: bf16 [rows, dim], weight: bf16 [vocab, dim], rows hidden_stride and weight_stride elements
+ *   apart; target int32 [rows]; loss, lse fp32 [rows] (either may be NULL).
+ * fat_linear_cross_entropy_bwd: gradients of grad_scale * sum_r dloss_r loss_r (dloss fp32 [rows]; NULL:
+ *   ones), with lse as the forward gives it: dhidden bf16 [rows, dim] and dweight bf16 [vocab, dim], both
+ *   contiguous and OVERWRITTEN, either NULL if it is not wanted. dz, the gradient of the logits, is
+ *   rounded to bf16 as the operand of the two products; sums are fp32, without atomics whose order
+ *   matters: a call's result does not depend on timing. Hidden rows that are ignored may hold anything (NaN,
+ *   infinities); the others and the weights are finite.
+ *   A target at or beyond vocab sets FAT_DEVERR_INDEX (that row: loss 0, gradient 0).
+ * dim a multiple of 8, up to 65536; strides multiples of 8; any vocab and rows up to 2^28 each
+ * (FAT_EUNSUPPORTED beyond, and for more than 2^30 tiles of 256 rows x 16 entries); logit_scale > 0,
+ * z_loss >= 0. Index and statistics arrays need 4-byte alignment, the others 16. Results and workspace lie
+ * over no other array of the call. workspace: fat_linear_cross_entropy_workspace_size bytes (256-byte
+ * aligned, contents need not be initialised), for one call at a time: captured graphs that may overlap
+ * take one each. Its size depends on the current device's SMs. The forward's is 8 bytes for up to 256
+ * logits; the backward's holds a copy of the hidden rows and dz of two pieces of the vocabulary (up to 256 MB
+ * with their sums in fp32 beside them).
+ */
+typedef struct {
+  int32_t rows, vocab, dim;
+  int64_t hidden_stride, weight_stride; /* elements from row to row */
+  float logit_scale, z_loss;
+  void *stream;
+} fat_linear_ce_shape_t;
+size_t fat_linear_cross_entropy_workspace_size(const fat_linear_ce_shape_t *shape, int backward);
+int fat_linear_cross_entropy_fwd(const fat_linear_ce_shape_t *shape, const void *hidden,
+                                 const void *weight, const int32_t *target, void *workspace,
+                                 size_t workspace_bytes, float *loss, float *lse);
+int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *shape, const void *hidden,
+                                 const void *weight, const int32_t *target, const float *lse,
+                                 const float *dloss, float grad_scale, void *workspace,
+                                 size_t workspace_bytes, void *dhidden, void *dweight);
 
 /*
  * Paged key/value cache: the operators of a serving step. (No counterpart in the FAT5 report beyond
