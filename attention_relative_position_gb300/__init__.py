@@ -21,7 +21,7 @@ __all__ = [
     "fat_xattn_splitkv_num_splits", "fat_rope_apply", "fat_rmsnorm_fwd", "fat_rmsnorm_bwd",
     "fat_cross_entropy", "fat_linear_cross_entropy_fwd", "fat_linear_cross_entropy_bwd",
     "fat_linear_cross_entropy_workspace_size", "fat_paged_plan", "fat_rope_init", "fat_rope_embed", "fat_paged_append",
-    "fat_paged_attn", "fat_paged_attn_workspace_size", "FAT_DEVERR_TIMEOUT_FWD",
+    "fat_paged_attn", "fat_paged_attn_workspace_size", "fat_paged_tree_plan", "fat_paged_tree_attn", "FAT_DEVERR_TIMEOUT_FWD",
     "FAT_DEVERR_TIMEOUT_BWD", "FAT_DEVERR_INDEX", "FAT_DEVERR_SEQLENS", "FAT_DEVERR_PAGES",
     "LIB_PATH",
 ]
@@ -97,6 +97,12 @@ class _LinearCeShape(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("dim", ctypes.c_int32),
                 ("hidden_stride", ctypes.c_int64), ("weight_stride", ctypes.c_int64),
                 ("logit_scale", ctypes.c_float), ("z_loss", ctypes.c_float),
+                ("stream", ctypes.c_void_p)]
+
+
+class _TreeShape(ctypes.Structure):
+    _fields_ = [("total_q", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("max_seqlen_q", ctypes.c_int32), ("mask_words", ctypes.c_int32),
                 ("stream", ctypes.c_void_p)]
 
 
@@ -190,6 +196,11 @@ def load(path: Optional[str] = None):
     lib.fat_paged_attn.argtypes = [P(_PagedShape), P(_Cache), vp, vp, vp, vp, vp, i32, i32, i32,
                                    vp, i32, f32, vp, ctypes.c_size_t, vp, vp]
     lib.fat_paged_attn.restype = i32
+    lib.fat_paged_tree_plan.argtypes = [P(_TreeShape)] + [vp] * 5
+    lib.fat_paged_tree_plan.restype = i32
+    lib.fat_paged_tree_attn.argtypes = [P(_PagedShape), P(_Cache)] + [vp] * 6 + [
+        i32, vp, i32, i32, i32, vp, f32, vp, ctypes.c_size_t, vp, vp]
+    lib.fat_paged_tree_attn.restype = i32
     lib.fat_paged_attn_workspace_size.argtypes = [P(_PagedShape), P(_Cache)]
     lib.fat_paged_attn_workspace_size.restype = ctypes.c_size_t
     lib.fat_attn_get_device_error.argtypes = [vp, ctypes.POINTER(i32)]
@@ -740,6 +751,39 @@ def fat_paged_attn(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, ma
                                        softmax_scale, out, lse, workspace, _stream_arg(stream))
     if type(r) is int:
         raise FatAttnError(r, "fat_paged_attn")
+    return r
+
+
+def fat_paged_tree_plan(parents, cu_seqlens_q, seqlens_k, max_seqlen_q: int, positions=None,
+                        tree_mask=None, stream=None):
+    """The maps of a step whose new tokens are trees of drafted tokens: parents int32 [T], of each
+    node the index within its request of the earlier node that it follows (-1: the cached context).
+    Returns (positions int32 [T] = seqlens_k - nodes + depth, tree_mask int32 [T, words]: the bits of
+    the node's path). Rows behind the last request get 0."""
+    r = (_calls or _load_calls()).tree_plan(parents, cu_seqlens_q, seqlens_k, max_seqlen_q, positions,
+                                            tree_mask, _stream_arg(stream))
+    if type(r) is int:
+        raise FatAttnError(r, "fat_paged_tree_plan")
+    return r
+
+
+def fat_paged_tree_attn(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, positions,
+                        tree_mask, max_seqlen_q: int, max_seqlen_k: int, bias_table=None,
+                        num_buckets: int = 0, max_distance: int = 0, bidirectional: bool = True,
+                        alibi_slopes=None, softmax_scale: float = 1.0, out=None, lse=None,
+                        workspace=None, stream=None):
+    """fat_paged_attn for trees of drafted tokens (appended first): a query sees the keys before its
+    request's first query and, of the request's own, those whose bit is set in its row of tree_mask
+    (int32 [Tq, words], any pattern); biases go by positions (int32 [Tq]). fat_paged_tree_plan makes
+    both. workspace: fat_paged_attn_workspace_size bytes (None: allocated here), for one call at a
+    time. Returns (out bf16 [Tq, Hq, d], lse fp32 [Hq, Tq])."""
+    r = (_calls or _load_calls()).tree_attn(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k,
+                                            positions, tree_mask, max_seqlen_q, max_seqlen_k,
+                                            bias_table, num_buckets, max_distance, bidirectional,
+                                            alibi_slopes, softmax_scale, out, lse, workspace,
+                                            _stream_arg(stream))
+    if type(r) is int:
+        raise FatAttnError(r, "fat_paged_tree_attn")
     return r
 
 

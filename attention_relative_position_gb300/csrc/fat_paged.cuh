@@ -36,6 +36,12 @@ struct PagedParams {
   int sms;
   int split;      // 0: items are not cut (each goes to the CTA in whose share it begins)
   float *part;    // partial rows of this kernel's grid (see PartLayout)
+  // Trees (null: a request's queries follow one another): query j sees the keys before the request's
+  // first query and those further ones whose bit is set in its row of `mask`, and sits at key position
+  // pos[row], as does the key that it brings.
+  const int32_t *pos;
+  const uint32_t *mask;
+  int mask_words;
 };
 
 // A request as the kernels see it.
@@ -49,9 +55,27 @@ __device__ __forceinline__ PagedDoc paged_doc(const PagedParams &p, int i) {
   const int eq = __ldg(p.cu + i + 1);
   d.lk = __ldg(p.lk + i);
   d.ok = d.sq >= 0 && eq >= d.sq && eq <= p.total_q && eq - d.sq <= p.max_q && d.lk >= 0 &&
-         d.lk <= p.max_k && d.lk <= ((long long)p.width << p.log2_page);
+         d.lk <= p.max_k && d.lk <= ((long long)p.width << p.log2_page) &&
+         (p.pos == nullptr || d.lk >= eq - d.sq);
   d.lq = eq - d.sq;
   return d;
+}
+
+// Trees: the key position of row `row` of a request whose first query is at `shift` (its last key at
+// lk - 1): what lies outside is taken as the nearest end.
+__device__ __forceinline__ int tree_pos(const PagedParams &p, int row, int shift, int lk) {
+  return min(max(__ldg(p.pos + row), shift), lk - 1);
+}
+// The bits of keys n .. n + 31 behind the first query's for a row of the mask (n < 0: keys before it, which
+// every row sees); bits at or beyond lim are 0.
+__device__ __forceinline__ uint32_t tree_bits(const PagedParams &p, const uint32_t *row, int n,
+                                              int lim) {
+  if (n <= -32) return lim >= 32 ? 0xffffffffu : lim <= 0 ? 0u : (1u << lim) - 1u;
+  const int i = n >> 5;  // -1 for n in -32 .. -1
+  const uint32_t lo = i < 0 ? 0xffffffffu : i < p.mask_words ? __ldg(row + i) : 0u;
+  const uint32_t hi = i + 1 < p.mask_words ? __ldg(row + i + 1) : 0u;
+  const uint32_t b = __funnelshift_r(lo, hi, n & 31);
+  return lim >= 32 ? b : lim <= 0 ? 0u : b & ((1u << lim) - 1u);
 }
 
 // ---- costs --------------------------------------------------------------------------------------

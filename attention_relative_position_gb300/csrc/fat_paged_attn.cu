@@ -209,24 +209,17 @@ int check_shape(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
 
 bool odd(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
-}  // namespace
-}  // namespace fat
+struct Tree {
+  const int32_t *pos, *mask;
+  int words;
+};
 
-using namespace fat;
-
-extern "C" {
-
-size_t fat_paged_attn_workspace_size(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache) {
-  if (check_shape(sh, cache)) return 0;
-  return workspace_bound(sh, cache);
-}
-
-int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, const void *q,
-                   const int32_t *block_table, const int32_t *cu_seqlens_q,
-                   const int32_t *seqlens_k, const float *bias_table, int num_buckets,
-                   int max_distance, int bidirectional, const float *alibi_slopes, int causal,
-                   float softmax_scale, void *workspace, size_t workspace_bytes, void *out,
-                   float *lse) {
+// Both calls; tree: null for fat_paged_attn.
+int attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, const void *q,
+         const int32_t *block_table, const int32_t *cu_seqlens_q, const int32_t *seqlens_k,
+         const Tree *tree, const float *bias_table, int num_buckets, int max_distance,
+         int bidirectional, const float *alibi_slopes, int causal, float softmax_scale,
+         void *workspace, size_t workspace_bytes, void *out, float *lse) {
   int rc = check_shape(sh, cache);
   if (rc) return rc;
   int lg = 0;
@@ -243,8 +236,11 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
                      num_buckets * group > kMaxBiasEntries))
     return FAT_EUNSUPPORTED;
   if (sh->total_q == 0 || sh->num_seqs == 0 || sh->max_seqlen_q == 0) return FAT_OK;
-  if (!q || !cu_seqlens_q || !seqlens_k || !out || (sh->table_width > 0 && !block_table))
+  if (!q || !cu_seqlens_q || !seqlens_k || !out || (sh->table_width > 0 && !block_table) ||
+      (tree && (!tree->pos || !tree->mask)))
     return FAT_EINVAL_NULL;
+  if (tree && (odd(tree->pos, 4) || odd(tree->mask, 4) || tree->words < (sh->max_seqlen_q + 31LL) / 32))
+    return FAT_EINVAL_SHAPE;
   const Plan plan = make_plan(sh, cache);
   const size_t need = plan.bytes;
   if (need && !workspace) return FAT_EINVAL_NULL;
@@ -270,6 +266,11 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   p.lk = seqlens_k;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = softmax_scale * kLog2e;
+  if (tree) {
+    p.pos = tree->pos;
+    p.mask = reinterpret_cast<const uint32_t *>(tree->mask);
+    p.mask_words = tree->words;
+  }
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
   runtime_knobs(&p.timeout_ns, &p.debug_flags);
@@ -294,6 +295,42 @@ int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, 
   const int tile_ctas = plan.tile ? paged_tile_ctas() : 0, few_ctas = plan.few ? paged_few_ctas() : 0;
   return d == 64 ? launch_merge<64>(p, p.part, tile_ctas, pf.part, few_ctas, s)
                  : launch_merge<128>(p, p.part, tile_ctas, pf.part, few_ctas, s);
+}
+
+}  // namespace
+}  // namespace fat
+
+using namespace fat;
+
+extern "C" {
+
+size_t fat_paged_attn_workspace_size(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache) {
+  if (check_shape(sh, cache)) return 0;
+  return workspace_bound(sh, cache);
+}
+
+int fat_paged_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, const void *q,
+                   const int32_t *block_table, const int32_t *cu_seqlens_q,
+                   const int32_t *seqlens_k, const float *bias_table, int num_buckets,
+                   int max_distance, int bidirectional, const float *alibi_slopes, int causal,
+                   float softmax_scale, void *workspace, size_t workspace_bytes, void *out,
+                   float *lse) {
+  return attn(sh, cache, q, block_table, cu_seqlens_q, seqlens_k, nullptr, bias_table, num_buckets,
+              max_distance, bidirectional, alibi_slopes, causal, softmax_scale, workspace,
+              workspace_bytes, out, lse);
+}
+
+int fat_paged_tree_attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, const void *q,
+                        const int32_t *block_table, const int32_t *cu_seqlens_q,
+                        const int32_t *seqlens_k, const int32_t *positions,
+                        const int32_t *tree_mask, int mask_words, const float *bias_table,
+                        int num_buckets, int max_distance, int bidirectional,
+                        const float *alibi_slopes, float softmax_scale, void *workspace,
+                        size_t workspace_bytes, void *out, float *lse) {
+  const Tree tree{positions, tree_mask, mask_words};
+  return attn(sh, cache, q, block_table, cu_seqlens_q, seqlens_k, &tree, bias_table, num_buckets,
+              max_distance, bidirectional, alibi_slopes, 0, softmax_scale, workspace, workspace_bytes,
+              out, lse);
 }
 
 }  // extern "C"

@@ -158,7 +158,7 @@ struct FewStages {
   }
 };
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(kThreads, 2)
     fat_paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
@@ -326,7 +326,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t qf[D / 16][4];
     int qpos[2], lim[2], head[2];
     float slope[2], far_pos[2], far_neg[2];
-    const int lim_all = p.causal ? min(shift, it.lk - 1) : it.lk - 1;  // every row sees up to here
+    // every row sees up to here
+    const int lim_all = TREE ? shift - 1 : p.causal ? min(shift, it.lk - 1) : it.lk - 1;
+    uint32_t bits[2];  // trees: which of the request's own keys (16 at most) a row sees
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[D / 8][4];
 #pragma unroll
@@ -353,6 +355,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < 2; ++i) {
           const int r = i ? r1 : r0, q = r / G;
           qpos[i] = q + shift;
+          if (TREE) {
+            const int row = it.sq + min(q, it.lq - 1);
+            qpos[i] = tree_pos(p, row, shift, it.lk);
+            bits[i] = __ldg(p.mask + (size_t)row * p.mask_words);
+            if (__ldg(p.pos + row) != qpos[i]) atomicOr(p.err, FAT_DEVERR_INDEX);
+          }
           head[i] = it.hk * G + (r - q * G);
           lim[i] = p.causal ? min(qpos[i], it.lk - 1) : it.lk - 1;
           slope[i] = p.bias.slopes ? __ldg(p.bias.slopes + head[i]) * kLog2e : 0.f;
@@ -400,9 +408,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[t][e] *= p.scale_log2;
-        } else if (k0 - (shift + it.lq - 1) >= p.bias.sat_pos ||
-                   k0 + KT - 1 - shift <= -p.bias.sat_neg) {  // every delta on one far side
-          const bool pos = k0 - (shift + it.lq - 1) >= p.bias.sat_pos;
+        } else if (TREE ? k0 + KT <= shift - p.bias.sat_neg
+                        : k0 - (shift + it.lq - 1) >= p.bias.sat_pos ||
+                              k0 + KT - 1 - shift <= -p.bias.sat_neg) {
+          // every delta on one far side
+          const bool pos = !TREE && k0 - (shift + it.lq - 1) >= p.bias.sat_pos;
           const float kk[2] = {pos ? -slope[0] : slope[0], pos ? -slope[1] : slope[1]};
           const float c0[2] = {fmaf(kk[0], (float)(kb - qpos[0]), pos ? far_pos[0] : far_neg[0]),
                                fmaf(kk[1], (float)(kb - qpos[1]), pos ? far_pos[1] : far_neg[1])};
@@ -417,7 +427,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int i = e >> 1, delta = kb + 8 * t + (e & 1) - qpos[i];
+              const int i = e >> 1;
+              int kp = kb + 8 * t + (e & 1);
+              if (TREE && kp >= shift)
+                kp = tree_pos(p, it.sq + min(kp - shift, it.lq - 1), shift, it.lk);
+              const int delta = kp - qpos[i];
               float b = -slope[i] * fabsf((float)delta);
               if (t5) {
                 const int bk = lut[min(max(delta + p.bias.sat_neg, 0), span)];
@@ -430,8 +444,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (kb + 8 * t + (e & 1) > lim[e >> 1]) x[t][e] = -INFINITY;
+            for (int e = 0; e < 4; ++e) {
+              const int key = kb + 8 * t + (e & 1);
+              bool hide = key > lim[e >> 1];
+              if (TREE && key >= shift) hide = hide || !((bits[e >> 1] >> ((key - shift) & 31)) & 1u);
+              if (hide) x[t][e] = -INFINITY;
+            }
         }
         // the running maximum, moved only when it grows by more than 2^32
         float mx[2] = {-INFINITY, -INFINITY};
@@ -661,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   grid_dep_wait();
 }
 
-template <int D>
+template <int D, bool TREE>
 int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
   PagedParams pp = p;
   CUtensorMap mk, mv;
@@ -670,9 +688,9 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
   if (!rc) rc = make_tmap_pages(&mv, c.v, c, rows, &pp.head_outer);
   if (rc) return rc;
   const size_t smem = FewCfg<D>::bytes(p.bias) + 1024;
-  if (prepare_kernel((const void *)fat_paged_few_kernel<D>, smem, kThreads, kRegsNeeded))
-    return FAT_ECUDA;
-  return launch_dependent("paged few-row kernel launch", fat_paged_few_kernel<D>,
+  const auto kernel = fat_paged_few_kernel<D, TREE>;
+  if (prepare_kernel((const void *)kernel, smem, kThreads, kRegsNeeded)) return FAT_ECUDA;
+  return launch_dependent("paged few-row kernel launch", kernel,
                           dim3((unsigned)paged_few_ctas()), kThreads, smem, stream, mk, mv, pp);
 }
 
@@ -681,7 +699,9 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
 int paged_few_ctas() { return 2 * (sm_count() > 0 ? sm_count() : 152); }
 
 int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
-  return c.head_dim == 64 ? launch_t<64>(p, c, stream) : launch_t<128>(p, c, stream);
+  if (p.pos != nullptr)
+    return c.head_dim == 64 ? launch_t<64, true>(p, c, stream) : launch_t<128, true>(p, c, stream);
+  return c.head_dim == 64 ? launch_t<64, false>(p, c, stream) : launch_t<128, false>(p, c, stream);
 }
 
 }  // namespace fat

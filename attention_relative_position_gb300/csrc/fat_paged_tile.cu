@@ -197,6 +197,40 @@ __device__ __forceinline__ void tile_edge(uint32_t tS, float scale_log2, float r
   tmem_st_wait();
 }
 
+// The same for trees, for the tiles that hold keys of the request's own tokens or lie near them: key
+// position by position (those of the own tokens are the tokens'), bias, and the row's bits. first: key of
+// column 0; row_mask: this row's words; tok0: the request's first token.
+template <int COLS>
+__device__ __forceinline__ void tile_tree(uint32_t tS, const PagedParams &p, const uint8_t *lut,
+                                          const float *tab, float slope, int qpos, int first, int shift,
+                                          int lk, int tok0, const uint32_t *row_mask) {
+#pragma unroll 1
+  for (int c = 0; c < COLS; c += 32) {
+    uint32_t x[32];
+    tmem_ld32(tS + c, x);
+    const int key0 = first + c;
+    const uint32_t bits = tree_bits(p, row_mask, key0 - shift, lk - key0);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float b = 0.f;
+      if (p.bias.has_bias) {
+        int kp = key0 + i;
+        if (kp >= shift) kp = tree_pos(p, tok0 + min(kp, lk - 1) - shift, shift, lk);
+        const int delta = kp - qpos;
+        b = -slope * fabsf((float)delta);
+        if (tab != nullptr) {
+          const int near = min(max(delta, -p.bias.sat_neg), p.bias.sat_pos);
+          b = fmaf(__ldg(tab + lut[near - p.bias.lut_lo] * p.hq), kLog2e, b);
+        }
+      }
+      const float v = fmaf(__uint_as_float(x[i]), p.scale_log2, b);
+      x[i] = __float_as_uint((bits >> i) & 1u ? v : -INFINITY);
+    }
+    tmem_st32(tS + c, x);
+  }
+  tmem_st_wait();
+}
+
 // 32 CHUNKS columns of the S row from tensor memory as logits x (log2 units):
 // S * scale + rowc + kk * j, columns from lim on masked; returns the row's maximum.
 template <int CHUNKS, bool LINEAR, bool MASK>
@@ -251,7 +285,7 @@ __device__ __forceinline__ void tile_exp(const uint32_t (&x)[CHUNKS][32], uint64
   }
 }
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     fat_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
@@ -643,7 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // positions: of the tile's first and last row, and of this one (a row without a token: as
       // the last one's)
       const int pos_lo = it.shift + it.q0 + t_row * tq, pos_hi = pos_lo + ntok - 1;
-      const int qpos = min(pos_lo + rq, pos_hi);
+      int qpos = min(pos_lo + rq, pos_hi);
+      const uint32_t *row_mask = nullptr;
+      if (TREE) {
+        const int at = it.row0 + t_row * tq + min(rq, ntok - 1);
+        qpos = tree_pos(p, at, it.shift, it.lk);
+        row_mask = p.mask + (size_t)at * p.mask_words;
+        if (__ldg(p.pos + at) != qpos) atomicOr(p.err, FAT_DEVERR_INDEX);
+      }
       const float slope = has_slopes ? __ldg(p.bias.slopes + h) * kLog2e : 0.f;
       const float *tab = has_table ? p.bias.table + h : nullptr;
       float c_pos = 0.f, c_neg = 0.f;
@@ -663,7 +704,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lim = min(it.lk - ks, p.causal ? qpos - ks + 1 : 128);
         float rowc = 0.f, kk = 0.f;
         bool near = false;
-        if (p.bias.has_bias) {
+        if (TREE) {  // own keys, and what is near them, by tile_tree
+          near = ks + 128 > it.shift - (p.bias.has_bias ? p.bias.sat_neg : 0);
+          kk = slope;
+          rowc = fmaf(kk, (float)(ks - qpos), c_neg);
+        } else if (p.bias.has_bias) {
           const bool far_pos = ks - pos_hi >= p.bias.sat_pos;
           near = !far_pos && ks + 127 - pos_lo > -p.bias.sat_neg;
           kk = far_pos ? -slope : slope;
@@ -681,7 +726,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool edge = near || need_mask;
           if (edge) {
             const uint8_t *row_lut = lut + (ks - qpos - p.bias.lut_lo);
-            if (near)
+            if (TREE)
+              tile_tree<128>(tS, p, lut, tab, slope, qpos, ks, it.shift, it.lk, it.row0 - it.q0,
+                             row_mask);
+            else if (near)
               tile_edge<128, true>(tS, scale, 0.f, 0.f, row_lut, tab, p.hq, slope, ks - qpos, lim);
             else
               tile_edge<128, false>(tS, scale, rowc, kk, row_lut, tab, p.hq, slope, ks - qpos, lim);
@@ -734,9 +782,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t x[2][32];
             float mx;
             if (near) {
-              tile_edge<64, true>(tH, p.scale_log2, 0.f, 0.f,
-                                  lut + (ks + c0 - qpos - p.bias.lut_lo), tab, p.hq, slope,
-                                  ks + c0 - qpos, lim - c0);
+              if (TREE)
+                tile_tree<64>(tH, p, lut, tab, slope, qpos, ks + c0, it.shift, it.lk, it.row0 - it.q0,
+                              row_mask);
+              else
+                tile_edge<64, true>(tH, p.scale_log2, 0.f, 0.f,
+                                    lut + (ks + c0 - qpos - p.bias.lut_lo), tab, p.hq, slope,
+                                    ks + c0 - qpos, lim - c0);
               mx = tile_logits<2, false, false>(tH, x, 1.f, -m_ref, 0.f, 0);
             } else {
               const float rc = fmaf(kk, (float)c0, rowc) - m_ref;
@@ -916,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool TREE>
 int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
   using C = TileCfg<D>;
   PagedParams pp = p;
@@ -927,9 +979,9 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
   if (rc) return rc;
   if (make_tmap_rows(&mq, p.q, p.total_q, p.hq, D, p.group, 128 / p.group)) return FAT_ECUDA;
   const size_t smem = 1024 + C::OFF_LUT + (p.bias.table ? (size_t)((p.bias.lut_len + 15) & ~15) : 0);
-  if (prepare_kernel((const void *)fat_paged_tile_kernel<D>, smem, kThreads, C::REGS_NEEDED))
-    return FAT_ECUDA;
-  return launch_dependent("paged tile kernel launch", fat_paged_tile_kernel<D>,
+  const auto kernel = fat_paged_tile_kernel<D, TREE>;
+  if (prepare_kernel((const void *)kernel, smem, kThreads, C::REGS_NEEDED)) return FAT_ECUDA;
+  return launch_dependent("paged tile kernel launch", kernel,
                           dim3((unsigned)paged_tile_ctas()), kThreads, smem, stream, mq, mk, mv, pp);
 }
 
@@ -938,7 +990,9 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
 int paged_tile_ctas() { return sm_count() > 0 ? sm_count() : 152; }
 
 int launch_paged_tile(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
-  return c.head_dim == 64 ? launch_t<64>(p, c, stream) : launch_t<128>(p, c, stream);
+  if (p.pos != nullptr)
+    return c.head_dim == 64 ? launch_t<64, true>(p, c, stream) : launch_t<128, true>(p, c, stream);
+  return c.head_dim == 64 ? launch_t<64, false>(p, c, stream) : launch_t<128, false>(p, c, stream);
 }
 
 }  // namespace fat

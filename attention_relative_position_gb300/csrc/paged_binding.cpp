@@ -23,6 +23,8 @@ decltype(&fat_rope_embed) p_rope;
 decltype(&fat_paged_append) p_append;
 decltype(&fat_paged_attn) p_attn;
 decltype(&fat_paged_attn_workspace_size) p_attn_ws;
+decltype(&fat_paged_tree_plan) p_tree_plan;
+decltype(&fat_paged_tree_attn) p_tree_attn;
 decltype(&fat_linear_cross_entropy_fwd) p_lce_fwd;
 decltype(&fat_linear_cross_entropy_bwd) p_lce_bwd;
 decltype(&fat_linear_cross_entropy_workspace_size) p_lce_ws;
@@ -339,97 +341,6 @@ ENTRY(attn_workspace, 5)
   return PyLong_FromSize_t(p_attn_ws(&sh, &c));
 ENTRY_END
 
-// q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q, max_seqlen_k, bias_table,
-// num_buckets, max_distance, bidirectional, alibi_slopes, causal, softmax_scale, out, lse, workspace,
-// stream
-ENTRY(attn, 19)
-  const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[3], "block_table");
-  check_rows(q, "q", 3, -1);
-  check_contiguous(q, "q");
-  const int dev = q.get_device();
-  const fat_paged_cache_t c = cache_of(a[1], a[2], dev);
-  const int64_t Tq = q.size(0), Hq = q.size(1);
-  if (q.size(2) != c.head_dim)
-    refuse(PyExc_ValueError, "%s and the cache have different head dimensions", "q");
-  check_rank(table, "block_table", 2);
-  const int64_t num = tensor(a[5], "seqlens_k").numel();
-  if (table.size(0) != num)
-    refuse(PyExc_ValueError, "%s must have a row for every request", "block_table");
-  const int32_t *pt = ints(a[3], "block_table", -1, dev);
-  const int32_t *pcu = ints(a[4], "cu_seqlens_q", num + 1, dev);
-  const int32_t *plk = ints(a[5], "seqlens_k", num, dev);
-  const int32_t nb = integer(a[9], "num_buckets"), md = integer(a[10], "max_distance");
-  const float *bias = a[8] == Py_None ? nullptr : floats(a[8], "bias_table", {nb, Hq}, dev);
-  const float *slopes = a[12] == Py_None ? nullptr : floats(a[12], "alibi_slopes", {Hq}, dev);
-  const int bidir = truth(a[11]) ? 1 : 0, causal = truth(a[13]) ? 1 : 0;
-  const float scale = (float)number(a[14]);
-  const OnStream on(a[18], dev);
-  const fat_paged_shape_t sh = attn_shape(q, num, table.size(1), a[6], a[7], on.stream);
-  at::Tensor out, lse, ws;
-  void *po;
-  float *pl;
-  if (a[15] == Py_None) {
-    out = make(q.sizes(), at::kBFloat16, dev);
-    po = out.data_ptr();
-  } else {
-    const at::Tensor &t = tensor(a[15], "out");
-    check(t, "out", at::kBFloat16, dev);
-    check_shape(t, "out", q.sizes());
-    check_contiguous(t, "out");
-    po = t.data_ptr();
-  }
-  if (a[16] == Py_None) {
-    lse = make({Hq, Tq}, at::kFloat, dev);
-    pl = static_cast<float *>(lse.data_ptr());
-  } else {
-    pl = const_cast<float *>(floats(a[16], "lse", {Hq, Tq}, dev));
-  }
-  void *pw;
-  size_t bytes;
-  if (a[17] == Py_None) {
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-    bytes = p_attn_ws(&sh, &c);
-    ws = make({(int64_t)bytes}, at::kByte, dev);
-    pw = ws.data_ptr();
-  } else {
-    const at::Tensor &t = tensor(a[17], "workspace");
-    if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
-      refuse(PyExc_ValueError, "%s must be a contiguous CUDA tensor on q's device", "workspace");
-    pw = t.data_ptr();
-    bytes = t.nbytes();
-  }
-  const int rc = call_on(dev, [&] {
-    return p_attn(&sh, &c, q.data_ptr(), pt, pcu, plk, bias, nb, md, bidir, slopes, causal, scale, pw,
-                  bytes, po, pl);
-  });
-  if (rc) return PyLong_FromLong(rc);
-  PyObject *o = out.defined() ? THPVariable_Wrap(out) : Py_NewRef(a[15]);
-  PyObject *l = lse.defined() ? THPVariable_Wrap(lse) : Py_NewRef(a[16]);
-  PyObject *res = PyTuple_New(2);
-  if (!res) return nullptr;
-  PyTuple_SET_ITEM(res, 0, o);
-  PyTuple_SET_ITEM(res, 1, l);
-  return res;
-ENTRY_END
-
-// ---- output layer and loss
-fat_linear_ce_shape_t head_shape(const at::Tensor &h, const at::Tensor &w, PyObject *z_loss,
-                                 PyObject *logit_scale) {
-  check_rows(h, "hidden", 2, -1);
-  check_rows(w, "weight", 2, h.get_device());
-  if (w.size(1) != h.size(1))
-    refuse(PyExc_ValueError, "%s and hidden have different row lengths", "weight");
-  fat_linear_ce_shape_t sh{};
-  sh.rows = small(h.size(0), "hidden");
-  sh.vocab = small(w.size(0), "weight");
-  sh.dim = small(h.size(1), "hidden");
-  // a stride over one row says nothing
-  sh.hidden_stride = h.size(0) > 1 ? h.stride(0) : h.size(1);
-  sh.weight_stride = w.size(0) > 1 ? w.stride(0) : w.size(1);
-  sh.z_loss = (float)number(z_loss);
-  sh.logit_scale = (float)number(logit_scale);
-  return sh;
-}
 // A given workspace, or one of the size that the call needs, made here.
 struct Workspace {
   at::Tensor made;
@@ -479,6 +390,117 @@ PyObject *two(PyObject *a, PyObject *b) {
   return res;
 }
 
+// Both attention calls. a: q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k; b: max_seqlen_q,
+// max_seqlen_k, bias_table, num_buckets, max_distance, bidirectional, alibi_slopes, then for
+// fat_paged_attn causal, for both softmax_scale, out, lse, workspace, stream. tree: positions, tree_mask.
+PyObject *attention(PyObject *const *a, PyObject *const *b, PyObject *const *tree) {
+  const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[3], "block_table");
+  check_rows(q, "q", 3, -1);
+  check_contiguous(q, "q");
+  const int dev = q.get_device();
+  const fat_paged_cache_t c = cache_of(a[1], a[2], dev);
+  const int64_t Tq = q.size(0), Hq = q.size(1);
+  if (q.size(2) != c.head_dim)
+    refuse(PyExc_ValueError, "%s and the cache have different head dimensions", "q");
+  check_rank(table, "block_table", 2);
+  const int64_t num = tensor(a[5], "seqlens_k").numel();
+  if (table.size(0) != num)
+    refuse(PyExc_ValueError, "%s must have a row for every request", "block_table");
+  const int32_t *pt = ints(a[3], "block_table", -1, dev);
+  const int32_t *pcu = ints(a[4], "cu_seqlens_q", num + 1, dev);
+  const int32_t *plk = ints(a[5], "seqlens_k", num, dev);
+  const int32_t *pos = nullptr, *mask = nullptr;
+  int32_t words = 0;
+  if (tree) {
+    pos = ints(tree[0], "positions", Tq, dev);
+    const at::Tensor &t = tensor(tree[1], "tree_mask");
+    check_rank(t, "tree_mask", 2);
+    if (t.size(0) != Tq) refuse(PyExc_ValueError, "%s must have a row for every query", "tree_mask");
+    mask = ints(tree[1], "tree_mask", -1, dev);
+    words = small(t.size(1), "tree_mask");
+  }
+  const int32_t nb = integer(b[3], "num_buckets"), md = integer(b[4], "max_distance");
+  const float *bias = b[2] == Py_None ? nullptr : floats(b[2], "bias_table", {nb, Hq}, dev);
+  const float *slopes = b[6] == Py_None ? nullptr : floats(b[6], "alibi_slopes", {Hq}, dev);
+  const int bidir = truth(b[5]) ? 1 : 0, causal = tree ? 0 : truth(b[7]) ? 1 : 0;
+  PyObject *const *r = b + (tree ? 7 : 8);
+  const float scale = (float)number(r[0]);
+  const OnStream on(r[4], dev);
+  const fat_paged_shape_t sh = attn_shape(q, num, table.size(1), b[0], b[1], on.stream);
+  const Result out(r[1], "out", q.sizes(), at::kBFloat16, dev);
+  const Result lse(r[2], "lse", {Hq, Tq}, at::kFloat, dev);
+  const Workspace ws(r[3], dev, [&] { return p_attn_ws(&sh, &c); });
+  const int rc = call_on(dev, [&] {
+    if (tree)
+      return p_tree_attn(&sh, &c, q.data_ptr(), pt, pcu, plk, pos, mask, words, bias, nb, md, bidir,
+                         slopes, scale, ws.ptr, ws.bytes, out.ptr, static_cast<float *>(lse.ptr));
+    return p_attn(&sh, &c, q.data_ptr(), pt, pcu, plk, bias, nb, md, bidir, slopes, causal, scale,
+                  ws.ptr, ws.bytes, out.ptr, static_cast<float *>(lse.ptr));
+  });
+  if (rc) return PyLong_FromLong(rc);
+  return two(out.object(), lse.object());
+}
+
+ENTRY(attn, 19)
+  return attention(a, a + 6, nullptr);
+ENTRY_END
+
+// q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, positions, tree_mask, max_seqlen_q, ...
+ENTRY(tree_attn, 20)
+  return attention(a, a + 8, a + 6);
+ENTRY_END
+
+// parents, cu_seqlens_q, seqlens_k, max_seqlen_q, positions, tree_mask, stream
+ENTRY(tree_plan, 7)
+  const at::Tensor &par = tensor(a[0], "parents");
+  check(par, "parents", at::kInt, -1);
+  const int dev = par.get_device();
+  const int64_t T = par.numel(), num = tensor(a[2], "seqlens_k").numel();
+  const int32_t *pp = ints(a[0], "parents", -1, dev);
+  const int32_t *pcu = ints(a[1], "cu_seqlens_q", num + 1, dev);
+  const int32_t *plk = ints(a[2], "seqlens_k", num, dev);
+  const int32_t most = integer(a[3], "max_seqlen_q");
+  int64_t words = most < 0 ? 0 : (most + 31ll) / 32;
+  if (a[5] != Py_None) {
+    const at::Tensor &t = tensor(a[5], "tree_mask");
+    check_rank(t, "tree_mask", 2);
+    words = t.size(1);
+  }
+  const OnStream on(a[6], dev);
+  const Result pos(a[4], "positions", {T}, at::kInt, dev);
+  const Result mask(a[5], "tree_mask", {T, words}, at::kInt, dev);
+  fat_tree_shape_t sh{};
+  sh.total_q = small(T, "parents");
+  sh.num_seqs = small(num, "seqlens_k");
+  sh.max_seqlen_q = most;
+  sh.mask_words = small(words, "tree_mask");
+  sh.stream = on.stream;
+  const int rc = call_on(dev, [&] {
+    return p_tree_plan(&sh, pp, pcu, plk, static_cast<int32_t *>(pos.ptr),
+                       static_cast<int32_t *>(mask.ptr));
+  });
+  if (rc) return PyLong_FromLong(rc);
+  return two(pos.object(), mask.object());
+ENTRY_END
+
+// ---- output layer and loss
+fat_linear_ce_shape_t head_shape(const at::Tensor &h, const at::Tensor &w, PyObject *z_loss,
+                                 PyObject *logit_scale) {
+  check_rows(h, "hidden", 2, -1);
+  check_rows(w, "weight", 2, h.get_device());
+  if (w.size(1) != h.size(1))
+    refuse(PyExc_ValueError, "%s and hidden have different row lengths", "weight");
+  fat_linear_ce_shape_t sh{};
+  sh.rows = small(h.size(0), "hidden");
+  sh.vocab = small(w.size(0), "weight");
+  sh.dim = small(h.size(1), "hidden");
+  // a stride over one row says nothing
+  sh.hidden_stride = h.size(0) > 1 ? h.stride(0) : h.size(1);
+  sh.weight_stride = w.size(0) > 1 ? w.stride(0) : w.size(1);
+  sh.z_loss = (float)number(z_loss);
+  sh.logit_scale = (float)number(logit_scale);
+  return sh;
+}
 // rows, vocab, dim, backward
 ENTRY(lce_workspace, 4)
   fat_linear_ce_shape_t sh{};
@@ -550,6 +572,8 @@ ENTRY(bind, 2)
   BIND(p_append, "fat_paged_append");
   BIND(p_attn, "fat_paged_attn");
   BIND(p_attn_ws, "fat_paged_attn_workspace_size");
+  BIND(p_tree_plan, "fat_paged_tree_plan");
+  BIND(p_tree_attn, "fat_paged_tree_attn");
   BIND(p_lce_fwd, "fat_linear_cross_entropy_fwd");
   BIND(p_lce_bwd, "fat_linear_cross_entropy_bwd");
   BIND(p_lce_ws, "fat_linear_cross_entropy_workspace_size");
@@ -561,7 +585,8 @@ ENTRY_END
 #define METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(plan),           METHOD(rope), METHOD(append),
                          METHOD(attn_workspace), METHOD(attn), METHOD(lce_workspace),
-                         METHOD(lce_fwd),        METHOD(lce_bwd), METHOD(bind),
+                         METHOD(lce_fwd),        METHOD(lce_bwd), METHOD(tree_plan),
+                         METHOD(tree_attn),      METHOD(bind),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -65,7 +65,8 @@ extern "C" {
 /* bits of the device error word */
 #define FAT_DEVERR_TIMEOUT_FWD 1 /* a forward pipeline wait exceeded its time limit */
 #define FAT_DEVERR_TIMEOUT_BWD 2 /* a backward pipeline wait exceeded its time limit */
-#define FAT_DEVERR_INDEX 8       /* a target at or beyond the vocabulary, a slot beyond the cache */
+#define FAT_DEVERR_INDEX 8       /* a target beyond the vocabulary, a slot beyond the cache, a tree's bad
+                                    parent or position */
 #define FAT_DEVERR_SEQLENS 4     /* cu_seqlens had an entry outside [0, total_tokens] or out of
                                     order, or a document longer than max_seqlen (its rows beyond
                                     the grid were not computed) */
@@ -531,6 +532,52 @@ int fat_paged_attn(const fat_paged_shape_t *shape, const fat_paged_cache_t *cach
                    int max_distance, int bidirectional, const float *alibi_slopes, int causal,
                    float softmax_scale, void *workspace, size_t workspace_bytes, void *out,
                    float *lse);
+
+/*
+ * Trees of drafted tokens over a paged cache (verification of a tree in one step). Request i's new tokens are
+ * the nodes of a tree (or of several): their keys and values are appended behind the cached context in
+ * the nodes' order (fat_paged_plan's slots), but a node sees, besides the context, only its own path.
+ *
+ * fat_paged_tree_plan: parents [total_q], of each node the index, within its request, of the node that it
+ * follows (an earlier one), or -1 where it follows the context. Results, of all total_q rows:
+ *   positions [total_q]: seqlens_k - nodes + depth, what the node's rotary angles and biases go by;
+ *   tree_mask [total_q, mask_words]: bit b of word w is node 32 w + b of the same request, set for the node
+ *     itself and its ancestors.
+ * Rows behind cu_seqlens_q[num_seqs], and of requests of more than max_seqlen_q nodes or whose seqlens_k is
+ * smaller than their nodes (FAT_DEVERR_SEQLENS), get 0 and no bits; a parent that is no earlier node counts as
+ * -1 (FAT_DEVERR_INDEX); with a corrupt cu_seqlens_q (FAT_DEVERR_SEQLENS) the rows concerned are left as they
+ * were. mask_words at least ceil(max_seqlen_q / 32); max_seqlen_q at most 4096 (FAT_EUNSUPPORTED). The
+ * results lie over no other array of the call.
+ */
+typedef struct {
+  int32_t total_q;      /* rows of parents, positions and tree_mask */
+  int32_t num_seqs;
+  int32_t max_seqlen_q; /* bound on the requests' node counts */
+  int32_t mask_words;
+  void *stream;
+} fat_tree_shape_t;
+int fat_paged_tree_plan(const fat_tree_shape_t *shape, const int32_t *parents,
+                        const int32_t *cu_seqlens_q, const int32_t *seqlens_k, int32_t *positions,
+                        int32_t *tree_mask);
+
+/*
+ * fat_paged_attn for such trees: query j of a request sees the keys before the request's first query's
+ * (index below seqlens_k - queries), and of its own queries' keys those whose bit is set in row j of
+ * tree_mask (any pattern, not only paths; bits at or beyond the query count are not read as keys). A row that
+ * sees nothing has out 0, lse -infinity. The bias's delta is key position - positions[j]; a key of the
+ * context lies at its index, that of query k at positions[k]. A position outside [seqlens_k - queries,
+ * seqlens_k) sets FAT_DEVERR_INDEX and is taken as the nearest end. All else, the workspace's size
+ * too, as fat_paged_attn without its causal mask; a request with fewer keys than queries sets
+ * FAT_DEVERR_SEQLENS and is left out. Keys and values that a node does not see are finite as well: they
+ * enter its product with weight 0.
+ */
+int fat_paged_tree_attn(const fat_paged_shape_t *shape, const fat_paged_cache_t *cache, const void *q,
+                        const int32_t *block_table, const int32_t *cu_seqlens_q,
+                        const int32_t *seqlens_k, const int32_t *positions,
+                        const int32_t *tree_mask, int mask_words, const float *bias_table,
+                        int num_buckets, int max_distance, int bidirectional,
+                        const float *alibi_slopes, float softmax_scale, void *workspace,
+                        size_t workspace_bytes, void *out, float *lse);
 
 /* Synchronises `stream`, reads the current GPU's device error word, clears it, and returns
    FAT_OK if it was zero, else FAT_EDEVICE with the word's bits stored in *bits (if not NULL). */

@@ -111,3 +111,63 @@ def attention(q, k_cache, v_cache, block_table, cu_q, lk, **kw):
     if kw.get("slopes") is not None and len(lk):
         b += float(np.abs(kw["slopes"]).max()) * (int(max(lk)) + int(np.diff(cu_q).max()))
     return out, lse, a, x, b
+
+
+def tree_plan(parents, cu_q, lk, total, max_nodes, words):
+    """(positions [total], mask [total, words]) of trees of drafted tokens, node by node; bad parents count
+    as -1, requests of more than max_nodes nodes or fewer keys than nodes get zeros."""
+    pos, mask = np.zeros(total, np.int64), np.zeros((total, words), np.uint32)
+    for i in range(len(lk)):
+        sq, m = int(cu_q[i]), int(cu_q[i + 1] - cu_q[i])
+        if m > max_nodes or lk[i] < m:
+            continue
+        paths = []
+        for j in range(m):
+            p = int(parents[sq + j])
+            paths.append((paths[p] if 0 <= p < j else []) + [j])
+            pos[sq + j] = int(lk[i]) - m + len(paths[j]) - 1
+            for a in paths[j]:
+                mask[sq + j, a // 32] |= np.uint32(1 << (a % 32))
+    return pos, mask.view(np.int32)
+
+
+def tree_attention(q, k_cache, v_cache, block_table, cu_q, lk, positions, mask, bias=None, bucket=None,
+                   slopes=None, scale=1.0):
+    """(out, lse, A, S, B) as of `attention`, for queries that see the context before their request's first
+    one and the own keys of their mask bits. bucket(deltas): bucket of each key position - query position."""
+    k, v = (gather(c, block_table, lk, k_cache.shape[0]) for c in (k_cache, v_cache))
+    total, hq = int(cu_q[-1]), q.shape[1]
+    group = hq // k.shape[1]
+    out, lse = np.zeros((total, hq, q.shape[2])), np.full((hq, total), -np.inf)
+    a, s, big, at = np.zeros_like(out), 0.0, 0.0, 0
+    words = np.asarray(mask).view(np.uint32)
+    for i in range(len(lk)):
+        sq, m, n = int(cu_q[i]), int(cu_q[i + 1] - cu_q[i]), int(lk[i])
+        ki, vi = k[at:at + n], v[at:at + n]
+        at += n
+        if m == 0 or n < m:
+            continue
+        c = n - m
+        own = np.array([[(int(words[sq + j, b // 32]) >> (b % 32)) & 1 for b in range(m)]
+                        for j in range(m)], bool)
+        see = np.concatenate([np.ones((m, c), bool), own], 1)
+        where = np.clip(np.asarray(positions[sq:sq + m], np.int64), c, n - 1)
+        delta = np.concatenate([np.arange(c), where])[None] - where[:, None]
+        for h in range(hq):
+            qh, kh, vh = q[sq:sq + m, h], ki[:, h // group], vi[:, h // group]
+            x, b = scale * (qh @ kh.T), np.zeros(delta.shape)
+            s = max(s, abs(scale) * float((np.abs(qh) @ np.abs(kh).T).max()))
+            if bias is not None:
+                b = b + bias[bucket(delta), h]
+            if slopes is not None:
+                b = b - slopes[h] * np.abs(delta)
+            big = max(big, float(np.abs(b).max()))
+            x = np.where(see, x + b, -np.inf)
+            top = x.max(1)
+            some = np.isfinite(top)
+            p = np.exp(x[some] - top[some, None])
+            lse[h, sq:sq + m][some] = top[some] + np.log(p.sum(1))
+            p /= p.sum(1, keepdims=True)
+            out[sq:sq + m, h][some] = p @ vh
+            a[sq:sq + m, h][some] = p @ np.abs(vh)
+    return out, lse, a, s, big
