@@ -49,6 +49,7 @@ struct PagedDoc {
   int sq, lq, lk;
   bool ok;
 };
+template <bool TREE>
 __device__ __forceinline__ PagedDoc paged_doc(const PagedParams &p, int i) {
   PagedDoc d;
   d.sq = __ldg(p.cu + i);
@@ -56,7 +57,7 @@ __device__ __forceinline__ PagedDoc paged_doc(const PagedParams &p, int i) {
   d.lk = __ldg(p.lk + i);
   d.ok = d.sq >= 0 && eq >= d.sq && eq <= p.total_q && eq - d.sq <= p.max_q && d.lk >= 0 &&
          d.lk <= p.max_k && d.lk <= ((long long)p.width << p.log2_page) &&
-         (p.pos == nullptr || d.lk >= eq - d.sq);
+         (!TREE || d.lk >= eq - d.sq);
   d.lq = eq - d.sq;
   return d;
 }
@@ -241,19 +242,19 @@ __device__ __forceinline__ long long share_scan(long long v, ShareSmem<NT> &s, l
 // is the number of CTAs that share the line), report corrupt requests once, stage the requests the
 // stretch may hold. Up to NT requests, one per thread, are read once; more are read again to find
 // the stretch's first.
-template <int NT, typename CostFn, typename OtherFn, typename CtasFn>
+template <int NT, bool TREE, typename CostFn, typename OtherFn, typename CtasFn>
 __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share, const CostFn &cost,
                                             const OtherFn &other, CtasFn ctas, ShareSmem<NT> &s) {
   const int tid = threadIdx.x;
   const bool small = p.n <= NT;
   Share r;
   PagedDoc d{0, 0, 0, false};
-  if (tid < p.n) d = paged_doc(p, tid);
+  if (tid < p.n) d = paged_doc<TREE>(p, tid);
   long long first, total, before, other_total = 0;
   if (p.both) {
     long long mine = d.ok && d.lq > 0 ? other(d) : 0;
     for (int i = tid + NT; i < p.n; i += NT) {
-      const PagedDoc e = paged_doc(p, i);
+      const PagedDoc e = paged_doc<TREE>(p, i);
       if (e.ok && e.lq > 0) mine += other(e);
     }
     share_scan<NT>(mine, s, &other_total);
@@ -262,7 +263,7 @@ __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share,
   {
     long long mine = first;
     for (int i = tid + NT; i < p.n; i += NT) {
-      const PagedDoc e = paged_doc(p, i);
+      const PagedDoc e = paged_doc<TREE>(p, i);
       if (!e.ok && blockIdx.x == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
       if (e.ok && e.lq > 0) mine += cost(e);
     }
@@ -294,7 +295,7 @@ __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share,
     for (int i0 = 0;; i0 += NT) {  // the stretch begins in one of the requests: this ends
       long long c = 0, chunk;
       if (i0 + tid < p.n) {
-        const PagedDoc e = paged_doc(p, i0 + tid);
+        const PagedDoc e = paged_doc<TREE>(p, i0 + tid);
         c = e.ok && e.lq > 0 ? cost(e) : 0;
       }
       before = share_scan<NT>(c, s, &chunk);
@@ -308,7 +309,7 @@ __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share,
     __syncthreads();
     for (int i = tid; i < kShareDocs; i += NT) {
       PagedDoc e{0, 0, 0, false};
-      if (s.doc + i < p.n) e = paged_doc(p, s.doc + i);
+      if (s.doc + i < p.n) e = paged_doc<TREE>(p, s.doc + i);
       s.sq[i] = e.sq;
       s.lq[i] = e.ok ? e.lq : 0;
       s.lk[i] = e.lk;
@@ -320,12 +321,12 @@ __device__ __forceinline__ Share share_find(const PagedParams &p, int min_share,
   return r;
 }
 
-template <int NT>
+template <bool TREE, int NT>
 __device__ __forceinline__ PagedDoc share_doc(const PagedParams &p, const ShareSmem<NT> &s,
                                               int first_doc, int doc) {
   const int i = doc - first_doc;
   if (i < kShareDocs) return PagedDoc{s.sq[i], s.lq[i], s.lk[i], s.lq[i] > 0};
-  PagedDoc d = paged_doc(p, doc);
+  PagedDoc d = paged_doc<TREE>(p, doc);
   d.ok = d.ok && d.lq > 0;
   return d;
 }
@@ -345,5 +346,9 @@ int paged_tile_ctas();
 constexpr int kWholeStages = 24, kWholeKeys = 1024;
 int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
 int launch_paged_tile(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
+// Trees: rows of an item of the kernel that takes requests of up to 128 rows, when none has more than
+// `rows` (0: the tile kernel's).
+int paged_mid_rows(long long rows);
+int launch_paged_mid(const PagedParams &p, const fat_paged_cache_t &c, int rows, cudaStream_t stream);
 
 }  // namespace fat

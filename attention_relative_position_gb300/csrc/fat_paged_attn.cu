@@ -151,6 +151,24 @@ int launch_merge(const PagedParams &p, float *tile_part, int tile_ctas, float *f
                           kMergeWarps * 32, 0, stream, p, tile_part, tile_ctas, few_part, few_ctas);
 }
 
+// The same for the tree kernel's items alone.
+template <int ROWS, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32, 4)
+    fat_paged_tree_merge_kernel(const __grid_constant__ PagedParams p) {
+  __shared__ float sum_s[kMergeWarps][kMergeCh + 2][32];
+  constexpr int kBlocks = ROWS / 32;
+  grid_dep_launch();
+  grid_dep_wait();
+  merge_chain<ROWS, D>(p, p.part, p.sms, blockIdx.x / kBlocks, blockIdx.x % kBlocks, kBlocks, sum_s);
+}
+template <int D>
+int launch_tree_merge(const PagedParams &p, int rows, cudaStream_t stream) {
+  const auto kernel =
+      rows == 64 ? fat_paged_tree_merge_kernel<64, D> : fat_paged_tree_merge_kernel<128, D>;
+  return launch_dependent("paged tree merge launch", kernel, dim3((unsigned)(p.sms * (rows / 32))),
+                          kMergeWarps * 32, 0, stream, p);
+}
+
 // The kernels a call launches and their partial rows' places in the workspace. Bounds that allow
 // few rows only need one kernel. A total of num_seqs * max_seqlen_q rows says that the requests most
 // likely have max_seqlen_q queries each: then the tile kernel alone takes every request, whatever its
@@ -280,8 +298,14 @@ int attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, const void
   const int d = cache->head_dim;
   const cudaStream_t s = static_cast<cudaStream_t>(sh->stream);
   p.split = plan.split;
-  PagedParams pf = p;
   p.part = static_cast<float *>(workspace);
+  const int rows = paged_mid_rows((long long)sh->max_seqlen_q * group);
+  if (tree && plan.tile && rows) {
+    rc = launch_paged_mid(p, *cache, rows, s);
+    if (rc || !plan.split) return rc;
+    return d == 64 ? launch_tree_merge<64>(p, rows, s) : launch_tree_merge<128>(p, rows, s);
+  }
+  PagedParams pf = p;
   pf.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.few_off);
   if (plan.tile) {
     rc = launch_paged_tile(p, *cache, s);

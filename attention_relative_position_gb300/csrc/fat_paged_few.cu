@@ -82,7 +82,7 @@ struct FewItem {
   int s0, s1;                    // the stages taken here
   bool begins, ends;
 };
-template <int D>
+template <int D, bool TREE>
 struct FewWalk {
   const PagedParams &p;
   const ShareSmem<kThreads> &sm;
@@ -91,7 +91,7 @@ struct FewWalk {
   int off;         // cost of the current item that lies before the stretch
   __device__ bool next(FewItem &it) {
     while (left > 0 && doc < p.n) {
-      const PagedDoc d = share_doc(p, sm, first_doc, doc);
+      const PagedDoc d = share_doc<TREE>(p, sm, first_doc, doc);
       if (!d.ok || (long long)d.lq * p.group > p.few_rows) {
         ++doc;
         hk = 0;
@@ -134,14 +134,14 @@ struct FewWalk {
 
 // The stages of one warp, in order: of a short item all (items take turns over the warps), of a
 // longer one every kWarps-th, continuing the turn of the item before.
-template <int D>
+template <int D, bool TREE>
 struct FewStages {
-  FewWalk<D> walk;
+  FewWalk<D, TREE> walk;
   FewItem it;
   int s, step;   // next stage of `it` and the distance to the one after
   int turn;      // stages dealt so far, modulo kWarps
   int shorts;    // short items so far
-  __device__ explicit FewStages(const FewWalk<D> &w) : walk(w), s(0), step(1), turn(0), shorts(0) {}
+  __device__ explicit FewStages(const FewWalk<D, TREE> &w) : walk(w), s(0), step(1), turn(0), shorts(0) {}
   // The next item with its first stage for `warp` (s >= it.s1: none of its stages).
   __device__ bool item(int warp) {
     if (!walk.next(it)) return false;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     r->valid = 0;
   }
   const FewCost<D> cost{p};
-  const Share sh = share_find<kThreads>(
+  const Share sh = share_find<kThreads, TREE>(
       p, kMinShare, cost, TileCost{p, 128 / p.group, 2 * (128 / p.group)},
       [&](long long mine, long long other) {
         return 2 * (p.sms - (p.both ? tile_sms<D>(p, other, mine) : 0));
@@ -203,10 +203,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
   const Watchdog wd{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
-  const PagedDoc d0 = share_doc(p, share_s, sh.doc, sh.doc);
+  const PagedDoc d0 = share_doc<TREE>(p, share_s, sh.doc, sh.doc);
   const int cost0 = few_item_cost((d0.lk + KT - 1) / KT);
   const int hk0 = (int)div_small(sh.off, cost0);
-  const FewWalk<D> start{p, share_s, sh.doc, sh.doc, hk0, sh.hi - sh.lo,
+  const FewWalk<D, TREE> start{p, share_s, sh.doc, sh.doc, hk0, sh.hi - sh.lo,
                          (int)(sh.off - (long long)hk0 * cost0)};
 
   if (warp >= kWarps) {
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int log2_box = min(p.log2_page, C::LOG2_KT);  // rows of a copy
     const uint64_t once = l2_evict_first();  // a request's keys and values are read once
     const int in_mask = (1 << p.log2_page) - 1;
-    FewStages<D> ahead(start);
+    FewStages<D, TREE> ahead(start);
     int slot = 0, phase = 1;
     bool ok = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
     while (ok && ahead.item(w)) {
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t *full = bars + warp * kRing, *empty = bars + (kWarps + warp) * kRing;
 
   // ---- computation
-  FewStages<D> cur(start);
+  FewStages<D, TREE> cur(start);
   const int G = p.group;
   const int r0 = lane >> 2, r1 = r0 + 8;  // this thread's rows, keys 2 (lane % 4) + {0, 1} + 8 t
   const bool t5 = p.bias.table != nullptr;

@@ -1,0 +1,724 @@
+// fat_paged_mid.cu -- attention of trees of drafted tokens over a paged cache: calls whose requests have up
+// to 128 rows (queries x group heads) per key/value head, and more than the few-row kernel takes.
+//
+// As in the few-row kernel the work is one read of the requests' keys and values; 64 or 128 rows make it
+// enough for the tensor cores. The rows are the narrow side of both products, so that a step costs what
+// its rows need and the softmax keeps every lane busy:
+//   S^T = K Q^T (128 keys x R rows), P = 2^(S - reference), O^T += V^T P^T (channels x R rows).
+// Two warpgroups of softmax threads share a tile's rows, half of them each. A thread holds one key's logits
+// against its group's rows (a TMEM lane); what it subtracts per row, the reference, is a shared number. A
+// row's reference is its maximum over the first tile taken, and is raised (O and the sums scaled) only when
+// a weight would exceed 2^32: a group's 128 threads vote once a tile, and a maximum over the keys, across
+// lanes, is formed only then. A thread sums its own key's weights in a register per row (unrounded, fp32);
+// the threads' sums are added at an item's end. Key tiles go from the last one backwards, from the
+// request's own tokens and the largest linear bias on. P is rounded to bf16, as in the tile kernel.
+// One persistent CTA per SM takes an equal share of all key tiles (fat_paged.cuh):
+//   warps 0-7  softmax, epilogue, zeros over the values behind the last key;
+//   warp 8     producer: Q of an item (64 rows: two buffers), key and value tiles of 128 tokens in one ring of
+//              slots, in the order of their use (K0 K1 V0 K2 V1 ..), a lane per page;
+//   warp 9     issues the products; the next tile's S runs beside this tile's softmax.
+#include <algorithm>
+#include <cstdint>
+
+#include "fat_paged.cuh"
+
+namespace fat {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kSoftWarps = 8, kWarpProd = 8, kWarpMma = 9;
+constexpr int kMinShare = 2;  // key tiles a CTA takes at least
+constexpr int kItemCost = 2;  // cost of an item beside its key tiles
+constexpr float kNoRow = 3e38f;     // reference of a row without a token: its weights are 0
+constexpr float kFreshRow = -1e30f; // of a row that has seen no key
+
+template <int D, int R>
+struct MidCfg {
+  static constexpr int DB = D / 64;
+  static constexpr int BLK = 128 * 128;          // 128 keys x 64 channels
+  static constexpr int TILE = DB * BLK;          // K or V of a tile
+  static constexpr int NS = D == 64 ? 8 : R == 64 ? 5 : 4;  // slots
+  static constexpr int QB = R == 64 ? 2 : 1;     // buffers of Q
+  static constexpr int QBLK = R * 128, QTILE = DB * QBLK;
+  static constexpr int PBLK = 128 * 128;         // 128 keys x 64 rows
+  static constexpr int OFF_Q = NS * TILE;
+  static constexpr int OFF_P = OFF_Q + QB * QTILE;
+  static constexpr int RW = R / 2;               // rows of a softmax warpgroup
+  static constexpr int PB = D == 64 ? 2 : 1;     // buffers of P
+  static constexpr int PTILE = R / 64 * PBLK;
+  static constexpr int OFF_ROW = OFF_P + PB * PTILE + 1024;  // behind the staged rows
+  // per row: slope; bias of a far key at the first query's position less the reference; minus the reference;
+  // the reference; sum or factor; int2: position - shift, head; float [4 warps]: maxima
+  static constexpr int OFF_SLOPE = OFF_ROW, OFF_FAR = OFF_SLOPE + R * 4, OFF_NREF = OFF_FAR + R * 4;
+  static constexpr int OFF_REF = OFF_NREF + R * 4, OFF_FAC = OFF_REF + R * 4, OFF_FARB = OFF_FAC + R * 4;
+  static constexpr int OFF_INT = OFF_FARB + R * 4, OFF_MAX = OFF_INT + R * 8;
+  static constexpr int OFF_BAR = OFF_MAX + 4 * R * 4;
+  static constexpr int OFF_THR = OFF_BAR + 320;
+  static constexpr int OFF_SHARE = OFF_THR + kMaxThresholds * 4;
+  static constexpr int OFF_LUT = (OFF_SHARE + (int)sizeof(ShareSmem<kThreads>) + 15) & ~15;
+  static int bytes(const BiasParams &b) {
+    return OFF_LUT + (b.table ? (b.sat_neg + b.sat_pos + 1 + 15) & ~15 : 0);
+  }
+  static_assert((2 * QB + 2 * NS + 10) * 8 + 8 <= 320, "barrier block");
+  static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
+  static constexpr int LD = 132;  // floats of a staged row of the epilogue (16 a warpgroup, in P's place)
+  static_assert(2 * 16 * LD * 4 <= PTILE + 1024, "staged rows");
+  static constexpr uint32_t COL_O = 2 * R, TMEM_COLS = 4 * R;
+  static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, R, 0, 0);
+  static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, R, 1, 1);
+};
+
+// Blocks of a request's tokens (rows / group each at most) and the tokens of one.
+__device__ __forceinline__ int mid_blocks(int lq, int rows, int group, int *per) {
+  const int most = rows / group, n = (lq + most - 1) / most;
+  *per = (lq + n - 1) / n;
+  return n;
+}
+template <int R>
+struct MidCost {
+  const PagedParams &p;
+  __device__ long long operator()(const PagedDoc &d) const {
+    int per;
+    return (long long)p.hkv * mid_blocks(d.lq, R, p.group, &per) * (((d.lk + 127) >> 7) + kItemCost);
+  }
+};
+struct NoCost {
+  __device__ long long operator()(const PagedDoc &) const { return 0; }
+};
+
+struct MidItem {
+  int doc, hk, row0, ntok, tok0;  // row0: first token of q and out; tok0: the request's first
+  int lk, shift, nkv, j0, j1;     // key tile nkv - 1 - j for j in [j0, j1)
+  bool begins, ends;
+};
+template <int R>
+struct MidWalk {
+  const PagedParams &p;
+  const ShareSmem<kThreads> &sm;
+  int first_doc, doc, hk, b;
+  long long left;  // cost still to take
+  int off;         // cost of the current item that lies before the stretch
+  __device__ MidWalk(const PagedParams &pp, const ShareSmem<kThreads> &s, const Share &sh)
+      : p(pp), sm(s), first_doc(sh.doc), doc(sh.doc), left(sh.hi - sh.lo) {
+    const PagedDoc d = share_doc<true>(p, sm, doc, doc);
+    int per;
+    const int n = mid_blocks(d.lq, R, p.group, &per), cost = ((d.lk + 127) >> 7) + kItemCost;
+    const int item = (int)div_small(sh.off, cost);
+    hk = item / n;
+    b = item - hk * n;
+    off = (int)(sh.off - (long long)item * cost);
+  }
+  __device__ bool next(MidItem &it) {
+    while (left > 0 && doc < p.n) {
+      const PagedDoc d = share_doc<true>(p, sm, first_doc, doc);
+      if (!d.ok) {
+        ++doc;
+        hk = b = 0;
+        continue;
+      }
+      int per;
+      const int n = mid_blocks(d.lq, R, p.group, &per);
+      it.nkv = (d.lk + 127) >> 7;
+      const int cost = it.nkv + kItemCost, o = off;
+      off = 0;
+      const int take = (int)min(left, (long long)(cost - o));
+      left -= take;
+      it.doc = doc;
+      it.hk = hk;
+      it.tok0 = d.sq;
+      it.row0 = d.sq + b * per;
+      it.ntok = min(per, d.lq - b * per);
+      it.lk = d.lk;
+      it.shift = d.lk - d.lq;
+      if (++b == n) {
+        b = 0;
+        if (++hk == p.hkv) {
+          hk = 0;
+          ++doc;
+        }
+      }
+      if (!p.split) {  // whole items: the one that begins earlier is another CTA's
+        if (o > 0) continue;
+        it.j0 = 0;
+        it.j1 = it.nkv;
+        it.begins = it.ends = true;
+        return true;
+      }
+      // the fixed part of the cost comes first, before the key tiles
+      it.j0 = max(o - kItemCost, 0);
+      it.j1 = max(o + take - kItemCost, 0);
+      it.begins = it.j0 == 0;
+      it.ends = o + take == cost;
+      if (it.j0 == it.j1) continue;  // a boundary before its tiles (a request has a key at least)
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ bool bar_any(int id, bool v) {  // of a softmax warpgroup
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
+// bit j of lane i's word -> bit i of lane j's
+__device__ __forceinline__ uint32_t transpose32(uint32_t x, int lane) {
+  uint32_t m = 0x0000ffffu;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, s);
+    x = (lane & s) ? (x & ~m) | ((y & ~m) >> s) : (x & m) | ((y & m) << s);
+    m ^= m << (s >> 1);
+  }
+  return x;
+}
+__device__ __forceinline__ float warp_max_f32(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    fat_paged_mid_kernel(const __grid_constant__ CUtensorMap tm_q,
+                         const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ PagedParams p) {
+  using C = MidCfg<D, R>;
+  constexpr int NS = C::NS, QB = C::QB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto &share_s = *reinterpret_cast<ShareSmem<kThreads> *>(sm + C::OFF_SHARE);
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);  // [QB] each
+  uint64_t *q_empty = q_full + QB;
+  uint64_t *full = q_empty + QB;  // [NS] each
+  uint64_t *empty = full + NS;
+  uint64_t *s_full = empty + NS;  // [2] each
+  uint64_t *s_free = s_full + 2;
+  uint64_t *p_ready = s_free + 2;  // [2]
+  uint64_t *o_ready = p_ready + 2;  // [2]: a tile's last products are complete: P is free, O is up to date
+  uint64_t *o_free = o_ready + 2;
+  uint64_t *done = o_free + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  int *thr_s = reinterpret_cast<int *>(sm + C::OFF_THR);
+  uint8_t *lut = sm + C::OFF_LUT;
+  const int G = p.group, tq = R / G, RT = tq * G;  // tokens and rows of a block
+  grid_dep_launch();
+  if (tid == 0) {
+    for (int i = 0; i < QB; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_free + i, kSoftWarps);
+      mbar_init(p_ready + i, kSoftWarps);
+      mbar_init(o_ready + i, 1);
+    }
+    mbar_init(o_free, kSoftWarps);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  for (int i = tid; i < p.bias.n_thr; i += kThreads) thr_s[i] = p.bias.thr[i];
+  // rows of the Q buffers that no token fills (group does not divide R): zeros, never overwritten
+  for (int i = tid; i < QB * C::DB * (R - RT) * 8; i += kThreads) {
+    const int blk = i / ((R - RT) * 8), rest = i % ((R - RT) * 8);
+    *reinterpret_cast<uint4 *>(sm + C::OFF_Q + blk * C::QBLK + RT * 128 + rest * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  grid_dep_wait();
+  if (p.split && tid < 2) part_record(p.part, blockIdx.x, tid)->valid = 0;
+  const Share sh = share_find<kThreads, true>(p, kMinShare, MidCost<R>{p}, NoCost{},
+                                              [&](long long, long long) { return p.sms; }, share_s);
+  if (p.bias.table != nullptr)  // (behind share_find's barriers)
+    for (int i = tid; i <= p.bias.sat_neg + p.bias.sat_pos; i += kThreads)
+      lut[i] = (uint8_t)t5_bucket_staged(i - p.bias.sat_neg, p.bias, thr_s);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Watchdog wd{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
+  const bool work = sh.lo < sh.hi;
+  if (work) {
+    MidWalk<R> walk(p, share_s, sh);
+    MidItem it;
+    auto slot_full = [&](uint32_t u) { return mbar_wait(full + u % NS, (u / NS) & 1, wd); };
+    if (warp == kWarpProd) {
+      // ------------------------------------------------------------------ producer
+      const int kbox = min(128, 1 << p.log2_page), pieces = 128 / kbox;
+      const int in_mask = (1 << p.log2_page) - 1;
+      uint32_t u = 0;
+      int ni = 0;
+      bool ok = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
+      while (ok && walk.next(it)) {
+        const int n = it.j1 - it.j0, qb = ni % QB;
+        if (ni >= QB && !(ok = warp_wait(q_empty + qb, (ni / QB - 1) & 1, wd))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full + qb, (uint32_t)RT * 128 * C::DB);
+          for (int b = 0; b < C::DB; ++b)
+            tma_load_3d(&tm_q, q_full + qb, sm + C::OFF_Q + qb * C::QTILE + b * C::QBLK, 64 * b, it.hk * G,
+                        it.row0);
+        }
+        ++ni;
+        if (p.bias.table != nullptr)
+          for (int b = lane; b < p.bias.nb; b += 32)
+            prefetch_l1(p.bias.table + (size_t)b * p.hq + it.hk * G);
+        const int32_t *row = p.table + (size_t)it.doc * p.width;
+        auto fetch = [&](int j) -> int {  // this lane's page of the j-th tile
+          const int tok = (it.nkv - 1 - it.j0 - j) * 128 + lane * kbox;
+          return j < n && lane < pieces && tok < it.lk ? __ldg(row + (tok >> p.log2_page)) : 0;
+        };
+        auto copy = [&](const CUtensorMap *map, int j, int page) {
+          const uint32_t s = u % NS;
+          if (u >= NS && !(ok = warp_wait(empty + s, (u / NS - 1) & 1, wd))) return;
+          const int kt = it.nkv - 1 - it.j0 - j, tok = kt * 128 + lane * kbox;
+          const int nvalid = min(pieces, (it.lk - kt * 128 + kbox - 1) / kbox);
+          if (lane == 0) mbar_arrive_expect_tx(full + s, (uint32_t)nvalid * kbox * 128 * C::DB);
+          __syncwarp();
+          if (lane < nvalid) {
+            if ((unsigned)page >= (unsigned)p.num_pages) {
+              atomicOr(p.err, FAT_DEVERR_PAGES);
+              page = p.num_pages;  // just outside: filled with zeros
+            }
+            const int in = tok & in_mask;
+            const int c1 = p.head_outer ? in : it.hk, c2 = p.head_outer ? it.hk : in;
+            for (int b = 0; b < C::DB; ++b)
+              tma_load_4d(map, full + s, sm + s * C::TILE + b * C::BLK + lane * kbox * 128, 64 * b, c1, c2,
+                          page);
+          }
+          ++u;
+        };
+        int page = fetch(0), next = fetch(1);
+        copy(&tm_k, 0, page);
+        for (int j = 0; ok && j < n; ++j) {
+          const int after = fetch(j + 2);
+          if (j + 1 < n) copy(&tm_k, j + 1, next);
+          if (ok) copy(&tm_v, j, page);
+          page = next;
+          next = after;
+        }
+      }
+      if (*abort_flag) {  // copies may still be on their way: give them time to land
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+      }
+    } else if (warp == kWarpMma) {
+      // ------------------------------------------------------------------ products
+      if (lane == 0) {
+        uint32_t u = 0, g = 0;
+        int ni = 0;
+        bool ok = true;
+        while (ok && walk.next(it)) {
+          const int n = it.j1 - it.j0, qb = ni % QB;
+          const uint64_t dQ = sw128_desc(smem_u32(sm + C::OFF_Q + qb * C::QTILE), 16, 1024);
+          auto issue_S = [&](int j) {  // tile j of the item, from slot u
+            const uint32_t gs = g + j, buf = gs & 1;
+            if (!(ok = slot_full(u))) return;
+            if (gs >= 2 && !(ok = mbar_wait(s_free + buf, (gs / 2 - 1) & 1, wd))) return;
+            tc_fence_after();
+            const uint64_t dK = sw128_desc(smem_u32(sm + (u % NS) * C::TILE), 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ss(tmem + R * buf, dK + (((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4),
+                          dQ + (((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4), C::IDESC_S, kk > 0);
+            mma_commit(s_full + buf);
+            mma_commit(empty + u % NS);
+            if (j == n - 1) mma_commit(q_empty + qb);
+            ++u;
+          };
+          if (!(ok = mbar_wait(q_full + qb, (ni / QB) & 1, wd))) break;
+          issue_S(0);
+          for (int j = 0; ok && j < n; ++j) {
+            if (j + 1 < n) issue_S(j + 1);
+            if (!ok || !(ok = slot_full(u) && mbar_wait(p_ready + ((g + j) & 1), ((g + j) / 2) & 1, wd))) break;
+            // the first product overwrites O: the previous item's rows have been read
+            if (j == 0 && ni > 0 && !(ok = mbar_wait(o_free, (ni - 1) & 1, wd))) break;
+            tc_fence_after();
+            const uint64_t dP =
+                sw128_desc(smem_u32(sm + C::OFF_P + ((g + j) % C::PB) * C::PTILE), C::PBLK, 1024);
+            // head_dim 64: the channels twice (the second block of 64 is the first again)
+            const uint64_t dV = sw128_desc(smem_u32(sm + (u % NS) * C::TILE), D == 128 ? C::BLK : 0, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ss(tmem + C::COL_O, dV + ((kk * 2048) >> 4), dP + ((kk * 2048) >> 4), C::IDESC_PV,
+                          j > 0 || kk > 0);
+            mma_commit(empty + u % NS);
+            mma_commit(o_ready + ((g + j) & 1));
+            ++u;
+          }
+          g += n;
+          ++ni;
+        }
+        mma_commit(done);
+        mbar_wait_teardown(done, 0, kTeardownNs);
+      }
+    } else {
+      // ------------------------------------------------------------------ softmax: thread = key
+      constexpr int RW = C::RW;
+      const int wg = warp >> 2, t = tid & 127, rb = wg * RW, bar = 1 + wg;
+      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+      // per-row numbers of this group's rows
+      float *slope_s = reinterpret_cast<float *>(sm + C::OFF_SLOPE) + rb;
+      float *far_s = reinterpret_cast<float *>(sm + C::OFF_FAR) + rb;
+      float *nref_s = reinterpret_cast<float *>(sm + C::OFF_NREF) + rb;
+      float *ref_s = reinterpret_cast<float *>(sm + C::OFF_REF) + rb;
+      float *fac_s = reinterpret_cast<float *>(sm + C::OFF_FAC) + rb;
+      float *farb_s = reinterpret_cast<float *>(sm + C::OFF_FARB) + rb;
+      int2 *int_s = reinterpret_cast<int2 *>(sm + C::OFF_INT) + rb;
+      float *max_s = reinterpret_cast<float *>(sm + C::OFF_MAX) + 4 * rb;  // [warps][RW]
+      const bool t5 = p.bias.table != nullptr, biased = p.bias.has_bias != 0;
+      const bool slopes = p.bias.slopes != nullptr;
+      const int span = p.bias.sat_neg + p.bias.sat_pos;
+      auto set_ref = [&](float r) {  // of row rb + t
+        ref_s[t] = r;
+        nref_s[t] = -r;
+        far_s[t] = farb_s[t] - r;
+      };
+      auto o_wait = [&](uint32_t i) { return warp_wait(o_ready + (i & 1), (i / 2) & 1, wd); };
+      uint32_t u = 0, g = 0;
+      bool ok = true;
+      while (ok && walk.next(it)) {
+        const int n = it.j1 - it.j0, rows = it.ntok * G;
+        const int mine = min(rows - rb, RW);  // rows of this group (none: it only keeps step)
+        if (t < RW && mine > 0) {
+          const int r = rb + min(t, mine - 1), q = r / G, h = it.hk * G + (r - q * G);
+          const int row = it.row0 + q, pos = tree_pos(p, row, it.shift, it.lk);
+          if (__ldg(p.pos + row) != pos) atomicOr(p.err, FAT_DEVERR_INDEX);
+          prefetch_l1(p.mask + (size_t)row * p.mask_words);
+          const float slope = slopes ? __ldg(p.bias.slopes + h) * kLog2e : 0.f;
+          const float far = t5 ? __ldg(p.bias.table + (size_t)lut[0] * p.hq + h) * kLog2e : 0.f;
+          slope_s[t] = slope;
+          farb_s[t] = far - slope * (float)(pos - it.shift);
+          int_s[t] = make_int2(pos - it.shift, h);
+          set_ref(t < mine ? kFreshRow : kNoRow);
+        }
+        uint64_t sum[RW / 2];  // of this thread's weights, rows 2 i and 2 i + 1
+#pragma unroll
+        for (int i = 0; i < RW / 2; ++i) sum[i] = 0;
+        named_bar_sync(bar, 128);
+        for (int j = 0; j < n; ++j) {
+          const uint32_t gt = g + j, buf = gt & 1;
+          const uint32_t tS = tmem + lane_off + R * buf + rb;
+          const int k0 = (it.nkv - 1 - it.j0 - j) * 128, key = k0 + t;
+          if (!(ok = warp_wait(s_full + buf, (gt / 2) & 1, wd))) break;
+          tc_fence_after();
+          if (mine > 0) {
+            float scale = p.scale_log2;
+            const bool edge = k0 + 128 > it.shift - (biased ? p.bias.sat_neg : 0);
+            const bool linear = slopes && !edge;
+            const float *cst_s = edge ? nref_s : far_s;
+            if (edge) {
+              // Own keys, or cached ones near them: logits where they stand, masked by the rows' bits. A
+              // thread's key is the same for all rows, and so is its position.
+              const int key0 = k0 + (warp & 3) * 32;
+              const int kp = key < it.shift ? key - it.shift
+                                            : tree_pos(p, it.tok0 + min(key, it.lk - 1) - it.shift, it.shift,
+                                                       it.lk) - it.shift;
+#pragma unroll 1
+              for (int c = 0; c < mine; c += 32) {
+                const int q = (rb + min(c + lane, mine - 1)) / G;
+                const uint32_t see = transpose32(
+                    tree_bits(p, p.mask + (size_t)(it.row0 + q) * p.mask_words, key0 - it.shift,
+                              it.lk - key0), lane);
+                uint32_t x[32];
+                tmem_ld32(tS + c, x);
+                if (!biased) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    x[i] = (see >> i) & 1u ? __float_as_uint(__uint_as_float(x[i]) * scale) : 0xff800000u;
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    const int2 rc = int_s[c + i];
+                    const int delta = kp - rc.x;
+                    float b = -slope_s[c + i] * fabsf((float)delta);
+                    if (t5) {
+                      const int bk = lut[min(max(delta + p.bias.sat_neg, 0), span)];
+                      b = fmaf(__ldg(p.bias.table + bk * p.hq + rc.y), kLog2e, b);
+                    }
+                    x[i] = (see >> i) & 1u ? __float_as_uint(fmaf(__uint_as_float(x[i]), scale, b))
+                                           : 0xff800000u;
+                  }
+                }
+                tmem_st32(tS + c, x);
+              }
+              tmem_st_wait();
+              scale = 1.f;
+            }
+            const float delta0 = (float)(key - it.shift);
+            // logits of 32 rows less their references
+            auto logits = [&](int c, float (&y)[32]) {
+              uint32_t x[32];
+              tmem_ld32(tS + c, x);
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float4 m = *reinterpret_cast<const float4 *>(cst_s + c + i);
+                if (linear) {
+                  const float4 k = *reinterpret_cast<const float4 *>(slope_s + c + i);
+                  m.x = fmaf(k.x, delta0, m.x);
+                  m.y = fmaf(k.y, delta0, m.y);
+                  m.z = fmaf(k.z, delta0, m.z);
+                  m.w = fmaf(k.w, delta0, m.w);
+                }
+                y[i] = fmaf(__uint_as_float(x[i]), scale, m.x);
+                y[i + 1] = fmaf(__uint_as_float(x[i + 1]), scale, m.y);
+                y[i + 2] = fmaf(__uint_as_float(x[i + 2]), scale, m.z);
+                y[i + 3] = fmaf(__uint_as_float(x[i + 3]), scale, m.w);
+              }
+            };
+            bool raise = j == 0;
+            if (!raise) {
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < mine; c += 32) {
+                float y[32];
+                logits(c, y);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) top = fmax3(top, y[i], y[i + 1]);
+              }
+              raise = bar_any(bar, top > 32.f);
+            }
+            if (raise) {
+              // The rows' maxima over the tile, and new references where they passed 2^32. A row that has seen
+              // no key has a reference of -1e30, which loses the logit: its maximum is taken anew, from 0.
+              bool fresh = false;
+              if (t < RW) {
+                fresh = ref_s[t] == kFreshRow;
+                if (fresh) set_ref(0.f);
+              }
+              named_bar_sync(bar, 128);
+#pragma unroll 1
+              for (int c = 0; c < mine; c += 32) {
+                float y[32], best = -INFINITY;
+                logits(c, y);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float m = warp_max_f32(y[i]);
+                  if (lane == i) best = m;
+                }
+                max_s[(warp & 3) * RW + c + lane] = best;
+              }
+              named_bar_sync(bar, 128);
+              if (t < RW) {
+                const float mx = fmaxf(fmaxf(max_s[t], max_s[RW + t]), fmaxf(max_s[2 * RW + t], max_s[3 * RW + t]));
+                float f = 1.f;
+                if (t < mine) {
+                  if (fresh) {
+                    if (!(mx != mx)) set_ref(mx > -1e30f ? mx : kFreshRow);  // (a NaN shows in the sum)
+                  } else if (mx > 32.f) {
+                    f = ex2(-mx);
+                    set_ref(ref_s[t] + mx);
+                  }
+                }
+                fac_s[t] = f;
+              }
+              named_bar_sync(bar, 128);
+              if (j > 0) {  // what was summed so far
+                if (!(ok = o_wait(gt - 1))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < mine; c += 8) {
+                  uint32_t a[8];
+                  const uint32_t tO = tmem + lane_off + C::COL_O + rb + c;
+                  tmem_ld8(tO, a);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) a[i] = __float_as_uint(__uint_as_float(a[i]) * fac_s[c + i]);
+                  tmem_st8(tO, a);
+                }
+                tmem_st_wait();
+#pragma unroll
+                for (int i = 0; i < RW / 2; ++i)
+                  sum[i] = f2_mul(sum[i], f2_pack(fac_s[2 * i], fac_s[2 * i + 1]));
+              }
+            }
+            // P, once the products that read its place are complete
+            if (gt >= C::PB && !(ok = o_wait(gt - C::PB))) break;
+            const uint32_t sP = smem_u32(sm + C::OFF_P + (gt % C::PB) * C::PTILE);
+#pragma unroll
+            for (int c = 0; c < RW; c += 32) {
+              if (c > 0 && c >= mine) break;
+              float y[32];
+              logits(c, y);
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float a = ex2(y[2 * i]), b = ex2(y[2 * i + 1]);
+                sum[c / 2 + i] = f2_add(sum[c / 2 + i], f2_pack(a, b));
+                w[i] = pack_bf16x2(a, b);
+              }
+              const int r = rb + c;
+              const uint32_t at = sP + (r >> 6) * C::PBLK + t * 128;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                st_shared_v4(at + (((((r & 63) >> 3) + i) ^ (t & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2],
+                             w[4 * i + 3]);
+            }
+          } else if (gt >= C::PB) {  // a group without rows keeps step: its arrivals count for this tile
+            if (!(ok = o_wait(gt - C::PB))) break;
+          }
+          tc_fence_before();
+          // values behind the last key: whatever the page holds, they are 0
+          if (wg == 0 && k0 + 128 > it.lk) {
+            const uint32_t v = u + (n == 1 ? 1 : 2);  // (the item's first tile)
+            if (!(ok = __all_sync(0xffffffffu, slot_full(v)))) break;
+            if (key >= it.lk)
+#pragma unroll
+              for (int c = 0; c < 8 * C::DB; ++c)
+                *reinterpret_cast<uint4 *>(sm + (v % NS) * C::TILE + (c >> 3) * C::BLK + t * 128 +
+                                           (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(s_free + buf);
+            mbar_arrive(p_ready + (gt & 1));
+          }
+        }
+        if (!ok) break;
+        g += n;
+        u += 2 * n;
+        // ---- the item's rows
+        if (!(ok = o_wait(g - 1))) break;
+        tc_fence_after();
+        const bool whole = it.begins && it.ends;
+        const int which = it.begins ? 1 : 0;
+        if (!whole && tid == 0) {
+          PartRecord *rec = part_record(p.part, blockIdx.x, which);
+          rec->valid = 1;
+          rec->ends = it.ends;
+          rec->row0 = it.row0;
+          rec->hk = it.hk;
+          rec->rows = rows;
+        }
+        constexpr int LD = C::LD;
+        float *stage = reinterpret_cast<float *>(sm + C::OFF_P) + wg * 16 * LD;  // [16][LD]: P has been used
+        if (mine > 0) {
+#pragma unroll
+          for (int c = 0; c < RW; c += 16) {  // the threads' sums of 16 rows
+            if (c >= mine) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              f2_unpack(sum[c / 2 + i], stage[2 * i * LD + t], stage[(2 * i + 1) * LD + t]);
+            named_bar_sync(bar, 128);
+            float l = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 v = *reinterpret_cast<const float4 *>(stage + (t >> 3) * LD + (t & 7) * 4 + 32 * i);
+              l += (v.x + v.y) + (v.z + v.w);
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if ((t & 7) == 0) fac_s[c + (t >> 3)] = l;
+            named_bar_sync(bar, 128);
+          }
+#pragma unroll 1
+          for (int c = 0; c < mine; c += 16) {  // and the rows
+            uint32_t x[16];
+            tmem_ld16(tmem + lane_off + C::COL_O + rb + c, x);
+            if (t < D)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) stage[i * LD + t] = __uint_as_float(x[i]);
+            named_bar_sync(bar, 128);
+            const int left = min(16, mine - c);
+            if (whole) {
+              for (int i = t; i < left * (D / 8); i += 128) {
+                const int rr = i / (D / 8), ch = (i % (D / 8)) * 8, h = int_s[c + rr].y;
+                const float l = fac_s[c + rr], inv = l == 0.f ? 0.f : 1.0f / l;
+                const float4 a = *reinterpret_cast<const float4 *>(stage + rr * LD + ch);
+                const float4 b = *reinterpret_cast<const float4 *>(stage + rr * LD + ch + 4);
+                const size_t row = (size_t)it.row0 + (rb + c + rr) / G;
+                *reinterpret_cast<uint4 *>(p.out + (row * p.hq + h) * D + ch) =
+                    make_uint4(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv),
+                               pack_bf16x2(b.x * inv, b.y * inv), pack_bf16x2(b.z * inv, b.w * inv));
+                if (ch == 0 && p.lse != nullptr)
+                  p.lse[(size_t)h * p.total_q + row] =
+                      l == 0.f ? -INFINITY : (ref_s[c + rr] + __log2f(l)) * kLn2;
+              }
+            } else {
+              float *po = part_rows<R, D>(p.part, gridDim.x, blockIdx.x, which);
+              float *ps = part_stats<R, D>(p.part, gridDim.x, blockIdx.x, which);
+              for (int i = t; i < 16 * (D / 4); i += 128) {
+                const int rr = i & 15, c4 = i >> 4;
+                if (rr < left)
+                  *part_quad<R>(po, rb + c + rr, c4) =
+                      *reinterpret_cast<const float4 *>(stage + rr * LD + 4 * c4);
+              }
+              if (t < left) {
+                const float l = fac_s[c + t];
+                *reinterpret_cast<float2 *>(ps + (rb + c + t) * 2) =
+                    make_float2(l == 0.f ? -INFINITY : ref_s[c + t], l);
+              }
+            }
+            named_bar_sync(bar, 128);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int D, int R>
+int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream) {
+  using C = MidCfg<D, R>;
+  PagedParams pp = p;
+  CUtensorMap mq, mk, mv;
+  const int kbox = std::min(128, 1 << pp.log2_page);
+  int rc = make_tmap_pages(&mk, c.k, c, kbox, &pp.head_outer);
+  if (!rc) rc = make_tmap_pages(&mv, c.v, c, kbox, &pp.head_outer);
+  if (rc) return rc;
+  if (make_tmap_rows(&mq, p.q, p.total_q, p.hq, D, p.group, R / p.group)) return FAT_ECUDA;
+  const size_t smem = C::bytes(p.bias) + 1024;
+  const auto kernel = fat_paged_mid_kernel<D, R>;
+  if (prepare_kernel((const void *)kernel, smem, kThreads, 0)) return FAT_ECUDA;
+  return launch_dependent("paged tree kernel launch", kernel, dim3((unsigned)paged_tile_ctas()),
+                          kThreads, smem, stream, mq, mk, mv, pp);
+}
+
+}  // namespace
+
+int paged_mid_rows(long long rows) { return rows <= 64 ? 64 : rows <= 128 ? 128 : 0; }
+
+int launch_paged_mid(const PagedParams &p, const fat_paged_cache_t &c, int rows, cudaStream_t stream) {
+  if (c.head_dim == 64) return rows == 64 ? launch_t<64, 64>(p, c, stream) : launch_t<64, 128>(p, c, stream);
+  return rows == 64 ? launch_t<128, 64>(p, c, stream) : launch_t<128, 128>(p, c, stream);
+}
+
+}  // namespace fat

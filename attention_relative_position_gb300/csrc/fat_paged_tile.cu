@@ -92,6 +92,7 @@ struct TileCfg {
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
 };
 
+template <bool TREE>
 struct TileWalk {
   const PagedParams &p;
   const ShareSmem<kThreads> &sm;
@@ -102,7 +103,7 @@ struct TileWalk {
                       const Share &sh)
       : p(pp), sm(s), tq(c.tq), blk(c.blk), first_doc(sh.doc), doc(sh.doc), b(0),
         left(sh.hi - sh.lo) {
-    const PagedDoc d = share_doc(p, sm, doc, doc);
+    const PagedDoc d = share_doc<TREE>(p, sm, doc, doc);
     const long long per = tile_head_cost(d, tq, blk, p.causal);
     hk = (int)div_small(sh.off, per);
     long long rest = sh.off - hk * per;
@@ -111,7 +112,7 @@ struct TileWalk {
   }
   __device__ bool next(TileItem &it) {
     while (left > 0 && doc < p.n) {
-      const PagedDoc d = share_doc(p, sm, first_doc, doc);
+      const PagedDoc d = share_doc<TREE>(p, sm, first_doc, doc);
       if (!d.ok || (long long)d.lq * p.group <= p.few_rows) {
         ++doc;
         hk = b = 0;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.split && tid < 2) part_record(p.part, blockIdx.x, tid)->valid = 0;
   for (int i = tid; i < p.bias.n_thr; i += kThreads) thr_s[i] = p.bias.thr[i];
   const TileCost cost{p, tq, 2 * tq};
-  const Share share = share_find<kThreads>(
+  const Share share = share_find<kThreads, TREE>(
       p, kMinShare, cost, FewCost<D>{p},
       [&](long long mine, long long other) { return tile_sms<D>(p, mine, other); }, share_s);
   if (share.lo >= share.hi) return;
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpProd) {
     // ------------------------------------------------------------------ producer
     const int kbox = min(128, 1 << p.log2_page), pieces = 128 / kbox;
-    TileWalk walk(p, share_s, cost, share);
+    TileWalk<TREE> walk(p, share_s, cost, share);
     TileItem it;
     uint32_t J = 0;      // K/V stream position
     int ni = 0;          // items with keys

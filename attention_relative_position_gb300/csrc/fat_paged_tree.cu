@@ -5,10 +5,10 @@
 //   depth_j = 0 where the parent is -1 (the node follows the cached context), else depth_parent + 1;
 //   path_j = {j} and the parent's path; position_j = seqlens_k - nodes + depth_j.
 //
-// A block per request: its parents in shared memory, a thread per node that walks up to the root. Parents
-// come before their children, so the path's bits are met from the highest word of the row to the lowest,
-// one word in a register at a time. Tens of kilobytes: bound by the launch and by the longest path (a
-// step of the walk is one read of shared memory).
+// A warp per request, 32 nodes at a time, a lane each. Within such a group the paths are closed by doubling
+// (five rounds: a lane's bits take in those of the lane at the end of its path so far, and the path gets twice
+// as long); what lies before the group is the row of the node that the path enters it from, written earlier by
+// the same warp. Kilobytes to a megabyte: bound by the launch and by a group's chain of shuffles and loads.
 #include <algorithm>
 #include <cstdint>
 
@@ -19,7 +19,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxNodes = 4096;
-constexpr int kPadBlocks = 4;  // blocks that clear the rows behind the last request
 
 struct TreeParams {
   int total, n, max_nodes, words;
@@ -30,58 +29,70 @@ struct TreeParams {
 };
 
 __global__ void __launch_bounds__(kThreads) fat_paged_tree_plan_kernel(const TreeParams p) {
-  extern __shared__ int16_t up[];  // [max_nodes]
+  __shared__ int16_t depth_s[kThreads / 32][kMaxNodes];
   grid_dep_launch();
   grid_dep_wait();
-  const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= p.n) {  // rows behind the last request
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gtid = blockIdx.x * kThreads + threadIdx.x, gthreads = gridDim.x * kThreads;
+  {  // rows behind the last request
     const int end = __ldg(p.cu + p.n);
-    if (end < 0 || end > p.total) return;
-    const int b = blockIdx.x - p.n;
-    for (long long r = end + (long long)b * kThreads + tid; r < p.total; r += kPadBlocks * kThreads)
-      p.pos[r] = 0;
-    const long long last = (long long)p.total * p.words;
-    for (long long i = (long long)end * p.words + b * kThreads + tid; i < last;
-         i += kPadBlocks * kThreads)
-      p.mask[i] = 0u;
-    return;
+    if (end >= 0) {
+      for (long long r = end + (long long)gtid; r < p.total; r += gthreads) p.pos[r] = 0;
+      for (long long i = (long long)end * p.words + gtid; i < (long long)p.total * p.words; i += gthreads)
+        p.mask[i] = 0u;
+    }
   }
-  const int sq = __ldg(p.cu + blockIdx.x), eq = __ldg(p.cu + blockIdx.x + 1);
-  const int lk = __ldg(p.lk + blockIdx.x), m = eq - sq;
+  const int i = blockIdx.x * (kThreads / 32) + warp;
+  if (i >= p.n) return;
+  const int sq = __ldg(p.cu + i), eq = __ldg(p.cu + i + 1), lk = __ldg(p.lk + i), m = eq - sq;
   if (sq < 0 || eq < sq || eq > p.total) {  // corrupt: no rows of its own
-    if (tid == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
+    if (lane == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
     return;
   }
-  const bool ok = m <= p.max_nodes && lk >= m;
-  if (!ok && tid == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
-  if (ok)
-    for (int j = tid; j < m; j += kThreads) {
-      int u = __ldg(p.parents + sq + j);
-      if (u < -1 || u >= j) {
-        atomicOr(p.err, FAT_DEVERR_INDEX);
-        u = -1;
-      }
-      up[j] = (int16_t)u;
+  uint32_t *rows = p.mask + (size_t)sq * p.words;
+  if (m > p.max_nodes || lk < m) {
+    if (lane == 0) atomicOr(p.err, FAT_DEVERR_SEQLENS);
+    for (int j = lane; j < m; j += 32) p.pos[sq + j] = 0;
+    for (long long j = lane; j < (long long)m * p.words; j += 32) rows[j] = 0u;
+    return;
+  }
+  int16_t *depth = depth_s[warp];
+  int next = lane < m ? __ldg(p.parents + sq + lane) : -1;
+  for (int j0 = 0; j0 < m; j0 += 32) {
+    const int j = j0 + lane;
+    int parent = next;
+    if (j + 32 < m) next = __ldg(p.parents + sq + j + 32);
+    if (j < m && (parent < -1 || parent >= j)) {
+      atomicOr(p.err, FAT_DEVERR_INDEX);
+      parent = -1;
     }
-  __syncthreads();
-  for (int j = tid; j < m; j += kThreads) {
-    uint32_t *row = p.mask + (size_t)(sq + j) * p.words;
-    int w = p.words - 1, depth = -1;
-    if (ok) {
-      for (; w > j >> 5; --w) row[w] = 0u;
-      uint32_t bits = 0;
-      for (int a = j; a >= 0; a = up[a]) {
-        for (; w > a >> 5; --w) {
-          row[w] = bits;
-          bits = 0;
-        }
-        bits |= 1u << (a & 31);
-        ++depth;
+    if (j >= m) parent = -1;
+    // bits: the part of the path within the group; up: where it goes on (a lane, or none)
+    uint32_t bits = 1u << lane;
+    int up = parent >= j0 ? parent - j0 : -1, enter = parent;  // enter: the node before the group, or -1
+#pragma unroll
+    for (int s = 0; s < 5; ++s) {
+      const int from = up < 0 ? lane : up;
+      const uint32_t b = __shfl_sync(0xffffffffu, bits, from);
+      const int u = __shfl_sync(0xffffffffu, up, from), e = __shfl_sync(0xffffffffu, enter, from);
+      if (up >= 0) {
+        bits |= b;
+        enter = e;
+        up = u;
       }
-      row[w--] = bits;
     }
-    for (; w >= 0; --w) row[w] = 0u;
-    p.pos[sq + j] = ok ? lk - m + depth : 0;
+    if (j < m) {
+      uint32_t *row = rows + (size_t)j * p.words;
+      const uint32_t *before = rows + (size_t)max(enter, 0) * p.words;
+      const int g = j0 >> 5;
+      for (int w = 0; w < g; ++w) row[w] = enter >= 0 ? before[w] : 0u;
+      row[g] = bits;
+      for (int w = g + 1; w < p.words; ++w) row[w] = 0u;
+      const int d = __popc(bits) + (enter >= 0 ? depth[enter] : 0);
+      depth[j] = (int16_t)d;
+      p.pos[sq + j] = lk - m + d - 1;
+    }
+    __syncwarp();  // the rows are read by the groups behind them
   }
 }
 
@@ -131,7 +142,10 @@ extern "C" int fat_paged_tree_plan(const fat_tree_shape_t *sh, const int32_t *pa
   p.lk = seqlens_k;
   p.pos = positions;
   p.mask = reinterpret_cast<uint32_t *>(tree_mask);
+  // a warp per request, and for the rows behind them at least as many threads as one in eight rows
+  const long long warps = std::max<long long>(sh->num_seqs, sh->total_q / 256);
+  const int blocks = (int)std::min<long long>((warps + kThreads / 32 - 1) / (kThreads / 32), 1 << 22);
   return launch_dependent("paged tree plan launch", fat_paged_tree_plan_kernel,
-                          dim3((unsigned)(sh->num_seqs + kPadBlocks)), kThreads,
-                          (size_t)sh->max_seqlen_q * 2, static_cast<cudaStream_t>(sh->stream), p);
+                          dim3((unsigned)std::max(blocks, 1)), kThreads, 0,
+                          static_cast<cudaStream_t>(sh->stream), p);
 }
