@@ -14,9 +14,9 @@
 // request's own tokens and the largest linear bias on. P is rounded to bf16, as in the tile kernel.
 // One persistent CTA per SM takes an equal share of all key tiles (fat_paged.cuh):
 //   warps 0-7  softmax, epilogue, zeros over the values behind the last key;
-//   warp 8     producer: Q of an item (64 rows: two buffers), key and value tiles of 128 tokens in one ring of
-//              slots, in the order of their use (K0 K1 V0 K2 V1 ..), a lane per page;
-//   warp 9     issues the products; the next tile's S runs beside this tile's softmax.
+//   warp 8     Q of an item (64 rows: two buffers) and its key tiles of 128 tokens, a lane per page;
+//   warp 9     issues the products; S of two tiles ahead runs beside this tile's softmax (three buffers);
+//   warp 10    value tiles (one warp for both put a copy off every 0.45 us).
 #include <algorithm>
 #include <cstdint>
 
@@ -25,8 +25,8 @@
 namespace fat {
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kSoftWarps = 8, kWarpProd = 8, kWarpMma = 9;
+constexpr int kThreads = 352;
+constexpr int kSoftWarps = 8, kWarpK = 8, kWarpMma = 9, kWarpV = 10;
 constexpr int kMinShare = 2;  // key tiles a CTA takes at least
 constexpr int kItemCost = 2;  // cost of an item beside its key tiles
 constexpr float kNoRow = 3e38f;     // reference of a row without a token: its weights are 0
@@ -37,14 +37,17 @@ struct MidCfg {
   static constexpr int DB = D / 64;
   static constexpr int BLK = 128 * 128;          // 128 keys x 64 channels
   static constexpr int TILE = DB * BLK;          // K or V of a tile
-  static constexpr int NS = D == 64 ? 8 : R == 64 ? 5 : 4;  // slots
+  // stages of K and of V: what is in flight bounds the rate of the copies
+  static constexpr int KS = D == 64 ? 5 : 2, VS = D == 64 ? (R == 64 ? 6 : 5) : R == 64 ? 3 : 2;
   static constexpr int QB = R == 64 ? 2 : 1;     // buffers of Q
   static constexpr int QBLK = R * 128, QTILE = DB * QBLK;
   static constexpr int PBLK = 128 * 128;         // 128 keys x 64 rows
-  static constexpr int OFF_Q = NS * TILE;
+  static constexpr int OFF_V = KS * TILE;
+  static constexpr int OFF_Q = OFF_V + VS * TILE;
   static constexpr int OFF_P = OFF_Q + QB * QTILE;
   static constexpr int RW = R / 2;               // rows of a softmax warpgroup
-  static constexpr int PB = D == 64 ? 2 : 1;     // buffers of P
+  static constexpr int PB = 1;                   // buffers of P
+  static constexpr int SB = 3;                   // and of S
   static constexpr int PTILE = R / 64 * PBLK;
   static constexpr int OFF_ROW = OFF_P + PB * PTILE + 1024;  // behind the staged rows
   // per row: slope; bias of a far key at the first query's position less the reference; minus the reference;
@@ -59,11 +62,11 @@ struct MidCfg {
   static int bytes(const BiasParams &b) {
     return OFF_LUT + (b.table ? (b.sat_neg + b.sat_pos + 1 + 15) & ~15 : 0);
   }
-  static_assert((2 * QB + 2 * NS + 10) * 8 + 8 <= 320, "barrier block");
+  static_assert((2 * QB + 2 * KS + 2 * VS + 2 * SB + 6) * 8 + 8 <= 320, "barrier block");
   static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
   static constexpr int LD = 132;  // floats of a staged row of the epilogue (16 a warpgroup, in P's place)
   static_assert(2 * 16 * LD * 4 <= PTILE + 1024, "staged rows");
-  static constexpr uint32_t COL_O = 2 * R, TMEM_COLS = 4 * R;
+  static constexpr uint32_t COL_O = SB * R, TMEM_COLS = 4 * R;
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, R, 0, 0);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, R, 1, 1);
 };
@@ -198,18 +201,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ PagedParams p) {
   using C = MidCfg<D, R>;
-  constexpr int NS = C::NS, QB = C::QB;
+  constexpr int KS = C::KS, VS = C::VS, QB = C::QB, SB = C::SB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto &share_s = *reinterpret_cast<ShareSmem<kThreads> *>(sm + C::OFF_SHARE);
   uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);  // [QB] each
   uint64_t *q_empty = q_full + QB;
-  uint64_t *full = q_empty + QB;  // [NS] each
-  uint64_t *empty = full + NS;
-  uint64_t *s_full = empty + NS;  // [2] each
-  uint64_t *s_free = s_full + 2;
-  uint64_t *p_ready = s_free + 2;  // [2]
+  uint64_t *k_full = q_empty + QB;  // [KS] each
+  uint64_t *k_empty = k_full + KS;
+  uint64_t *v_full = k_empty + KS;  // [VS] each
+  uint64_t *v_empty = v_full + VS;
+  uint64_t *s_full = v_empty + VS;  // [SB] each
+  uint64_t *s_free = s_full + SB;
+  uint64_t *p_ready = s_free + SB;  // [2]
   uint64_t *o_ready = p_ready + 2;  // [2]: a tile's last products are complete: P is free, O is up to date
   uint64_t *o_free = o_ready + 2;
   uint64_t *done = o_free + 1;
@@ -224,13 +229,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
     }
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * KS; ++i) mbar_init(k_full + i, 1);
+    for (int i = 0; i < 2 * VS; ++i) mbar_init(v_full + i, 1);
+    for (int i = 0; i < SB; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(s_free + i, kSoftWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(p_ready + i, kSoftWarps);
       mbar_init(o_ready + i, 1);
     }
@@ -270,38 +275,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (work) {
     MidWalk<R> walk(p, share_s, sh);
     MidItem it;
-    auto slot_full = [&](uint32_t u) { return mbar_wait(full + u % NS, (u / NS) & 1, wd); };
-    if (warp == kWarpProd) {
-      // ------------------------------------------------------------------ producer
+    if (warp == kWarpK || warp == kWarpV) {
+      // ------------------------------------------------------------------ producers
+      const bool keys = warp == kWarpK;
       const int kbox = min(128, 1 << p.log2_page), pieces = 128 / kbox;
       const int in_mask = (1 << p.log2_page) - 1;
-      uint32_t u = 0;
+      const uint32_t stages = keys ? KS : VS;
+      const CUtensorMap *map = keys ? &tm_k : &tm_v;
+      uint64_t *full = keys ? k_full : v_full, *empty = keys ? k_empty : v_empty;
+      uint8_t *ring = sm + (keys ? 0 : C::OFF_V);
+      const uint64_t once = l2_evict_first();  // a request's keys and values are read once
+      uint32_t slot = 0, phase = 1;
       int ni = 0;
       bool ok = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
       while (ok && walk.next(it)) {
         const int n = it.j1 - it.j0, qb = ni % QB;
-        if (ni >= QB && !(ok = warp_wait(q_empty + qb, (ni / QB - 1) & 1, wd))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full + qb, (uint32_t)RT * 128 * C::DB);
-          for (int b = 0; b < C::DB; ++b)
-            tma_load_3d(&tm_q, q_full + qb, sm + C::OFF_Q + qb * C::QTILE + b * C::QBLK, 64 * b, it.hk * G,
-                        it.row0);
-        }
-        ++ni;
-        if (p.bias.table != nullptr)
-          for (int b = lane; b < p.bias.nb; b += 32)
-            prefetch_l1(p.bias.table + (size_t)b * p.hq + it.hk * G);
         const int32_t *row = p.table + (size_t)it.doc * p.width;
         auto fetch = [&](int j) -> int {  // this lane's page of the j-th tile
           const int tok = (it.nkv - 1 - it.j0 - j) * 128 + lane * kbox;
           return j < n && lane < pieces && tok < it.lk ? __ldg(row + (tok >> p.log2_page)) : 0;
         };
-        auto copy = [&](const CUtensorMap *map, int j, int page) {
-          const uint32_t s = u % NS;
-          if (u >= NS && !(ok = warp_wait(empty + s, (u / NS - 1) & 1, wd))) return;
+        int page = fetch(0), next = fetch(1);
+        if (keys) {
+          if (ni >= QB && !(ok = warp_wait(q_empty + qb, (ni / QB - 1) & 1, wd))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(q_full + qb, (uint32_t)RT * 128 * C::DB);
+            for (int b = 0; b < C::DB; ++b)
+              tma_load_3d(&tm_q, q_full + qb, sm + C::OFF_Q + qb * C::QTILE + b * C::QBLK, 64 * b,
+                          it.hk * G, it.row0);
+          }
+        } else if (p.bias.table != nullptr) {
+          for (int b = lane; b < p.bias.nb; b += 32)
+            prefetch_l1(p.bias.table + (size_t)b * p.hq + it.hk * G);
+        }
+        ++ni;
+        for (int j = 0; j < n; ++j) {
+          const int after = fetch(j + 2);
+          if (!(ok = warp_wait(empty + slot, phase, wd))) break;
           const int kt = it.nkv - 1 - it.j0 - j, tok = kt * 128 + lane * kbox;
           const int nvalid = min(pieces, (it.lk - kt * 128 + kbox - 1) / kbox);
-          if (lane == 0) mbar_arrive_expect_tx(full + s, (uint32_t)nvalid * kbox * 128 * C::DB);
+          if (lane == 0) mbar_arrive_expect_tx(full + slot, (uint32_t)nvalid * kbox * 128 * C::DB);
           __syncwarp();
           if (lane < nvalid) {
             if ((unsigned)page >= (unsigned)p.num_pages) {
@@ -311,17 +324,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int in = tok & in_mask;
             const int c1 = p.head_outer ? in : it.hk, c2 = p.head_outer ? it.hk : in;
             for (int b = 0; b < C::DB; ++b)
-              tma_load_4d(map, full + s, sm + s * C::TILE + b * C::BLK + lane * kbox * 128, 64 * b, c1, c2,
-                          page);
+              tma_load_4d(map, full + slot, ring + slot * C::TILE + b * C::BLK + lane * kbox * 128, 64 * b, c1,
+                          c2, page, once);
           }
-          ++u;
-        };
-        int page = fetch(0), next = fetch(1);
-        copy(&tm_k, 0, page);
-        for (int j = 0; ok && j < n; ++j) {
-          const int after = fetch(j + 2);
-          if (j + 1 < n) copy(&tm_k, j + 1, next);
-          if (ok) copy(&tm_v, j, page);
+          if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+          }
           page = next;
           next = after;
         }
@@ -332,53 +341,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------------ products
-      if (lane == 0) {
-        uint32_t u = 0, g = 0;
+      // (the whole warp walks and waits, and an elected lane issues: a lane alone took 0.2 us more a tile)
+      {
+        uint32_t g = 0;
         int ni = 0;
         bool ok = true;
         while (ok && walk.next(it)) {
           const int n = it.j1 - it.j0, qb = ni % QB;
           const uint64_t dQ = sw128_desc(smem_u32(sm + C::OFF_Q + qb * C::QTILE), 16, 1024);
-          auto issue_S = [&](int j) {  // tile j of the item, from slot u
-            const uint32_t gs = g + j, buf = gs & 1;
-            if (!(ok = slot_full(u))) return;
-            if (gs >= 2 && !(ok = mbar_wait(s_free + buf, (gs / 2 - 1) & 1, wd))) return;
+          auto issue_S = [&](int j) {  // tile j of the item
+            const uint32_t gs = g + j, buf = gs % SB, s = gs % KS;
+            if (!(ok = warp_wait(k_full + s, (gs / KS) & 1, wd))) return;
+            if (gs >= SB && !(ok = warp_wait(s_free + buf, (gs / SB - 1) & 1, wd))) return;
             tc_fence_after();
-            const uint64_t dK = sw128_desc(smem_u32(sm + (u % NS) * C::TILE), 16, 1024);
+            const uint64_t dK = sw128_desc(smem_u32(sm + s * C::TILE), 16, 1024);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ss(tmem + R * buf, dK + (((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4),
+              mma_bf16_ss_e(tmem + R * buf, dK + (((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4),
                           dQ + (((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4), C::IDESC_S, kk > 0);
-            mma_commit(s_full + buf);
-            mma_commit(empty + u % NS);
-            if (j == n - 1) mma_commit(q_empty + qb);
-            ++u;
+            mma_commit_e(s_full + buf);
+            mma_commit_e(k_empty + s);
+            if (j == n - 1) mma_commit_e(q_empty + qb);
           };
-          if (!(ok = mbar_wait(q_full + qb, (ni / QB) & 1, wd))) break;
-          issue_S(0);
+          if (!(ok = warp_wait(q_full + qb, (ni / QB) & 1, wd))) break;
+          for (int j = 0; ok && j < min(n, SB - 1); ++j) issue_S(j);
           for (int j = 0; ok && j < n; ++j) {
-            if (j + 1 < n) issue_S(j + 1);
-            if (!ok || !(ok = slot_full(u) && mbar_wait(p_ready + ((g + j) & 1), ((g + j) / 2) & 1, wd))) break;
+            if (j + SB - 1 < n) issue_S(j + SB - 1);
+            const uint32_t s = (g + j) % VS;
+            const uint32_t gt = g + j;
+            if (!ok || !(ok = warp_wait(v_full + s, (gt / VS) & 1, wd) &&
+                              warp_wait(p_ready + (gt & 1), (gt / 2) & 1, wd)))
+              break;
             // the first product overwrites O: the previous item's rows have been read
-            if (j == 0 && ni > 0 && !(ok = mbar_wait(o_free, (ni - 1) & 1, wd))) break;
+            if (j == 0 && ni > 0 && !(ok = warp_wait(o_free, (ni - 1) & 1, wd))) break;
             tc_fence_after();
             const uint64_t dP =
                 sw128_desc(smem_u32(sm + C::OFF_P + ((g + j) % C::PB) * C::PTILE), C::PBLK, 1024);
             // head_dim 64: the channels twice (the second block of 64 is the first again)
-            const uint64_t dV = sw128_desc(smem_u32(sm + (u % NS) * C::TILE), D == 128 ? C::BLK : 0, 1024);
+            const uint64_t dV =
+                sw128_desc(smem_u32(sm + C::OFF_V + s * C::TILE), D == 128 ? C::BLK : 0, 1024);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ss(tmem + C::COL_O, dV + ((kk * 2048) >> 4), dP + ((kk * 2048) >> 4), C::IDESC_PV,
+              mma_bf16_ss_e(tmem + C::COL_O, dV + ((kk * 2048) >> 4), dP + ((kk * 2048) >> 4), C::IDESC_PV,
                           j > 0 || kk > 0);
-            mma_commit(empty + u % NS);
-            mma_commit(o_ready + ((g + j) & 1));
-            ++u;
+            mma_commit_e(v_empty + s);
+            mma_commit_e(o_ready + ((g + j) & 1));
           }
           g += n;
           ++ni;
         }
-        mma_commit(done);
-        mbar_wait_teardown(done, 0, kTeardownNs);
+        mma_commit_e(done);
+        if (lane == 0) mbar_wait_teardown(done, 0, kTeardownNs);
+        __syncwarp();
       }
     } else {
       // ------------------------------------------------------------------ softmax: thread = key
@@ -403,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         far_s[t] = farb_s[t] - r;
       };
       auto o_wait = [&](uint32_t i) { return warp_wait(o_ready + (i & 1), (i / 2) & 1, wd); };
-      uint32_t u = 0, g = 0;
+      uint32_t g = 0;
       bool ok = true;
       while (ok && walk.next(it)) {
         const int n = it.j1 - it.j0, rows = it.ntok * G;
@@ -425,10 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < RW / 2; ++i) sum[i] = 0;
         named_bar_sync(bar, 128);
         for (int j = 0; j < n; ++j) {
-          const uint32_t gt = g + j, buf = gt & 1;
+          const uint32_t gt = g + j, buf = gt % SB;
           const uint32_t tS = tmem + lane_off + R * buf + rb;
           const int k0 = (it.nkv - 1 - it.j0 - j) * 128, key = k0 + t;
-          if (!(ok = warp_wait(s_full + buf, (gt / 2) & 1, wd))) break;
+          if (!(ok = warp_wait(s_full + buf, (gt / SB) & 1, wd))) break;
           tc_fence_after();
           if (mine > 0) {
             float scale = p.scale_log2;
@@ -587,12 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           // values behind the last key: whatever the page holds, they are 0
           if (wg == 0 && k0 + 128 > it.lk) {
-            const uint32_t v = u + (n == 1 ? 1 : 2);  // (the item's first tile)
-            if (!(ok = __all_sync(0xffffffffu, slot_full(v)))) break;
+            const uint32_t v = gt % VS;
+            if (!(ok = warp_wait(v_full + v, (gt / VS) & 1, wd))) break;
             if (key >= it.lk)
 #pragma unroll
               for (int c = 0; c < 8 * C::DB; ++c)
-                *reinterpret_cast<uint4 *>(sm + (v % NS) * C::TILE + (c >> 3) * C::BLK + t * 128 +
+                *reinterpret_cast<uint4 *>(sm + C::OFF_V + v * C::TILE + (c >> 3) * C::BLK + t * 128 +
                                            (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
@@ -604,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         g += n;
-        u += 2 * n;
         // ---- the item's rows
         if (!(ok = o_wait(g - 1))) break;
         tc_fence_after();
