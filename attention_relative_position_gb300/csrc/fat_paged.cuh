@@ -346,9 +346,7 @@ int paged_tile_ctas();
 constexpr int kWholeStages = 24, kWholeKeys = 1024;
 int launch_paged_few(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
 int launch_paged_tile(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stream);
-// Trees: rows of an item of the kernel that takes requests of up to 128 rows, when none has more than
-// `rows` (0: the tile kernel's).
-int paged_mid_rows(long long rows);
+// Trees: items of `rows` (64 or 128) rows.
 int launch_paged_mid(const PagedParams &p, const fat_paged_cache_t &c, int rows, cudaStream_t stream);
 
 }  // namespace fat

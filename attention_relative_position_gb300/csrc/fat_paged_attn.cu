@@ -211,6 +211,22 @@ size_t workspace_bound(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) 
   return bytes;
 }
 
+// Trees of more than 16 rows: rows of the items of the tree kernel, 0 where the tile kernel does better. That is
+// for more than 128 rows a request (the tree kernel reads keys again for every 128, the tile kernel for every
+// 256), where every request has as many (else the few-row kernel's launch and its share of the SMs come on
+// top) and 128-row items would fill the SMs. Tree kernel against tile kernel, 32 heads over 8 of 128, us:
+//   16 trees of 24 to 61 tokens over 1500 to 6000 keys 90 / 127, of 61 110 / 96, of 33 over 4000 101 / 92;
+//   1 of 60 over 8000 40 / 67, 4 of 48 over 4000 42 / 46; up to 128 rows: 64 of 32 (16 heads over 4) over 4000
+//   115 / 169, 64 of 12 over 1000 to 4000 69 / 127.
+int tree_rows(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
+  const int group = sh->num_heads_q / c->num_heads;
+  const long long rows = (long long)sh->max_seqlen_q * group;
+  if (rows <= 64) return 64;
+  if (rows <= 128 || (long long)sh->num_seqs * sh->max_seqlen_q != sh->total_q) return 128;
+  const long long blocks = (sh->max_seqlen_q + 128 / group - 1) / (128 / group);
+  return sh->num_seqs * c->num_heads * blocks <= paged_tile_ctas() ? 128 : 0;
+}
+
 int check_shape(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
   if (!sh || !c) return FAT_EINVAL_NULL;
   if (sh->total_q < 0 || sh->num_seqs < 0 || sh->max_seqlen_q < 0 || sh->max_seqlen_k < 0 ||
@@ -299,8 +315,8 @@ int attn(const fat_paged_shape_t *sh, const fat_paged_cache_t *cache, const void
   const cudaStream_t s = static_cast<cudaStream_t>(sh->stream);
   p.split = plan.split;
   p.part = static_cast<float *>(workspace);
-  const int rows = paged_mid_rows((long long)sh->max_seqlen_q * group);
-  if (tree && plan.tile && rows) {
+  const int rows = tree && plan.tile ? tree_rows(sh, cache) : 0;
+  if (rows) {
     rc = launch_paged_mid(p, *cache, rows, s);
     if (rc || !plan.split) return rc;
     return d == 64 ? launch_tree_merge<64>(p, rows, s) : launch_tree_merge<128>(p, rows, s);

@@ -1,5 +1,5 @@
-// fat_paged_mid.cu -- attention of trees of drafted tokens over a paged cache: calls whose requests have up
-// to 128 rows (queries x group heads) per key/value head, and more than the few-row kernel takes.
+// fat_paged_mid.cu -- attention of trees of drafted tokens over a paged cache: more rows (queries x group heads
+// per key/value head) than the few-row kernel takes, in items of 64 or 128.
 //
 // As in the few-row kernel the work is one read of the requests' keys and values; 64 or 128 rows make it
 // enough for the tensor cores. The rows are the narrow side of both products, so that a step costs what
@@ -7,12 +7,13 @@
 //   S^T = K Q^T (128 keys x R rows), P = 2^(S - reference), O^T += V^T P^T (channels x R rows).
 // Two warpgroups of softmax threads share a tile's rows, half of them each. A thread holds one key's logits
 // against its group's rows (a TMEM lane); what it subtracts per row, the reference, is a shared number. A
-// row's reference is its maximum over the first tile taken, and is raised (O and the sums scaled) only when
-// a weight would exceed 2^32: a group's 128 threads vote once a tile, and a maximum over the keys, across
-// lanes, is formed only then. A thread sums its own key's weights in a register per row (unrounded, fp32);
+// row's reference is the largest of eight logits of the first tile taken, and is raised to the maximum (O and
+// the sums scaled) when a weight would exceed 2^32: a group's 128 threads vote once a tile, and a maximum
+// over the keys, across lanes, is formed only then. A thread sums its own key's weights in a register per row (unrounded, fp32);
 // the threads' sums are added at an item's end. Key tiles go from the last one backwards, from the
 // request's own tokens and the largest linear bias on. P is rounded to bf16, as in the tile kernel.
-// One persistent CTA per SM takes an equal share of all key tiles (fat_paged.cuh):
+// One persistent CTA per SM takes an equal share of all key tiles (fat_paged.cuh); requests of more rows are
+// cut into blocks of them (their keys are found in L2 again):
 //   warps 0-7  softmax, epilogue, zeros over the values behind the last key;
 //   warp 8     Q of an item (64 rows: two buffers) and its key tiles of 128 tokens, a lane per page;
 //   warp 9     issues the products; S of two tiles ahead runs beside this tile's softmax (three buffers);
@@ -25,7 +26,10 @@
 namespace fat {
 namespace {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;  // (warp 11 only completes the third warpgroup)
+constexpr int kSoftRegs = 208, kOtherRegs = 88;
+constexpr int kRegsNeeded = 256 * kSoftRegs + 128 * kOtherRegs;
+static_assert(kRegsNeeded <= kThreads * ((65536 / kThreads) & ~7), "register split");
 constexpr int kSoftWarps = 8, kWarpK = 8, kWarpMma = 9, kWarpV = 10;
 constexpr int kMinShare = 2;  // key tiles a CTA takes at least
 constexpr int kItemCost = 2;  // cost of an item beside its key tiles
@@ -38,7 +42,7 @@ struct MidCfg {
   static constexpr int BLK = 128 * 128;          // 128 keys x 64 channels
   static constexpr int TILE = DB * BLK;          // K or V of a tile
   // stages of K and of V: what is in flight bounds the rate of the copies
-  static constexpr int KS = D == 64 ? 5 : 2, VS = D == 64 ? (R == 64 ? 6 : 5) : R == 64 ? 3 : 2;
+  static constexpr int KS = D == 64 ? 5 : 2, VS = D == 64 ? (R == 64 ? 6 : 4) : R == 64 ? 3 : 2;
   static constexpr int QB = R == 64 ? 2 : 1;     // buffers of Q
   static constexpr int QBLK = R * 128, QTILE = DB * QBLK;
   static constexpr int PBLK = 128 * 128;         // 128 keys x 64 rows
@@ -51,11 +55,11 @@ struct MidCfg {
   static constexpr int PTILE = R / 64 * PBLK;
   static constexpr int OFF_ROW = OFF_P + PB * PTILE + 1024;  // behind the staged rows
   // per row: slope; bias of a far key at the first query's position less the reference; minus the reference;
-  // the reference; sum or factor; int2: position - shift, head; float [4 warps]: maxima
+  // the reference; sum or factor; int2: position - shift, head
   static constexpr int OFF_SLOPE = OFF_ROW, OFF_FAR = OFF_SLOPE + R * 4, OFF_NREF = OFF_FAR + R * 4;
   static constexpr int OFF_REF = OFF_NREF + R * 4, OFF_FAC = OFF_REF + R * 4, OFF_FARB = OFF_FAC + R * 4;
-  static constexpr int OFF_INT = OFF_FARB + R * 4, OFF_MAX = OFF_INT + R * 8;
-  static constexpr int OFF_BAR = OFF_MAX + 4 * R * 4;
+  static constexpr int OFF_INT = OFF_FARB + R * 4, OFF_MAX = OFF_INT + R * 8;  // float [2][8][RW]: maxima
+  static constexpr int OFF_BAR = OFF_MAX + 8 * R * 4;
   static constexpr int OFF_THR = OFF_BAR + 320;
   static constexpr int OFF_SHARE = OFF_THR + kMaxThresholds * 4;
   static constexpr int OFF_LUT = (OFF_SHARE + (int)sizeof(ShareSmem<kThreads>) + 15) & ~15;
@@ -64,8 +68,9 @@ struct MidCfg {
   }
   static_assert((2 * QB + 2 * KS + 2 * VS + 2 * SB + 6) * 8 + 8 <= 320, "barrier block");
   static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
-  static constexpr int LD = 132;  // floats of a staged row of the epilogue (16 a warpgroup, in P's place)
-  static_assert(2 * 16 * LD * 4 <= PTILE + 1024, "staged rows");
+  static constexpr int LD = 132;  // floats of a staged row of the epilogue (in P's place)
+  static constexpr int SR = R / 4;  // staged rows of a warpgroup
+  static_assert(2 * SR * LD * 4 <= PTILE + 1024, "staged rows");
   static constexpr uint32_t COL_O = SB * R, TMEM_COLS = 4 * R;
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, R, 0, 0);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, R, 1, 1);
@@ -272,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
   const bool work = sh.lo < sh.hi;
+  if (warp >= kSoftWarps) regs_dec<kOtherRegs>();
   if (work) {
     MidWalk<R> walk(p, share_s, sh);
     MidItem it;
@@ -394,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_wait_teardown(done, 0, kTeardownNs);
         __syncwarp();
       }
-    } else {
+    } else if (warp < kSoftWarps) {
       // ------------------------------------------------------------------ softmax: thread = key
+      regs_inc<kSoftRegs>();
       constexpr int RW = C::RW;
       const int wg = warp >> 2, t = tid & 127, rb = wg * RW, bar = 1 + wg;
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float *fac_s = reinterpret_cast<float *>(sm + C::OFF_FAC) + rb;
       float *farb_s = reinterpret_cast<float *>(sm + C::OFF_FARB) + rb;
       int2 *int_s = reinterpret_cast<int2 *>(sm + C::OFF_INT) + rb;
-      float *max_s = reinterpret_cast<float *>(sm + C::OFF_MAX) + 4 * rb;  // [warps][RW]
+      float *max_s = reinterpret_cast<float *>(sm + C::OFF_MAX) + 8 * rb;  // [8][RW]
       const bool t5 = p.bias.table != nullptr, biased = p.bias.has_bias != 0;
       const bool slopes = p.bias.slopes != nullptr;
       const int span = p.bias.sat_neg + p.bias.sat_pos;
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           slope_s[t] = slope;
           farb_s[t] = far - slope * (float)(pos - it.shift);
           int_s[t] = make_int2(pos - it.shift, h);
-          set_ref(t < mine ? kFreshRow : kNoRow);
+          set_ref(t < mine ? 0.f : kNoRow);
         }
         uint64_t sum[RW / 2];  // of this thread's weights, rows 2 i and 2 i + 1
 #pragma unroll
@@ -488,38 +495,56 @@ __global__ void __launch_bounds__(kThreads, 1)
               scale = 1.f;
             }
             const float delta0 = (float)(key - it.shift);
-            // logits of 32 rows less their references
-            auto logits = [&](int c, float (&y)[32]) {
+            // logits of 32 rows less their references, in pairs
+            const uint64_t scale2 = f2_pack(scale, scale), delta2 = f2_pack(delta0, delta0);
+            auto logits = [&](int c, uint64_t *y) {
               uint32_t x[32];
               tmem_ld32(tS + c, x);
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
-                float4 m = *reinterpret_cast<const float4 *>(cst_s + c + i);
+                ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(cst_s + c + i);
                 if (linear) {
-                  const float4 k = *reinterpret_cast<const float4 *>(slope_s + c + i);
-                  m.x = fmaf(k.x, delta0, m.x);
-                  m.y = fmaf(k.y, delta0, m.y);
-                  m.z = fmaf(k.z, delta0, m.z);
-                  m.w = fmaf(k.w, delta0, m.w);
+                  const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(slope_s + c + i);
+                  m.x = f2_fma(k.x, delta2, m.x);
+                  m.y = f2_fma(k.y, delta2, m.y);
                 }
-                y[i] = fmaf(__uint_as_float(x[i]), scale, m.x);
-                y[i + 1] = fmaf(__uint_as_float(x[i + 1]), scale, m.y);
-                y[i + 2] = fmaf(__uint_as_float(x[i + 2]), scale, m.z);
-                y[i + 3] = fmaf(__uint_as_float(x[i + 3]), scale, m.w);
+                y[i / 2] = f2_fma(f2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, m.x);
+                y[i / 2 + 1] =
+                    f2_fma(f2_pack(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), scale2, m.y);
               }
             };
-            bool raise = j == 0;
-            if (!raise) {
-              float top = -INFINITY;
-#pragma unroll 1
-              for (int c = 0; c < mine; c += 32) {
-                float y[32];
-                logits(c, y);
+            uint64_t y[RW / 2];  // of this group's rows
+            auto all_logits = [&]() {
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) top = fmax3(top, y[i], y[i + 1]);
+              for (int c = 0; c < RW; c += 32)
+                if (c == 0 || c < mine) logits(c, y + c / 2);
+            };
+            if (j == 0) {  // references from eight keys of the tile (those that their row sees)
+              all_logits();
+              if ((t & 15) == 0) {
+#pragma unroll
+                for (int i = 0; i < RW / 2; i += 2)
+                  *reinterpret_cast<ulonglong2 *>(max_s + (t >> 4) * RW + 2 * i) = make_ulonglong2(y[i], y[i + 1]);
               }
-              raise = bar_any(bar, top > 32.f);
+              named_bar_sync(bar, 128);
+              if (t < mine) {
+                float mx = max_s[t];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) mx = fmaxf(mx, max_s[i * RW + t]);
+                set_ref(mx > -1e30f ? mx : mx != mx ? 0.f : kFreshRow);  // (a NaN shows in the sum)
+              }
+              named_bar_sync(bar, 128);
             }
+            all_logits();
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < RW / 2; ++i) {
+              if (i >= 16 && mine <= 32) break;
+              float a, b;
+              f2_unpack(y[i], a, b);
+              top = fmax3(top, a, b);
+            }
+            const bool raise = bar_any(bar, top > 32.f);
             if (raise) {
               // The rows' maxima over the tile, and new references where they passed 2^32. A row that has seen
               // no key has a reference of -1e30, which loses the logit: its maximum is taken anew, from 0.
@@ -531,12 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               named_bar_sync(bar, 128);
 #pragma unroll 1
               for (int c = 0; c < mine; c += 32) {
-                float y[32], best = -INFINITY;
+                float best = -INFINITY;
                 logits(c, y);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float m = warp_max_f32(y[i]);
-                  if (lane == i) best = m;
+                for (int i = 0; i < 16; ++i) {
+                  float a, b;
+                  f2_unpack(y[i], a, b);
+                  a = warp_max_f32(a);
+                  b = warp_max_f32(b);
+                  if (lane == 2 * i) best = a;
+                  if (lane == 2 * i + 1) best = b;
                 }
                 max_s[(warp & 3) * RW + c + lane] = best;
               }
@@ -572,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < RW / 2; ++i)
                   sum[i] = f2_mul(sum[i], f2_pack(fac_s[2 * i], fac_s[2 * i + 1]));
               }
+              all_logits();
             }
             // P, once the products that read its place are complete
             if (gt >= C::PB && !(ok = o_wait(gt - C::PB))) break;
@@ -579,12 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < RW; c += 32) {
               if (c > 0 && c >= mine) break;
-              float y[32];
-              logits(c, y);
               uint32_t w[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float a = ex2(y[2 * i]), b = ex2(y[2 * i + 1]);
+                float a, b;
+                f2_unpack(y[c / 2 + i], a, b);
+                a = ex2(a);
+                b = ex2(b);
                 sum[c / 2 + i] = f2_add(sum[c / 2 + i], f2_pack(a, b));
                 w[i] = pack_bf16x2(a, b);
               }
@@ -632,35 +663,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           rec->rows = rows;
         }
         constexpr int LD = C::LD;
-        float *stage = reinterpret_cast<float *>(sm + C::OFF_P) + wg * 16 * LD;  // [16][LD]: P has been used
+        constexpr int SR = C::SR;
+        float *stage = reinterpret_cast<float *>(sm + C::OFF_P) + wg * SR * LD;  // [SR][LD]: P has been used
         if (mine > 0) {
 #pragma unroll
-          for (int c = 0; c < RW; c += 16) {  // the threads' sums of 16 rows
+          for (int c = 0; c < RW; c += SR) {  // the threads' sums, 128 / SR threads a row
             if (c >= mine) break;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < SR / 2; ++i)
               f2_unpack(sum[c / 2 + i], stage[2 * i * LD + t], stage[(2 * i + 1) * LD + t]);
             named_bar_sync(bar, 128);
+            constexpr int TR = 128 / SR;
             float l = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 v = *reinterpret_cast<const float4 *>(stage + (t >> 3) * LD + (t & 7) * 4 + 32 * i);
+            for (int i = 0; i < SR / 4; ++i) {
+              const float4 v =
+                  *reinterpret_cast<const float4 *>(stage + (t / TR) * LD + (t % TR) * 4 + TR * 4 * i);
               l += (v.x + v.y) + (v.z + v.w);
             }
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if ((t & 7) == 0) fac_s[c + (t >> 3)] = l;
+            for (int o = 1; o < TR; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (t % TR == 0) fac_s[c + t / TR] = l;
             named_bar_sync(bar, 128);
           }
 #pragma unroll 1
-          for (int c = 0; c < mine; c += 16) {  // and the rows
-            uint32_t x[16];
-            tmem_ld16(tmem + lane_off + C::COL_O + rb + c, x);
+          for (int c = 0; c < mine; c += SR) {  // and the rows
+            uint32_t x[SR];
+            if constexpr (SR == 32)
+              tmem_ld32(tmem + lane_off + C::COL_O + rb + c, x);
+            else
+              tmem_ld16(tmem + lane_off + C::COL_O + rb + c, x);
             if (t < D)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) stage[i * LD + t] = __uint_as_float(x[i]);
+              for (int i = 0; i < SR; ++i) stage[i * LD + t] = __uint_as_float(x[i]);
             named_bar_sync(bar, 128);
-            const int left = min(16, mine - c);
+            const int left = min(SR, mine - c);
             if (whole) {
               for (int i = t; i < left * (D / 8); i += 128) {
                 const int rr = i / (D / 8), ch = (i % (D / 8)) * 8, h = int_s[c + rr].y;
@@ -678,8 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               float *po = part_rows<R, D>(p.part, gridDim.x, blockIdx.x, which);
               float *ps = part_stats<R, D>(p.part, gridDim.x, blockIdx.x, which);
-              for (int i = t; i < 16 * (D / 4); i += 128) {
-                const int rr = i & 15, c4 = i >> 4;
+              for (int i = t; i < SR * (D / 4); i += 128) {
+                const int rr = i % SR, c4 = i / SR;
                 if (rr < left)
                   *part_quad<R>(po, rb + c + rr, c4) =
                       *reinterpret_cast<const float4 *>(stage + rr * LD + 4 * c4);
@@ -720,14 +757,12 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
   if (make_tmap_rows(&mq, p.q, p.total_q, p.hq, D, p.group, R / p.group)) return FAT_ECUDA;
   const size_t smem = C::bytes(p.bias) + 1024;
   const auto kernel = fat_paged_mid_kernel<D, R>;
-  if (prepare_kernel((const void *)kernel, smem, kThreads, 0)) return FAT_ECUDA;
+  if (prepare_kernel((const void *)kernel, smem, kThreads, kRegsNeeded)) return FAT_ECUDA;
   return launch_dependent("paged tree kernel launch", kernel, dim3((unsigned)paged_tile_ctas()),
                           kThreads, smem, stream, mq, mk, mv, pp);
 }
 
 }  // namespace
-
-int paged_mid_rows(long long rows) { return rows <= 64 ? 64 : rows <= 128 ? 128 : 0; }
 
 int launch_paged_mid(const PagedParams &p, const fat_paged_cache_t &c, int rows, cudaStream_t stream) {
   if (c.head_dim == 64) return rows == 64 ? launch_t<64, 64>(p, c, stream) : launch_t<64, 128>(p, c, stream);
