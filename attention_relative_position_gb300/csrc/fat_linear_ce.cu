@@ -17,12 +17,14 @@
 // One kernel does all products: pairs of CTAs on two SMs, one tcgen05 product of 256 x 256 x 16 for both
 // (cta_group::2: each CTA stages half of the rows and half of the columns, so a stage is 32 KB a CTA for
 // the work of 64 KB), persistent over a list of tiles:
-//   warps 0-3  epilogue, a row (TMEM lane) per thread; two accumulators, so a tile's epilogue runs beside
-//              the next tile's products;
-//   warp 4     producer: boxes of 64 x 64 elements by TMA, 128-byte swizzle; the same boxes serve
+//   warps 0-7  epilogue, a row (TMEM lane) per thread, each warpgroup half of the columns; two accumulators,
+//              so a tile's epilogue runs beside the next tile's products;
+//   warp 8     producer: boxes of 64 x 64 elements by TMA, 128-byte swizzle; the same boxes serve
 //              operands whose reduction runs along their rows (K-major: hidden rows and weights of the logits,
 //              dz of dh) or across them (MN-major: weights of dh, dz and hidden rows of dw);
-//   warp 5     issues the products (the pair's first CTA).
+//   warp 9     issues the products (the pair's first CTA).
+// Up to 128 rows (scores of drafted tokens) the weights are the tall side instead: 256 vocabulary entries x
+// the rows, a stage holds little but weights, and more of them are on their way.
 #include <algorithm>
 #include <cstdint>
 
@@ -31,17 +33,30 @@
 namespace fat {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kEpiWarps = 4, kWarpProd = 4, kWarpMma = 5;
-constexpr int kStages = 6;
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8, kWarpProd = 8, kWarpMma = 9;
 constexpr int kHalf = 128 * 128;          // one operand's half of a stage: 128 rows x 64 bf16
-constexpr int kStage = 2 * kHalf;
 constexpr int kBuf = 32 * 128;            // staged output of a warp: 32 rows x 128 bytes
-constexpr int kOffBuf = kStages * kStage;
-constexpr int kOffBar = kOffBuf + kEpiWarps * 2 * kBuf;
-constexpr int kSmem = kOffBar + 256 + 1024;
-static_assert(kSmem <= kSmemLimit, "shared memory");
 constexpr int kTile = 256;                // rows and columns of a pair's tile
+constexpr int kFewHeadRows = 128;         // forward calls of at most so many rows take the few-row form
+constexpr int kMaxPairs = 128;
+
+// The kernel's forms, and what each has in shared memory.
+enum Mode { kForward, kBackward, kFew };
+template <int MODE>
+struct HeadCfg {
+  static constexpr int STAGES = MODE == kBackward ? 6 : MODE == kForward ? 6 : 10;  // at most
+  static constexpr int OFF_BUF = MODE == kFew ? 186 * 1024 : STAGES * 2 * kHalf;
+  // backward: an output buffer a warp; few rows: targets, and 32 rows of logits a warpgroup
+  static constexpr int LD = 132;  // floats from row to row of these
+  static constexpr int OFF_ROWS = OFF_BUF + kFewHeadRows * 4;
+  static constexpr int OFF_BAR = MODE == kBackward ? OFF_BUF + kEpiWarps * kBuf
+                                 : MODE == kFew    ? OFF_ROWS + 2 * 32 * LD * 4
+                                                   : OFF_BUF;
+  static constexpr int SMEM = OFF_BAR + 320 + 1024;
+  static_assert((2 * STAGES + 5) * 8 + 8 <= 320, "barrier block");
+  static_assert(SMEM <= kSmemLimit, "shared memory");
+};
 
 enum Kind { kLogits, kProb, kDx, kDw };
 
@@ -53,7 +68,8 @@ struct HeadParams {
   int row_tiles, col_tiles;
   int row_group;           // forward: row tiles that walk the vocabulary together
   // forward
-  float2 *part;            // [col_tiles][rows]: maximum (log2 units), sum
+  int stages, stage_bytes; // few rows: stages and their size
+  float2 *part;            // [2 col_tiles][rows]: maximum (log2 units), sum (of each half of a tile)
   float *zt;               // [rows]: the target's logit
   const int32_t *target;
   float scale;
@@ -65,12 +81,19 @@ struct HeadParams {
   int dx_add, dw_add;             // add to what the piece before left (fp32)
   int dx_f32, dw_f32;
   int dx_rows;                    // rows of a split's partial dh
-  // logits of the next piece
+  int dx_first;                   // dh's tiles take longer than dw's: they come first
+  // logits of the next piece: pair q takes tiles prob_first[q] up to prob_first[q + 1] behind the others
   int pv0, pr0, prow_tiles;
+  uint16_t prob_first[kMaxPairs + 1];
   const float4 *rec;       // [rows, padded]: lse (log2 units), factor, subtracted at the target, target
   int *err;
   long long timeout_ns;
   int debug_flags;
+};
+
+template <int N>
+struct Threads {
+  static constexpr int value = N;
 };
 
 struct Job {
@@ -79,11 +102,14 @@ struct Job {
   int split;
 };
 
-template <bool BWD>
-__device__ __forceinline__ bool job_at(const HeadParams &p, int j, Job &o) {
+// Tile i of a pair. Forward: dealt in turns. Backward: the products' tiles in alternating turns (the longer
+// kind first), then the pair's share of the next piece's logits, which evens out what the turns left.
+template <int MODE>
+__device__ __forceinline__ bool job_at(const HeadParams &p, int pair, int i, Job &o) {
   o.split = 0;
   o.k0 = 0;
-  if (!BWD) {
+  if (MODE != kBackward) {
+    const int j = pair + i * p.pairs;
     if (j >= p.row_tiles * p.col_tiles) return false;
     const int per = p.row_group * p.col_tiles, g = j / per, rest = j - g * per;
     const int cnt = min(p.row_group, p.row_tiles - g * p.row_group);
@@ -94,33 +120,44 @@ __device__ __forceinline__ bool job_at(const HeadParams &p, int j, Job &o) {
     o.k1 = (p.dim + 63) >> 6;
     return true;
   }
-  if (j < p.n_dw) {
-    const int v = j / p.d_tiles;
-    o.kind = kDw;
-    o.m0 = v * kTile;  // within the piece
-    o.n0 = (j - v * p.d_tiles) * kTile;
-    o.k1 = p.r_kb;
+  const int longs = p.n_dw + p.n_dx, full = longs / p.pairs;
+  int j = i * p.pairs + ((i & 1) ? p.pairs - 1 - pair : pair);
+  const int mine = full + (full * p.pairs + ((full & 1) ? p.pairs - 1 - pair : pair) < longs ? 1 : 0);
+  if (i >= mine) {
+    j = p.prob_first[pair] + i - mine;
+    if (j >= p.prob_first[pair + 1]) return false;
+    const int v = j / p.prow_tiles;
+    o.kind = kProb;
+    o.m0 = (j - v * p.prow_tiles) * kTile;
+    o.n0 = v * kTile;
+    o.k1 = (p.dim + 63) >> 6;
     return true;
   }
-  j -= p.n_dw;
-  if (j < p.n_dx) {
-    const int d = j % p.d_tiles, rest = j / p.d_tiles;
+  bool dx = p.dx_first;
+  const int first = dx ? p.n_dx : p.n_dw;
+  if (j >= first) {
+    j -= first;
+    dx = !dx;
+  }
+  // (a pair's turns meet all channel tiles alike: the last one is cheaper)
+  const int rest = j / p.d_tiles, d = (j + rest) % p.d_tiles;
+  o.n0 = d * kTile;
+  if (dx) {
     o.kind = kDx;
-    o.n0 = d * kTile;
     o.split = rest % p.dx_splits;
     o.m0 = rest / p.dx_splits * kTile;
     o.k0 = o.split * p.dx_kb;
     o.k1 = min(o.k0 + p.dx_kb, p.p_kb);
-    return true;
+  } else {
+    o.kind = kDw;
+    o.m0 = rest * kTile;  // within the piece
+    o.k1 = p.r_kb;
   }
-  j -= p.n_dx;
-  if (j >= p.n_prob) return false;
-  const int v = j / p.prow_tiles;
-  o.kind = kProb;
-  o.m0 = (j - v * p.prow_tiles) * kTile;
-  o.n0 = v * kTile;
-  o.k1 = (p.dim + 63) >> 6;
   return true;
+}
+// Columns of a tile of dh or dw: 256, of the last one 128 where they do.
+__device__ __forceinline__ int d_cols(const HeadParams &p, int n0) {
+  return p.dim - n0 <= 128 ? 128 : 256;
 }
 
 // ---- what the pair needs beyond sm103_ptx.cuh -----------------------------------------------------
@@ -196,9 +233,6 @@ __device__ __forceinline__ void add_box(const CUtensorMap *map, uint32_t src, in
       "r"(x), "r"(y), "r"(src)
       : "memory");
 }
-__device__ __forceinline__ void bulk_wait_read_1() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
@@ -222,35 +256,31 @@ __device__ __forceinline__ void keep_below(uint32_t (&x)[32], int lim, float v) 
     if (i >= lim) x[i] = __float_as_uint(v);
 }
 
-// A warp's 32 rows x 128 bytes to global memory through its staging buffers.
+// A warp's 32 rows x 128 bytes to global memory through its staging buffer.
 struct Staged {
-  uint32_t buf[2];
-  int lane, n;
-  __device__ uint32_t next() {
-    if (n >= 2) {
-      if (lane == 0) bulk_wait_read_1();  // the copy before the last one has read its buffer
-      __syncwarp();
-    }
-    return buf[n & 1];
+  uint32_t buf;
+  int lane;
+  __device__ void wait() {  // the copy before has read the buffer
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
   }
-  __device__ void put(uint32_t b, int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t w) const {
-    st_shared_v4(b + lane * 128 + ((chunk ^ (lane & 7)) << 4), x, y, z, w);
+  __device__ void put(int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t w) const {
+    st_shared_v4(buf + lane * 128 + ((chunk ^ (lane & 7)) << 4), x, y, z, w);
   }
   __device__ void send(const CUtensorMap *map, bool add, int x, int y) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       if (add)
-        add_box(map, buf[n & 1], x, y);
+        add_box(map, buf, x, y);
       else
-        store_box(map, buf[n & 1], x, y);
+        store_box(map, buf, x, y);
       bulk_commit_group();
     }
-    ++n;
   }
 };
 
-template <bool BWD>
+template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fat_head_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_p,      // dz of this piece, read
@@ -258,19 +288,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_dx,
                     const __grid_constant__ CUtensorMap tm_dw,
                     const __grid_constant__ HeadParams p) {
+  using C = HeadCfg<MODE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cta_rank(), pair = blockIdx.x >> 1;
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + kOffBar);  // of the first CTA
-  uint64_t *empty = full + kStages;                             // of each CTA
-  uint64_t *acc_full = empty + kStages;                         // [2] of each CTA
-  uint64_t *acc_empty = acc_full + 2;                           // [2] of the first CTA
-  uint64_t *done = acc_empty + 2;                               // of the first CTA
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);  // of the first CTA
+  uint64_t *empty = full + C::STAGES;                              // of each CTA
+  uint64_t *acc_full = empty + C::STAGES;                          // [2] of each CTA
+  uint64_t *acc_empty = acc_full + 2;                              // [2] of the first CTA
+  uint64_t *done = acc_empty + 2;                                  // of the first CTA
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int stages = MODE == kFew ? p.stages : C::STAGES;
+  const int stage_bytes = MODE == kFew ? p.stage_bytes : 2 * kHalf;
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
@@ -297,53 +330,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Watchdog wd{abort_flag, p.err, BWD ? FAT_DEVERR_TIMEOUT_BWD : FAT_DEVERR_TIMEOUT_FWD,
+  const Watchdog wd{abort_flag, p.err, MODE == kBackward ? FAT_DEVERR_TIMEOUT_BWD : FAT_DEVERR_TIMEOUT_FWD,
                     p.timeout_ns};
-  grid_dep_wait();
   grid_dep_launch();
+  grid_dep_wait();
 
   if (warp == kWarpProd) {
     // ------------------------------------------------------------------ producer
     if (lane == 0) {
-      uint32_t it = 0;
+      int slot = 0;
+      uint32_t phase = 1;
       bool ok = !(p.debug_flags & 1);  // test hook: no copies, the waits run out
       Job job;
-      for (int j = pair; ok && job_at<BWD>(p, j, job); j += p.pairs) {
+      for (int i = 0; ok && job_at<MODE>(p, pair, i, job); ++i) {
         const int kind = job.kind;
-        const int bhalf = kind == kLogits ? p.bn >> 1 : 128;
-        for (int k = job.k0; k < job.k1; ++k, ++it) {
-          const int s = it % kStages;
-          if (it >= kStages && !(ok = mbar_wait(empty + s, (it / kStages - 1) & 1, wd))) break;
-          const uint32_t a = smem_u32(sm + s * kStage), b = a + kHalf;
-          const uint32_t bar = in_first(full + s);
-          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * (kHalf + bhalf * 128));
+        // rows of this CTA's half of the second operand
+        const int bhalf = MODE != kBackward ? p.bn >> 1 : kind == kProb ? 128 : d_cols(p, job.n0) >> 1;
+        for (int k = job.k0; k < job.k1; ++k) {
+          if (!(ok = mbar_wait(empty + slot, phase, wd))) break;
+          const uint32_t a = smem_u32(sm) + slot * stage_bytes, b = a + kHalf;
+          const uint32_t bar = in_first(full + slot);
+          if (rank == 0) mbar_arrive_expect_tx(full + slot, 2 * (kHalf + bhalf * 128));
           const int m = job.m0 + rank * 128, n = job.n0 + rank * bhalf;
-          if (kind == kLogits || kind == kProb) {
-            const int m1 = kind == kProb ? m + p.pr0 : m, n1 = kind == kProb ? n + p.pv0 : n;
-            load_pair(&tm_x, bar, a, k * 64, m1);
-            load_pair(&tm_x, bar, a + 8192, k * 64, m1 + 64);
-            if (!BWD) {
-              load_pair(&tm_w, bar, b, k * 64, n1);  // a box of bn / 2 rows
-            } else {
-              load_pair(&tm_w, bar, b, k * 64, n1);
-              load_pair(&tm_w, bar, b + 8192, k * 64, n1 + 64);
-            }
+          if (MODE == kForward) {
+            load_pair(&tm_x, bar, a, k * 64, m);  // boxes of 128 and of bn / 2 rows
+            load_pair(&tm_w, bar, b, k * 64, n);
+          } else if (MODE == kFew) {
+            load_pair(&tm_w, bar, a, k * 64, m);
+            load_pair(&tm_x, bar, b, k * 64, n);
+          } else if (kind == kProb) {
+            load_pair(&tm_x, bar, a, k * 64, p.pr0 + m);
+            load_pair(&tm_x, bar, a + 8192, k * 64, p.pr0 + m + 64);
+            load_pair(&tm_w, bar, b, k * 64, p.pv0 + n);
+            load_pair(&tm_w, bar, b + 8192, k * 64, p.pv0 + n + 64);
           } else if (kind == kDx) {
             load_pair(&tm_p, bar, a, k * 64, m);
             load_pair(&tm_p, bar, a + 8192, k * 64, m + 64);
             load_pair(&tm_w, bar, b, n, p.v0 + k * 64);
-            load_pair(&tm_w, bar, b + 8192, n + 64, p.v0 + k * 64);
+            if (bhalf == 128) load_pair(&tm_w, bar, b + 8192, n + 64, p.v0 + k * 64);
           } else {
             load_pair(&tm_p, bar, a, m, k * 64);
             load_pair(&tm_p, bar, a + 8192, m + 64, k * 64);
             load_pair(&tm_x, bar, b, n, p.r0 + k * 64);
-            load_pair(&tm_x, bar, b + 8192, n + 64, p.r0 + k * 64);
+            if (bhalf == 128) load_pair(&tm_x, bar, b + 8192, n + 64, p.r0 + k * 64);
+          }
+          if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
           }
         }
       }
       // every stage's last use has been released: nothing arrives here after this CTA has ended
-      for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
-        ok = mbar_wait(empty + i % kStages, (i / kStages) & 1, wd);
+      for (int i = 0; ok && i < stages; ++i) {
+        ok = mbar_wait(empty + slot, phase, wd);
+        if (++slot == stages) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
       if (*abort_flag) {  // copies may still be on their way: give them time to land
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
@@ -352,28 +396,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------------ products
     if (rank == 0 && lane == 0) {
-      uint32_t it = 0, n = 0;
+      int slot = 0;
+      uint32_t phase = 0, n = 0;
       bool ok = true;
       Job job;
-      for (int j = pair; ok && job_at<BWD>(p, j, job); j += p.pairs, ++n) {
-        const bool a_mn = job.kind == kDw, b_mn = job.kind >= kDx;
-        const uint32_t idesc =
-            idesc_bf16_f32(256, job.kind == kLogits ? p.bn : 256, a_mn ? 1 : 0, b_mn ? 1 : 0);
+      for (int i = 0; ok && job_at<MODE>(p, pair, i, job); ++i, ++n) {
+        const bool a_mn = MODE == kBackward && job.kind == kDw, b_mn = MODE == kBackward && job.kind >= kDx;
+        const int cols = MODE != kBackward ? p.bn : b_mn ? d_cols(p, job.n0) : 256;
+        const uint32_t idesc = idesc_bf16_f32(256, cols, a_mn ? 1 : 0, b_mn ? 1 : 0);
         const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
         const uint32_t d = tmem + 256 * (n & 1);
         if (n >= 2 && !(ok = wait_cluster(acc_empty + (n & 1), (n / 2 - 1) & 1, wd))) break;
         tc_fence_after();
-        for (int k = job.k0; k < job.k1; ++k, ++it) {
-          const int s = it % kStages;
-          if (!(ok = wait_cluster(full + s, (it / kStages) & 1, wd))) break;
+        for (int k = job.k0; k < job.k1; ++k) {
+          if (!(ok = wait_cluster(full + slot, phase, wd))) break;
           tc_fence_after();
-          const uint32_t a = smem_u32(sm + s * kStage);
+          const uint32_t a = smem_u32(sm) + slot * stage_bytes;
           const uint64_t da = sw128_desc(a, a_mn ? 8192 : 16, 1024);
           const uint64_t db = sw128_desc(a + kHalf, b_mn ? 8192 : 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_pair(d, da + kk * a_step, db + kk * b_step, idesc, k > job.k0 || kk > 0);
-          commit_pair(empty + s);
+          commit_pair(empty + slot);
+          if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
         commit_pair(acc_full + (n & 1));
       }
@@ -382,28 +430,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    Staged st{{smem_u32(sm + kOffBuf + warp * 2 * kBuf), smem_u32(sm + kOffBuf + warp * 2 * kBuf + kBuf)},
-              lane, 0};
-    const int row_in = rank * 128 + warp * 32;  // the warp's first row of the pair's tile
+    const int half = warp >> 2;  // of the columns
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const int row_in = rank * 128 + (warp & 3) * 32;  // the warp's first row of the pair's tile
+    Staged st{smem_u32(sm + C::OFF_BUF + warp * kBuf), lane};
+    int *target_s = reinterpret_cast<int *>(sm + C::OFF_BUF);
+    float *rows_s = reinterpret_cast<float *>(sm + C::OFF_ROWS) + half * 32 * C::LD;
+    if (MODE == kFew) {
+      const int t = tid & 127;  // each warpgroup its own rows' targets
+      if (t < kFewHeadRows / 2) {
+        const int r = half * (p.bn >> 1) + t;
+        target_s[half * (kFewHeadRows / 2) + t] = t < p.bn >> 1 && r < p.rows ? __ldg(p.target + r) : -1;
+      }
+      target_s += half * (kFewHeadRows / 2);
+      named_bar_sync(1 + half, 128);
+    }
     uint32_t n = 0;
     bool ok = true;
     Job job;
-    for (int j = pair; ok && job_at<BWD>(p, j, job); j += p.pairs, ++n) {
+    for (int i = 0; ok && job_at<MODE>(p, pair, i, job); ++i, ++n) {
       const uint32_t d = tmem + lane_off + 256 * (n & 1);
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(in_first(acc_empty + (n & 1)));
       };
-      if constexpr (!BWD) {
+      if constexpr (MODE == kForward) {
         const int row = job.m0 + row_in + lane;
         const int t = row < p.rows ? __ldg(p.target + row) : -1;
-        const int lim = min(p.bn, p.vocab - job.n0);
+        // this warpgroup's columns
+        const int c0 = 128 * half, lim = min(min(p.bn, p.vocab - job.n0), c0 + 128);
         if (!(ok = warp_wait_cluster(acc_full + (n & 1), (n / 2) & 1, wd))) break;
         tc_fence_after();
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        for (int c = 0; c < lim; c += 32) {
+        for (int c = c0; c < lim; c += 32) {
           uint32_t x[32];
           tmem_ld32(d + c, x);
           if (c + 32 > lim) keep_below(x, lim - c, -INFINITY);
@@ -416,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float m_use = m == -INFINITY ? 0.f : m;
         const uint64_t sl = f2_pack(p.sl2, p.sl2), neg = f2_pack(-m_use, -m_use);
         uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-        for (int c = 0; c < lim; c += 32) {
+        for (int c = c0; c < lim; c += 32) {
           uint32_t x[32];
           tmem_ld32(d + c, x);
           const int at = t - job.n0 - c;
@@ -439,24 +499,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float s0, s1;
         f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
         if (row < p.rows)
-          p.part[(size_t)(job.n0 / p.bn) * p.rows + row] = make_float2(m, s0 + s1);
+          p.part[(size_t)(2 * (job.n0 / p.bn) + half) * p.rows + row] = make_float2(m, s0 + s1);
+      } else if constexpr (MODE == kFew) {
+        // A thread holds a vocabulary entry's logits of this warpgroup's rows, and passes them on through shared
+        // memory to the threads that share a row: its statistics over the CTA's 128 entries.
+        const int r0 = half * (p.bn >> 1), nr = min(p.rows - r0, p.bn >> 1);
+        const int t = tid & 127, v0 = job.m0 + rank * 128;
+        const bool in = v0 + t < p.vocab;
+        if (!(ok = warp_wait_cluster(acc_full + (n & 1), (n / 2) & 1, wd))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < nr; c += 32) {
+          const int cnt = min(nr - c, 32);
+          uint32_t x[32];
+          tmem_ld32(d + r0 + c, x);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < cnt) rows_s[i * C::LD + t] = in ? __uint_as_float(x[i]) : -INFINITY;
+          if (c + 32 >= nr) release();
+          named_bar_sync(1 + half, 128);
+          auto row_stats = [&](auto threads) {  // `threads` of them a row
+            constexpr int TR = decltype(threads)::value, N = 128 / TR;
+            const int r = t / TR, part = t % TR;
+            float y[N], mx = -INFINITY, e = 0.f;
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k) {
+              const float4 q = *reinterpret_cast<const float4 *>(rows_s + r * C::LD + 4 * (part + TR * k));
+              y[4 * k] = q.x;
+              y[4 * k + 1] = q.y;
+              y[4 * k + 2] = q.z;
+              y[4 * k + 3] = q.w;
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) mx = fmaxf(mx, y[k]);
+#pragma unroll
+            for (int o = 1; o < TR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float m = mx * p.sl2, use = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int k = 0; k < N; ++k) e += ex2(fmaf(y[k], p.sl2, -use));
+#pragma unroll
+            for (int o = 1; o < TR; o <<= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+            if (part == 0 && r < cnt) {
+              const int row = r0 + c + r, at = target_s[c + r] - v0;
+              p.part[(size_t)(2 * (job.m0 / kTile) + rank) * p.rows + row] = make_float2(m, e);
+              if (at >= 0 && at < 128 && v0 + at < p.vocab) p.zt[row] = rows_s[r * C::LD + at] * p.scale;
+            }
+          };
+          if (cnt <= 8)
+            row_stats(Threads<16>{});
+          else
+            row_stats(Threads<4>{});
+          named_bar_sync(1 + half, 128);
+        }
+        if (nr <= 0) release();
       } else {
         float4 rec = make_float4(0.f, 0.f, 0.f, 0.f);
         if (job.kind == kProb) rec = __ldg(p.rec + p.pr0 + job.m0 + row_in + lane);
         if (!(ok = warp_wait_cluster(acc_full + (n & 1), (n / 2) & 1, wd))) break;
         tc_fence_after();
+        const int c0 = 128 * half;
         if (job.kind == kProb) {
           const int lim = p.vocab - (p.pv0 + job.n0);
           const int t = __float_as_int(rec.w) - (p.pv0 + job.n0);
           const uint64_t sl = f2_pack(p.sl2, p.sl2), neg = f2_pack(-rec.x, -rec.x);
           const uint64_t f = f2_pack(rec.y, rec.y);
-          for (int c = 0; c < kTile; c += 64) {
+#pragma unroll 1
+          for (int c = c0; c < c0 + 128; c += 64) {
             uint32_t x[2][32];
             tmem_ld32_issue(d + c, x[0]);
             tmem_ld32_issue(d + c + 32, x[1]);
             tmem_ld32_fence(x[0]);
             tmem_ld32_fence(x[1]);
-            const uint32_t b = st.next();
+            st.wait();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float y[32];
@@ -480,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                st.put(b, 4 * h + i, pack_bf16x2(y[8 * i], y[8 * i + 1]),
+                st.put(4 * h + i, pack_bf16x2(y[8 * i], y[8 * i + 1]),
                        pack_bf16x2(y[8 * i + 2], y[8 * i + 3]), pack_bf16x2(y[8 * i + 4], y[8 * i + 5]),
                        pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
             }
@@ -492,16 +606,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const bool f32 = dx ? p.dx_f32 : p.dw_f32, add = dx ? p.dx_add : p.dw_add;
           // rows: of dh (its split's partial), or the vocabulary's entries
           const int y = (dx ? job.split * p.dx_rows + (p.dx_f32 ? 0 : p.r0) : p.v0) + job.m0 + row_in;
-          const int cols = min(kTile, p.dim - job.n0);
+          const int cols = min(c0 + 128, p.dim - job.n0);
           const int step = f32 ? 32 : 64;
-          for (int c = 0; c < cols; c += step) {
-            const uint32_t b = st.next();
+#pragma unroll 1
+          for (int c = c0; c < cols; c += step) {
+            st.wait();
             uint32_t x[32];
             if (f32) {
               tmem_ld32(d + c, x);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                st.put(b, i, x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                st.put(i, x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
             } else {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
@@ -513,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   for (int k = 0; k < 4; ++k)
                     w[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]),
                                        __uint_as_float(x[8 * i + 2 * k + 1]));
-                  st.put(b, 4 * h + i, w[0], w[1], w[2], w[3]);
+                  st.put(4 * h + i, w[0], w[1], w[2], w[3]);
                 }
               }
             }
@@ -523,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         release();
       }
     }
-    if (BWD && lane == 0) bulk_wait_all();
+    if (MODE == kBackward && lane == 0) bulk_wait_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -536,14 +651,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---- statistics of the tiles to lse and loss --------------------------------------------------------
-// RB rows a block, 256 / RB threads a row, each a share of the tiles.
+// RB rows a block, 256 / RB threads a row, each a share of the halves of tiles.
 template <int RB>
 __global__ void __launch_bounds__(256) fat_head_merge_kernel(const float2 *part, const float *zt,
                                                              const int32_t *target, int rows,
                                                              int tiles, int vocab, float zc,
                                                              float *loss, float *lse_out, int *err) {
   constexpr int TL = 256 / RB;
-  __shared__ float2 red[TL][RB];
+  __shared__ float2 red[8][RB];
+  grid_dep_launch();
   grid_dep_wait();
   const int r = threadIdx.x % RB, y = threadIdx.x / RB;
   const int row = blockIdx.x * RB + r;
@@ -566,10 +682,14 @@ __global__ void __launch_bounds__(256) fat_head_merge_kernel(const float2 *part,
       for (int u = 0; u < U; ++u) add(v[u]);
     }
   }
-  red[y][r] = make_float2(m, s);
+#pragma unroll
+  for (int o = RB; o < 32; o <<= 1)  // over the lanes of the row, then over the warps
+    add(make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o)));
+  if ((threadIdx.x & 31) < RB) red[threadIdx.x >> 5][r] = make_float2(m, s);
   __syncthreads();
-  if (y != 0 || row >= rows) return;
-  for (int i = 1; i < TL; ++i) add(red[i][r]);
+  if (threadIdx.x >= RB || row >= rows) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) add(red[i][r]);
   const float lse = m * kLn2 + logf(s);
   const int t = __ldg(target + row);
   if (t >= vocab) atomicOr(err, FAT_DEVERR_INDEX);
@@ -583,10 +703,10 @@ __global__ void __launch_bounds__(256) fat_head_merge_kernel(const float2 *part,
 __global__ void __launch_bounds__(256)
     fat_head_rows_kernel(const uint4 *hidden, long long stride16, const int32_t *target,
                          const float *lse, const float *dloss, float grad_scale, float scale, float zc,
-                         int rows, int padded, int vocab, int chunks, uint4 *copy, float4 *rec,
-                         int *err) {
-  grid_dep_wait();
+                         int rows, int padded, int vocab, int chunks, int pitch16, uint4 *copy,
+                         float4 *rec, int *err) {
   grid_dep_launch();
+  grid_dep_wait();
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= padded) return;
   const int t = row < rows ? __ldg(target + row) : -1;
@@ -603,13 +723,26 @@ __global__ void __launch_bounds__(256)
   }
   if (row >= rows) return;
   for (int c = lane; c < chunks; c += 32)
-    copy[(size_t)row * chunks + c] =
+    copy[(size_t)row * pitch16 + c] =
         counts ? __ldg(hidden + row * stride16 + c) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// rows of `chunks` 16-byte pieces, source_pitch and pitch of them apart
+__global__ void __launch_bounds__(256) fat_head_copy_kernel(const uint4 *src, long long source_pitch,
+                                                            long long n, int chunks, int pitch, uint4 *dst) {
+  grid_dep_launch();
+  grid_dep_wait();
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+    const long long row = i / chunks;
+    const int c = (int)(i - row * chunks);
+    dst[row * pitch + c] = __ldg(src + row * source_pitch + c);
+  }
 }
 
 // dst = bf16(sum of the parts), eight values a thread
 __global__ void __launch_bounds__(256) fat_head_sum_kernel(const float4 *part, long long n8, int parts,
                                                            long long part_stride4, uint4 *dst) {
+  grid_dep_launch();
   grid_dep_wait();
   const long long i = blockIdx.x * 256ll + threadIdx.x;
   if (i >= n8) return;
@@ -649,33 +782,55 @@ int check(const fat_linear_ce_shape_t *s) {
   return FAT_OK;
 }
 
+template <int MODE>
+bool head_ready() {
+  return prepare_kernel((const void *)fat_head_kernel<MODE>, HeadCfg<MODE>::SMEM, kThreads, 0) == 0;
+}
+// Pairs of CTAs that run at once (0: no device)
 int head_pairs() {
-  if (prepare_kernel((const void *)fat_head_kernel<false>, kSmem, kThreads, 0) ||
-      prepare_kernel((const void *)fat_head_kernel<true>, kSmem, kThreads, 0))
-    return 0;
-  return max_pair_ctas((const void *)fat_head_kernel<true>, kSmem, kThreads) / 2;
+  if (!head_ready<kForward>() || !head_ready<kBackward>() || !head_ready<kFew>()) return 0;
+  return std::min(kMaxPairs, max_pair_ctas((const void *)fat_head_kernel<kBackward>,
+                                           HeadCfg<kBackward>::SMEM, kThreads) / 2);
 }
 
-// Columns of a forward tile: 256, or as many fewer as leave the same number of rounds over the pairs.
-// Few rows: one row of weights read by every pair alike.
-int forward_columns(const fat_linear_ce_shape_t *s, int pairs) {
-  const long long rt = ceil_div(s->rows, kTile);
-  const long long rounds = ceil_div(rt * ceil_div(s->vocab, kTile), pairs);
-  int bn = kTile;
-  while (bn > 32 && rt * ceil_div(s->vocab, bn - 16) <= rounds * pairs) bn -= 16;
-  return bn;
-}
+// Forward: tiles of 256 rows x 256 entries, or as many fewer entries as leave the same number of rounds over
+// the pairs; up to 128 rows tiles of 256 entries x the rows. Entries as the tall side against rows, us:
+// one row, 32768 entries of 512 channels 11.6 / 17.8; 17 rows of 1024 channels 20.5 / 25.9; 64 20.4 / 20.8.
+// Boxes whose rows begin between two 32-byte sectors (rows of an odd number of 16 bytes) are loaded at about
+// half the rate: forward calls of many rows copy such hidden rows and weights to rows padded to kCopyPad
+// channels (776 channels, 2077 rows and 50021 entries 159 us without, 135 with; 1024 rows and 32768
+// entries 54 and 58). The backward's copy of the hidden rows is padded anyway; copying the weights too gained
+// and lost up to 6% there.
+constexpr int kCopyPad = 64, kCopyRows = 1536;
+bool copies_rows(const fat_linear_ce_shape_t *s) { return s->dim % 16 && s->rows >= kCopyRows; }
+int copy_pitch(const fat_linear_ce_shape_t *s) { return ceil_div(s->dim, kCopyPad) * kCopyPad; }
 
 struct FwdPlan {
-  int bn, tiles;
-  size_t zt, bytes;
+  bool few;
+  int bn, row_tiles, col_tiles, parts;
+  size_t zt, hidden, weight, bytes;  // hidden, weight: their copies, of calls that make them
 };
 FwdPlan forward_plan(const fat_linear_ce_shape_t *s, int pairs) {
-  FwdPlan f;
-  f.bn = forward_columns(s, pairs);
-  f.tiles = ceil_div(s->vocab, f.bn);
-  f.zt = round256((size_t)f.tiles * s->rows * 8);
-  f.bytes = f.zt + (size_t)s->rows * 4;
+  FwdPlan f{};
+  f.few = s->rows <= kFewHeadRows;
+  if (f.few) {
+    f.bn = ceil_div(s->rows, 16) * 16;
+    f.row_tiles = ceil_div(s->vocab, kTile);
+    f.col_tiles = 1;
+  } else {
+    const long long rt = f.row_tiles = ceil_div(s->rows, kTile);
+    const long long rounds = ceil_div(rt * ceil_div(s->vocab, kTile), pairs);
+    f.bn = kTile;
+    while (f.bn > 32 && rt * ceil_div(s->vocab, f.bn - 16) <= rounds * pairs) f.bn -= 16;
+    f.col_tiles = ceil_div(s->vocab, f.bn);
+  }
+  f.parts = 2 * f.row_tiles * f.col_tiles / (f.few ? 1 : f.row_tiles);
+  f.zt = round256((size_t)f.parts * s->rows * 8);
+  f.bytes = f.hidden = f.weight = f.zt + round256((size_t)s->rows * 4);
+  if (copies_rows(s)) {
+    f.weight = f.hidden + round256((size_t)s->rows * copy_pitch(s) * 2);
+    f.bytes = f.weight + (size_t)s->vocab * copy_pitch(s) * 2;
+  }
   return f;
 }
 
@@ -687,6 +842,7 @@ struct BwdPlan {
   int block, blocks;     // rows of a block (a multiple of 256) and their number
   int piece, pieces;     // vocabulary entries of a piece (a multiple of 256), pieces of a block
   int splits, split_kb;  // of the vocabulary in dh
+  int pitch;             // channels from row to row of the copy of the hidden rows
   bool dx_parts;         // dh goes through fp32 partials
   bool dw_parts;         // and dw
   size_t rec, copy, p[2], dx, dw, bytes;
@@ -719,13 +875,74 @@ BwdPlan backward_plan(const fat_linear_ce_shape_t *s, int pairs) {
     return here;
   };
   b.rec = take((size_t)b.block * b.blocks * 16);
-  b.copy = take((size_t)s->rows * s->dim * 2);
+  b.pitch = copy_pitch(s);
+  b.copy = take((size_t)s->rows * b.pitch * 2);
   const int buffers = b.pieces * b.blocks > 1 ? 2 : 1;
   for (int i = 0; i < 2; ++i) b.p[i] = i < buffers ? take((size_t)b.block * b.piece * 2) : b.p[0];
   if (b.dx_parts) b.dx = take((size_t)b.splits * b.block * s->dim * 4);
   if (b.dw_parts) b.dw = take((size_t)s->vocab * s->dim * 4);
   b.bytes = at;
   return b;
+}
+
+// The pairs of a launch and their shares of the next piece's logits: what each one's turns at the products'
+// tiles cost is filled up to one level.
+void share_tiles(HeadParams &p, int pairs) {
+  const int longs = p.n_dw + p.n_dx;
+  p.pairs = std::max(1, std::min(pairs, longs + p.n_prob));
+  p.dx_first = p.dx_kb > p.r_kb;
+  const int per = (p.dim + 63) / 64;  // k blocks of a logits tile
+  int load[kMaxPairs] = {0}, most = 0;
+  const int first = p.dx_first ? p.n_dx : p.n_dw;
+  for (int i = 0, j = 0; j < longs; ++i)
+    for (int at = 0; at < p.pairs && j < longs; ++at, ++j) {
+      const int cost = (j < first) == (p.dx_first != 0) ? p.dx_kb : p.r_kb;
+      int &l = load[i & 1 ? p.pairs - 1 - at : at];
+      l += cost;
+      most = std::max(most, l);
+    }
+  auto room = [&](int level, int q) { return level > load[q] ? (level - load[q]) / per : 0; };
+  auto total = [&](int level) {
+    int n = 0;
+    for (int q = 0; q < p.pairs; ++q) n += room(level, q);
+    return n;
+  };
+  // the lowest level up to which all tiles fit; what is too many is left out of pairs that reach it exactly
+  int lo = 0, hi = most + per * (p.n_prob / p.pairs + 1);
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (total(mid) >= p.n_prob)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  int over = total(lo) - p.n_prob, at = 0;
+  for (int q = 0; q < p.pairs; ++q) {
+    p.prob_first[q] = (uint16_t)at;
+    int n = room(lo, q);
+    if (over > 0 && n > room(lo - 1, q)) {
+      --n;
+      --over;
+    }
+    at += n;
+  }
+  p.prob_first[p.pairs] = (uint16_t)p.n_prob;
+}
+
+// Rows of an odd number of 16 bytes to the workspace, and where they are from there on.
+int copy_rows(const fat_linear_ce_shape_t *s, const void **rows, long long *stride, long long n, void *to,
+              cudaStream_t stream) {
+  if (*stride % 16 == 0) return FAT_OK;
+  const int pitch = copy_pitch(s);
+  const long long all = n * (s->dim / 8);
+  const int blocks = (int)std::min<long long>((all + 255) / 256, 16ll * std::max(sm_count(), 1));
+  const int rc = launch_dependent("linear cross-entropy copy launch", fat_head_copy_kernel,
+                                  dim3((unsigned)blocks), 256, 0, stream,
+                                  static_cast<const uint4 *>(*rows), *stride / 8, all, s->dim / 8, pitch / 8,
+                                  static_cast<uint4 *>(to));
+  *rows = to;
+  *stride = pitch;
+  return rc;
 }
 
 struct Span {
@@ -787,31 +1004,44 @@ int fat_linear_cross_entropy_fwd(const fat_linear_ce_shape_t *s, const void *hid
   p.scale = s->logit_scale;
   p.sl2 = s->logit_scale * kLog2e;
   p.bn = f.bn;
-  p.row_tiles = ceil_div(s->rows, kTile);
-  p.col_tiles = f.tiles;
+  p.row_tiles = f.row_tiles;
+  p.col_tiles = f.col_tiles;
   // row tiles that walk the vocabulary together: their hidden rows stay in L2 (32 MB)
-  p.row_group = std::max(1, std::min<int>(p.row_tiles, (int)((32ll << 20) / (512ll * s->dim))));
-  const int tiles = p.row_tiles * p.col_tiles;
-  p.pairs = std::min(pairs, tiles);
+  p.row_group = f.few ? f.row_tiles
+                      : std::max(1, std::min<int>(p.row_tiles, (int)((32ll << 20) / (512ll * s->dim))));
+  p.pairs = std::min(pairs, p.row_tiles * p.col_tiles);
   p.part = static_cast<float2 *>(workspace);
   p.zt = reinterpret_cast<float *>(static_cast<char *>(workspace) + f.zt);
   p.target = target;
-  CUtensorMap mx, mw;
-  if (make_tmap_matrix(&mx, hidden, s->rows, s->dim, s->hidden_stride, 64, false) ||
-      make_tmap_matrix(&mw, weight, s->vocab, s->dim, s->weight_stride, f.bn / 2, false))
-    return FAT_ECUDA;
+  p.stage_bytes = kHalf + (f.bn / 2 * 128 + 1023) / 1024 * 1024;
+  p.stages = std::min<int>(HeadCfg<kFew>::STAGES, HeadCfg<kFew>::OFF_BUF / p.stage_bytes);
+  const int half = f.bn / 2;
   const cudaStream_t stream = static_cast<cudaStream_t>(s->stream);
-  rc = launch_dependent("linear cross-entropy launch", fat_head_kernel<false>,
-                        dim3((unsigned)(2 * p.pairs)), kThreads, kSmem, stream, mx, mw, mx, mx, mx, mx,
-                        p);
+  long long hidden_stride = s->hidden_stride, weight_stride = s->weight_stride;
+  if (copies_rows(s)) {
+    char *ws = static_cast<char *>(workspace);
+    rc = copy_rows(s, &hidden, &hidden_stride, s->rows, ws + f.hidden, stream);
+    if (!rc) rc = copy_rows(s, &weight, &weight_stride, s->vocab, ws + f.weight, stream);
+    if (rc) return rc;
+  }
+  CUtensorMap mx, mw;
+  if (make_tmap_matrix(&mx, hidden, s->rows, s->dim, hidden_stride, f.few ? half : 128, false) ||
+      make_tmap_matrix(&mw, weight, s->vocab, s->dim, weight_stride, f.few ? 128 : half, false))
+    return FAT_ECUDA;
+  const dim3 grid((unsigned)(2 * p.pairs));
+  rc = f.few ? launch_dependent("linear cross-entropy launch", fat_head_kernel<kFew>, grid, kThreads,
+                                HeadCfg<kFew>::SMEM, stream, mx, mw, mx, mx, mx, mx, p)
+             : launch_dependent("linear cross-entropy launch", fat_head_kernel<kForward>, grid, kThreads,
+                                HeadCfg<kForward>::SMEM, stream, mx, mw, mx, mx, mx, mx, p);
   if (rc) return rc;
-  if (s->rows < 256)
-    return launch_dependent("linear cross-entropy merge launch", fat_head_merge_kernel<4>,
-                            dim3((unsigned)ceil_div(s->rows, 4)), 256, 0, stream, p.part, p.zt, target,
-                            p.rows, f.tiles, p.vocab, s->z_loss, loss, lse, p.err);
-  return launch_dependent("linear cross-entropy merge launch", fat_head_merge_kernel<32>,
-                          dim3((unsigned)ceil_div(s->rows, 32)), 256, 0, stream, p.part, p.zt, target,
-                          p.rows, f.tiles, p.vocab, s->z_loss, loss, lse, p.err);
+  // a row's statistics over as many threads as keep the SMs busy
+  const auto merge = s->rows < 1024   ? fat_head_merge_kernel<4>
+                     : s->rows < 8192 ? fat_head_merge_kernel<8>
+                                      : fat_head_merge_kernel<32>;
+  const int rb = s->rows < 1024 ? 4 : s->rows < 8192 ? 8 : 32;
+  return launch_dependent("linear cross-entropy merge launch", merge, dim3((unsigned)ceil_div(s->rows, rb)),
+                          256, 0, stream, p.part, p.zt, target, p.rows, f.parts, p.vocab, s->z_loss, loss,
+                          lse, p.err);
 }
 
 int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *s, const void *hidden,
@@ -865,7 +1095,7 @@ int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *s, const void *hid
                         dim3((unsigned)(padded / 8)), 256, 0, stream,
                         static_cast<const uint4 *>(hidden), (long long)(s->hidden_stride / 8), target,
                         lse, dloss, grad_scale, s->logit_scale, s->z_loss, s->rows, padded, s->vocab,
-                        s->dim / 8, static_cast<uint4 *>(copy), rec, p.err);
+                        s->dim / 8, b.pitch / 8, static_cast<uint4 *>(copy), rec, p.err);
   if (rc) return rc;
   p.rows = s->rows;
   p.vocab = s->vocab;
@@ -874,7 +1104,7 @@ int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *s, const void *hid
   p.rec = rec;
   p.d_tiles = ceil_div(s->dim, kTile);
   CUtensorMap mx, mw, mp[2], mps[2], mdx{}, mdw{};
-  if (make_tmap_matrix(&mx, copy, s->rows, s->dim, s->dim, 64, false) ||
+  if (make_tmap_matrix(&mx, copy, s->rows, s->dim, b.pitch, 64, false) ||
       make_tmap_matrix(&mw, weight, s->vocab, s->dim, s->weight_stride, 64, false))
     return FAT_ECUDA;
   for (int i = 0; i < 2; ++i)
@@ -921,10 +1151,10 @@ int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *s, const void *hid
       p.prow_tiles = ceil_div(block_rows(ni), kTile);
       p.n_prob = p.prow_tiles * ceil_div(piece_vocab(nc), kTile);
     }
-    p.pairs = std::max(1, std::min(pairs, p.n_dw + p.n_dx + p.n_prob));
-    rc = launch_dependent("linear cross-entropy backward launch", fat_head_kernel<true>,
-                          dim3((unsigned)(2 * p.pairs)), kThreads, kSmem, stream, mx, mw, mp[q & 1],
-                          mps[(q + 1) & 1], mdx, mdw, p);
+    share_tiles(p, pairs);
+    rc = launch_dependent("linear cross-entropy backward launch", fat_head_kernel<kBackward>,
+                          dim3((unsigned)(2 * p.pairs)), kThreads, HeadCfg<kBackward>::SMEM, stream, mx, mw,
+                          mp[q & 1], mps[(q + 1) & 1], mdx, mdw, p);
     if (rc) return rc;
     if (q >= 0 && c == b.pieces - 1 && dhidden && b.dx_parts) {
       const long long n8 = (long long)block_rows(i) * s->dim / 8;
