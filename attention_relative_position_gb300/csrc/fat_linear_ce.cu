@@ -332,7 +332,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{abort_flag, p.err, MODE == kBackward ? FAT_DEVERR_TIMEOUT_BWD : FAT_DEVERR_TIMEOUT_FWD,
                     p.timeout_ns};
-  grid_dep_launch();
   grid_dep_wait();
 
   if (warp == kWarpProd) {
@@ -643,6 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  grid_dep_launch();
   cluster_sync();
   if (warp == kWarpMma) {
     tc_fence_after();

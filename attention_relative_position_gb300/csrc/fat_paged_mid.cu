@@ -33,8 +33,9 @@ static_assert(kRegsNeeded <= kThreads * ((65536 / kThreads) & ~7), "register spl
 constexpr int kSoftWarps = 8, kWarpK = 8, kWarpMma = 9, kWarpV = 10;
 constexpr int kMinShare = 2;  // key tiles a CTA takes at least
 constexpr int kItemCost = 2;  // cost of an item beside its key tiles
-constexpr float kNoRow = 3e38f;     // reference of a row without a token: its weights are 0
-constexpr float kFreshRow = -1e30f; // of a row that has seen no key
+constexpr float kNoRow = 3e38f;      // reference of a row without a token: its weights are 0
+constexpr float kFreshRow = -3e38f;  // of a row that has seen no key: whatever it sees calls for a new one
+constexpr float kSeen = -2.9e38f;    // logits above this count as seen (biases down to -2e38, times log2 e)
 
 template <int D, int R>
 struct MidCfg {
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float mx = max_s[t];
 #pragma unroll
                 for (int i = 1; i < 8; ++i) mx = fmaxf(mx, max_s[i * RW + t]);
-                set_ref(mx > -1e30f ? mx : mx != mx ? 0.f : kFreshRow);  // (a NaN shows in the sum)
+                set_ref(mx > kSeen ? mx : mx != mx ? 0.f : kFreshRow);  // (a NaN shows in the sum)
               }
               named_bar_sync(bar, 128);
             }
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool raise = bar_any(bar, top > 32.f);
             if (raise) {
               // The rows' maxima over the tile, and new references where they passed 2^32. A row that has seen
-              // no key has a reference of -1e30, which loses the logit: its maximum is taken anew, from 0.
+              // no key has a reference of -3e38, which loses the logit: its maximum is taken anew, from 0.
               bool fresh = false;
               if (t < RW) {
                 fresh = ref_s[t] == kFreshRow;
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float f = 1.f;
                 if (t < mine) {
                   if (fresh) {
-                    if (!(mx != mx)) set_ref(mx > -1e30f ? mx : kFreshRow);  // (a NaN shows in the sum)
+                    if (!(mx != mx)) set_ref(mx > kSeen ? mx : kFreshRow);  // (a NaN shows in the sum)
                   } else if (mx > 32.f) {
                     f = ex2(-mx);
                     set_ref(ref_s[t] + mx);

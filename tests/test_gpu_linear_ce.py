@@ -59,7 +59,8 @@ def _check_fwd(h, w, t, z_loss=0.0, scale=1.0, bits=0, **kw):
 
 SHAPES = [(1, 1, 8), (1, 300, 64), (2, 16, 16), (3, 17, 72), (37, 5000, 768), (255, 257, 64),
           (256, 256, 128), (257, 513, 136), (300, 2000, 520), (5, 40001, 64), (1, 131072, 64),
-          (129, 20000, 1032), (700, 1025, 2048), (2500, 3001, 192)]
+          (129, 20000, 1032), (700, 1025, 2048), (2500, 3001, 192), (8, 127, 64), (9, 128, 64), (16, 129, 64),
+          (17, 511, 64), (64, 513, 1032), (128, 3000, 264), (1537, 700, 200), (2000, 300, 24)]
 
 
 @pytest.mark.parametrize("rows,vocab,dim", SHAPES)
@@ -108,6 +109,21 @@ def test_pieces(rows, vocab, dim):
     h, w, t = _inputs(rows, vocab, dim, ignored=0.1)
     _check_fwd(h, w, t, z_loss=1e-4)
     _check_bwd(h, w, t, z_loss=1e-4, grad_scale=1.0 / rows)
+
+
+def test_odd_rows_with_other_strides():
+    """Many rows of an odd number of 16 bytes: rows a stride apart that needs no copy, and one that does."""
+    for pad in (8, 16):
+        h = torch.randn(1600, 72 + pad, device=DEV).to(torch.bfloat16)[:, :72]
+        w = (0.2 * torch.randn(500, 72 + pad, device=DEV)).to(torch.bfloat16)[:, :72]
+        t = torch.randint(0, 500, (1600,), device=DEV).to(torch.int32)
+        _check_fwd(h, w, t)
+        _check_bwd(h, w, t)
+    # an even number of them, rows an odd number apart
+    h = torch.randn(1600, 72, device=DEV).to(torch.bfloat16)[:, :64]
+    w = (0.2 * torch.randn(500, 72, device=DEV)).to(torch.bfloat16)[:, :64]
+    _check_fwd(h, w, t)
+    _check_bwd(h, w, t)
 
 
 def test_strided_rows():
@@ -257,3 +273,118 @@ def test_on_a_given_stream():
         g2 = fa.fat_linear_cross_entropy_bwd(h, w, t, e2, stream=s)
     s.synchronize()
     assert torch.equal(l2, loss) and torch.equal(g2[0], dh) and torch.equal(g2[1], dw)
+
+
+@pytest.mark.parametrize("rows,vocab,dim", [(1, 3000, 64), (128, 500, 72), (300, 700, 136), (1600, 520, 72),
+                                            (17000, 5000, 40)])
+def test_workspace_of_the_given_size(rows, vocab, dim):
+    """Nothing is written behind the bytes that the size names, and what they held does not matter."""
+    h, w, t = _inputs(rows, vocab, dim, ignored=0.1)
+    loss, lse = fa.fat_linear_cross_entropy_fwd(h, w, t)
+    want = (loss, lse, *fa.fat_linear_cross_entropy_bwd(h, w, t, lse))
+    for fill in (0xff, 0x7f):
+        ws = [torch.full((fa.fat_linear_cross_entropy_workspace_size(rows, vocab, dim, backward=b) + 4096,),
+                         fill, dtype=torch.uint8, device=DEV) for b in (False, True)]
+        got = (*fa.fat_linear_cross_entropy_fwd(h, w, t, workspace=ws[0][:-4096]),
+               *fa.fat_linear_cross_entropy_bwd(h, w, t, lse, workspace=ws[1][:-4096]))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        assert all((x[-4096:] == fill).all() for x in ws) and _errors() == 0
+        for b in (False, True):  # a byte less is refused
+            with pytest.raises(fa.FatAttnError):
+                if b:
+                    fa.fat_linear_cross_entropy_bwd(h, w, t, lse, workspace=ws[1][:-4097])
+                else:
+                    fa.fat_linear_cross_entropy_fwd(h, w, t, workspace=ws[0][:-4097])
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_watchdog(rows):
+    """No copies are issued: the waits run out, the status says so, and the next call is right."""
+    h, w, t = _inputs(rows, 900, 128)
+    _, lse = fa.fat_linear_cross_entropy_fwd(h, w, t)
+    try:
+        fa.fat_attn_debug_set_watchdog(50_000_000, 1)
+        fa.fat_linear_cross_entropy_fwd(h, w, t)
+        assert _errors() == fa.FAT_DEVERR_TIMEOUT_FWD
+        fa.fat_linear_cross_entropy_bwd(h, w, t, lse)
+        assert _errors() == fa.FAT_DEVERR_TIMEOUT_BWD
+    finally:
+        fa.fat_attn_debug_set_watchdog(0, 0)
+    _check_fwd(h, w, t)
+    _check_bwd(h, w, t)
+
+
+def test_two_calls_at_once():
+    sets = [_inputs(700, 4000, 264, seed=s) for s in (1, 2)]
+    want = []
+    for h, w, t in sets:
+        loss, lse = fa.fat_linear_cross_entropy_fwd(h, w, t)
+        want.append((loss, lse, *fa.fat_linear_cross_entropy_bwd(h, w, t, lse)))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        got = []
+        for (h, w, t), s in zip(sets, streams):
+            loss, lse = fa.fat_linear_cross_entropy_fwd(h, w, t, stream=s)
+            got.append((loss, lse, *fa.fat_linear_cross_entropy_bwd(h, w, t, lse, stream=s)))
+        torch.cuda.synchronize()
+        for g, x in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, x))
+
+
+def test_arguments_are_checked():
+    h, w, t = _inputs(20, 300, 64)
+    loss, lse = fa.fat_linear_cross_entropy_fwd(h, w, t)
+    f, b = fa.fat_linear_cross_entropy_fwd, fa.fat_linear_cross_entropy_bwd
+    for call, err in (
+            (lambda: f(h.float(), w, t), TypeError), (lambda: f(h, w.float(), t), TypeError),
+            (lambda: f(h, w, t.long()), TypeError), (lambda: f(h, w, t[:-1]), ValueError),
+            (lambda: f(h, w[:, :56], t), ValueError), (lambda: f(h.cpu(), w, t), ValueError),
+            (lambda: f(h[0], w, t), ValueError), (lambda: f(h[:, ::2], w[:, ::2], t), ValueError),
+            (lambda: f(h, w, t, loss=loss[:-1]), ValueError), (lambda: f(h, w, t, lse=loss.double()), TypeError),
+            (lambda: f(h[:, :60], w[:, :60], t), fa.FatAttnError),
+            (lambda: f(h, w, t, logit_scale=0.0), fa.FatAttnError),
+            (lambda: f(h, w, t, z_loss=-1.0), fa.FatAttnError),
+            (lambda: f(h, w, t, loss=loss, lse=loss), fa.FatAttnError),
+            (lambda: f(h, w, t, lse=h.view(torch.float32).view(-1)[:20]), fa.FatAttnError),
+            (lambda: f(h, w, t, workspace=w.view(torch.uint8).view(-1)), fa.FatAttnError),
+            (lambda: b(h, w, t, lse.double()), TypeError), (lambda: b(h, w, t, lse[:-1]), ValueError),
+            (lambda: b(h, w, t, lse, dloss=lse[:-1]), ValueError),
+            (lambda: b(h, w, t, lse, dhidden=h), fa.FatAttnError),
+            (lambda: b(h, w, t, lse, dweight=w), fa.FatAttnError),
+            (lambda: b(h, w, t, lse, dweight=w.float()), TypeError),
+            (lambda: b(h, w, t, lse, dhidden=torch.empty_like(h)[:, :32]), ValueError),
+            (lambda: b(h, w, t, lse, want_dhidden=False, dhidden=torch.empty_like(h)), ValueError)):
+        with pytest.raises(err):
+            call()
+    assert _errors() == 0
+
+
+def test_large_vocabulary_times_channels():
+    """Weights and their gradient beyond 2^31 elements."""
+    rows, vocab, dim = 130, 1100000, 2048
+    g = torch.Generator(device=DEV).manual_seed(4)
+    h = torch.randn(rows, dim, generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.empty(vocab, dim, dtype=torch.bfloat16, device=DEV)
+    for i in range(0, vocab, 100000):
+        w[i:i + 100000] = 0.04 * torch.randn(100000, dim, generator=g, device=DEV)
+    t = torch.randint(vocab - 1000, vocab, (rows,), generator=g, device=DEV).to(torch.int32)
+    loss, lse = fa.fat_linear_cross_entropy_fwd(h, w, t)
+    few = fa.fat_linear_cross_entropy_fwd(h[:5], w, t[:5])
+    parts = [torch.logsumexp(h.double() @ w[i:i + 100000].double().t(), 1) for i in range(0, vocab, 100000)]
+    want = torch.logsumexp(torch.stack(parts), 0)
+    tol = 2 * _logit_tol(h, w[:2000], 1.0) + 2.0 ** -24 * 4000
+    assert (lse.double() - want).abs().max() <= tol and (few[1].double() - want[:5]).abs().max() <= tol
+    zt = (h.double() * w[t.long()].double()).sum(1)
+    assert (loss.double() - (want - zt)).abs().max() <= 2 * tol
+    dh, dw = fa.fat_linear_cross_entropy_bwd(h, w, t, lse)
+    assert _errors() == 0
+    # rows of the weights' gradient near both ends: each a sum over 130 rows, dz and the result rounded
+    for at in (slice(0, 50), slice(vocab - 1000, vocab)):
+        z = torch.exp(h.double() @ w[at].double().t() - want[:, None])
+        hot = torch.arange(vocab, device=DEV)[at][None] == t[:, None]
+        dz = z - hot.double()
+        x = dz.t() @ h.double()
+        off = (2.0 ** -8 + 1e-3) * (z + hot).t() @ h.double().abs() + 2.0 ** -8 * x.abs()
+        assert ((dw[at].double() - x).abs() <= off).all()

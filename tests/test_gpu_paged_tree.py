@@ -164,6 +164,15 @@ CASES = {
                         words=5),
     "tile_random_d64": dict(lq=[200, 64], ctx=[0, 0], hq=2, hkv=2, d=64, page=16, mask="random",
                             t5=T5B, alibi=True),
+    # requests of as many rows each, more blocks of 128 rows than SMs
+    "many": dict(lq=[140] * 12, ctx=[0, 1, 127, 128, 129, 300, 500, 700, 5, 60, 70, 900], hq=8, hkv=8,
+                 d=64, page=16, t5=T5D, reach=4),
+    "many_d128": dict(lq=[80] * 13, ctx=[0, 1100, 48, 47, 49, 300, 500, 700, 5, 60, 70, 9, 600], hq=16,
+                      hkv=8, d=128, page=64, alibi=True, reach=3),
+    "many_random": dict(lq=[150] * 40, ctx=[0] * 39 + [1200], hq=2, hkv=2, d=64, page=64, mask="random",
+                        t5=T5B),
+    # three tiles of own keys: rows that see nothing in the first tiles taken
+    "random_long": dict(lq=[300, 380, 2], ctx=[0, 0, 200], hq=2, hkv=2, d=128, page=16, mask="random"),
     "mixed": dict(lq=[1, 60, 3, 0, 16, 40], ctx=[2000, 30, 1000, 5, 800, 4000], hq=8, hkv=2, d=64,
                   page=16, t5=T5D),
     "mixed_d128": dict(lq=[1, 50, 4, 1], ctx=[700, 1300, 0, 5000], hq=16, hkv=4, d=128, page=128,
@@ -177,6 +186,47 @@ def test_attention(name):
     out, lse = t.run()
     assert _errors() == 0
     t.check(out, lse)
+
+
+# Logits of hundreds: the first reference of a row is passed by far more than 2^32 in later tiles, again and
+# again, and whole tiles vanish beside others.
+@pytest.mark.parametrize("std", [3.0, 12.0])
+@pytest.mark.parametrize("lq,hq,hkv,d", [([60, 17], 2, 2, 64), ([128], 2, 2, 128), ([30, 32], 8, 4, 128),
+                                         ([5], 6, 2, 128), ([140] * 12, 8, 8, 64)])
+def test_large_logits(std, lq, hq, hkv, d):
+    t = Tree(lq, [1500, 800] + [100] * 10 if len(lq) > 2 else [1500, 800][:len(lq)], hq=hq, hkv=hkv, d=d,
+             page=64, std=std, seed=3, alibi=True)
+    t.check(*t.run())
+
+
+@pytest.mark.parametrize("low", [-float("inf"), float(np.finfo(np.float32).min), -1e38])
+@pytest.mark.parametrize("lq,ctx,hq,hkv,d", [([5, 3], [40, 3], 2, 2, 64), ([40, 20], [700, 9], 2, 1, 64),
+                                             ([61], [300], 4, 2, 128), ([140] * 12, [90] * 12, 8, 8, 64)])
+def test_bias_that_masks(low, lq, ctx, hq, hkv, d):
+    """T5 buckets whose bias is -infinity, the lowest fp32 value, or far below every logit: keys there get no
+    weight beside any other key; a row of such keys alone gets none (or, at -1e38, the softmax of its biases:
+    all equal to fp32, so that every key it sees gets the same weight)."""
+    t = Tree(lq, ctx, hq=hq, hkv=hkv, d=d, page=16, t5=T5D, seed=2)
+    p = t.p
+    p.bias[:, 0] = low            # head 0: every key
+    p.bias[1:9, 1] = low          # head 1: distances 1 to 8
+    out, lse = t.run()
+    assert _errors() == 0
+    p.bias[p.bias < -2e38] = -float("inf")
+    ro, rl, a, s, b = t.oracle()
+    got, gl = _wide(out), lse.double().cpu().numpy()
+    if low < -2e38:
+        assert (gl[0] == -np.inf).all() and (got[:, 0] == 0).all()
+    else:
+        assert (np.abs(gl[0] / low - 1) < 1e-6).all()
+    heads = np.arange(1, p.hq)
+    fin = np.isfinite(p.bias.cpu().numpy()) & (p.bias.cpu().numpy() > -1e37)
+    big = float(np.abs(p.bias.cpu().numpy()[fin]).max())
+    ex = (p.d * s + 4 * (s + big)) * 2.0 ** -24
+    tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2 * ex + 2.0 ** -18) * a * 1.01 + 1e-30
+    assert (np.abs(got - ro)[:, heads] <= tol[:, heads]).all()
+    ok = rl[heads] > -1e37
+    assert (np.abs(gl[heads] - rl[heads])[ok] <= (ex + 2.0 ** -18 + 2.0 ** -22 * np.abs(rl[heads]))[ok]).all()
 
 
 @pytest.mark.parametrize("layout", ["head", "block"])
@@ -263,6 +313,84 @@ def test_captured_and_replayed(name):
         want = out.clone()
         call()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("name", ["few_d128_group4", "tile_group1", "tile_group4", "many"])
+def test_watchdog(name):
+    """No copies are issued: the waits run out, the status says so, and the next call is right."""
+    t = Tree(seed=33, **CASES[name])
+    try:
+        fa.fat_attn_debug_set_watchdog(50_000_000, 1)
+        t.run()
+        assert _errors() == fa.FAT_DEVERR_TIMEOUT_FWD
+    finally:
+        fa.fat_attn_debug_set_watchdog(0, 0)
+    t.check(*t.run())
+    assert _errors() == 0
+
+
+@pytest.mark.parametrize("name", ["few_d128_group4", "tile_group4", "tile_large", "many", "mixed_d128"])
+def test_workspace_of_the_given_size(name):
+    """Nothing is written behind the bytes that the size names, whatever they held."""
+    t = Tree(seed=12, **CASES[name])
+    p = t.p
+    size = fa.fat_paged_attn_workspace_size(p.q, p.kc, _i32(p.cu), t.most, 2000)
+    buf = torch.full((size + 4096,), 0xff, dtype=torch.uint8, device=DEV)
+    k = int(max(p.lk))
+    t.check(*t.run(max_k=max(2000, k), workspace=buf[:size] if k <= 2000 else None))
+    assert (buf[size:] == 0xff).all() and _errors() == 0
+
+
+@pytest.mark.parametrize("name", ["few_d128_group4", "tile_group4", "tile_group1", "many"])
+@pytest.mark.parametrize("bad", [-1, 1 << 20])
+def test_bad_page_counts_as_zeros(name, bad):
+    t = Tree(seed=14, **CASES[name])
+    p = t.p
+    i = int(np.argmax(p.lk))
+    p.table[i, 0] = bad
+    out, lse = t.run()
+    assert _errors() == fa.FAT_DEVERR_PAGES
+    t.check(out, lse)
+
+
+@pytest.mark.parametrize("name", ["few_page_edges", "tile_group1", "tile_group4", "many"])
+def test_nan_shows_in_its_rows(name):
+    t = Tree(seed=15, **CASES[name])
+    p = t.p
+    clean, clean_lse = t.run()
+    p.q[2, 0] = float("nan")
+    out, lse = t.run()
+    assert torch.isnan(out[2, 0]).all() and torch.isnan(lse[0, 2])
+    keep = torch.ones_like(lse, dtype=torch.bool)
+    keep[0, 2] = False
+    # (the others: as before, but for what rows that share a vote do together)
+    t.p.q[2, 0] = 0
+    ro, rl, a, s, b = t.oracle()
+    assert torch.isfinite(out.transpose(0, 1)[keep]).all()
+    ex = (p.d * s + 4 * (s + b)) * 2.0 ** -24
+    off = (lse[:, :p.total].double().cpu() - torch.from_numpy(rl)).abs()[keep[:, :p.total].cpu()]
+    assert (off <= ex + 2.0 ** -18 + 2.0 ** -22 * np.abs(rl).max()).all()
+
+
+def test_two_calls_at_once():
+    a, b = Tree(seed=16, **CASES["tile_group4"]), Tree(seed=17, **CASES["mixed"])
+    want = [x.run() for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    args = [dict(arrays=x.p.arrays(), positions=_i32(x.pos), mask=_i32(x.mask)) for x in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [x.run(stream=s, **k) for x, s, k in zip((a, b), streams, args)]
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_requests_share_pages():
+    """The same context pages under two trees."""
+    t = Tree([20, 20], [256, 256], hq=4, hkv=2, d=64, page=64, seed=18)
+    p = t.p
+    p.table[1, :4] = p.table[0, :4]
+    t.check(*t.run())
 
 
 def test_arguments_are_checked():
