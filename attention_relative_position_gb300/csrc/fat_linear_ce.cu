@@ -864,6 +864,9 @@ BwdPlan backward_plan(const fat_linear_ce_shape_t *s, int pairs) {
   const long long share = (dx_tiles * kb + dw_units) / pairs;
   const int longest = (int)std::max<long long>(16, share / 2);
   b.splits = std::max(1, ceil_div(kb, longest));
+  // no more of them than fill their rounds over the pairs
+  const long long rounds = std::max<long long>(1, (2 * dx_tiles * b.splits + pairs) / (2 * pairs));
+  if (b.splits > 1) b.splits = (int)std::max<long long>(1, std::min<long long>(b.splits, rounds * pairs / dx_tiles));
   b.split_kb = ceil_div(kb, b.splits);
   b.splits = ceil_div(kb, b.split_kb);
   b.dx_parts = b.splits > 1 || b.pieces > 1;
