@@ -42,10 +42,15 @@ constexpr int kFewHeadRows = 128;         // forward calls of at most so many ro
 constexpr int kMaxPairs = 128;
 
 // The kernel's forms, and what each has in shared memory.
-enum Mode { kForward, kBackward, kFew };
+enum Mode { kForward, kBackward, kFew, kLong };
+// The tensor cores cut off what a sum loses at every step, towards zero. The loss adds up at most kChunk
+// blocks of 64 channels there, and further ones in fp32 with rounding: kLong is the forward of more
+// channels, whose epilogue keeps a tile's logits in registers (lse against 64 bits, 3808 channels: 1.9e-6
+// without, LONGERR with; 1024 channels 3.5e-7).
+constexpr int kChunk = 16;
 template <int MODE>
 struct HeadCfg {
-  static constexpr int STAGES = MODE == kBackward ? 6 : MODE == kForward ? 6 : 10;  // at most
+  static constexpr int STAGES = MODE == kFew ? 10 : 6;  // at most
   static constexpr int OFF_BUF = MODE == kFew ? 186 * 1024 : STAGES * 2 * kHalf;
   // backward: an output buffer a warp; few rows: targets, and 32 rows of logits a warpgroup
   static constexpr int LD = 132;  // floats from row to row of these
@@ -351,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t bar = in_first(full + slot);
           if (rank == 0) mbar_arrive_expect_tx(full + slot, 2 * (kHalf + bhalf * 128));
           const int m = job.m0 + rank * 128, n = job.n0 + rank * bhalf;
-          if (MODE == kForward) {
+          if (MODE == kForward || MODE == kLong) {
             load_pair(&tm_x, bar, a, k * 64, m);  // boxes of 128 and of bn / 2 rows
             load_pair(&tm_w, bar, b, k * 64, n);
           } else if (MODE == kFew) {
@@ -399,30 +404,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, n = 0;
       bool ok = true;
       Job job;
-      for (int i = 0; ok && job_at<MODE>(p, pair, i, job); ++i, ++n) {
+      for (int i = 0; ok && job_at<MODE>(p, pair, i, job); ++i) {
         const bool a_mn = MODE == kBackward && job.kind == kDw, b_mn = MODE == kBackward && job.kind >= kDx;
         const int cols = MODE != kBackward ? p.bn : b_mn ? d_cols(p, job.n0) : 256;
         const uint32_t idesc = idesc_bf16_f32(256, cols, a_mn ? 1 : 0, b_mn ? 1 : 0);
         const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-        const uint32_t d = tmem + 256 * (n & 1);
-        if (n >= 2 && !(ok = wait_cluster(acc_empty + (n & 1), (n / 2 - 1) & 1, wd))) break;
-        tc_fence_after();
-        for (int k = job.k0; k < job.k1; ++k) {
-          if (!(ok = wait_cluster(full + slot, phase, wd))) break;
+        for (int k0 = job.k0; ok && k0 < job.k1; ++n) {  // an accumulator's share of the reduction
+          const int k1 = MODE == kFew || MODE == kLong ? min(k0 + kChunk, job.k1) : job.k1;
+          const uint32_t d = tmem + 256 * (n & 1);
+          if (n >= 2 && !(ok = wait_cluster(acc_empty + (n & 1), (n / 2 - 1) & 1, wd))) break;
           tc_fence_after();
-          const uint32_t a = smem_u32(sm) + slot * stage_bytes;
-          const uint64_t da = sw128_desc(a, a_mn ? 8192 : 16, 1024);
-          const uint64_t db = sw128_desc(a + kHalf, b_mn ? 8192 : 16, 1024);
+          for (int k = k0; k < k1; ++k) {
+            if (!(ok = wait_cluster(full + slot, phase, wd))) break;
+            tc_fence_after();
+            const uint32_t a = smem_u32(sm) + slot * stage_bytes;
+            const uint64_t da = sw128_desc(a, a_mn ? 8192 : 16, 1024);
+            const uint64_t db = sw128_desc(a + kHalf, b_mn ? 8192 : 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_pair(d, da + kk * a_step, db + kk * b_step, idesc, k > job.k0 || kk > 0);
-          commit_pair(empty + slot);
-          if (++slot == stages) {
-            slot = 0;
-            phase ^= 1;
+            for (int kk = 0; kk < 4; ++kk)
+              mma_pair(d, da + kk * a_step, db + kk * b_step, idesc, k > k0 || kk > 0);
+            commit_pair(empty + slot);
+            if (++slot == stages) {
+              slot = 0;
+              phase ^= 1;
+            }
           }
+          commit_pair(acc_full + (n & 1));
+          k0 = k1;
         }
-        commit_pair(acc_full + (n & 1));
       }
       commit_pair(done, 1);
       mbar_wait_teardown(done, 0, kTeardownNs);
@@ -444,11 +453,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       target_s += half * (kFewHeadRows / 2);
       named_bar_sync(1 + half, 128);
     }
-    uint32_t n = 0;
+    uint32_t n = 0;  // accumulators so far
     bool ok = true;
     Job job;
     for (int i = 0; ok && job_at<MODE>(p, pair, i, job); ++i, ++n) {
-      const uint32_t d = tmem + lane_off + 256 * (n & 1);
+      uint32_t d = tmem + lane_off + 256 * (n & 1);
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -499,23 +508,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
         if (row < p.rows)
           p.part[(size_t)(2 * (job.n0 / p.bn) + half) * p.rows + row] = make_float2(m, s0 + s1);
+      } else if constexpr (MODE == kLong) {
+        // the same with the logits in registers, summed over the accumulators
+        const int row = job.m0 + row_in + lane;
+        const int t = row < p.rows ? __ldg(p.target + row) : -1;
+        const int c0 = 128 * half, lim = min(p.bn, p.vocab - job.n0) - c0;
+        uint64_t z[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) z[c] = 0;
+        for (int k = job.k0;;) {
+          if (!(ok = warp_wait_cluster(acc_full + (n & 1), (n / 2) & 1, wd))) break;
+          tc_fence_after();
+          d = tmem + lane_off + 256 * (n & 1) + c0;
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            if (c >= lim) break;
+            uint32_t x[16];
+            tmem_ld16(d + c, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              z[c / 2 + i] = f2_add(z[c / 2 + i],
+                                    f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])));
+          }
+          release();
+          k += kChunk;
+          if (k >= job.k1) break;
+          ++n;
+        }
+        if (!ok) break;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 2) {
+          float a, b;
+          f2_unpack(z[c / 2], a, b);
+          if (c + 2 > lim) {
+            a = c < lim ? a : -INFINITY;
+            b = -INFINITY;
+            z[c / 2] = f2_pack(a, b);
+          }
+          mx = fmax3(mx, a, b);
+        }
+        const float m = mx * p.sl2, m_use = m == -INFINITY ? 0.f : m;
+        const uint64_t sl = f2_pack(p.sl2, p.sl2), neg = f2_pack(-m_use, -m_use);
+        const int at = t - job.n0 - c0;
+        if (__any_sync(0xffffffffu, at >= 0 && at < 128 && at < lim)) {
+          float zt = 0.f;
+#pragma unroll
+          for (int c = 0; c < 128; c += 2) {
+            float a, b;
+            f2_unpack(z[c / 2], a, b);
+            if (at == c) zt = a;
+            if (at == c + 1) zt = b;
+          }
+          if (at >= 0 && at < 128 && at < lim) p.zt[row] = zt * p.scale;
+        }
+        uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          float a, b;
+          f2_unpack(f2_fma(z[c], sl, neg), a, b);
+          sum[c & 1] = f2_add(sum[c & 1], f2_pack(ex2(a), ex2(b)));
+        }
+        float s0, s1;
+        f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+        if (row < p.rows)
+          p.part[(size_t)(2 * (job.n0 / p.bn) + half) * p.rows + row] = make_float2(m, s0 + s1);
       } else if constexpr (MODE == kFew) {
         // A thread holds a vocabulary entry's logits of this warpgroup's rows, and passes them on through shared
         // memory to the threads that share a row: its statistics over the CTA's 128 entries.
         const int r0 = half * (p.bn >> 1), nr = min(p.rows - r0, p.bn >> 1);
         const int t = tid & 127, v0 = job.m0 + rank * 128;
         const bool in = v0 + t < p.vocab;
-        if (!(ok = warp_wait_cluster(acc_full + (n & 1), (n / 2) & 1, wd))) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < nr; c += 32) {
+        float x[2][32];
+        for (int k = job.k0;;) {
+          if (!(ok = warp_wait_cluster(acc_full + (n & 1), (n / 2) & 1, wd))) break;
+          tc_fence_after();
+          d = tmem + lane_off + 256 * (n & 1) + r0;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (32 * c >= nr) break;
+            uint32_t y[32];
+            tmem_ld32(d + 32 * c, y);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              x[c][i] = k > job.k0 ? x[c][i] + __uint_as_float(y[i]) : __uint_as_float(y[i]);
+          }
+          release();
+          k += kChunk;
+          if (k >= job.k1) break;
+          ++n;
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          if (c >= nr) break;
           const int cnt = min(nr - c, 32);
-          uint32_t x[32];
-          tmem_ld32(d + r0 + c, x);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (i < cnt) rows_s[i * C::LD + t] = in ? __uint_as_float(x[i]) : -INFINITY;
-          if (c + 32 >= nr) release();
+            if (i < cnt) rows_s[i * C::LD + t] = in ? x[c / 32][i] : -INFINITY;
           named_bar_sync(1 + half, 128);
           auto row_stats = [&](auto threads) {  // `threads` of them a row
             constexpr int TR = decltype(threads)::value, N = 128 / TR;
@@ -550,7 +640,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             row_stats(Threads<4>{});
           named_bar_sync(1 + half, 128);
         }
-        if (nr <= 0) release();
       } else {
         float4 rec = make_float4(0.f, 0.f, 0.f, 0.f);
         if (job.kind == kProb) rec = __ldg(p.rec + p.pr0 + job.m0 + row_in + lane);
@@ -788,7 +877,8 @@ bool head_ready() {
 }
 // Pairs of CTAs that run at once (0: no device)
 int head_pairs() {
-  if (!head_ready<kForward>() || !head_ready<kBackward>() || !head_ready<kFew>()) return 0;
+  if (!head_ready<kForward>() || !head_ready<kBackward>() || !head_ready<kFew>() || !head_ready<kLong>())
+    return 0;
   return std::min(kMaxPairs, max_pair_ctas((const void *)fat_head_kernel<kBackward>,
                                            HeadCfg<kBackward>::SMEM, kThreads) / 2);
 }
@@ -1032,10 +1122,10 @@ int fat_linear_cross_entropy_fwd(const fat_linear_ce_shape_t *s, const void *hid
       make_tmap_matrix(&mw, weight, s->vocab, s->dim, weight_stride, f.few ? 128 : half, false))
     return FAT_ECUDA;
   const dim3 grid((unsigned)(2 * p.pairs));
-  rc = f.few ? launch_dependent("linear cross-entropy launch", fat_head_kernel<kFew>, grid, kThreads,
-                                HeadCfg<kFew>::SMEM, stream, mx, mw, mx, mx, mx, mx, p)
-             : launch_dependent("linear cross-entropy launch", fat_head_kernel<kForward>, grid, kThreads,
-                                HeadCfg<kForward>::SMEM, stream, mx, mw, mx, mx, mx, mx, p);
+  const bool more = s->dim > kChunk * 64;
+  const auto kernel = f.few ? fat_head_kernel<kFew> : more ? fat_head_kernel<kLong> : fat_head_kernel<kForward>;
+  rc = launch_dependent("linear cross-entropy launch", kernel, grid, kThreads,
+                        f.few ? HeadCfg<kFew>::SMEM : HeadCfg<kForward>::SMEM, stream, mx, mw, mx, mx, mx, mx, p);
   if (rc) return rc;
   // a row's statistics over as many threads as keep the SMs busy
   const auto merge = s->rows < 1024   ? fat_head_merge_kernel<4>

@@ -413,8 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto o_wait = [&](uint32_t i) { return warp_wait(o_ready + (i & 1), (i / 2) & 1, wd); };
       uint32_t g = 0;
+      int ni = 0;
       bool ok = true;
-      while (ok && walk.next(it)) {
+      for (; ok && walk.next(it); ++ni) {
         const int n = it.j1 - it.j0, rows = it.ntok * G;
         const int mine = min(rows - rb, RW);  // rows of this group (none: it only keeps step)
         if (t < RW && mine > 0) {
@@ -591,8 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               all_logits();
             }
-            // P, once the products that read its place are complete
+            // P, once the products that read its place are complete, and both groups' staged rows of the item
+            // before have left it
             if (gt >= C::PB && !(ok = o_wait(gt - C::PB))) break;
+            if (j == 0 && ni > 0 && !(ok = warp_wait(o_free, (ni - 1) & 1, wd))) break;
             const uint32_t sP = smem_u32(sm + C::OFF_P + (gt % C::PB) * C::PTILE);
 #pragma unroll
             for (int c = 0; c < RW; c += 32) {
