@@ -8,8 +8,10 @@
 // The logits exist only as accumulators in tensor memory. Forward: tiles of 256 rows x up to 256
 // vocabulary entries; the epilogue leaves a tile's maximum and sum of exponentials per row (8 bytes for
 // 256 logits), which a second grid merges. Backward: the vocabulary in pieces; a piece's logits are
-// computed again, their gradient (s folded in) goes to the workspace in bf16, and two products take it
-// from there: dh += dz W and dw = dz^T H. A launch does the products of one piece and the logits of
+// computed again, their gradient goes to the workspace in bf16, and two products take it from there:
+// dh += dz W and dw = dz^T H. dz is kept without grad_scale and s, which scale the results: bf16 holds the
+// large entries, p - 1 at the targets, best when they are next to 1 (with 1 / rows in them all of them
+// round the same way, and so do the results: 251 rows 0.0038 off against 0.0023). A launch does the products of one piece and the logits of
 // the next, so that its last wave is filled with short tiles.
 // Bound by the tensor cores (2, 4 and 2 N V D operations in the three products, 2 in the loss) from some
 // 300 rows on, below that by the read of the weights (and the write of their gradient).
@@ -46,7 +48,7 @@ enum Mode { kForward, kBackward, kFew, kLong };
 // The tensor cores cut off what a sum loses at every step, towards zero. The loss adds up at most kChunk
 // blocks of 64 channels there, and further ones in fp32 with rounding: kLong is the forward of more
 // channels, whose epilogue keeps a tile's logits in registers (lse against 64 bits, 3808 channels: 1.9e-6
-// without, LONGERR with; 1024 channels 3.5e-7).
+// without, 3.5e-7 with; 1024 channels 3.5e-7).
 constexpr int kChunk = 16;
 template <int MODE>
 struct HeadCfg {
@@ -85,6 +87,7 @@ struct HeadParams {
   int v0, r0;
   int dx_add, dw_add;             // add to what the piece before left (fp32)
   int dx_f32, dw_f32;
+  float out_scale;                // of results in bf16
   int dx_rows;                    // rows of a split's partial dh
   int dx_first;                   // dh's tiles take longer than dw's: they come first
   // logits of the next piece: pair q takes tiles prob_first[q] up to prob_first[q + 1] behind the others
@@ -714,8 +717,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   uint32_t w[4];
 #pragma unroll
                   for (int k = 0; k < 4; ++k)
-                    w[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]),
-                                       __uint_as_float(x[8 * i + 2 * k + 1]));
+                    w[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]) * p.out_scale,
+                                       __uint_as_float(x[8 * i + 2 * k + 1]) * p.out_scale);
                   st.put(4 * h + i, w[0], w[1], w[2], w[3]);
                 }
               }
@@ -791,8 +794,7 @@ __global__ void __launch_bounds__(256) fat_head_merge_kernel(const float2 *part,
 // values are 0 in the copy, for 0 * NaN would reach dw.
 __global__ void __launch_bounds__(256)
     fat_head_rows_kernel(const uint4 *hidden, long long stride16, const int32_t *target,
-                         const float *lse, const float *dloss, float grad_scale, float scale, float zc,
-                         int rows, int padded, int vocab, int chunks, int pitch16, uint4 *copy,
+                         const float *lse, const float *dloss, float zc, int rows, int padded, int vocab, int chunks, int pitch16, uint4 *copy,
                          float4 *rec, int *err) {
   grid_dep_launch();
   grid_dep_wait();
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(256)
     if (t >= vocab) atomicOr(err, FAT_DEVERR_INDEX);
     if (counts) {
       const float l = __ldg(lse + row);
-      const float g = grad_scale * scale * (dloss ? __ldg(dloss + row) : 1.f);
+      const float g = dloss ? __ldg(dloss + row) : 1.f;
       r = make_float4(l * kLog2e, g * (1.f + 2.f * zc * l), g, __int_as_float(t));
     }
     rec[row] = r;
@@ -828,9 +830,9 @@ __global__ void __launch_bounds__(256) fat_head_copy_kernel(const uint4 *src, lo
   }
 }
 
-// dst = bf16(sum of the parts), eight values a thread
+// dst = bf16(scale * sum of the parts), eight values a thread
 __global__ void __launch_bounds__(256) fat_head_sum_kernel(const float4 *part, long long n8, int parts,
-                                                           long long part_stride4, uint4 *dst) {
+                                                           long long part_stride4, float scale, uint4 *dst) {
   grid_dep_launch();
   grid_dep_wait();
   const long long i = blockIdx.x * 256ll + threadIdx.x;
@@ -847,8 +849,8 @@ __global__ void __launch_bounds__(256) fat_head_sum_kernel(const float4 *part, l
     b.z += y.z;
     b.w += y.w;
   }
-  dst[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
-                      pack_bf16x2(b.z, b.w));
+  dst[i] = make_uint4(pack_bf16x2(a.x * scale, a.y * scale), pack_bf16x2(a.z * scale, a.w * scale),
+                      pack_bf16x2(b.x * scale, b.y * scale), pack_bf16x2(b.z * scale, b.w * scale));
 }
 
 // ---- host -----------------------------------------------------------------------------------------------
@@ -1187,7 +1189,7 @@ int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *s, const void *hid
   rc = launch_dependent("linear cross-entropy rows launch", fat_head_rows_kernel,
                         dim3((unsigned)(padded / 8)), 256, 0, stream,
                         static_cast<const uint4 *>(hidden), (long long)(s->hidden_stride / 8), target,
-                        lse, dloss, grad_scale, s->logit_scale, s->z_loss, s->rows, padded, s->vocab,
+                        lse, dloss, s->z_loss, s->rows, padded, s->vocab,
                         s->dim / 8, b.pitch / 8, static_cast<uint4 *>(copy), rec, p.err);
   if (rc) return rc;
   p.rows = s->rows;
@@ -1195,6 +1197,7 @@ int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *s, const void *hid
   p.dim = s->dim;
   p.sl2 = s->logit_scale * kLog2e;
   p.rec = rec;
+  p.out_scale = grad_scale * s->logit_scale;
   p.d_tiles = ceil_div(s->dim, kTile);
   CUtensorMap mx, mw, mp[2], mps[2], mdx{}, mdw{};
   if (make_tmap_matrix(&mx, copy, s->rows, s->dim, b.pitch, 64, false) ||
@@ -1255,7 +1258,7 @@ int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *s, const void *hid
       rc = launch_dependent("linear cross-entropy sum launch", fat_head_sum_kernel,
                             dim3((unsigned)ceil_div(n8, 256)), 256, 0, stream,
                             reinterpret_cast<const float4 *>(dx_part), n8, b.splits,
-                            (long long)b.block * s->dim / 4,
+                            (long long)b.block * s->dim / 4, p.out_scale,
                             reinterpret_cast<uint4 *>(dhidden) + (long long)i * b.block * s->dim / 8);
       if (rc) return rc;
     }
@@ -1264,7 +1267,7 @@ int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *s, const void *hid
     const long long n8 = (long long)s->vocab * s->dim / 8;
     rc = launch_dependent("linear cross-entropy sum launch", fat_head_sum_kernel,
                           dim3((unsigned)ceil_div(n8, 256)), 256, 0, stream,
-                          reinterpret_cast<const float4 *>(dw_part), n8, 1, 0ll,
+                          reinterpret_cast<const float4 *>(dw_part), n8, 1, 0ll, p.out_scale,
                           static_cast<uint4 *>(dweight));
     if (rc) return rc;
   }
