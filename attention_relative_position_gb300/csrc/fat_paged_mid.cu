@@ -54,7 +54,7 @@ struct MidCfg {
   static constexpr int PB = 1;                   // buffers of P
   static constexpr int SB = 3;                   // and of S
   static constexpr int PTILE = R / 64 * PBLK;
-  static constexpr int OFF_ROW = OFF_P + PB * PTILE + 1024;  // behind the staged rows
+  static constexpr int OFF_ROW = OFF_P + PB * PTILE;
   // per row: slope; bias of a far key at the first query's position less the reference; minus the reference;
   // the reference; sum or factor; int2: position - shift, head
   static constexpr int OFF_SLOPE = OFF_ROW, OFF_FAR = OFF_SLOPE + R * 4, OFF_NREF = OFF_FAR + R * 4;
@@ -69,9 +69,10 @@ struct MidCfg {
   }
   static_assert((2 * QB + 2 * KS + 2 * VS + 2 * SB + 6) * 8 + 8 <= 320, "barrier block");
   static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
-  static constexpr int LD = 132;  // floats of a staged row of the epilogue (in P's place)
-  static constexpr int SR = R / 4;  // staged rows of a warpgroup
-  static_assert(2 * SR * LD * 4 <= PTILE + 1024, "staged rows");
+  // Rows that a warpgroup stages at a time in P's place, 128 floats each, their quads swizzled. With 128 rows
+  // it is the block of P that only this group writes: the other one's next item may begin meanwhile.
+  static constexpr int SR = R / 4;
+  static_assert(2 * SR * 512 == PTILE, "staged rows");
   static constexpr uint32_t COL_O = SB * R, TMEM_COLS = 4 * R;
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, R, 0, 0);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, R, 1, 1);
@@ -592,10 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               all_logits();
             }
-            // P, once the products that read its place are complete, and both groups' staged rows of the item
-            // before have left it
+            // P, once the products that read its place are complete, and the staged rows of the item before have
+            // left it (64 rows: the other group's share its block)
             if (gt >= C::PB && !(ok = o_wait(gt - C::PB))) break;
-            if (j == 0 && ni > 0 && !(ok = warp_wait(o_free, (ni - 1) & 1, wd))) break;
+            if (R == 64 && j == 0 && ni > 0 && !(ok = warp_wait(o_free, (ni - 1) & 1, wd))) break;
             const uint32_t sP = smem_u32(sm + C::OFF_P + (gt % C::PB) * C::PTILE);
 #pragma unroll
             for (int c = 0; c < RW; c += 32) {
@@ -653,23 +654,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           rec->hk = it.hk;
           rec->rows = rows;
         }
-        constexpr int LD = C::LD;
         constexpr int SR = C::SR;
-        float *stage = reinterpret_cast<float *>(sm + C::OFF_P) + wg * SR * LD;  // [SR][LD]: P has been used
+        float *stage = reinterpret_cast<float *>(sm + C::OFF_P) + wg * SR * 128;  // [SR][128]: P has been used
+        auto staged = [&](int row, int quad) { return stage + row * 128 + ((quad ^ (row & 7)) << 2); };
+        auto mine_of = [&](int row) { return staged(row, t >> 2) + (t & 3); };  // this thread's column
         if (mine > 0) {
 #pragma unroll
           for (int c = 0; c < RW; c += SR) {  // the threads' sums, 128 / SR threads a row
             if (c >= mine) break;
 #pragma unroll
             for (int i = 0; i < SR / 2; ++i)
-              f2_unpack(sum[c / 2 + i], stage[2 * i * LD + t], stage[(2 * i + 1) * LD + t]);
+              f2_unpack(sum[c / 2 + i], *mine_of(2 * i), *mine_of(2 * i + 1));
             named_bar_sync(bar, 128);
             constexpr int TR = 128 / SR;
             float l = 0.f;
 #pragma unroll
             for (int i = 0; i < SR / 4; ++i) {
-              const float4 v =
-                  *reinterpret_cast<const float4 *>(stage + (t / TR) * LD + (t % TR) * 4 + TR * 4 * i);
+              const float4 v = *reinterpret_cast<const float4 *>(staged(t / TR, t % TR + TR * i));
               l += (v.x + v.y) + (v.z + v.w);
             }
 #pragma unroll
@@ -686,15 +687,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld16(tmem + lane_off + C::COL_O + rb + c, x);
             if (t < D)
 #pragma unroll
-              for (int i = 0; i < SR; ++i) stage[i * LD + t] = __uint_as_float(x[i]);
+              for (int i = 0; i < SR; ++i) *mine_of(i) = __uint_as_float(x[i]);
             named_bar_sync(bar, 128);
             const int left = min(SR, mine - c);
             if (whole) {
               for (int i = t; i < left * (D / 8); i += 128) {
                 const int rr = i / (D / 8), ch = (i % (D / 8)) * 8, h = int_s[c + rr].y;
                 const float l = fac_s[c + rr], inv = l == 0.f ? 0.f : 1.0f / l;
-                const float4 a = *reinterpret_cast<const float4 *>(stage + rr * LD + ch);
-                const float4 b = *reinterpret_cast<const float4 *>(stage + rr * LD + ch + 4);
+                const float4 a = *reinterpret_cast<const float4 *>(staged(rr, ch / 4));
+                const float4 b = *reinterpret_cast<const float4 *>(staged(rr, ch / 4 + 1));
                 const size_t row = (size_t)it.row0 + (rb + c + rr) / G;
                 *reinterpret_cast<uint4 *>(p.out + (row * p.hq + h) * D + ch) =
                     make_uint4(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv),
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int rr = i % SR, c4 = i / SR;
                 if (rr < left)
                   *part_quad<R>(po, rb + c + rr, c4) =
-                      *reinterpret_cast<const float4 *>(stage + rr * LD + 4 * c4);
+                      *reinterpret_cast<const float4 *>(staged(rr, c4));
               }
               if (t < left) {
                 const float l = fac_s[c + t];
