@@ -166,7 +166,9 @@ struct PartRecord {
   int row0;    // first row of q and out of the item's block (token), and its key/value head
   int hk;
   int rows;    // packed rows (token-major, the group's heads inside)
-  int pad[3];
+  int pos;     // tree kernel: which part of how many
+  int parts;
+  int pad;
 };
 __host__ __device__ inline size_t part_records_floats(int ctas) {
   return (size_t)ctas * 2 * sizeof(PartRecord) / 4;

@@ -29,27 +29,15 @@ constexpr int kMergeBatch = 4;  // parts whose loads a lane has in flight
 constexpr int kMergeCh = 8;
 constexpr int kTileBlocks = 8, kFewBlocks = 2;
 
+// The chain of n parts that begins in CTA c, by block y of the ny that share it.
 template <int ROWS, int D>
-__device__ __forceinline__ void merge_chain(const PagedParams &p, float *part, int ctas, int c,
-                                            int y, int ny, float (*sum_s)[kMergeCh + 2][32]) {
+__device__ __forceinline__ void merge_parts(const PagedParams &p, float *part, int ctas, int c, int n,
+                                            const PartRecord &rec, int y, int ny,
+                                            float (*sum_s)[kMergeCh + 2][32]) {
   constexpr int RL = ROWS < 32 ? ROWS : 32;        // rows side by side in a warp
   constexpr int CH = kMergeCh;                     // channels per lane
   constexpr int RG = ROWS / RL, CG = D / CH / (32 / RL);  // tasks: row groups x channel groups
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const PartRecord rec = *part_record(part, c, 1);
-  // parts 1 .. n - 1 lie in CTAs c + 1 .. c + n - 1 (the first records are loaded beside rec)
-  int n = 1;
-  for (int i0 = 1;; i0 += 32) {
-    const int i = c + i0 + lane;
-    int2 next = make_int2(0, 0);  // valid, ends
-    if (i < ctas) next = *reinterpret_cast<const int2 *>(part_record(part, i, 0));
-    if (!rec.valid) return;
-    const unsigned end = __ballot_sync(0xffffffffu, !next.x || next.y);
-    if (end) {
-      n = min(i0 + __ffs(end), ctas - c);
-      break;
-    }
-  }
   const bool shared = n > kLongChain;
   const int first = shared ? y : y * kMergeWarps + w;
   const int step = shared ? ny : ny * kMergeWarps;
@@ -124,6 +112,27 @@ __device__ __forceinline__ void merge_chain(const PagedParams &p, float *part, i
   }
 }
 
+template <int ROWS, int D>
+__device__ __forceinline__ void merge_chain(const PagedParams &p, float *part, int ctas, int c,
+                                            int y, int ny, float (*sum_s)[kMergeCh + 2][32]) {
+  const int lane = threadIdx.x & 31;
+  const PartRecord rec = *part_record(part, c, 1);
+  // parts 1 .. n - 1 lie in CTAs c + 1 .. c + n - 1 (the first records are loaded beside rec)
+  int n = 1;
+  for (int i0 = 1;; i0 += 32) {
+    const int i = c + i0 + lane;
+    int2 next = make_int2(0, 0);  // valid, ends
+    if (i < ctas) next = *reinterpret_cast<const int2 *>(part_record(part, i, 0));
+    if (!rec.valid) return;
+    const unsigned end = __ballot_sync(0xffffffffu, !next.x || next.y);
+    if (end) {
+      n = min(i0 + __ffs(end), ctas - c);
+      break;
+    }
+  }
+  merge_parts<ROWS, D>(p, part, ctas, c, n, rec, y, ny, sum_s);
+}
+
 // Blocks [0, tile_ctas * kTileBlocks) merge the tile kernel's items, the others the few-row kernel's.
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32, 4)
@@ -151,7 +160,10 @@ int launch_merge(const PagedParams &p, float *tile_part, int tile_ctas, float *f
                           kMergeWarps * 32, 0, stream, p, tile_part, tile_ctas, few_part, few_ctas);
 }
 
-// The same for the tree kernel's items alone.
+// The same for the tree kernel's items alone, whose records say which part of how many they are: the blocks of
+// all of a chain's CTAs share its tasks, so that a chain over most of the grid has a block for each (one
+// request over 8000 keys, 16 heads over 4 of 128: 12 tokens 17 us, with the first CTA's blocks alone 45; 30
+// tokens 21 / 55).
 template <int ROWS, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     fat_paged_tree_merge_kernel(const __grid_constant__ PagedParams p) {
@@ -159,7 +171,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
   constexpr int kBlocks = ROWS / 32;
   grid_dep_launch();
   grid_dep_wait();
-  merge_chain<ROWS, D>(p, p.part, p.sms, blockIdx.x / kBlocks, blockIdx.x % kBlocks, kBlocks, sum_s);
+  const int cta = blockIdx.x / kBlocks, y = blockIdx.x % kBlocks;
+  const PartRecord rec[2] = {*part_record(p.part, cta, 0), *part_record(p.part, cta, 1)};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!rec[i].valid) continue;
+    // (a part of n >= 1 in the grid, by the line's arithmetic; a record that is none is passed over)
+    const int pos = rec[i].pos, n = rec[i].parts, c = cta - pos;
+    if (pos < 0 || pos >= n || c < 0 || n > p.sms - c) continue;
+    merge_parts<ROWS, D>(p, p.part, p.sms, c, n, rec[i], pos * kBlocks + y, n * kBlocks, sum_s);
+  }
 }
 template <int D>
 int launch_tree_merge(const PagedParams &p, int rows, cudaStream_t stream) {
@@ -215,9 +236,9 @@ size_t workspace_bound(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) 
 // for more than 128 rows a request (the tree kernel reads keys again for every 128, the tile kernel for every
 // 256), where every request has as many (else the few-row kernel's launch and its share of the SMs come on
 // top) and 128-row items would fill the SMs. Tree kernel against tile kernel, 32 heads over 8 of 128, us:
-//   16 trees of 24 to 61 tokens over 1500 to 6000 keys 90 / 127, of 61 110 / 96, of 33 over 4000 101 / 92;
-//   1 of 60 over 8000 40 / 67, 4 of 48 over 4000 42 / 46; up to 128 rows: 64 of 32 (16 heads over 4) over 4000
-//   115 / 169, 64 of 12 over 1000 to 4000 69 / 127.
+//   16 trees of 24 to 61 tokens over 1500 to 6000 keys 88 / 127, of 61 110 / 96, of 33 over 4000 101 / 92;
+//   1 of 60 over 8000 35 / 67, 4 of 48 over 4000 42 / 46; up to 128 rows: 64 of 32 (16 heads over 4) over 4000
+//   115 / 169, 64 of 12 over 1000 to 4000 68 / 127.
 int tree_rows(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
   const int group = sh->num_heads_q / c->num_heads;
   const long long rows = (long long)sh->max_seqlen_q * group;

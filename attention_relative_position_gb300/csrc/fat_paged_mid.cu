@@ -27,9 +27,6 @@ namespace fat {
 namespace {
 
 constexpr int kThreads = 384;  // (warp 11 only completes the third warpgroup)
-constexpr int kSoftRegs = 208, kOtherRegs = 88;
-constexpr int kRegsNeeded = 256 * kSoftRegs + 128 * kOtherRegs;
-static_assert(kRegsNeeded <= kThreads * ((65536 / kThreads) & ~7), "register split");
 constexpr int kSoftWarps = 8, kWarpK = 8, kWarpMma = 9, kWarpV = 10;
 constexpr int kMinShare = 2;  // key tiles a CTA takes at least
 constexpr int kItemCost = 2;  // cost of an item beside its key tiles
@@ -51,15 +48,19 @@ struct MidCfg {
   static constexpr int OFF_Q = OFF_V + VS * TILE;
   static constexpr int OFF_P = OFF_Q + QB * QTILE;
   static constexpr int RW = R / 2;               // rows of a softmax warpgroup
+  // registers of a softmax thread and of the others (neither spills; 208 and 88 did in both)
+  static constexpr int SOFT_REGS = R == 64 ? 200 : 216, OTHER_REGS = R == 64 ? 104 : 72;
+  static constexpr int REGS = 256 * SOFT_REGS + 128 * OTHER_REGS;
+  static_assert(REGS <= kThreads * ((65536 / kThreads) & ~7), "register split");
   static constexpr int PB = 1;                   // buffers of P
   static constexpr int SB = 3;                   // and of S
   static constexpr int PTILE = R / 64 * PBLK;
   static constexpr int OFF_ROW = OFF_P + PB * PTILE;
   // per row: slope; bias of a far key at the first query's position less the reference; minus the reference;
-  // the reference; sum or factor; int2: position - shift, head
+  // the reference; sum or factor; int2: position - shift, head; its place in out behind the item's first row
   static constexpr int OFF_SLOPE = OFF_ROW, OFF_FAR = OFF_SLOPE + R * 4, OFF_NREF = OFF_FAR + R * 4;
   static constexpr int OFF_REF = OFF_NREF + R * 4, OFF_FAC = OFF_REF + R * 4, OFF_FARB = OFF_FAC + R * 4;
-  static constexpr int OFF_INT = OFF_FARB + R * 4, OFF_MAX = OFF_INT + R * 8;  // float [2][8][RW]: maxima
+  static constexpr int OFF_INT = OFF_FARB + R * 4, OFF_OUT = OFF_INT + R * 8, OFF_MAX = OFF_OUT + R * 4;  // float [2][8][RW]: maxima
   static constexpr int OFF_BAR = OFF_MAX + 8 * R * 4;
   static constexpr int OFF_THR = OFF_BAR + 320;
   static constexpr int OFF_SHARE = OFF_THR + kMaxThresholds * 4;
@@ -69,10 +70,6 @@ struct MidCfg {
   }
   static_assert((2 * QB + 2 * KS + 2 * VS + 2 * SB + 6) * 8 + 8 <= 320, "barrier block");
   static_assert(OFF_LUT + kMaxBiasSpan + 16 + 1024 <= kSmemLimit, "shared memory");
-  // Rows that a warpgroup stages at a time in P's place, 128 floats each, their quads swizzled. With 128 rows
-  // it is the block of P that only this group writes: the other one's next item may begin meanwhile.
-  static constexpr int SR = R / 4;
-  static_assert(2 * SR * 512 == PTILE, "staged rows");
   static constexpr uint32_t COL_O = SB * R, TMEM_COLS = 4 * R;
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, R, 0, 0);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, R, 1, 1);
@@ -163,6 +160,15 @@ struct MidWalk {
       return true;
     }
     return false;
+  }
+  // Of the CTAs in which the item has tiles the first one, and their number (stretch: this CTA's on the line of
+  // costs; all but the last one's are as long).
+  __device__ int first_cta(const MidItem &it, const long long *stretch, int *parts) const {
+    const long long tiles = stretch[1] - left - it.j1;  // where the first one lies
+    const long long share = blockIdx.x ? div_small(stretch[0], blockIdx.x) : stretch[1];
+    const int c = (int)div_small(tiles, share);
+    *parts = (int)div_small(tiles + it.nkv - 1, share) + 1 - c;
+    return c;
   }
 };
 
@@ -257,6 +263,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.split && tid < 2) part_record(p.part, blockIdx.x, tid)->valid = 0;
   const Share sh = share_find<kThreads, true>(p, kMinShare, MidCost<R>{p}, NoCost{},
                                               [&](long long, long long) { return p.sms; }, share_s);
+  __shared__ long long stretch_s[2];
+  if (tid == 0) {
+    stretch_s[0] = sh.lo;
+    stretch_s[1] = sh.hi;
+  }
   if (p.bias.table != nullptr)  // (behind share_find's barriers)
     for (int i = tid; i <= p.bias.sat_neg + p.bias.sat_pos; i += kThreads)
       lut[i] = (uint8_t)t5_bucket_staged(i - p.bias.sat_neg, p.bias, thr_s);
@@ -266,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{abort_flag, p.err, FAT_DEVERR_TIMEOUT_FWD, p.timeout_ns};
   const bool work = sh.lo < sh.hi;
-  if (warp >= kSoftWarps) regs_dec<kOtherRegs>();
+  if (warp >= kSoftWarps) regs_dec<C::OTHER_REGS>();
   if (work) {
     MidWalk<R> walk(p, share_s, sh);
     MidItem it;
@@ -391,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp < kSoftWarps) {
       // ------------------------------------------------------------------ softmax: thread = key
-      regs_inc<kSoftRegs>();
+      regs_inc<C::SOFT_REGS>();
       constexpr int RW = C::RW;
       const int wg = warp >> 2, t = tid & 127, rb = wg * RW, bar = 1 + wg;
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -403,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float *fac_s = reinterpret_cast<float *>(sm + C::OFF_FAC) + rb;
       float *farb_s = reinterpret_cast<float *>(sm + C::OFF_FARB) + rb;
       int2 *int_s = reinterpret_cast<int2 *>(sm + C::OFF_INT) + rb;
+      int *out_s = reinterpret_cast<int *>(sm + C::OFF_OUT) + rb;
       float *max_s = reinterpret_cast<float *>(sm + C::OFF_MAX) + 8 * rb;  // [8][RW]
       const bool t5 = p.bias.table != nullptr, biased = p.bias.has_bias != 0;
       const bool slopes = p.bias.slopes != nullptr;
@@ -419,22 +431,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok && walk.next(it); ++ni) {
         const int n = it.j1 - it.j0, rows = it.ntok * G;
         const int mine = min(rows - rb, RW);  // rows of this group (none: it only keeps step)
-        if (t < RW && mine > 0) {
-          const int r = rb + min(t, mine - 1), q = r / G, h = it.hk * G + (r - q * G);
-          const int row = it.row0 + q, pos = tree_pos(p, row, it.shift, it.lk);
-          if (__ldg(p.pos + row) != pos) atomicOr(p.err, FAT_DEVERR_INDEX);
-          prefetch_l1(p.mask + (size_t)row * p.mask_words);
-          const float slope = slopes ? __ldg(p.bias.slopes + h) * kLog2e : 0.f;
-          const float far = t5 ? __ldg(p.bias.table + (size_t)lut[0] * p.hq + h) * kLog2e : 0.f;
-          slope_s[t] = slope;
-          farb_s[t] = far - slope * (float)(pos - it.shift);
-          int_s[t] = make_int2(pos - it.shift, h);
-          set_ref(t < mine ? 0.f : kNoRow);
+        if (mine > 0) {  // row t's numbers; its position arrives beside the first tile's logits
+          const int rt = rb + min(t, mine - 1), q = rt / G, h = it.hk * G + (rt - q * G);
+          int pos_in = 0;
+          if (t < RW) {
+            pos_in = __ldg(p.pos + it.row0 + q);
+            prefetch_l1(p.mask + (size_t)(it.row0 + q) * p.mask_words);
+          }
+          if (!(ok = warp_wait(s_full + g % SB, (g / SB) & 1, wd))) break;
+          if (t < RW) {
+            const int pos = min(max(pos_in, it.shift), it.lk - 1);
+            if (pos_in != pos) atomicOr(p.err, FAT_DEVERR_INDEX);
+            const float slope = slopes ? __ldg(p.bias.slopes + h) * kLog2e : 0.f;
+            const float far = t5 ? __ldg(p.bias.table + (size_t)lut[0] * p.hq + h) * kLog2e : 0.f;
+            slope_s[t] = slope;
+            farb_s[t] = far - slope * (float)(pos - it.shift);
+            int_s[t] = make_int2(pos - it.shift, h);
+            out_s[t] = q * p.hq + h;
+            set_ref(t < mine ? 0.f : kNoRow);
+          }
+          named_bar_sync(bar, 128);
         }
         uint64_t sum[RW / 2];  // of this thread's weights, rows 2 i and 2 i + 1
 #pragma unroll
         for (int i = 0; i < RW / 2; ++i) sum[i] = 0;
-        named_bar_sync(bar, 128);
         for (int j = 0; j < n; ++j) {
           const uint32_t gt = g + j, buf = gt % SB;
           const uint32_t tS = tmem + lane_off + R * buf + rb;
@@ -593,10 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               all_logits();
             }
-            // P, once the products that read its place are complete, and the staged rows of the item before have
-            // left it (64 rows: the other group's share its block)
+            // P, once the products that read its place are complete
             if (gt >= C::PB && !(ok = o_wait(gt - C::PB))) break;
-            if (R == 64 && j == 0 && ni > 0 && !(ok = warp_wait(o_free, (ni - 1) & 1, wd))) break;
             const uint32_t sP = smem_u32(sm + C::OFF_P + (gt % C::PB) * C::PTILE);
 #pragma unroll
             for (int c = 0; c < RW; c += 32) {
@@ -623,14 +641,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();
           // values behind the last key: whatever the page holds, they are 0
-          if (wg == 0 && k0 + 128 > it.lk) {
+          if (k0 + 128 > it.lk) {
             const uint32_t v = gt % VS;
             if (!(ok = warp_wait(v_full + v, (gt / VS) & 1, wd))) break;
-            if (key >= it.lk)
+            for (int i = (it.lk - k0) * 8 + tid; i < 1024; i += 256)
 #pragma unroll
-              for (int c = 0; c < 8 * C::DB; ++c)
-                *reinterpret_cast<uint4 *>(sm + C::OFF_V + v * C::TILE + (c >> 3) * C::BLK + t * 128 +
-                                           (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              for (int c = 0; c < C::DB; ++c)
+                *reinterpret_cast<uint4 *>(sm + C::OFF_V + v * C::TILE + c * C::BLK + i * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -641,9 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         g += n;
-        // ---- the item's rows
-        if (!(ok = o_wait(g - 1))) break;
-        tc_fence_after();
+        // ---- the item's rows: their sums over the threads (beside the last products), then O, whose TMEM lanes
+        // are channels. Four lanes trade a 4 x 4 block, after which each has four channels of a row.
         const bool whole = it.begins && it.ends;
         const int which = it.begins ? 1 : 0;
         if (!whole && tid == 0) {
@@ -653,73 +670,82 @@ __global__ void __launch_bounds__(kThreads, 1)
           rec->row0 = it.row0;
           rec->hk = it.hk;
           rec->rows = rows;
+          rec->pos = (int)blockIdx.x - walk.first_cta(it, stretch_s, &rec->parts);
         }
-        constexpr int SR = C::SR;
-        float *stage = reinterpret_cast<float *>(sm + C::OFF_P) + wg * SR * 128;  // [SR][128]: P has been used
-        auto staged = [&](int row, int quad) { return stage + row * 128 + ((quad ^ (row & 7)) << 2); };
-        auto mine_of = [&](int row) { return staged(row, t >> 2) + (t & 3); };  // this thread's column
         if (mine > 0) {
 #pragma unroll
-          for (int c = 0; c < RW; c += SR) {  // the threads' sums, 128 / SR threads a row
-            if (c >= mine) break;
+          for (int c = 0; c < RW; c += 32) {
+            if (c > 0 && c >= mine) break;
+            float s[32];
 #pragma unroll
-            for (int i = 0; i < SR / 2; ++i)
-              f2_unpack(sum[c / 2 + i], *mine_of(2 * i), *mine_of(2 * i + 1));
-            named_bar_sync(bar, 128);
-            constexpr int TR = 128 / SR;
-            float l = 0.f;
+            for (int i = 0; i < 16; ++i) f2_unpack(sum[c / 2 + i], s[2 * i], s[2 * i + 1]);
 #pragma unroll
-            for (int i = 0; i < SR / 4; ++i) {
-              const float4 v = *reinterpret_cast<const float4 *>(staged(t / TR, t % TR + TR * i));
-              l += (v.x + v.y) + (v.z + v.w);
-            }
+            for (int o = 16; o > 0; o >>= 1)  // lane i ends with row c + i
 #pragma unroll
-            for (int o = 1; o < TR; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (t % TR == 0) fac_s[c + t / TR] = l;
-            named_bar_sync(bar, 128);
+              for (int i = 0; i < o; ++i) {
+                const float keep = (lane & o) ? s[i + o] : s[i], give = (lane & o) ? s[i] : s[i + o];
+                s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+              }
+            max_s[(warp & 3) * RW + c + lane] = s[0];
           }
-#pragma unroll 1
-          for (int c = 0; c < mine; c += SR) {  // and the rows
-            uint32_t x[SR];
-            if constexpr (SR == 32)
-              tmem_ld32(tmem + lane_off + C::COL_O + rb + c, x);
-            else
-              tmem_ld16(tmem + lane_off + C::COL_O + rb + c, x);
-            if (t < D)
-#pragma unroll
-              for (int i = 0; i < SR; ++i) *mine_of(i) = __uint_as_float(x[i]);
-            named_bar_sync(bar, 128);
-            const int left = min(SR, mine - c);
+          named_bar_sync(bar, 128);
+          if (t < mine) {
+            const float l = (max_s[t] + max_s[RW + t]) + (max_s[2 * RW + t] + max_s[3 * RW + t]);
             if (whole) {
-              for (int i = t; i < left * (D / 8); i += 128) {
-                const int rr = i / (D / 8), ch = (i % (D / 8)) * 8, h = int_s[c + rr].y;
-                const float l = fac_s[c + rr], inv = l == 0.f ? 0.f : 1.0f / l;
-                const float4 a = *reinterpret_cast<const float4 *>(staged(rr, ch / 4));
-                const float4 b = *reinterpret_cast<const float4 *>(staged(rr, ch / 4 + 1));
-                const size_t row = (size_t)it.row0 + (rb + c + rr) / G;
-                *reinterpret_cast<uint4 *>(p.out + (row * p.hq + h) * D + ch) =
-                    make_uint4(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv),
-                               pack_bf16x2(b.x * inv, b.y * inv), pack_bf16x2(b.z * inv, b.w * inv));
-                if (ch == 0 && p.lse != nullptr)
-                  p.lse[(size_t)h * p.total_q + row] =
-                      l == 0.f ? -INFINITY : (ref_s[c + rr] + __log2f(l)) * kLn2;
-              }
+              fac_s[t] = l == 0.f ? 0.f : 1.0f / l;
+              if (p.lse != nullptr)
+                p.lse[(size_t)int_s[t].y * p.total_q + it.row0 + (rb + t) / G] =
+                    l == 0.f ? -INFINITY : (ref_s[t] + __log2f(l)) * kLn2;
             } else {
-              float *po = part_rows<R, D>(p.part, gridDim.x, blockIdx.x, which);
-              float *ps = part_stats<R, D>(p.part, gridDim.x, blockIdx.x, which);
-              for (int i = t; i < SR * (D / 4); i += 128) {
-                const int rr = i % SR, c4 = i / SR;
-                if (rr < left)
-                  *part_quad<R>(po, rb + c + rr, c4) =
-                      *reinterpret_cast<const float4 *>(staged(rr, c4));
-              }
-              if (t < left) {
-                const float l = fac_s[c + t];
-                *reinterpret_cast<float2 *>(ps + (rb + c + t) * 2) =
-                    make_float2(l == 0.f ? -INFINITY : ref_s[c + t], l);
-              }
+              *reinterpret_cast<float2 *>(part_stats<R, D>(p.part, gridDim.x, blockIdx.x, which) +
+                                          (rb + t) * 2) = make_float2(l == 0.f ? -INFINITY : ref_s[t], l);
             }
-            named_bar_sync(bar, 128);
+          }
+          named_bar_sync(bar, 128);
+        }
+        if (!(ok = o_wait(g - 1))) break;
+        tc_fence_after();
+        const int ch = t & (D - 4), odd = lane & 1, high = lane & 2;
+        __nv_bfloat16 *out = p.out + (size_t)it.row0 * p.hq * D + ch;
+        float *po = whole ? nullptr : part_rows<R, D>(p.part, gridDim.x, blockIdx.x, which);
+#pragma unroll 1
+        for (int c = 0; c < mine; c += 16) {
+          uint32_t x[16];
+          tmem_ld16(tmem + lane_off + C::COL_O + rb + c, x);
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            if (D == 64 && (a & 1) != ((warp >> 1) & 1)) continue;  // (the channels twice: half the rows each)
+            const int row = c + 4 * a + (lane & 3);
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(x[4 * a + i]);
+            if (whole) {
+              const float4 f = *reinterpret_cast<const float4 *>(fac_s + c + 4 * a);
+              v[0] *= f.x;
+              v[1] *= f.y;
+              v[2] *= f.z;
+              v[3] *= f.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {  // rows i and i + 1: two channels of one of them
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+              const float kept = odd ? v[i + 1] : v[i];
+              v[i] = odd ? got : kept;
+              v[i + 1] = odd ? kept : got;
+            }
+            if (whole) {
+              const uint32_t w0 = pack_bf16x2(v[0], v[1]), w1 = pack_bf16x2(v[2], v[3]);
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w0 : w1, 2);
+              if (row < mine)
+                *reinterpret_cast<uint2 *>(out + (size_t)out_s[row] * D) =
+                    high ? make_uint2(got, w1) : make_uint2(w0, got);
+            } else {
+              const float g0 = __shfl_xor_sync(0xffffffffu, high ? v[0] : v[2], 2);
+              const float g1 = __shfl_xor_sync(0xffffffffu, high ? v[1] : v[3], 2);
+              if (row < mine)
+                *part_quad<R>(po, rb + row, ch >> 2) =
+                    high ? make_float4(g0, g1, v[2], v[3]) : make_float4(v[0], v[1], g0, g1);
+            }
           }
         }
         tc_fence_before();
@@ -749,7 +775,7 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
   if (make_tmap_rows(&mq, p.q, p.total_q, p.hq, D, p.group, R / p.group)) return FAT_ECUDA;
   const size_t smem = C::bytes(p.bias) + 1024;
   const auto kernel = fat_paged_mid_kernel<D, R>;
-  if (prepare_kernel((const void *)kernel, smem, kThreads, kRegsNeeded)) return FAT_ECUDA;
+  if (prepare_kernel((const void *)kernel, smem, kThreads, C::REGS)) return FAT_ECUDA;
   return launch_dependent("paged tree kernel launch", kernel, dim3((unsigned)paged_tile_ctas()),
                           kThreads, smem, stream, mq, mk, mv, pp);
 }
