@@ -11,8 +11,8 @@
 // computed again, their gradient goes to the workspace in bf16, and two products take it from there:
 // dh += dz W and dw = dz^T H. dz is kept without grad_scale and s, which scale the results: bf16 holds the
 // large entries, p - 1 at the targets, best when they are next to 1 (with 1 / rows in them all of them
-// round the same way, and so do the results: 251 rows 0.0038 off against 0.0023). A launch does the products of one piece and the logits of
-// the next, so that its last wave is filled with short tiles.
+// round the same way, and so do the results: 251 rows 0.0038 off against 0.0017). A launch does the products of one
+// piece and the logits of the next, so that its last wave is filled with short tiles.
 // Bound by the tensor cores (2, 4 and 2 N V D operations in the three products, 2 in the loss) from some
 // 300 rows on, below that by the read of the weights (and the write of their gradient).
 //

@@ -9,8 +9,8 @@
 // against its group's rows (a TMEM lane); what it subtracts per row, the reference, is a shared number. A
 // row's reference is the largest of eight logits of the first tile taken, and is raised to the maximum (O and
 // the sums scaled) when a weight would exceed 2^32: a group's 128 threads vote once a tile, and a maximum
-// over the keys, across lanes, is formed only then. A thread sums its own key's weights in a register per row (unrounded, fp32);
-// the threads' sums are added at an item's end. Key tiles go from the last one backwards, from the
+// over the keys, across lanes, is formed only then. A thread sums its own key's weights in a register per row
+// (unrounded, fp32); the threads' sums are added at an item's end. Key tiles go from the last one backwards, from the
 // request's own tokens and the largest linear bias on. P is rounded to bf16, as in the tile kernel.
 // One persistent CTA per SM takes an equal share of all key tiles (fat_paged.cuh); requests of more rows are
 // cut into blocks of them (their keys are found in L2 again):
@@ -50,8 +50,8 @@ struct MidCfg {
   static constexpr int RW = R / 2;               // rows of a softmax warpgroup
   // registers of a softmax thread and of the others (neither spills; 208 and 88 did in both)
   static constexpr int SOFT_REGS = R == 64 ? 200 : 216, OTHER_REGS = R == 64 ? 104 : 72;
-  static constexpr int REGS = 256 * SOFT_REGS + 128 * OTHER_REGS;
-  static_assert(REGS <= kThreads * ((65536 / kThreads) & ~7), "register split");
+  static constexpr int REGS_NEEDED = 256 * SOFT_REGS + 128 * OTHER_REGS;
+  static_assert(REGS_NEEDED <= kThreads * ((65536 / kThreads) & ~7), "register split");
   static constexpr int PB = 1;                   // buffers of P
   static constexpr int SB = 3;                   // and of S
   static constexpr int PTILE = R / 64 * PBLK;
@@ -775,7 +775,7 @@ int launch_t(const PagedParams &p, const fat_paged_cache_t &c, cudaStream_t stre
   if (make_tmap_rows(&mq, p.q, p.total_q, p.hq, D, p.group, R / p.group)) return FAT_ECUDA;
   const size_t smem = C::bytes(p.bias) + 1024;
   const auto kernel = fat_paged_mid_kernel<D, R>;
-  if (prepare_kernel((const void *)kernel, smem, kThreads, C::REGS)) return FAT_ECUDA;
+  if (prepare_kernel((const void *)kernel, smem, kThreads, C::REGS_NEEDED)) return FAT_ECUDA;
   return launch_dependent("paged tree kernel launch", kernel, dim3((unsigned)paged_tile_ctas()),
                           kThreads, smem, stream, mq, mk, mv, pp);
 }

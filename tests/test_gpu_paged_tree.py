@@ -503,3 +503,20 @@ def test_verification_step(graph):
     tol = 2.1 * (256 / 16 + 16) * 2.0 ** -23 * float((out.reshape(total, -1).double().abs()
                                                      @ weight.double().abs().t()).max()) + 1e-4
     assert (loss.double() - score).abs().max() <= tol
+
+
+# Items over most of the grid (more parts than a warp's task holds), a few parts beside whole items, and parts of
+# requests that begin where another ends; 64 and 128 rows, a group of rows that a warpgroup has none of.
+@pytest.mark.parametrize("lq,ctx,hq,hkv,d", [
+    ([30], [11000], 2, 2, 64), ([30], [9000], 4, 2, 128), ([100], [9001], 1, 1, 64), ([70], [8900], 1, 1, 128),
+    ([25, 3, 30], [4000, 20, 5003], 2, 1, 128), ([17, 40, 64, 20], [2000, 1999, 30, 2500], 4, 2, 64),
+    ([20] * 9, [1100 + 130 * i for i in range(9)], 6, 2, 128)])
+def test_long_contexts_in_parts(lq, ctx, hq, hkv, d):
+    t = Tree(lq, ctx, hq=hq, hkv=hkv, d=d, page=64, seed=21, alibi=True)
+    size = fa.fat_paged_attn_workspace_size(t.p.q, t.p.kc, _i32(t.p.cu), t.most, int(max(t.p.lk)))
+    ws = torch.full((size,), 0xff, dtype=torch.uint8, device=DEV)
+    out, lse = t.run(workspace=ws)
+    assert _errors() == 0
+    t.check(out, lse)
+    again, lse2 = t.run(workspace=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
