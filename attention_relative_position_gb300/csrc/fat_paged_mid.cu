@@ -751,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free);
+        if (mine > 0) named_bar_sync(bar, 128);  // out_s has been read: the next item's may be written
       }
     }
   }
