@@ -520,3 +520,13 @@ def test_long_contexts_in_parts(lq, ctx, hq, hkv, d):
     t.check(out, lse)
     again, lse2 = t.run(workspace=ws)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+# More requests than a block has threads, and more in a CTA's stretch than it stages; few rows and many.
+@pytest.mark.parametrize("lq,hq,d", [([20, 1, 3] + [1, 2] * 700 + [0, 17], 2, 128), ([1] * 10500 + [33], 1, 64),
+                                     ([1, 2] * 3000 + [4], 2, 64)])
+def test_many_requests(lq, hq, d):
+    t = Tree(lq, [(5 * i) % 23 for i in range(len(lq))], hq=hq, hkv=1, d=d, page=16, seed=13)
+    out, lse = t.run()
+    assert _errors() == 0
+    t.check(out, lse)
