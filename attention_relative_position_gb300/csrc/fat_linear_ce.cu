@@ -584,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool in = v0 + t < p.vocab;
         float x[2][32];
         for (int k = job.k0;;) {
-          if (!(ok = warp_wait_cluster(acc_full + (n & 1), (n / 2) & 1, wd))) break;
+          if (ok) ok = warp_wait_cluster(acc_full + (n & 1), (n / 2) & 1, wd);
           tc_fence_after();
           d = tmem + lane_off + 256 * (n & 1) + r0;
 #pragma unroll
@@ -601,7 +601,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (k >= job.k1) break;
           ++n;
         }
-        if (!ok) break;
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           if (c >= nr) break;
@@ -643,6 +642,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             row_stats(Threads<4>{});
           named_bar_sync(1 + half, 128);
         }
+        // (the warps meet at barriers: after a wait that ran out they leave together)
+        ok = !named_bar_any(1 + half, 128, !ok);
       } else {
         float4 rec = make_float4(0.f, 0.f, 0.f, 0.f);
         if (job.kind == kProb) rec = __ldg(p.rec + p.pr0 + job.m0 + row_in + lane);

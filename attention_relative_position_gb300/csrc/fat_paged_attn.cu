@@ -236,9 +236,9 @@ size_t workspace_bound(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) 
 // for more than 128 rows a request (the tree kernel reads keys again for every 128, the tile kernel for every
 // 256), where every request has as many (else the few-row kernel's launch and its share of the SMs come on
 // top) and 128-row items would fill the SMs. Tree kernel against tile kernel, 32 heads over 8 of 128, us:
-//   16 trees of 24 to 61 tokens over 1500 to 6000 keys 88 / 127, of 61 110 / 96, of 33 over 4000 101 / 92;
+//   16 trees of 24 to 61 tokens over 1500 to 6000 keys 89 / 127, of 61 110 / 96, of 33 over 4000 101 / 92;
 //   1 of 60 over 8000 35 / 67, 4 of 48 over 4000 42 / 46; up to 128 rows: 64 of 32 (16 heads over 4) over 4000
-//   115 / 169, 64 of 12 over 1000 to 4000 68 / 127.
+//   115 / 169, 64 of 12 over 1000 to 4000 69 / 127.
 int tree_rows(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) {
   const int group = sh->num_heads_q / c->num_heads;
   const long long rows = (long long)sh->max_seqlen_q * group;

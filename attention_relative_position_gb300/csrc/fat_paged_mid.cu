@@ -172,16 +172,6 @@ struct MidWalk {
   }
 };
 
-__device__ __forceinline__ bool bar_any(int id, bool v) {  // of a softmax warpgroup
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id)
-      : "memory");
-  return r != 0;
-}
 // bit j of lane i's word -> bit i of lane j's
 __device__ __forceinline__ uint32_t transpose32(uint32_t x, int lane) {
   uint32_t m = 0x0000ffffu;
@@ -427,6 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto o_wait = [&](uint32_t i) { return warp_wait(o_ready + (i & 1), (i / 2) & 1, wd); };
       uint32_t g = 0;
       int ni = 0;
+      // A group's warps meet at barriers, so none leaves alone: once a wait has run out (ok) a warp waits no more
+      // and goes through the motions until a vote ends the loops for all of them.
       bool ok = true;
       for (; ok && walk.next(it); ++ni) {
         const int n = it.j1 - it.j0, rows = it.ntok * G;
@@ -438,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pos_in = __ldg(p.pos + it.row0 + q);
             prefetch_l1(p.mask + (size_t)(it.row0 + q) * p.mask_words);
           }
-          if (!(ok = warp_wait(s_full + g % SB, (g / SB) & 1, wd))) break;
+          ok = warp_wait(s_full + g % SB, (g / SB) & 1, wd);
           if (t < RW) {
             const int pos = min(max(pos_in, it.shift), it.lk - 1);
             if (pos_in != pos) atomicOr(p.err, FAT_DEVERR_INDEX);
@@ -459,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t gt = g + j, buf = gt % SB;
           const uint32_t tS = tmem + lane_off + R * buf + rb;
           const int k0 = (it.nkv - 1 - it.j0 - j) * 128, key = k0 + t;
-          if (!(ok = warp_wait(s_full + buf, (gt / SB) & 1, wd))) break;
+          if (ok) ok = warp_wait(s_full + buf, (gt / SB) & 1, wd);
           tc_fence_after();
           if (mine > 0) {
             float scale = p.scale_log2;
@@ -554,8 +546,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               f2_unpack(y[i], a, b);
               top = fmax3(top, a, b);
             }
-            const bool raise = bar_any(bar, top > 32.f);
+            const bool raise = named_bar_any(bar, 128, top > 32.f || !ok);
             if (raise) {
+              if (named_bar_any(bar, 128, !ok)) {
+                ok = false;
+                break;
+              }
               // The rows' maxima over the tile, and new references where they passed 2^32. A row that has seen
               // no key has a reference of -3e38, which loses the logit: its maximum is taken anew, from 0.
               bool fresh = false;
@@ -595,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               named_bar_sync(bar, 128);
               if (j > 0) {  // what was summed so far
-                if (!(ok = o_wait(gt - 1))) break;
+                ok = o_wait(gt - 1);
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < mine; c += 8) {
@@ -614,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               all_logits();
             }
             // P, once the products that read its place are complete
-            if (gt >= C::PB && !(ok = o_wait(gt - C::PB))) break;
+            if (ok && gt >= C::PB) ok = o_wait(gt - C::PB);
             const uint32_t sP = smem_u32(sm + C::OFF_P + (gt % C::PB) * C::PTILE);
 #pragma unroll
             for (int c = 0; c < RW; c += 32) {
@@ -636,28 +632,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st_shared_v4(at + (((((r & 63) >> 3) + i) ^ (t & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2],
                              w[4 * i + 3]);
             }
-          } else if (gt >= C::PB) {  // a group without rows keeps step: its arrivals count for this tile
-            if (!(ok = o_wait(gt - C::PB))) break;
+          } else if (ok && gt >= C::PB) {  // a group without rows keeps step: its arrivals count for this tile
+            ok = o_wait(gt - C::PB);
           }
           tc_fence_before();
           // values behind the last key: whatever the page holds, they are 0
           if (k0 + 128 > it.lk) {
             const uint32_t v = gt % VS;
-            if (!(ok = warp_wait(v_full + v, (gt / VS) & 1, wd))) break;
-            for (int i = (it.lk - k0) * 8 + tid; i < 1024; i += 256)
+            if (ok) ok = warp_wait(v_full + v, (gt / VS) & 1, wd);
+            if (ok)
+              for (int i = (it.lk - k0) * 8 + tid; i < 1024; i += 256)
 #pragma unroll
-              for (int c = 0; c < C::DB; ++c)
-                *reinterpret_cast<uint4 *>(sm + C::OFF_V + v * C::TILE + c * C::BLK + i * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < C::DB; ++c)
+                  *reinterpret_cast<uint4 *>(sm + C::OFF_V + v * C::TILE + c * C::BLK + i * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
+          if (ok && lane == 0) {
             mbar_arrive(s_free + buf);
             mbar_arrive(p_ready + (gt & 1));
           }
         }
-        if (!ok) break;
         g += n;
         // ---- the item's rows: their sums over the threads (beside the last products), then O, whose TMEM lanes
         // are channels. Four lanes trade a 4 x 4 block, after which each has four channels of a row.
@@ -703,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           named_bar_sync(bar, 128);
         }
-        if (!(ok = o_wait(g - 1))) break;
+        if (ok) ok = o_wait(g - 1);
         tc_fence_after();
         const int ch = t & (D - 4), odd = lane & 1, high = lane & 2;
         __nv_bfloat16 *out = p.out + (size_t)it.row0 * p.hq * D + ch;
@@ -750,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(o_free);
-        if (mine > 0) named_bar_sync(bar, 128);  // out_s has been read: the next item's may be written
+        if (ok && lane == 0) mbar_arrive(o_free);
+        ok = !named_bar_any(bar, 128, !ok);  // (and out_s has been read: the next item's may be written)
       }
     }
   }
