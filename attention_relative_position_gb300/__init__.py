@@ -177,6 +177,8 @@ def load(path: Optional[str] = None):
     lib.fat_rope_apply.restype = i32
     P = ctypes.POINTER
     H = P(_LinearCeShape)
+    lib.fat_attn_debug_head_columns.argtypes = [H, i32]
+    lib.fat_attn_debug_head_columns.restype = i32
     lib.fat_linear_cross_entropy_workspace_size.argtypes = [H, i32]
     lib.fat_linear_cross_entropy_workspace_size.restype = ctypes.c_size_t
     lib.fat_linear_cross_entropy_fwd.argtypes = [H, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]

@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "../../include/fat_attn_debug.h"
 #include "fat_attn_internal.cuh"
 
 namespace fat {
@@ -40,8 +41,10 @@ constexpr int kEpiWarps = 8, kWarpProd = 8, kWarpMma = 9;
 constexpr int kHalf = 128 * 128;          // one operand's half of a stage: 128 rows x 64 bf16
 constexpr int kBuf = 32 * 128;            // staged output of a warp: 32 rows x 128 bytes
 constexpr int kTile = 256;                // rows and columns of a pair's tile
+constexpr int kColStep = 32;              // a pair's product of 256 rows has 32, 64, .. 256 columns
 constexpr int kFewHeadRows = 128;         // forward calls of at most so many rows take the few-row form
 constexpr int kMaxPairs = 128;
+static_assert(kTile % kColStep == 0 && kFewHeadRows % kColStep == 0, "columns of a product");
 
 // The kernel's forms, and what each has in shared memory.
 enum Mode { kForward, kBackward, kFew, kLong };
@@ -887,8 +890,9 @@ int head_pairs() {
 }
 
 // Forward: tiles of 256 rows x 256 entries, or as many fewer entries as leave the same number of rounds over
-// the pairs; up to 128 rows tiles of 256 entries x the rows. Entries as the tall side against rows, us:
-// one row, 32768 entries of 512 channels 11.6 / 17.8; 17 rows of 1024 channels 20.5 / 25.9; 64 20.4 / 20.8.
+// the pairs; up to 128 rows tiles of 256 entries x the rows (widths are multiples of kColStep). Entries
+// as the tall side against rows, us: one row, 32768 entries of 512 channels 11.6 / 17.8; 17 rows of 1024
+// channels 20.5 / 25.9; 64 20.4 / 20.8.
 // Boxes whose rows begin between two 32-byte sectors (rows of an odd number of 16 bytes) are loaded at about
 // half the rate: forward calls of many rows copy such hidden rows and weights to rows padded to kCopyPad
 // channels (776 channels, 2077 rows and 50021 entries 159 us without, 135 with; 1024 rows and 32768
@@ -907,14 +911,15 @@ FwdPlan forward_plan(const fat_linear_ce_shape_t *s, int pairs) {
   FwdPlan f{};
   f.few = s->rows <= kFewHeadRows;
   if (f.few) {
-    f.bn = ceil_div(s->rows, 16) * 16;
+    f.bn = ceil_div(s->rows, kColStep) * kColStep;
     f.row_tiles = ceil_div(s->vocab, kTile);
     f.col_tiles = 1;
   } else {
     const long long rt = f.row_tiles = ceil_div(s->rows, kTile);
     const long long rounds = ceil_div(rt * ceil_div(s->vocab, kTile), pairs);
     f.bn = kTile;
-    while (f.bn > 32 && rt * ceil_div(s->vocab, f.bn - 16) <= rounds * pairs) f.bn -= 16;
+    while (f.bn > kColStep && rt * ceil_div(s->vocab, f.bn - kColStep) <= rounds * pairs)
+      f.bn -= kColStep;
     f.col_tiles = ceil_div(s->vocab, f.bn);
   }
   f.parts = 2 * f.row_tiles * f.col_tiles / (f.few ? 1 : f.row_tiles);
@@ -1063,6 +1068,10 @@ size_t fat_linear_cross_entropy_workspace_size(const fat_linear_ce_shape_t *s, i
   const int pairs = head_pairs();
   if (pairs == 0 || s->rows == 0) return 0;
   return backward ? backward_plan(s, pairs).bytes : forward_plan(s, pairs).bytes;
+}
+
+int fat_attn_debug_head_columns(const fat_linear_ce_shape_t *s, int pairs) {
+  return check(s) || s->rows == 0 || pairs < 1 ? 0 : forward_plan(s, pairs).bn;
 }
 
 int fat_linear_cross_entropy_fwd(const fat_linear_ce_shape_t *s, const void *hidden,

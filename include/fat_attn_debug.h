@@ -33,6 +33,13 @@ int fat_attn_debug_buckets(long long delta_lo, int n, int num_buckets, int max_d
  */
 void fat_attn_debug_set_watchdog(long long timeout_ns, int flags);
 
+/*
+ * Columns of the logits tiles (and so of their tensor-core products) of
+ * fat_linear_cross_entropy_fwd for this shape on a device with room for `pairs` pairs of CTAs; 0
+ * for a shape that is refused or has no rows. Host only.
+ */
+int fat_attn_debug_head_columns(const fat_linear_ce_shape_t *shape, int pairs);
+
 #ifdef __cplusplus
 }
 #endif
