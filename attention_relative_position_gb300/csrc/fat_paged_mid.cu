@@ -32,6 +32,9 @@ constexpr int kMinShare = 2;  // key tiles a CTA takes at least
 constexpr int kItemCost = 2;  // cost of an item beside its key tiles
 constexpr float kNoRow = 3e38f;      // reference of a row without a token: its weights are 0
 constexpr float kFreshRow = -3e38f;  // of a row that has seen no key: whatever it sees calls for a new one
+// From here on a bias (in log2 units) leaves of a logit whole numbers at most, and a reference like it cannot say
+// which: rows with such biases for their far keys form logits and references as one rounded sum each.
+constexpr float kLargeBias = 16777216.f;
 constexpr float kSeen = -2.9e38f;    // logits above this count as seen (biases down to -2e38, times log2 e)
 
 template <int D, int R>
@@ -48,7 +51,8 @@ struct MidCfg {
   static constexpr int OFF_Q = OFF_V + VS * TILE;
   static constexpr int OFF_P = OFF_Q + QB * QTILE;
   static constexpr int RW = R / 2;               // rows of a softmax warpgroup
-  // registers of a softmax thread and of the others (neither spills; 208 and 88 did in both)
+  // registers of a softmax thread and of the others (28 bytes spill at 128 rows, whose times are those of a build
+  // without; 208 and 88 spill more in both)
   static constexpr int SOFT_REGS = R == 64 ? 200 : 216, OTHER_REGS = R == 64 ? 104 : 72;
   static constexpr int REGS_NEEDED = 256 * SOFT_REGS + 128 * OTHER_REGS;
   static_assert(REGS_NEEDED <= kThreads * ((65536 / kThreads) & ~7), "register split");
@@ -423,9 +427,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok && walk.next(it); ++ni) {
         const int n = it.j1 - it.j0, rows = it.ntok * G;
         const int mine = min(rows - rb, RW);  // rows of this group (none: it only keeps step)
+        int near = 0;  // from this key on logits are formed one by one
         if (mine > 0) {  // row t's numbers; its position arrives beside the first tile's logits
           const int rt = rb + min(t, mine - 1), q = rt / G, h = it.hk * G + (rt - q * G);
           int pos_in = 0;
+          bool large = false;
           if (t < RW) {
             pos_in = __ldg(p.pos + it.row0 + q);
             prefetch_l1(p.mask + (size_t)(it.row0 + q) * p.mask_words);
@@ -441,8 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int_s[t] = make_int2(pos - it.shift, h);
             out_s[t] = q * p.hq + h;
             set_ref(t < mine ? 0.f : kNoRow);
+            const float most = fmaxf(fabsf(far), fabsf(slope) * (float)it.lk);
+            large = t < mine && most >= kLargeBias && fabsf(far) < INFINITY;
           }
-          named_bar_sync(bar, 128);
+          if (!named_bar_any(bar, 128, large)) near = it.shift - (biased ? p.bias.sat_neg : 0);
         }
         uint64_t sum[RW / 2];  // of this thread's weights, rows 2 i and 2 i + 1
 #pragma unroll
@@ -455,12 +463,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (mine > 0) {
             float scale = p.scale_log2;
-            const bool edge = k0 + 128 > it.shift - (biased ? p.bias.sat_neg : 0);
+            const bool edge = k0 + 128 > near;
             const bool linear = slopes && !edge;
             const float *cst_s = edge ? nref_s : far_s;
             if (edge) {
               // Own keys, or cached ones near them: logits where they stand, masked by the rows' bits. A
-              // thread's key is the same for all rows, and so is its position.
+              // thread's key is the same for all rows, and so is its position. (Beside large biases every key:
+              // a reference such as -1e10 holds no more of the logit than these do.)
               const int key0 = k0 + (warp & 3) * 32;
               const int kp = key < it.shift ? key - it.shift
                                             : tree_pos(p, it.tok0 + min(key, it.lk - 1) - it.shift, it.shift,
@@ -552,12 +561,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
               }
-              // The rows' maxima over the tile, and new references where they passed 2^32. A row that has seen
-              // no key has a reference of -3e38, which loses the logit: its maximum is taken anew, from 0.
-              bool fresh = false;
-              if (t < RW) {
-                fresh = ref_s[t] == kFreshRow;
-                if (fresh) set_ref(0.f);
+              // The rows' maxima over the tile, and new references where they passed 2^32. They are taken from
+              // reference 0: a low reference (-3e38 of a row that has seen no key, or of keys with masking biases)
+              // has rounded the other keys' logits away.
+              if (t < mine) {
+                fac_s[t] = ref_s[t];
+                set_ref(0.f);
               }
               named_bar_sync(bar, 128);
 #pragma unroll 1
@@ -580,12 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mx = fmaxf(fmaxf(max_s[t], max_s[RW + t]), fmaxf(max_s[2 * RW + t], max_s[3 * RW + t]));
                 float f = 1.f;
                 if (t < mine) {
-                  if (fresh) {
-                    if (!(mx != mx)) set_ref(mx > kSeen ? mx : kFreshRow);  // (a NaN shows in the sum)
-                  } else if (mx > 32.f) {
-                    f = ex2(-mx);
-                    set_ref(ref_s[t] + mx);
-                  }
+                  const float old = fac_s[t];
+                  const bool up = mx > kSeen && mx > old + 32.f;  // (not if mx is NaN: that shows in the sum)
+                  if (up) f = ex2(old - mx);
+                  set_ref(up ? mx : old);
                 }
                 fac_s[t] = f;
               }

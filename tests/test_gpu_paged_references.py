@@ -1,0 +1,81 @@
+"""Attention over a paged cache beside biases that mask with large finite numbers: what such keys leave in a
+row's running maximum must not reach the row's other keys. Trees of drafted tokens against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import attention_relative_position_gb300 as fa  # noqa: F401
+from test_gpu_paged import _errors, _wide
+from test_gpu_paged_tree import T5D, Tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    _errors()
+
+
+def _patterns(p, low, pattern, rng):
+    """Buckets of heads that mask: every near one (whole tiles of masked keys come first), every second
+    distance, or any."""
+    b = p.bias  # [32, heads]: distances 0 to 15, then up to 128
+    hide = np.zeros(b.shape, bool)
+    if pattern == "near":
+        hide[:31] = True
+    elif pattern == "odd":
+        hide[1:16:2, ::2] = True
+        hide[0:16:2, 1::2] = True
+        hide[16:28] = True
+    else:
+        hide = rng.random(b.shape) < 0.7
+        hide[31, ::2] = False
+    b[torch.as_tensor(hide, device=b.device)] = low
+    return hide
+
+
+# A masked key's weight beside any other key of its row is exp(-1e6 + logits) = 0 in any arithmetic, so the
+# oracle leaves those keys out. A row that sees nothing else has logits that fp32 rounds to within 2^-24 of the
+# bias: its lse is the bias, up to some such roundings, a logit and the logarithm of the number of keys, and its
+# output a mean of values.
+def _check(t, out, lse, low):
+    p = t.p
+    b = p.bias.cpu().numpy()
+    p.bias[p.bias <= low] = -float("inf")
+    ro, rl, a, s, _ = t.oracle()
+    big = float(np.abs(b[b > low]).max(initial=0.0))
+    ex = (p.d * s + 4 * (s + big)) * 2.0 ** -24
+    got, gl = _wide(out[:p.total]), lse.cpu().numpy()[:, :p.total].astype(np.float64)
+    assert np.isfinite(got).all() and np.isfinite(gl).all()
+    fin = np.isfinite(rl)
+    assert (np.abs(gl[~fin] - low) <= 2.0 ** -21 * abs(low) + s + 9).all()
+    most = np.nanmax(np.abs(_wide(p.vc)))  # (places behind the last keys hold NaN)
+    assert (np.abs(got) <= most * (1 + 2.0 ** -7)).all()
+    assert fin.mean() > 0.2
+    err, tol = np.abs(got - ro), 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2 * ex + 2.0 ** -18) * a * 1.01 + 1e-30
+    rows = fin.T
+    assert (err[rows] <= tol[rows]).all(), (err[rows] / tol[rows]).max()
+    ltol = ex + 2.0 ** -18 + 2.0 ** -22 * np.abs(rl[fin])
+    assert (np.abs(gl[fin] - rl[fin]) <= ltol).all(), np.abs(gl[fin] - rl[fin]).max()
+
+
+ITEMS = {
+    "few": dict(lq=[5, 3], ctx=[1500, 140], hq=2, hkv=2, d=64),
+    "rows64": dict(lq=[30, 25], ctx=[1500, 133], hq=2, hkv=2, d=64),
+    "rows64_d128": dict(lq=[12, 15], ctx=[700, 2300], hq=8, hkv=2, d=128),
+    "rows128": dict(lq=[60, 100], ctx=[300, 1400], hq=2, hkv=2, d=64),
+    "rows128_d128": dict(lq=[61, 24], ctx=[1300, 300], hq=8, hkv=2, d=128),
+    "tile": dict(lq=[140] * 12, ctx=[400] * 12, hq=8, hkv=8, d=64),
+}
+
+
+@pytest.mark.parametrize("low", [-1e6, -1e10, -1e30, -2e38])
+@pytest.mark.parametrize("std", [1.0, 12.0])
+@pytest.mark.parametrize("pattern", ["near", "odd", "any"])
+@pytest.mark.parametrize("item", ITEMS)
+def test_large_masking_biases(item, pattern, std, low):
+    t = Tree(page=64, t5=T5D, std=std, seed=5, **ITEMS[item])
+    _patterns(t.p, low, pattern, np.random.default_rng(9))
+    out, lse = t.run()
+    assert _errors() == 0
+    _check(t, out, lse, low)
