@@ -40,6 +40,9 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kWarpProd = 8, kWarpMma = 9, kWarpTail = 11;
+// head_dim 128: logits are formed less the row's reference up to this one, and whole beyond it: one as of keys with
+// masking biases (-1e10) would round the other keys' logits away.
+constexpr float kFarRef = 1024.f;
 constexpr int kMinShare = 4;  // cost units (a key tile of one Q tile) a CTA takes at least
 
 struct TileItem {
@@ -779,7 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t tH = tS + 64 * ((gi & 1) ^ half);
             const int c0 = 64 * half;
-            const float m_ref = m == -INFINITY ? 0.f : m;
+            const bool apart = !(fabsf(m) < kFarRef);  // the reference from the logits
+            const float m_ref = apart ? 0.f : m;
             uint32_t x[2][32];
             float mx;
             if (near) {
@@ -805,15 +809,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_before();
               mbar_arrive(s_read + t);
             }
-            float sub = 0.f;  // what the exponentials still subtract
-            bool need = false;
-            if (m == -INFINITY) {  // no key of this row so far: what was summed is zero
-              if (mx != -INFINITY) m = sub = mx;
-            } else {
-              need = mx > 32.f;
+            // what the exponentials still subtract, and the new reference less the old one
+            float sub = 0.f, up = 0.f;
+            if (apart) {
+              if (m == -INFINITY) {  // no key of this row so far: what was summed is zero
+                m = mx;
+              } else if (mx > m + 32.f) {
+                up = mx - m;
+                m = mx;
+              }
+              sub = m == -INFINITY ? 0.f : m;
+            } else if (mx > 32.f) {
+              up = sub = mx;
+              m += mx;
             }
-            if (__any_sync(0xffffffffu, need)) {
-              const float f = need ? ex2(-mx) : 1.f;
+            if (__any_sync(0xffffffffu, up > 0.f)) {
+              const float f = ex2(-up);
               if (i + half > 0) {  // O, once the products so far are complete
                 ok = half == 0 ? warp_wait(o_ready + t, (gi - 1) & 1, wd)
                                : warp_wait(o_half + t, gi & 1, wd);
@@ -831,10 +842,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               l *= f;
 #pragma unroll
               for (int k = 0; k < 4; ++k) sum2[k] = f2_mul(sum2[k], f2_pack(f, f));
-              if (need) {
-                m += mx;
-                sub = mx;
-              }
             }
             if (__any_sync(0xffffffffu, sub != 0.f))
               tile_exp<2, true>(x, f2_pack(sub, sub), tP + 32 * half, sum2);

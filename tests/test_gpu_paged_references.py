@@ -79,3 +79,30 @@ def test_large_masking_biases(item, pattern, std, low):
     out, lse = t.run()
     assert _errors() == 0
     _check(t, out, lse, low)
+
+
+# The tile kernel: trees that fill the GPU with blocks of 128 rows, and chains (fat_paged_attn), whose keys are
+# a tree's of one path.
+CHAINS = {
+    "few": dict(lq=[5, 3], ctx=[1500, 140], hq=2, hkv=2, d=64),
+    "few_d128": dict(lq=[4, 2], ctx=[700, 2300], hq=8, hkv=2, d=128),
+    "tile": dict(lq=[300, 25], ctx=[900, 133], hq=2, hkv=2, d=64),
+    "tile_d128": dict(lq=[130, 40, 17], ctx=[700, 0, 2300], hq=4, hkv=2, d=128),
+}
+
+
+@pytest.mark.parametrize("low", [-1e6, -1e10, -1e30, -2e38])
+@pytest.mark.parametrize("std", [1.0, 12.0])
+@pytest.mark.parametrize("pattern", ["near", "odd", "any"])
+@pytest.mark.parametrize("chain", [None, *CHAINS])
+def test_large_masking_biases_of_tiles(chain, pattern, std, low):
+    case = CHAINS[chain] if chain else dict(lq=[140] * 12, ctx=[400] * 12, hq=8, hkv=8, d=128)
+    t = Tree(page=64, t5=T5D, std=std, seed=6, reach=1 if chain else 3, **case)
+    _patterns(t.p, low, pattern, np.random.default_rng(8))
+    if chain:
+        t.p.causal = True
+        out, lse = t.p.run()
+    else:
+        out, lse = t.run()
+    assert _errors() == 0
+    _check(t, out, lse, low)
