@@ -84,6 +84,9 @@ size_t fwd_smem_bytes(int head_dim, int lut_len, int nt) {
   return 1024 + base + (((size_t)lut_len * 4 + 15) & ~(size_t)15) + kMaxThresholds * 4 + 256 * 4;
 }
 
+// Up to this reference (log2 units) logits are formed less the reference at once (d = 128).
+constexpr float kFarRef = 8192.f;
+
 // Load the S row from TMEM (all four 32-column loads in flight), form
 // x = S * scale_log2 + bias - m_ref (log2 units, m_ref the row's current reference max) two
 // columns per packed fp32x2 instruction, apply the mask, and return the row maximum of x.
@@ -620,7 +623,9 @@ __global__ void __launch_bounds__(FwdCfg<D, NT>::NTHREADS, FwdCfg<D, NT>::MIN_BL
         // subtraction unless the max moves (with d = 64 the extra registers cost more than the
         // subtraction saves)
         constexpr bool FOLD = !C::SEP_P;
-        const float m_ref = (FOLD && m != -INFINITY) ? m : 0.f;
+        // (a far reference, as of keys with masking biases, would round the others' logits away)
+        const bool apart = !FOLD || !(fabsf(m) < kFarRef);
+        const float m_ref = apart ? 0.f : m;
         rowc -= m_ref;
         const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
         uint32_t x[4][32];
@@ -645,7 +650,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NT>::NTHREADS, FwdCfg<D, NT>::MIN_BL
           sub = (mx == -INFINITY) ? 0.f : mx;
         } else {
           const bool fresh = m == -INFINITY;  // no key of this row so far
-          const bool need = fresh ? (mx != -INFINITY) : (mx > (FOLD ? 0.f : m) + 32.0f);
+          const bool need = fresh ? (mx != -INFINITY) : (mx > (apart ? m : 0.f) + 32.0f);
           if (C::SEP_P) {  // P_t and O_t are still read by PV_{j-1}
             ok = __all_sync(0xffffffffu, mbar_wait(o_ready + t, (j - 1) & 1, wd));
             if (!ok) break;
@@ -658,7 +663,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NT>::NTHREADS, FwdCfg<D, NT>::MIN_BL
               if (!ok) break;
               tc_fence_after();
             }
-            const float f = need ? (fresh ? 0.f : ex2(FOLD ? -mx : m - mx)) : 1.0f;
+            const float f = need ? (fresh ? 0.f : ex2(apart ? m - mx : -mx)) : 1.0f;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -669,10 +674,11 @@ __global__ void __launch_bounds__(FwdCfg<D, NT>::NTHREADS, FwdCfg<D, NT>::MIN_BL
             }
             if (need) {
               l *= f;
-              m = (fresh || !FOLD) ? mx : m + mx;
+              m = apart ? mx : m + mx;
               sub = mx;
             }
           }
+          if (FOLD && apart) sub = m == -INFINITY ? 0.f : m;
         }
         // turn order (d = 64, two tiles): tile 0 waits for tile 1's exponentials of the previous
         // key tile, tile 1 for tile 0's of this one. Only the order of work depends on it, so the
