@@ -179,6 +179,8 @@ def load(path: Optional[str] = None):
     H = P(_LinearCeShape)
     lib.fat_attn_debug_head_columns.argtypes = [H, i32]
     lib.fat_attn_debug_head_columns.restype = i32
+    lib.fat_attn_debug_head_workspace.argtypes = [H, i32, i32, P(ctypes.c_size_t)]
+    lib.fat_attn_debug_head_workspace.restype = ctypes.c_size_t
     lib.fat_linear_cross_entropy_workspace_size.argtypes = [H, i32]
     lib.fat_linear_cross_entropy_workspace_size.restype = ctypes.c_size_t
     lib.fat_linear_cross_entropy_fwd.argtypes = [H, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
@@ -636,7 +638,8 @@ def _stream_arg(stream):
 
 def fat_linear_cross_entropy_workspace_size(rows: int, vocab: int, dim: int,
                                             backward: bool = False) -> int:
-    """Workspace bytes of fat_linear_cross_entropy_fwd (or _bwd) on the current device."""
+    """Workspace bytes of fat_linear_cross_entropy_fwd (or _bwd) on the current device, for calls of up to
+    `rows` rows."""
     return (_calls or _load_calls()).lce_workspace(rows, vocab, dim, backward)
 
 

@@ -6,8 +6,8 @@
 //   dh = s dz W, dw = s dz^T H.
 //
 // The logits exist only as accumulators in tensor memory. Forward: tiles of 256 rows x up to 256
-// vocabulary entries; the epilogue leaves a tile's maximum and sum of exponentials per row (8 bytes for
-// 256 logits), which a second grid merges. Backward: the vocabulary in pieces; a piece's logits are
+// vocabulary entries; the epilogue leaves the maximum and sum of exponentials of each half of a tile's row
+// (8 bytes for up to 128 logits), which a second grid merges. Backward: the vocabulary in pieces; a piece's logits are
 // computed again, their gradient goes to the workspace in bf16, and two products take it from there:
 // dh += dz W and dw = dz^T H. dz is kept without grad_scale and s, which scale the results: bf16 holds the
 // large entries, p - 1 at the targets, best when they are next to 1 (with 1 / rows in them all of them
@@ -986,6 +986,33 @@ BwdPlan backward_plan(const fat_linear_ce_shape_t *s, int pairs) {
   return b;
 }
 
+// What every call of at most s->rows rows takes: plans of fewer rows may cut the vocabulary into more tiles, pieces
+// or splits than those of more, so each part is counted by a bound that grows with the rows.
+size_t forward_bytes(const fat_linear_ce_shape_t *s, int pairs) {
+  // statistics: two of 8 bytes a row for each tile; tiles are narrowed only within the same rounds over the pairs
+  const size_t tiles = (size_t)ceil_div(s->rows, kTile) * ceil_div(s->vocab, kTile) + pairs;
+  size_t bytes = round256(tiles * 2 * kTile * 8) + round256((size_t)s->rows * 4);
+  if (copies_rows(s))
+    bytes += round256((size_t)s->rows * copy_pitch(s) * 2) + round256((size_t)s->vocab * copy_pitch(s) * 2);
+  return bytes;
+}
+size_t backward_bytes(const fat_linear_ce_shape_t *s, int pairs) {
+  const int d_tiles = ceil_div(s->dim, kTile);
+  const long long tiles = ceil_div(s->rows, kTile), blocks = std::max(1, ceil_div(tiles * kTile, kMaxBlock));
+  const long long block = std::min<long long>(tiles, kMaxBlock / kTile), vpad = ceil_div(s->vocab, kTile) * (long long)kTile;
+  // records (a block's last tiles may hold no row) and the copy of the hidden rows
+  size_t bytes = round256((size_t)(tiles + blocks - 1) * kTile * 16) + round256((size_t)s->rows * copy_pitch(s) * 2);
+  // dz: all of it (of two blocks, as many rows each), or two pieces of up to kPiece values
+  const bool one = tiles * kTile * vpad <= kPiece;
+  bytes += one ? (size_t)(tiles + (blocks > 1)) * kTile * vpad * 2 : (size_t)kPiece * 4;
+  // dh's partials: its tiles, and splits that fill up to two rounds over the pairs, of 16 k blocks at least each
+  const long long most = (long long)block * ceil_div(ceil_div(s->vocab, 64), 16);
+  const long long parts = std::min(most, block + 3 * ceil_div(pairs, d_tiles));
+  if (!one || parts > block) bytes += round256((size_t)std::max(parts, block) * kTile * s->dim * 4);
+  if (blocks > 1) bytes += round256((size_t)s->vocab * s->dim * 4);
+  return bytes;
+}
+
 // The pairs of a launch and their shares of the next piece's logits: what each one's turns at the products'
 // tiles cost is filled up to one level.
 void share_tiles(HeadParams &p, int pairs) {
@@ -1067,7 +1094,14 @@ size_t fat_linear_cross_entropy_workspace_size(const fat_linear_ce_shape_t *s, i
   if (check(s)) return 0;
   const int pairs = head_pairs();
   if (pairs == 0 || s->rows == 0) return 0;
-  return backward ? backward_plan(s, pairs).bytes : forward_plan(s, pairs).bytes;
+  return backward ? backward_bytes(s, pairs) : forward_bytes(s, pairs);
+}
+
+size_t fat_attn_debug_head_workspace(const fat_linear_ce_shape_t *s, int pairs, int backward, size_t *used) {
+  if (used) *used = 0;
+  if (check(s) || s->rows == 0 || pairs < 1) return 0;
+  if (used) *used = backward ? backward_plan(s, pairs).bytes : forward_plan(s, pairs).bytes;
+  return backward ? backward_bytes(s, pairs) : forward_bytes(s, pairs);
 }
 
 int fat_attn_debug_head_columns(const fat_linear_ce_shape_t *s, int pairs) {
@@ -1087,7 +1121,7 @@ int fat_linear_cross_entropy_fwd(const fat_linear_ce_shape_t *s, const void *hid
   const int pairs = head_pairs();
   if (pairs == 0) return FAT_ECUDA;
   const FwdPlan f = forward_plan(s, pairs);
-  if (workspace_bytes < f.bytes) return FAT_EINVAL_SHAPE;
+  if (workspace_bytes < forward_bytes(s, pairs)) return FAT_EINVAL_SHAPE;
   const Span out[3] = {Span(loss, (size_t)s->rows * 4), Span(lse, (size_t)s->rows * 4),
                        Span(workspace, f.bytes)};
   const Span in[3] = {rows_span(hidden, s->rows, s->hidden_stride, s->dim, 2),
@@ -1175,7 +1209,7 @@ int fat_linear_cross_entropy_bwd(const fat_linear_ce_shape_t *s, const void *hid
   const int pairs = head_pairs();
   if (pairs == 0) return FAT_ECUDA;
   const BwdPlan b = backward_plan(s, pairs);
-  if (workspace_bytes < b.bytes) return FAT_EINVAL_SHAPE;
+  if (workspace_bytes < backward_bytes(s, pairs)) return FAT_EINVAL_SHAPE;
   const size_t n4 = (size_t)s->rows * 4;
   const Span out[3] = {Span(dhidden, (size_t)s->rows * s->dim * 2),
                        Span(dweight, (size_t)s->vocab * s->dim * 2), Span(workspace, b.bytes)};

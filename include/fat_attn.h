@@ -343,19 +343,23 @@ int fat_cross_entropy(long long rows, int vocab, const void *logits, const int32
  * fat_linear_cross_entropy_bwd: gradients of grad_scale * sum_r dloss_r loss_r (dloss fp32 [rows]; NULL:
  *   ones), with lse as the forward gives it: dhidden bf16 [rows, dim] and dweight bf16 [vocab, dim], both
  *   contiguous and OVERWRITTEN, either NULL if it is not wanted. dz, the gradient of the logits, is
- *   rounded to bf16 (without grad_scale and logit_scale) as the operand of the two products; sums are fp32, without atomics whose order
- *   matters: a call's result does not depend on timing. Hidden rows that are ignored may hold anything (NaN,
- *   infinities); the others and the weights are finite.
+ *   rounded to bf16 (without grad_scale and logit_scale) as the operand of the two products; sums are
+ *   fp32, without atomics whose order matters: a call's result does not depend on timing. Hidden rows
+ *   that are ignored may hold anything (NaN, infinities); the others and the weights are finite.
  *   A target at or beyond vocab sets FAT_DEVERR_INDEX (that row: loss 0, gradient 0).
  * dim a multiple of 8, up to 65536; strides multiples of 8; any vocab and rows up to 2^28 each
  * (FAT_EUNSUPPORTED beyond, and for more than 2^30 tiles of 256 rows x 16 entries); logit_scale > 0,
- * z_loss >= 0. Index and statistics arrays need 4-byte alignment, the others 16. Results and workspace lie
- * over no other array of the call. workspace: fat_linear_cross_entropy_workspace_size bytes (256-byte
- * aligned, contents need not be initialised), for one call at a time: captured graphs that may overlap
- * take one each. Its size depends on the current device's SMs. The forward's is 8 bytes for up to 128
- * logits, and for calls of at least 1536 rows whose dim is an odd multiple of 8 a copy of the hidden rows and
- * weights with longer rows (odd numbers of 16 bytes load at half the rate); the backward's holds a copy of the hidden rows and dz of two pieces of the vocabulary (up to 256 MB
- * with their sums in fp32 beside them).
+ * z_loss >= 0. Index and statistics arrays need 4-byte alignment, the others 16. Results and workspace
+ * lie over no other array of the call.
+ * workspace: fat_linear_cross_entropy_workspace_size bytes (256-byte aligned, contents need not be
+ * initialised), for one call at a time: captured graphs that may overlap take one each. One for a
+ * number of rows does for fewer of the same vocab and dim. Its size depends on the current device's
+ * SMs. The forward's holds 8 bytes for up to 128 logits of a row, and for calls of at least 1536 rows
+ * whose dim is an odd multiple of 8 a copy of the hidden rows and weights with longer rows (odd
+ * numbers of 16 bytes load at half the rate). The backward's holds a copy of the hidden rows; dz in
+ * bf16, all of it (up to 128 MB) or two pieces of the vocabulary (256 MB); partial sums of dhidden in
+ * fp32, dim * 1 KB for each 256 rows of up to 16384 and for up to three more for each pair of SMs and
+ * 256 channels; and beyond 16384 rows dweight in fp32 as well, vocab * dim * 4 bytes.
  */
 typedef struct {
   int32_t rows, vocab, dim;

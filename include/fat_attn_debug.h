@@ -40,6 +40,13 @@ void fat_attn_debug_set_watchdog(long long timeout_ns, int flags);
  */
 int fat_attn_debug_head_columns(const fat_linear_ce_shape_t *shape, int pairs);
 
+/*
+ * fat_linear_cross_entropy_workspace_size on such a device, and in *used (if not NULL) the bytes that
+ * the call touches. Host only.
+ */
+size_t fat_attn_debug_head_workspace(const fat_linear_ce_shape_t *shape, int pairs, int backward,
+                                     size_t *used);
+
 #ifdef __cplusplus
 }
 #endif

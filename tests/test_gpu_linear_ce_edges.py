@@ -1,7 +1,9 @@
 """GPU parity of the output layer's cross-entropy at the edges of its tiles and workspaces, against fp64."""
 import pytest
+import torch
 
-from test_gpu_linear_ce import _check_fwd, _errors, _inputs
+import attention_relative_position_gb300 as fa
+from test_gpu_linear_ce import _check_bwd, _check_fwd, _errors, _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +26,16 @@ def test_widths_of_few_rows(rows):
 def test_widths_of_many_rows(cols, dim):
     h, w, t = _inputs(200, 70 * cols - 5, dim, ignored=0.2)
     _check_fwd(h, w, t)
+
+
+# fewer rows may be cut into more tiles, pieces or splits than the rows that the workspace was made for
+@pytest.mark.parametrize("rows,more,vocab,dim", [
+    (256, 257, 5000, 64), (128, 129, 40000, 64), (500, 1537, 9000, 72), (1024, 1280, 131072, 64),
+    (300, 16385, 5000, 136), (512, 900, 20000, 1032)])
+def test_workspace_of_more_rows(rows, more, vocab, dim):
+    h, w, t = _inputs(rows, vocab, dim, ignored=0.1)
+    size = [fa.fat_linear_cross_entropy_workspace_size(more, vocab, dim, backward=b) for b in (False, True)]
+    ws = [torch.full((n + 4096,), 0xff, dtype=torch.uint8, device="cuda") for n in size]
+    _check_fwd(h, w, t, workspace=ws[0][:-4096])
+    _check_bwd(h, w, t, grad_scale=1.0 / rows, workspace=ws[1][:-4096])
+    assert all((x[-4096:] == 0xff).all() for x in ws)
