@@ -548,11 +548,14 @@ int fat_paged_attn(const fat_paged_shape_t *shape, const fat_paged_cache_t *cach
  *   positions [total_q]: seqlens_k - nodes + depth, what the node's rotary angles and biases go by;
  *   tree_mask [total_q, mask_words]: bit b of word w is node 32 w + b of the same request, set for the node
  *     itself and its ancestors.
- * Rows behind cu_seqlens_q[num_seqs], and of requests of more than max_seqlen_q nodes or whose seqlens_k is
- * smaller than their nodes (FAT_DEVERR_SEQLENS), get 0 and no bits; a parent that is no earlier node counts as
- * -1 (FAT_DEVERR_INDEX); with a corrupt cu_seqlens_q (FAT_DEVERR_SEQLENS) the rows concerned are left as they
- * were. mask_words at least ceil(max_seqlen_q / 32); max_seqlen_q at most 4096 (FAT_EUNSUPPORTED). The
- * results lie over no other array of the call.
+ * Rows behind cu_seqlens_q[num_seqs], and of requests of more than max_seqlen_q nodes or whose
+ * seqlens_k is smaller than their nodes (FAT_DEVERR_SEQLENS), get 0 and no bits; a parent that is no
+ * earlier node counts as -1 (FAT_DEVERR_INDEX). With a corrupt cu_seqlens_q (FAT_DEVERR_SEQLENS) a
+ * request whose bounds lie outside [0, total_q] or out of order writes no rows; where other bounds make
+ * requests claim each other's rows, such a row holds what one of them, or the rows behind the last
+ * one, gives it. mask_words at least ceil(max_seqlen_q / 32); max_seqlen_q at most 4096
+ * (FAT_EUNSUPPORTED; a request has one warp, which drafted trees of up to some hundred nodes suit, and
+ * larger ones are right but slow). The results lie over no other array of the call.
  */
 typedef struct {
   int32_t total_q;      /* rows of parents, positions and tree_mask */

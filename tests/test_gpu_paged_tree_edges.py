@@ -1,10 +1,13 @@
-"""Trees of drafted tokens over a paged cache: workspaces of the size that the library names, in every kernel."""
+"""Trees of drafted tokens over a paged cache: workspaces of the size that the library names, in every kernel,
+and maps beside corrupt row bounds."""
+import numpy as np
 import pytest
 import torch
 
 import attention_relative_position_gb300 as fa
+from oracle import paged
 from test_gpu_paged import _errors, _i32
-from test_gpu_paged_tree import T5D, Tree
+from test_gpu_paged_tree import T5D, Tree, _parents
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -55,3 +58,35 @@ def test_nothing_behind_the_workspace(name):
     with pytest.raises(fa.FatAttnError):
         t.run(workspace=buf[:1024])
     assert _errors() == 0
+
+
+# cu_seqlens_q with one bad entry, and the requests whose rows no other request claims: theirs are right; rows of
+# a request with bounds outside the arrays or out of order stay as they were, unless another one claims them.
+@pytest.mark.parametrize("at,value,right,left", [
+    (1, -3, (2, 3), (0, 13)), (2, 1000, (0, 3), (9, 33)), (2, 3, (3,), (0, 0)), (4, 1000, (0, 1, 2), (33, 39)),
+    (4, 30, (0, 1), (0, 0)), (2, 9, (0, 3), (0, 0)), (0, 5, (1, 2, 3), (0, 5))])
+def test_plan_beside_corrupt_bounds(at, value, right, left):
+    rng = np.random.default_rng(4)
+    lq, most, words = [9, 4, 20, 6], 20, 2
+    lk = np.array(lq) + 10
+    par = _parents(rng, lq, 3)
+    cu = np.concatenate([[0], np.cumsum(lq)])
+    pos, mask = paged.tree_plan(par, cu, lk, 39, most, words)
+    bad = cu.copy()
+    bad[at] = value
+    guard = 64
+    p = torch.full((39 + 2 * guard,), -9, dtype=torch.int32, device=DEV)
+    m = torch.full((39 + 2 * guard, words), -9, dtype=torch.int32, device=DEV)
+    fa.fat_paged_tree_plan(_i32(par), _i32(bad), _i32(lk), most, positions=p[guard:-guard],
+                           tree_mask=m[guard:-guard])
+    # (bounds that are still in order only make another request, whose parents are those of other nodes)
+    assert _errors() & (fa.FAT_DEVERR_INDEX if at == 0 else fa.FAT_DEVERR_SEQLENS)
+    p, m = p.cpu().numpy(), m.cpu().numpy()
+    for x in (p, m):
+        assert (x[:guard] == -9).all() and (x[-guard:] == -9).all()
+    p, m = p[guard:-guard], m[guard:-guard]
+    for i in right:
+        rows = slice(cu[i], cu[i + 1])
+        np.testing.assert_array_equal(p[rows], pos[rows])
+        np.testing.assert_array_equal(m[rows], mask[rows])
+    assert (p[slice(*left)] == -9).all() and (m[slice(*left)] == -9).all()
