@@ -2,9 +2,9 @@
 padding-free varlen packing, forward and backward.
 
 This module is a thin binding over libfatattn.so (C ABI in include/fat_attn.h), by ctypes and, for the
-paged-cache and output-layer calls, a small extension module: it only marshals torch tensors into pointers and sizes. Every step of the computation runs in the CUDA
-kernels of the library; there is no other implementation to fall back to, and a missing or
-unloadable library raises immediately.
+paged-cache and output-layer calls, a small extension module: it only marshals torch tensors into
+pointers and sizes. Every step of the computation runs in the CUDA kernels of the library; there is no
+other implementation to fall back to, and a missing or unloadable library raises immediately.
 """
 from __future__ import annotations
 
@@ -20,10 +20,10 @@ __all__ = [
     "fat_attn_bwd_noalloc", "fat_xattn_fwd", "fat_xattn_bwd", "fat_xattn_bwd_workspace_size",
     "fat_xattn_splitkv_num_splits", "fat_rope_apply", "fat_rmsnorm_fwd", "fat_rmsnorm_bwd",
     "fat_cross_entropy", "fat_linear_cross_entropy_fwd", "fat_linear_cross_entropy_bwd",
-    "fat_linear_cross_entropy_workspace_size", "fat_paged_plan", "fat_rope_init", "fat_rope_embed", "fat_paged_append",
-    "fat_paged_attn", "fat_paged_attn_workspace_size", "fat_paged_tree_plan", "fat_paged_tree_attn", "FAT_DEVERR_TIMEOUT_FWD",
-    "FAT_DEVERR_TIMEOUT_BWD", "FAT_DEVERR_INDEX", "FAT_DEVERR_SEQLENS", "FAT_DEVERR_PAGES",
-    "LIB_PATH",
+    "fat_linear_cross_entropy_workspace_size", "fat_paged_plan", "fat_rope_init", "fat_rope_embed",
+    "fat_paged_append", "fat_paged_attn", "fat_paged_attn_workspace_size", "fat_paged_tree_plan",
+    "fat_paged_tree_attn", "FAT_DEVERR_TIMEOUT_FWD", "FAT_DEVERR_TIMEOUT_BWD", "FAT_DEVERR_INDEX",
+    "FAT_DEVERR_SEQLENS", "FAT_DEVERR_PAGES", "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfatattn.so")

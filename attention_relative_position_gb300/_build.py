@@ -1,6 +1,7 @@
 """Builds libfatattn.so (the CUDA library behind include/fat_attn.h) in-tree with nvcc for
 sm_103a. Translation units compile in parallel; the link uses nvcc with the static CUDA runtime. The
-extension module of the paged-cache and output-layer calls is compiled beside them with g++ against torch's headers."""
+extension module of the paged-cache and output-layer calls is compiled beside them with g++ against
+torch's headers."""
 from __future__ import annotations
 
 import concurrent.futures as cf

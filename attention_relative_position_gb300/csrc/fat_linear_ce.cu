@@ -7,12 +7,14 @@
 //
 // The logits exist only as accumulators in tensor memory. Forward: tiles of 256 rows x up to 256
 // vocabulary entries; the epilogue leaves the maximum and sum of exponentials of each half of a tile's row
-// (8 bytes for up to 128 logits), which a second grid merges. Backward: the vocabulary in pieces; a piece's logits are
-// computed again, their gradient goes to the workspace in bf16, and two products take it from there:
-// dh += dz W and dw = dz^T H. dz is kept without grad_scale and s, which scale the results: bf16 holds the
-// large entries, p - 1 at the targets, best when they are next to 1 (with 1 / rows in them all of them
-// round the same way, and so do the results: 251 rows 0.0038 off against 0.0017). A launch does the products of one
-// piece and the logits of the next, so that its last wave is filled with short tiles.
+// (8 bytes for up to 128 logits), which a second grid merges. Backward: the vocabulary in pieces; a
+// piece's logits are computed again, their gradient goes to the workspace in bf16, and two products take
+// it from there: dh += dz W and dw = dz^T H. (One bf16 a value: most gradients are 0.0022 to 0.0025 off in
+// the mean where the results' own rounding gives 0.0017; two would double the products.) dz is kept without
+// grad_scale and s, which scale the results: bf16 holds the large entries, p - 1 at the targets, best when
+// they are next to 1 (with 1 / rows in them all of them round the same way, and so do the results: 251 rows
+// 0.0038 off against 0.0017). A launch does the products of one piece and the logits of the next, so that
+// its last wave is filled with short tiles.
 // Bound by the tensor cores (2, 4 and 2 N V D operations in the three products, 2 in the loss) from some
 // 300 rows on, below that by the read of the weights (and the write of their gradient).
 //
@@ -580,8 +582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (row < p.rows)
           p.part[(size_t)(2 * (job.n0 / p.bn) + half) * p.rows + row] = make_float2(m, s0 + s1);
       } else if constexpr (MODE == kFew) {
-        // A thread holds a vocabulary entry's logits of this warpgroup's rows, and passes them on through shared
-        // memory to the threads that share a row: its statistics over the CTA's 128 entries.
+        // A thread holds a vocabulary entry's logits of this warpgroup's rows, and passes them on through
+        // shared memory to the threads that share a row: its statistics over the CTA's 128 entries.
         const int r0 = half * (p.bn >> 1), nr = min(p.rows - r0, p.bn >> 1);
         const int t = tid & 127, v0 = job.m0 + rank * 128;
         const bool in = v0 + t < p.vocab;
@@ -798,7 +800,8 @@ __global__ void __launch_bounds__(256) fat_head_merge_kernel(const float2 *part,
 // values are 0 in the copy, for 0 * NaN would reach dw.
 __global__ void __launch_bounds__(256)
     fat_head_rows_kernel(const uint4 *hidden, long long stride16, const int32_t *target,
-                         const float *lse, const float *dloss, float zc, int rows, int padded, int vocab, int chunks, int pitch16, uint4 *copy,
+                         const float *lse, const float *dloss, float zc, int rows, int padded,
+                         int vocab, int chunks, int pitch16, uint4 *copy,
                          float4 *rec, int *err) {
   grid_dep_launch();
   grid_dep_wait();
@@ -964,7 +967,8 @@ BwdPlan backward_plan(const fat_linear_ce_shape_t *s, int pairs) {
   b.splits = std::max(1, ceil_div(kb, longest));
   // no more of them than fill their rounds over the pairs
   const long long rounds = std::max<long long>(1, (2 * dx_tiles * b.splits + pairs) / (2 * pairs));
-  if (b.splits > 1) b.splits = (int)std::max<long long>(1, std::min<long long>(b.splits, rounds * pairs / dx_tiles));
+  if (b.splits > 1)
+    b.splits = (int)std::max<long long>(1, std::min<long long>(b.splits, rounds * pairs / dx_tiles));
   b.split_kb = ceil_div(kb, b.splits);
   b.splits = ceil_div(kb, b.split_kb);
   b.dx_parts = b.splits > 1 || b.pieces > 1;
@@ -986,26 +990,29 @@ BwdPlan backward_plan(const fat_linear_ce_shape_t *s, int pairs) {
   return b;
 }
 
-// What every call of at most s->rows rows takes: plans of fewer rows may cut the vocabulary into more tiles, pieces
-// or splits than those of more, so each part is counted by a bound that grows with the rows.
+// What every call of at most s->rows rows takes: plans of fewer rows may cut the vocabulary into more
+// tiles, pieces or splits than those of more, so each part is counted by a bound that grows with the rows.
 size_t forward_bytes(const fat_linear_ce_shape_t *s, int pairs) {
-  // statistics: two of 8 bytes a row for each tile; tiles are narrowed only within the same rounds over the pairs
+  // statistics: two of 8 bytes a row for each tile; tiles are narrowed within the same rounds over the pairs
   const size_t tiles = (size_t)ceil_div(s->rows, kTile) * ceil_div(s->vocab, kTile) + pairs;
   size_t bytes = round256(tiles * 2 * kTile * 8) + round256((size_t)s->rows * 4);
   if (copies_rows(s))
-    bytes += round256((size_t)s->rows * copy_pitch(s) * 2) + round256((size_t)s->vocab * copy_pitch(s) * 2);
+    bytes += round256((size_t)s->rows * copy_pitch(s) * 2) +
+             round256((size_t)s->vocab * copy_pitch(s) * 2);
   return bytes;
 }
 size_t backward_bytes(const fat_linear_ce_shape_t *s, int pairs) {
   const int d_tiles = ceil_div(s->dim, kTile);
   const long long tiles = ceil_div(s->rows, kTile), blocks = std::max(1, ceil_div(tiles * kTile, kMaxBlock));
-  const long long block = std::min<long long>(tiles, kMaxBlock / kTile), vpad = ceil_div(s->vocab, kTile) * (long long)kTile;
+  const long long block = std::min<long long>(tiles, kMaxBlock / kTile);
+  const long long vpad = ceil_div(s->vocab, kTile) * (long long)kTile;
   // records (a block's last tiles may hold no row) and the copy of the hidden rows
-  size_t bytes = round256((size_t)(tiles + blocks - 1) * kTile * 16) + round256((size_t)s->rows * copy_pitch(s) * 2);
+  size_t bytes = round256((size_t)(tiles + blocks - 1) * kTile * 16) +
+                 round256((size_t)s->rows * copy_pitch(s) * 2);
   // dz: all of it (of two blocks, as many rows each), or two pieces of up to kPiece values
   const bool one = tiles * kTile * vpad <= kPiece;
   bytes += one ? (size_t)(tiles + (blocks > 1)) * kTile * vpad * 2 : (size_t)kPiece * 4;
-  // dh's partials: its tiles, and splits that fill up to two rounds over the pairs, of 16 k blocks at least each
+  // dh's partials: its tiles, and splits that fill two rounds and a bit over the pairs, of 16 k blocks at least
   const long long most = (long long)block * ceil_div(ceil_div(s->vocab, 64), 16);
   const long long parts = std::min(most, block + 3 * ceil_div(pairs, d_tiles));
   if (!one || parts > block) bytes += round256((size_t)std::max(parts, block) * kTile * s->dim * 4);
@@ -1171,7 +1178,8 @@ int fat_linear_cross_entropy_fwd(const fat_linear_ce_shape_t *s, const void *hid
   const bool more = s->dim > kChunk * 64;
   const auto kernel = f.few ? fat_head_kernel<kFew> : more ? fat_head_kernel<kLong> : fat_head_kernel<kForward>;
   rc = launch_dependent("linear cross-entropy launch", kernel, grid, kThreads,
-                        f.few ? HeadCfg<kFew>::SMEM : HeadCfg<kForward>::SMEM, stream, mx, mw, mx, mx, mx, mx, p);
+                        f.few ? HeadCfg<kFew>::SMEM : HeadCfg<kForward>::SMEM, stream, mx, mw, mx, mx, mx,
+                        mx, p);
   if (rc) return rc;
   // a row's statistics over as many threads as keep the SMs busy
   const auto merge = s->rows < 1024   ? fat_head_merge_kernel<4>

@@ -232,8 +232,8 @@ size_t workspace_bound(const fat_paged_shape_t *sh, const fat_paged_cache_t *c) 
   return bytes;
 }
 
-// Trees of more than 16 rows: rows of the items of the tree kernel, 0 where the tile kernel does better. That is
-// for more than 128 rows a request (the tree kernel reads keys again for every 128, the tile kernel for every
+// Trees of more than 16 rows: rows of the items of the tree kernel, 0 where the tile kernel does better. That
+// is for more than 128 rows a request (the tree kernel reads keys again for every 128, the tile kernel for every
 // 256), where every request has as many (else the few-row kernel's launch and its share of the SMs come on
 // top) and 128-row items would fill the SMs. Tree kernel against tile kernel, 32 heads over 8 of 128, us:
 //   16 trees of 24 to 61 tokens over 1500 to 6000 keys 89 / 127, of 61 110 / 96, of 33 over 4000 101 / 92;

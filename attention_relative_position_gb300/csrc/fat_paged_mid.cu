@@ -10,8 +10,10 @@
 // row's reference is the largest of eight logits of the first tile taken, and is raised to the maximum (O and
 // the sums scaled) when a weight would exceed 2^32: a group's 128 threads vote once a tile, and a maximum
 // over the keys, across lanes, is formed only then. A thread sums its own key's weights in a register per row
-// (unrounded, fp32); the threads' sums are added at an item's end. Key tiles go from the last one backwards, from the
-// request's own tokens and the largest linear bias on. P is rounded to bf16, as in the tile kernel.
+// (unrounded, fp32); the threads' sums are added at an item's end. Key tiles go from the last one backwards,
+// from the request's own tokens and the largest linear bias on. P is rounded to bf16, as in the tile kernel
+// (outputs 0.0023 off in the mean, 0.0017 with the few-row kernel's two parts, for which shared memory has
+// no room beside 128 rows and would take a stage of values beside 64).
 // One persistent CTA per SM takes an equal share of all key tiles (fat_paged.cuh); requests of more rows are
 // cut into blocks of them (their keys are found in L2 again):
 //   warps 0-7  softmax, epilogue, zeros over the values behind the last key;
@@ -32,8 +34,8 @@ constexpr int kMinShare = 2;  // key tiles a CTA takes at least
 constexpr int kItemCost = 2;  // cost of an item beside its key tiles
 constexpr float kNoRow = 3e38f;      // reference of a row without a token: its weights are 0
 constexpr float kFreshRow = -3e38f;  // of a row that has seen no key: whatever it sees calls for a new one
-// From here on a bias (in log2 units) leaves of a logit whole numbers at most, and a reference like it cannot say
-// which: rows with such biases for their far keys form logits and references as one rounded sum each.
+// From here on a bias (in log2 units) leaves of a logit whole numbers at most, and a reference like it cannot
+// say which: rows with such biases for their far keys form logits and references as one rounded sum each.
 constexpr float kLargeBias = 16777216.f;
 constexpr float kSeen = -2.9e38f;    // logits above this count as seen (biases down to -2e38, times log2 e)
 
@@ -51,8 +53,8 @@ struct MidCfg {
   static constexpr int OFF_Q = OFF_V + VS * TILE;
   static constexpr int OFF_P = OFF_Q + QB * QTILE;
   static constexpr int RW = R / 2;               // rows of a softmax warpgroup
-  // registers of a softmax thread and of the others (28 bytes spill at 128 rows, whose times are those of a build
-  // without; 208 and 88 spill more in both)
+  // registers of a softmax thread and of the others (28 bytes spill at 128 rows, whose times are those of a
+  // build without; 208 and 88 spill more in both)
   static constexpr int SOFT_REGS = R == 64 ? 200 : 216, OTHER_REGS = R == 64 ? 104 : 72;
   static constexpr int REGS_NEEDED = 256 * SOFT_REGS + 128 * OTHER_REGS;
   static_assert(REGS_NEEDED <= kThreads * ((65536 / kThreads) & ~7), "register split");
@@ -64,7 +66,8 @@ struct MidCfg {
   // the reference; sum or factor; int2: position - shift, head; its place in out behind the item's first row
   static constexpr int OFF_SLOPE = OFF_ROW, OFF_FAR = OFF_SLOPE + R * 4, OFF_NREF = OFF_FAR + R * 4;
   static constexpr int OFF_REF = OFF_NREF + R * 4, OFF_FAC = OFF_REF + R * 4, OFF_FARB = OFF_FAC + R * 4;
-  static constexpr int OFF_INT = OFF_FARB + R * 4, OFF_OUT = OFF_INT + R * 8, OFF_MAX = OFF_OUT + R * 4;  // float [2][8][RW]: maxima
+  static constexpr int OFF_INT = OFF_FARB + R * 4, OFF_OUT = OFF_INT + R * 8;
+  static constexpr int OFF_MAX = OFF_OUT + R * 4;  // float [2][8][RW]: maxima
   static constexpr int OFF_BAR = OFF_MAX + 8 * R * 4;
   static constexpr int OFF_THR = OFF_BAR + 320;
   static constexpr int OFF_SHARE = OFF_THR + kMaxThresholds * 4;
@@ -421,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto o_wait = [&](uint32_t i) { return warp_wait(o_ready + (i & 1), (i / 2) & 1, wd); };
       uint32_t g = 0;
       int ni = 0;
-      // A group's warps meet at barriers, so none leaves alone: once a wait has run out (ok) a warp waits no more
-      // and goes through the motions until a vote ends the loops for all of them.
+      // A group's warps meet at barriers, so none leaves alone: once a wait has run out (ok) a warp waits no
+      // more and goes through the motions until a vote ends the loops for all of them.
       bool ok = true;
       for (; ok && walk.next(it); ++ni) {
         const int n = it.j1 - it.j0, rows = it.ntok * G;
@@ -535,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if ((t & 15) == 0) {
 #pragma unroll
                 for (int i = 0; i < RW / 2; i += 2)
-                  *reinterpret_cast<ulonglong2 *>(max_s + (t >> 4) * RW + 2 * i) = make_ulonglong2(y[i], y[i + 1]);
+                  *reinterpret_cast<ulonglong2 *>(max_s + (t >> 4) * RW + 2 * i) =
+                      make_ulonglong2(y[i], y[i + 1]);
               }
               named_bar_sync(bar, 128);
               if (t < mine) {
@@ -562,8 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
               }
               // The rows' maxima over the tile, and new references where they passed 2^32. They are taken from
-              // reference 0: a low reference (-3e38 of a row that has seen no key, or of keys with masking biases)
-              // has rounded the other keys' logits away.
+              // reference 0: a low reference (-3e38 of a row that has seen no key, or of keys with masking
+              // biases) has rounded the other keys' logits away.
               if (t < mine) {
                 fac_s[t] = ref_s[t];
                 set_ref(0.f);
@@ -586,7 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               named_bar_sync(bar, 128);
               if (t < RW) {
-                const float mx = fmaxf(fmaxf(max_s[t], max_s[RW + t]), fmaxf(max_s[2 * RW + t], max_s[3 * RW + t]));
+                const float mx = fmaxf(fmaxf(max_s[t], max_s[RW + t]),
+                                       fmaxf(max_s[2 * RW + t], max_s[3 * RW + t]));
                 float f = 1.f;
                 if (t < mine) {
                   const float old = fac_s[t];
@@ -636,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t at = sP + (r >> 6) * C::PBLK + t * 128;
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                st_shared_v4(at + (((((r & 63) >> 3) + i) ^ (t & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2],
-                             w[4 * i + 3]);
+                st_shared_v4(at + (((((r & 63) >> 3) + i) ^ (t & 7)) << 4), w[4 * i], w[4 * i + 1],
+                             w[4 * i + 2], w[4 * i + 3]);
             }
           } else if (ok && gt >= C::PB) {  // a group without rows keeps step: its arrivals count for this tile
             ok = o_wait(gt - C::PB);
@@ -662,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         g += n;
-        // ---- the item's rows: their sums over the threads (beside the last products), then O, whose TMEM lanes
-        // are channels. Four lanes trade a 4 x 4 block, after which each has four channels of a row.
+        // ---- the item's rows: their sums over the threads (beside the last products), then O, whose TMEM
+        // lanes are channels. Four lanes trade a 4 x 4 block, after which each has four channels of a row.
         const bool whole = it.begins && it.ends;
         const int which = it.begins ? 1 : 0;
         if (!whole && tid == 0) {

@@ -40,8 +40,8 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kWarpProd = 8, kWarpMma = 9, kWarpTail = 11;
-// head_dim 128: logits are formed less the row's reference up to this one, and whole beyond it: one as of keys with
-// masking biases (-1e10) would round the other keys' logits away.
+// head_dim 128: logits are formed less the row's reference up to this one (log2 units), and whole beyond it:
+// one as of keys with masking biases (-1e10) would round the other keys' logits away.
 constexpr float kFarRef = 1024.f;
 constexpr int kMinShare = 4;  // cost units (a key tile of one Q tile) a CTA takes at least
 

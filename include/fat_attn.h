@@ -511,6 +511,9 @@ int fat_paged_append(const fat_append_shape_t *shape, const fat_paged_cache_t *c
  *     initialised), for this call alone until it has finished: calls that may overlap, and captured
  *     graphs that do, take one each. The size never falls as total_q, num_seqs, max_seqlen_q or
  *     max_seqlen_k grows: one buffer for the largest bounds serves every smaller step too.
+ *   - Logits, statistics and sums are fp32. Weights are rounded as operands of their product with the
+ *     values: to 16 bits where max_seqlen_q * num_heads_q / num_heads is at most 16 (in a step of mixed
+ *     lengths for the requests whose own queries make no more), else to bf16.
  * head_dim 64 or 128, num_heads_q / num_heads at most 128, max_seqlen_k at most 2^30.
  * A call whose total_q is exactly num_seqs * max_seqlen_q (beyond 16 rows a request, queries x
  * group) is taken as a batch of equal chunks; a step whose rows are padded to that total runs faster
@@ -577,7 +580,8 @@ int fat_paged_tree_plan(const fat_tree_shape_t *shape, const int32_t *parents,
  * seqlens_k) sets FAT_DEVERR_INDEX and is taken as the nearest end. All else, the workspace's size
  * too, as fat_paged_attn without its causal mask; a request with fewer keys than queries sets
  * FAT_DEVERR_SEQLENS and is left out. Keys and values that a node does not see are finite as well: they
- * enter its product with weight 0.
+ * enter its product with weight 0. Weights are rounded to 16 bits where max_seqlen_q * num_heads_q /
+ * num_heads is at most 16, else to bf16, for every request of the call.
  */
 int fat_paged_tree_attn(const fat_paged_shape_t *shape, const fat_paged_cache_t *cache, const void *q,
                         const int32_t *block_table, const int32_t *cu_seqlens_q,
