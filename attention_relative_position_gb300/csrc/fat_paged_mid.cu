@@ -35,7 +35,9 @@ constexpr int kItemCost = 2;  // cost of an item beside its key tiles
 constexpr float kNoRow = 3e38f;      // reference of a row without a token: its weights are 0
 constexpr float kFreshRow = -3e38f;  // of a row that has seen no key: whatever it sees calls for a new one
 // From here on a bias (in log2 units) leaves of a logit whole numbers at most, and a reference like it cannot
-// say which: rows with such biases for their far keys form logits and references as one rounded sum each.
+// say which: rows with such biases for their far keys form logits as one rounded sum each, as long as their
+// references are as large, too. That is for parts of items that begin behind the near keys: 64 trees of 12 nodes
+// with -1e9 as the far T5 buckets' bias 98 -> 100 us (4000 keys of 128 channels) and 133 -> 147 (8000 of 64).
 constexpr float kLargeBias = 16777216.f;
 constexpr float kSeen = -2.9e38f;    // logits above this count as seen (biases down to -2e38, times log2 e)
 
@@ -53,8 +55,7 @@ struct MidCfg {
   static constexpr int OFF_Q = OFF_V + VS * TILE;
   static constexpr int OFF_P = OFF_Q + QB * QTILE;
   static constexpr int RW = R / 2;               // rows of a softmax warpgroup
-  // registers of a softmax thread and of the others (28 bytes spill at 128 rows, whose times are those of a
-  // build without; 208 and 88 spill more in both)
+  // registers of a softmax thread and of the others (neither spills; 208 and 88 did in both)
   static constexpr int SOFT_REGS = R == 64 ? 200 : 216, OTHER_REGS = R == 64 ? 104 : 72;
   static constexpr int REGS_NEEDED = 256 * SOFT_REGS + 128 * OTHER_REGS;
   static_assert(REGS_NEEDED <= kThreads * ((65536 / kThreads) & ~7), "register split");
@@ -431,10 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = it.j1 - it.j0, rows = it.ntok * G;
         const int mine = min(rows - rb, RW);  // rows of this group (none: it only keeps step)
         int near = 0;  // from this key on logits are formed one by one
+        // (all of the group's threads; r: row t's reference, or what it may become)
+        auto choose_near = [&](float r) {
+          const float far = t < mine ? farb_s[t] : 0.f;
+          const bool large = fmaxf(fabsf(far), t < mine ? fabsf(slope_s[t]) * (float)it.lk : 0.f) >= kLargeBias &&
+                             fabsf(far) < INFINITY && fmaxf(fabsf(r), far) >= kLargeBias;
+          near = named_bar_any(bar, 128, large) ? 0 : it.shift - (biased ? p.bias.sat_neg : 0);
+        };
         if (mine > 0) {  // row t's numbers; its position arrives beside the first tile's logits
           const int rt = rb + min(t, mine - 1), q = rt / G, h = it.hk * G + (rt - q * G);
           int pos_in = 0;
-          bool large = false;
           if (t < RW) {
             pos_in = __ldg(p.pos + it.row0 + q);
             prefetch_l1(p.mask + (size_t)(it.row0 + q) * p.mask_words);
@@ -450,10 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int_s[t] = make_int2(pos - it.shift, h);
             out_s[t] = q * p.hq + h;
             set_ref(t < mine ? 0.f : kNoRow);
-            const float most = fmaxf(fabsf(far), fabsf(slope) * (float)it.lk);
-            large = t < mine && most >= kLargeBias && fabsf(far) < INFINITY;
           }
-          if (!named_bar_any(bar, 128, large)) near = it.shift - (biased ? p.bias.sat_neg : 0);
+          choose_near(INFINITY);
         }
         uint64_t sum[RW / 2];  // of this thread's weights, rows 2 i and 2 i + 1
 #pragma unroll
@@ -471,8 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *cst_s = edge ? nref_s : far_s;
             if (edge) {
               // Own keys, or cached ones near them: logits where they stand, masked by the rows' bits. A
-              // thread's key is the same for all rows, and so is its position. (Beside large biases every key:
-              // a reference such as -1e10 holds no more of the logit than these do.)
+              // thread's key is the same for all rows, and so is its position.
               const int key0 = k0 + (warp & 3) * 32;
               const int kp = key < it.shift ? key - it.shift
                                             : tree_pos(p, it.tok0 + min(key, it.lk - 1) - it.shift, it.shift,
@@ -489,6 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int i = 0; i < 32; ++i)
                     x[i] = (see >> i) & 1u ? __float_as_uint(__uint_as_float(x[i]) * scale) : 0xff800000u;
+                } else if (R == 64 && k0 + 128 <= it.shift - p.bias.sat_neg) {
+                  // far keys, beside large biases (128 rows have no registers left for this form)
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    x[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), scale,
+                                                fmaf(slope_s[c + i], (float)(key - it.shift), farb_s[c + i])));
                 } else {
 #pragma unroll
                   for (int i = 0; i < 32; ++i) {
@@ -548,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 1; i < 8; ++i) mx = fmaxf(mx, max_s[i * RW + t]);
                 set_ref(mx > kSeen ? mx : mx != mx ? 0.f : kFreshRow);  // (a NaN shows in the sum)
               }
-              named_bar_sync(bar, 128);
+              choose_near(t < mine ? ref_s[t] : 0.f);
             }
             all_logits();
             float top = -INFINITY;
@@ -601,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fac_s[t] = f;
               }
-              named_bar_sync(bar, 128);
+              choose_near(t < mine ? ref_s[t] : 0.f);
               if (j > 0) {  // what was summed so far
                 ok = o_wait(gt - 1);
                 tc_fence_after();

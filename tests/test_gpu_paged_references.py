@@ -106,3 +106,25 @@ def test_large_masking_biases_of_tiles(chain, pattern, std, low):
         out, lse = t.run()
     assert _errors() == 0
     _check(t, out, lse, low)
+
+
+# Far keys that are masked, in items of which a part begins behind the near ones; then all keys, whose rows' logits
+# differ by hundreds: beside such biases fp32 cannot tell the keys apart, but every row has a result.
+@pytest.mark.parametrize("low", [-1e9, -1e30, 1e10])
+@pytest.mark.parametrize("std", [1.0, 12.0])
+@pytest.mark.parametrize("lq,hq,hkv,d", [([30], 2, 2, 64), ([30], 4, 2, 128), ([100], 1, 1, 64), ([70], 1, 1, 128),
+                                         ([5], 2, 2, 64), ([16] * 3, 4, 2, 128)])
+def test_masked_far_keys_in_parts(lq, hq, hkv, d, std, low):
+    t = Tree(lq, [6000] * len(lq), hq=hq, hkv=hkv, d=d, page=64, seed=21, t5=T5D, std=std)
+    if low < 0:
+        t.p.bias[28:] = low
+        out, lse = t.run()
+        assert _errors() == 0
+        _check(t, out, lse, low)
+        t.p.bias[:] = low
+    else:  # the others are masked instead
+        t.p.bias[28:] += low
+    out, lse = t.run()
+    got, gl = _wide(out[:t.p.total]), lse.double().cpu().numpy()
+    assert np.isfinite(got).all() and (np.abs(gl / low - 1) < 1e-6).all()
+    assert (np.abs(got) <= np.nanmax(np.abs(_wide(t.p.vc))) * (1 + 2.0 ** -7)).all()
