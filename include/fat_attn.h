@@ -501,7 +501,8 @@ int fat_paged_append(const fat_append_shape_t *shape, const fat_paged_cache_t *c
  *     weight 0, and an infinite one makes the output NaN. A NaN in a query, or in a key it sees, makes
  *     its output and lse NaN.
  *   - A bias of -infinity (or below -2e38: logits are formed times log2 e) masks its keys; a row
- *     that is left with none gets 0 and lse -infinity.
+ *     that is left with none gets 0 and lse -infinity. Keys with large finite biases (-1e9) get the
+ *     weight that fp32 can tell: none beside other keys; among themselves their logits are lost.
  *   - Requests may name the same pages (a common prefix).
  *   - A page index outside [0, num_pages) sets FAT_DEVERR_PAGES; its keys and values count as 0.
  *   - A request whose query count exceeds max_seqlen_q or whose seqlens_k is negative, exceeds
